@@ -410,6 +410,122 @@ int dsa_index_bounded_stats(void* ws, dsa_stream_t stream, uint64_t* tiles_skipp
                             uint64_t* tiles_bounded);
 
 /* ---------------------------------------------------------------------------
+ * Heads of new tokens: norm and position rotation on the way to where they
+ * are read.  The pages start from finished indexer queries, queries and cache
+ * rows; these calls make them from a layer's raw projections.  The cache
+ * layout is that of "Day-0 Adaptation of Ultra-Large-Scale MoE Models on
+ * Heterogeneous AI Accelerators", section 4 (the layout written must match
+ * the addresses the gather reads).
+ *
+ * A part is one tensor of `heads` heads of `dim` elements for each of N
+ * tokens.  Each head x[0..dim) is, in fp32,
+ *   normed over its first norm_dim elements (the others pass through):
+ *     DSA_NORM_RMS    y = x / sqrt(mean(x^2) + eps) * weight + bias
+ *     DSA_NORM_LAYER  y = (x - m) / sqrt(mean((x - m)^2) + eps) * weight + bias
+ *   rotated in [rope_offset, rope_offset + rope_dim): pair i becomes
+ *     (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i],
+ *     the pair being elements (2 i, 2 i + 1) if interleaved, else
+ *     (i, i + rope_dim / 2) of that range; t is reduced modulo 2 pi in
+ *     integers, so it stays exact to ~1e-7 at any position (inv_freq <= 1);
+ *   rounded once to out_dtype (E4M3 saturates at +-448).
+ * in, out and weights are device pointers.  heads >= 1; dim a multiple of 8,
+ * 8..1024; strides in elements, multiples of 8; in and a bf16 out 16-byte
+ * aligned, an FP8 out 8-byte; weight and bias 16-byte aligned; rope_offset
+ * and rope_dim even.  out may be in itself (bf16, same strides); otherwise
+ * the two, and the outs of different parts, must not overlap.
+ */
+#define DSA_NORM_NONE 0
+#define DSA_NORM_RMS 1
+#define DSA_NORM_LAYER 2
+#define DSA_MAX_HEAD_PARTS 4 /* parts per list */
+
+typedef struct dsa_head_part {
+  const void* in;           /* bf16, token t head h at in + t*in_token_stride + h*in_head_stride */
+  int64_t in_token_stride;
+  int64_t in_head_stride;
+  void* out;                /* of out_dtype */
+  int64_t out_token_stride; /* elements between tokens; of a pool: between its rows */
+  int64_t out_head_stride;
+  int32_t out_dtype;        /* DSA_BF16 or DSA_FP8_E4M3 */
+  int32_t heads;
+  int32_t dim;
+  int32_t norm;             /* DSA_NORM_* */
+  int32_t norm_dim;         /* 1..dim when norm is not NONE */
+  float eps;                /* >= 0 */
+  const float* weight;      /* [norm_dim] fp32, or NULL (1) */
+  const float* bias;        /* [norm_dim] fp32, or NULL (0) */
+  int32_t rope_offset;
+  int32_t rope_dim;         /* 0: no rotation */
+  int32_t interleaved;
+  int32_t reserved_;        /* set to 0 */
+  const float* inv_freq;    /* [rope_dim / 2] fp32, finite */
+} dsa_head_part;
+
+/* dsa_head_norm_rope: the parts (1..DSA_MAX_HEAD_PARTS tensors, such as the
+ * latent queries' rotated part and the indexer queries, or queries and keys)
+ * of N tokens at positions pos [N] (device int32), in one launch.  `parts` is
+ * a host array, read before the call returns.  pos may be NULL when no part
+ * rotates.
+ * Errors: DSA_ERR_INVALID for null pointers, N < 0, n_parts, strides or
+ * alignment; DSA_ERR_UNSUPPORTED for other dims, dtypes or norms, and for
+ * more than 2^31 - 1 (token, head) rows in all.
+ */
+int dsa_head_norm_rope(const dsa_head_part* parts, int n_parts, const int32_t* pos, int N,
+                       dsa_stream_t stream);
+
+/* dsa_cache_append: dsa_cache_write with the transform on the way.  cache
+ * parts (1..DSA_MAX_HEAD_PARTS: K or latent rows, V rows, indexer keys) go to
+ * physical row block_table[seq][pos / block_size] * block_size
+ * + pos % block_size of their pool `out` (rows out_token_stride elements
+ * apart, heads out_head_stride apart inside a row); heads parts (0..
+ * DSA_MAX_HEAD_PARTS, may be NULL) are the same tokens' queries, written as
+ * dsa_head_norm_rope writes them, in the same launch.
+ *  seq, pos    [N] int32 sequence and position of each token; both NULL: the
+ *              append form of a decode step, token i is position
+ *              seq_lens[i] - 1 of sequence i (N <= batch)
+ *  ws          dsa_cache_append_workspace_size() bytes (the status word)
+ * A token whose sequence, position or page is out of range has its cache rows
+ * skipped and sets DSA_STATUS_BAD_BLOCK; its heads parts are still written,
+ * rotated by its position.  The same physical row twice in one call: as for
+ * dsa_cache_write.  Other errors as for dsa_head_norm_rope.
+ */
+size_t dsa_cache_append_workspace_size(void);
+int dsa_cache_append(const dsa_paged_layout* layout, const int32_t* seq, const int32_t* pos, int N,
+                     const dsa_head_part* cache, int n_cache, const dsa_head_part* heads,
+                     int n_heads, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * dsa_prefix_attn_decode: exact attention of one query per sequence over all
+ * of its cached positions, for a batch that shares a prefix.  Where no more
+ * than K positions are eligible the selection keeps every one of them, and
+ * this call needs neither scores nor an index list; requests behind one
+ * prompt read its pages once for the whole batch.  Same arithmetic as
+ * dsa_sparse_attn_decode with every position selected:
+ *     z_p = sm_scale * q[b][h] . K_p,  out[b][h] = sum_p softmax(z)_p V_p,
+ *     lse[b][h] = log sum_p exp(z_p),  p < seq_lens[b]
+ *  prefix_len  0..max_seq_len: positions [0, prefix_len) hold the same rows
+ *              for every sequence with seq_lens[b] >= prefix_len (normally
+ *              the same pages; they are read through the block-table row of
+ *              the first such sequence).  A shorter sequence shares nothing:
+ *              its own pages alone are read.  0: dense decode attention.
+ *  q           [B][Hq][Dqk] bf16, B = layout->batch
+ *  k_pool, v_pool, strides: as for dsa_sparse_attn_decode (v_pool may be
+ *              k_pool); Hq 1..128, Dqk 8..576 and Dv 8..512 multiples of 8
+ *  out         [B][Hq][Dv] bf16 (0 for an empty sequence)
+ *  lse         [B][Hq] fp32, or NULL (-inf for an empty sequence)
+ *  ws          dsa_prefix_attn_decode_workspace_size() bytes
+ * Errors: DSA_ERR_INVALID / DSA_ERR_UNSUPPORTED as for
+ * dsa_sparse_attn_decode and for prefix_len out of range.  Device: a position
+ * behind a bad block id is left out and sets DSA_STATUS_BAD_BLOCK; a length
+ * beyond the block table's row is cut there and sets DSA_STATUS_BAD_LENGTH.
+ */
+size_t dsa_prefix_attn_decode_workspace_size(int B, int Hq, int Dqk, int Dv, int prefix_len);
+int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const void* k_pool,
+                           int64_t k_row_stride, const void* v_pool, int64_t v_row_stride, int Hq,
+                           int Dqk, int Dv, int prefix_len, float sm_scale, void* out, float* lse,
+                           void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Utilities (no counterpart on the pages).
  * dsa_get_status: copy the status word of a workspace to *status (host), after
  *   the work queued on `stream` so far has finished (this call synchronises the

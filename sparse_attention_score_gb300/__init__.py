@@ -40,6 +40,8 @@ STATUS_BAD_BLOCK = 0x1
 STATUS_BAD_INDEX = 0x2
 STATUS_BAD_LENGTH = 0x4
 STATUS_TIMEOUT = 0x8
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+MAX_HEAD_PARTS = 4
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -60,6 +62,18 @@ class PagedLayoutC(ctypes.Structure):
                 ("max_blocks_per_seq", ctypes.c_int32), ("batch", ctypes.c_int32),
                 ("max_seq_len", ctypes.c_int32), ("reserved_", ctypes.c_int32),
                 ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p)]
+
+
+class HeadPartC(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("in_token_stride", ctypes.c_int64),
+                ("in_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("out_dtype", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("norm", ctypes.c_int32), ("norm_dim", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("rope_offset", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("reserved_", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p)]
 
 
 _vp, _i, _i64, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -113,6 +127,12 @@ _sig("dsa_sparse_attn_decode", _i, [_LP, _vp, _vp, _i64, _vp, _i64, _i, _i, _i, 
 _sig("dsa_sparse_attn_prefill_workspace_size", _sz, [_i, _i, _i, _i, _i])
 _sig("dsa_sparse_attn_prefill", _i, [_LP, _vp, _vp, _i64, _vp, _i64, _i, _i, _i, _vp, _vp, _i, _vp,
                                      _i, _f, _vp, _vp, _vp, _sz, _vp])
+_sig("dsa_head_norm_rope", _i, [_vp, _i, _vp, _i, _vp])
+_sig("dsa_cache_append_workspace_size", _sz, [])
+_sig("dsa_cache_append", _i, [_LP, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _sz, _vp])
+_sig("dsa_prefix_attn_decode_workspace_size", _sz, [_i, _i, _i, _i, _i])
+_sig("dsa_prefix_attn_decode", _i, [_LP, _vp, _vp, _i64, _vp, _i64, _i, _i, _i, _i, _f, _vp, _vp,
+                                    _vp, _sz, _vp])
 
 SYMBOLS = ("dsa_version", "dsa_launch_count", "dsa_last_error_string", "dsa_get_status",
            "dsa_selftest_bounded_wait",
@@ -128,7 +148,9 @@ SYMBOLS = ("dsa_version", "dsa_launch_count", "dsa_last_error_string", "dsa_get_
            "dsa_prefill_step_chunked_workspace_size", "dsa_prefill_step_chunked",
            "dsa_index_bounds_update_workspace_size", "dsa_index_bounds_update",
            "dsa_index_score_bounded_workspace_size", "dsa_index_score_bounded",
-           "dsa_index_bounded_stats")
+           "dsa_index_bounded_stats",
+           "dsa_head_norm_rope", "dsa_cache_append_workspace_size", "dsa_cache_append",
+           "dsa_prefix_attn_decode_workspace_size", "dsa_prefix_attn_decode")
 
 
 def lib() -> ctypes.CDLL:
@@ -525,6 +547,201 @@ def prefill_step_chunked(layout: PagedLayout, seq, q_pos, n_eligible, k_new, k_p
                                        Hq, Dqk, Dv, K, float(sm_scale), ld, int(chunk), pi, po, pl,
                                        pws, ws.numel(), _stream(stream))
     _check(rc, "dsa_prefill_step_chunked")
+
+
+class HeadPart:
+    """One tensor of new tokens' heads, normed and rotated on the way to `out`
+    (include/dsa.h, dsa_head_part).
+
+    x [N, heads, dim] bf16, any strides with the last dim contiguous (a slice
+    of a projection's output).  out: [N, heads, dim] bf16 or FP8 E4M3, strided
+    likewise, for head_norm_rope and cache_append(heads=...); a paged pool
+    [num_blocks, block_size, heads * dim or wider] (or [.., heads, dim]),
+    contiguous, for cache_append(cache).  norm: "none", "rms" or "layer" over
+    the first norm_dim elements (default: all), weight / bias fp32 [norm_dim].
+    rope_dim > 0 rotates elements [rope_offset, rope_offset + rope_dim) by
+    position * inv_freq (fp32 [rope_dim / 2]); interleaved pairs
+    (2 i, 2 i + 1), else (i, i + rope_dim / 2).  Shapes and types are checked
+    here, once; the tensors are kept alive by the part.
+    """
+
+    def __init__(self, x, out, *, norm="none", norm_dim=None, eps=1e-6, weight=None, bias=None,
+                 rope_offset=0, rope_dim=0, interleaved=False, inv_freq=None):
+        if x.dim() != 3 or x.stride(2) != 1 and x.shape[2] > 1:
+            raise ValueError("x: [N, heads, dim] with a contiguous last dim is required")
+        if x.dtype != torch.bfloat16:
+            raise TypeError(f"x: {x.dtype}; bfloat16 is required")
+        if out.element_size() not in _KEY or (out.element_size() == 2 and
+                                              out.dtype != torch.bfloat16):
+            raise TypeError(f"out: {out.dtype}; bfloat16 or an 8-bit type is required")
+        if norm not in NORMS:
+            raise ValueError(f"norm: {norm!r}; one of {', '.join(NORMS)}")
+        n, heads, dim = x.shape
+        norm_dim = dim if norm_dim is None else int(norm_dim)
+        if norm == "none":
+            norm_dim = 0
+        for t, name, count in ((weight, "weight", norm_dim), (bias, "bias", norm_dim),
+                               (inv_freq, "inv_freq", int(rope_dim) // 2)):
+            if t is not None:
+                if t.dtype != torch.float32:
+                    raise TypeError(f"{name}: {t.dtype}; float32 is required")
+                if not t.is_contiguous() or t.numel() < count:
+                    raise ValueError(f"{name}: {count} contiguous elements are required")
+        if rope_dim and inv_freq is None:
+            raise ValueError("inv_freq: required when rope_dim > 0")
+        self.x, self.out, self.weight, self.bias, self.inv_freq = x, out, weight, bias, inv_freq
+        self.N = int(n)
+        self._spec = (int(heads), int(dim), NORMS[norm], norm_dim, float(eps), int(rope_offset),
+                      int(rope_dim), 1 if interleaved else 0)
+
+    def _c(self, paged: bool) -> HeadPartC:
+        heads, dim, norm, norm_dim, eps, roff, rdim, inter = self._spec
+        x, out = self.x, self.out
+        if paged:
+            if out.dim() not in (3, 4) or not out.is_contiguous():
+                raise ValueError("out: a contiguous pool [num_blocks, block_size, width] is required")
+            ts, hs = out.stride(1), dim
+            if ts < heads * dim:
+                raise ValueError(f"out: pool rows of {ts} elements; {heads * dim} are needed")
+        else:
+            if tuple(out.shape) != (self.N, heads, dim) or out.stride(2) != 1 and dim > 1:
+                raise ValueError(f"out: {tuple(out.shape)}; {(self.N, heads, dim)} with a "
+                                 "contiguous last dim is required")
+            ts, hs = out.stride(0), out.stride(1)
+        opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        return HeadPartC(x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), ts, hs,
+                         _elt_dtype(out), heads, dim, norm, norm_dim, eps, opt(self.weight),
+                         opt(self.bias), roff, rdim, inter, 0, opt(self.inv_freq))
+
+    def tensors(self):
+        return [(t, n) for t, n in ((self.x, "x"), (self.out, "out"), (self.weight, "weight"),
+                                    (self.bias, "bias"), (self.inv_freq, "inv_freq"))
+                if t is not None]
+
+
+class HeadParts:
+    """A list of 1..4 :class:`HeadPart` of the same tokens, with the C array the
+    calls take.  A program whose buffers stay where they are builds it once."""
+
+    def __init__(self, parts):
+        self.parts = list(parts)
+        if not 1 <= len(self.parts) <= MAX_HEAD_PARTS:
+            raise ValueError(f"1 to {MAX_HEAD_PARTS} parts are taken")
+        self.N = self.parts[0].N
+        if any(p.N != self.N for p in self.parts):
+            raise ValueError("the parts differ in their number of tokens")
+        self.rotates = any(p._spec[6] for p in self.parts)
+        self.out_bytes = [p.out.element_size() * p.out.numel() for p in self.parts]
+        self._arrays = {}
+        self._device = None
+
+    def __len__(self):
+        return len(self.parts)
+
+    def c(self, paged: bool):
+        arr = self._arrays.get(paged)
+        if arr is None:
+            arr = (HeadPartC * len(self.parts))(*[p._c(paged) for p in self.parts])
+            self._arrays[paged] = arr
+        return arr
+
+    def device(self) -> int:
+        """Index of the GPU that holds every tensor of the parts."""
+        if self._device is None:
+            index = None
+            for p in self.parts:
+                for t, name in p.tensors():
+                    if not t.is_cuda:
+                        raise ValueError(f"{name}: a CUDA tensor is required")
+                    if index is None:
+                        index = t.device.index
+                    if t.device.index != index:
+                        raise ValueError(f"{name}: on {t.device}, other tensors on cuda:{index}")
+            self._device = index
+        return self._device
+
+
+def _parts(parts) -> HeadParts:
+    return parts if isinstance(parts, HeadParts) else HeadParts(parts)
+
+
+def _on_current(device: int):
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{device}; the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def head_norm_rope(parts, pos=None, stream=None):
+    """Norm and rotate the heads of N tokens at positions pos [N] int32, one
+    launch for up to four tensors (include/dsa.h, dsa_head_norm_rope).  parts:
+    a :class:`HeadParts`, or a list of :class:`HeadPart`."""
+    parts = _parts(parts)
+    N = parts.N
+    if pos is None and parts.rotates:
+        raise ValueError("pos: required when a part rotates")
+    arr = parts.c(False)
+    (ppos,) = _Args().add(pos, "pos", _I32, N).ptrs()
+    _on_current(parts.device())
+    rc = _lib.dsa_head_norm_rope(arr, len(arr), ppos, N, _stream(stream))
+    _check(rc, "dsa_head_norm_rope")
+
+
+def cache_append_workspace_size() -> int:
+    return int(_lib.dsa_cache_append_workspace_size())
+
+
+def cache_append(layout: PagedLayout, seq, pos, cache, ws, heads=None, stream=None):
+    """Store the new tokens' K (or latent), V and indexer-key rows in the paged
+    pools, normed and rotated on the way, and with heads= their queries in the
+    same launch (include/dsa.h, dsa_cache_append).  cache: :class:`HeadParts`
+    (or a list of :class:`HeadPart`) whose outs are pools; seq, pos [N] int32,
+    or both None: token i is position seq_lens[i] - 1 of sequence i."""
+    cache = _parts(cache)
+    N = cache.N
+    arr = cache.c(True)
+    for p, have in zip(cache.parts, cache.out_bytes):
+        need = _rows(layout, p.out.stride(1)) * p.out.element_size()
+        if have < need:
+            raise ValueError(f"out: a pool of {have} bytes; the layout needs {need}")
+    harr, nh = None, 0
+    if heads is not None:
+        heads = _parts(heads)
+        if heads.N != N:
+            raise ValueError(f"heads: {heads.N} tokens; the cache parts have {N}")
+        harr, nh = heads.c(False), len(heads)
+    a = _Args(layout).add(seq, "seq", _I32, N).add(pos, "pos", _I32, N).add(ws, "ws", _WS)
+    pseq, ppos, pws = a.ptrs()
+    dev = cache.device()
+    if nh and heads.device() != dev:
+        raise ValueError("heads: on another device than the cache parts")
+    _on_current(dev)
+    rc = _lib.dsa_cache_append(layout.c(), pseq, ppos, N, arr, len(arr), harr, nh, pws, ws.numel(),
+                               _stream(stream))
+    _check(rc, "dsa_cache_append")
+
+
+def prefix_attn_decode_workspace_size(B, Hq, Dqk, Dv, prefix_len) -> int:
+    return int(_lib.dsa_prefix_attn_decode_workspace_size(B, Hq, Dqk, Dv, int(prefix_len)))
+
+
+def prefix_attn_decode(layout: PagedLayout, q, k_pool, v_pool, prefix_len, sm_scale, out, lse, ws,
+                       stream=None):
+    """Exact attention of one query per sequence over all its cached positions;
+    the first prefix_len, shared by the batch, are read once (include/dsa.h,
+    dsa_prefix_attn_decode).  prefix_len 0: dense decode attention."""
+    B, Hq, Dqk = q.shape
+    Dv = out.shape[2]
+    if B != layout.batch:
+        raise ValueError(f"q: {B} sequences; the layout has {layout.batch}")
+    ks, vs = k_pool.shape[-1], v_pool.shape[-1]
+    a = _Args(layout).add(q, "q", _BF16).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
+    a.add(v_pool, "v_pool", _BF16, _rows(layout, vs)).add(out, "out", _BF16, B * Hq * Dv)
+    a.add(lse, "lse", _F32, B * Hq).add(ws, "ws", _WS)
+    pq, pk, pv, po, pl, pws = a.ptrs()
+    _on_current(q.device.index)
+    rc = _lib.dsa_prefix_attn_decode(layout.c(), pq, pk, ks, pv, vs, Hq, Dqk, Dv, int(prefix_len),
+                                     float(sm_scale), po, pl, pws, ws.numel(), _stream(stream))
+    _check(rc, "dsa_prefix_attn_decode")
 
 
 def get_status(ws, clear: bool = True, stream=None) -> int:

@@ -273,6 +273,91 @@ int dsa_cache_write(const dsa_paged_layout* layout, const int32_t* seq, const in
                      reinterpret_cast<cudaStream_t>(stream));
 }
 
+// ------------------------------------------------- heads of new tokens --
+int dsa_head_norm_rope(const dsa_head_part* parts, int n_parts, const int32_t* pos, int N,
+                       dsa_stream_t stream) {
+  if (!parts || n_parts < 1 || n_parts > DSA_MAX_HEAD_PARTS || N < 0)
+    return set_error(DSA_ERR_INVALID, "head_norm_rope: 1..4 parts and N >= 0");
+  for (int i = 0; i < n_parts; ++i)
+    if (parts[i].rope_dim && !pos)
+      return set_error(DSA_ERR_INVALID, "head_norm_rope: a rotated part needs pos");
+  return head_transform(nullptr, nullptr, pos, N, nullptr, 0, parts, n_parts, nullptr,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dsa_cache_append_workspace_size(void) { return kWsHeader; }
+
+int dsa_cache_append(const dsa_paged_layout* layout, const int32_t* seq, const int32_t* pos, int N,
+                     const dsa_head_part* cache, int n_cache, const dsa_head_part* heads,
+                     int n_heads, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  LayoutDev lay;
+  int rc = check_layout(layout, &lay);
+  if (rc) return rc;
+  if (!cache || n_cache < 1 || n_cache > DSA_MAX_HEAD_PARTS || n_heads < 0 ||
+      n_heads > DSA_MAX_HEAD_PARTS || (n_heads && !heads))
+    return set_error(DSA_ERR_INVALID, "cache_append: 1..4 cache parts and 0..4 heads parts");
+  if ((seq == nullptr) != (pos == nullptr) || N < 0)
+    return set_error(DSA_ERR_INVALID, "cache_append: seq and pos both or neither, N >= 0");
+  if (!seq && N > layout->batch)
+    return set_error(DSA_ERR_INVALID, "cache_append: the append form needs N <= batch");
+  rc = check_ws(ws, ws_bytes, kWsHeader);
+  if (rc) return rc;
+  return head_transform(&lay, seq, pos, N, cache, n_cache, heads, n_heads,
+                        reinterpret_cast<int*>(ws), reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------- prefix attention --
+size_t dsa_prefix_attn_decode_workspace_size(int B, int Hq, int Dqk, int Dv, int prefix_len) {
+  if (B < 1 || Hq < 1 || Dqk < 1 || Dv < 1 || prefix_len < 0) return kWsHeader;
+  return prefix_attn_ws(B, Hq, Dqk, Dv, prefix_len);
+}
+
+int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const void* k_pool,
+                           int64_t k_row_stride, const void* v_pool, int64_t v_row_stride, int Hq,
+                           int Dqk, int Dv, int prefix_len, float sm_scale, void* out, float* lse,
+                           void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  PrefixAttnParams p{};
+  int rc = check_layout(layout, &p.lay);
+  if (rc) return rc;
+  if (!q || !k_pool || !v_pool || !out)
+    return set_error(DSA_ERR_INVALID, "prefix_attn_decode: NULL tensor pointer");
+  if (prefix_len < 0 || prefix_len > layout->max_seq_len)
+    return set_error(DSA_ERR_INVALID, "prefix_attn_decode: prefix_len must be in 0..max_seq_len");
+  if (k_row_stride < Dqk || v_row_stride < Dv || (k_row_stride % 8) || (v_row_stride % 8) ||
+      k_row_stride > (1LL << 31) || v_row_stride > (1LL << 31))
+    return set_error(DSA_ERR_INVALID,
+                     "prefix_attn_decode: row strides must cover Dqk/Dv and be multiples of 8");
+  if (Hq < 1 || Hq > 128 || Dqk < 8 || Dqk > 576 || Dqk % 8 || Dv < 8 || Dv > 512 || Dv % 8)
+    return set_error(DSA_ERR_UNSUPPORTED,
+                     "prefix_attn_decode: supported Hq 1..128, Dqk 8..576 and Dv 8..512 in "
+                     "multiples of 8");
+  if ((long long)layout->batch > 65535)
+    return set_error(DSA_ERR_UNSUPPORTED, "prefix_attn_decode: batch > 65535");
+  if ((long long)layout->num_blocks * layout->block_size > 0x7fffffffLL)
+    return set_error(DSA_ERR_UNSUPPORTED, "prefix_attn_decode: pools beyond 2^31 - 1 rows");
+  if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return set_error(DSA_ERR_INVALID,
+                     "prefix_attn_decode: q / k_pool / v_pool / out must be 16-byte aligned");
+  if (!(sm_scale > 0.0f) || sm_scale > 3.4e38f)
+    return set_error(DSA_ERR_INVALID, "prefix_attn_decode: sm_scale must be a positive number");
+  rc = check_ws(ws, ws_bytes, prefix_attn_ws(layout->batch, Hq, Dqk, Dv, prefix_len));
+  if (rc) return rc;
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.kp = reinterpret_cast<const __nv_bfloat16*>(k_pool);
+  p.ks = (long long)k_row_stride;
+  p.vp = reinterpret_cast<const __nv_bfloat16*>(v_pool);
+  p.vs = (long long)v_row_stride;
+  p.Hq = Hq;
+  p.Dqk = Dqk;
+  p.Dv = Dv;
+  p.prefix = prefix_len;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = reinterpret_cast<int*>(ws);
+  return launch_prefix_attn(p, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
 static int attn_common(const dsa_paged_layout* layout, const void* q, const void* k_pool,
                        int64_t k_row_stride, const void* v_pool, int64_t v_row_stride, int Hq,
                        int Dqk, int Dv, const int32_t* q_seq, const int32_t* q_pos, int Nq,

@@ -127,6 +127,30 @@ int cache_write(const LayoutDev& lay, const int32_t* seq, const int32_t* pos, in
                 const void* kidx_new, int D_i, int kidx_dtype, void* kidx_pool, int* status,
                 cudaStream_t s, int seq_const = -1);
 
+// head_transform.cu: norm and rotation of the heads of N new tokens; `cache`
+// parts go through the block table of `lay`, `heads` parts to strided tensors.
+// pos NULL: the append form (position seq_lens[i] - 1 of sequence i).
+int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos, int N,
+                   const dsa_head_part* cache, int n_cache, const dsa_head_part* heads,
+                   int n_heads, int* status, cudaStream_t s);
+
+// prefix_attn.cu: one query per sequence over every cached position
+struct PrefixAttnParams {
+  LayoutDev lay;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* kp;
+  long long ks;
+  const __nv_bfloat16* vp;
+  long long vs;
+  int Hq, Dqk, Dv, prefix;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  int* status;
+};
+size_t prefix_attn_ws(int B, int Hq, int Dqk, int Dv, int prefix);
+int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s);
+
 // host-side bookkeeping (dsa_api.cu)
 void count_launch(int n = 1);
 int set_error(int code, const std::string& msg);
