@@ -113,6 +113,21 @@ def test_prefix_attn_matches_64_bits(name):
     p.check(name)
 
 
+def test_many_short_lines_per_pair_stay_in_step():
+    """Sequences of a few tiles with 64 heads: one CTA of a pair has no rows of
+    any line, and must not run ahead of the other.  Many runs of one problem,
+    all equal bit for bit."""
+    need_gpu()
+    dsa = lib()
+    g = np.random.default_rng(5)
+    p = Problem(50, [int(n) for n in g.integers(1, 2049, 48)], bs=64, prefix=0, **LATENT).run(dsa)
+    p.check("first run")
+    first = p.out.clone()
+    for _ in range(200):
+        dsa.prefix_attn_decode(p.lay, p.q, p.kp, p.vp, 0, p.scale, p.out, p.lse, p.ws)
+        assert torch.equal(p.out, first)
+
+
 def test_large_scores_and_peaked_rows():
     """Scores of +-hundreds: the running maximum moves by far more than fp32's
     exponent range between tiles."""
