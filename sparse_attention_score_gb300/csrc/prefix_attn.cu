@@ -60,25 +60,26 @@ constexpr int kRows = 128;             // rows of a pair, 64 per CTA
 constexpr int kMaxChunks = 9;          // 64-dim chunks of a query row
 constexpr int kStages = 7;
 constexpr int kStageBytes = 16384;
-constexpr int kThreads = 192;          // softmax 0-3, producer 4, MMA 5
+constexpr int kThreads = 224;          // softmax 0-3, producers 4 and 6, MMA 5
 constexpr int kMaxPairs = 80;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;          // two S buffers of 128 columns
 constexpr uint32_t kColO = 256;        // O: 128 columns per 256 dims of V
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kTabs = 6;               // tiles whose row table is kept (see the producer)
+constexpr int kTabs = 6;               // tiles whose mask is kept (see the producer)
 
 struct __align__(1024) Smem {
   uint8_t ring[kStages][kStageBytes];
   uint8_t q[kMaxChunks][64 * 128];
   uint8_t p[kTile / 64][64 * 128];
-  int tab[kTabs][kTile];               // physical row of each group of R positions
+  int tab[2][2][kTile];                // per producer, tiles u and u + 1: physical row
+                                       // of each group of R positions
   uint32_t mask[kTabs][kTile / 32];    // usable positions
   int whole[kTabs];                    // every position of the tile is usable
   uint64_t full[kStages], empty[kStages], qfull, qempty, sfull[2], pfull, pvdone;
   uint64_t vfull[kTabs], smsync[2], done;
   float redm[2][2][64];
-  int issued[kStages];
+  int units;  // stages filled, for the drain after a failure
   unsigned long long sum;
   int src, line0, tile0;
   uint32_t tmem_base;
@@ -218,46 +219,51 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
 }
 
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr)
                : "memory");
 }
 
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// mbar_wait for a barrier that the pair's other CTA arrives on.
-__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+// mbar_wait of a whole warp on a barrier that the pair's other CTA may arrive
+// on.  (Default semantics: what crosses CTAs is ordered by the async proxy's
+// own completion, or was made visible to it by its writer's proxy fence.  With
+// .acquire.cluster and .release.cluster the softmax spent 1,100 cycles more
+// per tile.)
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                           uint64_t limit_ns = 2000000000ull) {
-  if (try_wait_cluster(bar, parity)) return true;
+  auto done = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, ok != 0) != 0;
+  };
+  if (done()) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (done()) return true;
     if ((it & 63u) == 0) {
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > limit_ns) return false;
+      if (__any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > limit_ns)) return false;
     }
   }
 }
 
-__device__ __forceinline__ bool warp_pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, pair_wait(bar, parity, abort));
-}
+// The issuing roles run as whole warps on warp-uniform values and one elected
+// lane (always the same) issues: descriptors and coordinates then stay in
+// uniform registers.  Issued from a single-lane branch each MMA cost ~140
+// cycles of register moves, twice its time on the tensor cores.
 
 // TMA box into this CTA's shared memory; its bytes count on `bar` of CTA 0.
-__device__ __forceinline__ void tma_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x,
+__device__ __forceinline__ void tma_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
                                          int y) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];\n\t}\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
@@ -265,19 +271,31 @@ __device__ __forceinline__ void tma_pair(void* dst, const CUtensorMap* map, uint
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
 // Arrive on this barrier of both CTAs when the MMAs issued so far are done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;\n\t}\n" ::"r"(bar),
       "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void expect_tx_elected(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(bar),
+      "r"(bytes)
       : "memory");
 }
 
@@ -303,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smraw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
   const PrefixAttnParams& a = g.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // warp-uniform
   const int rank = (int)cluster_rank();
   launch_dependents();
 
@@ -311,8 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.abort = 0;
     sm.sum = 0;
     sm.src = 0x7fffffff;
+    sm.units = 0;
     for (int i = 0; i < kStages; ++i) {
-      sm.issued[i] = 0;
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
@@ -419,156 +438,175 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers are set up
   tc_fence_after();
-  const uint32_t tbase = sm.tmem_base;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
   const int line0 = sm.line0, tile0 = sm.tile0;
   const int Cq = (a.Dqk + 63) / 64;
   const int cols = (a.Dv + 127) / 128;     // 128-column halves of V instructions
   const int ninst = (cols + 1) / 2;        // instructions of 256 columns; the last may have 128
 
-  if (warp == 4) {
-    // ------------------------------------------------------------ producer --
+  if (warp == 4 || warp == 6) {
+    // ----------------------------------------------------------- producers --
+    // Two warps fill the stages in turn (a stage takes one warp ~350 cycles of
+    // waiting, table reads and issue; the MMAs empty one in 256).
+    const int me = warp >> 1 & 1;  // warp 4: 0, even stages of the sequence; warp 6: 1
     Tiles tk, tv;
     tk.init(g, row_lines, src, line0, tile0, mine);
     tv = tk;
     Ring r;
-    int uk = 0, uv = 0, nq = 0;
+    int uk = 0, uv = 0, nq = 0, unit = 0;
     bool ok = true;
     const int R = g.R, per = kTile / R;  // groups per tile
     const int lgR = 31 - __clz(R);
+    const int none = (int)g.pool_rows;   // a row outside the pool: zeros
     const uint32_t qbar = leader_addr(&sm.qfull);
+    const uint32_t fbar = leader_addr(&sm.full[0]);
+    const uint32_t ring = smem_u32(sm.ring[0]);
+    const uint32_t empty = smem_u32(&sm.empty[0]), full = smem_u32(&sm.full[0]);
+    // physical row of the tile's group i: `none` past the line's end, -1 - none
+    // behind a bad block id
+    auto lookup = [&](const Tiles& t, int i) {
+      const long long p = t.pos() + (long long)i * R;
+      if (p >= t.w.p1) return none;
+      const uint32_t q = (uint32_t)p / (uint32_t)a.lay.bs;
+      const int page = __ldg(&a.lay.bt[(long long)t.w.trow * a.lay.maxb + q]);
+      if (page < 0 || page >= a.lay.nb) return -1 - none;
+      return page * a.lay.bs + (int)((uint32_t)p - q * (uint32_t)a.lay.bs);
+    };
+    int ahead = tk.ok && lane < per ? lookup(tk, lane) : none;  // of the next tile to stage
     while ((tk.ok || uv < uk) && ok) {
       if (tk.ok) {
         const int slot = uk % kTabs;
-        const long long pos = tk.pos();
         const int keys = tk.keys();
-        if (tk.first) {  // the line's queries, once the previous line's last S is done
-          if (nq > 0 && !__all_sync(0xffffffffu, pair_wait(&sm.qempty, (nq - 1) & 1, &sm.abort))) {
-            ok = false;
-            break;
+        int* tab = sm.tab[me][uk & 1];
+        bool bad = false;
+        for (int i = lane; i < per; i += 32) {
+          int row = i < 32 ? ahead : lookup(tk, i);
+          if (row < 0) {
+            bad = true;
+            row = -1;
           }
-          const bool both = tk.w.rows > 64;
-          if (rank == 0 && lane == 0)
-            mbar_arrive_expect_tx(&sm.qfull, (both ? 2 : 1) * Cq * 64 * 128);
-          __syncwarp();
-          if ((rank == 0 || both) && lane < Cq)
-            tma_pair(sm.q[lane], &maps.q, qbar, 64 * lane, tk.w.row0 + 64 * rank);
+          tab[i] = row;
+        }
+        if (bad) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
+        __syncwarp();
+        Tiles tn = tk;
+        tn.next(g, row_lines, src);
+        if (tn.ok && lane < per) ahead = lookup(tn, lane);
+        if (tk.first) {  // the line's queries, once the previous line's last S is done
+          if (me == 0) {
+            if (nq > 0 && !pair_wait(smem_u32(&sm.qempty), (nq - 1) & 1, &sm.abort)) {
+              ok = false;
+              break;
+            }
+            const bool both = tk.w.rows > 64;
+            if (rank == 0) expect_tx_elected(smem_u32(&sm.qfull), (both ? 2 : 1) * Cq * 64 * 128);
+            if (rank == 0 || both)
+              for (int c = 0; c < Cq; ++c)
+                tma_pair(smem_u32(sm.q[0]) + c * 8192, &maps.q, qbar, 64 * c,
+                         tk.w.row0 + 64 * rank);
+          }
           ++nq;
         }
-        // physical rows of the tile's groups.  The slot was tile uk - 6's: at
-        // most the ring's 7 stages of the K and V issued before (at least one
-        // of each per tile) are not yet read by the MMAs, so O of that tile
-        // has begun and its softmax is past the mask.
-        for (int i = lane; i < per; i += 32) {
-          const long long p = pos + (long long)i * R;
-          int row = -1;
-          if (p < tk.w.p1) {
-            const long long v = phys_row(a.lay.bt, a.lay.maxb, a.lay.bs, a.lay.nb, tk.w.trow, p);
-            row = (int)v;
-            if (v < 0) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
+        if (me == 1) {
+          // usable positions of the tile.  The slot was tile uk - 6's: at most
+          // the ring's 7 stages of the K and V issued before (at least one of
+          // each per tile) are not yet read by the MMAs, so O of that tile has
+          // begun and its softmax is past the mask.
+          uint32_t word = 0;
+          if (lane < kTile / 32) {
+            const int k0 = 32 * lane;
+            if (R >= 32) {
+              word = tab[k0 >> lgR] >= 0 ? 0xffffffffu : 0u;
+            } else {
+              for (int i = 0; i < 32; i += R)
+                if (tab[(k0 + i) >> lgR] >= 0) word |= ((1u << R) - 1u) << i;
+            }
+            const int n = keys - k0;
+            if (n < 32) word &= n <= 0 ? 0u : (1u << n) - 1u;
+            sm.mask[slot][lane] = word;
           }
-          sm.tab[slot][i] = row;
-        }
-        __syncwarp();
-        uint32_t word = 0;
-        if (lane < kTile / 32) {
-          const int k0 = 32 * lane;
-          if (R >= 32) {
-            word = sm.tab[slot][k0 >> lgR] >= 0 ? 0xffffffffu : 0u;
-          } else {
-            for (int i = 0; i < 32; i += R)
-              if (sm.tab[slot][(k0 + i) >> lgR] >= 0) word |= ((1u << R) - 1u) << i;
+          const bool whole = __all_sync(0xffffffffu, lane >= kTile / 32 || word == 0xffffffffu);
+          if (lane == 0) {
+            sm.whole[slot] = whole;
+            mbar_arrive(&sm.vfull[slot]);
           }
-          const int n = keys - k0;
-          if (n < 32) word &= n <= 0 ? 0u : (1u << n) - 1u;
-          sm.mask[slot][lane] = word;
-        }
-        const bool whole = __all_sync(0xffffffffu, lane >= kTile / 32 || word == 0xffffffffu);
-        if (lane == 0) {
-          sm.whole[slot] = whole;
-          mbar_arrive(&sm.vfull[slot]);
         }
         const int nb = 128 >> lgR;  // boxes per stage
-        for (int c = 0; c < Cq; ++c) {
-          if (!__all_sync(0xffffffffu, pair_wait(&sm.empty[r.s], r.phase ^ 1, &sm.abort))) {
-            ok = false;
-            break;
-          }
-          if (rank == 0 && lane == 0) {
-            mbar_arrive_expect_tx(&sm.full[r.s], 2 * kStageBytes);
-            ++sm.issued[r.s];
-          }
-          __syncwarp();
-          const uint32_t bar = leader_addr(&sm.full[r.s]);
-          for (int i = lane; i < nb; i += 32) {
-            const int row = sm.tab[slot][rank * nb + i];
-            tma_pair(sm.ring[r.s] + i * R * 128, &maps.k, bar, 64 * c,
-                     row >= 0 ? row : (int)g.pool_rows);
+        const int* mytab = tab + rank * nb;
+        const int row0 = mytab[0] >= 0 ? mytab[0] : none;  // stages of one or two boxes
+        const int row1 = nb < 2 || mytab[1] < 0 ? none : mytab[1];
+        for (int c = 0; c < Cq; ++c, ++unit) {
+          if ((unit & 1) == me) {
+            if (!pair_wait(empty + 8 * r.s, r.phase ^ 1, &sm.abort)) { ok = false; break; }
+            if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * kStageBytes);
+            const uint32_t dst = ring + r.s * kStageBytes, bar = fbar + 8 * r.s;
+            if (nb == 2) {
+              tma_pair(dst, &maps.k, bar, 64 * c, row0);
+              tma_pair(dst + kStageBytes / 2, &maps.k, bar, 64 * c, row1);
+            } else {
+              for (int i = 0; i < nb; ++i)
+                tma_pair(dst + i * R * 128, &maps.k, bar, 64 * c, mytab[i] >= 0 ? mytab[i] : none);
+            }
           }
           r.step();
         }
         if (!ok) break;
         ++uk;
-        tk.next(g, row_lines, src);
+        tk = tn;
       }
       // V runs one tile behind K, as the MMAs do
-      if (uk - uv == 2 || !tk.ok) {
-        if (uv < uk) {
-          const int slot = uv % kTabs;
-          const int keys = tv.keys();
-          const int nkk = (keys + 63) / 64;
-          const int nb = 64 >> lgR;
-          for (int i = 0; i < ninst && ok; ++i) {
-            const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;  // 64-column blocks per CTA
-            const int x0 = 256 * i + 64 * blocks * rank;
-            for (int kk = 0; kk < nkk; ++kk) {
-              if (!__all_sync(0xffffffffu, pair_wait(&sm.empty[r.s], r.phase ^ 1, &sm.abort))) {
-                ok = false;
-                break;
-              }
-              if (rank == 0 && lane == 0) {
-                mbar_arrive_expect_tx(&sm.full[r.s], 2 * blocks * 64 * 128);
-                ++sm.issued[r.s];
-              }
-              __syncwarp();
-              const uint32_t bar = leader_addr(&sm.full[r.s]);
-              for (int e = lane; e < nb * blocks; e += 32) {
-                const int blk = e / nb, gi = e - blk * nb;
+      if ((uk - uv == 2 || !tk.ok) && uv < uk) {
+        const int* tab = sm.tab[me][uv & 1];
+        const int keys = tv.keys();
+        const int nkk = (keys + 63) / 64;
+        const int nb = 64 >> lgR;
+        for (int i = 0; i < ninst && ok; ++i) {
+          const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;  // 64-column blocks per CTA
+          const int x0 = 256 * i + 64 * blocks * rank;
+          for (int kk = 0; kk < nkk; ++kk, ++unit) {
+            if ((unit & 1) == me) {
+              if (!pair_wait(empty + 8 * r.s, r.phase ^ 1, &sm.abort)) { ok = false; break; }
+              if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * blocks * 64 * 128);
+              const uint32_t bar = fbar + 8 * r.s;
+              for (int gi = 0; gi < nb; ++gi) {
                 const int k0 = 64 * kk + gi * R;  // first position of the group in the tile
-                const int row = sm.tab[slot][k0 >> lgR];
-                uint8_t* dst = sm.ring[r.s] + blk * 8192 + gi * R * 128;
-                const int x = x0 + 64 * blk;
-                const int n = keys - k0;  // cached positions of the group
-                if (row < 0 || n >= R) {
-                  tma_pair(dst, &maps.v, bar, x, row >= 0 ? row : (int)g.pool_rows);
-                } else {
-                  // the line ends inside the group
+                const int row = tab[k0 >> lgR];
+                const int n = keys - k0;          // cached positions of the group
+                uint32_t dst = ring + r.s * kStageBytes + gi * R * 128;
+                if (row < 0 || n >= R || n <= 0) {
+                  tma_pair(dst, &maps.v, bar, x0, row >= 0 ? row : none);
+                  if (blocks == 2) tma_pair(dst + 8192, &maps.v, bar, x0 + 64, row >= 0 ? row : none);
+                  continue;
+                }
+                // the line ends inside the group
+                for (int blk = 0; blk < blocks; ++blk, dst += 8192) {
+                  const int x = x0 + 64 * blk;
                   int j = 0;
                   for (; j + 8 <= R; j += 8)
                     if (j + 8 <= n || j >= n) {
-                      tma_pair(dst + j * 128, &maps.v8, bar, x,
-                               j < n ? row + j : (int)g.pool_rows);
+                      tma_pair(dst + j * 128, &maps.v8, bar, x, j < n ? row + j : none);
                     } else {
                       for (int q = j; q < j + 8; ++q)
-                        tma_pair(dst + q * 128, &maps.v1, bar, x,
-                                 q < n ? row + q : (int)g.pool_rows);
+                        tma_pair(dst + q * 128, &maps.v1, bar, x, q < n ? row + q : none);
                     }
                   for (; j < R; ++j)
-                    tma_pair(dst + j * 128, &maps.v1, bar, x, j < n ? row + j : (int)g.pool_rows);
+                    tma_pair(dst + j * 128, &maps.v1, bar, x, j < n ? row + j : none);
                 }
               }
-              r.step();
             }
+            r.step();
           }
-          if (!ok) break;
-          ++uv;
-          tv.next(g, row_lines, src);
         }
+        if (!ok) break;
+        ++uv;
+        tv.next(g, row_lines, src);
       }
     }
+    if (lane == 0) atomicMax(&sm.units, unit);
     if (!ok && lane == 0) fail(sm, a.status);
   } else if (warp == 5) {
     // ---------------------------------------------------------- MMA issuer --
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       Tiles ts, tv;
       ts.init(g, row_lines, src, line0, tile0, mine);
       tv = ts;
@@ -576,63 +614,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       int us = 0, uv = 0, nq = 0;
       bool ok = true;
       const uint32_t idS = instr_desc(kRows, 256, 1, 1, 0, 0);
+      const uint32_t empty = smem_u32(&sm.empty[0]), full = smem_u32(&sm.full[0]);
+      // descriptors: the address field counts 16 bytes; a step of 16 dims or
+      // positions is 32 bytes of a K-major operand, 2048 of V
+      const uint64_t dq = smem_desc(smem_u32(sm.q[0]), 16, 1024, kSwizzle128B);
+      const uint64_t dp = smem_desc(smem_u32(sm.p[0]), 16, 1024, kSwizzle128B);
+      const uint64_t dk = smem_desc(smem_u32(sm.ring[0]), 16, 1024, kSwizzle128B);
+      const uint64_t dv = smem_desc(smem_u32(sm.ring[0]), 8192, 1024, kSwizzle128B);
       while ((ts.ok || uv < us) && ok) {
         if (ts.ok) {
           if (ts.first) {
-            if (!pair_wait(&sm.qfull, nq & 1, &sm.abort)) { ok = false; break; }
+            if (!pair_wait(smem_u32(&sm.qfull), nq & 1, &sm.abort)) { ok = false; break; }
             ++nq;
           }
           // S buffer us % 2 was read before the weights of tile us - 2 were
           // announced, which O of that tile has waited for
           const uint32_t d = tbase + kColS + 128 * (us & 1);
           for (int c = 0; c < Cq; ++c) {
-            if (!pair_wait(&sm.full[r.s], r.phase, &sm.abort)) { ok = false; break; }
+            if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t qa = smem_u32(sm.q[c]), kb = smem_u32(sm.ring[r.s]);
+            const uint64_t qa = dq + 512 * c, kb = dk + 1024 * r.s;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_pair(d, smem_desc(qa + 32 * k, 16, 1024, kSwizzle128B),
-                       smem_desc(kb + 32 * k, 16, 1024, kSwizzle128B), idS, (c + k) > 0 ? 1u : 0u);
-            commit_pair(&sm.empty[r.s]);
+            for (int k = 0; k < 4; ++k) mma_pair(d, qa + 2 * k, kb + 2 * k, idS, c + k);
+            commit_pair(empty + 8 * r.s);
             r.step();
           }
           if (!ok) break;
-          commit_pair(&sm.sfull[us & 1]);
-          if (ts.last) commit_pair(&sm.qempty);
+          commit_pair(smem_u32(&sm.sfull[us & 1]));
+          if (ts.last) commit_pair(smem_u32(&sm.qempty));
           ++us;
           ts.next(g, row_lines, src);
         }
-        if (us - uv == 2 || !ts.ok) {
-          if (uv < us) {
-            const int nkk = (tv.keys() + 63) / 64;
-            if (!pair_wait(&sm.pfull, uv & 1, &sm.abort)) { ok = false; break; }
-            tc_fence_after();
-            for (int i = 0; i < ninst && ok; ++i) {
-              const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;
-              const uint32_t id = instr_desc(kRows, 128 * blocks, 1, 1, 0, 1);
-              const uint32_t d = tbase + kColO + 128 * i;
-              for (int kk = 0; kk < nkk; ++kk) {
-                if (!pair_wait(&sm.full[r.s], r.phase, &sm.abort)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t pa = smem_u32(sm.p[kk]), vb = smem_u32(sm.ring[r.s]);
+        if ((us - uv == 2 || !ts.ok) && uv < us) {
+          const int nkk = (tv.keys() + 63) / 64;
+          if (!pair_wait(smem_u32(&sm.pfull), uv & 1, &sm.abort)) { ok = false; break; }
+          for (int i = 0; i < ninst && ok; ++i) {
+            const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;
+            const uint32_t id = instr_desc(kRows, 128 * blocks, 1, 1, 0, 1);
+            const uint32_t d = tbase + kColO + 128 * i;
+            for (int kk = 0; kk < nkk; ++kk) {
+              if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
+              tc_fence_after();
+              const uint64_t pa = dp + 512 * kk, vb = dv + 1024 * r.s;
+              const int add = tv.first ? kk : 1;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_pair(d, smem_desc(pa + 32 * k, 16, 1024, kSwizzle128B),
-                           smem_desc(vb + 2048 * k, 8192, 1024, kSwizzle128B), id,
-                           (!tv.first || kk + k > 0) ? 1u : 0u);
-                commit_pair(&sm.empty[r.s]);
-                r.step();
-              }
+              for (int k = 0; k < 4; ++k) mma_pair(d, pa + 2 * k, vb + 128 * k, id, add + k);
+              commit_pair(empty + 8 * r.s);
+              r.step();
             }
-            if (!ok) break;
-            commit_pair(&sm.pvdone);
-            ++uv;
-            tv.next(g, row_lines, src);
           }
+          if (!ok) break;
+          commit_pair(smem_u32(&sm.pvdone));
+          ++uv;
+          tv.next(g, row_lines, src);
         }
       }
-      if (!ok) fail(sm, a.status);
-      commit_pair(&sm.done);
+      if (!ok && lane == 0) fail(sm, a.status);
+      commit_pair(smem_u32(&sm.done));
     }
   } else {
     // -------------------------------------------------------------- softmax --
@@ -653,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = -INFINITY;
         l = 0.0f;
       }
-      if (!warp_pair_wait(&sm.sfull[u & 1], (u >> 1) & 1, &sm.abort)) { ok = false; break; }
+      if (!pair_wait(smem_u32(&sm.sfull[u & 1]), (u >> 1) & 1, &sm.abort)) { ok = false; break; }
       tc_fence_after();
       if (live) {
         uint32_t z[4][32];
@@ -661,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld_32cols(ta + 32 * q, z[q]);
         tmem_wait_ld();
-        if (!warp_pair_wait(&sm.vfull[u % kTabs], (u / kTabs) & 1, &sm.abort)) { ok = false; break; }
+        if (!pair_wait(smem_u32(&sm.vfull[u % kTabs]), (u / kTabs) & 1, &sm.abort)) { ok = false; break; }
         if (!sm.whole[u % kTabs]) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -680,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.redm[u & 1][half][row] = mt;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
-        if (!warp_pair_wait(&sm.smsync[warp & 1], sp, &sm.abort)) { ok = false; break; }
+        if (!pair_wait(smem_u32(&sm.smsync[warp & 1]), sp, &sm.abort)) { ok = false; break; }
         sp ^= 1;
         mt = fmaxf(mt, sm.redm[u & 1][half ^ 1][row]) * c;
         float f = 1.0f;
@@ -708,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         // the previous O product has read P, and O may be rescaled
-        if (u > 0 && !warp_pair_wait(&sm.pvdone, (u - 1) & 1, &sm.abort)) { ok = false; break; }
+        if (u > 0 && !pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) { ok = false; break; }
         tc_fence_after();
         if (!t.first && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
@@ -730,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-      } else if (u > 0 && !warp_pair_wait(&sm.pvdone, (u - 1) & 1, &sm.abort)) {
+      } else if (u > 0 && !pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) {
         // a warp without rows keeps in step: two arrivals of it in one phase
         // of pfull would stand for a warp that has not written its weights
         ok = false;
@@ -740,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) arrive_cluster(pbar);
       if (t.last) {
         // this pair's partial of the line: O out of TMEM, unnormalised
-        if (!warp_pair_wait(&sm.pvdone, u & 1, &sm.abort)) { ok = false; break; }
+        if (!pair_wait(smem_u32(&sm.pvdone), u & 1, &sm.abort)) { ok = false; break; }
         tc_fence_after();
         if (live) {
           const int slot = t.w.pre ? pair + t.w.line
@@ -768,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm.redm[(u + 1) & 1][half][row] = l;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
-          if (!warp_pair_wait(&sm.smsync[warp & 1], sp, &sm.abort)) { ok = false; break; }
+          if (!pair_wait(smem_u32(&sm.smsync[warp & 1]), sp, &sm.abort)) { ok = false; break; }
           sp ^= 1;
           if (half == 0)
             reinterpret_cast<float2*>(g.ml)[(size_t)slot * kRows + 64 * rank + row] =
@@ -776,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // nobody writes redm[(u + 1) & 1] again before this read is done
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
-          if (!warp_pair_wait(&sm.smsync[warp & 1], sp, &sm.abort)) { ok = false; break; }
+          if (!pair_wait(smem_u32(&sm.smsync[warp & 1]), sp, &sm.abort)) { ok = false; break; }
           sp ^= 1;
         }
       }
@@ -787,13 +825,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (warp == 0) {
     int never = 0;
     // MMAs of the pair done; after a failure also the copies in flight
-    pair_wait(&sm.done, 0, &never, 100000000ull);
+    pair_wait(smem_u32(&sm.done), 0, &never, 100000000ull);
     if (sm.abort && rank == 0) {
-      for (int i = 0; i < kStages; ++i)
-        if (sm.issued[i] > 0) pair_wait(&sm.full[i], (sm.issued[i] - 1) & 1, &never, 10000000ull);
+      for (int i = 0; i < kStages; ++i) {
+        const int n = (sm.units - i + kStages - 1) / kStages;  // fills of this stage
+        if (n > 0) pair_wait(smem_u32(&sm.full[i]), (n - 1) & 1, &never, 10000000ull);
+      }
     }
   }
   tc_fence_before();
