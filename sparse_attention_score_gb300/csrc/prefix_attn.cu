@@ -58,30 +58,28 @@ using namespace sm100;
 constexpr int kTile = 256;             // positions per tile
 constexpr int kRows = 128;             // rows of a pair, 64 per CTA
 constexpr int kMaxChunks = 9;          // 64-dim chunks of a query row
-constexpr int kStages = 7;
+constexpr int kStagesK = 4, kStagesV = 3;
 constexpr int kStageBytes = 16384;
-constexpr int kThreads = 224;          // softmax 0-3, producers 4 and 6, MMA 5
+constexpr int kThreads = 256;          // softmax 0-3, K 4 (producer) and 5 (MMA), V 6 and 7
 constexpr int kMaxPairs = 80;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;          // two S buffers of 128 columns
 constexpr uint32_t kColO = 256;        // O: 128 columns per 256 dims of V
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kTabs = 6;               // tiles whose mask is kept (see the producer)
+constexpr int kTabs = 8;               // tiles whose mask is kept (see the K producer)
 
 struct __align__(1024) Smem {
-  uint8_t ring[kStages][kStageBytes];
+  uint8_t ringk[kStagesK][kStageBytes];
+  uint8_t ringv[kStagesV][kStageBytes];
   uint8_t q[kMaxChunks][64 * 128];
   uint8_t p[kTile / 64][64 * 128];
-  int tab[2][2][kTile];                // per producer, tiles u and u + 1: physical row
-                                       // of each group of R positions
+  int tab[2][kTile];                   // per producer: physical row of each group of R positions
   uint32_t mask[kTabs][kTile / 32];    // usable positions
   int whole[kTabs];                    // every position of the tile is usable
-  uint64_t full[kStages], empty[kStages], qfull, qempty, sfull[2], pfull, pvdone;
+  uint64_t fullk[kStagesK], emptyk[kStagesK], fullv[kStagesV], emptyv[kStagesV], qfull, qempty, sfull[2], sfree[2], pfull, pvdone;
   uint64_t vfull[kTabs], smsync[2], done;
   float redm[2][2][64];
-  int units;  // stages filled, for the drain after a failure
-  unsigned long long sum;
-  int src, line0, tile0;
+  int fills[2];  // stages filled, for the drain after a failure
   uint32_t tmem_base;
   int abort;
 };
@@ -95,26 +93,32 @@ struct Maps {
 struct Geo {
   PrefixAttnParams a;
   int R;            // rows per box
+  int lgbs;         // log2 of the page size, or -1
   int row_tiles;    // of 128 rows over B * Hq
   int prefix_tiles;
   int Rl;           // rows of a sequence's partial: 64 or 128
-  long long pool_rows;
-  long long* off;   // [B + 1] first tile of each sequence's line, then the total
+  int pool_rows;
+  long long* off;   // [B + 1] first unit of each sequence's line, then the total
   float* ml;        // [slot][128][2]
   float* po;        // prefix slots [Dv / 4][128][4], then sequence slots [Dv / 4][Rl][4]
   int slots_pre;
 };
 
-__device__ __forceinline__ long long seq_len(const PrefixAttnParams& a, int b) {
-  long long L = __ldg(&a.lay.seq_lens[b]);
+__device__ __forceinline__ int seq_len(const PrefixAttnParams& a, int b) {
+  const int L = __ldg(&a.lay.seq_lens[b]);
   const long long cap = (long long)a.lay.maxb * a.lay.bs;
-  if (L > cap) L = cap;
-  return L < 0 ? 0 : L;
+  return L < 0 ? 0 : (L > cap ? (int)cap : L);
 }
 
-__device__ __forceinline__ int own_tiles(const PrefixAttnParams& a, long long L) {
-  const long long n = L >= a.prefix ? L - a.prefix : L;
-  return (int)((n + kTile - 1) / kTile);
+__device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + kTile - 1) / kTile); }
+
+// A line of T tiles counts T + 1 units in the split over the pairs: starting
+// and ending one (queries in, first scores, O out) costs about one tile more
+// (7,000 cycles against 8,000 measured with 64 short lines on the last pair;
+// unit 0 of a line has no tile).
+__device__ __forceinline__ int own_units(const PrefixAttnParams& a, int L) {
+  const int t = tiles_of(L >= a.prefix ? L - a.prefix : L);
+  return t > 0 ? t + 1 : 0;
 }
 
 __device__ __forceinline__ float* slot_po(const Geo& g, int slot, bool pre) {
@@ -123,85 +127,140 @@ __device__ __forceinline__ float* slot_po(const Geo& g, int slot, bool pre) {
                    (size_t)(slot - g.slots_pre) * g.Rl * g.a.Dv;
 }
 
-// The tiles [lo, hi) of one pair, line by line.
-struct Walker {
-  int line;          // row tiles first, then sequences
-  int t, t1;         // this pair's tiles of the line: [t, t1)
-  long long left;    // tiles left in this pair, this line's included
-  bool pre;
-  int rows;          // rows of the line
-  int row0;          // first row of the line
+// The split, computed by each warp for itself.
+struct Plan {
+  int src;             // first sequence that has the whole prefix
+  int row_lines;       // lines over the prefix
+  long long pre, total;
+  long long mine;      // units of this pair
+  int line0, unit0;    // where they start
+};
+
+__device__ __forceinline__ long long warp_total(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// A value that every lane has, known to be so: what the compiler cannot prove
+// warp-uniform (anything loaded) costs each issued copy and MMA a loop over
+// lanes on its operands.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+__device__ __forceinline__ Plan make_plan(const Geo& g, int pair, int pairs, int lane) {
+  const PrefixAttnParams& a = g.a;
+  Plan p;
+  long long sum = 0;
+  int src = 0x7fffffff, n0 = 0;
+#pragma unroll 4
+  for (int b = lane; b < a.lay.batch; b += 32) {
+    const int L = seq_len(a, b);
+    const int n = own_units(a, L);
+    if (b == lane) n0 = n;
+    sum += n;
+    if (L >= a.prefix && b < src) src = b;
+  }
+  sum = __shfl_sync(0xffffffffu, warp_total(sum), 0);
+  p.src = uniform(__reduce_min_sync(0xffffffffu, src));
+  p.row_lines = (a.prefix > 0 && p.src != 0x7fffffff) ? g.row_tiles : 0;
+  p.pre = (long long)p.row_lines * (g.prefix_tiles + 1);
+  p.total = p.pre + sum;
+  const int G = p.total < pairs ? (int)p.total : pairs;
+  const long long lo = pair < G ? p.total * pair / G : 0;
+  p.mine = pair < G ? p.total * (pair + 1) / G - lo : 0;
+  p.line0 = p.unit0 = 0;
+  if (p.mine > 0) {
+    if (lo < p.pre) {
+      p.line0 = (int)(lo / (g.prefix_tiles + 1));
+      p.unit0 = (int)(lo - (long long)p.line0 * (g.prefix_tiles + 1));
+    } else {
+      long long at = p.pre;
+      for (int b0 = 0; b0 < a.lay.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const int n = b0 == 0 ? n0 : (b < a.lay.batch ? own_units(a, seq_len(a, b)) : 0);
+        const long long end = at + warp_scan(n, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, end > lo);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          p.line0 = p.row_lines + b0 + l;
+          p.unit0 = (int)(lo - __shfl_sync(0xffffffffu, end - n, l));
+          break;
+        }
+        at = __shfl_sync(0xffffffffu, end, 31);
+      }
+      p.line0 = uniform(p.line0);
+      p.unit0 = uniform(p.unit0);
+    }
+  }
+  return p;
+}
+
+// The tiles of one pair, line by line: t in [first_t, t1) of `line`.
+struct Tiles {
+  int line, t, t1, first_t;
+  int row0, rows;    // rows of the line
   int trow;          // row of the block table
-  long long p0, p1;  // positions of the line
+  int p0, p1;        // positions of the line
+  long long left;    // units of this pair behind this line
   bool ok;
 
-  __device__ void load(const Geo& g, int row_lines, int src) {
-    if (line < row_lines) {
-      pre = true;
+  // units [v, ...) of the line; false if this pair has no tile of them
+  __device__ bool load(const Geo& g, const Plan& p, int v) {
+    if (line < p.row_lines) {
       row0 = line * kRows;
       const int n = g.a.lay.batch * g.a.Hq - row0;
       rows = n < kRows ? n : kRows;
-      trow = src;
+      trow = p.src;
       p0 = 0;
       p1 = g.a.prefix;
     } else {
-      pre = false;
-      const int b = line - row_lines;
-      row0 = b * g.a.Hq;
+      trow = line - p.row_lines;
+      row0 = trow * g.a.Hq;
       rows = g.a.Hq;
-      trow = b;
-      p1 = seq_len(g.a, b);
+      p1 = uniform(seq_len(g.a, trow));
       p0 = p1 >= g.a.prefix ? g.a.prefix : 0;
     }
-    const long long n = (p1 - p0 + kTile - 1) / kTile - t;
-    t1 = t + (int)(n < left ? n : left);
+    const int T = tiles_of(p1 - p0);
+    const int n = T > 0 ? T + 1 - v : 0;
+    const int take = n < left ? n : (int)left;
+    left -= take;
+    t = first_t = v > 0 ? v - 1 : 0;
+    t1 = v + take - 1;
+    return t1 > t;
   }
-  __device__ void init(const Geo& g, int row_lines, int src, int line0, int tile0, long long n) {
-    line = line0;
-    t = tile0;
-    left = n;
-    ok = n > 0;
-    if (ok) load(g, row_lines, src);
-  }
-  // the next line with tiles, once t has reached t1
-  __device__ void next_line(const Geo& g, int row_lines, int src, long long used) {
-    left -= used;
-    ok = left > 0;
-    t = 0;
-    while (ok) {
+  __device__ void next_line(const Geo& g, const Plan& p) {
+    ok = false;
+    while (left > 0 && !ok) {
       ++line;
-      load(g, row_lines, src);
-      if (t1 > 0) break;
+      ok = load(g, p, 0);
     }
   }
-};
-
-// One tile after the other over the lines.
-struct Tiles {
-  Walker w;
-  int first_t;
-  bool ok, first, last;
-  __device__ void set() {
-    ok = w.ok;
-    first = ok && w.t == first_t;
-    last = ok && w.t == w.t1 - 1;
+  __device__ void init(const Geo& g, const Plan& p) {
+    line = p.line0;
+    left = p.mine;
+    t = t1 = first_t = 0;
+    ok = left > 0 && load(g, p, p.unit0);
+    if (!ok) next_line(g, p);
   }
-  __device__ void init(const Geo& g, int rl, int src, int line0, int tile0, long long n) {
-    w.init(g, rl, src, line0, tile0, n);
-    first_t = w.t;
-    set();
+  __device__ __forceinline__ void next(const Geo& g, const Plan& p) {
+    if (++t >= t1) next_line(g, p);
   }
-  __device__ void next(const Geo& g, int rl, int src) {
-    if (++w.t >= w.t1) {
-      w.next_line(g, rl, src, w.t1 - first_t);
-      first_t = 0;
-    }
-    set();
-  }
-  __device__ long long pos() const { return w.p0 + (long long)w.t * kTile; }
-  __device__ int keys() const {
-    const long long n = w.p1 - pos();
-    return n < kTile ? (int)n : kTile;
+  __device__ __forceinline__ bool first() const { return t == first_t; }
+  __device__ __forceinline__ bool last() const { return t + 1 == t1; }
+  __device__ __forceinline__ bool pre(const Plan& p) const { return line < p.row_lines; }
+  __device__ __forceinline__ int pos() const { return p0 + t * kTile; }
+  __device__ __forceinline__ int keys() const {
+    const int n = p1 - pos();
+    return n < kTile ? n : kTile;
   }
 };
 
@@ -304,17 +363,29 @@ __device__ __forceinline__ void fail(Smem& sm, int* status) {
   flag_status(status, DSA_STATUS_TIMEOUT);
 }
 
-// Ring position of the producer and of the MMA issuer.
+// Position in a ring of n stages.
+template <int n>
 struct Ring {
   int s = 0;
   uint32_t phase = 0;
-  __device__ void step() {
-    if (++s == kStages) {
+  __device__ __forceinline__ void step() {
+    if (++s == n) {
       s = 0;
       phase ^= 1;
     }
   }
 };
+
+// Physical row of group i of a tile: `none` (a row outside the pool, which
+// loads as zeros) past the line's end, -1 behind a bad block id.
+__device__ __forceinline__ int group_row(const Geo& g, const Tiles& t, int i, int lgR) {
+  const unsigned p = (unsigned)t.pos() + (unsigned)(i << lgR);
+  if (p >= (unsigned)t.p1) return g.pool_rows;
+  const unsigned q = g.lgbs >= 0 ? p >> g.lgbs : p / (unsigned)g.a.lay.bs;
+  const int page = __ldg(&g.a.lay.bt[(long long)t.trow * g.a.lay.maxb + q]);
+  if (page < 0 || page >= g.a.lay.nb) return -1;
+  return page * g.a.lay.bs + (int)(p - q * (unsigned)g.a.lay.bs);
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     k_prefix_attn(const __grid_constant__ Maps maps, const __grid_constant__ Geo g) {
@@ -328,23 +399,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     sm.abort = 0;
-    sm.sum = 0;
-    sm.src = 0x7fffffff;
-    sm.units = 0;
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
+    sm.fills[0] = sm.fills[1] = 0;
+    for (int i = 0; i < kStagesK; ++i) {
+      mbar_init(&sm.fullk[i], 1);
+      mbar_init(&sm.emptyk[i], 1);
+    }
+    for (int i = 0; i < kStagesV; ++i) {
+      mbar_init(&sm.fullv[i], 1);
+      mbar_init(&sm.emptyv[i], 1);
     }
     mbar_init(&sm.qfull, 1);
     mbar_init(&sm.qempty, 1);
     mbar_init(&sm.sfull[0], 1);
     mbar_init(&sm.sfull[1], 1);
-    mbar_init(&sm.pfull, 8);  // one arrival per softmax warp of both CTAs
+    mbar_init(&sm.sfree[0], 8);  // one arrival per softmax warp of both CTAs
+    mbar_init(&sm.sfree[1], 8);
+    mbar_init(&sm.pfull, 8);
     mbar_init(&sm.pvdone, 1);
     for (int i = 0; i < kTabs; ++i) mbar_init(&sm.vfull[i], 1);
     mbar_init(&sm.smsync[0], 2);
     mbar_init(&sm.smsync[1], 2);
-    mbar_init(&sm.done, 1);
+    mbar_init(&sm.done, 2);
     fence_mbar_init();
   }
   if (warp == 5) {
@@ -361,313 +436,270 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  grid_dependency_wait();  // everything below reads inputs of earlier kernels
-
-  // total tiles, and the first sequence that has the whole prefix
-  {
-    unsigned long long n = 0;
-    int src = 0x7fffffff;
-    for (int b = threadIdx.x; b < a.lay.batch; b += kThreads) {
-      const long long L = seq_len(a, b);
-      n += own_tiles(a, L);
-      if (L >= a.prefix && b < src) src = b;
-      if (blockIdx.x == 0 && __ldg(&a.lay.seq_lens[b]) > L) flag_status(a.status, DSA_STATUS_BAD_LENGTH);
-    }
-    if (n) atomicAdd(&sm.sum, n);
-    if (src != 0x7fffffff) atomicMin(&sm.src, src);
-  }
-  __syncthreads();
-  const int src = sm.src;
-  const int row_lines = (a.prefix > 0 && src != 0x7fffffff) ? g.row_tiles : 0;
-  const long long pre_tiles = (long long)row_lines * g.prefix_tiles;
-  const long long total = pre_tiles + (long long)sm.sum;
-  int G = gridDim.x >> 1;
-  if (G > total) G = (int)total;
-  const int pair = blockIdx.x >> 1;
-  const long long lo = pair < G ? total * pair / G : 0;
-  const long long mine = pair < G ? total * (pair + 1) / G - lo : 0;
-  if (warp == 4) {  // line and tile of `lo`
-    int line0 = 0, tile0 = 0;
-    if (mine > 0) {
-      if (lo < pre_tiles) {
-        line0 = (int)(lo / g.prefix_tiles);
-        tile0 = (int)(lo - (long long)line0 * g.prefix_tiles);
-      } else {
-        long long at = pre_tiles;
-        for (int b0 = 0; b0 < a.lay.batch; b0 += 32) {
-          const int n = b0 + lane < a.lay.batch ? own_tiles(a, seq_len(a, b0 + lane)) : 0;
-          long long inc = n;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-          }
-          const unsigned hit = __ballot_sync(0xffffffffu, at + inc > lo);
-          if (hit) {
-            const int l = __ffs(hit) - 1;
-            const long long end = at + __shfl_sync(0xffffffffu, inc, l);
-            line0 = row_lines + b0 + l;
-            tile0 = (int)(lo - (end - __shfl_sync(0xffffffffu, n, l)));
-            break;
-          }
-          at += __shfl_sync(0xffffffffu, inc, 31);
-        }
-      }
-    }
-    if (lane == 0) {
-      sm.line0 = line0;
-      sm.tile0 = tile0;
-    }
-  }
-  if (blockIdx.x == 1 && warp == 0) {  // first tile of every sequence, for the merge
-    long long at = pre_tiles;
-    for (int b0 = 0; b0 < a.lay.batch; b0 += 32) {
-      const int b = b0 + lane;
-      const int n = b < a.lay.batch ? own_tiles(a, seq_len(a, b)) : 0;
-      long long inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (b < a.lay.batch) g.off[b] = at + inc - n;
-      at += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) g.off[a.lay.batch] = total;
-  }
-  __syncthreads();
   cluster_sync_all();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
-  const int line0 = sm.line0, tile0 = sm.tile0;
+  grid_dependency_wait();  // everything below reads inputs of earlier kernels
+
+  const int pair = blockIdx.x >> 1;
+  const Plan plan = make_plan(g, pair, gridDim.x >> 1, lane);
+  if (blockIdx.x == 1 && warp == 0) {
+    // for the merge: first unit of every sequence's line
+    long long at = plan.pre;
+    for (int b0 = 0; b0 < a.lay.batch; b0 += 32) {
+      const int b = b0 + lane;
+      int n = 0;
+      if (b < a.lay.batch) {
+        const int L = seq_len(a, b);
+        n = own_units(a, L);
+        if (__ldg(&a.lay.seq_lens[b]) > L) flag_status(a.status, DSA_STATUS_BAD_LENGTH);
+      }
+      const long long end = at + warp_scan(n, lane);
+      if (b < a.lay.batch) g.off[b] = end - n;
+      at = __shfl_sync(0xffffffffu, end, 31);
+    }
+    if (lane == 0) g.off[a.lay.batch] = plan.total;
+  }
   const int Cq = (a.Dqk + 63) / 64;
   const int cols = (a.Dv + 127) / 128;     // 128-column halves of V instructions
   const int ninst = (cols + 1) / 2;        // instructions of 256 columns; the last may have 128
 
-  if (warp == 4 || warp == 6) {
-    // ----------------------------------------------------------- producers --
-    // Two warps fill the stages in turn (a stage takes one warp ~350 cycles of
-    // waiting, table reads and issue; the MMAs empty one in 256).
-    const int me = warp >> 1 & 1;  // warp 4: 0, even stages of the sequence; warp 6: 1
-    Tiles tk, tv;
-    tk.init(g, row_lines, src, line0, tile0, mine);
-    tv = tk;
-    Ring r;
-    int uk = 0, uv = 0, nq = 0, unit = 0;
+  const int R = g.R, per = kTile / R;  // groups per tile
+  const int lgR = 31 - __clz(R);
+  const int none = g.pool_rows;
+
+  if (warp == 4) {
+    // ---------------------------------------------------------- K producer --
+    // Queries, keys, and which positions of each tile are usable.
+    Tiles t;
+    t.init(g, plan);
+    Ring<kStagesK> r;
+    int u = 0, nq = 0;
     bool ok = true;
-    const int R = g.R, per = kTile / R;  // groups per tile
-    const int lgR = 31 - __clz(R);
-    const int none = (int)g.pool_rows;   // a row outside the pool: zeros
-    const uint32_t qbar = leader_addr(&sm.qfull);
-    const uint32_t fbar = leader_addr(&sm.full[0]);
-    const uint32_t ring = smem_u32(sm.ring[0]);
-    const uint32_t empty = smem_u32(&sm.empty[0]), full = smem_u32(&sm.full[0]);
-    // physical row of the tile's group i: `none` past the line's end, -1 - none
-    // behind a bad block id
-    auto lookup = [&](const Tiles& t, int i) {
-      const long long p = t.pos() + (long long)i * R;
-      if (p >= t.w.p1) return none;
-      const uint32_t q = (uint32_t)p / (uint32_t)a.lay.bs;
-      const int page = __ldg(&a.lay.bt[(long long)t.w.trow * a.lay.maxb + q]);
-      if (page < 0 || page >= a.lay.nb) return -1 - none;
-      return page * a.lay.bs + (int)((uint32_t)p - q * (uint32_t)a.lay.bs);
-    };
-    int ahead = tk.ok && lane < per ? lookup(tk, lane) : none;  // of the next tile to stage
-    while ((tk.ok || uv < uk) && ok) {
-      if (tk.ok) {
-        const int slot = uk % kTabs;
-        const int keys = tk.keys();
-        int* tab = sm.tab[me][uk & 1];
-        bool bad = false;
-        for (int i = lane; i < per; i += 32) {
-          int row = i < 32 ? ahead : lookup(tk, i);
-          if (row < 0) {
-            bad = true;
-            row = -1;
-          }
-          tab[i] = row;
-        }
-        if (bad) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
-        __syncwarp();
-        Tiles tn = tk;
-        tn.next(g, row_lines, src);
-        if (tn.ok && lane < per) ahead = lookup(tn, lane);
-        if (tk.first) {  // the line's queries, once the previous line's last S is done
-          if (me == 0) {
-            if (nq > 0 && !pair_wait(smem_u32(&sm.qempty), (nq - 1) & 1, &sm.abort)) {
-              ok = false;
-              break;
-            }
-            const bool both = tk.w.rows > 64;
-            if (rank == 0) expect_tx_elected(smem_u32(&sm.qfull), (both ? 2 : 1) * Cq * 64 * 128);
-            if (rank == 0 || both)
-              for (int c = 0; c < Cq; ++c)
-                tma_pair(smem_u32(sm.q[0]) + c * 8192, &maps.q, qbar, 64 * c,
-                         tk.w.row0 + 64 * rank);
-          }
-          ++nq;
-        }
-        if (me == 1) {
-          // usable positions of the tile.  The slot was tile uk - 6's: at most
-          // the ring's 7 stages of the K and V issued before (at least one of
-          // each per tile) are not yet read by the MMAs, so O of that tile has
-          // begun and its softmax is past the mask.
-          uint32_t word = 0;
-          if (lane < kTile / 32) {
-            const int k0 = 32 * lane;
-            if (R >= 32) {
-              word = tab[k0 >> lgR] >= 0 ? 0xffffffffu : 0u;
-            } else {
-              for (int i = 0; i < 32; i += R)
-                if (tab[(k0 + i) >> lgR] >= 0) word |= ((1u << R) - 1u) << i;
-            }
-            const int n = keys - k0;
-            if (n < 32) word &= n <= 0 ? 0u : (1u << n) - 1u;
-            sm.mask[slot][lane] = word;
-          }
-          const bool whole = __all_sync(0xffffffffu, lane >= kTile / 32 || word == 0xffffffffu);
-          if (lane == 0) {
-            sm.whole[slot] = whole;
-            mbar_arrive(&sm.vfull[slot]);
-          }
-        }
-        const int nb = 128 >> lgR;  // boxes per stage
-        const int* mytab = tab + rank * nb;
-        const int row0 = mytab[0] >= 0 ? mytab[0] : none;  // stages of one or two boxes
-        const int row1 = nb < 2 || mytab[1] < 0 ? none : mytab[1];
-        for (int c = 0; c < Cq; ++c, ++unit) {
-          if ((unit & 1) == me) {
-            if (!pair_wait(empty + 8 * r.s, r.phase ^ 1, &sm.abort)) { ok = false; break; }
-            if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * kStageBytes);
-            const uint32_t dst = ring + r.s * kStageBytes, bar = fbar + 8 * r.s;
-            if (nb == 2) {
-              tma_pair(dst, &maps.k, bar, 64 * c, row0);
-              tma_pair(dst + kStageBytes / 2, &maps.k, bar, 64 * c, row1);
-            } else {
-              for (int i = 0; i < nb; ++i)
-                tma_pair(dst + i * R * 128, &maps.k, bar, 64 * c, mytab[i] >= 0 ? mytab[i] : none);
-            }
-          }
-          r.step();
-        }
-        if (!ok) break;
-        ++uk;
-        tk = tn;
+    const uint32_t qbar = leader_addr(&sm.qfull), fbar = leader_addr(&sm.fullk[0]);
+    const uint32_t ring = smem_u32(sm.ringk[0]);
+    const uint32_t empty = smem_u32(&sm.emptyk[0]), full = smem_u32(&sm.fullk[0]);
+    const int nb = 128 >> lgR;  // boxes per stage
+    int* tab = sm.tab[0];
+    const int* mytab = tab + rank * nb;
+    int ahead = t.ok && lane < per ? group_row(g, t, lane, lgR) : none;  // of the next tile
+    while (t.ok) {
+      bool bad = lane < per && ahead < 0;
+      if (lane < per) tab[lane] = ahead;
+      for (int i = lane + 32; i < per; i += 32) {
+        const int row = group_row(g, t, i, lgR);
+        bad |= row < 0;
+        tab[i] = row;
       }
-      // V runs one tile behind K, as the MMAs do
-      if ((uk - uv == 2 || !tk.ok) && uv < uk) {
-        const int* tab = sm.tab[me][uv & 1];
-        const int keys = tv.keys();
-        const int nkk = (keys + 63) / 64;
-        const int nb = 64 >> lgR;
-        for (int i = 0; i < ninst && ok; ++i) {
-          const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;  // 64-column blocks per CTA
-          const int x0 = 256 * i + 64 * blocks * rank;
-          for (int kk = 0; kk < nkk; ++kk, ++unit) {
-            if ((unit & 1) == me) {
-              if (!pair_wait(empty + 8 * r.s, r.phase ^ 1, &sm.abort)) { ok = false; break; }
-              if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * blocks * 64 * 128);
-              const uint32_t bar = fbar + 8 * r.s;
-              for (int gi = 0; gi < nb; ++gi) {
-                const int k0 = 64 * kk + gi * R;  // first position of the group in the tile
-                const int row = tab[k0 >> lgR];
-                const int n = keys - k0;          // cached positions of the group
-                uint32_t dst = ring + r.s * kStageBytes + gi * R * 128;
+      if (bad) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
+      __syncwarp();
+      const bool first = t.first();
+      const int keys = t.keys(), row0 = t.row0;
+      const bool both = t.rows > 64;
+      t.next(g, plan);
+      if (t.ok && lane < per) ahead = group_row(g, t, lane, lgR);
+      {
+        // Usable positions.  The slot was tile u - 8's: K of tile u - 5 at
+        // the latest has left the ring of 4 stages, so S of it was issued, so
+        // the softmax of tile u - 7 is done.
+        const int slot = u % kTabs;
+        uint32_t word = 0;
+        if (lane < kTile / 32) {
+          const int k0 = 32 * lane;
+          if (R >= 32) {
+            word = tab[k0 >> lgR] >= 0 ? 0xffffffffu : 0u;
+          } else {
+            for (int i = 0; i < 32; i += R)
+              if (tab[(k0 + i) >> lgR] >= 0) word |= ((1u << R) - 1u) << i;
+          }
+          const int n = keys - k0;
+          if (n < 32) word &= n <= 0 ? 0u : (1u << n) - 1u;
+          sm.mask[slot][lane] = word;
+        }
+        const bool whole = __all_sync(0xffffffffu, lane >= kTile / 32 || word == 0xffffffffu);
+        if (lane == 0) {
+          sm.whole[slot] = whole;
+          mbar_arrive(&sm.vfull[slot]);
+        }
+      }
+      if (first) {  // the line's queries, once the previous line's last S is done
+        if (nq > 0 && !pair_wait(smem_u32(&sm.qempty), (nq - 1) & 1, &sm.abort)) { ok = false; break; }
+        if (rank == 0) expect_tx_elected(smem_u32(&sm.qfull), (both ? 2 : 1) * Cq * 64 * 128);
+        if (rank == 0 || both)
+          for (int c = 0; c < Cq; ++c)
+            tma_pair(smem_u32(sm.q[0]) + c * 8192, &maps.q, qbar, 64 * c, row0 + 64 * rank);
+        ++nq;
+      }
+      const int r0 = uniform(mytab[0] >= 0 ? mytab[0] : none);  // a stage of two boxes
+      const int r1 = uniform(nb < 2 || mytab[1] < 0 ? none : mytab[1]);
+      for (int c = 0; c < Cq; ++c) {
+        if (!pair_wait(empty + 8 * r.s, r.phase ^ 1, &sm.abort)) { ok = false; break; }
+        if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * kStageBytes);
+        const uint32_t dst = ring + r.s * kStageBytes, bar = fbar + 8 * r.s;
+        if (nb == 2) {
+          tma_pair(dst, &maps.k, bar, 64 * c, r0);
+          tma_pair(dst + kStageBytes / 2, &maps.k, bar, 64 * c, r1);
+        } else {
+          for (int i = 0; i < nb; ++i)
+            tma_pair(dst + ((i << lgR) << 7), &maps.k, bar, 64 * c, mytab[i] >= 0 ? mytab[i] : none);
+        }
+        r.step();
+        if (lane == 0) sm.fills[0] = u * Cq + c + 1;
+      }
+      if (!ok) break;
+      ++u;
+      __syncwarp();
+    }
+    if (!ok && lane == 0) fail(sm, a.status);
+  } else if (warp == 6) {
+    // ---------------------------------------------------------- V producer --
+    Tiles t;
+    t.init(g, plan);
+    Ring<kStagesV> r;
+    int n_fills = 0;
+    bool ok = true;
+    const uint32_t fbar = leader_addr(&sm.fullv[0]);
+    const uint32_t ring = smem_u32(sm.ringv[0]);
+    const uint32_t empty = smem_u32(&sm.emptyv[0]), full = smem_u32(&sm.fullv[0]);
+    const int nb = 64 >> lgR;
+    int* tab = sm.tab[1];
+    int ahead = t.ok && lane < per ? group_row(g, t, lane, lgR) : none;
+    while (t.ok) {
+      if (lane < per) tab[lane] = ahead;
+      for (int i = lane + 32; i < per; i += 32) tab[i] = group_row(g, t, i, lgR);
+      __syncwarp();
+      const int keys = t.keys();
+      const int nkk = (keys + 63) >> 6;
+      t.next(g, plan);
+      if (t.ok && lane < per) ahead = group_row(g, t, lane, lgR);
+      for (int i = 0; i < ninst && ok; ++i) {
+        const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;  // 64-column blocks per CTA
+        const int x0 = 256 * i + 64 * blocks * rank;
+        for (int kk = 0; kk < nkk; ++kk) {
+          int row = uniform(tab[(64 * kk) >> lgR]);
+          if (!pair_wait(empty + 8 * r.s, r.phase ^ 1, &sm.abort)) { ok = false; break; }
+          if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * blocks * 64 * 128);
+          const uint32_t bar = fbar + 8 * r.s;
+          uint32_t dst = ring + r.s * kStageBytes;
+          if (nb == 1 && (row < 0 || keys - 64 * kk >= 64)) {
+            row = row >= 0 ? row : none;
+            tma_pair(dst, &maps.v, bar, x0, row);
+            if (blocks == 2) tma_pair(dst + 8192, &maps.v, bar, x0 + 64, row);
+          } else {
+            for (int gi = 0; gi < nb; ++gi, dst += R * 128) {
+              const int k0 = 64 * kk + (gi << lgR);  // first position of the group in the tile
+              row = tab[k0 >> lgR];
+              const int n = keys - k0;               // cached positions of the group
+              for (int blk = 0; blk < blocks; ++blk) {
+                const int x = x0 + 64 * blk;
+                const uint32_t d = dst + 8192 * blk;
                 if (row < 0 || n >= R || n <= 0) {
-                  tma_pair(dst, &maps.v, bar, x0, row >= 0 ? row : none);
-                  if (blocks == 2) tma_pair(dst + 8192, &maps.v, bar, x0 + 64, row >= 0 ? row : none);
+                  tma_pair(d, &maps.v, bar, x, row >= 0 ? row : none);
                   continue;
                 }
                 // the line ends inside the group
-                for (int blk = 0; blk < blocks; ++blk, dst += 8192) {
-                  const int x = x0 + 64 * blk;
-                  int j = 0;
-                  for (; j + 8 <= R; j += 8)
-                    if (j + 8 <= n || j >= n) {
-                      tma_pair(dst + j * 128, &maps.v8, bar, x, j < n ? row + j : none);
-                    } else {
-                      for (int q = j; q < j + 8; ++q)
-                        tma_pair(dst + q * 128, &maps.v1, bar, x, q < n ? row + q : none);
-                    }
-                  for (; j < R; ++j)
-                    tma_pair(dst + j * 128, &maps.v1, bar, x, j < n ? row + j : none);
-                }
+                int j = 0;
+                for (; j + 8 <= R; j += 8)
+                  if (j + 8 <= n || j >= n) {
+                    tma_pair(d + j * 128, &maps.v8, bar, x, j < n ? row + j : none);
+                  } else {
+                    for (int q = j; q < j + 8; ++q)
+                      tma_pair(d + q * 128, &maps.v1, bar, x, q < n ? row + q : none);
+                  }
+                for (; j < R; ++j)
+                  tma_pair(d + j * 128, &maps.v1, bar, x, j < n ? row + j : none);
               }
             }
+          }
+          r.step();
+          ++n_fills;
+        }
+      }
+      if (lane == 0) sm.fills[1] = n_fills;
+      if (!ok) break;
+      __syncwarp();
+    }
+    if (!ok && lane == 0) fail(sm, a.status);
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ S issuer --
+    // S and O are issued by two warps: one warp needs ~450 cycles per stage
+    // (waits and loop included) for MMAs of 256, so a tile took 7,700 cycles.
+    if (rank == 0) {
+      Tiles t;
+      t.init(g, plan);
+      Ring<kStagesK> r;
+      int u = 0, nq = 0;
+      bool ok = true;
+      const uint32_t id = instr_desc(kRows, 256, 1, 1, 0, 0);
+      const uint32_t empty = smem_u32(&sm.emptyk[0]), full = smem_u32(&sm.fullk[0]);
+      // descriptors: the address field counts 16 bytes; a step of 16 dims or
+      // positions is 32 bytes of a K-major operand, 2048 of V
+      const uint64_t dq = smem_desc(smem_u32(sm.q[0]), 16, 1024, kSwizzle128B);
+      const uint64_t dk = smem_desc(smem_u32(sm.ringk[0]), 16, 1024, kSwizzle128B);
+      while (t.ok && ok) {
+        if (t.first()) {
+          if (!pair_wait(smem_u32(&sm.qfull), nq & 1, &sm.abort)) { ok = false; break; }
+          ++nq;
+        }
+        // the softmax of tile u - 2 has read this S buffer
+        if (u >= 2 && !pair_wait(smem_u32(&sm.sfree[u & 1]), ((u >> 1) & 1) ^ 1, &sm.abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t d = tbase + kColS + 128 * (u & 1);
+        uint64_t qa = dq;
+        for (int c = 0; c < Cq; ++c, qa += 512) {
+          if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t kb = dk + 1024 * r.s;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_pair(d, qa + 2 * k, kb + 2 * k, id, c + k);
+          commit_pair(empty + 8 * r.s);
+          r.step();
+        }
+        if (!ok) break;
+        commit_pair(smem_u32(&sm.sfull[u & 1]));
+        if (t.last()) commit_pair(smem_u32(&sm.qempty));
+        ++u;
+        t.next(g, plan);
+      }
+      if (!ok && lane == 0) fail(sm, a.status);
+      commit_pair(smem_u32(&sm.done));
+    }
+  } else if (warp == 7) {
+    // ------------------------------------------------------------ O issuer --
+    if (rank == 0) {
+      Tiles t;
+      t.init(g, plan);
+      Ring<kStagesV> r;
+      int u = 0;
+      bool ok = true;
+      const uint32_t empty = smem_u32(&sm.emptyv[0]), full = smem_u32(&sm.fullv[0]);
+      const uint64_t dp = smem_desc(smem_u32(sm.p[0]), 16, 1024, kSwizzle128B);
+      const uint64_t dv = smem_desc(smem_u32(sm.ringv[0]), 8192, 1024, kSwizzle128B);
+      while (t.ok && ok) {
+        const int nkk = (t.keys() + 63) >> 6;
+        const int add0 = t.first() ? 0 : 1;
+        t.next(g, plan);
+        if (!pair_wait(smem_u32(&sm.pfull), u & 1, &sm.abort)) { ok = false; break; }
+        for (int i = 0; i < ninst && ok; ++i) {
+          const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;
+          const uint32_t id = instr_desc(kRows, 128 * blocks, 1, 1, 0, 1);
+          const uint32_t d = tbase + kColO + 128 * i;
+          uint64_t pa = dp;
+          for (int kk = 0; kk < nkk; ++kk, pa += 512) {
+            if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t vb = dv + 1024 * r.s;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_pair(d, pa + 2 * k, vb + 128 * k, id, add0 + kk + k);
+            commit_pair(empty + 8 * r.s);
             r.step();
           }
         }
         if (!ok) break;
-        ++uv;
-        tv.next(g, row_lines, src);
-      }
-    }
-    if (lane == 0) atomicMax(&sm.units, unit);
-    if (!ok && lane == 0) fail(sm, a.status);
-  } else if (warp == 5) {
-    // ---------------------------------------------------------- MMA issuer --
-    if (rank == 0) {
-      Tiles ts, tv;
-      ts.init(g, row_lines, src, line0, tile0, mine);
-      tv = ts;
-      Ring r;
-      int us = 0, uv = 0, nq = 0;
-      bool ok = true;
-      const uint32_t idS = instr_desc(kRows, 256, 1, 1, 0, 0);
-      const uint32_t empty = smem_u32(&sm.empty[0]), full = smem_u32(&sm.full[0]);
-      // descriptors: the address field counts 16 bytes; a step of 16 dims or
-      // positions is 32 bytes of a K-major operand, 2048 of V
-      const uint64_t dq = smem_desc(smem_u32(sm.q[0]), 16, 1024, kSwizzle128B);
-      const uint64_t dp = smem_desc(smem_u32(sm.p[0]), 16, 1024, kSwizzle128B);
-      const uint64_t dk = smem_desc(smem_u32(sm.ring[0]), 16, 1024, kSwizzle128B);
-      const uint64_t dv = smem_desc(smem_u32(sm.ring[0]), 8192, 1024, kSwizzle128B);
-      while ((ts.ok || uv < us) && ok) {
-        if (ts.ok) {
-          if (ts.first) {
-            if (!pair_wait(smem_u32(&sm.qfull), nq & 1, &sm.abort)) { ok = false; break; }
-            ++nq;
-          }
-          // S buffer us % 2 was read before the weights of tile us - 2 were
-          // announced, which O of that tile has waited for
-          const uint32_t d = tbase + kColS + 128 * (us & 1);
-          for (int c = 0; c < Cq; ++c) {
-            if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
-            tc_fence_after();
-            const uint64_t qa = dq + 512 * c, kb = dk + 1024 * r.s;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_pair(d, qa + 2 * k, kb + 2 * k, idS, c + k);
-            commit_pair(empty + 8 * r.s);
-            r.step();
-          }
-          if (!ok) break;
-          commit_pair(smem_u32(&sm.sfull[us & 1]));
-          if (ts.last) commit_pair(smem_u32(&sm.qempty));
-          ++us;
-          ts.next(g, row_lines, src);
-        }
-        if ((us - uv == 2 || !ts.ok) && uv < us) {
-          const int nkk = (tv.keys() + 63) / 64;
-          if (!pair_wait(smem_u32(&sm.pfull), uv & 1, &sm.abort)) { ok = false; break; }
-          for (int i = 0; i < ninst && ok; ++i) {
-            const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;
-            const uint32_t id = instr_desc(kRows, 128 * blocks, 1, 1, 0, 1);
-            const uint32_t d = tbase + kColO + 128 * i;
-            for (int kk = 0; kk < nkk; ++kk) {
-              if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
-              tc_fence_after();
-              const uint64_t pa = dp + 512 * kk, vb = dv + 1024 * r.s;
-              const int add = tv.first ? kk : 1;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_pair(d, pa + 2 * k, vb + 128 * k, id, add + k);
-              commit_pair(empty + 8 * r.s);
-              r.step();
-            }
-          }
-          if (!ok) break;
-          commit_pair(smem_u32(&sm.pvdone));
-          ++uv;
-          tv.next(g, row_lines, src);
-        }
+        commit_pair(smem_u32(&sm.pvdone));
+        ++u;
       }
       if (!ok && lane == 0) fail(sm, a.status);
       commit_pair(smem_u32(&sm.done));
@@ -678,43 +710,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 1;               // half of the tile's positions, of O's columns
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const float c = a.scale_log2;
-    const uint32_t pbar = leader_addr(&sm.pfull);
+    const uint32_t pbar = leader_addr(&sm.pfull), fbar = leader_addr(&sm.sfree[0]);
     Tiles t;
-    t.init(g, row_lines, src, line0, tile0, mine);
+    t.init(g, plan);
     int u = 0;
     uint32_t sp = 0;
     bool ok = true;
     float m = -INFINITY, l = 0.0f;
     while (t.ok && ok) {
-      const bool live = t.w.rows > 64 * rank;  // else this CTA's rows are not of the line
-      if (t.first) {
+      const bool live = t.rows > 64 * rank;  // else this CTA's rows are not of the line
+      if (t.first()) {
         m = -INFINITY;
         l = 0.0f;
       }
       if (!pair_wait(smem_u32(&sm.sfull[u & 1]), (u >> 1) & 1, &sm.abort)) { ok = false; break; }
       tc_fence_after();
       if (live) {
-        uint32_t z[4][32];
+        // Two passes over S in TMEM, 32 columns at a time: the maximum while
+        // the tensor cores work on O of the previous tile, then the weights
+        // straight into P.  Rolled loops on purpose: one pass holding all 128
+        // scores in registers is 1,200 unrolled instructions, and fetching
+        // them past the issuing warps slowed those down.
         const uint32_t ta = tbase + lanes + kColS + 128 * (u & 1);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld_32cols(ta + 32 * q, z[q]);
-        tmem_wait_ld();
         if (!pair_wait(smem_u32(&sm.vfull[u % kTabs]), (u / kTabs) & 1, &sm.abort)) { ok = false; break; }
-        if (!sm.whole[u % kTabs]) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t w = sm.mask[u % kTabs][4 * half + q];
+        const bool whole = sm.whole[u % kTabs] != 0;
+        const uint32_t* mask = &sm.mask[u % kTabs][4 * half];
+        float mt = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t z[32];
+          tmem_ld_32cols(ta + 32 * q, z);
+          tmem_wait_ld();
+          if (!whole) {
+            const uint32_t w = mask[q];
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!((w >> i) & 1u)) z[q][i] = 0xff800000u;
+              if (!((w >> i) & 1u)) z[i] = 0xff800000u;
           }
+          float m4[4] = {mt, __uint_as_float(z[0]), __uint_as_float(z[1]), __uint_as_float(z[2])};
+#pragma unroll
+          for (int i = 3; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(z[i]));
+          mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(z[q][i]));
-        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         sm.redm[u & 1][half][row] = mt;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
@@ -731,24 +768,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mt;
         }
         const float mm = m == -INFINITY ? 0.0f : m;
-        l *= f;
-        float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t pk[64];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float e0 = ex2_approx(fmaf(__uint_as_float(z[q][i]), c, -mm));
-            const float e1 = ex2_approx(fmaf(__uint_as_float(z[q][i + 1]), c, -mm));
-            ls[q] += e0 + e1;
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
-            pk[(32 * q + i) / 2] = *reinterpret_cast<const uint32_t*>(&b2);
-          }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         // the previous O product has read P, and O may be rescaled
         if (u > 0 && !pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) { ok = false; break; }
         tc_fence_after();
-        if (!t.first && __any_sync(0xffffffffu, resc)) {
+        if (!t.first() && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
           for (int q = 0; q < 2 * cols; ++q) {
             uint32_t v[32];
@@ -760,12 +783,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
+        float ls[2] = {l * f, 0.0f};
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t z[32];
+          tmem_ld_32cols(ta + 32 * q, z);
+          tmem_wait_ld();
+          if (!whole) {
+            const uint32_t w = mask[q];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          uint8_t* dst = sm.p[2 * half + (k >> 3)] + row * 128 + (((k & 7) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst) =
-              make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
+            for (int i = 0; i < 32; ++i)
+              if (!((w >> i) & 1u)) z[i] = 0xff800000u;
+          }
+          uint8_t* dst = sm.p[2 * half + (q >> 1)] + row * 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // eight weights, 16 bytes of the row's 128-byte line
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float e0 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i]), c, -mm));
+              const float e1 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i + 1]), c, -mm));
+              ls[0] += e0;
+              ls[1] += e1;
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+              pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            *reinterpret_cast<uint4*>(dst + (((4 * (q & 1) + k) ^ (row & 7)) << 4)) =
+                make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
         }
+        l = ls[0] + ls[1];
         fence_proxy_async_smem();
         tc_fence_before();
       } else if (u > 0 && !pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) {
@@ -775,16 +822,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       __syncwarp();
-      if (lane == 0) arrive_cluster(pbar);
-      if (t.last) {
+      if (lane == 0) {
+        arrive_cluster(pbar);
+        arrive_cluster(fbar + 8 * (u & 1));
+      }
+      if (t.last()) {
         // this pair's partial of the line: O out of TMEM, unnormalised
         if (!pair_wait(smem_u32(&sm.pvdone), u & 1, &sm.abort)) { ok = false; break; }
         tc_fence_after();
         if (live) {
-          const int slot = t.w.pre ? pair + t.w.line
-                                   : g.slots_pre + pair + (t.w.line - row_lines);
-          const int Rw = t.w.pre ? kRows : g.Rl;
-          float4* po = reinterpret_cast<float4*>(slot_po(g, slot, t.w.pre)) + 64 * rank + row;
+          const bool pre = t.pre(plan);
+          const int slot = pre ? pair + t.line : g.slots_pre + pair + t.trow;
+          const int Rw = pre ? kRows : g.Rl;
+          float4* po = reinterpret_cast<float4*>(slot_po(g, slot, pre)) + 64 * rank + row;
 #pragma unroll 1
           for (int q = 0; q < 2 * cols; ++q) {
             const int i = q >> 2;
@@ -819,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       ++u;
-      t.next(g, row_lines, src);
+      t.next(g, plan);
     }
     if (!ok && lane == 0) fail(sm, a.status);
   }
@@ -830,9 +880,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // MMAs of the pair done; after a failure also the copies in flight
     pair_wait(smem_u32(&sm.done), 0, &never, 100000000ull);
     if (sm.abort && rank == 0) {
-      for (int i = 0; i < kStages; ++i) {
-        const int n = (sm.units - i + kStages - 1) / kStages;  // fills of this stage
-        if (n > 0) pair_wait(smem_u32(&sm.full[i]), (n - 1) & 1, &never, 10000000ull);
+      for (int i = 0; i < kStagesK; ++i) {
+        const int n = (sm.fills[0] - i + kStagesK - 1) / kStagesK;  // fills of this stage
+        if (n > 0) pair_wait(smem_u32(&sm.fullk[i]), (n - 1) & 1, &never, 10000000ull);
+      }
+      for (int i = 0; i < kStagesV; ++i) {
+        const int n = (sm.fills[1] - i + kStagesV - 1) / kStagesV;
+        if (n > 0) pair_wait(smem_u32(&sm.fullv[i]), (n - 1) & 1, &never, 10000000ull);
       }
     }
   }
@@ -851,79 +905,95 @@ __global__ void __launch_bounds__(kThreads, 1)
 // 128 columns), 256 threads: a lane is a row (partials are stored with rows
 // innermost, so a warp reads 512 contiguous bytes per float4 of columns), the
 // warps take the columns in turn; the finished block is turned in shared
-// memory and written row by row.
+// memory and written row by row.  Statistics and columns of four partials are
+// in flight at once: a row of nine partials takes three round trips.
 constexpr int kMergeThreads = 256;
+constexpr int kMergeBatch = 4;
 
 __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const __grid_constant__ Geo g,
                                                                 int pairs) {
   __shared__ uint32_t tile[32][66];  // 128 bf16 per row, padded
   const PrefixAttnParams& a = g.a;
-  grid_dependency_wait();
-  launch_dependents();
   const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y * 32 + lane;
   const int x0 = blockIdx.z * 128;
-  const long long total = g.off[a.lay.batch], o0 = g.off[b], o1 = g.off[b + 1];
-  int G = pairs;
-  if (G > total) G = (int)total;
+  grid_dependency_wait();
+  launch_dependents();
+  const long long total = g.off[a.lay.batch], o0 = g.off[b], o1 = g.off[b + 1], pre = g.off[0];
+  const int G = total < pairs ? (int)total : pairs;
   const bool mine = h < a.Hq;
-  const long long L = seq_len(a, b);
-  // partials: prefix slots p0 .. p0 + np - 1, sequence slots s0 .. s0 + ns - 1
+  // partials: prefix slots p0 .. p0 + np - 1, sequence slots s0 .. s0 + ns - 1;
+  // unit x is pair ((x + 1) G - 1) / total's, unit 0 of a line has no tile
   int p0 = 0, np = 0, s0 = 0, ns = 0, prow = 0;
-  const long long first = g.off[0];
-  if (first > 0 && L >= a.prefix && mine) {
+  if (pre > 0 && mine && seq_len(a, b) >= a.prefix) {
     const int r = b * a.Hq + h, line = r / kRows;
     prow = r - line * kRows;
-    const long long x = (long long)line * g.prefix_tiles;
-    const int c0 = (int)(((x + 1) * G - 1) / total);
-    const int c1 = (int)(((x + g.prefix_tiles) * G - 1) / total);
+    const long long x = (long long)line * (g.prefix_tiles + 1);
+    const int c0 = (int)(((x + 2) * G - 1) / total);
+    const int c1 = (int)(((x + g.prefix_tiles + 1) * G - 1) / total);
     p0 = c0 + line;
     np = c1 - c0 + 1;
   }
   if (o1 > o0 && mine) {
-    const int c0 = (int)(((o0 + 1) * G - 1) / total);
+    const int c0 = (int)(((o0 + 2) * G - 1) / total);
     const int c1 = (int)((o1 * G - 1) / total);
     s0 = g.slots_pre + c0 + b;
     ns = c1 - c0 + 1;
   }
   const float2* ml = reinterpret_cast<const float2*>(g.ml);
   const int n = np + ns;
-  auto stat = [&](int i) {
-    return i < np ? __ldcg(&ml[(size_t)(p0 + i) * kRows + prow])
-                  : __ldcg(&ml[(size_t)(s0 + i - np) * kRows + h]);
-  };
-  float M = -INFINITY;
-  for (int i = 0; i < n; ++i) {
-    const float2 v = stat(i);
-    if (v.y != 0.0f) M = fmaxf(M, v.x);
-  }
-  const float Ms = M == -INFINITY ? 0.0f : M;
-  float l = 0.0f;
+  float M = -INFINITY, l = 0.0f;
   float4 acc[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < n; ++i) {
-    const float2 v = stat(i);
-    const float w = v.y != 0.0f ? exp2f(v.x - Ms) : 0.0f;
-    if (v.y != 0.0f) l = fmaf(v.y, w, l);
-    const bool pre = i < np;
-    const int Rw = pre ? kRows : g.Rl;
-    const float4* po = reinterpret_cast<const float4*>(
-                           slot_po(g, pre ? p0 + i : s0 + i - np, pre)) + (pre ? prow : h);
-    float4 x[4];
+  for (int i0 = 0; i0 < n; i0 += kMergeBatch) {
+    float2 st[kMergeBatch];
+    float4 x[kMergeBatch][4];
+#pragma unroll
+    for (int q = 0; q < kMergeBatch; ++q) {
+      const int i = i0 + q;
+      const bool isp = i < np;
+      const int slot = isp ? p0 + i : s0 + i - np, row = isp ? prow : h;
+      const int Rw = isp ? kRows : g.Rl;
+      st[q] = make_float2(-INFINITY, 0.0f);
+      if (i < n) st[q] = __ldcg(&ml[(size_t)slot * kRows + row]);
+      const float4* po = reinterpret_cast<const float4*>(slot_po(g, slot, isp)) + row;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int dv = x0 + 4 * (warp + 8 * j);
+        x[q][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n && dv < a.Dv) x[q][j] = __ldcg(&po[(size_t)(dv / 4) * Rw]);
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int q = 0; q < kMergeBatch; ++q)
+      if (st[q].y != 0.0f) Mn = fmaxf(Mn, st[q].x);
+    const float Ms = Mn == -INFINITY ? 0.0f : Mn;
+    const float f = M == -INFINITY ? 1.0f : exp2f(M - Ms);
+    l *= f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int dv = x0 + 4 * (warp + 8 * j);
-      x[j] = dv < a.Dv && v.y != 0.0f ? __ldcg(&po[(size_t)(dv / 4) * Rw])
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      acc[j].x *= f;
+      acc[j].y *= f;
+      acc[j].z *= f;
+      acc[j].w *= f;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      acc[j].x = fmaf(w, x[j].x, acc[j].x);
-      acc[j].y = fmaf(w, x[j].y, acc[j].y);
-      acc[j].z = fmaf(w, x[j].z, acc[j].z);
-      acc[j].w = fmaf(w, x[j].w, acc[j].w);
+    for (int q = 0; q < kMergeBatch; ++q) {
+      if (st[q].y != 0.0f) {  // an empty partial (no usable position) is left out
+        const float w = exp2f(st[q].x - Ms);
+        l = fmaf(st[q].y, w, l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[j].x = fmaf(w, x[q][j].x, acc[j].x);
+          acc[j].y = fmaf(w, x[q][j].y, acc[j].y);
+          acc[j].z = fmaf(w, x[q][j].z, acc[j].z);
+          acc[j].w = fmaf(w, x[q][j].w, acc[j].w);
+        }
+      }
     }
+    M = Mn;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
@@ -987,10 +1057,13 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   g.row_tiles = w.row_tiles;
   g.Rl = w.Rl;
   g.prefix_tiles = (p.prefix + kTile - 1) / kTile;
-  g.pool_rows = (long long)p.lay.nb * p.lay.bs;
+  g.pool_rows = (int)((long long)p.lay.nb * p.lay.bs);
   int R = 64;
   while (p.lay.bs % R || p.prefix % R) R >>= 1;
   g.R = R;
+  g.lgbs = -1;
+  for (int i = 0; i <= 10; ++i)
+    if (p.lay.bs == 1 << i) g.lgbs = i;
   Maps m;
   int rc = make_tmap_2d(&m.q, p.q, false, p.Dqk, (uint64_t)p.lay.batch * p.Hq, (uint64_t)p.Dqk * 2,
                         64, 64);
@@ -1009,8 +1082,8 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   int pairs = max_active_clusters((const void*)k_prefix_attn, kThreads, smem, 2);
   if (pairs < 1) return set_error(DSA_ERR_CUDA, "prefix_attn_decode: no cluster of two CTAs fits");
   if (pairs > kMaxPairs) pairs = kMaxPairs;
-  const long long bound = (long long)g.row_tiles * g.prefix_tiles +
-                          (long long)p.lay.batch * ((p.lay.max_len + kTile - 1) / kTile);
+  const long long bound = (long long)g.row_tiles * (g.prefix_tiles + 1) +
+                          (long long)p.lay.batch * (p.lay.max_len / kTile + 2);
   if (pairs > bound) pairs = bound < 1 ? 1 : (int)bound;
   cudaError_t e = launch_pdl_cluster(k_prefix_attn, dim3((unsigned)(2 * pairs)), dim3(kThreads),
                                      smem, 2, s, m, g);
