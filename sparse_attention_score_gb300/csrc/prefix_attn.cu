@@ -76,7 +76,8 @@ struct __align__(1024) Smem {
   int tab[2][kTile];                   // per producer: physical row of each group of R positions
   uint32_t mask[kTabs][kTile / 32];    // usable positions
   int whole[kTabs];                    // every position of the tile is usable
-  uint64_t fullk[kStagesK], emptyk[kStagesK], fullv[kStagesV], emptyv[kStagesV], qfull, qempty, sfull[2], sfree[2], pfull, pvdone;
+  uint64_t fullk[kStagesK], emptyk[kStagesK], fullv[kStagesV], emptyv[kStagesV], qfull, qempty;
+  uint64_t sfull[2], sfree[2], oready[2], pfull[4], pdone[2], pvdone;
   uint64_t vfull[kTabs], smsync[2], done;
   float redm[2][2][64];
   int fills[2];  // stages filled, for the drain after a failure
@@ -412,9 +413,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.qempty, 1);
     mbar_init(&sm.sfull[0], 1);
     mbar_init(&sm.sfull[1], 1);
-    mbar_init(&sm.sfree[0], 8);  // one arrival per softmax warp of both CTAs
-    mbar_init(&sm.sfree[1], 8);
-    mbar_init(&sm.pfull, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.sfree[i], 8);   // one arrival per softmax warp of both CTAs
+      mbar_init(&sm.oready[i], 8);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.pfull[i], 4);  // of the warps that write the chunk
+    mbar_init(&sm.pdone[0], 1);
+    mbar_init(&sm.pdone[1], 1);
     mbar_init(&sm.pvdone, 1);
     for (int i = 0; i < kTabs; ++i) mbar_init(&sm.vfull[i], 1);
     mbar_init(&sm.smsync[0], 2);
@@ -572,11 +577,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nkk = (keys + 63) >> 6;
       t.next(g, plan);
       if (t.ok && lane < per) ahead = group_row(g, t, lane, lgR);
-      for (int i = 0; i < ninst && ok; ++i) {
-        const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;  // 64-column blocks per CTA
-        const int x0 = 256 * i + 64 * blocks * rank;
-        for (int kk = 0; kk < nkk; ++kk) {
-          int row = uniform(tab[(64 * kk) >> lgR]);
+      for (int j = 0; j < 4 && ok; ++j) {
+        const int kk = (j >> 1) | ((j & 1) << 1);  // the O issuer's order
+        if (kk >= nkk) continue;
+        int row = uniform(tab[(64 * kk) >> lgR]);
+        for (int i = 0; i < ninst; ++i) {
+          const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;  // 64-column blocks per CTA
+          const int x0 = 256 * i + 64 * blocks * rank;
           if (!pair_wait(empty + 8 * r.s, r.phase ^ 1, &sm.abort)) { ok = false; break; }
           if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * blocks * 64 * 128);
           const uint32_t bar = fbar + 8 * r.s;
@@ -681,21 +688,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nkk = (t.keys() + 63) >> 6;
         const int add0 = t.first() ? 0 : 1;
         t.next(g, plan);
-        if (!pair_wait(smem_u32(&sm.pfull), u & 1, &sm.abort)) { ok = false; break; }
-        for (int i = 0; i < ninst && ok; ++i) {
-          const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;
-          const uint32_t id = instr_desc(kRows, 128 * blocks, 1, 1, 0, 1);
-          const uint32_t d = tbase + kColO + 128 * i;
-          uint64_t pa = dp;
-          for (int kk = 0; kk < nkk; ++kk, pa += 512) {
-            if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
-            tc_fence_after();
-            const uint64_t vb = dv + 1024 * r.s;
+        // O is rescaled, or read out for the line before
+        if (!pair_wait(smem_u32(&sm.oready[u & 1]), (u >> 1) & 1, &sm.abort)) { ok = false; break; }
+        // the weights in chunks of 64 positions, the two halves' in turn, as
+        // the softmax finishes them; a chunk is free for the next tile's
+        // weights as soon as both products of it are done
+        for (int j = 0; j < 4 && ok; ++j) {
+          const int kk = (j >> 1) | ((j & 1) << 1);  // 0, 2, 1, 3
+          if (!pair_wait(smem_u32(&sm.pfull[kk]), u & 1, &sm.abort)) { ok = false; break; }
+          if (kk < nkk) {
+            const uint64_t pa = dp + 512 * kk;
+            for (int i = 0; i < ninst; ++i) {
+              const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;
+              const uint32_t id = instr_desc(kRows, 128 * blocks, 1, 1, 0, 1);
+              const uint32_t d = tbase + kColO + 128 * i;
+              if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
+              tc_fence_after();
+              const uint64_t vb = dv + 1024 * r.s;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_pair(d, pa + 2 * k, vb + 128 * k, id, add0 + kk + k);
-            commit_pair(empty + 8 * r.s);
-            r.step();
+              for (int k = 0; k < 4; ++k) mma_pair(d, pa + 2 * k, vb + 128 * k, id, add0 + j + k);
+              commit_pair(empty + 8 * r.s);
+              r.step();
+            }
+            if (!ok) break;
           }
+          if (j < 2) commit_pair(smem_u32(&sm.pdone[j]));
         }
         if (!ok) break;
         commit_pair(smem_u32(&sm.pvdone));
@@ -710,7 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 1;               // half of the tile's positions, of O's columns
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const float c = a.scale_log2;
-    const uint32_t pbar = leader_addr(&sm.pfull), fbar = leader_addr(&sm.sfree[0]);
+    const uint32_t pbar = leader_addr(&sm.pfull[2 * half]), fbar = leader_addr(&sm.sfree[0]);
+    const uint32_t obar = leader_addr(&sm.oready[0]);
     Tiles t;
     t.init(g, plan);
     int u = 0;
@@ -768,10 +786,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = mt;
         }
         const float mm = m == -INFINITY ? 0.0f : m;
-        // the previous O product has read P, and O may be rescaled
-        if (u > 0 && !pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) { ok = false; break; }
-        tc_fence_after();
         if (!t.first() && __any_sync(0xffffffffu, resc)) {
+          // O of the tiles before is complete (u > 0: not the first tile)
+          if (!pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) { ok = false; break; }
+          tc_fence_after();
 #pragma unroll 1
           for (int q = 0; q < 2 * cols; ++q) {
             uint32_t v[32];
@@ -783,6 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(obar + 8 * (u & 1));
         float ls[2] = {l * f, 0.0f};
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
@@ -794,6 +815,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (!((w >> i) & 1u)) z[i] = 0xff800000u;
+          }
+          // The previous tile's products have read this chunk of P: the
+          // half's first chunk by its own barrier, the second by the whole
+          // tile's, which every tile waits for here once (a phase of pvdone
+          // left out would make a later wait test the wrong one).
+          if ((q & 1) == 0 && u > 0 &&
+              !pair_wait(q == 0 ? smem_u32(&sm.pdone[half]) : smem_u32(&sm.pvdone), (u - 1) & 1,
+                         &sm.abort)) {
+            ok = false;
+            break;
           }
           uint8_t* dst = sm.p[2 * half + (q >> 1)] + row * 128;
 #pragma unroll
@@ -811,21 +842,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(dst + (((4 * (q & 1) + k) ^ (row & 7)) << 4)) =
                 make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
+          if (q & 1) {  // a chunk is written
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(pbar + 8 * (q >> 1));
+          }
         }
+        if (!ok) break;
         l = ls[0] + ls[1];
-        fence_proxy_async_smem();
-        tc_fence_before();
-      } else if (u > 0 && !pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) {
-        // a warp without rows keeps in step: two arrivals of it in one phase
-        // of pfull would stand for a warp that has not written its weights
-        ok = false;
-        break;
+      } else {
+        // A warp without rows keeps in step with the others: two arrivals of
+        // it in one phase would stand for a warp that is not yet there.
+        if (lane == 0) arrive_cluster(obar + 8 * (u & 1));
+        for (int q = 0; q < 2 && ok; ++q) {
+          if (u > 0 && !pair_wait(q == 0 ? smem_u32(&sm.pdone[half]) : smem_u32(&sm.pvdone),
+                                  (u - 1) & 1, &sm.abort))
+            ok = false;
+          else if (lane == 0)
+            arrive_cluster(pbar + 8 * q);
+        }
+        if (!ok) break;
       }
       __syncwarp();
-      if (lane == 0) {
-        arrive_cluster(pbar);
-        arrive_cluster(fbar + 8 * (u & 1));
-      }
+      if (lane == 0) arrive_cluster(fbar + 8 * (u & 1));
       if (t.last()) {
         // this pair's partial of the line: O out of TMEM, unnormalised
         if (!pair_wait(smem_u32(&sm.pvdone), u & 1, &sm.abort)) { ok = false; break; }

@@ -128,6 +128,22 @@ def test_many_short_lines_per_pair_stay_in_step():
         assert torch.equal(p.out, first)
 
 
+def test_slow_copies_of_v_do_not_reorder_a_pair():
+    """Prefixes that leave boxes of 4 rows and 1 row (V arrives slowly) with
+    several tiles of a line on one pair, so that the softmax runs far ahead of
+    the second product."""
+    need_gpu()
+    dsa = lib()
+    for prefix, bs, dv in ((500, 32, 64), (500, 32, 128), (1021, 16, 512), (516, 48, 320)):
+        p = Problem(prefix, [prefix + (37 * i) % 90 for i in range(70)], bs=bs, prefix=prefix, Hq=64,
+                    Dqk=96, Dv=dv, latent=False).run(dsa)
+        p.check(f"prefix {prefix} dv {dv}")
+        first = p.out.clone()
+        for _ in range(20):
+            dsa.prefix_attn_decode(p.lay, p.q, p.kp, p.vp, prefix, p.scale, p.out, p.lse, p.ws)
+            assert torch.equal(p.out, first)
+
+
 def test_large_scores_and_peaked_rows():
     """Scores of +-hundreds: the running maximum moves by far more than fp32's
     exponent range between tiles."""
