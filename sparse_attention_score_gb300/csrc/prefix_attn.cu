@@ -113,13 +113,16 @@ __device__ __forceinline__ int seq_len(const PrefixAttnParams& a, int b) {
 
 __device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + kTile - 1) / kTile); }
 
-// A line of T tiles counts T + 1 units in the split over the pairs: starting
-// and ending one (queries in, first scores, O out) costs about one tile more
-// (7,000 cycles against 8,000 measured with 64 short lines on the last pair;
-// unit 0 of a line has no tile).
+// A line of T tiles counts T + kLineUnits units in the split over the pairs,
+// the first of which have no tile: starting and ending a line (queries in,
+// first scores, last products, O out) costs about two tiles more (11,000
+// cycles against 5,700 per tile, measured on the pairs that took 41 short
+// lines each).
+constexpr int kLineUnits = 2;
+
 __device__ __forceinline__ int own_units(const PrefixAttnParams& a, int L) {
   const int t = tiles_of(L >= a.prefix ? L - a.prefix : L);
-  return t > 0 ? t + 1 : 0;
+  return t > 0 ? t + kLineUnits : 0;
 }
 
 __device__ __forceinline__ float* slot_po(const Geo& g, int slot, bool pre) {
@@ -173,7 +176,7 @@ __device__ __forceinline__ Plan make_plan(const Geo& g, int pair, int pairs, int
   sum = __shfl_sync(0xffffffffu, warp_total(sum), 0);
   p.src = uniform(__reduce_min_sync(0xffffffffu, src));
   p.row_lines = (a.prefix > 0 && p.src != 0x7fffffff) ? g.row_tiles : 0;
-  p.pre = (long long)p.row_lines * (g.prefix_tiles + 1);
+  p.pre = (long long)p.row_lines * (g.prefix_tiles + kLineUnits);
   p.total = p.pre + sum;
   const int G = p.total < pairs ? (int)p.total : pairs;
   const long long lo = pair < G ? p.total * pair / G : 0;
@@ -181,8 +184,8 @@ __device__ __forceinline__ Plan make_plan(const Geo& g, int pair, int pairs, int
   p.line0 = p.unit0 = 0;
   if (p.mine > 0) {
     if (lo < p.pre) {
-      p.line0 = (int)(lo / (g.prefix_tiles + 1));
-      p.unit0 = (int)(lo - (long long)p.line0 * (g.prefix_tiles + 1));
+      p.line0 = (int)(lo / (g.prefix_tiles + kLineUnits));
+      p.unit0 = (int)(lo - (long long)p.line0 * (g.prefix_tiles + kLineUnits));
     } else {
       long long at = p.pre;
       for (int b0 = 0; b0 < a.lay.batch; b0 += 32) {
@@ -231,11 +234,11 @@ struct Tiles {
       p0 = p1 >= g.a.prefix ? g.a.prefix : 0;
     }
     const int T = tiles_of(p1 - p0);
-    const int n = T > 0 ? T + 1 - v : 0;
+    const int n = T > 0 ? T + kLineUnits - v : 0;
     const int take = n < left ? n : (int)left;
     left -= take;
-    t = first_t = v > 0 ? v - 1 : 0;
-    t1 = v + take - 1;
+    t = first_t = v > kLineUnits ? v - kLineUnits : 0;
+    t1 = v + take - kLineUnits;
     return t1 > t;
   }
   __device__ void next_line(const Geo& g, const Plan& p) {
@@ -963,19 +966,19 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const __grid_con
   const int G = total < pairs ? (int)total : pairs;
   const bool mine = h < a.Hq;
   // partials: prefix slots p0 .. p0 + np - 1, sequence slots s0 .. s0 + ns - 1;
-  // unit x is pair ((x + 1) G - 1) / total's, unit 0 of a line has no tile
+  // unit x is pair ((x + 1) G - 1) / total's
   int p0 = 0, np = 0, s0 = 0, ns = 0, prow = 0;
   if (pre > 0 && mine && seq_len(a, b) >= a.prefix) {
     const int r = b * a.Hq + h, line = r / kRows;
     prow = r - line * kRows;
-    const long long x = (long long)line * (g.prefix_tiles + 1);
-    const int c0 = (int)(((x + 2) * G - 1) / total);
-    const int c1 = (int)(((x + g.prefix_tiles + 1) * G - 1) / total);
+    const long long x = (long long)line * (g.prefix_tiles + kLineUnits);
+    const int c0 = (int)(((x + kLineUnits + 1) * G - 1) / total);
+    const int c1 = (int)(((x + kLineUnits + g.prefix_tiles) * G - 1) / total);
     p0 = c0 + line;
     np = c1 - c0 + 1;
   }
   if (o1 > o0 && mine) {
-    const int c0 = (int)(((o0 + 2) * G - 1) / total);
+    const int c0 = (int)(((o0 + kLineUnits + 1) * G - 1) / total);
     const int c1 = (int)((o1 * G - 1) / total);
     s0 = g.slots_pre + c0 + b;
     ns = c1 - c0 + 1;
@@ -1122,8 +1125,8 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   int pairs = max_active_clusters((const void*)k_prefix_attn, kThreads, smem, 2);
   if (pairs < 1) return set_error(DSA_ERR_CUDA, "prefix_attn_decode: no cluster of two CTAs fits");
   if (pairs > kMaxPairs) pairs = kMaxPairs;
-  const long long bound = (long long)g.row_tiles * (g.prefix_tiles + 1) +
-                          (long long)p.lay.batch * (p.lay.max_len / kTile + 2);
+  const long long bound = (long long)g.row_tiles * (g.prefix_tiles + kLineUnits) +
+                          (long long)p.lay.batch * (p.lay.max_len / kTile + 1 + kLineUnits);
   if (pairs > bound) pairs = bound < 1 ? 1 : (int)bound;
   cudaError_t e = launch_pdl_cluster(k_prefix_attn, dim3((unsigned)(2 * pairs)), dim3(kThreads),
                                      smem, 2, s, m, g);
