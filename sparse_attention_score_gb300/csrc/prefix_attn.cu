@@ -41,8 +41,8 @@
 // Boxes are R rows high, R the largest power of two (at most 64) that divides
 // the page size and the prefix length: such a group of positions never
 // crosses a page.  A group that the sequence ends in is staged for V in boxes
-// of 8 rows and 1 row, and rows past the end, or behind a bad block id, from
-// outside the pool, which TMA fills with zeros: whatever the cache holds
+// of powers of two rows, and rows past the end, or behind a bad block id, come
+// from outside the pool, which TMA fills with zeros: whatever the cache holds
 // there (NaN included) never meets a weight of 0.
 // Every wait is bounded (DSA_STATUS_TIMEOUT, then the pair winds down).
 #include "device_common.cuh"
@@ -88,7 +88,7 @@ struct __align__(1024) Smem {
 static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory of k_prefix_attn");
 
 struct Maps {
-  CUtensorMap q, k, v, v8, v1;
+  CUtensorMap q, k, v[7];  // v[i]: boxes of 2^i rows
 };
 
 struct Geo {
@@ -140,6 +140,12 @@ struct Plan {
   int line0, unit0;    // where they start
 };
 
+// a / b for a, b >= 0, in 32 bits where they fit (a 64-bit division is a long
+// instruction sequence).
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 __device__ __forceinline__ long long warp_total(long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -179,12 +185,12 @@ __device__ __forceinline__ Plan make_plan(const Geo& g, int pair, int pairs, int
   p.pre = (long long)p.row_lines * (g.prefix_tiles + kLineUnits);
   p.total = p.pre + sum;
   const int G = p.total < pairs ? (int)p.total : pairs;
-  const long long lo = pair < G ? p.total * pair / G : 0;
-  p.mine = pair < G ? p.total * (pair + 1) / G - lo : 0;
+  const long long lo = pair < G ? quot(p.total * pair, G) : 0;
+  p.mine = pair < G ? quot(p.total * (pair + 1), G) - lo : 0;
   p.line0 = p.unit0 = 0;
   if (p.mine > 0) {
     if (lo < p.pre) {
-      p.line0 = (int)(lo / (g.prefix_tiles + kLineUnits));
+      p.line0 = (int)quot(lo, g.prefix_tiles + kLineUnits);
       p.unit0 = (int)(lo - (long long)p.line0 * (g.prefix_tiles + kLineUnits));
     } else {
       long long at = p.pre;
@@ -440,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 4 && lane == 0) {
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.k);
-    tma_prefetch_desc(&maps.v);
+    tma_prefetch_desc(&maps.v[31 - __clz(g.R)]);
   }
   tc_fence_before();
   __syncthreads();
@@ -570,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring = smem_u32(sm.ringv[0]);
     const uint32_t empty = smem_u32(&sm.emptyv[0]), full = smem_u32(&sm.fullv[0]);
     const int nb = 64 >> lgR;
+    const CUtensorMap* vmap = &maps.v[lgR];
     int* tab = sm.tab[1];
     int ahead = t.ok && lane < per ? group_row(g, t, lane, lgR) : none;
     while (t.ok) {
@@ -593,31 +600,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t dst = ring + r.s * kStageBytes;
           if (nb == 1 && (row < 0 || keys - 64 * kk >= 64)) {
             row = row >= 0 ? row : none;
-            tma_pair(dst, &maps.v, bar, x0, row);
-            if (blocks == 2) tma_pair(dst + 8192, &maps.v, bar, x0 + 64, row);
+            tma_pair(dst, &maps.v[6], bar, x0, row);
+            if (blocks == 2) tma_pair(dst + 8192, &maps.v[6], bar, x0 + 64, row);
           } else {
             for (int gi = 0; gi < nb; ++gi, dst += R * 128) {
               const int k0 = 64 * kk + (gi << lgR);  // first position of the group in the tile
-              row = tab[k0 >> lgR];
+              row = uniform(tab[k0 >> lgR]);
               const int n = keys - k0;               // cached positions of the group
               for (int blk = 0; blk < blocks; ++blk) {
                 const int x = x0 + 64 * blk;
                 const uint32_t d = dst + 8192 * blk;
                 if (row < 0 || n >= R || n <= 0) {
-                  tma_pair(d, &maps.v, bar, x, row >= 0 ? row : none);
+                  tma_pair(d, vmap, bar, x, row >= 0 ? row : none);
                   continue;
                 }
-                // the line ends inside the group
-                int j = 0;
-                for (; j + 8 <= R; j += 8)
-                  if (j + 8 <= n || j >= n) {
-                    tma_pair(d + j * 128, &maps.v8, bar, x, j < n ? row + j : none);
-                  } else {
-                    for (int q = j; q < j + 8; ++q)
-                      tma_pair(d + q * 128, &maps.v1, bar, x, q < n ? row + q : none);
+                // the line ends inside the group: its rows, then zeros, in
+                // boxes of powers of two
+                int at = 0;
+                for (int e = lgR - 1; e >= 0; --e)
+                  if (n >> e & 1) {
+                    tma_pair(d + at * 128, &maps.v[e], bar, x, row + at);
+                    at += 1 << e;
                   }
-                for (; j < R; ++j)
-                  tma_pair(d + j * 128, &maps.v1, bar, x, j < n ? row + j : none);
+                for (int e = lgR - 1; e >= 0; --e)
+                  if ((R - n) >> e & 1) {
+                    tma_pair(d + at * 128, &maps.v[e], bar, x, none);
+                    at += 1 << e;
+                  }
               }
             }
           }
@@ -944,56 +953,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Join the partials of each row.  Grid (B, groups of 32 heads, quarters of
-// 128 columns), 256 threads: a lane is a row (partials are stored with rows
-// innermost, so a warp reads 512 contiguous bytes per float4 of columns), the
-// warps take the columns in turn; the finished block is turned in shared
-// memory and written row by row.  Statistics and columns of four partials are
-// in flight at once: a row of nine partials takes three round trips.
+// Join the partials of each row.  Grid (B, groups of 32 heads, groups of 32 J
+// columns), 256 threads: a lane is a row and a warp J times four columns
+// (partials are stored with rows innermost, so a warp reads 512 contiguous
+// bytes), the finished block is turned in shared memory and written row by
+// row.  With few rows a row has many partials (about one per pair), and the
+// join is a chain of round trips: J = 1 with eight partials in flight (7
+// sequences, 24 partials a row: 5 us, 12 us with J = 4).  With many rows the
+// partials are few and the blocks many, each with its own look at the plan:
+// J = 4 with four in flight (32 sequences of 64 heads: 3 us, 6 us with J = 1).
 constexpr int kMergeThreads = 256;
-constexpr int kMergeBatch = 4;
 
+template <int J, int kBatch>
 __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const __grid_constant__ Geo g,
                                                                 int pairs) {
-  __shared__ uint32_t tile[32][66];  // 128 bf16 per row, padded
+  constexpr int kCols = 32 * J;
+  __shared__ uint2 tile[32][8 * J + 1];  // four bf16 each, padded
   const PrefixAttnParams& a = g.a;
   const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y * 32 + lane;
-  const int x0 = blockIdx.z * 128;
+  const int x0 = blockIdx.z * kCols;
   grid_dependency_wait();
   launch_dependents();
-  const long long total = g.off[a.lay.batch], o0 = g.off[b], o1 = g.off[b + 1], pre = g.off[0];
+  const long long total = __ldcg(&g.off[a.lay.batch]), o0 = __ldcg(&g.off[b]),
+                  o1 = __ldcg(&g.off[b + 1]), pre = __ldcg(&g.off[0]);
+  const int L = seq_len(a, b);
   const int G = total < pairs ? (int)total : pairs;
   const bool mine = h < a.Hq;
   // partials: prefix slots p0 .. p0 + np - 1, sequence slots s0 .. s0 + ns - 1;
   // unit x is pair ((x + 1) G - 1) / total's
   int p0 = 0, np = 0, s0 = 0, ns = 0, prow = 0;
-  if (pre > 0 && mine && seq_len(a, b) >= a.prefix) {
+  if (pre > 0 && mine && L >= a.prefix) {
     const int r = b * a.Hq + h, line = r / kRows;
     prow = r - line * kRows;
     const long long x = (long long)line * (g.prefix_tiles + kLineUnits);
-    const int c0 = (int)(((x + kLineUnits + 1) * G - 1) / total);
-    const int c1 = (int)(((x + kLineUnits + g.prefix_tiles) * G - 1) / total);
+    const int c0 = (int)quot((x + kLineUnits + 1) * G - 1, total);
+    const int c1 = (int)quot((x + kLineUnits + g.prefix_tiles) * G - 1, total);
     p0 = c0 + line;
     np = c1 - c0 + 1;
   }
   if (o1 > o0 && mine) {
-    const int c0 = (int)(((o0 + kLineUnits + 1) * G - 1) / total);
-    const int c1 = (int)((o1 * G - 1) / total);
+    const int c0 = (int)quot((o0 + kLineUnits + 1) * G - 1, total);
+    const int c1 = (int)quot(o1 * G - 1, total);
     s0 = g.slots_pre + c0 + b;
     ns = c1 - c0 + 1;
   }
   const float2* ml = reinterpret_cast<const float2*>(g.ml);
   const int n = np + ns;
   float M = -INFINITY, l = 0.0f;
-  float4 acc[4];
+  float4 acc[J];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += kMergeBatch) {
-    float2 st[kMergeBatch];
-    float4 x[kMergeBatch][4];
+  for (int j = 0; j < J; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    float2 st[kBatch];
+    float4 x[kBatch][J];
 #pragma unroll
-    for (int q = 0; q < kMergeBatch; ++q) {
+    for (int q = 0; q < kBatch; ++q) {
       const int i = i0 + q;
       const bool isp = i < np;
       const int slot = isp ? p0 + i : s0 + i - np, row = isp ? prow : h;
@@ -1002,7 +1017,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const __grid_con
       if (i < n) st[q] = __ldcg(&ml[(size_t)slot * kRows + row]);
       const float4* po = reinterpret_cast<const float4*>(slot_po(g, slot, isp)) + row;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < J; ++j) {
         const int dv = x0 + 4 * (warp + 8 * j);
         x[q][j] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i < n && dv < a.Dv) x[q][j] = __ldcg(&po[(size_t)(dv / 4) * Rw]);
@@ -1010,25 +1025,25 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const __grid_con
     }
     float Mn = M;
 #pragma unroll
-    for (int q = 0; q < kMergeBatch; ++q)
+    for (int q = 0; q < kBatch; ++q)
       if (st[q].y != 0.0f) Mn = fmaxf(Mn, st[q].x);
     const float Ms = Mn == -INFINITY ? 0.0f : Mn;
     const float f = M == -INFINITY ? 1.0f : exp2f(M - Ms);
     l *= f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       acc[j].x *= f;
       acc[j].y *= f;
       acc[j].z *= f;
       acc[j].w *= f;
     }
 #pragma unroll
-    for (int q = 0; q < kMergeBatch; ++q) {
+    for (int q = 0; q < kBatch; ++q) {
       if (st[q].y != 0.0f) {  // an empty partial (no usable position) is left out
         const float w = exp2f(st[q].x - Ms);
         l = fmaf(st[q].y, w, l);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < J; ++j) {
           acc[j].x = fmaf(w, x[q][j].x, acc[j].x);
           acc[j].y = fmaf(w, x[q][j].y, acc[j].y);
           acc[j].z = fmaf(w, x[q][j].z, acc[j].z);
@@ -1040,21 +1055,22 @@ __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const __grid_con
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < J; ++j) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[j].x * inv, acc[j].y * inv);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[j].z * inv, acc[j].w * inv);
-    tile[lane][2 * (warp + 8 * j)] = *reinterpret_cast<const uint32_t*>(&lo);
-    tile[lane][2 * (warp + 8 * j) + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+    tile[lane][warp + 8 * j] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                          *reinterpret_cast<const uint32_t*>(&hi));
   }
   if (a.lse && blockIdx.z == 0 && warp == 0 && mine)
     a.lse[(size_t)b * a.Hq + h] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
   __syncthreads();
-  const int w4 = min(128, a.Dv - x0) / 8;  // 16-byte pieces of a row's quarter
-  for (int i = threadIdx.x; i < 32 * 16; i += kMergeThreads) {
-    const int r = i >> 4, k = i & 15, hh = blockIdx.y * 32 + r;
-    if (hh < a.Hq && k < w4)
-      *reinterpret_cast<uint4*>(a.out + ((size_t)b * a.Hq + hh) * a.Dv + x0 + 8 * k) =
-          make_uint4(tile[r][4 * k], tile[r][4 * k + 1], tile[r][4 * k + 2], tile[r][4 * k + 3]);
+#pragma unroll
+  for (int i = 0; i < J; ++i) {
+    const int e = threadIdx.x + kMergeThreads * i;
+    const int r = e / (8 * J), k = e % (8 * J);  // row, four columns
+    const int hh = blockIdx.y * 32 + r, x = x0 + 4 * k;
+    if (hh < a.Hq && x < a.Dv)
+      *reinterpret_cast<uint2*>(a.out + ((size_t)b * a.Hq + hh) * a.Dv + x) = tile[r][k];
   }
 }
 
@@ -1112,12 +1128,9 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
                         64, 64);
   if (!rc)
     rc = make_tmap_2d(&m.k, p.kp, false, p.Dqk, (uint64_t)g.pool_rows, (uint64_t)p.ks * 2, 64, R);
-  if (!rc)
-    rc = make_tmap_2d(&m.v, p.vp, false, p.Dv, (uint64_t)g.pool_rows, (uint64_t)p.vs * 2, 64, R);
-  if (!rc)
-    rc = make_tmap_2d(&m.v8, p.vp, false, p.Dv, (uint64_t)g.pool_rows, (uint64_t)p.vs * 2, 64, 8);
-  if (!rc)
-    rc = make_tmap_2d(&m.v1, p.vp, false, p.Dv, (uint64_t)g.pool_rows, (uint64_t)p.vs * 2, 64, 1);
+  for (int i = 0; i < 7 && !rc; ++i)
+    rc = make_tmap_2d(&m.v[i], p.vp, false, p.Dv, (uint64_t)g.pool_rows, (uint64_t)p.vs * 2, 64,
+                      1u << i);
   if (rc) return rc;
   const size_t smem = sizeof(Smem) + 1024;
   rc = ensure_dynamic_smem((const void*)k_prefix_attn, (int)smem, "prefix_attn_decode");
@@ -1134,10 +1147,16 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
   rc = check_launch("prefix_attn_decode");
   if (rc) return rc;
-  e = launch_pdl(k_prefix_merge,
-                 dim3((unsigned)p.lay.batch, (unsigned)((p.Hq + 31) / 32),
-                      (unsigned)((p.Dv + 127) / 128)),
-                 dim3(kMergeThreads), 0, s, g, pairs);
+  const unsigned heads = (unsigned)((p.Hq + 31) / 32);
+  const long long small = (long long)p.lay.batch * heads * ((p.Dv + 31) / 32);
+  if (small <= 4LL * sm_count())
+    e = launch_pdl(k_prefix_merge<1, 8>,
+                   dim3((unsigned)p.lay.batch, heads, (unsigned)((p.Dv + 31) / 32)),
+                   dim3(kMergeThreads), 0, s, g, pairs);
+  else
+    e = launch_pdl(k_prefix_merge<4, 4>,
+                   dim3((unsigned)p.lay.batch, heads, (unsigned)((p.Dv + 127) / 128)),
+                   dim3(kMergeThreads), 0, s, g, pairs);
   count_launch();
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
   return check_launch("prefix_attn_decode merge");
