@@ -953,125 +953,224 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Join the partials of each row.  Grid (B, groups of 32 heads, groups of 32 J
-// columns), 256 threads: a lane is a row and a warp J times four columns
+// The join of each row's partials, in two shapes.  Both take a lane per row
 // (partials are stored with rows innermost, so a warp reads 512 contiguous
-// bytes), the finished block is turned in shared memory and written row by
-// row.  With few rows a row has many partials (about one per pair), and the
-// join is a chain of round trips: J = 1 with eight partials in flight (7
-// sequences, 24 partials a row: 5 us, 12 us with J = 4).  With many rows the
-// partials are few and the blocks many, each with its own look at the plan:
-// J = 4 with four in flight (32 sequences of 64 heads: 3 us, 6 us with J = 1).
+// bytes), turn the finished block in shared memory and write it row by row.
 constexpr int kMergeThreads = 256;
 
+// Where the partials of row h of sequence b are: prefix slots p0 .. p0 + np - 1
+// (row prow), sequence slots s0 .. s0 + ns - 1 (row h).
+struct RowParts {
+  int p0 = 0, np = 0, s0 = 0, ns = 0, prow = 0;
+  __device__ RowParts(const Geo& g, int pairs, int b, int h) {
+    const PrefixAttnParams& a = g.a;
+    const long long total = __ldcg(&g.off[a.lay.batch]), o0 = __ldcg(&g.off[b]),
+                    o1 = __ldcg(&g.off[b + 1]), pre = __ldcg(&g.off[0]);
+    const int L = seq_len(a, b);
+    const int G = total < pairs ? (int)total : pairs;
+    if (h >= a.Hq) return;
+    // unit x is pair ((x + 1) G - 1) / total's
+    if (pre > 0 && L >= a.prefix) {
+      const int r = b * a.Hq + h, line = r / kRows;
+      prow = r - line * kRows;
+      const long long x = (long long)line * (g.prefix_tiles + kLineUnits);
+      const int c0 = (int)quot((x + kLineUnits + 1) * G - 1, total);
+      const int c1 = (int)quot((x + kLineUnits + g.prefix_tiles) * G - 1, total);
+      p0 = c0 + line;
+      np = c1 - c0 + 1;
+    }
+    if (o1 > o0) {
+      const int c0 = (int)quot((o0 + kLineUnits + 1) * G - 1, total);
+      const int c1 = (int)quot(o1 * G - 1, total);
+      s0 = g.slots_pre + c0 + b;
+      ns = c1 - c0 + 1;
+    }
+  }
+  __device__ int count() const { return np + ns; }
+  __device__ float2 stat(const Geo& g, int i, int h) const {
+    const float2* ml = reinterpret_cast<const float2*>(g.ml);
+    return i < np ? __ldcg(&ml[(size_t)(p0 + i) * kRows + prow])
+                  : __ldcg(&ml[(size_t)(s0 + i - np) * kRows + h]);
+  }
+  // the partial's float4 of columns 0..3 of the row; `step` float4 to the next
+  __device__ const float4* cols(const Geo& g, int i, int h, int* step) const {
+    const bool pre = i < np;
+    *step = pre ? kRows : g.Rl;
+    return reinterpret_cast<const float4*>(slot_po(g, pre ? p0 + i : s0 + i - np, pre)) +
+           (pre ? prow : h);
+  }
+};
+
+// Running (M, l, acc) with a batch of partials folded in; an empty partial (no
+// usable position: l = 0) is left out.
 template <int J, int kBatch>
+__device__ __forceinline__ void fold(float& M, float& l, float4 (&acc)[J],
+                                     const float2 (&st)[kBatch], const float4 (&x)[kBatch][J]) {
+  float Mn = M;
+#pragma unroll
+  for (int q = 0; q < kBatch; ++q)
+    if (st[q].y != 0.0f) Mn = fmaxf(Mn, st[q].x);
+  const float Ms = Mn == -INFINITY ? 0.0f : Mn;
+  const float f = M == -INFINITY ? 1.0f : exp2f(M - Ms);
+  l *= f;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    acc[j].x *= f;
+    acc[j].y *= f;
+    acc[j].z *= f;
+    acc[j].w *= f;
+  }
+#pragma unroll
+  for (int q = 0; q < kBatch; ++q) {
+    if (st[q].y != 0.0f) {
+      const float w = exp2f(st[q].x - Ms);
+      l = fmaf(st[q].y, w, l);
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        acc[j].x = fmaf(w, x[q][j].x, acc[j].x);
+        acc[j].y = fmaf(w, x[q][j].y, acc[j].y);
+        acc[j].z = fmaf(w, x[q][j].z, acc[j].z);
+        acc[j].w = fmaf(w, x[q][j].w, acc[j].w);
+      }
+    }
+  }
+  M = Mn;
+}
+
+__device__ __forceinline__ uint2 pack4(const float4& v, float f) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+__device__ __forceinline__ float lse_of(float M, float l) {
+  return l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+}
+
+// Many rows: grid (B, groups of 32 heads, groups of 128 columns); a warp takes
+// 16 columns and all partials of its rows, four in flight (32 sequences of 64
+// heads: 3 us; 6 us with blocks of 32 columns, each with its own look at the
+// plan).
 __global__ void __launch_bounds__(kMergeThreads) k_prefix_merge(const __grid_constant__ Geo g,
                                                                 int pairs) {
-  constexpr int kCols = 32 * J;
-  __shared__ uint2 tile[32][8 * J + 1];  // four bf16 each, padded
+  constexpr int kBatch = 4;
+  __shared__ uint2 tile[32][33];  // four bf16 each, padded
   const PrefixAttnParams& a = g.a;
   const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = blockIdx.y * 32 + lane;
-  const int x0 = blockIdx.z * kCols;
+  const int x0 = blockIdx.z * 128;
   grid_dependency_wait();
   launch_dependents();
-  const long long total = __ldcg(&g.off[a.lay.batch]), o0 = __ldcg(&g.off[b]),
-                  o1 = __ldcg(&g.off[b + 1]), pre = __ldcg(&g.off[0]);
-  const int L = seq_len(a, b);
-  const int G = total < pairs ? (int)total : pairs;
-  const bool mine = h < a.Hq;
-  // partials: prefix slots p0 .. p0 + np - 1, sequence slots s0 .. s0 + ns - 1;
-  // unit x is pair ((x + 1) G - 1) / total's
-  int p0 = 0, np = 0, s0 = 0, ns = 0, prow = 0;
-  if (pre > 0 && mine && L >= a.prefix) {
-    const int r = b * a.Hq + h, line = r / kRows;
-    prow = r - line * kRows;
-    const long long x = (long long)line * (g.prefix_tiles + kLineUnits);
-    const int c0 = (int)quot((x + kLineUnits + 1) * G - 1, total);
-    const int c1 = (int)quot((x + kLineUnits + g.prefix_tiles) * G - 1, total);
-    p0 = c0 + line;
-    np = c1 - c0 + 1;
-  }
-  if (o1 > o0 && mine) {
-    const int c0 = (int)quot((o0 + kLineUnits + 1) * G - 1, total);
-    const int c1 = (int)quot(o1 * G - 1, total);
-    s0 = g.slots_pre + c0 + b;
-    ns = c1 - c0 + 1;
-  }
-  const float2* ml = reinterpret_cast<const float2*>(g.ml);
-  const int n = np + ns;
+  const RowParts rp(g, pairs, b, h);
+  const int n = rp.count();
   float M = -INFINITY, l = 0.0f;
-  float4 acc[J];
+  float4 acc[4];
 #pragma unroll
-  for (int j = 0; j < J; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < n; i0 += kBatch) {
     float2 st[kBatch];
-    float4 x[kBatch][J];
+    float4 x[kBatch][4];
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       const int i = i0 + q;
-      const bool isp = i < np;
-      const int slot = isp ? p0 + i : s0 + i - np, row = isp ? prow : h;
-      const int Rw = isp ? kRows : g.Rl;
       st[q] = make_float2(-INFINITY, 0.0f);
-      if (i < n) st[q] = __ldcg(&ml[(size_t)slot * kRows + row]);
-      const float4* po = reinterpret_cast<const float4*>(slot_po(g, slot, isp)) + row;
+      int step = 0;
+      const float4* po = nullptr;
+      if (i < n) {
+        st[q] = rp.stat(g, i, h);
+        po = rp.cols(g, i, h, &step);
+      }
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const int dv = x0 + 4 * (warp + 8 * j);
         x[q][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < n && dv < a.Dv) x[q][j] = __ldcg(&po[(size_t)(dv / 4) * Rw]);
+        if (i < n && dv < a.Dv) x[q][j] = __ldcg(&po[(size_t)(dv / 4) * step]);
       }
     }
-    float Mn = M;
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q)
-      if (st[q].y != 0.0f) Mn = fmaxf(Mn, st[q].x);
-    const float Ms = Mn == -INFINITY ? 0.0f : Mn;
-    const float f = M == -INFINITY ? 1.0f : exp2f(M - Ms);
-    l *= f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      acc[j].x *= f;
-      acc[j].y *= f;
-      acc[j].z *= f;
-      acc[j].w *= f;
-    }
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      if (st[q].y != 0.0f) {  // an empty partial (no usable position) is left out
-        const float w = exp2f(st[q].x - Ms);
-        l = fmaf(st[q].y, w, l);
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          acc[j].x = fmaf(w, x[q][j].x, acc[j].x);
-          acc[j].y = fmaf(w, x[q][j].y, acc[j].y);
-          acc[j].z = fmaf(w, x[q][j].z, acc[j].z);
-          acc[j].w = fmaf(w, x[q][j].w, acc[j].w);
-        }
-      }
-    }
-    M = Mn;
+    fold(M, l, acc, st, x);
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[j].x * inv, acc[j].y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[j].z * inv, acc[j].w * inv);
-    tile[lane][warp + 8 * j] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                          *reinterpret_cast<const uint32_t*>(&hi));
-  }
-  if (a.lse && blockIdx.z == 0 && warp == 0 && mine)
-    a.lse[(size_t)b * a.Hq + h] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+  for (int j = 0; j < 4; ++j) tile[lane][warp + 8 * j] = pack4(acc[j], inv);
+  if (a.lse && blockIdx.z == 0 && warp == 0 && h < a.Hq) a.lse[(size_t)b * a.Hq + h] = lse_of(M, l);
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < J; ++i) {
-    const int e = threadIdx.x + kMergeThreads * i;
-    const int r = e / (8 * J), k = e % (8 * J);  // row, four columns
-    const int hh = blockIdx.y * 32 + r, x = x0 + 4 * k;
+  for (int i = 0; i < 4; ++i) {
+    const int r = warp + 8 * i;  // row; a lane writes four columns
+    const int hh = blockIdx.y * 32 + r, x = x0 + 4 * lane;
     if (hh < a.Hq && x < a.Dv)
-      *reinterpret_cast<uint2*>(a.out + ((size_t)b * a.Hq + hh) * a.Dv + x) = tile[r][k];
+      *reinterpret_cast<uint2*>(a.out + ((size_t)b * a.Hq + hh) * a.Dv + x) = tile[r][lane];
   }
+}
+
+// Few rows, each with about as many partials as there are pairs: grid (B,
+// groups of 32 heads, groups of 32 columns); the eight warps share the
+// partials, all of a row's first 24 in flight at once, and are joined in
+// shared memory (7 sequences, 22 partials a row: 3.3 us against 5.5 us
+// with a warp on four columns of all partials, eight in flight).
+__global__ void __launch_bounds__(kMergeThreads)
+    k_prefix_merge_deep(const __grid_constant__ Geo g, int pairs) {
+  constexpr int kBatch = 3;
+  __shared__ float4 part[8][8][32];  // [warp][four columns][row]
+  __shared__ float2 stat[8][32];
+  __shared__ uint2 tile[32][9];
+  const PrefixAttnParams& a = g.a;
+  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * 32 + lane;
+  const int x0 = blockIdx.z * 32;
+  grid_dependency_wait();
+  launch_dependents();
+  const RowParts rp(g, pairs, b, h);
+  const int n = rp.count();
+  float M = -INFINITY, l = 0.0f;
+  float4 acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = warp; i0 < n; i0 += 8 * kBatch) {
+    float2 st[kBatch];
+    float4 x[kBatch][8];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int i = i0 + 8 * q;
+      st[q] = make_float2(-INFINITY, 0.0f);
+      int step = 0;
+      const float4* po = nullptr;
+      if (i < n) {
+        st[q] = rp.stat(g, i, h);
+        po = rp.cols(g, i, h, &step);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[q][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n && x0 + 4 * j < a.Dv) x[q][j] = __ldcg(&po[(size_t)(x0 / 4 + j) * step]);
+      }
+    }
+    fold(M, l, acc, st, x);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[warp][j][lane] = acc[j];
+  stat[warp][lane] = make_float2(M, l);
+  __syncthreads();
+  {
+    // warp w joins the eight warps' sums of columns 4 w .. 4 w + 3
+    float2 st[8];
+    float4 x[8][1], sum[1] = {make_float4(0.f, 0.f, 0.f, 0.f)};
+    float Mj = -INFINITY, lj = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      st[q] = stat[q][lane];
+      x[q][0] = part[q][warp][lane];
+    }
+    fold(Mj, lj, sum, st, x);
+    tile[lane][warp] = pack4(sum[0], lj == 0.0f ? 0.0f : 1.0f / lj);
+    if (a.lse && blockIdx.z == 0 && warp == 0 && h < a.Hq)
+      a.lse[(size_t)b * a.Hq + h] = lse_of(Mj, lj);
+  }
+  __syncthreads();
+  const int r = threadIdx.x >> 3, k = threadIdx.x & 7;  // row, four columns
+  const int hh = blockIdx.y * 32 + r, x = x0 + 4 * k;
+  if (hh < a.Hq && x < a.Dv)
+    *reinterpret_cast<uint2*>(a.out + ((size_t)b * a.Hq + hh) * a.Dv + x) = tile[r][k];
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -1150,11 +1249,11 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   const unsigned heads = (unsigned)((p.Hq + 31) / 32);
   const long long small = (long long)p.lay.batch * heads * ((p.Dv + 31) / 32);
   if (small <= 4LL * sm_count())
-    e = launch_pdl(k_prefix_merge<1, 8>,
+    e = launch_pdl(k_prefix_merge_deep,
                    dim3((unsigned)p.lay.batch, heads, (unsigned)((p.Dv + 31) / 32)),
                    dim3(kMergeThreads), 0, s, g, pairs);
   else
-    e = launch_pdl(k_prefix_merge<4, 4>,
+    e = launch_pdl(k_prefix_merge,
                    dim3((unsigned)p.lay.batch, heads, (unsigned)((p.Dv + 127) / 128)),
                    dim3(kMergeThreads), 0, s, g, pairs);
   count_launch();
