@@ -16,11 +16,26 @@
 //   store   one rounding, to bf16 or to saturating E4M3.
 //
 // Angles: t / 2 pi is wanted modulo 1 only, and far positions have t in the
-// millions, where an fp32 product is off by whole turns' fractions.  A
-// frequency is turned once into a 64-bit fixed-point fraction of a turn (one
-// fp64 product, rounded to 2^-64 turns), and pos times that, modulo 2^64, is
-// an integer product that wraps where the angle does: for inv_freq <= 1 the
-// error is below pos * 2^-54 turns.  Its upper 32 bits go through sincospif.
+// millions, where an fp32 product is off by whole fractions of a turn.  A
+// frequency becomes a 64-bit fixed-point fraction of a turn (its mantissa times
+// 2^64 / 2 pi, an integer product), and pos times that, modulo 2^64, wraps
+// where the angle does: for inv_freq <= 1 the error is below pos * 2^-63
+// turns.  Its upper 32 bits go through sincospif.
+//
+// One warp per item.  A head takes 8, 16 or 32 lanes (8 elements, 16 bytes per
+// lane; heads beyond 256 elements three or four times that per lane), so a
+// warp holds four, two or one heads at a time.  An item is a group of heads of
+// one token, or, where a token has fewer heads than the warp holds, one head
+// of several tokens.  The warp forms the item's sines and cosines once; on
+// the usual shapes each lane then folds them with the weights into
+//   y_i = r (x_i A_i + partner_i B_i) + C_i,    r = 1 / rms (or deviation),
+// so a head costs ~90 instructions of a warp whatever the norm and rotation,
+// below the 145 that the memory system leaves time for.  Heads are loaded four
+// at a time per lane to keep ~50 KB a SM in flight.  Other shapes (a norm or a
+// rotation that ends inside 8 elements, or a rotated pair on both sides of the
+// norm's end) take a plain path through shared memory.
+// Measured on GB300 (16384 tokens, 64 rotated heads of 64 to bf16 and 64 heads
+// of 128 to E4M3, 671 MB): HEADS_PROMPT.
 #include <cuda_runtime.h>
 
 #include <string>
@@ -47,8 +62,10 @@ struct HeadJob {
   float eps;
   int heads, dim, norm, norm_dim, rope_off, rope_dim;
   int interleaved, fp8, paged;
-  int groups;    // head groups per token
-  int group;     // heads per group
+  int fast;      // the folded form applies
+  int by_token;  // items: one head of several tokens, instead of heads of one token
+  int groups;    // by_token 0: head groups per token; 1: heads
+  int group;     // by_token 0: heads per group; 1: tokens per item
   int first;     // first item of this job
 };
 
@@ -64,11 +81,27 @@ struct HeadParams {
   HeadJob job[kMaxJobs];
 };
 
-// Fraction of a turn per position, in units of 2^-64 turns.
+// Fraction of a turn per position, in units of 2^-64 turns: |f| / 2 pi =
+// mantissa * 2^(e - 150) / 2 pi, with 2^64 / 2 pi as an integer.
 __device__ __forceinline__ unsigned long long turns_of(float f) {
-  double t = (double)f * 0.15915494309189533577;  // f / 2 pi
-  t -= rint(t);  // in [-1/2, 1/2]
-  return (unsigned long long)__double2ll_rn(t * 18446744073709551616.0);
+  constexpr unsigned long long kTurn = 0x28BE60DB9391054Aull;  // 2^64 / 2 pi
+  const uint32_t bits = __float_as_uint(f);
+  int e = (int)(bits >> 23 & 0xffu);
+  uint32_t m = bits & 0x7fffffu;
+  if (e)
+    m |= 0x800000u;
+  else
+    e = 1;
+  const unsigned long long lo = kTurn * m, hi = __umul64hi(kTurn, m);
+  const int s = 150 - e;  // the product times 2^-s
+  unsigned long long u;
+  if (s <= 0)
+    u = s > -64 ? lo << -s : 0;
+  else if (s < 64)
+    u = (hi << (64 - s)) | (lo >> s);
+  else
+    u = s < 128 ? hi >> (s - 64) : 0;
+  return (int)bits < 0 ? 0ull - u : u;
 }
 
 // (cos, sin) of pos * f.
@@ -120,26 +153,33 @@ __device__ __forceinline__ void store8(const HeadJob& j, long long off, const fl
   }
 }
 
-// The heads [h0, h1) of one token: L lanes per head, granules of 8 elements,
-// J granules per lane.
+// What a lane knows of its head: the sub-warp's token and where it goes.
+struct Where {
+  long long tok;       // its token, -1: none
+  long long out_base;  // element offset of the token's heads, -1: not stored
+  int h0, h1;          // by_token 0: heads h0 .. h1 - 1; 1: the one head h0
+  const float2* cs;    // cosines and sines of its token
+};
+
+// Plain path.  L lanes per head, J granules of 8 elements per lane.
 template <int L, int J>
-__device__ void transform(const HeadJob& j, long long tok, int h0, int h1, long long out_base,
-                          const float2* cs, float* stage) {
+__device__ __noinline__ void transform_plain(const HeadJob& j, const Where w, float* stage) {
   const int lane = threadIdx.x & 31;
   const int sub = lane / L, li = lane % L;
   constexpr int kRows = 32 / L;
   const int G = j.dim >> 3;
   const int half = j.rope_dim >> 1;
-  for (int h = h0; h < h1; h += kRows) {
-    const int hh = h + sub;
-    const bool live = hh < h1;
+  const int step = j.by_token ? j.heads : kRows;  // by_token: one round
+  for (int h = w.h0; h < w.h1; h += step) {
+    const int hh = j.by_token ? h : h + sub;
+    const bool live = hh < w.h1 && w.tok >= 0;
     float v[J][8];
 #pragma unroll
     for (int k = 0; k < J; ++k) {
       const int g = li + L * k;
       uint4 raw = make_uint4(0, 0, 0, 0);
       if (live && g < G)
-        raw = *reinterpret_cast<const uint4*>(j.in + tok * j.in_ts + hh * j.in_hs + 8 * g);
+        raw = *reinterpret_cast<const uint4*>(j.in + w.tok * j.in_ts + hh * j.in_hs + 8 * g);
       unpack8(raw, v[k]);
     }
     if (j.norm != DSA_NORM_NONE) {
@@ -184,7 +224,7 @@ __device__ void transform(const HeadJob& j, long long tok, int h0, int h1, long 
           for (int i = 0; i < 8; i += 2) {
             const int e = 8 * (li + L * k) + i - j.rope_off;
             if (e >= 0 && e < j.rope_dim) {
-              const float2 c = cs[e >> 1];
+              const float2 c = w.cs[e >> 1];
               const float a = v[k][i], b = v[k][i + 1];
               v[k][i] = a * c.x - b * c.y;
               v[k][i + 1] = b * c.x + a * c.y;
@@ -207,7 +247,7 @@ __device__ void transform(const HeadJob& j, long long tok, int h0, int h1, long 
             const int e = 8 * (li + L * k) + i - j.rope_off;
             if (e >= 0 && e < j.rope_dim) {
               const bool first = e < half;
-              const float2 c = cs[first ? e : e - half];
+              const float2 c = w.cs[first ? e : e - half];
               const float p = st[first ? e + half : e - half];
               v[k][i] = first ? v[k][i] * c.x - p * c.y : v[k][i] * c.x + p * c.y;
             }
@@ -215,17 +255,232 @@ __device__ void transform(const HeadJob& j, long long tok, int h0, int h1, long 
         __syncwarp();
       }
     }
-    if (live && out_base >= 0) {
+    if (live && w.out_base >= 0) {
 #pragma unroll
       for (int k = 0; k < J; ++k) {
         const int g = li + L * k;
-        if (g < G) store8(j, out_base + hh * j.out_hs + 8 * g, v[k]);
+        if (g < G) store8(j, w.out_base + hh * j.out_hs + 8 * g, v[k]);
       }
     }
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32) k_head_transform(const __grid_constant__ HeadParams p) {
+// A lane's coefficients for granule g: y_i = r (x_i A_i + partner_i B_i) + C_i.
+struct Coef {
+  float A[8], B[8], C[8];
+  bool turned;  // the granule is rotated
+};
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+__device__ __forceinline__ void coefs(const HeadJob& j, int g, const float2* cs, Coef& c) {
+  const int rel = 8 * g - j.rope_off;
+  c.turned = rel >= 0 && rel < j.rope_dim;
+  const int half = j.rope_dim >> 1;
+  int gp = g;  // partner granule of the split halves
+  float sgn = 0.0f;
+  if (c.turned) {
+    if (j.interleaved) {
+      const float4* t = reinterpret_cast<const float4*>(cs + (rel >> 1));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 v = t[i];
+        c.A[4 * i] = c.A[4 * i + 1] = v.x;
+        c.B[4 * i] = -v.y;
+        c.B[4 * i + 1] = v.y;
+        c.A[4 * i + 2] = c.A[4 * i + 3] = v.z;
+        c.B[4 * i + 2] = -v.w;
+        c.B[4 * i + 3] = v.w;
+      }
+    } else {
+      const bool first = rel < half;
+      gp = first ? g + (half >> 3) : g - (half >> 3);
+      sgn = first ? -1.0f : 1.0f;
+      const float4* t = reinterpret_cast<const float4*>(cs + (first ? rel : rel - half));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = t[i];
+        c.A[2 * i] = v.x;
+        c.B[2 * i] = sgn * v.y;
+        c.A[2 * i + 1] = v.z;
+        c.B[2 * i + 1] = sgn * v.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c.A[i] = 1.0f;
+      c.B[i] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c.C[i] = 0.0f;
+  if (j.norm == DSA_NORM_NONE || 8 * g >= j.norm_dim) return;
+  float p[8], q[8];
+  if (j.bias) {
+    load8(j.bias + 8 * g, p);
+    load8(j.bias + 8 * gp, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      c.C[i] = c.turned ? p[i] * c.A[i] + (j.interleaved ? p[i ^ 1] : q[i]) * c.B[i] : p[i];
+  }
+  if (j.weight) {
+    load8(j.weight + 8 * g, p);
+    load8(j.weight + 8 * gp, q);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c.A[i] *= p[i];
+      c.B[i] *= j.interleaved ? p[i ^ 1] : q[i];
+    }
+  }
+}
+
+// 1 / rms or 1 / deviation of a head (and its mean), from the sums over its
+// normed elements.
+template <int L, int J>
+__device__ __forceinline__ float norm_of(const HeadJob& j, const uint4 (&raw)[J], int li,
+                                         float* mean) {
+  *mean = 0.0f;
+  if (j.norm == DSA_NORM_NONE) return 1.0f;
+  const float inv = 1.0f / (float)j.norm_dim;
+  float q = 0.0f;
+  if (j.norm == DSA_NORM_LAYER) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < J; ++k)
+      if (8 * (li + L * k) < j.norm_dim) {
+        float v[8];
+        unpack8(raw[k], v);
+        s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      }
+    *mean = row_sum<L>(s) * inv;
+  }
+#pragma unroll
+  for (int k = 0; k < J; ++k)
+    if (8 * (li + L * k) < j.norm_dim) {
+      float v[8];
+      unpack8(raw[k], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] -= *mean;
+        q = fmaf(v[i], v[i], q);
+      }
+    }
+  return rsqrtf(row_sum<L>(q) * inv + j.eps);
+}
+
+__device__ __forceinline__ void finish8(const HeadJob& j, const Coef& c, float (&v)[8], int plane,
+                                        float r, float mean, bool normed, long long off, bool put) {
+  if (normed) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] -= mean;
+  }
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = v[i] * c.A[i];
+  if (j.rope_dim) {
+    if (j.interleaved) {
+      if (c.turned) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(v[i ^ 1], c.B[i], y[i]);
+      }
+    } else {
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(0xffffffffu, v[i], plane);
+      if (c.turned) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(p[i], c.B[i], y[i]);
+      }
+    }
+  }
+  if (normed) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = fmaf(r, y[i], c.C[i]);
+  }
+  if (put) store8(j, off, y);
+}
+
+// Heads of at most 8 L elements: coefficients in registers, up to four heads
+// in flight per lane.
+template <int L>
+__device__ __forceinline__ void transform_narrow(const HeadJob& j, const Where& w) {
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / L, li = lane % L;
+  constexpr int kRows = 32 / L, kFlight = 4;
+  const bool mine = 8 * li < j.dim;
+  Coef c;
+  coefs(j, mine ? li : 0, w.cs, c);
+  if (!mine) c.turned = false;
+  const int half8 = j.rope_dim >> 4;
+  const int rel = 8 * li - j.rope_off;
+  const int plane = c.turned && !j.interleaved ? (rel < (j.rope_dim >> 1) ? lane + half8 : lane - half8)
+                                                : lane;
+  const bool normed = j.norm != DSA_NORM_NONE && 8 * li < j.norm_dim;
+  const int step = j.by_token ? 1 : kRows;
+  const int lead = j.by_token ? 0 : sub;
+  for (int h = w.h0; h < w.h1; h += kFlight * step) {
+    uint4 raw[kFlight][1];
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) {
+      const int hh = h + q * step + lead;
+      raw[q][0] = make_uint4(0, 0, 0, 0);
+      if (mine && hh < w.h1 && w.tok >= 0)
+        raw[q][0] = *reinterpret_cast<const uint4*>(j.in + w.tok * j.in_ts + hh * j.in_hs + 8 * li);
+    }
+#pragma unroll
+    for (int q = 0; q < kFlight; ++q) {
+      if (h + q * step >= w.h1) break;
+      const int hh = h + q * step + lead;
+      float mean, v[8];
+      const float r = norm_of<L, 1>(j, raw[q], li, &mean);
+      unpack8(raw[q][0], v);
+      finish8(j, c, v, plane, r, mean, normed, w.out_base + hh * j.out_hs + 8 * li,
+              mine && hh < w.h1 && w.tok >= 0 && w.out_base >= 0);
+    }
+  }
+}
+
+// Heads beyond 256 elements: a warp per head, J granules per lane.
+template <int J>
+__device__ __forceinline__ void transform_wide(const HeadJob& j, const Where& w) {
+  const int lane = threadIdx.x & 31;
+  const int half8 = j.rope_dim >> 4;
+  for (int h = w.h0; h < w.h1; ++h) {
+    uint4 raw[J];
+#pragma unroll
+    for (int k = 0; k < J; ++k) {
+      raw[k] = make_uint4(0, 0, 0, 0);
+      if (8 * (lane + 32 * k) < j.dim)
+        raw[k] = *reinterpret_cast<const uint4*>(j.in + w.tok * j.in_ts + h * j.in_hs + 8 * (lane + 32 * k));
+    }
+    float mean;
+    const float r = norm_of<32, J>(j, raw, lane, &mean);
+#pragma unroll
+    for (int k = 0; k < J; ++k) {
+      const int g = lane + 32 * k;
+      const bool mine = 8 * g < j.dim;
+      Coef c;
+      coefs(j, mine ? g : 0, w.cs, c);
+      if (!mine) c.turned = false;
+      const int plane = c.turned && !j.interleaved
+                            ? (8 * g - j.rope_off < (j.rope_dim >> 1) ? lane + half8 : lane - half8)
+                            : lane;
+      float v[8];
+      unpack8(raw[k], v);
+      finish8(j, c, v, plane, r, mean, j.norm != DSA_NORM_NONE && 8 * g < j.norm_dim,
+              w.out_base + h * j.out_hs + 8 * g, mine && w.out_base >= 0);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kWarps * 32, 7)
+    k_head_transform(const __grid_constant__ HeadParams p) {
   extern __shared__ float4 smraw[];
   grid_dependency_wait();
   launch_dependents();
@@ -233,48 +488,76 @@ __global__ void __launch_bounds__(kWarps * 32) k_head_transform(const __grid_con
   float* base = reinterpret_cast<float*>(smraw) + (size_t)warp * (2 * p.cs_len + p.stage_len);
   float2* cs = reinterpret_cast<float2*>(base);
   float* stage = base + 2 * p.cs_len;
-  for (long long item = (long long)blockIdx.x * kWarps + warp; item < p.items;
-       item += (long long)gridDim.x * kWarps) {
-    int n = 0;
-    while (n + 1 < p.n_jobs && item >= p.job[n + 1].first) ++n;
-    const HeadJob& j = p.job[n];
-    const int at = (int)item - j.first;
-    const int t = at / j.groups, grp = at - t * j.groups;
-    const int h0 = grp * j.group, h1 = min(j.heads, h0 + j.group);
-    // position of the token, and the pool row of a paged destination
-    const int b = p.seq ? __ldg(&p.seq[t]) : t;
-    int pos = 0;
-    if (p.pos)
-      pos = __ldg(&p.pos[t]);
-    else if (b < p.lay.batch)
-      pos = __ldg(&p.lay.seq_lens[b]) - 1;
-    long long out_base = t * j.out_ts;
-    if (j.paged) {
-      long long row = -1;
-      if (b >= 0 && b < p.lay.batch && pos >= 0)
-        row = phys_row(p.lay.bt, p.lay.maxb, p.lay.bs, p.lay.nb, b, pos);
-      if (row < 0) {
-        if (lane == 0) flag_status(p.status, DSA_STATUS_BAD_BLOCK);
-        continue;
-      }
-      out_base = row * j.out_ts;
+  const int item = blockIdx.x * kWarps + warp;
+  if (item >= p.items) return;
+  int n = 0;
+  while (n + 1 < p.n_jobs && item >= p.job[n + 1].first) ++n;
+  const HeadJob& j = p.job[n];
+  const int at = item - j.first;
+  const int G = j.dim >> 3;
+  const int L = G <= 8 ? 8 : G <= 16 ? 16 : 32;
+  const int sub = lane / L, li = lane % L;
+  const int hi = at / j.groups, lo = at - hi * j.groups;
+  int t;
+  Where w;
+  if (j.by_token) {
+    t = hi * j.group + sub;
+    w.h0 = lo;
+    w.h1 = lo + 1;
+  } else {
+    t = hi;
+    w.h0 = lo * j.group;
+    w.h1 = min(j.heads, w.h0 + j.group);
+  }
+  const bool there = t < p.N && (!j.by_token || sub < j.group);
+  w.tok = there ? t : -1;
+  // position of the token, and the pool row of a paged destination
+  const int b = !there ? -1 : p.seq ? __ldg(&p.seq[t]) : t;
+  int pos = 0;
+  if (there && p.pos)
+    pos = __ldg(&p.pos[t]);
+  else if (b >= 0 && b < p.lay.batch)
+    pos = __ldg(&p.lay.seq_lens[b]) - 1;
+  w.out_base = there ? t * j.out_ts : -1;
+  if (j.paged && there) {
+    long long row = -1;
+    if (b >= 0 && b < p.lay.batch && pos >= 0)
+      row = phys_row(p.lay.bt, p.lay.maxb, p.lay.bs, p.lay.nb, b, pos);
+    if (row < 0 && li == 0) flag_status(p.status, DSA_STATUS_BAD_BLOCK);
+    w.out_base = row < 0 ? -1 : row * j.out_ts;
+  }
+  const int half = j.rope_dim >> 1;
+  w.cs = cs;
+  if (half) {
+    if (j.by_token) {
+      float2* mine = cs + sub * ((half + 1) & ~1);
+      for (int i = li; i < half; i += L) mine[i] = rotation(__ldg(&j.inv_freq[i]), pos);
+      w.cs = mine;
+    } else {
+      for (int i = lane; i < half; i += 32) cs[i] = rotation(__ldg(&j.inv_freq[i]), pos);
     }
-    if (j.rope_dim) {
-      __syncwarp();
-      for (int i = lane; i < (j.rope_dim >> 1); i += 32) cs[i] = rotation(__ldg(&j.inv_freq[i]), pos);
-      __syncwarp();
-    }
-    const int G = j.dim >> 3;
-    if (G <= 8)
-      transform<8, 1>(j, t, h0, h1, out_base, cs, stage);
-    else if (G <= 16)
-      transform<16, 1>(j, t, h0, h1, out_base, cs, stage);
+    __syncwarp();
+  }
+  if (j.fast) {
+    if (L == 8)
+      transform_narrow<8>(j, w);
+    else if (L == 16)
+      transform_narrow<16>(j, w);
     else if (G <= 32)
-      transform<32, 1>(j, t, h0, h1, out_base, cs, stage);
+      transform_narrow<32>(j, w);
     else if (G <= 96)
-      transform<32, 3>(j, t, h0, h1, out_base, cs, stage);
+      transform_wide<3>(j, w);
     else
-      transform<32, 4>(j, t, h0, h1, out_base, cs, stage);
+      transform_wide<4>(j, w);
+  } else {
+    if (L == 8)
+      transform_plain<8, 1>(j, w, stage);
+    else if (L == 16)
+      transform_plain<16, 1>(j, w, stage);
+    else if (G <= 32)
+      transform_plain<32, 1>(j, w, stage);
+    else
+      transform_plain<32, 4>(j, w, stage);
   }
 }
 
@@ -354,30 +637,55 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
   p.N = N;
   p.status = status;
   p.n_jobs = n_cache + n_heads;
-  long long items = 0;
   for (int i = 0; i < p.n_jobs; ++i) {
     HeadJob& j = p.job[i];
     const bool paged = i < n_cache;
     const int rc = check_part(paged ? cache[i] : heads[i - n_cache], N, paged, &j);
     if (rc) return rc;
     const int rpw = rows_per_warp(j.dim);
-    j.group = rpw;
-    j.groups = (j.heads + j.group - 1) / j.group;
-    j.first = (int)items;
-    items += (long long)N * j.groups;
-    if (items > 0x7fffffffLL)
-      return set_error(DSA_ERR_UNSUPPORTED, "head parts: tokens x heads beyond 2^31 - 1");
-    if (j.rope_dim / 2 > p.cs_len) p.cs_len = j.rope_dim / 2;
-    if (!j.interleaved && rpw * j.rope_dim > p.stage_len) p.stage_len = rpw * j.rope_dim;
+    j.by_token = j.heads < rpw;
+    // the folded form: norm and rotation begin and end at whole granules, and
+    // a rotated granule and its partner are both normed or both not, and in
+    // the same register of two lanes
+    const int r0 = j.rope_off, r1 = j.rope_off + j.rope_dim;
+    j.fast = (j.norm == DSA_NORM_NONE || j.norm_dim % 8 == 0) &&
+             (j.rope_dim == 0 ||
+              (r0 % 8 == 0 && r1 % 8 == 0 && (j.interleaved || j.rope_dim % 16 == 0) &&
+               (j.norm == DSA_NORM_NONE || r1 <= j.norm_dim || r0 >= j.norm_dim) &&
+               (j.interleaved || j.dim <= 256 || r0 / 256 == (r1 - 1) / 256)));
+    const int pairs = ((j.rope_dim / 2 + 1) & ~1) * (j.by_token ? rpw : 1);
+    if (pairs > p.cs_len) p.cs_len = pairs;
+    if (!j.fast && !j.interleaved && rpw * j.rope_dim > p.stage_len) p.stage_len = rpw * j.rope_dim;
   }
+  p.stage_len = (p.stage_len + 3) & ~3;
+  // Heads per item: as many rounds of the warp as still leave an item for each
+  // of ~32 warps per SM (the sines, cosines and coefficients are the item's),
+  // one where there are few tokens and latency counts.
+  long long items = 0;
+  for (int rounds = 8; rounds >= 1; rounds /= 2) {
+    items = 0;
+    for (int i = 0; i < p.n_jobs; ++i) {
+      HeadJob& j = p.job[i];
+      const int rpw = rows_per_warp(j.dim);
+      j.first = items > 0x7fffffffLL ? 0 : (int)items;
+      if (j.by_token) {
+        j.group = rpw;
+        j.groups = j.heads;
+        items += (long long)((N + rpw - 1) / rpw) * j.heads;
+      } else {
+        j.group = rounds * rpw < j.heads ? rounds * rpw : j.heads;
+        j.groups = (j.heads + j.group - 1) / j.group;
+        items += (long long)N * j.groups;
+      }
+    }
+    if (items >= 32LL * sm_count()) break;
+  }
+  if (items > 0x7fffffffLL)
+    return set_error(DSA_ERR_UNSUPPORTED, "head parts: tokens x heads beyond 2^31 - 1");
   if (N == 0) return DSA_OK;
   p.items = (int)items;
-  p.cs_len = (p.cs_len + 1) & ~1;
-  p.stage_len = (p.stage_len + 3) & ~3;
   const size_t smem = sizeof(float) * kWarps * (2 * (size_t)p.cs_len + p.stage_len);
-  long long grid = (items + kWarps - 1) / kWarps;
-  const long long cap = 16LL * sm_count();
-  if (grid > cap) grid = cap;
+  const long long grid = (items + kWarps - 1) / kWarps;
   const cudaError_t e =
       launch_pdl(k_head_transform, dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p);
   count_launch();
