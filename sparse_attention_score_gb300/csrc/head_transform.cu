@@ -50,6 +50,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kMaxJobs = 2 * DSA_MAX_HEAD_PARTS;
 constexpr int kMaxDim = 1024;
+constexpr int kFlight = 4;  // 16-byte loads in flight per lane
 
 struct HeadJob {
   const __nv_bfloat16* in;
@@ -120,24 +121,61 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& r, float (&v)[8]) {
+// Pairs of fp32 in one 64-bit register: Blackwell multiplies and adds two at a
+// time (PTX mul / fma .f32x2), which the instruction-bound path here needs.
+typedef unsigned long long f2;
+
+__device__ __forceinline__ f2 pair2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& r, f2 (&v)[4]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = pair2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+
+__device__ __forceinline__ void unpack8(const uint4& r, float (&v)[8]) {
+  f2 p[4];
+  unpack8(r, p);
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const float2 f = split2(p[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
   }
 }
 
-__device__ __forceinline__ void store8(const HeadJob& j, long long off, const float (&v)[8]) {
+__device__ __forceinline__ void store8(const HeadJob& j, long long off, const f2 (&v)[4]) {
   if (j.fp8) {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]),
-                                                   __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]),
-                                                   __NV_SATFINITE, __NV_E4M3);
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(split2(v[2 * i]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(split2(v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
       w[i] = lo | (hi << 16);
     }
     *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(j.out) + off) = make_uint2(w[0], w[1]);
@@ -145,12 +183,20 @@ __device__ __forceinline__ void store8(const HeadJob& j, long long off, const fl
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      const float2 f = split2(v[i]);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
     *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(j.out) + off) =
         make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+
+__device__ __forceinline__ void store8(const HeadJob& j, long long off, const float (&v)[8]) {
+  f2 p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = pair2(v[2 * i], v[2 * i + 1]);
+  store8(j, off, p);
 }
 
 // What a lane knows of its head: the sub-warp's token and where it goes.
@@ -265,221 +311,308 @@ __device__ __noinline__ void transform_plain(const HeadJob& j, const Where w, fl
   }
 }
 
-// A lane's coefficients for granule g: y_i = r (x_i A_i + partner_i B_i) + C_i.
-struct Coef {
-  float A[8], B[8], C[8];
-  bool turned;  // the granule is rotated
+// The folded form, one instantiation per kind of norm and rotation.
+enum { kNoNorm = 0, kScale = 1, kFull = 2 };  // none; RMS without a bias; mean and / or bias
+enum { kNoTurn = 0, kNeighbours = 1, kHalves = 2 };
+template <int n>
+struct Int {
+  static constexpr int value = n;
+};
+template <int n, int t>
+struct Form {
+  static constexpr int norm = n, turn = t;
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+// A lane's coefficients for granule g: y_i = r (x_i A_i + partner_i B_i) + C_i.
+template <int kNorm, int kTurn>
+struct Coef {
+  f2 A[4], B[kTurn ? 4 : 1], C[kNorm == kFull ? 4 : 1];
+  bool turned;   // the granule is rotated
+  bool normed;
+  int plane;     // lane that holds the partner granule (kHalves)
+};
+
+__device__ __forceinline__ void load8(const float* p, f2 (&v)[4]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
   const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  v[0] = pair2(a.x, a.y);
+  v[1] = pair2(a.z, a.w);
+  v[2] = pair2(b.x, b.y);
+  v[3] = pair2(b.z, b.w);
 }
 
-__device__ __forceinline__ void coefs(const HeadJob& j, int g, const float2* cs, Coef& c) {
+__device__ __forceinline__ f2 swap2(f2 v) {
+  const float2 f = split2(v);
+  return pair2(f.y, f.x);
+}
+
+template <int kNorm, int kTurn>
+__device__ __forceinline__ void coefs(const HeadJob& j, int g, int lane, const float2* cs,
+                                      Coef<kNorm, kTurn>& c) {
   const int rel = 8 * g - j.rope_off;
-  c.turned = rel >= 0 && rel < j.rope_dim;
-  const int half = j.rope_dim >> 1;
+  c.turned = kTurn != kNoTurn && 8 * g < j.dim && rel >= 0 && rel < j.rope_dim;
+  c.normed = kNorm != kNoNorm && 8 * g < j.norm_dim;
+  c.plane = lane;
   int gp = g;  // partner granule of the split halves
-  float sgn = 0.0f;
-  if (c.turned) {
-    if (j.interleaved) {
-      const float4* t = reinterpret_cast<const float4*>(cs + (rel >> 1));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 v = t[i];
-        c.A[4 * i] = c.A[4 * i + 1] = v.x;
-        c.B[4 * i] = -v.y;
-        c.B[4 * i + 1] = v.y;
-        c.A[4 * i + 2] = c.A[4 * i + 3] = v.z;
-        c.B[4 * i + 2] = -v.w;
-        c.B[4 * i + 3] = v.w;
+  for (int i = 0; i < 4; ++i) c.A[i] = pair2(1.0f, 1.0f);
+  if (kTurn != kNoTurn) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.B[i] = pair2(0.0f, 0.0f);
+    if (c.turned) {
+      if (kTurn == kNeighbours) {
+        const float4* t = reinterpret_cast<const float4*>(cs + (rel >> 1));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 v = t[i];
+          c.A[2 * i] = pair2(v.x, v.x);
+          c.B[2 * i] = pair2(-v.y, v.y);
+          c.A[2 * i + 1] = pair2(v.z, v.z);
+          c.B[2 * i + 1] = pair2(-v.w, v.w);
+        }
+      } else {
+        const int half = j.rope_dim >> 1;
+        const bool first = rel < half;
+        const int d = first ? half >> 3 : -(half >> 3);
+        gp = g + d;
+        c.plane = lane + d;
+        const float sgn = first ? -1.0f : 1.0f;
+        const float4* t = reinterpret_cast<const float4*>(cs + (first ? rel : rel - half));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = t[i];
+          c.A[i] = pair2(v.x, v.z);
+          c.B[i] = pair2(sgn * v.y, sgn * v.w);
+        }
       }
-    } else {
-      const bool first = rel < half;
-      gp = first ? g + (half >> 3) : g - (half >> 3);
-      sgn = first ? -1.0f : 1.0f;
-      const float4* t = reinterpret_cast<const float4*>(cs + (first ? rel : rel - half));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = t[i];
-        c.A[2 * i] = v.x;
-        c.B[2 * i] = sgn * v.y;
-        c.A[2 * i + 1] = v.z;
-        c.B[2 * i + 1] = sgn * v.w;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c.A[i] = 1.0f;
-      c.B[i] = 0.0f;
     }
   }
+  if (kNorm == kFull) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c.C[i] = 0.0f;
-  if (j.norm == DSA_NORM_NONE || 8 * g >= j.norm_dim) return;
-  float p[8], q[8];
-  if (j.bias) {
+    for (int i = 0; i < 4; ++i) c.C[i] = pair2(0.0f, 0.0f);
+  }
+  if (!c.normed) return;
+  f2 p[4], q[4];
+  if (kNorm == kFull && j.bias) {
     load8(j.bias + 8 * g, p);
-    load8(j.bias + 8 * gp, q);
+    if (kTurn == kHalves) load8(j.bias + 8 * gp, q);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      c.C[i] = c.turned ? p[i] * c.A[i] + (j.interleaved ? p[i ^ 1] : q[i]) * c.B[i] : p[i];
+    for (int i = 0; i < 4; ++i) {
+      c.C[i] = p[i];
+      if (kTurn != kNoTurn && c.turned)
+        c.C[i] = fma2(kTurn == kHalves ? q[i] : swap2(p[i]), c.B[i], mul2(p[i], c.A[i]));
+    }
   }
   if (j.weight) {
     load8(j.weight + 8 * g, p);
-    load8(j.weight + 8 * gp, q);
+    if (kTurn == kHalves) load8(j.weight + 8 * gp, q);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c.A[i] *= p[i];
-      c.B[i] *= j.interleaved ? p[i ^ 1] : q[i];
+    for (int i = 0; i < 4; ++i) {
+      c.A[i] = mul2(c.A[i], p[i]);
+      if (kTurn != kNoTurn) c.B[i] = mul2(c.B[i], kTurn == kHalves ? q[i] : swap2(p[i]));
     }
   }
 }
 
-// 1 / rms or 1 / deviation of a head (and its mean), from the sums over its
-// normed elements.
-template <int L, int J>
-__device__ __forceinline__ float norm_of(const HeadJob& j, const uint4 (&raw)[J], int li,
-                                         float* mean) {
-  *mean = 0.0f;
-  if (j.norm == DSA_NORM_NONE) return 1.0f;
+// 1 / rms or 1 / deviation of a head, from the sums over its normed elements;
+// kFull also takes the mean off the values.
+template <int L, int J, int kNorm>
+__device__ __forceinline__ float normalise(const HeadJob& j, f2 (&v)[J][4], int li) {
+  if (kNorm == kNoNorm) return 1.0f;
   const float inv = 1.0f / (float)j.norm_dim;
-  float q = 0.0f;
-  if (j.norm == DSA_NORM_LAYER) {
-    float s = 0.0f;
+  if (kNorm == kFull && j.norm == DSA_NORM_LAYER) {
+    f2 s = pair2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < J; ++k)
+      if (8 * (li + L * k) < j.norm_dim) s = add2(s, add2(add2(v[k][0], v[k][1]), add2(v[k][2], v[k][3])));
+    const float2 t = split2(s);
+    const float mean = row_sum<L>(t.x + t.y) * inv;
+    const f2 off = pair2(-mean, -mean);
 #pragma unroll
     for (int k = 0; k < J; ++k)
       if (8 * (li + L * k) < j.norm_dim) {
-        float v[8];
-        unpack8(raw[k], v);
-        s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k][i] = add2(v[k][i], off);
       }
-    *mean = row_sum<L>(s) * inv;
   }
+  f2 q = pair2(0.0f, 0.0f);
 #pragma unroll
   for (int k = 0; k < J; ++k)
     if (8 * (li + L * k) < j.norm_dim) {
-      float v[8];
-      unpack8(raw[k], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] -= *mean;
-        q = fmaf(v[i], v[i], q);
-      }
+      for (int i = 0; i < 4; ++i) q = fma2(v[k][i], v[k][i], q);
     }
-  return rsqrtf(row_sum<L>(q) * inv + j.eps);
+  const float2 t = split2(q);
+  return rsqrtf(row_sum<L>(t.x + t.y) * inv + j.eps);
 }
 
-__device__ __forceinline__ void finish8(const HeadJob& j, const Coef& c, float (&v)[8], int plane,
-                                        float r, float mean, bool normed, long long off, bool put) {
-  if (normed) {
+template <int kNorm, int kTurn>
+__device__ __forceinline__ void finish8(const HeadJob& j, const Coef<kNorm, kTurn>& c,
+                                        const f2 (&v)[4], float r, long long off, bool put) {
+  f2 y[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] -= mean;
-  }
-  float y[8];
+  for (int i = 0; i < 4; ++i) y[i] = mul2(v[i], c.A[i]);
+  if (kTurn == kNeighbours) {
+    if (c.turned) {  // elsewhere a neighbour's NaN must not meet a B of 0
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = v[i] * c.A[i];
-  if (j.rope_dim) {
-    if (j.interleaved) {
-      if (c.turned) {
+      for (int i = 0; i < 4; ++i) y[i] = fma2(swap2(v[i]), c.B[i], y[i]);
+    }
+  } else if (kTurn == kHalves) {
+    f2 p[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(v[i ^ 1], c.B[i], y[i]);
-      }
-    } else {
-      float p[8];
+    for (int i = 0; i < 4; ++i) p[i] = __shfl_sync(0xffffffffu, v[i], c.plane);
+    if (c.turned) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(0xffffffffu, v[i], plane);
-      if (c.turned) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(p[i], c.B[i], y[i]);
-      }
+      for (int i = 0; i < 4; ++i) y[i] = fma2(p[i], c.B[i], y[i]);
     }
   }
-  if (normed) {
+  if (kNorm != kNoNorm) {
+    const float rr = c.normed ? r : 1.0f;
+    const f2 r2 = pair2(rr, rr);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(r, y[i], c.C[i]);
+    for (int i = 0; i < 4; ++i) y[i] = kNorm == kFull ? fma2(r2, y[i], c.C[i]) : mul2(r2, y[i]);
   }
   if (put) store8(j, off, y);
 }
 
 // Heads of at most 8 L elements: coefficients in registers, up to four heads
 // in flight per lane.
-template <int L>
+template <int L, int kNorm, int kTurn>
 __device__ __forceinline__ void transform_narrow(const HeadJob& j, const Where& w) {
   const int lane = threadIdx.x & 31;
   const int sub = lane / L, li = lane % L;
-  constexpr int kRows = 32 / L, kFlight = 4;
-  const bool mine = 8 * li < j.dim;
-  Coef c;
-  coefs(j, mine ? li : 0, w.cs, c);
-  if (!mine) c.turned = false;
-  const int half8 = j.rope_dim >> 4;
-  const int rel = 8 * li - j.rope_off;
-  const int plane = c.turned && !j.interleaved ? (rel < (j.rope_dim >> 1) ? lane + half8 : lane - half8)
-                                                : lane;
-  const bool normed = j.norm != DSA_NORM_NONE && 8 * li < j.norm_dim;
+  constexpr int kRows = 32 / L;
+  Coef<kNorm, kTurn> c;
+  coefs(j, li, lane, w.cs, c);
+  const bool mine = 8 * li < j.dim && w.tok >= 0;
   const int step = j.by_token ? 1 : kRows;
-  const int lead = j.by_token ? 0 : sub;
-  for (int h = w.h0; h < w.h1; h += kFlight * step) {
-    uint4 raw[kFlight][1];
+  const int h0 = w.h0 + (j.by_token ? 0 : sub);
+  const __nv_bfloat16* in = j.in + w.tok * j.in_ts + h0 * j.in_hs + 8 * li;
+  long long off = w.out_base + h0 * j.out_hs + 8 * li;
+  const long long in_step = step * j.in_hs, out_step = step * j.out_hs;
+  const bool put = mine && w.out_base >= 0;
+  const int rounds = (w.h1 - w.h0 + step - 1) / step;
+  const int left = w.h1 - h0;  // of this sub-warp
+  for (int r0 = 0; r0 < rounds; r0 += kFlight) {
+    uint4 raw[kFlight];
 #pragma unroll
     for (int q = 0; q < kFlight; ++q) {
-      const int hh = h + q * step + lead;
-      raw[q][0] = make_uint4(0, 0, 0, 0);
-      if (mine && hh < w.h1 && w.tok >= 0)
-        raw[q][0] = *reinterpret_cast<const uint4*>(j.in + w.tok * j.in_ts + hh * j.in_hs + 8 * li);
+      raw[q] = make_uint4(0, 0, 0, 0);
+      if (mine && (r0 + q) * step < left) raw[q] = *reinterpret_cast<const uint4*>(in + q * in_step);
     }
 #pragma unroll
     for (int q = 0; q < kFlight; ++q) {
-      if (h + q * step >= w.h1) break;
-      const int hh = h + q * step + lead;
-      float mean, v[8];
-      const float r = norm_of<L, 1>(j, raw[q], li, &mean);
-      unpack8(raw[q][0], v);
-      finish8(j, c, v, plane, r, mean, normed, w.out_base + hh * j.out_hs + 8 * li,
-              mine && hh < w.h1 && w.tok >= 0 && w.out_base >= 0);
+      if (r0 + q >= rounds) break;
+      f2 v[1][4];
+      unpack8(raw[q], v[0]);
+      const float r = normalise<L, 1, kNorm>(j, v, li);
+      finish8(j, c, v[0], r, off + q * out_step, put && (r0 + q) * step < left);
     }
+    in += kFlight * in_step;
+    off += kFlight * out_step;
   }
 }
 
-// Heads beyond 256 elements: a warp per head, J granules per lane.
-template <int J>
-__device__ __forceinline__ void transform_wide(const HeadJob& j, const Where& w) {
+// Heads beyond 256 elements: a warp per head, J granules per lane.  raw: head
+// w.h0.
+template <int J, int kNorm, int kTurn>
+__device__ __forceinline__ void transform_wide(const HeadJob& j, const Where& w, uint4 (&raw)[J]) {
   const int lane = threadIdx.x & 31;
-  const int half8 = j.rope_dim >> 4;
   for (int h = w.h0; h < w.h1; ++h) {
-    uint4 raw[J];
+    f2 v[J][4];
 #pragma unroll
-    for (int k = 0; k < J; ++k) {
-      raw[k] = make_uint4(0, 0, 0, 0);
-      if (8 * (lane + 32 * k) < j.dim)
-        raw[k] = *reinterpret_cast<const uint4*>(j.in + w.tok * j.in_ts + h * j.in_hs + 8 * (lane + 32 * k));
+    for (int k = 0; k < J; ++k) unpack8(raw[k], v[k]);
+    if (h + 1 < w.h1) {
+      const uint4* in = reinterpret_cast<const uint4*>(j.in + w.tok * j.in_ts + (h + 1) * j.in_hs);
+#pragma unroll
+      for (int k = 0; k < J; ++k)
+        if (8 * (lane + 32 * k) < j.dim) raw[k] = in[lane + 32 * k];
     }
-    float mean;
-    const float r = norm_of<32, J>(j, raw, lane, &mean);
+    const float r = normalise<32, J, kNorm>(j, v, lane);
 #pragma unroll
     for (int k = 0; k < J; ++k) {
       const int g = lane + 32 * k;
-      const bool mine = 8 * g < j.dim;
-      Coef c;
-      coefs(j, mine ? g : 0, w.cs, c);
-      if (!mine) c.turned = false;
-      const int plane = c.turned && !j.interleaved
-                            ? (8 * g - j.rope_off < (j.rope_dim >> 1) ? lane + half8 : lane - half8)
-                            : lane;
-      float v[8];
-      unpack8(raw[k], v);
-      finish8(j, c, v, plane, r, mean, j.norm != DSA_NORM_NONE && 8 * g < j.norm_dim,
-              w.out_base + h * j.out_hs + 8 * g, mine && w.out_base >= 0);
+      Coef<kNorm, kTurn> c;
+      coefs(j, g, lane, w.cs, c);
+      finish8(j, c, v[k], r, w.out_base + h * j.out_hs + 8 * g, 8 * g < j.dim && w.out_base >= 0);
     }
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32, 7)
+// One of the nine instantiations, by the part's norm and rotation.
+template <typename F>
+__device__ __forceinline__ void by_form(const HeadJob& j, F f) {
+  auto turn = [&](auto norm) {
+    constexpr int n = decltype(norm)::value;
+    if (j.rope_dim == 0)
+      f(Form<n, kNoTurn>());
+    else if (j.interleaved)
+      f(Form<n, kNeighbours>());
+    else
+      f(Form<n, kHalves>());
+  };
+  if (j.norm == DSA_NORM_NONE)
+    turn(Int<kNoNorm>());
+  else if (j.norm == DSA_NORM_RMS && !j.bias)
+    turn(Int<kScale>());
+  else
+    turn(Int<kFull>());
+}
+
+// The position of token t, and where its heads go (w.tok, h0, h1 are set).
+__device__ __forceinline__ int locate(const HeadParams& p, const HeadJob& j, int t, bool flag,
+                                      Where& w) {
+  const bool there = w.tok >= 0;
+  const int b = !there ? -1 : p.seq ? __ldg(&p.seq[t]) : t;
+  int pos = 0;
+  if (there && p.pos)
+    pos = __ldg(&p.pos[t]);
+  else if (b >= 0 && b < p.lay.batch)
+    pos = __ldg(&p.lay.seq_lens[b]) - 1;
+  w.out_base = there ? t * j.out_ts : -1;
+  if (j.paged && there) {
+    long long row = -1;
+    if (b >= 0 && b < p.lay.batch && pos >= 0) {
+      const unsigned slot = (unsigned)pos / (unsigned)p.lay.bs;
+      if (slot < (unsigned)p.lay.maxb) {
+        const int page = __ldg(&p.lay.bt[(long long)b * p.lay.maxb + slot]);
+        if (page >= 0 && page < p.lay.nb)
+          row = (long long)page * p.lay.bs + (pos - (int)(slot * (unsigned)p.lay.bs));
+      }
+    }
+    if (row < 0 && flag) flag_status(p.status, DSA_STATUS_BAD_BLOCK);
+    w.out_base = row < 0 ? -1 : row * j.out_ts;
+  }
+  return pos;
+}
+
+template <int J>
+__device__ __forceinline__ void wide_item(const HeadParams& p, const HeadJob& j, int t, Where& w,
+                                          float2* cs) {
+  const int lane = threadIdx.x & 31;
+  // the first head is on its way while position and page are looked up
+  const uint4* in = reinterpret_cast<const uint4*>(j.in + t * j.in_ts + w.h0 * j.in_hs);
+  uint4 raw[J];
+#pragma unroll
+  for (int k = 0; k < J; ++k) {
+    raw[k] = make_uint4(0, 0, 0, 0);
+    if (8 * (lane + 32 * k) < j.dim) raw[k] = in[lane + 32 * k];
+  }
+  const int pos = locate(p, j, t, lane == 0, w);
+  const int half = j.rope_dim >> 1;
+  w.cs = cs;
+  for (int i = lane; i < half; i += 32) cs[i] = rotation(__ldg(&j.inv_freq[i]), pos);
+  __syncwarp();
+  by_form(j, [&](auto f) { transform_wide<J, f.norm, f.turn>(j, w, raw); });
+}
+
+// What the parts of a launch need: heads of up to 256 elements in the folded
+// form, wider ones too, or the plain path as well.  (One kernel for all three
+// has the registers of the last.)
+enum { kNarrowOnly = 0, kWithWide = 1, kWithPlain = 2 };
+
+template <int kKind>
+__global__ void __launch_bounds__(kWarps * 32, 8)
     k_head_transform(const __grid_constant__ HeadParams p) {
   extern __shared__ float4 smraw[];
   grid_dependency_wait();
@@ -511,21 +644,14 @@ __global__ void __launch_bounds__(kWarps * 32, 7)
   }
   const bool there = t < p.N && (!j.by_token || sub < j.group);
   w.tok = there ? t : -1;
-  // position of the token, and the pool row of a paged destination
-  const int b = !there ? -1 : p.seq ? __ldg(&p.seq[t]) : t;
-  int pos = 0;
-  if (there && p.pos)
-    pos = __ldg(&p.pos[t]);
-  else if (b >= 0 && b < p.lay.batch)
-    pos = __ldg(&p.lay.seq_lens[b]) - 1;
-  w.out_base = there ? t * j.out_ts : -1;
-  if (j.paged && there) {
-    long long row = -1;
-    if (b >= 0 && b < p.lay.batch && pos >= 0)
-      row = phys_row(p.lay.bt, p.lay.maxb, p.lay.bs, p.lay.nb, b, pos);
-    if (row < 0 && li == 0) flag_status(p.status, DSA_STATUS_BAD_BLOCK);
-    w.out_base = row < 0 ? -1 : row * j.out_ts;
+  if (kKind != kNarrowOnly && G > 32 && (kKind == kWithWide || j.fast)) {
+    if (G <= 96)
+      wide_item<3>(p, j, t, w, cs);
+    else
+      wide_item<4>(p, j, t, w, cs);
+    return;
   }
+  const int pos = locate(p, j, t, li == 0, w);
   const int half = j.rope_dim >> 1;
   w.cs = cs;
   if (half) {
@@ -538,18 +664,7 @@ __global__ void __launch_bounds__(kWarps * 32, 7)
     }
     __syncwarp();
   }
-  if (j.fast) {
-    if (L == 8)
-      transform_narrow<8>(j, w);
-    else if (L == 16)
-      transform_narrow<16>(j, w);
-    else if (G <= 32)
-      transform_narrow<32>(j, w);
-    else if (G <= 96)
-      transform_wide<3>(j, w);
-    else
-      transform_wide<4>(j, w);
-  } else {
+  if (kKind == kWithPlain && !j.fast) {
     if (L == 8)
       transform_plain<8, 1>(j, w, stage);
     else if (L == 16)
@@ -558,7 +673,16 @@ __global__ void __launch_bounds__(kWarps * 32, 7)
       transform_plain<32, 1>(j, w, stage);
     else
       transform_plain<32, 4>(j, w, stage);
+    return;
   }
+  by_form(j, [&](auto f) {
+    if (L == 8)
+      transform_narrow<8, f.norm, f.turn>(j, w);
+    else if (L == 16)
+      transform_narrow<16, f.norm, f.turn>(j, w);
+    else
+      transform_narrow<32, f.norm, f.turn>(j, w);
+  });
 }
 
 bool aligned(const void* q, unsigned a) { return ((uintptr_t)q & (a - 1)) == 0; }
@@ -637,6 +761,7 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
   p.N = N;
   p.status = status;
   p.n_jobs = n_cache + n_heads;
+  int kind = kNarrowOnly;
   for (int i = 0; i < p.n_jobs; ++i) {
     HeadJob& j = p.job[i];
     const bool paged = i < n_cache;
@@ -655,6 +780,10 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
                (j.interleaved || j.dim <= 256 || r0 / 256 == (r1 - 1) / 256)));
     const int pairs = ((j.rope_dim / 2 + 1) & ~1) * (j.by_token ? rpw : 1);
     if (pairs > p.cs_len) p.cs_len = pairs;
+    if (!j.fast)
+      kind = kWithPlain;
+    else if (j.dim > 256 && kind == kNarrowOnly)
+      kind = kWithWide;
     if (!j.fast && !j.interleaved && rpw * j.rope_dim > p.stage_len) p.stage_len = rpw * j.rope_dim;
   }
   p.stage_len = (p.stage_len + 3) & ~3;
@@ -662,7 +791,7 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
   // of ~32 warps per SM (the sines, cosines and coefficients are the item's),
   // one where there are few tokens and latency counts.
   long long items = 0;
-  for (int rounds = 8; rounds >= 1; rounds /= 2) {
+  for (int rounds = 16; rounds >= 1; rounds /= 2) {
     items = 0;
     for (int i = 0; i < p.n_jobs; ++i) {
       HeadJob& j = p.job[i];
@@ -687,7 +816,10 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
   const size_t smem = sizeof(float) * kWarps * (2 * (size_t)p.cs_len + p.stage_len);
   const long long grid = (items + kWarps - 1) / kWarps;
   const cudaError_t e =
-      launch_pdl(k_head_transform, dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p);
+      launch_pdl(kind == kNarrowOnly ? k_head_transform<kNarrowOnly>
+                 : kind == kWithWide ? k_head_transform<kWithWide>
+                                     : k_head_transform<kWithPlain>,
+                 dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p);
   count_launch();
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
   return check_launch("head_transform");
