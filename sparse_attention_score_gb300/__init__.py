@@ -631,7 +631,10 @@ class HeadParts:
         if any(p.N != self.N for p in self.parts):
             raise ValueError("the parts differ in their number of tokens")
         self.rotates = any(p._spec[6] for p in self.parts)
-        self.out_bytes = [p.out.element_size() * p.out.numel() for p in self.parts]
+        self.n = len(self.parts)
+        # rows of the smallest pool, for parts that go to paged pools
+        self.pool_rows = min((p.out.numel() // max(1, p.out.stride(1)) if p.out.dim() >= 3 else 0)
+                             for p in self.parts)
         self._arrays = {}
         self._device = None
 
@@ -665,10 +668,38 @@ def _parts(parts) -> HeadParts:
     return parts if isinstance(parts, HeadParts) else HeadParts(parts)
 
 
-def _on_current(device: int):
-    if device != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{device}; the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+# A call on a handful of tokens takes the GPU 3 us, so these two calls keep
+# their host side short: plain integers to ctypes, one look at the device.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _here(device: int, stream) -> int:
+    """Raw handle of the stream to launch on, after a look that the tensors'
+    device is the current one."""
+    cur = _get_device()
+    if device != cur:
+        raise ValueError(f"tensors on cuda:{device}; the current device is cuda:{cur}")
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(cur)
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _vec(t, name: str, elt: int, numel: int, device: int):
+    """Address of a contiguous operand on `device`, checked as _Args does."""
+    if t is None:
+        return None
+    if t.element_size() != elt:
+        raise TypeError(f"{name}: {t.dtype} has {t.element_size()}-byte elements; "
+                        f"the call needs {elt}")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements; the call needs at least {numel}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: a CUDA tensor on cuda:{device} is required")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
 def head_norm_rope(parts, pos=None, stream=None):
@@ -676,14 +707,16 @@ def head_norm_rope(parts, pos=None, stream=None):
     launch for up to four tensors (include/dsa.h, dsa_head_norm_rope).  parts:
     a :class:`HeadParts`, or a list of :class:`HeadPart`."""
     parts = _parts(parts)
-    N = parts.N
     if pos is None and parts.rotates:
         raise ValueError("pos: required when a part rotates")
     arr = parts.c(False)
-    (ppos,) = _Args().add(pos, "pos", _I32, N).ptrs()
-    _on_current(parts.device())
-    rc = _lib.dsa_head_norm_rope(arr, len(arr), ppos, N, _stream(stream))
-    _check(rc, "dsa_head_norm_rope")
+    if pos is not None and not pos.is_cuda:   # sizes first, then residency, as everywhere
+        _vec(pos, "pos", 4, parts.N, -1)
+    dev = parts.device()
+    rc = _lib.dsa_head_norm_rope(arr, parts.n, _vec(pos, "pos", 4, parts.N, dev), parts.N,
+                                 _here(dev, stream))
+    if rc:
+        raise DsaError(rc, "dsa_head_norm_rope")
 
 
 def cache_append_workspace_size() -> int:
@@ -699,25 +732,28 @@ def cache_append(layout: PagedLayout, seq, pos, cache, ws, heads=None, stream=No
     cache = _parts(cache)
     N = cache.N
     arr = cache.c(True)
-    for p, have in zip(cache.parts, cache.out_bytes):
-        need = _rows(layout, p.out.stride(1)) * p.out.element_size()
-        if have < need:
-            raise ValueError(f"out: a pool of {have} bytes; the layout needs {need}")
+    if cache.pool_rows < layout.num_blocks * layout.block_size:
+        raise ValueError(f"out: a pool of {cache.pool_rows} rows; the layout needs "
+                         f"{layout.num_blocks * layout.block_size}")
     harr, nh = None, 0
     if heads is not None:
         heads = _parts(heads)
         if heads.N != N:
             raise ValueError(f"heads: {heads.N} tokens; the cache parts have {N}")
-        harr, nh = heads.c(False), len(heads)
-    a = _Args(layout).add(seq, "seq", _I32, N).add(pos, "pos", _I32, N).add(ws, "ws", _WS)
-    pseq, ppos, pws = a.ptrs()
+        harr, nh = heads.c(False), heads.n
+    for t, name, elt, numel in ((seq, "seq", 4, N), (pos, "pos", 4, N), (ws, "ws", 1, 0)):
+        if t is not None and not t.is_cuda:   # sizes first, then residency, as everywhere
+            _vec(t, name, elt, numel, -1)
     dev = cache.device()
     if nh and heads.device() != dev:
         raise ValueError("heads: on another device than the cache parts")
-    _on_current(dev)
-    rc = _lib.dsa_cache_append(layout.c(), pseq, ppos, N, arr, len(arr), harr, nh, pws, ws.numel(),
-                               _stream(stream))
-    _check(rc, "dsa_cache_append")
+    if layout.block_table.get_device() != dev or layout.seq_lens.get_device() != dev:
+        raise ValueError(f"layout: block_table and seq_lens must be CUDA tensors on cuda:{dev}")
+    rc = _lib.dsa_cache_append(layout.c(), _vec(seq, "seq", 4, N, dev), _vec(pos, "pos", 4, N, dev),
+                               N, arr, cache.n, harr, nh, _vec(ws, "ws", 1, 0, dev), ws.numel(),
+                               _here(dev, stream))
+    if rc:
+        raise DsaError(rc, "dsa_cache_append")
 
 
 def prefix_attn_decode_workspace_size(B, Hq, Dqk, Dv, prefix_len) -> int:
@@ -734,14 +770,21 @@ def prefix_attn_decode(layout: PagedLayout, q, k_pool, v_pool, prefix_len, sm_sc
     if B != layout.batch:
         raise ValueError(f"q: {B} sequences; the layout has {layout.batch}")
     ks, vs = k_pool.shape[-1], v_pool.shape[-1]
-    a = _Args(layout).add(q, "q", _BF16).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
-    a.add(v_pool, "v_pool", _BF16, _rows(layout, vs)).add(out, "out", _BF16, B * Hq * Dv)
-    a.add(lse, "lse", _F32, B * Hq).add(ws, "ws", _WS)
-    pq, pk, pv, po, pl, pws = a.ptrs()
-    _on_current(q.device.index)
-    rc = _lib.dsa_prefix_attn_decode(layout.c(), pq, pk, ks, pv, vs, Hq, Dqk, Dv, int(prefix_len),
-                                     float(sm_scale), po, pl, pws, ws.numel(), _stream(stream))
-    _check(rc, "dsa_prefix_attn_decode")
+    rows = layout.num_blocks * layout.block_size
+    ops = ((q, "q", 2, 0), (k_pool, "k_pool", 2, rows * ks), (v_pool, "v_pool", 2, rows * vs),
+           (out, "out", 2, B * Hq * Dv), (lse, "lse", 4, B * Hq), (ws, "ws", 1, 0))
+    dev = q.get_device()
+    if dev < 0:
+        for o in ops:   # sizes first, then residency, as everywhere
+            _vec(*o, -1)
+        raise ValueError("q: a CUDA tensor is required")
+    if layout.block_table.get_device() != dev or layout.seq_lens.get_device() != dev:
+        raise ValueError(f"layout: block_table and seq_lens must be CUDA tensors on cuda:{dev}")
+    pq, pk, pv, po, pl, pws = [_vec(*o, dev) for o in ops]
+    rc = _lib.dsa_prefix_attn_decode(layout.c(), pq, pk, ks, pv, vs, Hq, Dqk, Dv, prefix_len,
+                                     sm_scale, po, pl, pws, ws.numel(), _here(dev, stream))
+    if rc:
+        raise DsaError(rc, "dsa_prefix_attn_decode")
 
 
 def get_status(ws, clear: bool = True, stream=None) -> int:

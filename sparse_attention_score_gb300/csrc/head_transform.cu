@@ -787,6 +787,10 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
     if (!j.fast && !j.interleaved && rpw * j.rope_dim > p.stage_len) p.stage_len = rpw * j.rope_dim;
   }
   p.stage_len = (p.stage_len + 3) & ~3;
+  long long rows = 0;  // parts of at most 2^31 heads each: no overflow
+  for (int i = 0; i < p.n_jobs; ++i) rows += (long long)N * p.job[i].heads;
+  if (rows > 0x7fffffffLL)
+    return set_error(DSA_ERR_UNSUPPORTED, "head parts: tokens x heads beyond 2^31 - 1");
   // Heads per item: as many rounds of the warp as still leave an item for each
   // of ~32 warps per SM (the sines, cosines and coefficients are the item's),
   // one where there are few tokens and latency counts.
@@ -796,7 +800,7 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
     for (int i = 0; i < p.n_jobs; ++i) {
       HeadJob& j = p.job[i];
       const int rpw = rows_per_warp(j.dim);
-      j.first = items > 0x7fffffffLL ? 0 : (int)items;
+      j.first = (int)items;
       if (j.by_token) {
         j.group = rpw;
         j.groups = j.heads;
@@ -809,8 +813,6 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
     }
     if (items >= 32LL * sm_count()) break;
   }
-  if (items > 0x7fffffffLL)
-    return set_error(DSA_ERR_UNSUPPORTED, "head parts: tokens x heads beyond 2^31 - 1");
   if (N == 0) return DSA_OK;
   p.items = (int)items;
   const size_t smem = sizeof(float) * kWarps * (2 * (size_t)p.cs_len + p.stage_len);
