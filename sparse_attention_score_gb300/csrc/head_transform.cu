@@ -51,6 +51,7 @@ constexpr int kWarps = 4;
 constexpr int kMaxJobs = 2 * DSA_MAX_HEAD_PARTS;
 constexpr int kMaxDim = 1024;
 constexpr int kFlight = 4;  // 16-byte loads in flight per lane
+constexpr int kWide = 3;    // granules per lane of a folded head beyond 256 elements
 
 struct HeadJob {
   const __nv_bfloat16* in;
@@ -63,7 +64,6 @@ struct HeadJob {
   float eps;
   int heads, dim, norm, norm_dim, rope_off, rope_dim;
   int interleaved, fp8, paged;
-  int fast;      // the folded form applies
   int by_token;  // items: one head of several tokens, instead of heads of one token
   int groups;    // by_token 0: head groups per token; 1: heads
   int group;     // by_token 0: heads per group; 1: tokens per item
@@ -105,9 +105,9 @@ __device__ __forceinline__ unsigned long long turns_of(float f) {
   return (int)bits < 0 ? 0ull - u : u;
 }
 
-// (cos, sin) of pos * f.
-__device__ __forceinline__ float2 rotation(float f, int pos) {
-  const unsigned long long u = turns_of(f) * (unsigned long long)(long long)pos;
+// (cos, sin) of pos * f, f as turns_of(f).
+__device__ __forceinline__ float2 rotation(unsigned long long turns, int pos) {
+  const unsigned long long u = turns * (unsigned long long)(long long)pos;
   const float x = (float)(int)(u >> 32) * 4.6566128730773926e-10f;  // half turns in [-1, 1)
   float s, c;
   sincospif(x, &s, &c);
@@ -332,13 +332,11 @@ struct Coef {
   int plane;     // lane that holds the partner granule (kHalves)
 };
 
-__device__ __forceinline__ void load8(const float* p, f2 (&v)[4]) {
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
   const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = pair2(a.x, a.y);
-  v[1] = pair2(a.z, a.w);
-  v[2] = pair2(b.x, b.y);
-  v[3] = pair2(b.z, b.w);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
 __device__ __forceinline__ f2 swap2(f2 v) {
@@ -354,63 +352,67 @@ __device__ __forceinline__ void coefs(const HeadJob& j, int g, int lane, const f
   c.normed = kNorm != kNoNorm && 8 * g < j.norm_dim;
   c.plane = lane;
   int gp = g;  // partner granule of the split halves
+  float A[8], B[8], C[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c.A[i] = pair2(1.0f, 1.0f);
-  if (kTurn != kNoTurn) {
+  for (int i = 0; i < 8; ++i) {
+    A[i] = 1.0f;
+    B[i] = C[i] = 0.0f;
+  }
+  if (kTurn != kNoTurn && c.turned) {
+    if (kTurn == kNeighbours) {
+      const float4* t = reinterpret_cast<const float4*>(cs + (rel >> 1));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c.B[i] = pair2(0.0f, 0.0f);
-    if (c.turned) {
-      if (kTurn == kNeighbours) {
-        const float4* t = reinterpret_cast<const float4*>(cs + (rel >> 1));
+      for (int i = 0; i < 2; ++i) {
+        const float4 v = t[i];
+        A[4 * i] = A[4 * i + 1] = v.x;
+        B[4 * i] = -v.y;
+        B[4 * i + 1] = v.y;
+        A[4 * i + 2] = A[4 * i + 3] = v.z;
+        B[4 * i + 2] = -v.w;
+        B[4 * i + 3] = v.w;
+      }
+    } else {
+      const int half = j.rope_dim >> 1;
+      const bool first = rel < half;
+      const int d = first ? half >> 3 : -(half >> 3);
+      gp = g + d;
+      c.plane = lane + d;
+      const float sgn = first ? -1.0f : 1.0f;
+      const float4* t = reinterpret_cast<const float4*>(cs + (first ? rel : rel - half));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 v = t[i];
-          c.A[2 * i] = pair2(v.x, v.x);
-          c.B[2 * i] = pair2(-v.y, v.y);
-          c.A[2 * i + 1] = pair2(v.z, v.z);
-          c.B[2 * i + 1] = pair2(-v.w, v.w);
-        }
-      } else {
-        const int half = j.rope_dim >> 1;
-        const bool first = rel < half;
-        const int d = first ? half >> 3 : -(half >> 3);
-        gp = g + d;
-        c.plane = lane + d;
-        const float sgn = first ? -1.0f : 1.0f;
-        const float4* t = reinterpret_cast<const float4*>(cs + (first ? rel : rel - half));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 v = t[i];
-          c.A[i] = pair2(v.x, v.z);
-          c.B[i] = pair2(sgn * v.y, sgn * v.w);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = t[i];
+        A[2 * i] = v.x;
+        B[2 * i] = sgn * v.y;
+        A[2 * i + 1] = v.z;
+        B[2 * i + 1] = sgn * v.w;
       }
     }
   }
-  if (kNorm == kFull) {
+  if (kNorm != kNoNorm && c.normed) {
+    float q[8], qp[8];  // of the element, of its partner
+    if (kNorm == kFull && j.bias) {
+      load8(j.bias + 8 * g, q);
+      if (kTurn == kHalves) load8(j.bias + 8 * gp, qp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c.C[i] = pair2(0.0f, 0.0f);
-  }
-  if (!c.normed) return;
-  f2 p[4], q[4];
-  if (kNorm == kFull && j.bias) {
-    load8(j.bias + 8 * g, p);
-    if (kTurn == kHalves) load8(j.bias + 8 * gp, q);
+      for (int i = 0; i < 8; ++i)
+        C[i] = kTurn == kNoTurn ? q[i] : q[i] * A[i] + (kTurn == kHalves ? qp[i] : q[i ^ 1]) * B[i];
+    }
+    if (j.weight) {
+      load8(j.weight + 8 * g, q);
+      if (kTurn == kHalves) load8(j.weight + 8 * gp, qp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c.C[i] = p[i];
-      if (kTurn != kNoTurn && c.turned)
-        c.C[i] = fma2(kTurn == kHalves ? q[i] : swap2(p[i]), c.B[i], mul2(p[i], c.A[i]));
+      for (int i = 0; i < 8; ++i) {
+        A[i] = kTurn == kNoTurn ? q[i] : A[i] * q[i];
+        if (kTurn != kNoTurn) B[i] *= kTurn == kHalves ? qp[i] : q[i ^ 1];
+      }
     }
   }
-  if (j.weight) {
-    load8(j.weight + 8 * g, p);
-    if (kTurn == kHalves) load8(j.weight + 8 * gp, q);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c.A[i] = mul2(c.A[i], p[i]);
-      if (kTurn != kNoTurn) c.B[i] = mul2(c.B[i], kTurn == kHalves ? q[i] : swap2(p[i]));
-    }
+  for (int i = 0; i < 4; ++i) {
+    c.A[i] = pair2(A[2 * i], A[2 * i + 1]);
+    if (kTurn != kNoTurn) c.B[i] = pair2(B[2 * i], B[2 * i + 1]);
+    if (kNorm == kFull) c.C[i] = pair2(C[2 * i], C[2 * i + 1]);
   }
 }
 
@@ -485,8 +487,8 @@ __device__ __forceinline__ void transform_narrow(const HeadJob& j, const Where& 
   Coef<kNorm, kTurn> c;
   coefs(j, li, lane, w.cs, c);
   const bool mine = 8 * li < j.dim && w.tok >= 0;
-  const int step = j.by_token ? 1 : kRows;
-  const int h0 = w.h0 + (j.by_token ? 0 : sub);
+  constexpr int step = kRows;
+  const int h0 = w.h0 + sub;
   const __nv_bfloat16* in = j.in + w.tok * j.in_ts + h0 * j.in_hs + 8 * li;
   long long off = w.out_base + h0 * j.out_hs + 8 * li;
   const long long in_step = step * j.in_hs, out_step = step * j.out_hs;
@@ -539,8 +541,10 @@ __device__ __forceinline__ void transform_wide(const HeadJob& j, const Where& w,
   }
 }
 
-// One of the nine instantiations, by the part's norm and rotation.
-template <typename F>
+// The instantiation for the part's norm and rotation.  kFull is right for every
+// norm; only heads in groups, where the rounds are many, have kScale too (each
+// form costs compile time and instruction cache).
+template <bool kScaleToo, typename F>
 __device__ __forceinline__ void by_form(const HeadJob& j, F f) {
   auto turn = [&](auto norm) {
     constexpr int n = decltype(norm)::value;
@@ -553,7 +557,7 @@ __device__ __forceinline__ void by_form(const HeadJob& j, F f) {
   };
   if (j.norm == DSA_NORM_NONE)
     turn(Int<kNoNorm>());
-  else if (j.norm == DSA_NORM_RMS && !j.bias)
+  else if (kScaleToo && j.norm == DSA_NORM_RMS && !j.bias)
     turn(Int<kScale>());
   else
     turn(Int<kFull>());
@@ -586,10 +590,10 @@ __device__ __forceinline__ int locate(const HeadParams& p, const HeadJob& j, int
   return pos;
 }
 
-template <int J>
 __device__ __forceinline__ void wide_item(const HeadParams& p, const HeadJob& j, int t, Where& w,
                                           float2* cs) {
   const int lane = threadIdx.x & 31;
+  constexpr int J = kWide;
   // the first head is on its way while position and page are looked up
   const uint4* in = reinterpret_cast<const uint4*>(j.in + t * j.in_ts + w.h0 * j.in_hs);
   uint4 raw[J];
@@ -601,18 +605,90 @@ __device__ __forceinline__ void wide_item(const HeadParams& p, const HeadJob& j,
   const int pos = locate(p, j, t, lane == 0, w);
   const int half = j.rope_dim >> 1;
   w.cs = cs;
-  for (int i = lane; i < half; i += 32) cs[i] = rotation(__ldg(&j.inv_freq[i]), pos);
+  for (int i = lane; i < half; i += 32) cs[i] = rotation(turns_of(__ldg(&j.inv_freq[i])), pos);
   __syncwarp();
-  by_form(j, [&](auto f) { transform_wide<J, f.norm, f.turn>(j, w, raw); });
+  by_form<false>(j, [&](auto f) { transform_wide<J, f.norm, f.turn>(j, w, raw); });
 }
 
-// What the parts of a launch need: heads of up to 256 elements in the folded
-// form, wider ones too, or the plain path as well.  (One kernel for all three
-// has the registers of the last.)
-enum { kNarrowOnly = 0, kWithWide = 1, kWithPlain = 2 };
+// One head of tokens t0, t0 + 1, .. t1 - 1, 32 / L at a time (parts with fewer
+// heads than a warp holds: cache rows).  The frequencies' turns stay in
+// registers, the next tokens' rows and positions are on their way while these
+// are worked on.
+template <int L, int J, int kNorm, int kTurn>
+__device__ __forceinline__ void transform_tokens(const HeadParams& p, const HeadJob& j, int t0, int t1,
+                                                 int h, float2* cs) {
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / L, li = lane % L;
+  constexpr int kRows = 32 / L;
+  const int half = kTurn == kNoTurn ? 0 : j.rope_dim >> 1;
+  float2* mine = cs + sub * ((half + 1) & ~1);
+  unsigned long long u[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (li + L * i < half) u[i] = turns_of(__ldg(&j.inv_freq[li + L * i]));
+  const __nv_bfloat16* in = j.in + h * j.in_hs + 8 * li;
+  Where w;
+  w.h0 = h;
+  w.h1 = h + 1;
+  w.cs = mine;
+  uint4 raw[J];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int k = 0; k < J; ++k) {
+      raw[k] = make_uint4(0, 0, 0, 0);
+      if (t < t1 && 8 * (li + L * k) < j.dim)
+        raw[k] = *reinterpret_cast<const uint4*>(in + t * j.in_ts + 8 * L * k);
+    }
+  };
+  fetch(t0 + sub);
+  w.tok = t0 + sub < t1 ? t0 + sub : -1;
+  int pos = locate(p, j, t0 + sub, li == 0, w);
+  for (int base = t0; base < t1; base += kRows) {
+    const int t = base + sub;
+    if (kTurn != kNoTurn) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (li + L * i < half) mine[li + L * i] = rotation(u[i], pos);
+      for (int i = li + 2 * L; i < half; i += L)
+        mine[i] = rotation(turns_of(__ldg(&j.inv_freq[i])), pos);
+      __syncwarp();
+    }
+    f2 v[J][4];
+#pragma unroll
+    for (int k = 0; k < J; ++k) unpack8(raw[k], v[k]);
+    const long long out = w.out_base + h * j.out_hs + 8 * li;
+    const bool put = w.tok >= 0 && w.out_base >= 0;
+    if (base + kRows < t1) {
+      fetch(t + kRows);
+      w.tok = t + kRows < t1 ? t + kRows : -1;
+      pos = locate(p, j, t + kRows, li == 0, w);
+    }
+    const float r = normalise<L, J, kNorm>(j, v, li);
+#pragma unroll
+    for (int k = 0; k < J; ++k) {
+      const int g = li + L * k;
+      const bool live = put && 8 * g < j.dim;
+      // granules L k .. L k + L - 1: all outside the rotation, for every lane?
+      if (kTurn != kNoTurn && (J == 1 || (8 * L * k < j.rope_off + j.rope_dim && 8 * L * (k + 1) > j.rope_off))) {
+        Coef<kNorm, kTurn> c;
+        coefs(j, g, lane, mine, c);
+        finish8(j, c, v[k], r, out + 8 * L * k, live);
+      } else {
+        Coef<kNorm, kNoTurn> c;
+        coefs(j, g, lane, mine, c);
+        finish8(j, c, v[k], r, out + 8 * L * k, live);
+      }
+    }
+  }
+}
+
+// What the parts of a launch need: folded heads of up to 256 elements, up to
+// 768 elements, or the plain path (then for all of its parts).
+enum { kNarrowOnly = 0, kWithWide = 1, kPlain = 2 };
 
 template <int kKind>
-__global__ void __launch_bounds__(kWarps * 32, 8)
+__global__ void __launch_bounds__(kWarps * 32, kKind == kNarrowOnly ? 8 : 6)
     k_head_transform(const __grid_constant__ HeadParams p) {
   extern __shared__ float4 smraw[];
   grid_dependency_wait();
@@ -631,9 +707,21 @@ __global__ void __launch_bounds__(kWarps * 32, 8)
   const int L = G <= 8 ? 8 : G <= 16 ? 16 : 32;
   const int sub = lane / L, li = lane % L;
   const int hi = at / j.groups, lo = at - hi * j.groups;
+  if (kKind != kPlain && j.by_token) {
+    const int t0 = hi * j.group, t1 = min(p.N, t0 + j.group);
+    by_form<false>(j, [&](auto f) {
+      if (G <= 16)
+        transform_tokens<16, 1, f.norm, f.turn>(p, j, t0, t1, lo, cs);
+      else if (kKind == kNarrowOnly || G <= 32)
+        transform_tokens<32, 1, f.norm, f.turn>(p, j, t0, t1, lo, cs);
+      else
+        transform_tokens<32, kWide, f.norm, f.turn>(p, j, t0, t1, lo, cs);
+    });
+    return;
+  }
   int t;
   Where w;
-  if (j.by_token) {
+  if (kKind == kPlain && j.by_token) {  // one round of tokens
     t = hi * j.group + sub;
     w.h0 = lo;
     w.h1 = lo + 1;
@@ -642,29 +730,25 @@ __global__ void __launch_bounds__(kWarps * 32, 8)
     w.h0 = lo * j.group;
     w.h1 = min(j.heads, w.h0 + j.group);
   }
-  const bool there = t < p.N && (!j.by_token || sub < j.group);
-  w.tok = there ? t : -1;
-  if (kKind != kNarrowOnly && G > 32 && (kKind == kWithWide || j.fast)) {
-    if (G <= 96)
-      wide_item<3>(p, j, t, w, cs);
-    else
-      wide_item<4>(p, j, t, w, cs);
+  w.tok = t < p.N ? t : -1;
+  if (kKind == kWithWide && G > 32) {
+    wide_item(p, j, t, w, cs);
     return;
   }
   const int pos = locate(p, j, t, li == 0, w);
   const int half = j.rope_dim >> 1;
   w.cs = cs;
   if (half) {
-    if (j.by_token) {
+    if (kKind == kPlain && j.by_token) {
       float2* mine = cs + sub * ((half + 1) & ~1);
-      for (int i = li; i < half; i += L) mine[i] = rotation(__ldg(&j.inv_freq[i]), pos);
+      for (int i = li; i < half; i += L) mine[i] = rotation(turns_of(__ldg(&j.inv_freq[i])), pos);
       w.cs = mine;
     } else {
-      for (int i = lane; i < half; i += 32) cs[i] = rotation(__ldg(&j.inv_freq[i]), pos);
+      for (int i = lane; i < half; i += 32) cs[i] = rotation(turns_of(__ldg(&j.inv_freq[i])), pos);
     }
     __syncwarp();
   }
-  if (kKind == kWithPlain && !j.fast) {
+  if (kKind == kPlain) {
     if (L == 8)
       transform_plain<8, 1>(j, w, stage);
     else if (L == 16)
@@ -675,7 +759,7 @@ __global__ void __launch_bounds__(kWarps * 32, 8)
       transform_plain<32, 4>(j, w, stage);
     return;
   }
-  by_form(j, [&](auto f) {
+  by_form<true>(j, [&](auto f) {
     if (L == 8)
       transform_narrow<8, f.norm, f.turn>(j, w);
     else if (L == 16)
@@ -767,24 +851,29 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
     const bool paged = i < n_cache;
     const int rc = check_part(paged ? cache[i] : heads[i - n_cache], N, paged, &j);
     if (rc) return rc;
-    const int rpw = rows_per_warp(j.dim);
-    j.by_token = j.heads < rpw;
+    j.by_token = j.heads == 1;
     // the folded form: norm and rotation begin and end at whole granules, and
     // a rotated granule and its partner are both normed or both not, and in
     // the same register of two lanes
     const int r0 = j.rope_off, r1 = j.rope_off + j.rope_dim;
-    j.fast = (j.norm == DSA_NORM_NONE || j.norm_dim % 8 == 0) &&
-             (j.rope_dim == 0 ||
-              (r0 % 8 == 0 && r1 % 8 == 0 && (j.interleaved || j.rope_dim % 16 == 0) &&
-               (j.norm == DSA_NORM_NONE || r1 <= j.norm_dim || r0 >= j.norm_dim) &&
-               (j.interleaved || j.dim <= 256 || r0 / 256 == (r1 - 1) / 256)));
-    const int pairs = ((j.rope_dim / 2 + 1) & ~1) * (j.by_token ? rpw : 1);
-    if (pairs > p.cs_len) p.cs_len = pairs;
-    if (!j.fast)
-      kind = kWithPlain;
+    const bool folds =
+        j.dim <= 256 * kWide && (j.norm == DSA_NORM_NONE || j.norm_dim % 8 == 0) &&
+        (j.rope_dim == 0 ||
+         (r0 % 8 == 0 && r1 % 8 == 0 && (j.interleaved || j.rope_dim % 16 == 0) &&
+          (j.norm == DSA_NORM_NONE || r1 <= j.norm_dim || r0 >= j.norm_dim) &&
+          (j.interleaved || j.dim <= 256 || r0 / 256 == (r1 - 1) / 256)));
+    if (!folds)
+      kind = kPlain;
     else if (j.dim > 256 && kind == kNarrowOnly)
       kind = kWithWide;
-    if (!j.fast && !j.interleaved && rpw * j.rope_dim > p.stage_len) p.stage_len = rpw * j.rope_dim;
+  }
+  for (int i = 0; i < p.n_jobs; ++i) {
+    HeadJob& j = p.job[i];
+    const int rpw = rows_per_warp(j.dim);
+    const int pairs = ((j.rope_dim / 2 + 1) & ~1) * (j.by_token ? rpw : 1);
+    if (pairs > p.cs_len) p.cs_len = pairs;
+    if (kind == kPlain && !j.interleaved && rpw * j.rope_dim > p.stage_len)
+      p.stage_len = rpw * j.rope_dim;
   }
   p.stage_len = (p.stage_len + 3) & ~3;
   long long rows = 0;  // parts of at most 2^31 heads each: no overflow
@@ -802,9 +891,10 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
       const int rpw = rows_per_warp(j.dim);
       j.first = (int)items;
       if (j.by_token) {
-        j.group = rpw;
+        // the folded token loop takes 16 lanes for a head of up to 128
+        j.group = kind == kPlain ? rpw : (j.dim <= 128 ? 2 : 1) * (rounds < 4 ? rounds : 4);
         j.groups = j.heads;
-        items += (long long)((N + rpw - 1) / rpw) * j.heads;
+        items += ((long long)N + j.group - 1) / j.group * j.heads;
       } else {
         j.group = rounds * rpw < j.heads ? rounds * rpw : j.heads;
         j.groups = (j.heads + j.group - 1) / j.group;
@@ -820,7 +910,7 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
   const cudaError_t e =
       launch_pdl(kind == kNarrowOnly ? k_head_transform<kNarrowOnly>
                  : kind == kWithWide ? k_head_transform<kWithWide>
-                                     : k_head_transform<kWithPlain>,
+                                     : k_head_transform<kPlain>,
                  dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p);
   count_launch();
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
