@@ -99,7 +99,7 @@ struct Geo {
   int prefix_tiles;
   int Rl;           // rows of a sequence's partial: 64 or 128
   int pool_rows;
-  long long* off;   // [B + 1] first unit of each sequence's line, then the total
+  int* off;         // [B + 1] first unit of each sequence's line, then the total
   float* ml;        // [slot][128][2]
   float* po;        // prefix slots [Dv / 4][128][4], then sequence slots [Dv / 4][Rl][4]
   int slots_pre;
@@ -131,12 +131,13 @@ __device__ __forceinline__ float* slot_po(const Geo& g, int slot, bool pre) {
                    (size_t)(slot - g.slots_pre) * g.Rl * g.a.Dv;
 }
 
-// The split, computed by each warp for itself.
+// The split, computed by each warp for itself.  Units are counted in 32 bits
+// (the host refuses more).
 struct Plan {
   int src;             // first sequence that has the whole prefix
   int row_lines;       // lines over the prefix
-  long long pre, total;
-  long long mine;      // units of this pair
+  int pre, total;      // units over the prefix, of all lines
+  int mine;            // units of this pair
   int line0, unit0;    // where they start
 };
 
@@ -146,16 +147,10 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-__device__ __forceinline__ long long warp_total(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+__device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
@@ -168,45 +163,65 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 
 __device__ __forceinline__ Plan make_plan(const Geo& g, int pair, int pairs, int lane) {
   const PrefixAttnParams& a = g.a;
+  constexpr int kKept = 4;  // sequences of the first 128 in registers
   Plan p;
-  long long sum = 0;
-  int src = 0x7fffffff, n0 = 0;
-#pragma unroll 4
-  for (int b = lane; b < a.lay.batch; b += 32) {
+  int kept[kKept], sum = 0, src = 0x7fffffff;
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int b = lane + 32 * i;
+    kept[i] = b < a.lay.batch ? seq_len(a, b) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int L = kept[i];
+    kept[i] = L >= 0 ? own_units(a, L) : 0;
+    sum += kept[i];
+    if (L >= a.prefix && lane + 32 * i < src) src = lane + 32 * i;
+  }
+  for (int b = lane + 32 * kKept; b < a.lay.batch; b += 32) {
     const int L = seq_len(a, b);
-    const int n = own_units(a, L);
-    if (b == lane) n0 = n;
-    sum += n;
+    sum += own_units(a, L);
     if (L >= a.prefix && b < src) src = b;
   }
-  sum = __shfl_sync(0xffffffffu, warp_total(sum), 0);
+  sum = uniform(__reduce_add_sync(0xffffffffu, sum));
   p.src = uniform(__reduce_min_sync(0xffffffffu, src));
   p.row_lines = (a.prefix > 0 && p.src != 0x7fffffff) ? g.row_tiles : 0;
-  p.pre = (long long)p.row_lines * (g.prefix_tiles + kLineUnits);
+  const int per = g.prefix_tiles + kLineUnits;
+  p.pre = p.row_lines * per;
   p.total = p.pre + sum;
-  const int G = p.total < pairs ? (int)p.total : pairs;
-  const long long lo = pair < G ? quot(p.total * pair, G) : 0;
-  p.mine = pair < G ? quot(p.total * (pair + 1), G) - lo : 0;
+  const int G = p.total < pairs ? p.total : pairs;
+  int lo = 0;
+  p.mine = 0;
+  if (pair < G) {  // [total pair / G, total (pair + 1) / G)
+    const int q = p.total / G, r = p.total - q * G;
+    lo = pair * q + pair * r / G;
+    p.mine = (pair + 1) * q + (pair + 1) * r / G - lo;
+  }
   p.line0 = p.unit0 = 0;
   if (p.mine > 0) {
     if (lo < p.pre) {
-      p.line0 = (int)quot(lo, g.prefix_tiles + kLineUnits);
-      p.unit0 = (int)(lo - (long long)p.line0 * (g.prefix_tiles + kLineUnits));
+      p.line0 = lo / per;
+      p.unit0 = lo - p.line0 * per;
     } else {
-      long long at = p.pre;
-      for (int b0 = 0; b0 < a.lay.batch; b0 += 32) {
-        const int b = b0 + lane;
-        const int n = b0 == 0 ? n0 : (b < a.lay.batch ? own_units(a, seq_len(a, b)) : 0);
-        const long long end = at + warp_scan(n, lane);
+      int at = p.pre;
+      auto find = [&](int b0, int n) {
+        const int end = at + warp_scan(n, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, end > lo);
         if (hit) {
           const int l = __ffs(hit) - 1;
           p.line0 = p.row_lines + b0 + l;
-          p.unit0 = (int)(lo - __shfl_sync(0xffffffffu, end - n, l));
-          break;
+          p.unit0 = lo - __shfl_sync(0xffffffffu, end - n, l);
+          return true;
         }
         at = __shfl_sync(0xffffffffu, end, 31);
-      }
+        return false;
+      };
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < kKept; ++i)
+        if (!found) found = find(32 * i, kept[i]);
+      for (int b0 = 32 * kKept; b0 < a.lay.batch && !found; b0 += 32)
+        found = find(b0, b0 + lane < a.lay.batch ? own_units(a, seq_len(a, b0 + lane)) : 0);
       p.line0 = uniform(p.line0);
       p.unit0 = uniform(p.unit0);
     }
@@ -220,7 +235,7 @@ struct Tiles {
   int row0, rows;    // rows of the line
   int trow;          // row of the block table
   int p0, p1;        // positions of the line
-  long long left;    // units of this pair behind this line
+  int left;          // units of this pair behind this line
   bool ok;
 
   // units [v, ...) of the line; false if this pair has no tile of them
@@ -241,7 +256,7 @@ struct Tiles {
     }
     const int T = tiles_of(p1 - p0);
     const int n = T > 0 ? T + kLineUnits - v : 0;
-    const int take = n < left ? n : (int)left;
+    const int take = n < left ? n : left;
     left -= take;
     t = first_t = v > kLineUnits ? v - kLineUnits : 0;
     t1 = v + take - kLineUnits;
@@ -459,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Plan plan = make_plan(g, pair, gridDim.x >> 1, lane);
   if (blockIdx.x == 1 && warp == 0) {
     // for the merge: first unit of every sequence's line
-    long long at = plan.pre;
+    int at = plan.pre;
     for (int b0 = 0; b0 < a.lay.batch; b0 += 32) {
       const int b = b0 + lane;
       int n = 0;
@@ -468,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         n = own_units(a, L);
         if (__ldg(&a.lay.seq_lens[b]) > L) flag_status(a.status, DSA_STATUS_BAD_LENGTH);
       }
-      const long long end = at + warp_scan(n, lane);
+      const int end = at + warp_scan(n, lane);
       if (b < a.lay.batch) g.off[b] = end - n;
       at = __shfl_sync(0xffffffffu, end, 31);
     }
@@ -498,6 +513,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int* mytab = tab + rank * nb;
     int ahead = t.ok && lane < per ? group_row(g, t, lane, lgR) : none;  // of the next tile
     while (t.ok) {
+      if (t.first()) {  // the line's queries, once the previous line's last S is done
+        if (nq > 0 && !pair_wait(smem_u32(&sm.qempty), (nq - 1) & 1, &sm.abort)) { ok = false; break; }
+        const bool both = t.rows > 64;
+        if (rank == 0) expect_tx_elected(smem_u32(&sm.qfull), (both ? 2 : 1) * Cq * 64 * 128);
+        if (rank == 0 || both)
+          for (int c = 0; c < Cq; ++c)
+            tma_pair(smem_u32(sm.q[0]) + c * 8192, &maps.q, qbar, 64 * c, t.row0 + 64 * rank);
+        ++nq;
+      }
       bool bad = lane < per && ahead < 0;
       if (lane < per) tab[lane] = ahead;
       for (int i = lane + 32; i < per; i += 32) {
@@ -507,11 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (bad) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
       __syncwarp();
-      const bool first = t.first();
-      const int keys = t.keys(), row0 = t.row0;
-      const bool both = t.rows > 64;
-      t.next(g, plan);
-      if (t.ok && lane < per) ahead = group_row(g, t, lane, lgR);
+      const int keys = t.keys();
       {
         // Usable positions.  The slot was tile u - 8's: K of tile u - 5 at
         // the latest has left the ring of 4 stages, so S of it was issued, so
@@ -536,14 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sm.vfull[slot]);
         }
       }
-      if (first) {  // the line's queries, once the previous line's last S is done
-        if (nq > 0 && !pair_wait(smem_u32(&sm.qempty), (nq - 1) & 1, &sm.abort)) { ok = false; break; }
-        if (rank == 0) expect_tx_elected(smem_u32(&sm.qfull), (both ? 2 : 1) * Cq * 64 * 128);
-        if (rank == 0 || both)
-          for (int c = 0; c < Cq; ++c)
-            tma_pair(smem_u32(sm.q[0]) + c * 8192, &maps.q, qbar, 64 * c, row0 + 64 * rank);
-        ++nq;
-      }
+      t.next(g, plan);
+      if (t.ok && lane < per) ahead = group_row(g, t, lane, lgR);
       const int r0 = uniform(mytab[0] >= 0 ? mytab[0] : none);  // a stage of two boxes
       const int r1 = uniform(nb < 2 || mytab[1] < 0 ? none : mytab[1]);
       for (int c = 0; c < Cq; ++c) {
@@ -888,19 +902,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int Rw = pre ? kRows : g.Rl;
           float4* po = reinterpret_cast<float4*>(slot_po(g, slot, pre)) + 64 * rank + row;
 #pragma unroll 1
-          for (int q = 0; q < 2 * cols; ++q) {
-            const int i = q >> 2;
-            const int n2 = (i < ninst - 1 || cols % 2 == 0) ? 128 : 64;  // columns per half
-            const int dv = 256 * i + n2 * half + 32 * (q & 3);
-            uint32_t v[32];
-            tmem_ld_32cols(tbase + lanes + kColO + 32 * q, v);
+          for (int q0 = 0; q0 < 2 * cols; q0 += 2) {
+            uint32_t v[2][32];
+            tmem_ld_32cols(tbase + lanes + kColO + 32 * q0, v[0]);
+            tmem_ld_32cols(tbase + lanes + kColO + 32 * q0 + 32, v[1]);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (dv + 4 * j < a.Dv)
-                po[(size_t)(dv / 4 + j) * Rw] =
-                    make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+            for (int e = 0; e < 2; ++e) {
+              const int q = q0 + e, i = q >> 2;
+              const int n2 = (i < ninst - 1 || cols % 2 == 0) ? 128 : 64;  // columns per half
+              const int dv = 256 * i + n2 * half + 32 * (q & 3);
+              float4* dst = po + (size_t)(dv / 4) * Rw;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (dv + 4 * j < a.Dv)
+                  dst[j * Rw] = make_float4(__uint_as_float(v[e][4 * j]), __uint_as_float(v[e][4 * j + 1]),
+                                            __uint_as_float(v[e][4 * j + 2]),
+                                            __uint_as_float(v[e][4 * j + 3]));
+            }
           }
           tc_fence_before();
           // the two halves' sums; the slot of redm is the next tile's, whose
@@ -1189,7 +1208,7 @@ Layout ws_layout(int B, int Hq, int Dv, int prefix) {
   w.slots_pre = prefix > 0 ? kMaxPairs + w.row_tiles : 0;
   w.slots_seq = kMaxPairs + B;
   w.off = kWsHeader;
-  w.ml = w.off + round256(sizeof(long long) * ((size_t)B + 1));
+  w.ml = w.off + round256(sizeof(int) * ((size_t)B + 1));
   w.po = w.ml + round256(sizeof(float) * 2 * kRows * ((size_t)w.slots_pre + w.slots_seq));
   w.total = w.po + sizeof(float) * (size_t)Dv *
                        ((size_t)w.slots_pre * kRows + (size_t)w.slots_seq * w.Rl);
@@ -1208,7 +1227,7 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   g.a = p;
   const Layout w = ws_layout(p.lay.batch, p.Hq, p.Dv, p.prefix);
   char* base = reinterpret_cast<char*>(ws);
-  g.off = reinterpret_cast<long long*>(base + w.off);
+  g.off = reinterpret_cast<int*>(base + w.off);
   g.ml = reinterpret_cast<float*>(base + w.ml);
   g.po = reinterpret_cast<float*>(base + w.po);
   g.slots_pre = w.slots_pre;
@@ -1239,6 +1258,8 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   if (pairs > kMaxPairs) pairs = kMaxPairs;
   const long long bound = (long long)g.row_tiles * (g.prefix_tiles + kLineUnits) +
                           (long long)p.lay.batch * (p.lay.max_len / kTile + 1 + kLineUnits);
+  if (bound > 0x7fffffffLL)
+    return set_error(DSA_ERR_UNSUPPORTED, "prefix_attn_decode: rows x positions beyond 2^31 tiles");
   if (pairs > bound) pairs = bound < 1 ? 1 : (int)bound;
   cudaError_t e = launch_pdl_cluster(k_prefix_attn, dim3((unsigned)(2 * pairs)), dim3(kThreads),
                                      smem, 2, s, m, g);
