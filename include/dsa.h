@@ -426,13 +426,13 @@ int dsa_index_bounded_stats(void* ws, dsa_stream_t stream, uint64_t* tiles_skipp
  *     (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq[i],
  *     the pair being elements (2 i, 2 i + 1) if interleaved, else
  *     (i, i + rope_dim / 2) of that range; t is reduced modulo 2 pi in
- *     integers, so it stays exact to ~1e-7 at any position (inv_freq <= 1);
+ *     integers, so it stays exact to ~2e-7 at any position (inv_freq <= 1);
  *   rounded once to out_dtype (E4M3 saturates at +-448).
  * in, out and weights are device pointers.  heads >= 1; dim a multiple of 8,
  * 8..1024; strides in elements, multiples of 8; in and a bf16 out 16-byte
  * aligned, an FP8 out 8-byte; weight and bias 16-byte aligned; rope_offset
- * and rope_dim even.  out may be in itself (bf16, same strides); otherwise
- * the two, and the outs of different parts, must not overlap.
+ * and rope_dim even.  out may be in itself (bf16, same strides); apart from
+ * that no part's out may overlap any part's in or out.
  */
 #define DSA_NORM_NONE 0
 #define DSA_NORM_RMS 1
@@ -468,7 +468,7 @@ typedef struct dsa_head_part {
  * rotates.
  * Errors: DSA_ERR_INVALID for null pointers, N < 0, n_parts, strides or
  * alignment; DSA_ERR_UNSUPPORTED for other dims, dtypes or norms, and for
- * more than 2^31 - 1 (token, head) rows in all.
+ * more than 2^31 - 64 (token, head) rows in all.
  */
 int dsa_head_norm_rope(const dsa_head_part* parts, int n_parts, const int32_t* pos, int N,
                        dsa_stream_t stream);
@@ -515,9 +515,11 @@ int dsa_cache_append(const dsa_paged_layout* layout, const int32_t* seq, const i
  *  lse         [B][Hq] fp32, or NULL (-inf for an empty sequence)
  *  ws          dsa_prefix_attn_decode_workspace_size() bytes
  * Errors: DSA_ERR_INVALID / DSA_ERR_UNSUPPORTED as for
- * dsa_sparse_attn_decode and for prefix_len out of range.  Device: a position
- * behind a bad block id is left out and sets DSA_STATUS_BAD_BLOCK; a length
- * beyond the block table's row is cut there and sets DSA_STATUS_BAD_LENGTH.
+ * dsa_sparse_attn_decode, for prefix_len out of range, and for more than 2^31
+ * tiles of 128 rows x 256 positions.  Device: a position behind a bad block id
+ * is left out and sets DSA_STATUS_BAD_BLOCK; a length beyond max_seq_len is
+ * cut there and sets DSA_STATUS_BAD_LENGTH; a bounded wait that ran out sets
+ * DSA_STATUS_TIMEOUT (the outputs are then not valid).
  */
 size_t dsa_prefix_attn_decode_workspace_size(int B, int Hq, int Dqk, int Dv, int prefix_len);
 int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const void* k_pool,

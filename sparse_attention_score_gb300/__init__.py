@@ -557,7 +557,7 @@ class HeadPart:
     of a projection's output).  out: [N, heads, dim] bf16 or FP8 E4M3, strided
     likewise, for head_norm_rope and cache_append(heads=...); a paged pool
     [num_blocks, block_size, heads * dim or wider] (or [.., heads, dim]),
-    contiguous, for cache_append(cache).  norm: "none", "rms" or "layer" over
+    contiguous, for cache_append(cache); FP8 as float8_e4m3fn or as uint8 codes.  norm: "none", "rms" or "layer" over
     the first norm_dim elements (default: all), weight / bias fp32 [norm_dim].
     rope_dim > 0 rotates elements [rope_offset, rope_offset + rope_dim) by
     position * inv_freq (fp32 [rope_dim / 2]); interleaved pairs
@@ -571,9 +571,9 @@ class HeadPart:
             raise ValueError("x: [N, heads, dim] with a contiguous last dim is required")
         if x.dtype != torch.bfloat16:
             raise TypeError(f"x: {x.dtype}; bfloat16 is required")
-        if out.element_size() not in _KEY or (out.element_size() == 2 and
-                                              out.dtype != torch.bfloat16):
-            raise TypeError(f"out: {out.dtype}; bfloat16 or an 8-bit type is required")
+        if out.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"out: {out.dtype}; bfloat16, float8_e4m3fn or uint8 (E4M3 codes) "
+                            "is required")
         if norm not in NORMS:
             raise ValueError(f"norm: {norm!r}; one of {', '.join(NORMS)}")
         n, heads, dim = x.shape
@@ -607,9 +607,13 @@ class HeadPart:
             if tuple(out.shape) != (self.N, heads, dim) or out.stride(2) != 1 and dim > 1:
                 raise ValueError(f"out: {tuple(out.shape)}; {(self.N, heads, dim)} with a "
                                  "contiguous last dim is required")
-            ts, hs = out.stride(0), out.stride(1)
+            # a dimension of one element may carry any stride
+            ts = out.stride(0) if self.N > 1 else 0
+            hs = out.stride(1) if heads > 1 else dim
+        xts = x.stride(0) if self.N > 1 else 0
+        xhs = x.stride(1) if heads > 1 else 0
         opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        return HeadPartC(x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), ts, hs,
+        return HeadPartC(x.data_ptr(), xts, xhs, out.data_ptr(), ts, hs,
                          _elt_dtype(out), heads, dim, norm, norm_dim, eps, opt(self.weight),
                          opt(self.bias), roff, rdim, inter, 0, opt(self.inv_freq))
 

@@ -338,8 +338,8 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
     return set_error(DSA_ERR_INVALID,
                      "prefix_attn_decode: q / k_pool / v_pool / out must be 16-byte aligned");
-  if (!(sm_scale > 0.0f) || sm_scale > 3.4e38f)
-    return set_error(DSA_ERR_INVALID, "prefix_attn_decode: sm_scale must be a positive number");
+  if (!(sm_scale > 0.0f) || sm_scale > 1e38f)
+    return set_error(DSA_ERR_INVALID, "prefix_attn_decode: sm_scale must be a positive number up to 1e38");
   rc = check_ws(ws, ws_bytes, prefix_attn_ws(layout->batch, Hq, Dqk, Dv, prefix_len));
   if (rc) return rc;
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);

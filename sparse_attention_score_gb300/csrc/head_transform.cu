@@ -23,19 +23,27 @@
 // turns.  Its upper 32 bits go through sincospif.
 //
 // One warp per item.  A head takes 8, 16 or 32 lanes (8 elements, 16 bytes per
-// lane; heads beyond 256 elements three or four times that per lane), so a
-// warp holds four, two or one heads at a time.  An item is a group of heads of
-// one token, or, where a token has fewer heads than the warp holds, one head
-// of several tokens.  The warp forms the item's sines and cosines once; on
-// the usual shapes each lane then folds them with the weights into
+// lane; heads beyond 256 elements three times that per lane), so a warp holds
+// four, two or one heads at a time.  An item is a group of heads of one token,
+// or, for parts of one head per token (cache rows), several tokens.  The
+// warp forms the item's sines and cosines once; each lane folds them with the
+// weights into
 //   y_i = r (x_i A_i + partner_i B_i) + C_i,    r = 1 / rms (or deviation),
-// so a head costs ~90 instructions of a warp whatever the norm and rotation,
-// below the 145 that the memory system leaves time for.  Heads are loaded four
-// at a time per lane to keep ~50 KB a SM in flight.  Other shapes (a norm or a
-// rotation that ends inside 8 elements, or a rotated pair on both sides of the
-// norm's end) take a plain path through shared memory.
-// Measured on GB300 (16384 tokens, 64 rotated heads of 64 to bf16 and 64 heads
-// of 128 to E4M3, 671 MB): HEADS_PROMPT.
+// so a head of 128 costs ~45 instructions of a warp whatever the norm and
+// rotation, with the products two at a time (packed fp32).  Heads are loaded
+// four at a time per lane.  A norm or rotation that ends inside 8 elements, a
+// rotated pair on both sides of the norm's end and heads beyond 768 elements
+// take a plain path through shared memory.
+//
+// Measured on GB300: 16384 tokens, 64 rotated heads of 64 to bf16 and 64 heads
+// of 128 to E4M3 (671 MB): 118 us, 5.7 TB/s, 84 % of the copy rate; 90 million
+// warp instructions keep 60 % of the issue slots busy.  16384 cache rows of
+// 576 with their indexer keys (44 MB): 21.6 us, where a third of the stalls
+// are for instructions (each warp runs long code for a few rows).  One decode
+// step of 32 tokens: 3 us, the launch.  Tried and left out: inputs requested
+// before the position and page are known (15 % slower, registers), and a
+// rolled loop over a wide head that reads it again from L1 (25-30 us for the
+// cache rows).
 #include <cuda_runtime.h>
 
 #include <string>
@@ -878,8 +886,8 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
   p.stage_len = (p.stage_len + 3) & ~3;
   long long rows = 0;  // parts of at most 2^31 heads each: no overflow
   for (int i = 0; i < p.n_jobs; ++i) rows += (long long)N * p.job[i].heads;
-  if (rows > 0x7fffffffLL)
-    return set_error(DSA_ERR_UNSUPPORTED, "head parts: tokens x heads beyond 2^31 - 1");
+  if (rows > 0x7fffffffLL - 63)  // room for the last block's idle warps in 32 bits
+    return set_error(DSA_ERR_UNSUPPORTED, "head parts: tokens x heads beyond 2^31 - 64");
   // Heads per item: as many rounds of the warp as still leave an item for each
   // of ~32 warps per SM (the sines, cosines and coefficients are the item's),
   // one where there are few tokens and latency counts.

@@ -29,14 +29,26 @@
 //       by more than 2^8, and O is rescaled in TMEM then;
 //   O   [128 x Dv] += P . V      V as stored (MN-major), N = 256 columns per
 //       instruction; CTA r stages half of the columns of all 256 positions.
-// P is rounded to bf16 for the second product (each weight off by 2^-9 on
-// average, like the output's own rounding); sums and statistics are fp32.
+// P is rounded to bf16 for the second product (each weight by at most 2^-8 of
+// itself, like the output's own rounding); sums and statistics are fp32.
 //
-// Warp roles (192 threads): 0-3 softmax and O out of TMEM; 4 producer: TMA
-// boxes of whole 64-dim chunks into a ring of 16 KB stages, in the order the
-// MMAs take them, and the tile's table of physical rows; 5 TMEM owner and,
-// in CTA 0 of the pair, MMA issuer.  S of the next tile is issued before O of
-// this one, so the softmax runs beside the tensor cores.
+// Warp roles (256 threads): 0-3 softmax and O out of TMEM; 4 fills the ring of
+// K (and Q, and the usable positions of a tile), 5 issues S; 6 fills the ring
+// of V, 7 issues O (5 and 7 in CTA 0 of the pair only).  Each ring has one
+// filler and one reader, so a barrier's phase is never a lap off.  The weights
+// are handed over in four chunks of 64 positions and their buffer is taken
+// back in halves, so that S of the next tile, its softmax and O of this one
+// run side by side.
+//
+// What bounds it.  A tile is 36 MMAs for S and 32 for O, 64 cycles each: 4,352
+// cycles of the tensor cores for 71 MFLOP.  Per CTA it also takes 278 KB from
+// L2 through 112 KB of rings: a stage comes round in ~1,450 cycles (copy 840,
+// MMAs 256, barriers and issue the rest), which allows ~77 bytes a cycle and
+// needs 64.  Measured on GB300: ~5,700 cycles per tile; 64 sequences of 64
+// heads behind a prefix of 65,536: 361 us, 1,620 TFLOP/s (84 % of the cuBLAS
+// rate); 32 sequences behind 16,384: 62 us, 1,250 TFLOP/s.  Short lines are
+// bound by the chain from the lengths to the output (one tile: 11 us, of it 3
+// until the first copy of K is issued and 2 to write O).
 //
 // Boxes are R rows high, R the largest power of two (at most 64) that divides
 // the page size and the prefix length: such a group of positions never
@@ -80,7 +92,7 @@ struct __align__(1024) Smem {
   uint64_t sfull[2], sfree[2], oready[2], pfull[4], pdone[2], pvdone;
   uint64_t vfull[kTabs], smsync[2], done;
   float redm[2][2][64];
-  int fills[2];  // stages filled, for the drain after a failure
+  int fills[3];  // stages of K and V, and Q: times filled, for the drain after a failure
   uint32_t tmem_base;
   int abort;
 };
@@ -107,8 +119,7 @@ struct Geo {
 
 __device__ __forceinline__ int seq_len(const PrefixAttnParams& a, int b) {
   const int L = __ldg(&a.lay.seq_lens[b]);
-  const long long cap = (long long)a.lay.maxb * a.lay.bs;
-  return L < 0 ? 0 : (L > cap ? (int)cap : L);
+  return L < 0 ? 0 : min(L, a.lay.max_len);  // the bound that the host counted with
 }
 
 __device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + kTile - 1) / kTile); }
@@ -424,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     sm.abort = 0;
-    sm.fills[0] = sm.fills[1] = 0;
+    sm.fills[0] = sm.fills[1] = sm.fills[2] = 0;
     for (int i = 0; i < kStagesK; ++i) {
       mbar_init(&sm.fullk[i], 1);
       mbar_init(&sm.emptyk[i], 1);
@@ -521,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < Cq; ++c)
             tma_pair(smem_u32(sm.q[0]) + c * 8192, &maps.q, qbar, 64 * c, t.row0 + 64 * rank);
         ++nq;
+        if (lane == 0) sm.fills[2] = nq;
       }
       bool bad = lane < per && ahead < 0;
       if (lane < per) tab[lane] = ahead;
@@ -655,8 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) fail(sm, a.status);
   } else if (warp == 5) {
     // ------------------------------------------------------------ S issuer --
-    // S and O are issued by two warps: one warp needs ~450 cycles per stage
-    // (waits and loop included) for MMAs of 256, so a tile took 7,700 cycles.
+    // (With one warp issuing S and O in turn a tile took 6,800 cycles.)
     if (rank == 0) {
       Tiles t;
       t.init(g, plan);
@@ -772,9 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live) {
         // Two passes over S in TMEM, 32 columns at a time: the maximum while
         // the tensor cores work on O of the previous tile, then the weights
-        // straight into P.  Rolled loops on purpose: one pass holding all 128
-        // scores in registers is 1,200 unrolled instructions, and fetching
-        // them past the issuing warps slowed those down.
+        // straight into P.  (One pass with the thread's 128 scores in
+        // registers took 439 us where this takes 434, and 225 registers.)
         const uint32_t ta = tbase + lanes + kColS + 128 * (u & 1);
         if (!pair_wait(smem_u32(&sm.vfull[u % kTabs]), (u / kTabs) & 1, &sm.abort)) { ok = false; break; }
         const bool whole = sm.whole[u % kTabs] != 0;
@@ -959,6 +969,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = (sm.fills[1] - i + kStagesV - 1) / kStagesV;
         if (n > 0) pair_wait(smem_u32(&sm.fullv[i]), (n - 1) & 1, &never, 10000000ull);
       }
+      if (sm.fills[2] > 0) pair_wait(smem_u32(&sm.qfull), (sm.fills[2] - 1) & 1, &never, 10000000ull);
+    } else if (sm.abort) {
+      // CTA 1's copies count on CTA 0's barriers; its own never completes, so
+      // this gives them a millisecond
+      pair_wait(smem_u32(&sm.qfull), 0, &never, 1000000ull);
     }
   }
   tc_fence_before();
@@ -1241,12 +1256,12 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   g.lgbs = -1;
   for (int i = 0; i <= 10; ++i)
     if (p.lay.bs == 1 << i) g.lgbs = i;
-  Maps m;
+  Maps m{};
   int rc = make_tmap_2d(&m.q, p.q, false, p.Dqk, (uint64_t)p.lay.batch * p.Hq, (uint64_t)p.Dqk * 2,
                         64, 64);
   if (!rc)
     rc = make_tmap_2d(&m.k, p.kp, false, p.Dqk, (uint64_t)g.pool_rows, (uint64_t)p.ks * 2, 64, R);
-  for (int i = 0; i < 7 && !rc; ++i)
+  for (int i = 0; (1 << i) <= R && !rc; ++i)
     rc = make_tmap_2d(&m.v[i], p.vp, false, p.Dv, (uint64_t)g.pool_rows, (uint64_t)p.vs * 2, 64,
                       1u << i);
   if (rc) return rc;

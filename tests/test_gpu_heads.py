@@ -134,6 +134,43 @@ def test_zeros_specials_and_far_positions(scale):
     assert_heads_close(f8, w, e)
 
 
+def test_dimensions_of_one_may_carry_any_stride():
+    """One token of one head out of odd places: the strides of its unit
+    dimensions say nothing."""
+    need_gpu()
+    dsa = lib()
+    g = torch.Generator().manual_seed(12)
+    base = _randn(g, 4096)
+    x = base.as_strided((1, 1, 64), (3, 5, 1), 64)
+    room = torch.zeros(512, dtype=BF, device="cuda")
+    out = room.as_strided((1, 1, 64), (7, 1, 1), 128)
+    s = _spec(g, 64, rdim=64)
+    pos = torch.tensor([77], dtype=torch.int32)
+    dsa.head_norm_rope([dsa.HeadPart(x, out, **s)], pos.cuda())
+    assert_heads_close(out, *transform64(x, pos, **s))
+    assert bool((room[:128] == 0).all()) and bool((room[192:] == 0).all())
+
+
+def test_many_tokens_of_every_kind_of_part():
+    """Enough tokens for the long items: groups of 16 rounds, loops over four
+    tokens, wide heads, and a last item that is not full."""
+    need_gpu()
+    dsa = lib()
+    g = torch.Generator().manual_seed(13)
+    N = 9001
+    pos = torch.randint(0, 1 << 20, (N,), generator=g, dtype=torch.int32)
+    parts = []
+    for heads, dim, ot, s in ((37, 128, F8, _spec(g, 128, rdim=64)),
+                              (1, 576, BF, _spec(g, 576, norm_dim=512, roff=512, rdim=64, inter=True)),
+                              (1, 64, BF, _spec(g, 64, "layer", rdim=64, bias=True)),
+                              (2, 320, BF, _spec(g, 320, rdim=128))):
+        x = _randn(g, N, heads, dim)
+        parts.append((x, torch.empty((N, heads, dim), dtype=ot, device="cuda"), s))
+    dsa.head_norm_rope([dsa.HeadPart(x, o, **s) for x, o, s in parts], pos.cuda())
+    for k, (x, o, s) in enumerate(parts):
+        assert_heads_close(o, *transform64(x, pos, **s), what=f"part {k}")
+
+
 def test_zero_tokens_launch_nothing():
     need_gpu()
     dsa = lib()

@@ -198,6 +198,25 @@ def test_lengths_beyond_the_table_are_cut_and_flagged():
     p.check("negative", lens=[0, 100])
 
 
+def test_other_rows_do_not_see_a_nan():
+    """A NaN in one sequence's query, and one in another's own cached rows,
+    stay in their sequences' outputs."""
+    need_gpu()
+    dsa = lib()
+    p = Problem(17, [700, 900, 650, 800], bs=64, prefix=640, **LATENT).run(dsa)
+    want, lse = p.out.clone(), p.lse.clone()
+    p.q[1, 5, 100] = float("nan")
+    page = int(p.bt[2, 645 // 64])
+    p.kp[page, 645 % 64, 3] = float("inf")
+    p.run(dsa, ws=p.ws)
+    assert torch.equal(p.out[0], want[0]) and torch.equal(p.out[3], want[3])
+    assert torch.equal(p.lse[0], lse[0]) and torch.equal(p.lse[3], lse[3])
+    keep = [h for h in range(64) if h != 5]
+    assert torch.equal(p.out[1, keep], want[1, keep])
+    assert bool(torch.isnan(p.out[1, 5].float()).all())
+    assert not bool(torch.isfinite(p.out[2].float()).all())
+
+
 def test_results_repeat_bit_for_bit_and_workspaces_are_reusable():
     need_gpu()
     dsa = lib()

@@ -95,7 +95,7 @@ def test_prefix_attn_refuses_bad_calls():
                                                 Dv, prefix, sc, out, lse, ws, wsb, None)
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(prefix=-1),
                 dict(prefix=201), dict(ks=56), dict(vs=56), dict(ks=68), dict(sc=0.0), dict(sc=-1.0),
-                dict(sc=float("nan")), dict(sc=float("inf")), dict(q=FAKE + 8), dict(k=FAKE + 8),
+                dict(sc=float("nan")), dict(sc=float("inf")), dict(sc=2e38), dict(q=FAKE + 8), dict(k=FAKE + 8),
                 dict(out=FAKE + 8), dict(lay=_lay(max_seq_len=257)), dict(lay=_lay(batch=0))):
         assert call(**bad) == -1, bad
     for bad in (dict(Hq=0), dict(Hq=129), dict(Dqk=60), dict(Dqk=584, ks=584), dict(Dv=520, vs=520),
@@ -116,6 +116,8 @@ def test_the_binding_checks_parts_before_the_c_abi():
         dsa.HeadPart(x.transpose(1, 2), x)
     with pytest.raises(TypeError, match="out"):
         dsa.HeadPart(x, x.half())
+    with pytest.raises(TypeError, match="out"):
+        dsa.HeadPart(x, x.to(torch.float8_e5m2))
     with pytest.raises(ValueError, match="norm"):
         dsa.HeadPart(x, x, norm="batch")
     with pytest.raises(TypeError, match="weight"):
