@@ -515,7 +515,7 @@ int dsa_cache_append(const dsa_paged_layout* layout, const int32_t* seq, const i
  *  lse         [B][Hq] fp32, or NULL (-inf for an empty sequence)
  *  ws          dsa_prefix_attn_decode_workspace_size() bytes
  * Errors: DSA_ERR_INVALID / DSA_ERR_UNSUPPORTED as for
- * dsa_sparse_attn_decode, for prefix_len out of range, and for more than 2^31
+ * dsa_sparse_attn_decode, for prefix_len out of range, and for more than 2^30
  * tiles of 128 rows x 256 positions.  Device: a position behind a bad block id
  * is left out and sets DSA_STATUS_BAD_BLOCK; a length beyond max_seq_len is
  * cut there and sets DSA_STATUS_BAD_LENGTH; a bounded wait that ran out sets

@@ -124,22 +124,31 @@ __device__ __forceinline__ int seq_len(const PrefixAttnParams& a, int b) {
 
 __device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + kTile - 1) / kTile); }
 
-// A line of T tiles counts T + kLineUnits units in the split over the pairs,
-// the first of which have no tile: starting and ending a line (queries in,
-// first scores, last products, O out) costs about two tiles more (11,000
-// cycles against 5,700 per tile, measured on the pairs that took 41 short
-// lines each).
+// The split counts in units: kTileUnits for a tile and kLineUnits more ahead of
+// a line's first, for starting and ending it (queries in, first scores, last
+// products, O out).  A tile belongs to the pair that holds its first unit.
+// Measured with a line weighing 0, 1/2, 1, 3/2 and 2 tiles more: 64 sequences
+// behind 65,536 positions 508, 409, 343, 355 and 356 us; 32 behind 16,384 72,
+// 68, 64, 62 and 62 us; 32 short ones 23.2, 23.1, 21.6, 22.1 and 21.9 us.
+constexpr int kTileUnits = 2;
 constexpr int kLineUnits = 2;
 
 __device__ __forceinline__ int own_units(const PrefixAttnParams& a, int L) {
   const int t = tiles_of(L >= a.prefix ? L - a.prefix : L);
-  return t > 0 ? t + kLineUnits : 0;
+  return t > 0 ? kTileUnits * t + kLineUnits : 0;
 }
 
 __device__ __forceinline__ float* slot_po(const Geo& g, int slot, bool pre) {
   return pre ? g.po + (size_t)slot * kRows * g.a.Dv
              : g.po + (size_t)g.slots_pre * kRows * g.a.Dv +
                    (size_t)(slot - g.slots_pre) * g.Rl * g.a.Dv;
+}
+
+// Pairs that take part: each has kTileUnits units or more, so every pair
+// between a line's first tile and its last has one of its tiles.
+__device__ __forceinline__ int pairs_used(int total, int pairs) {
+  const int most = total / kTileUnits;
+  return most < pairs ? most : pairs;
 }
 
 // The split, computed by each warp for itself.  Units are counted in 32 bits
@@ -197,10 +206,10 @@ __device__ __forceinline__ Plan make_plan(const Geo& g, int pair, int pairs, int
   sum = uniform(__reduce_add_sync(0xffffffffu, sum));
   p.src = uniform(__reduce_min_sync(0xffffffffu, src));
   p.row_lines = (a.prefix > 0 && p.src != 0x7fffffff) ? g.row_tiles : 0;
-  const int per = g.prefix_tiles + kLineUnits;
+  const int per = kTileUnits * g.prefix_tiles + kLineUnits;
   p.pre = p.row_lines * per;
   p.total = p.pre + sum;
-  const int G = p.total < pairs ? p.total : pairs;
+  const int G = pairs_used(p.total, pairs);
   int lo = 0;
   p.mine = 0;
   if (pair < G) {  // [total pair / G, total (pair + 1) / G)
@@ -249,6 +258,10 @@ struct Tiles {
   int left;          // units of this pair behind this line
   bool ok;
 
+  // first tile that begins at unit v of a line or behind it
+  static __device__ __forceinline__ int tile_at(int v) {
+    return v > kLineUnits ? (v - kLineUnits + kTileUnits - 1) / kTileUnits : 0;
+  }
   // units [v, ...) of the line; false if this pair has no tile of them
   __device__ bool load(const Geo& g, const Plan& p, int v) {
     if (line < p.row_lines) {
@@ -266,11 +279,11 @@ struct Tiles {
       p0 = p1 >= g.a.prefix ? g.a.prefix : 0;
     }
     const int T = tiles_of(p1 - p0);
-    const int n = T > 0 ? T + kLineUnits - v : 0;
+    const int n = T > 0 ? kTileUnits * T + kLineUnits - v : 0;
     const int take = n < left ? n : left;
     left -= take;
-    t = first_t = v > kLineUnits ? v - kLineUnits : 0;
-    t1 = v + take - kLineUnits;
+    t = first_t = tile_at(v);
+    t1 = tile_at(v + take);
     return t1 > t;
   }
   __device__ void next_line(const Geo& g, const Plan& p) {
@@ -526,11 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (t.ok) {
       if (t.first()) {  // the line's queries, once the previous line's last S is done
         if (nq > 0 && !pair_wait(smem_u32(&sm.qempty), (nq - 1) & 1, &sm.abort)) { ok = false; break; }
-        const bool both = t.rows > 64;
-        if (rank == 0) expect_tx_elected(smem_u32(&sm.qfull), (both ? 2 : 1) * Cq * 64 * 128);
-        if (rank == 0 || both)
-          for (int c = 0; c < Cq; ++c)
-            tma_pair(smem_u32(sm.q[0]) + c * 8192, &maps.q, qbar, 64 * c, t.row0 + 64 * rank);
+        // (a line of at most 64 rows: both CTAs take the same rows)
+        const int q0 = t.row0 + (t.rows > 64 ? 64 * rank : 0);
+        if (rank == 0) expect_tx_elected(smem_u32(&sm.qfull), 2 * Cq * 64 * 128);
+        for (int c = 0; c < Cq; ++c)
+          tma_pair(smem_u32(sm.q[0]) + c * 8192, &maps.q, qbar, 64 * c, q0);
         ++nq;
         if (lane == 0) sm.fills[2] = nq;
       }
@@ -773,181 +786,169 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     float m = -INFINITY, l = 0.0f;
     while (t.ok && ok) {
-      const bool live = t.rows > 64 * rank;  // else this CTA's rows are not of the line
       if (t.first()) {
         m = -INFINITY;
         l = 0.0f;
       }
       if (!pair_wait(smem_u32(&sm.sfull[u & 1]), (u >> 1) & 1, &sm.abort)) { ok = false; break; }
       tc_fence_after();
-      if (live) {
-        // Two passes over S in TMEM, 32 columns at a time: the maximum while
-        // the tensor cores work on O of the previous tile, then the weights
-        // straight into P.  (One pass with the thread's 128 scores in
-        // registers took 439 us where this takes 434, and 225 registers.)
-        const uint32_t ta = tbase + lanes + kColS + 128 * (u & 1);
-        if (!pair_wait(smem_u32(&sm.vfull[u % kTabs]), (u / kTabs) & 1, &sm.abort)) { ok = false; break; }
-        const bool whole = sm.whole[u % kTabs] != 0;
-        const uint32_t* mask = &sm.mask[u % kTabs][4 * half];
-        float mt = -INFINITY;
+      // Two passes over S in TMEM, 32 columns at a time: the maximum while
+      // the tensor cores work on O of the previous tile, then the weights
+      // straight into P.  (One pass with the thread's 128 scores in
+      // registers took 439 us where this takes 434, and 225 registers.)
+      const uint32_t ta = tbase + lanes + kColS + 128 * (u & 1);
+      if (!pair_wait(smem_u32(&sm.vfull[u % kTabs]), (u / kTabs) & 1, &sm.abort)) { ok = false; break; }
+      const bool whole = sm.whole[u % kTabs] != 0;
+      const uint32_t* mask = &sm.mask[u % kTabs][4 * half];
+      float mt = -INFINITY;
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t z[32];
-          tmem_ld_32cols(ta + 32 * q, z);
-          tmem_wait_ld();
-          if (!whole) {
-            const uint32_t w = mask[q];
+      for (int q = 0; q < 4; ++q) {
+        uint32_t z[32];
+        tmem_ld_32cols(ta + 32 * q, z);
+        tmem_wait_ld();
+        if (!whole) {
+          const uint32_t w = mask[q];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((w >> i) & 1u)) z[i] = 0xff800000u;
-          }
-          float m4[4] = {mt, __uint_as_float(z[0]), __uint_as_float(z[1]), __uint_as_float(z[2])};
-#pragma unroll
-          for (int i = 3; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(z[i]));
-          mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          for (int i = 0; i < 32; ++i)
+            if (!((w >> i) & 1u)) z[i] = 0xff800000u;
         }
-        sm.redm[u & 1][half][row] = mt;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
-        if (!pair_wait(smem_u32(&sm.smsync[warp & 1]), sp, &sm.abort)) { ok = false; break; }
-        sp ^= 1;
-        mt = fmaxf(mt, sm.redm[u & 1][half ^ 1][row]) * c;
-        float f = 1.0f;
-        bool resc = false;
-        if (mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY)) {
-          if (m > -INFINITY) {
-            f = exp2f(m - mt);
-            resc = true;
-          }
-          m = mt;
-        }
-        const float mm = m == -INFINITY ? 0.0f : m;
-        if (!t.first() && __any_sync(0xffffffffu, resc)) {
-          // O of the tiles before is complete (u > 0: not the first tile)
-          if (!pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll 1
-          for (int q = 0; q < 2 * cols; ++q) {
-            uint32_t v[32];
-            tmem_ld_32cols(tbase + lanes + kColO + 32 * q, v);
-            tmem_wait_ld();
+        float m4[4] = {mt, __uint_as_float(z[0]), __uint_as_float(z[1]), __uint_as_float(z[2])};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tmem_st_32cols(tbase + lanes + kColO + 32 * q, v);
-          }
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(obar + 8 * (u & 1));
-        float ls[2] = {l * f, 0.0f};
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t z[32];
-          tmem_ld_32cols(ta + 32 * q, z);
-          tmem_wait_ld();
-          if (!whole) {
-            const uint32_t w = mask[q];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((w >> i) & 1u)) z[i] = 0xff800000u;
-          }
-          // The previous tile's products have read this chunk of P: the
-          // half's first chunk by its own barrier, the second by the whole
-          // tile's, which every tile waits for here once (a phase of pvdone
-          // left out would make a later wait test the wrong one).
-          if ((q & 1) == 0 && u > 0 &&
-              !pair_wait(q == 0 ? smem_u32(&sm.pdone[half]) : smem_u32(&sm.pvdone), (u - 1) & 1,
-                         &sm.abort)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = sm.p[2 * half + (q >> 1)] + row * 128;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // eight weights, 16 bytes of the row's 128-byte line
-            uint32_t pk[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float e0 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i]), c, -mm));
-              const float e1 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i + 1]), c, -mm));
-              ls[0] += e0;
-              ls[1] += e1;
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
-              pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            *reinterpret_cast<uint4*>(dst + (((4 * (q & 1) + k) ^ (row & 7)) << 4)) =
-                make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          }
-          if (q & 1) {  // a chunk is written
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(pbar + 8 * (q >> 1));
-          }
-        }
-        if (!ok) break;
-        l = ls[0] + ls[1];
-      } else {
-        // A warp without rows keeps in step with the others: two arrivals of
-        // it in one phase would stand for a warp that is not yet there.
-        if (lane == 0) arrive_cluster(obar + 8 * (u & 1));
-        for (int q = 0; q < 2 && ok; ++q) {
-          if (u > 0 && !pair_wait(q == 0 ? smem_u32(&sm.pdone[half]) : smem_u32(&sm.pvdone),
-                                  (u - 1) & 1, &sm.abort))
-            ok = false;
-          else if (lane == 0)
-            arrive_cluster(pbar + 8 * q);
-        }
-        if (!ok) break;
+        for (int i = 3; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(z[i]));
+        mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       }
+      sm.redm[u & 1][half][row] = mt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
+      if (!pair_wait(smem_u32(&sm.smsync[warp & 1]), sp, &sm.abort)) { ok = false; break; }
+      sp ^= 1;
+      mt = fmaxf(mt, sm.redm[u & 1][half ^ 1][row]) * c;
+      float f = 1.0f;
+      bool resc = false;
+      if (mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY)) {
+        if (m > -INFINITY) {
+          f = exp2f(m - mt);
+          resc = true;
+        }
+        m = mt;
+      }
+      const float mm = m == -INFINITY ? 0.0f : m;
+      if (!t.first() && __any_sync(0xffffffffu, resc)) {
+        // O of the tiles before is complete (u > 0: not the first tile)
+        if (!pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll 1
+        for (int q = 0; q < 2 * cols; ++q) {
+          uint32_t v[32];
+          tmem_ld_32cols(tbase + lanes + kColO + 32 * q, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+          tmem_st_32cols(tbase + lanes + kColO + 32 * q, v);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(obar + 8 * (u & 1));
+      float ls[2] = {l * f, 0.0f};
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t z[32];
+        tmem_ld_32cols(ta + 32 * q, z);
+        tmem_wait_ld();
+        if (!whole) {
+          const uint32_t w = mask[q];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((w >> i) & 1u)) z[i] = 0xff800000u;
+        }
+        // The previous tile's products have read this chunk of P: the
+        // half's first chunk by its own barrier, the second by the whole
+        // tile's, which every tile waits for here once (a phase of pvdone
+        // left out would make a later wait test the wrong one).
+        if ((q & 1) == 0 && u > 0 &&
+            !pair_wait(q == 0 ? smem_u32(&sm.pdone[half]) : smem_u32(&sm.pvdone), (u - 1) & 1,
+                       &sm.abort)) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = sm.p[2 * half + (q >> 1)] + row * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // eight weights, 16 bytes of the row's 128-byte line
+          uint32_t pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e0 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i]), c, -mm));
+            const float e1 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i + 1]), c, -mm));
+            ls[0] += e0;
+            ls[1] += e1;
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+            pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          *reinterpret_cast<uint4*>(dst + (((4 * (q & 1) + k) ^ (row & 7)) << 4)) =
+              make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        if (q & 1) {  // a chunk is written
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(pbar + 8 * (q >> 1));
+        }
+      }
+      if (!ok) break;
+      l = ls[0] + ls[1];
       __syncwarp();
       if (lane == 0) arrive_cluster(fbar + 8 * (u & 1));
       if (t.last()) {
         // this pair's partial of the line: O out of TMEM, unnormalised
         if (!pair_wait(smem_u32(&sm.pvdone), u & 1, &sm.abort)) { ok = false; break; }
         tc_fence_after();
-        if (live) {
-          const bool pre = t.pre(plan);
-          const int slot = pre ? pair + t.line : g.slots_pre + pair + t.trow;
-          const int Rw = pre ? kRows : g.Rl;
-          float4* po = reinterpret_cast<float4*>(slot_po(g, slot, pre)) + 64 * rank + row;
+        const bool pre = t.pre(plan);
+        const int slot = pre ? pair + t.line : g.slots_pre + pair + t.trow;
+        const int Rw = pre ? kRows : g.Rl;
+        // A line of at most 64 rows is in both CTAs: each writes half of its
+        // columns (one SM stores ~30 bytes a cycle, 4,400 cycles for all).
+        const bool twice = t.rows <= 64;
+        const int r = twice ? row : 64 * rank + row;
+        const int qb = twice ? rank * cols : 0, qe = twice ? qb + cols : 2 * cols;
+        float4* po = reinterpret_cast<float4*>(slot_po(g, slot, pre)) + r;
 #pragma unroll 1
-          for (int q0 = 0; q0 < 2 * cols; q0 += 2) {
-            uint32_t v[2][32];
-            tmem_ld_32cols(tbase + lanes + kColO + 32 * q0, v[0]);
-            tmem_ld_32cols(tbase + lanes + kColO + 32 * q0 + 32, v[1]);
-            tmem_wait_ld();
+        for (int q0 = qb; q0 < qe; q0 += 2) {
+          uint32_t v[2][32];
+          tmem_ld_32cols(tbase + lanes + kColO + 32 * q0, v[0]);
+          if (q0 + 1 < qe) tmem_ld_32cols(tbase + lanes + kColO + 32 * q0 + 32, v[1]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int q = q0 + e, i = q >> 2;
-              const int n2 = (i < ninst - 1 || cols % 2 == 0) ? 128 : 64;  // columns per half
-              const int dv = 256 * i + n2 * half + 32 * (q & 3);
-              float4* dst = po + (size_t)(dv / 4) * Rw;
+          for (int e = 0; e < 2; ++e) {
+            const int q = q0 + e, i = q >> 2;
+            const int n2 = (i < ninst - 1 || cols % 2 == 0) ? 128 : 64;  // columns per half
+            const int dv = 256 * i + n2 * half + 32 * (q & 3);
+            float4* dst = po + (size_t)(dv / 4) * Rw;
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (dv + 4 * j < a.Dv)
-                  dst[j * Rw] = make_float4(__uint_as_float(v[e][4 * j]), __uint_as_float(v[e][4 * j + 1]),
-                                            __uint_as_float(v[e][4 * j + 2]),
-                                            __uint_as_float(v[e][4 * j + 3]));
-            }
+            for (int j = 0; j < 8; ++j)
+              if (q < qe && dv + 4 * j < a.Dv)
+                dst[j * Rw] = make_float4(__uint_as_float(v[e][4 * j]), __uint_as_float(v[e][4 * j + 1]),
+                                          __uint_as_float(v[e][4 * j + 2]),
+                                          __uint_as_float(v[e][4 * j + 3]));
           }
-          tc_fence_before();
-          // the two halves' sums; the slot of redm is the next tile's, whose
-          // own exchange comes after this one
-          sm.redm[(u + 1) & 1][half][row] = l;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
-          if (!pair_wait(smem_u32(&sm.smsync[warp & 1]), sp, &sm.abort)) { ok = false; break; }
-          sp ^= 1;
-          if (half == 0)
-            reinterpret_cast<float2*>(g.ml)[(size_t)slot * kRows + 64 * rank + row] =
-                make_float2(m, l + sm.redm[(u + 1) & 1][1][row]);
-          // nobody writes redm[(u + 1) & 1] again before this read is done
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
-          if (!pair_wait(smem_u32(&sm.smsync[warp & 1]), sp, &sm.abort)) { ok = false; break; }
-          sp ^= 1;
         }
+        tc_fence_before();
+        // the two halves' sums; the slot of redm is the next tile's, whose
+        // own exchange comes after this one
+        sm.redm[(u + 1) & 1][half][row] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
+        if (!pair_wait(smem_u32(&sm.smsync[warp & 1]), sp, &sm.abort)) { ok = false; break; }
+        sp ^= 1;
+        if (half == 0 && !(twice && rank == 1))
+          reinterpret_cast<float2*>(g.ml)[(size_t)slot * kRows + r] =
+              make_float2(m, l + sm.redm[(u + 1) & 1][1][row]);
+        // nobody writes redm[(u + 1) & 1] again before this read is done
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.smsync[warp & 1]);
+        if (!pair_wait(smem_u32(&sm.smsync[warp & 1]), sp, &sm.abort)) { ok = false; break; }
+        sp ^= 1;
       }
       ++u;
       t.next(g, plan);
@@ -1001,21 +1002,21 @@ struct RowParts {
     const long long total = __ldcg(&g.off[a.lay.batch]), o0 = __ldcg(&g.off[b]),
                     o1 = __ldcg(&g.off[b + 1]), pre = __ldcg(&g.off[0]);
     const int L = seq_len(a, b);
-    const int G = total < pairs ? (int)total : pairs;
+    const int G = pairs_used((int)total, pairs);
     if (h >= a.Hq) return;
-    // unit x is pair ((x + 1) G - 1) / total's
+    // unit x is pair ((x + 1) G - 1) / total's; a tile is its first unit's
     if (pre > 0 && L >= a.prefix) {
       const int r = b * a.Hq + h, line = r / kRows;
       prow = r - line * kRows;
-      const long long x = (long long)line * (g.prefix_tiles + kLineUnits);
-      const int c0 = (int)quot((x + kLineUnits + 1) * G - 1, total);
-      const int c1 = (int)quot((x + kLineUnits + g.prefix_tiles) * G - 1, total);
+      const long long x = (long long)line * (kTileUnits * g.prefix_tiles + kLineUnits) + kLineUnits;
+      const int c0 = (int)quot((x + 1) * G - 1, total);
+      const int c1 = (int)quot((x + kTileUnits * (g.prefix_tiles - 1) + 1) * G - 1, total);
       p0 = c0 + line;
       np = c1 - c0 + 1;
     }
     if (o1 > o0) {
       const int c0 = (int)quot((o0 + kLineUnits + 1) * G - 1, total);
-      const int c1 = (int)quot(o1 * G - 1, total);
+      const int c1 = (int)quot((o1 - kTileUnits + 1) * G - 1, total);
       s0 = g.slots_pre + c0 + b;
       ns = c1 - c0 + 1;
     }
@@ -1271,11 +1272,12 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   int pairs = max_active_clusters((const void*)k_prefix_attn, kThreads, smem, 2);
   if (pairs < 1) return set_error(DSA_ERR_CUDA, "prefix_attn_decode: no cluster of two CTAs fits");
   if (pairs > kMaxPairs) pairs = kMaxPairs;
-  const long long bound = (long long)g.row_tiles * (g.prefix_tiles + kLineUnits) +
-                          (long long)p.lay.batch * (p.lay.max_len / kTile + 1 + kLineUnits);
+  const long long bound =
+      (long long)g.row_tiles * (kTileUnits * (long long)g.prefix_tiles + kLineUnits) +
+      (long long)p.lay.batch * (kTileUnits * (p.lay.max_len / kTile + 1LL) + kLineUnits);
   if (bound > 0x7fffffffLL)
-    return set_error(DSA_ERR_UNSUPPORTED, "prefix_attn_decode: rows x positions beyond 2^31 tiles");
-  if (pairs > bound) pairs = bound < 1 ? 1 : (int)bound;
+    return set_error(DSA_ERR_UNSUPPORTED, "prefix_attn_decode: rows x positions beyond 2^30 tiles");
+  if (pairs > bound / kTileUnits) pairs = (int)(bound / kTileUnits);
   cudaError_t e = launch_pdl_cluster(k_prefix_attn, dim3((unsigned)(2 * pairs)), dim3(kThreads),
                                      smem, 2, s, m, g);
   count_launch();
