@@ -321,7 +321,7 @@ __device__ __noinline__ void transform_plain(const HeadJob& j, const Where w, fl
 
 // The folded form, one instantiation per kind of norm and rotation.
 enum { kNoNorm = 0, kScale = 1, kFull = 2 };  // none; RMS without a bias; mean and / or bias
-enum { kNoTurn = 0, kNeighbours = 1, kHalves = 2 };
+enum { kNoTurn = 0, kNeighbours = 1, kHalves = 2, kAny = 3 };  // kAny: either, from any even element
 template <int n>
 struct Int {
   static constexpr int value = n;
@@ -338,7 +338,62 @@ struct Coef {
   bool turned;   // the granule is rotated
   bool normed;
   int plane;     // lane that holds the partner granule (kHalves)
+  int at[kTurn == kAny ? 8 : 1];  // kAny: byte of each partner among the staged heads
+  unsigned pairs;                 // kAny: which pairs of the granule are rotated
 };
+
+// kAny: the heads of a warp's round in shared memory, as read (bf16).  Word w of
+// lane l's granule is word 32 w + l: a lane's partners are a fixed distance
+// away, so neither the writes nor the reads meet in a bank.
+constexpr int kStaged = 512;  // bytes of a round
+
+__device__ __forceinline__ void stage8(uint8_t* round, int lane, const uint4& raw) {
+  uint32_t* d = reinterpret_cast<uint32_t*>(round) + lane;
+  d[0] = raw.x;
+  d[32] = raw.y;
+  d[64] = raw.z;
+  d[96] = raw.w;
+}
+
+// Coefficients of a granule whose elements each have a partner of their own.
+// `first` is the lane of the head's first granule.
+template <int kNorm>
+__device__ __forceinline__ void coefs_any(const HeadJob& j, int g, int first, const float2* cs,
+                                          Coef<kNorm, kAny>& c) {
+  const int half = j.rope_dim >> 1;
+  c.normed = kNorm != kNoNorm && 8 * g < j.norm_dim;
+  c.pairs = 0;
+  float A[8], B[8], C[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = 8 * g + i, rel = e - j.rope_off;
+    int pe = e;
+    A[i] = 1.0f;
+    B[i] = C[i] = 0.0f;
+    if (8 * g < j.dim && rel >= 0 && rel < j.rope_dim) {
+      const bool minus = j.interleaved ? (i & 1) == 0 : rel < half;
+      pe = j.interleaved ? e ^ 1 : minus ? e + half : e - half;
+      const float2 t = cs[j.interleaved ? rel >> 1 : minus ? rel : rel - half];
+      A[i] = t.x;
+      B[i] = minus ? -t.y : t.y;
+      c.pairs |= 1u << (i >> 1);
+    }
+    c.at[i] = 4 * (32 * (pe >> 1 & 3) + first + (pe >> 3)) + 2 * (pe & 1);
+    if (kNorm != kNoNorm && c.normed) {  // then the partner is normed too
+      if (kNorm == kFull && j.bias) C[i] = __ldg(&j.bias[e]) * A[i] + __ldg(&j.bias[pe]) * B[i];
+      if (j.weight) {
+        A[i] *= __ldg(&j.weight[e]);
+        B[i] *= __ldg(&j.weight[pe]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c.A[i] = pair2(A[2 * i], A[2 * i + 1]);
+    c.B[i] = pair2(B[2 * i], B[2 * i + 1]);
+    if (kNorm == kFull) c.C[i] = pair2(C[2 * i], C[2 * i + 1]);
+  }
+}
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
@@ -425,9 +480,10 @@ __device__ __forceinline__ void coefs(const HeadJob& j, int g, int lane, const f
 }
 
 // 1 / rms or 1 / deviation of a head, from the sums over its normed elements;
-// kFull also takes the mean off the values.
+// kFull also takes the mean off the values (and returns it).
 template <int L, int J, int kNorm>
-__device__ __forceinline__ float normalise(const HeadJob& j, f2 (&v)[J][4], int li) {
+__device__ __forceinline__ float normalise(const HeadJob& j, f2 (&v)[J][4], int li, float* mean_out) {
+  *mean_out = 0.0f;
   if (kNorm == kNoNorm) return 1.0f;
   const float inv = 1.0f / (float)j.norm_dim;
   if (kNorm == kFull && j.norm == DSA_NORM_LAYER) {
@@ -437,6 +493,7 @@ __device__ __forceinline__ float normalise(const HeadJob& j, f2 (&v)[J][4], int 
       if (8 * (li + L * k) < j.norm_dim) s = add2(s, add2(add2(v[k][0], v[k][1]), add2(v[k][2], v[k][3])));
     const float2 t = split2(s);
     const float mean = row_sum<L>(t.x + t.y) * inv;
+    *mean_out = mean;
     const f2 off = pair2(-mean, -mean);
 #pragma unroll
     for (int k = 0; k < J; ++k)
@@ -458,7 +515,8 @@ __device__ __forceinline__ float normalise(const HeadJob& j, f2 (&v)[J][4], int 
 
 template <int kNorm, int kTurn>
 __device__ __forceinline__ void finish8(const HeadJob& j, const Coef<kNorm, kTurn>& c,
-                                        const f2 (&v)[4], float r, long long off, bool put) {
+                                        const f2 (&v)[4], float r, long long off, bool put,
+                                        float mean = 0.0f, const uint8_t* round = nullptr) {
   f2 y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) y[i] = mul2(v[i], c.A[i]);
@@ -466,6 +524,16 @@ __device__ __forceinline__ void finish8(const HeadJob& j, const Coef<kNorm, kTur
     if (c.turned) {  // elsewhere a neighbour's NaN must not meet a B of 0
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] = fma2(swap2(v[i]), c.B[i], y[i]);
+    }
+  } else if (kTurn == kAny) {
+    const float off2 = kNorm == kFull && c.normed ? mean : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = *reinterpret_cast<const uint16_t*>(round + c.at[2 * i]);
+      const uint32_t b = *reinterpret_cast<const uint16_t*>(round + c.at[2 * i + 1]);
+      f2 p = pair2(__uint_as_float(a << 16), __uint_as_float(b << 16));
+      if (kNorm == kFull) p = add2(p, pair2(-off2, -off2));
+      if (c.pairs >> i & 1) y[i] = fma2(p, c.B[i], y[i]);
     }
   } else if (kTurn == kHalves) {
     f2 p[4];
@@ -488,12 +556,15 @@ __device__ __forceinline__ void finish8(const HeadJob& j, const Coef<kNorm, kTur
 // Heads of at most 8 L elements: coefficients in registers, up to four heads
 // in flight per lane.
 template <int L, int kNorm, int kTurn>
-__device__ __forceinline__ void transform_narrow(const HeadJob& j, const Where& w) {
+__device__ __forceinline__ void transform_narrow(const HeadJob& j, const Where& w, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
   const int sub = lane / L, li = lane % L;
   constexpr int kRows = 32 / L;
   Coef<kNorm, kTurn> c;
-  coefs(j, li, lane, w.cs, c);
+  if constexpr (kTurn == kAny)
+    coefs_any(j, li, lane - li, w.cs, c);
+  else
+    coefs(j, li, lane, w.cs, c);
   const bool mine = 8 * li < j.dim && w.tok >= 0;
   constexpr int step = kRows;
   const int h0 = w.h0 + sub;
@@ -510,13 +581,21 @@ __device__ __forceinline__ void transform_narrow(const HeadJob& j, const Where& 
       raw[q] = make_uint4(0, 0, 0, 0);
       if (mine && (r0 + q) * step < left) raw[q] = *reinterpret_cast<const uint4*>(in + q * in_step);
     }
+    if (kTurn == kAny) {
+      __syncwarp();  // the rounds before are read
+#pragma unroll
+      for (int q = 0; q < kFlight; ++q) stage8(stage + kStaged * q, lane, raw[q]);
+      __syncwarp();
+    }
 #pragma unroll
     for (int q = 0; q < kFlight; ++q) {
       if (r0 + q >= rounds) break;
       f2 v[1][4];
       unpack8(raw[q], v[0]);
-      const float r = normalise<L, 1, kNorm>(j, v, li);
-      finish8(j, c, v[0], r, off + q * out_step, put && (r0 + q) * step < left);
+      float mean;
+      const float r = normalise<L, 1, kNorm>(j, v, li, &mean);
+      finish8(j, c, v[0], r, off + q * out_step, put && (r0 + q) * step < left, mean,
+              stage + kStaged * q);
     }
     in += kFlight * in_step;
     off += kFlight * out_step;
@@ -538,7 +617,8 @@ __device__ __forceinline__ void transform_wide(const HeadJob& j, const Where& w,
       for (int k = 0; k < J; ++k)
         if (8 * (lane + 32 * k) < j.dim) raw[k] = in[lane + 32 * k];
     }
-    const float r = normalise<32, J, kNorm>(j, v, lane);
+    float mean;
+    const float r = normalise<32, J, kNorm>(j, v, lane, &mean);
 #pragma unroll
     for (int k = 0; k < J; ++k) {
       const int g = lane + 32 * k;
@@ -552,12 +632,14 @@ __device__ __forceinline__ void transform_wide(const HeadJob& j, const Where& w,
 // The instantiation for the part's norm and rotation.  kFull is right for every
 // norm; only heads in groups, where the rounds are many, have kScale too (each
 // form costs compile time and instruction cache).
-template <bool kScaleToo, typename F>
+template <bool kScaleToo, bool kAnyTurns, typename F>
 __device__ __forceinline__ void by_form(const HeadJob& j, F f) {
   auto turn = [&](auto norm) {
     constexpr int n = decltype(norm)::value;
     if (j.rope_dim == 0)
       f(Form<n, kNoTurn>());
+    else if constexpr (kAnyTurns)
+      f(Form<n, kAny>());
     else if (j.interleaved)
       f(Form<n, kNeighbours>());
     else
@@ -615,7 +697,7 @@ __device__ __forceinline__ void wide_item(const HeadParams& p, const HeadJob& j,
   w.cs = cs;
   for (int i = lane; i < half; i += 32) cs[i] = rotation(turns_of(__ldg(&j.inv_freq[i])), pos);
   __syncwarp();
-  by_form<false>(j, [&](auto f) { transform_wide<J, f.norm, f.turn>(j, w, raw); });
+  by_form<false, false>(j, [&](auto f) { transform_wide<J, f.norm, f.turn>(j, w, raw); });
 }
 
 // One head of tokens t0, t0 + 1, .. t1 - 1, 32 / L at a time (parts with fewer
@@ -624,7 +706,7 @@ __device__ __forceinline__ void wide_item(const HeadParams& p, const HeadJob& j,
 // are worked on.
 template <int L, int J, int kNorm, int kTurn>
 __device__ __forceinline__ void transform_tokens(const HeadParams& p, const HeadJob& j, int t0, int t1,
-                                                 int h, float2* cs) {
+                                                 int h, float2* cs, uint8_t* stage) {
   const int lane = threadIdx.x & 31;
   const int sub = lane / L, li = lane % L;
   constexpr int kRows = 32 / L;
@@ -660,6 +742,7 @@ __device__ __forceinline__ void transform_tokens(const HeadParams& p, const Head
         if (li + L * i < half) mine[li + L * i] = rotation(u[i], pos);
       for (int i = li + 2 * L; i < half; i += L)
         mine[i] = rotation(turns_of(__ldg(&j.inv_freq[i])), pos);
+      if (kTurn == kAny) stage8(stage, lane, raw[0]);
       __syncwarp();
     }
     f2 v[J][4];
@@ -672,7 +755,15 @@ __device__ __forceinline__ void transform_tokens(const HeadParams& p, const Head
       w.tok = t + kRows < t1 ? t + kRows : -1;
       pos = locate(p, j, t + kRows, li == 0, w);
     }
-    const float r = normalise<L, J, kNorm>(j, v, li);
+    float mean;
+    const float r = normalise<L, J, kNorm>(j, v, li, &mean);
+    if constexpr (kTurn == kAny) {
+      static_assert(J == 1, "staged heads have a granule per lane");
+      Coef<kNorm, kAny> c;
+      coefs_any(j, li, lane - li, mine, c);
+      finish8(j, c, v[0], r, out, put && 8 * li < j.dim, mean, stage);
+      continue;
+    } else {
 #pragma unroll
     for (int k = 0; k < J; ++k) {
       const int g = li + L * k;
@@ -688,12 +779,14 @@ __device__ __forceinline__ void transform_tokens(const HeadParams& p, const Head
         finish8(j, c, v[k], r, out + 8 * L * k, live);
       }
     }
+    }
   }
 }
 
 // What the parts of a launch need: folded heads of up to 256 elements, up to
-// 768 elements, or the plain path (then for all of its parts).
-enum { kNarrowOnly = 0, kWithWide = 1, kPlain = 2 };
+// 768 elements, of up to 256 with rotations that begin or end inside 8
+// elements, or the plain path (then for all of its parts).
+enum { kNarrowOnly = 0, kWithWide = 1, kAnyTurn = 2, kPlain = 3 };
 
 template <int kKind>
 __global__ void __launch_bounds__(kWarps * 32, kKind == kNarrowOnly ? 8 : 6)
@@ -705,6 +798,7 @@ __global__ void __launch_bounds__(kWarps * 32, kKind == kNarrowOnly ? 8 : 6)
   float* base = reinterpret_cast<float*>(smraw) + (size_t)warp * (2 * p.cs_len + p.stage_len);
   float2* cs = reinterpret_cast<float2*>(base);
   float* stage = base + 2 * p.cs_len;
+  uint8_t* staged = reinterpret_cast<uint8_t*>(stage);
   const int item = blockIdx.x * kWarps + warp;
   if (item >= p.items) return;
   int n = 0;
@@ -717,13 +811,13 @@ __global__ void __launch_bounds__(kWarps * 32, kKind == kNarrowOnly ? 8 : 6)
   const int hi = at / j.groups, lo = at - hi * j.groups;
   if (kKind != kPlain && j.by_token) {
     const int t0 = hi * j.group, t1 = min(p.N, t0 + j.group);
-    by_form<false>(j, [&](auto f) {
+    by_form<false, kKind == kAnyTurn>(j, [&](auto f) {
       if (G <= 16)
-        transform_tokens<16, 1, f.norm, f.turn>(p, j, t0, t1, lo, cs);
-      else if (kKind == kNarrowOnly || G <= 32)
-        transform_tokens<32, 1, f.norm, f.turn>(p, j, t0, t1, lo, cs);
-      else
-        transform_tokens<32, kWide, f.norm, f.turn>(p, j, t0, t1, lo, cs);
+        transform_tokens<16, 1, f.norm, f.turn>(p, j, t0, t1, lo, cs, staged);
+      else if (kKind != kWithWide || G <= 32)
+        transform_tokens<32, 1, f.norm, f.turn>(p, j, t0, t1, lo, cs, staged);
+      else if constexpr (kKind == kWithWide)
+        transform_tokens<32, kWide, f.norm, f.turn>(p, j, t0, t1, lo, cs, staged);
     });
     return;
   }
@@ -767,13 +861,13 @@ __global__ void __launch_bounds__(kWarps * 32, kKind == kNarrowOnly ? 8 : 6)
       transform_plain<32, 4>(j, w, stage);
     return;
   }
-  by_form<true>(j, [&](auto f) {
+  by_form<true, kKind == kAnyTurn>(j, [&](auto f) {
     if (L == 8)
-      transform_narrow<8, f.norm, f.turn>(j, w);
+      transform_narrow<8, f.norm, f.turn>(j, w, staged);
     else if (L == 16)
-      transform_narrow<16, f.norm, f.turn>(j, w);
+      transform_narrow<16, f.norm, f.turn>(j, w, staged);
     else
-      transform_narrow<32, f.norm, f.turn>(j, w);
+      transform_narrow<32, f.norm, f.turn>(j, w, staged);
   });
 }
 
@@ -853,28 +947,30 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
   p.N = N;
   p.status = status;
   p.n_jobs = n_cache + n_heads;
-  int kind = kNarrowOnly;
+  bool plain = false, any = false, wide = false;
   for (int i = 0; i < p.n_jobs; ++i) {
     HeadJob& j = p.job[i];
     const bool paged = i < n_cache;
     const int rc = check_part(paged ? cache[i] : heads[i - n_cache], N, paged, &j);
     if (rc) return rc;
     j.by_token = j.heads == 1;
-    // the folded form: norm and rotation begin and end at whole granules, and
-    // a rotated granule and its partner are both normed or both not, and in
-    // the same register of two lanes
+    // the folded forms: the norm ends at a whole granule, and a rotated element
+    // and its partner are both normed or both not ...
     const int r0 = j.rope_off, r1 = j.rope_off + j.rope_dim;
-    const bool folds =
-        j.dim <= 256 * kWide && (j.norm == DSA_NORM_NONE || j.norm_dim % 8 == 0) &&
-        (j.rope_dim == 0 ||
-         (r0 % 8 == 0 && r1 % 8 == 0 && (j.interleaved || j.rope_dim % 16 == 0) &&
-          (j.norm == DSA_NORM_NONE || r1 <= j.norm_dim || r0 >= j.norm_dim) &&
-          (j.interleaved || j.dim <= 256 || r0 / 256 == (r1 - 1) / 256)));
-    if (!folds)
-      kind = kPlain;
-    else if (j.dim > 256 && kind == kNarrowOnly)
-      kind = kWithWide;
+    const bool folds = j.dim <= 256 * kWide && (j.norm == DSA_NORM_NONE || j.norm_dim % 8 == 0) &&
+                       (j.rope_dim == 0 || j.norm == DSA_NORM_NONE || r1 <= j.norm_dim ||
+                        r0 >= j.norm_dim);
+    // ... and partners in whole granules, the same register of two lanes; else
+    // they go through shared memory
+    const bool whole = j.rope_dim == 0 ||
+                       (r0 % 8 == 0 && r1 % 8 == 0 &&
+                        (j.interleaved || (j.rope_dim % 16 == 0 &&
+                                           (j.dim <= 256 || r0 / 256 == (r1 - 1) / 256))));
+    plain |= !folds;
+    any |= !whole;
+    wide |= j.dim > 256;
   }
+  const int kind = plain || (any && wide) ? kPlain : any ? kAnyTurn : wide ? kWithWide : kNarrowOnly;
   for (int i = 0; i < p.n_jobs; ++i) {
     HeadJob& j = p.job[i];
     const int rpw = rows_per_warp(j.dim);
@@ -884,6 +980,7 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
       p.stage_len = rpw * j.rope_dim;
   }
   p.stage_len = (p.stage_len + 3) & ~3;
+  if (kind == kAnyTurn) p.stage_len = kFlight * kStaged / 4;
   long long rows = 0;  // parts of at most 2^31 heads each: no overflow
   for (int i = 0; i < p.n_jobs; ++i) rows += (long long)N * p.job[i].heads;
   if (rows > 0x7fffffffLL - 63)  // room for the last block's idle warps in 32 bits
@@ -918,6 +1015,7 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
   const cudaError_t e =
       launch_pdl(kind == kNarrowOnly ? k_head_transform<kNarrowOnly>
                  : kind == kWithWide ? k_head_transform<kWithWide>
+                 : kind == kAnyTurn  ? k_head_transform<kAnyTurn>
                                      : k_head_transform<kPlain>,
                  dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p);
   count_launch();

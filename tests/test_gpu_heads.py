@@ -171,6 +171,39 @@ def test_many_tokens_of_every_kind_of_part():
         assert_heads_close(o, *transform64(x, pos, **s), what=f"part {k}")
 
 
+# dim, norm, rope offset, rope dim, interleaved, bias: rotations that begin or
+# end inside 8 elements, halves of odd and even length, up to the whole head
+LOOSE = [(40, "rms", 0, 26, False, False), (64, "layer", 2, 60, False, True),
+         (104, "none", 6, 98, False, False), (128, "rms", 0, 72, False, True),
+         (128, "layer", 10, 20, True, False), (200, "rms", 0, 200, False, False),
+         (256, "layer", 0, 250, False, True), (256, "none", 4, 252, True, False)]
+
+
+@pytest.mark.parametrize("shape", LOOSE, ids=lambda s: f"{s[0]}-{s[1]}-{s[3]}")
+@pytest.mark.parametrize("N,heads", [(1, 9), (301, 1), (2003, 21)])
+def test_rotations_that_end_inside_eight_elements(shape, N, heads):
+    """Together, in one launch, with a rotation in whole eights and a part that
+    is not rotated; values outside the rotation meet nothing of it."""
+    need_gpu()
+    dsa = lib()
+    dim, norm, roff, rdim, inter, bias = shape
+    g = torch.Generator().manual_seed(dim + rdim + N)
+    pos = torch.randint(0, 1 << 21, (N,), generator=g, dtype=torch.int32)
+    parts = []
+    for h, d, ot, s in ((heads, dim, BF, _spec(g, dim, norm, None, roff, rdim, inter, bias=bias)),
+                        (2, 64, F8, _spec(g, 64, rdim=64)), (1, 128, F8, _spec(g, 128, "layer"))):
+        x = _randn(g, N, h, d)
+        parts.append((x, torch.empty((N, h, d), dtype=ot, device="cuda"), s))
+    if norm == "none" and roff:
+        parts[0][0][0, 0, 0] = float("inf")
+    dsa.head_norm_rope([dsa.HeadPart(x, o, **s) for x, o, s in parts], pos.cuda())
+    for k, (x, o, s) in enumerate(parts):
+        if k == 0 and norm == "none" and roff:
+            assert float(o[0, 0, 0]) == float("inf")
+            o[0, 0, 0] = x[0, 0, 0] = 0.0
+        assert_heads_close(o, *transform64(x, pos, **s), what=f"part {k}")
+
+
 def test_zero_tokens_launch_nothing():
     need_gpu()
     dsa = lib()
