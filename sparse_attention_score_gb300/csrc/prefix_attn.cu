@@ -45,17 +45,18 @@
 // L2 through 112 KB of rings: a stage comes round in ~1,450 cycles (copy 840,
 // MMAs 256, barriers and issue the rest), which allows ~77 bytes a cycle and
 // needs 64.  Measured on GB300: ~5,700 cycles per tile; 64 sequences of 64
-// heads behind a prefix of 65,536: 361 us, 1,620 TFLOP/s (84 % of the cuBLAS
-// rate); 32 sequences behind 16,384: 62 us, 1,250 TFLOP/s.  Short lines are
-// bound by the chain from the lengths to the output (one tile: 11 us, of it 3
-// until the first copy of K is issued and 2 to write O).
+// heads behind a prefix of 65,536: 346 us, 1,690 TFLOP/s (88 % of the cuBLAS
+// rate); 32 sequences behind 16,384: 64 us, 1,210 TFLOP/s.  Short lines are
+// bound by the chain from the lengths to the output (one tile: 11.4 us, of it
+// 3 until the first copy of K is issued, 1 to write O and 3 for the join).
 //
 // Boxes are R rows high, R the largest power of two (at most 64) that divides
-// the page size and the prefix length: such a group of positions never
-// crosses a page.  A group that the sequence ends in is staged for V in boxes
-// of powers of two rows, and rows past the end, or behind a bad block id, come
-// from outside the pool, which TMA fills with zeros: whatever the cache holds
-// there (NaN included) never meets a weight of 0.
+// the page size: such a group of positions never crosses a page.  A sequence's
+// own tiles begin at the group that the prefix ends in.  A group that a line
+// begins or ends in is staged for V in boxes of powers of two rows, and rows
+// that are not the line's, or behind a bad block id, come from outside the
+// pool, which TMA fills with zeros: whatever the cache holds there (NaN
+// included) never meets a weight of 0.
 // Every wait is bounded (DSA_STATUS_TIMEOUT, then the pair winds down).
 #include "device_common.cuh"
 #include "dsa_internal.cuh"
@@ -110,6 +111,7 @@ struct Geo {
   int row_tiles;    // of 128 rows over B * Hq
   int prefix_tiles;
   int Rl;           // rows of a sequence's partial: 64 or 128
+  int start;        // first position of the group that the prefix ends in
   int pool_rows;
   int* off;         // [B + 1] first unit of each sequence's line, then the total
   float* ml;        // [slot][128][2]
@@ -133,8 +135,18 @@ __device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + kTi
 constexpr int kTileUnits = 2;
 constexpr int kLineUnits = 2;
 
-__device__ __forceinline__ int own_units(const PrefixAttnParams& a, int L) {
-  const int t = tiles_of(L >= a.prefix ? L - a.prefix : L);
+// Where the tiles of a sequence of L positions begin: behind the prefix, but at
+// a whole group of R positions (the few of the prefix before are masked), so
+// that the height of a box depends on the page size alone.  (With tiles that
+// began at the prefix's end and boxes that divided both, 8 sequences of 64
+// heads behind 9,285 positions took 280 us, now 26.)
+__device__ __forceinline__ int own_start(const Geo& g, int L) {
+  return L >= g.a.prefix ? g.start : 0;
+}
+
+__device__ __forceinline__ int own_units(const Geo& g, int L) {
+  const int own = L >= g.a.prefix ? L - g.a.prefix : L;
+  const int t = min(tiles_of(L - own_start(g, L)), own);  // none where own is 0
   return t > 0 ? kTileUnits * t + kLineUnits : 0;
 }
 
@@ -194,13 +206,13 @@ __device__ __forceinline__ Plan make_plan(const Geo& g, int pair, int pairs, int
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
     const int L = kept[i];
-    kept[i] = L >= 0 ? own_units(a, L) : 0;
+    kept[i] = L >= 0 ? own_units(g, L) : 0;
     sum += kept[i];
     if (L >= a.prefix && lane + 32 * i < src) src = lane + 32 * i;
   }
   for (int b = lane + 32 * kKept; b < a.lay.batch; b += 32) {
     const int L = seq_len(a, b);
-    sum += own_units(a, L);
+    sum += own_units(g, L);
     if (L >= a.prefix && b < src) src = b;
   }
   sum = uniform(__reduce_add_sync(0xffffffffu, sum));
@@ -241,7 +253,7 @@ __device__ __forceinline__ Plan make_plan(const Geo& g, int pair, int pairs, int
       for (int i = 0; i < kKept; ++i)
         if (!found) found = find(32 * i, kept[i]);
       for (int b0 = 32 * kKept; b0 < a.lay.batch && !found; b0 += 32)
-        found = find(b0, b0 + lane < a.lay.batch ? own_units(a, seq_len(a, b0 + lane)) : 0);
+        found = find(b0, b0 + lane < a.lay.batch ? own_units(g, seq_len(a, b0 + lane)) : 0);
       p.line0 = uniform(p.line0);
       p.unit0 = uniform(p.unit0);
     }
@@ -255,6 +267,7 @@ struct Tiles {
   int row0, rows;    // rows of the line
   int trow;          // row of the block table
   int p0, p1;        // positions of the line
+  int skip;          // the first of them are the prefix's
   int left;          // units of this pair behind this line
   bool ok;
 
@@ -269,16 +282,17 @@ struct Tiles {
       const int n = g.a.lay.batch * g.a.Hq - row0;
       rows = n < kRows ? n : kRows;
       trow = p.src;
-      p0 = 0;
+      p0 = skip = 0;
       p1 = g.a.prefix;
     } else {
       trow = line - p.row_lines;
       row0 = trow * g.a.Hq;
       rows = g.a.Hq;
       p1 = uniform(seq_len(g.a, trow));
-      p0 = p1 >= g.a.prefix ? g.a.prefix : 0;
+      p0 = own_start(g, p1);
+      skip = p1 >= g.a.prefix ? g.a.prefix - p0 : 0;
     }
-    const int T = tiles_of(p1 - p0);
+    const int T = min(tiles_of(p1 - p0), p1 - p0 - skip);
     const int n = T > 0 ? kTileUnits * T + kLineUnits - v : 0;
     const int take = n < left ? n : left;
     left -= take;
@@ -311,6 +325,8 @@ struct Tiles {
     const int n = p1 - pos();
     return n < kTile ? n : kTile;
   }
+  // positions of the tile ahead of the line's own (less than a group)
+  __device__ __forceinline__ int ahead() const { return t == 0 ? skip : 0; }
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -504,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0;
       if (b < a.lay.batch) {
         const int L = seq_len(a, b);
-        n = own_units(a, L);
+        n = own_units(g, L);
         if (__ldg(&a.lay.seq_lens[b]) > L) flag_status(a.status, DSA_STATUS_BAD_LENGTH);
       }
       const int end = at + warp_scan(n, lane);
@@ -556,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (bad) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
       __syncwarp();
-      const int keys = t.keys();
+      const int keys = t.keys(), skip = t.ahead();
       {
         // Usable positions.  The slot was tile u - 8's: K of tile u - 5 at
         // the latest has left the ring of 4 stages, so S of it was issued, so
@@ -573,6 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int n = keys - k0;
           if (n < 32) word &= n <= 0 ? 0u : (1u << n) - 1u;
+          const int no = skip - k0;
+          if (no > 0) word &= no >= 32 ? 0u : ~0u << no;
           sm.mask[slot][lane] = word;
         }
         const bool whole = __all_sync(0xffffffffu, lane >= kTile / 32 || word == 0xffffffffu);
@@ -622,8 +640,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < per) tab[lane] = ahead;
       for (int i = lane + 32; i < per; i += 32) tab[i] = group_row(g, t, i, lgR);
       __syncwarp();
-      const int keys = t.keys();
+      const int keys = t.keys(), skip = t.ahead();
       const int nkk = (keys + 63) >> 6;
+      const int whole0 = skip > 0, whole1 = keys >> 6;  // chunks that are all the line's
       t.next(g, plan);
       if (t.ok && lane < per) ahead = group_row(g, t, lane, lgR);
       for (int j = 0; j < 4 && ok; ++j) {
@@ -637,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * blocks * 64 * 128);
           const uint32_t bar = fbar + 8 * r.s;
           uint32_t dst = ring + r.s * kStageBytes;
-          if (nb == 1 && (row < 0 || keys - 64 * kk >= 64)) {
+          if (nb == 1 && kk >= whole0 && kk < whole1) {
             row = row >= 0 ? row : none;
             tma_pair(dst, &maps.v[6], bar, x0, row);
             if (blocks == 2) tma_pair(dst + 8192, &maps.v[6], bar, x0 + 64, row);
@@ -649,20 +668,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int blk = 0; blk < blocks; ++blk) {
                 const int x = x0 + 64 * blk;
                 const uint32_t d = dst + 8192 * blk;
-                if (row < 0 || n >= R || n <= 0) {
+                const int n0 = (kk | gi) == 0 ? skip : 0;
+                if (row < 0 || n <= 0 || (n >= R && n0 == 0)) {
                   tma_pair(d, vmap, bar, x, row >= 0 ? row : none);
                   continue;
                 }
-                // the line ends inside the group: its rows, then zeros, in
-                // boxes of powers of two
+                // the line begins or ends inside the group: zeros, its rows,
+                // zeros, in boxes of powers of two
+                const int n1 = n < R ? n : R;
                 int at = 0;
+                if (n0 > 0)
+                  for (int e = lgR - 1; e >= 0; --e)
+                    if (n0 >> e & 1) {
+                      tma_pair(d + at * 128, &maps.v[e], bar, x, none);
+                      at += 1 << e;
+                    }
                 for (int e = lgR - 1; e >= 0; --e)
-                  if (n >> e & 1) {
+                  if ((n1 - n0) >> e & 1) {
                     tma_pair(d + at * 128, &maps.v[e], bar, x, row + at);
                     at += 1 << e;
                   }
                 for (int e = lgR - 1; e >= 0; --e)
-                  if ((R - n) >> e & 1) {
+                  if ((R - n1) >> e & 1) {
                     tma_pair(d + at * 128, &maps.v[e], bar, x, none);
                     at += 1 << e;
                   }
@@ -680,7 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) fail(sm, a.status);
   } else if (warp == 5) {
     // ------------------------------------------------------------ S issuer --
-    // (With one warp issuing S and O in turn a tile took 6,800 cycles.)
+    // (With one warp issuing S and O in turn a tile took 7,700 cycles; with
+    // two and the weights handed over whole 6,800; with the chunks 5,700.)
     if (rank == 0) {
       Tiles t;
       t.init(g, plan);
@@ -1252,8 +1280,9 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   g.prefix_tiles = (p.prefix + kTile - 1) / kTile;
   g.pool_rows = (int)((long long)p.lay.nb * p.lay.bs);
   int R = 64;
-  while (p.lay.bs % R || p.prefix % R) R >>= 1;
+  while (p.lay.bs % R) R >>= 1;
   g.R = R;
+  g.start = p.prefix & -R;
   g.lgbs = -1;
   for (int i = 0; i <= 10; ++i)
     if (p.lay.bs == 1 << i) g.lgbs = i;

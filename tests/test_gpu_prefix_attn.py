@@ -113,6 +113,27 @@ def test_prefix_attn_matches_64_bits(name):
     p.check(name)
 
 
+@pytest.mark.parametrize("bs", [16, 48, 64, 128, 1024])
+@pytest.mark.parametrize("prefix", [1, 31, 33, 63, 100, 319, 1023])
+def test_prefixes_that_end_anywhere(bs, prefix):
+    """The sequences' own tiles begin inside a group of positions: what their
+    own pages hold ahead of them (NaN) is neither K nor V of theirs."""
+    need_gpu()
+    dsa = lib()
+    lens = [prefix - 1, prefix + 300, prefix, prefix + 1, prefix + 63, prefix + 64, prefix + 257]
+    for kw in (LATENT, dict(Hq=5, Dqk=72, Dv=200, latent=False)):
+        p = Problem(bs + prefix, lens, bs=bs, prefix=prefix, **kw)
+        if prefix % bs:
+            for b in range(2, len(lens)):          # sequence 1 is the prefix's source
+                page = int(p.bt[b, prefix // bs])
+                if lens[b] > prefix:
+                    p.kp[page, :prefix % bs] = float("nan")
+                    p.vp[page, :prefix % bs] = float("nan")
+        p.run(dsa)
+        assert dsa.get_status(p.ws) == 0
+        p.check(f"prefix {prefix} pages of {bs}")
+
+
 def test_many_short_lines_per_pair_stay_in_step():
     """Sequences of a few tiles with 64 heads: one CTA of a pair has no rows of
     any line, and must not run ahead of the other.  Many runs of one problem,
@@ -129,12 +150,13 @@ def test_many_short_lines_per_pair_stay_in_step():
 
 
 def test_slow_copies_of_v_do_not_reorder_a_pair():
-    """Prefixes that leave boxes of 4 rows and 1 row (V arrives slowly) with
+    """Pages that leave boxes of 4 rows and 1 row (V arrives slowly) with
     several tiles of a line on one pair, so that the softmax runs far ahead of
     the second product."""
     need_gpu()
     dsa = lib()
-    for prefix, bs, dv in ((500, 32, 64), (500, 32, 128), (1021, 16, 512), (516, 48, 320)):
+    for prefix, bs, dv in ((500, 4, 64), (500, 12, 128), (1021, 1, 512), (516, 20, 320), (500, 32, 64),
+                           (1021, 16, 512)):
         p = Problem(prefix, [prefix + (37 * i) % 90 for i in range(70)], bs=bs, prefix=prefix, Hq=64,
                     Dqk=96, Dv=dv, latent=False).run(dsa)
         p.check(f"prefix {prefix} dv {dv}")
