@@ -714,9 +714,11 @@ def head_norm_rope(parts, pos=None, stream=None):
     if pos is None and parts.rotates:
         raise ValueError("pos: required when a part rotates")
     arr = parts.c(False)
-    if pos is not None and not pos.is_cuda:   # sizes first, then residency, as everywhere
-        _vec(pos, "pos", 4, parts.N, -1)
-    dev = parts.device()
+    dev = parts._device
+    if dev is None:
+        if pos is not None and not pos.is_cuda:   # sizes first, then residency, as everywhere
+            _vec(pos, "pos", 4, parts.N, -1)
+        dev = parts.device()
     rc = _lib.dsa_head_norm_rope(arr, parts.n, _vec(pos, "pos", 4, parts.N, dev), parts.N,
                                  _here(dev, stream))
     if rc:
@@ -745,10 +747,12 @@ def cache_append(layout: PagedLayout, seq, pos, cache, ws, heads=None, stream=No
         if heads.N != N:
             raise ValueError(f"heads: {heads.N} tokens; the cache parts have {N}")
         harr, nh = heads.c(False), heads.n
-    for t, name, elt, numel in ((seq, "seq", 4, N), (pos, "pos", 4, N), (ws, "ws", 1, 0)):
-        if t is not None and not t.is_cuda:   # sizes first, then residency, as everywhere
-            _vec(t, name, elt, numel, -1)
-    dev = cache.device()
+    dev = cache._device
+    if dev is None:
+        for t, name, elt, numel in ((seq, "seq", 4, N), (pos, "pos", 4, N), (ws, "ws", 1, 0)):
+            if t is not None and not t.is_cuda:   # sizes first, then residency, as everywhere
+                _vec(t, name, elt, numel, -1)
+        dev = cache.device()
     if nh and heads.device() != dev:
         raise ValueError("heads: on another device than the cache parts")
     if layout.block_table.get_device() != dev or layout.seq_lens.get_device() != dev:
@@ -775,16 +779,17 @@ def prefix_attn_decode(layout: PagedLayout, q, k_pool, v_pool, prefix_len, sm_sc
         raise ValueError(f"q: {B} sequences; the layout has {layout.batch}")
     ks, vs = k_pool.shape[-1], v_pool.shape[-1]
     rows = layout.num_blocks * layout.block_size
-    ops = ((q, "q", 2, 0), (k_pool, "k_pool", 2, rows * ks), (v_pool, "v_pool", 2, rows * vs),
-           (out, "out", 2, B * Hq * Dv), (lse, "lse", 4, B * Hq), (ws, "ws", 1, 0))
-    dev = q.get_device()
+    dev = q.get_device()   # -1: the sizes are checked all the same, then q is refused
+    pq = _vec(q, "q", 2, 0, dev)
+    pk = _vec(k_pool, "k_pool", 2, rows * ks, dev)
+    pv = pk if v_pool is k_pool else _vec(v_pool, "v_pool", 2, rows * vs, dev)
+    po = _vec(out, "out", 2, B * Hq * Dv, dev)
+    pl = _vec(lse, "lse", 4, B * Hq, dev)
+    pws = _vec(ws, "ws", 1, 0, dev)
     if dev < 0:
-        for o in ops:   # sizes first, then residency, as everywhere
-            _vec(*o, -1)
         raise ValueError("q: a CUDA tensor is required")
     if layout.block_table.get_device() != dev or layout.seq_lens.get_device() != dev:
         raise ValueError(f"layout: block_table and seq_lens must be CUDA tensors on cuda:{dev}")
-    pq, pk, pv, po, pl, pws = [_vec(*o, dev) for o in ops]
     rc = _lib.dsa_prefix_attn_decode(layout.c(), pq, pk, ks, pv, vs, Hq, Dqk, Dv, prefix_len,
                                      sm_scale, po, pl, pws, ws.numel(), _here(dev, stream))
     if rc:
