@@ -161,6 +161,10 @@ int check_launch(const char* what);
 // apart; box of box_inner x box_rows.
 int make_tmap_2d(CUtensorMap* map, const void* base, bool one_byte, uint64_t inner_elems,
                  uint64_t rows, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);
+// bf16 [rows][cols] as boxes of box_rows rows x box_blocks blocks of 64 columns,
+// block after block in shared memory (128-byte swizzle); cols a multiple of 64.
+int make_tmap_blocks(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                     uint64_t row_stride_bytes, uint32_t box_rows, uint32_t box_blocks);
 int sm_count();  // of the current device
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current
 // device (once per kernel and device, thread-safe); DSA_ERR_CUDA on failure.

@@ -45,6 +45,22 @@ int make_tmap_2d(CUtensorMap* map, const void* base, bool one_byte, uint64_t inn
   return DSA_OK;
 }
 
+int make_tmap_blocks(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                     uint64_t row_stride_bytes, uint32_t box_rows, uint32_t box_blocks) {
+  auto fn = encode_fn();
+  if (!fn) return set_error(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[3] = {64, rows, cols / 64};
+  cuuint64_t strides[2] = {row_stride_bytes, 128};
+  cuuint32_t box[3] = {64, box_rows, box_blocks};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(DSA_ERR_CUDA, "cuTensorMapEncodeTiled failed with " + std::to_string((int)r));
+  return DSA_OK;
+}
+
 int sm_count() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;

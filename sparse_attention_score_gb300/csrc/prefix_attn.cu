@@ -56,7 +56,12 @@
 // begins or ends in is staged for V in boxes of powers of two rows, and rows
 // that are not the line's, or behind a bad block id, come from outside the
 // pool, which TMA fills with zeros: whatever the cache holds there (NaN
-// included) never meets a weight of 0.
+// included) never meets a weight of 0.  Pages below 64 rows take more boxes, and
+// what a box costs is its issue: rows come out of a lane's register by shuffle,
+// loops are short, and 16 or 32 rows of V take both 64-column blocks in one box.
+// 32 sequences behind 16,384 positions, own parts of up to 512: 56 us with
+// pages of 64, 64 with 32, 72 with 16, 92 with 8 (rows read from shared memory
+// one by one: 56, 87, 126 and 203).
 // Every wait is bounded (DSA_STATUS_TIMEOUT, then the pair winds down).
 #include "device_common.cuh"
 #include "dsa_internal.cuh"
@@ -101,13 +106,21 @@ struct __align__(1024) Smem {
 static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory of k_prefix_attn");
 
 struct Maps {
-  CUtensorMap q, k, v[7];  // v[i]: boxes of 2^i rows
+  CUtensorMap q, k, v[7];  // v[i]: boxes of 2^i rows of 64 columns
+  CUtensorMap v2;          // boxes of R rows of two 64-column blocks
 };
 
 struct Geo {
   PrefixAttnParams a;
   int R;            // rows per box
   int lgbs;         // log2 of the page size, or -1
+  // V is staged [group of Rv positions][64-column block][position of the group];
+  // where 16 <= R < 64, R itself, so that a box can hold both blocks (`wide`:
+  // Dv a multiple of 256) and 16 positions, an MMA's, still lie in one group.
+  // With R = 64 two boxes of 8 KB are ahead of one of 16: 345 against 350 us
+  // for 64 sequences behind 65,536 positions.
+  int Rv;
+  int wide;
   int row_tiles;    // of 128 rows over B * Hq
   int prefix_tiles;
   int Rl;           // rows of a sequence's partial: 64 or 128
@@ -380,7 +393,8 @@ __device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatil
 // uniform registers.  Issued from a single-lane branch each MMA cost ~140
 // cycles of register moves, twice its time on the tensor cores.
 
-// TMA box into this CTA's shared memory; its bytes count on `bar` of CTA 0.
+// TMA box (of one 64-column block, of several) into this CTA's shared memory; its
+// bytes count on `bar` of CTA 0.
 __device__ __forceinline__ void tma_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
                                          int y) {
   asm volatile(
@@ -389,6 +403,17 @@ __device__ __forceinline__ void tma_pair(uint32_t dst, const CUtensorMap* map, u
       "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
       " [%0], [%1, {%2, %3}], [%4];\n\t}\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_pair3(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x,
+                                          int y, int z) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 
@@ -601,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       t.next(g, plan);
       if (t.ok && lane < per) ahead = group_row(g, t, lane, lgR);
+      const int krows = lane < nb && mytab[lane] >= 0 ? mytab[lane] : none;
       const int r0 = uniform(mytab[0] >= 0 ? mytab[0] : none);  // a stage of two boxes
       const int r1 = uniform(nb < 2 || mytab[1] < 0 ? none : mytab[1]);
       for (int c = 0; c < Cq; ++c) {
@@ -611,8 +637,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_pair(dst, &maps.k, bar, 64 * c, r0);
           tma_pair(dst + kStageBytes / 2, &maps.k, bar, 64 * c, r1);
         } else {
-          for (int i = 0; i < nb; ++i)
-            tma_pair(dst + ((i << lgR) << 7), &maps.k, bar, 64 * c, mytab[i] >= 0 ? mytab[i] : none);
+          uint32_t to = dst;
+          for (int i0 = 0; i0 < nb; i0 += 32) {
+            int row = krows;
+            if (i0 > 0) row = mytab[i0 + lane] >= 0 ? mytab[i0 + lane] : none;
+            const int n = nb - i0 < 32 ? nb - i0 : 32;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i, to += R * 128)
+              tma_pair(to, &maps.k, bar, 64 * c, __shfl_sync(0xffffffffu, row, i));
+          }
         }
         r.step();
         if (lane == 0) sm.fills[0] = u * Cq + c + 1;
@@ -634,21 +667,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t empty = smem_u32(&sm.emptyv[0]), full = smem_u32(&sm.fullv[0]);
     const int nb = 64 >> lgR;
     const CUtensorMap* vmap = &maps.v[lgR];
+    const uint32_t bstep = g.Rv * 128;  // to the next block of a group
     int* tab = sm.tab[1];
     int ahead = t.ok && lane < per ? group_row(g, t, lane, lgR) : none;
     while (t.ok) {
-      if (lane < per) tab[lane] = ahead;
-      for (int i = lane + 32; i < per; i += 32) tab[i] = group_row(g, t, i, lgR);
-      __syncwarp();
       const int keys = t.keys(), skip = t.ahead();
       const int nkk = (keys + 63) >> 6;
-      const int whole0 = skip > 0, whole1 = keys >> 6;  // chunks that are all the line's
+      // the tile's groups, a lane each (more than 32, in pages of odd sizes, in
+      // shared memory), and those that the line begins or ends in
+      unsigned cuts = 0xffffffffu;
+      const int rows = ahead >= 0 ? ahead : none;
+      if (per <= 32) {
+        const int n = keys - (lane << lgR);
+        cuts = __ballot_sync(0xffffffffu, lane < per && rows != none && (n < R || (lane == 0 && skip > 0)));
+      } else {
+        for (int i = lane; i < per; i += 32) {
+          const int row = i < 32 ? ahead : group_row(g, t, i, lgR);
+          tab[i] = row >= 0 ? row : none;
+        }
+        __syncwarp();
+      }
       t.next(g, plan);
       if (t.ok && lane < per) ahead = group_row(g, t, lane, lgR);
       for (int j = 0; j < 4 && ok; ++j) {
         const int kk = (j >> 1) | ((j & 1) << 1);  // the O issuer's order
         if (kk >= nkk) continue;
-        int row = uniform(tab[(64 * kk) >> lgR]);
+        const int g0 = kk * nb;
+        const bool cut = per > 32 || (cuts >> g0 & ((1u << nb) - 1u)) != 0;
         for (int i = 0; i < ninst; ++i) {
           const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;  // 64-column blocks per CTA
           const int x0 = 256 * i + 64 * blocks * rank;
@@ -656,26 +701,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * blocks * 64 * 128);
           const uint32_t bar = fbar + 8 * r.s;
           uint32_t dst = ring + r.s * kStageBytes;
-          if (nb == 1 && kk >= whole0 && kk < whole1) {
-            row = row >= 0 ? row : none;
-            tma_pair(dst, &maps.v[6], bar, x0, row);
-            if (blocks == 2) tma_pair(dst + 8192, &maps.v[6], bar, x0 + 64, row);
+          const uint32_t gstep = R * 128 * (R >= 16 ? blocks : 1);
+          if (!cut && g.wide) {
+            const int z = x0 >> 6;
+#pragma unroll 1
+            for (int gi = 0; gi < nb; ++gi, dst += gstep)
+              tma_pair3(dst, &maps.v2, bar, 0, __shfl_sync(0xffffffffu, rows, g0 + gi), z);
+          } else if (!cut) {
+#pragma unroll 1
+            for (int gi = 0; gi < nb; ++gi, dst += gstep) {
+              const int row = __shfl_sync(0xffffffffu, rows, g0 + gi);
+              tma_pair(dst, vmap, bar, x0, row);
+              if (blocks == 2) tma_pair(dst + bstep, vmap, bar, x0 + 64, row);
+            }
           } else {
-            for (int gi = 0; gi < nb; ++gi, dst += R * 128) {
-              const int k0 = 64 * kk + (gi << lgR);  // first position of the group in the tile
-              row = uniform(tab[k0 >> lgR]);
-              const int n = keys - k0;               // cached positions of the group
+            for (int gi = 0; gi < nb; ++gi, dst += gstep) {
+              const int row = per <= 32 ? __shfl_sync(0xffffffffu, rows, g0 + gi) : uniform(tab[g0 + gi]);
+              const int k0 = (g0 + gi) << lgR, n = keys - k0;  // cached positions of the group
+              const int n0 = k0 == 0 ? skip : 0, n1 = n < R ? n : R;
               for (int blk = 0; blk < blocks; ++blk) {
                 const int x = x0 + 64 * blk;
-                const uint32_t d = dst + 8192 * blk;
-                const int n0 = (kk | gi) == 0 ? skip : 0;
-                if (row < 0 || n <= 0 || (n >= R && n0 == 0)) {
-                  tma_pair(d, vmap, bar, x, row >= 0 ? row : none);
+                const uint32_t d = dst + bstep * blk;
+                if (row == none || (n >= R && n0 == 0)) {
+                  tma_pair(d, vmap, bar, x, row);
                   continue;
                 }
-                // the line begins or ends inside the group: zeros, its rows,
-                // zeros, in boxes of powers of two
-                const int n1 = n < R ? n : R;
+                // zeros, the line's rows, zeros, in boxes of powers of two
                 int at = 0;
                 if (n0 > 0)
                   for (int e = lgR - 1; e >= 0; --e)
@@ -761,7 +812,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const uint32_t empty = smem_u32(&sm.emptyv[0]), full = smem_u32(&sm.fullv[0]);
       const uint64_t dp = smem_desc(smem_u32(sm.p[0]), 16, 1024, kSwizzle128B);
-      const uint64_t dv = smem_desc(smem_u32(sm.ringv[0]), 8192, 1024, kSwizzle128B);
+      const uint64_t dv = smem_desc(smem_u32(sm.ringv[0]), g.Rv * 128, 1024, kSwizzle128B);
+      // the second, third and fourth 16 positions of a chunk of two blocks
+      const int lgs = 27 - __clz(g.Rv), in = (1 << lgs) - 1;
+      const int o1 = (1 >> lgs) * 16 * g.Rv + (1 & in) * 128;
+      const int o2 = (2 >> lgs) * 16 * g.Rv + (2 & in) * 128;
+      const int o3 = (3 >> lgs) * 16 * g.Rv + (3 & in) * 128;
       while (t.ok && ok) {
         const int nkk = (t.keys() + 63) >> 6;
         const int add0 = t.first() ? 0 : 1;
@@ -783,8 +839,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
               tc_fence_after();
               const uint64_t vb = dv + 1024 * r.s;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_pair(d, pa + 2 * k, vb + 128 * k, id, add0 + j + k);
+              const bool two = blocks == 2;
+              mma_pair(d, pa, vb, id, add0 + j);
+              mma_pair(d, pa + 2, vb + (two ? o1 : 128), id, 1);
+              mma_pair(d, pa + 4, vb + (two ? o2 : 256), id, 1);
+              mma_pair(d, pa + 6, vb + (two ? o3 : 384), id, 1);
               commit_pair(empty + 8 * r.s);
               r.step();
             }
@@ -1294,6 +1353,10 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   for (int i = 0; (1 << i) <= R && !rc; ++i)
     rc = make_tmap_2d(&m.v[i], p.vp, false, p.Dv, (uint64_t)g.pool_rows, (uint64_t)p.vs * 2, 64,
                       1u << i);
+  g.Rv = R >= 16 ? R : 64;  // (smaller groups would cut an MMA's positions)
+  g.wide = R >= 16 && R < 64 && p.Dv % 256 == 0;
+  if (!rc && g.wide)
+    rc = make_tmap_blocks(&m.v2, p.vp, p.Dv, (uint64_t)g.pool_rows, (uint64_t)p.vs * 2, R, 2);
   if (rc) return rc;
   const size_t smem = sizeof(Smem) + 1024;
   rc = ensure_dynamic_smem((const void*)k_prefix_attn, (int)smem, "prefix_attn_decode");
