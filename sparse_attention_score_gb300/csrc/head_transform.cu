@@ -31,9 +31,13 @@
 //   y_i = r (x_i A_i + partner_i B_i) + C_i,    r = 1 / rms (or deviation),
 // so a head of 128 costs ~45 instructions of a warp whatever the norm and
 // rotation, with the products two at a time (packed fp32).  Heads are loaded
-// four at a time per lane.  A norm or rotation that ends inside 8 elements, a
-// rotated pair on both sides of the norm's end and heads beyond 768 elements
-// take a plain path through shared memory.
+// four at a time per lane.  Where a rotation begins or ends inside 8 elements
+// (or its halves do), each element has a partner of its own and the heads go
+// through shared memory as they were read, for the partners to be picked out
+// of (8192 tokens, 40 heads of 128 rotated in 104: 44 us; in 96, by shuffles,
+// 34).  A norm that ends inside 8 elements, a rotated pair on both sides of
+// the norm's end, heads beyond 768 elements, and beyond 256 with such a
+// rotation, take a plain path (195 us for the same heads).
 //
 // Measured on GB300: 16384 tokens, 64 rotated heads of 64 to bf16 and 64 heads
 // of 128 to E4M3 (671 MB): 118 us, 5.7 TB/s, 84 % of the copy rate; 90 million
@@ -985,9 +989,15 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
   for (int i = 0; i < p.n_jobs; ++i) rows += (long long)N * p.job[i].heads;
   if (rows > 0x7fffffffLL - 63)  // room for the last block's idle warps in 32 bits
     return set_error(DSA_ERR_UNSUPPORTED, "head parts: tokens x heads beyond 2^31 - 64");
-  // Heads per item: as many rounds of the warp as still leave an item for each
-  // of ~32 warps per SM (the sines, cosines and coefficients are the item's),
-  // one where there are few tokens and latency counts.
+  // Heads per item: as many rounds of the warp as still leave 12 items per SM
+  // (the sines, cosines and coefficients are the item's), 32 with 16 rounds and
+  // where all parts are rows of tokens, one round where there are few tokens
+  // and latency counts.  Measured with 12 and with 32 items: 200 tokens of 33 +
+  // 8 heads of 224 6.1 and 10.1 us, 777 tokens of 24 + 4 heads of 80 4.8 and
+  // 6.5; but 2000 tokens of 16 + 32 heads, with 16 rounds, 11.1 and 9.1, and
+  // 8112 rows of K, V and indexer keys 12.7 and 10.7.
+  bool rows_only = true;
+  for (int i = 0; i < p.n_jobs; ++i) rows_only &= p.job[i].by_token != 0;
   long long items = 0;
   for (int rounds = 16; rounds >= 1; rounds /= 2) {
     items = 0;
@@ -1003,10 +1013,12 @@ int head_transform(const LayoutDev* lay, const int32_t* seq, const int32_t* pos,
       } else {
         j.group = rounds * rpw < j.heads ? rounds * rpw : j.heads;
         j.groups = (j.heads + j.group - 1) / j.group;
+        const int even = (j.heads + j.groups - 1) / j.groups;  // no group much shorter
+        j.group = (even + rpw - 1) / rpw * rpw;
         items += (long long)N * j.groups;
       }
     }
-    if (items >= 32LL * sm_count()) break;
+    if (items >= (rounds > 8 || rows_only ? 32LL : 12LL) * sm_count()) break;
   }
   if (N == 0) return DSA_OK;
   p.items = (int)items;
