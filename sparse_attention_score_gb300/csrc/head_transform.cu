@@ -40,8 +40,8 @@
 // rotation, take a plain path (195 us for the same heads).
 //
 // Measured on GB300: 16384 tokens, 64 rotated heads of 64 to bf16 and 64 heads
-// of 128 to E4M3 (671 MB): 118 us, 5.7 TB/s, 84 % of the copy rate; 90 million
-// warp instructions keep 60 % of the issue slots busy.  16384 cache rows of
+// of 128 to E4M3 (671 MB): 118 us, 5.7 TB/s, 84 % of the copy rate; 84 million
+// warp instructions keep 56 % of the issue slots busy.  16384 cache rows of
 // 576 with their indexer keys (44 MB): 21.6 us, where a third of the stalls
 // are for instructions (each warp runs long code for a few rows).  One decode
 // step of 32 tokens: 3 us, the launch.  Tried and left out: inputs requested

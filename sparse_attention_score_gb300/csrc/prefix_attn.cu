@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Two passes over S in TMEM, 32 columns at a time: the maximum while
       // the tensor cores work on O of the previous tile, then the weights
       // straight into P.  (One pass with the thread's 128 scores in
-      // registers took 439 us where this takes 434, and 225 registers.)
+      // registers took 1 % longer, and 225 registers.)
       const uint32_t ta = tbase + lanes + kColS + 128 * (u & 1);
       if (!pair_wait(smem_u32(&sm.vfull[u % kTabs]), (u / kTabs) & 1, &sm.abort)) { ok = false; break; }
       const bool whole = sm.whole[u % kTabs] != 0;
