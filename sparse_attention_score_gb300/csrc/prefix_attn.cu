@@ -619,6 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm.mask[slot][lane] = word;
         }
         const bool whole = __all_sync(0xffffffffu, lane >= kTile / 32 || word == 0xffffffffu);
+        __syncwarp();  // lane 0's arrival releases every lane's word (a vote orders no memory)
         if (lane == 0) {
           sm.whole[slot] = whole;
           mbar_arrive(&sm.vfull[slot]);
