@@ -499,10 +499,15 @@ int dsa_cache_append(const dsa_paged_layout* layout, const int32_t* seq, const i
  * of its cached positions, for a batch that shares a prefix.  Where no more
  * than K positions are eligible the selection keeps every one of them, and
  * this call needs neither scores nor an index list; requests behind one
- * prompt read its pages once for the whole batch.  Same arithmetic as
+ * prompt read its pages once for the whole batch.  The result is that of
  * dsa_sparse_attn_decode with every position selected:
  *     z_p = sm_scale * q[b][h] . K_p,  out[b][h] = sum_p softmax(z)_p V_p,
  *     lse[b][h] = log sum_p exp(z_p),  p < seq_lens[b]
+ * Scores, maxima and sums are fp32.  The weights enter the product with V as
+ * bf16 hi + lo (each off by at most 2^-16 of itself) for a sequence of at most
+ * 512 positions, and rounded once to bf16 (at most 2^-8 of itself) for a longer
+ * one, as dsa_sparse_attn_decode has them for 64 heads of 576/512 (its other
+ * shapes keep fp32 weights).  out is rounded once.
  *  prefix_len  0..max_seq_len: positions [0, prefix_len) hold the same rows
  *              for every sequence with seq_lens[b] >= prefix_len (normally
  *              the same pages; they are read through the block-table row of

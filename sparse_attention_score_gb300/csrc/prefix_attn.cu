@@ -30,7 +30,21 @@
 //   O   [128 x Dv] += P . V      V as stored (MN-major), N = 256 columns per
 //       instruction; CTA r stages half of the columns of all 256 positions.
 // P is rounded to bf16 for the second product (each weight by at most 2^-8 of
-// itself, like the output's own rounding); sums and statistics are fp32.
+// itself, like the output's own rounding), except in short sequences; sums and
+// statistics are fp32.
+//
+// Short sequences.  Over a few positions the roundings of single weights do not
+// average out: with two or three, an output of N(0, 1) rows was off by up to
+// 1.1e-2.  Where a line's rows may have no more than 512 positions (the
+// sequence has, or the prefix), P is therefore kept as bf16 hi + lo, off by
+// 2^-16 of itself, as in the sparse attention.  Such a line's tiles are 128
+// positions: S is [128 x 128] (N = 128, a half of the tile 64 columns), each
+// half writes hi to the first and lo to the second of its two chunks of P, and
+// both are multiplied with the same 64 positions of V.  In a graph, against one
+// bf16 for every line: one sequence of one position 14.2 us, was 12.9; 32 of up
+// to 512 21.9, was 20.7; that a line may be short costs the others 1 to 3 %.
+// (Hi first, and lo once the half had read its scores again, with V staged
+// twice: 32 of up to 512 25.1 us.)
 //
 // Warp roles (256 threads): 0-3 softmax and O out of TMEM; 4 fills the ring of
 // K (and Q, and the usable positions of a tile), 5 issues S; 6 fills the ring
@@ -63,6 +77,8 @@
 // pages of 64, 64 with 32, 72 with 16, 92 with 8 (rows read from shared memory
 // one by one: 56, 87, 126 and 203).
 // Every wait is bounded (DSA_STATUS_TIMEOUT, then the pair winds down).
+#include <algorithm>
+
 #include "device_common.cuh"
 #include "dsa_internal.cuh"
 #include "sm100.cuh"
@@ -85,6 +101,7 @@ constexpr uint32_t kColS = 0;          // two S buffers of 128 columns
 constexpr uint32_t kColO = 256;        // O: 128 columns per 256 dims of V
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kTabs = 8;               // tiles whose mask is kept (see the K producer)
+constexpr int kShort = 512;            // lines of rows with at most this many positions: P as hi + lo
 
 struct __align__(1024) Smem {
   uint8_t ringk[kStagesK][kStageBytes];
@@ -137,7 +154,15 @@ __device__ __forceinline__ int seq_len(const PrefixAttnParams& a, int b) {
   return L < 0 ? 0 : min(L, a.lay.max_len);  // the bound that the host counted with
 }
 
-__device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + kTile - 1) / kTile); }
+// 1 where the rows of a line may have no more than kShort positions: its
+// tiles are half as long, and P is kept as hi + lo.
+__host__ __device__ __forceinline__ int is_short(int n) { return n <= kShort; }
+
+// Tiles of n positions; of half the length in a short line.
+__host__ __device__ __forceinline__ int tiles_of(int n, int brief) {
+  return (int)(((unsigned)n + (kTile >> brief) - 1) >> (8 - brief));
+}
+static_assert(kTile == 256, "tiles_of");
 
 // The split counts in units: kTileUnits for a tile and kLineUnits more ahead of
 // a line's first, for starting and ending it (queries in, first scores, last
@@ -159,7 +184,7 @@ __device__ __forceinline__ int own_start(const Geo& g, int L) {
 
 __device__ __forceinline__ int own_units(const Geo& g, int L) {
   const int own = L >= g.a.prefix ? L - g.a.prefix : L;
-  const int t = min(tiles_of(L - own_start(g, L)), own);  // none where own is 0
+  const int t = min(tiles_of(L - own_start(g, L), is_short(L)), own);  // none where own is 0
   return t > 0 ? kTileUnits * t + kLineUnits : 0;
 }
 
@@ -281,6 +306,7 @@ struct Tiles {
   int trow;          // row of the block table
   int p0, p1;        // positions of the line
   int skip;          // the first of them are the prefix's
+  int brief;         // is_short
   int left;          // units of this pair behind this line
   bool ok;
 
@@ -296,7 +322,7 @@ struct Tiles {
       rows = n < kRows ? n : kRows;
       trow = p.src;
       p0 = skip = 0;
-      p1 = g.a.prefix;
+      p1 = g.a.prefix;  // (its rows have as many positions, or more)
     } else {
       trow = line - p.row_lines;
       row0 = trow * g.a.Hq;
@@ -305,7 +331,8 @@ struct Tiles {
       p0 = own_start(g, p1);
       skip = p1 >= g.a.prefix ? g.a.prefix - p0 : 0;
     }
-    const int T = min(tiles_of(p1 - p0), p1 - p0 - skip);
+    brief = is_short(p1);
+    const int T = min(tiles_of(p1 - p0, brief), p1 - p0 - skip);
     const int n = T > 0 ? kTileUnits * T + kLineUnits - v : 0;
     const int take = n < left ? n : left;
     left -= take;
@@ -323,7 +350,7 @@ struct Tiles {
   __device__ void init(const Geo& g, const Plan& p) {
     line = p.line0;
     left = p.mine;
-    t = t1 = first_t = 0;
+    t = t1 = first_t = brief = 0;
     ok = left > 0 && load(g, p, p.unit0);
     if (!ok) next_line(g, p);
   }
@@ -333,10 +360,10 @@ struct Tiles {
   __device__ __forceinline__ bool first() const { return t == first_t; }
   __device__ __forceinline__ bool last() const { return t + 1 == t1; }
   __device__ __forceinline__ bool pre(const Plan& p) const { return line < p.row_lines; }
-  __device__ __forceinline__ int pos() const { return p0 + t * kTile; }
+  __device__ __forceinline__ int pos() const { return p0 + t * (kTile >> brief); }
   __device__ __forceinline__ int keys() const {
     const int n = p1 - pos();
-    return n < kTile ? n : kTile;
+    return min(n, kTile >> brief);
   }
   // positions of the tile ahead of the line's own (less than a group)
   __device__ __forceinline__ int ahead() const { return t == 0 ? skip : 0; }
@@ -467,10 +494,10 @@ struct Ring {
 };
 
 // Physical row of group i of a tile: `none` (a row outside the pool, which
-// loads as zeros) past the line's end, -1 behind a bad block id.
+// loads as zeros) past the tile's end, -1 behind a bad block id.
 __device__ __forceinline__ int group_row(const Geo& g, const Tiles& t, int i, int lgR) {
+  if ((i << lgR) >= t.keys()) return g.pool_rows;
   const unsigned p = (unsigned)t.pos() + (unsigned)(i << lgR);
-  if (p >= (unsigned)t.p1) return g.pool_rows;
   const unsigned q = g.lgbs >= 0 ? p >> g.lgbs : p / (unsigned)g.a.lay.bs;
   const int page = __ldg(&g.a.lay.bt[(long long)t.trow * g.a.lay.maxb + q]);
   if (page < 0 || page >= g.a.lay.nb) return -1;
@@ -573,9 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t qbar = leader_addr(&sm.qfull), fbar = leader_addr(&sm.fullk[0]);
     const uint32_t ring = smem_u32(sm.ringk[0]);
     const uint32_t empty = smem_u32(&sm.emptyk[0]), full = smem_u32(&sm.fullk[0]);
-    const int nb = 128 >> lgR;  // boxes per stage
     int* tab = sm.tab[0];
-    const int* mytab = tab + rank * nb;
     int ahead = t.ok && lane < per ? group_row(g, t, lane, lgR) : none;  // of the next tile
     while (t.ok) {
       if (t.first()) {  // the line's queries, once the previous line's last S is done
@@ -597,7 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (bad) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
       __syncwarp();
-      const int keys = t.keys(), skip = t.ahead();
+      const int keys = t.keys(), skip = t.ahead(), brief = t.brief;
+      const int nb = 128 >> brief >> lgR;  // boxes per stage
+      const uint32_t bytes = kStageBytes >> brief;
+      const int* mytab = tab + rank * nb;
       {
         // Usable positions.  The slot was tile u - 8's: K of tile u - 5 at
         // the latest has left the ring of 4 stages, so S of it was issued, so
@@ -618,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (no > 0) word &= no >= 32 ? 0u : ~0u << no;
           sm.mask[slot][lane] = word;
         }
-        const bool whole = __all_sync(0xffffffffu, lane >= kTile / 32 || word == 0xffffffffu);
+        const bool whole = __all_sync(0xffffffffu, lane >= kTile / 32 >> brief || word == 0xffffffffu);
         __syncwarp();  // lane 0's arrival releases every lane's word (a vote orders no memory)
         if (lane == 0) {
           sm.whole[slot] = whole;
@@ -632,11 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r1 = uniform(nb < 2 || mytab[1] < 0 ? none : mytab[1]);
       for (int c = 0; c < Cq; ++c) {
         if (!pair_wait(empty + 8 * r.s, r.phase ^ 1, &sm.abort)) { ok = false; break; }
-        if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * kStageBytes);
+        if (rank == 0) expect_tx_elected(full + 8 * r.s, 2 * bytes);
         const uint32_t dst = ring + r.s * kStageBytes, bar = fbar + 8 * r.s;
         if (nb == 2) {
           tma_pair(dst, &maps.k, bar, 64 * c, r0);
-          tma_pair(dst + kStageBytes / 2, &maps.k, bar, 64 * c, r1);
+          tma_pair(dst + R * 128, &maps.k, bar, 64 * c, r1);
         } else {
           uint32_t to = dst;
           for (int i0 = 0; i0 < nb; i0 += 32) {
@@ -672,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* tab = sm.tab[1];
     int ahead = t.ok && lane < per ? group_row(g, t, lane, lgR) : none;
     while (t.ok) {
-      const int keys = t.keys(), skip = t.ahead();
+      const int keys = t.keys(), skip = t.ahead(), brief = t.brief;
       const int nkk = (keys + 63) >> 6;
       // the tile's groups, a lane each (more than 32, in pages of odd sizes, in
       // shared memory), and those that the line begins or ends in
@@ -691,8 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.next(g, plan);
       if (t.ok && lane < per) ahead = group_row(g, t, lane, lgR);
       for (int j = 0; j < 4 && ok; ++j) {
-        const int kk = (j >> 1) | ((j & 1) << 1);  // the O issuer's order
-        if (kk >= nkk) continue;
+        // the O issuer's order; in a short line 0 and 1
+        const int kk = ((j >> 1) | ((j & 1) << 1)) >> brief;
+        if (kk >= nkk || j >= 4 >> brief) continue;
         const int g0 = kk * nb;
         const bool cut = per > 32 || (cuts >> g0 & ((1u << nb) - 1u)) != 0;
         for (int i = 0; i < ninst; ++i) {
@@ -767,7 +796,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       Ring<kStagesK> r;
       int u = 0, nq = 0;
       bool ok = true;
-      const uint32_t id = instr_desc(kRows, 256, 1, 1, 0, 0);
       const uint32_t empty = smem_u32(&sm.emptyk[0]), full = smem_u32(&sm.fullk[0]);
       // descriptors: the address field counts 16 bytes; a step of 16 dims or
       // positions is 32 bytes of a K-major operand, 2048 of V
@@ -784,6 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t d = tbase + kColS + 128 * (u & 1);
+        const uint32_t id = t.brief ? instr_desc(kRows, 128, 1, 1, 0, 0) : instr_desc(kRows, 256, 1, 1, 0, 0);
         uint64_t qa = dq;
         for (int c = 0; c < Cq; ++c, qa += 512) {
           if (!pair_wait(full + 8 * r.s, r.phase, &sm.abort)) { ok = false; break; }
@@ -821,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int o3 = (3 >> lgs) * 16 * g.Rv + (3 & in) * 128;
       while (t.ok && ok) {
         const int nkk = (t.keys() + 63) >> 6;
-        const int add0 = t.first() ? 0 : 1;
+        const int add0 = t.first() ? 0 : 1, brief = t.brief;
         t.next(g, plan);
         // O is rescaled, or read out for the line before
         if (!pair_wait(smem_u32(&sm.oready[u & 1]), (u >> 1) & 1, &sm.abort)) { ok = false; break; }
@@ -831,7 +860,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4 && ok; ++j) {
           const int kk = (j >> 1) | ((j & 1) << 1);  // 0, 2, 1, 3
           if (!pair_wait(smem_u32(&sm.pfull[kk]), u & 1, &sm.abort)) { ok = false; break; }
-          if (kk < nkk) {
+          // a short line: chunk kk and what it leaves, chunk kk + 1, on the same V
+          if (brief && !pair_wait(smem_u32(&sm.pfull[kk | 1]), u & 1, &sm.abort)) { ok = false; break; }
+          if (kk >> brief < nkk && j < 4 >> brief) {
             const uint64_t pa = dp + 512 * kk;
             for (int i = 0; i < ninst; ++i) {
               const int blocks = (i < ninst - 1 || cols % 2 == 0) ? 2 : 1;
@@ -845,6 +876,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_pair(d, pa + 2, vb + (two ? o1 : 128), id, 1);
               mma_pair(d, pa + 4, vb + (two ? o2 : 256), id, 1);
               mma_pair(d, pa + 6, vb + (two ? o3 : 384), id, 1);
+              if (brief) {
+                mma_pair(d, pa + 512, vb, id, 1);
+                mma_pair(d, pa + 514, vb + (two ? o1 : 128), id, 1);
+                mma_pair(d, pa + 516, vb + (two ? o2 : 256), id, 1);
+                mma_pair(d, pa + 518, vb + (two ? o3 : 384), id, 1);
+              }
               commit_pair(empty + 8 * r.s);
               r.step();
             }
@@ -887,10 +924,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ta = tbase + lanes + kColS + 128 * (u & 1);
       if (!pair_wait(smem_u32(&sm.vfull[u % kTabs]), (u / kTabs) & 1, &sm.abort)) { ok = false; break; }
       const bool whole = sm.whole[u % kTabs] != 0;
-      const uint32_t* mask = &sm.mask[u % kTabs][4 * half];
+      const int brief = t.brief, nq = 4 >> brief;  // 32 columns of S at a time
+      const uint32_t* mask = &sm.mask[u % kTabs][nq * half];
       float mt = -INFINITY;
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < nq; ++q) {
         uint32_t z[32];
         tmem_ld_32cols(ta + 32 * q, z);
         tmem_wait_ld();
@@ -940,9 +978,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) arrive_cluster(obar + 8 * (u & 1));
       float ls[2] = {l * f, 0.0f};
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t z[32];
+      // 32 columns of scores, the unusable ones -inf
+      auto scores = [&](int q, uint32_t (&z)[32]) {
         tmem_ld_32cols(ta + 32 * q, z);
         tmem_wait_ld();
         if (!whole) {
@@ -951,37 +988,80 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i)
             if (!((w >> i) & 1u)) z[i] = 0xff800000u;
         }
-        // The previous tile's products have read this chunk of P: the
-        // half's first chunk by its own barrier, the second by the whole
-        // tile's, which every tile waits for here once (a phase of pvdone
-        // left out would make a later wait test the wrong one).
-        if ((q & 1) == 0 && u > 0 &&
-            !pair_wait(q == 0 ? smem_u32(&sm.pdone[half]) : smem_u32(&sm.pvdone), (u - 1) & 1,
-                       &sm.abort)) {
-          ok = false;
-          break;
-        }
-        uint8_t* dst = sm.p[2 * half + (q >> 1)] + row * 128;
+      };
+      if (brief) {
+        // A short line's half has 64 columns: their weights' bf16 part goes to
+        // the half's first chunk of P, what that leaves to the second.
+        if (u > 0 && !pair_wait(smem_u32(&sm.pvdone), (u - 1) & 1, &sm.abort)) { ok = false; break; }
+        uint8_t* dst = sm.p[2 * half] + row * 128;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t z[32];
+          scores(q, z);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // eight weights, 16 bytes of the row's 128-byte line
-          uint32_t pk[4];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e0 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i]), c, -mm));
-            const float e1 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i + 1]), c, -mm));
-            ls[0] += e0;
-            ls[1] += e1;
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
-            pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            for (int i = 0; i < 4; ++i) {
+              const float e0 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i]), c, -mm));
+              const float e1 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i + 1]), c, -mm));
+              ls[0] += e0;
+              ls[1] += e1;
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
+              const float2 h = __bfloat1622float2(h2);
+              const __nv_bfloat162 l2 = __floats2bfloat162_rn(e0 - h.x, e1 - h.y);
+              hi[i] = *reinterpret_cast<const uint32_t*>(&h2);
+              lo[i] = *reinterpret_cast<const uint32_t*>(&l2);
+            }
+            uint8_t* to = dst + (((4 * q + k) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(to + sizeof(sm.p[0])) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          *reinterpret_cast<uint4*>(dst + (((4 * (q & 1) + k) ^ (row & 7)) << 4)) =
-              make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
-        if (q & 1) {  // a chunk is written
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_cluster(pbar + 8 * (q >> 1));
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          arrive_cluster(pbar);
+          arrive_cluster(pbar + 8);
+        }
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t z[32];
+          scores(q, z);
+          // The previous tile's products have read this chunk of P: the
+          // half's first chunk by its own barrier, the second by the whole
+          // tile's, which every tile waits for here once (a phase of pvdone
+          // left out would make a later wait test the wrong one).
+          if ((q & 1) == 0 && u > 0 &&
+              !pair_wait(q == 0 ? smem_u32(&sm.pdone[half]) : smem_u32(&sm.pvdone), (u - 1) & 1,
+                         &sm.abort)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = sm.p[2 * half + (q >> 1)] + row * 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // eight weights, 16 bytes of the row's 128-byte line
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float e0 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i]), c, -mm));
+              const float e1 = ex2_approx(fmaf(__uint_as_float(z[8 * k + 2 * i + 1]), c, -mm));
+              ls[0] += e0;
+              ls[1] += e1;
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+              pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            *reinterpret_cast<uint4*>(dst + (((4 * (q & 1) + k) ^ (row & 7)) << 4)) =
+                make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+          if (q & 1) {  // a chunk is written
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(pbar + 8 * (q >> 1));
+          }
         }
       }
       if (!ok) break;
@@ -1337,7 +1417,7 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   g.slots_pre = w.slots_pre;
   g.row_tiles = w.row_tiles;
   g.Rl = w.Rl;
-  g.prefix_tiles = (p.prefix + kTile - 1) / kTile;
+  g.prefix_tiles = tiles_of(p.prefix, is_short(p.prefix));
   g.pool_rows = (int)((long long)p.lay.nb * p.lay.bs);
   int R = 64;
   while (p.lay.bs % R) R >>= 1;
@@ -1365,9 +1445,12 @@ int launch_prefix_attn(const PrefixAttnParams& p, void* ws, cudaStream_t s) {
   int pairs = max_active_clusters((const void*)k_prefix_attn, kThreads, smem, 2);
   if (pairs < 1) return set_error(DSA_ERR_CUDA, "prefix_attn_decode: no cluster of two CTAs fits");
   if (pairs > kMaxPairs) pairs = kMaxPairs;
+  // most tiles of a sequence's own line: of the longest, or of the longest short one
+  const long long own = std::max(tiles_of(p.lay.max_len, 0),
+                                 tiles_of(std::min(p.lay.max_len, kShort), 1));
   const long long bound =
       (long long)g.row_tiles * (kTileUnits * (long long)g.prefix_tiles + kLineUnits) +
-      (long long)p.lay.batch * (kTileUnits * (p.lay.max_len / kTile + 1LL) + kLineUnits);
+      (long long)p.lay.batch * (kTileUnits * own + kLineUnits);
   if (bound > 0x7fffffffLL)
     return set_error(DSA_ERR_UNSUPPORTED, "prefix_attn_decode: rows x positions beyond 2^30 tiles");
   if (pairs > bound / kTileUnits) pairs = (int)(bound / kTileUnits);
