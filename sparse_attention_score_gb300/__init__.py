@@ -556,9 +556,11 @@ class HeadPart:
     x [N, heads, dim] bf16, any strides with the last dim contiguous (a slice
     of a projection's output).  out: [N, heads, dim] bf16 or FP8 E4M3, strided
     likewise, for head_norm_rope and cache_append(heads=...); a paged pool
-    [num_blocks, block_size, heads * dim or wider] (or [.., heads, dim]),
-    contiguous, for cache_append(cache); FP8 as float8_e4m3fn or as uint8 codes.  norm: "none", "rms" or "layer" over
-    the first norm_dim elements (default: all), weight / bias fp32 [norm_dim].
+    [num_blocks, block_size, heads * dim or wider], its heads packed, or
+    [num_blocks, block_size, heads or more, dim or wider], a head in each slot,
+    contiguous, for cache_append(cache); FP8 as float8_e4m3fn or as uint8 codes.
+    norm: "none", "rms" or "layer" over the first norm_dim elements (default:
+    all), weight / bias fp32 [norm_dim].
     rope_dim > 0 rotates elements [rope_offset, rope_offset + rope_dim) by
     position * inv_freq (fp32 [rope_dim / 2]); interleaved pairs
     (2 i, 2 i + 1), else (i, i + rope_dim / 2).  Shapes and types are checked
@@ -601,7 +603,12 @@ class HeadPart:
             if out.dim() not in (3, 4) or not out.is_contiguous():
                 raise ValueError("out: a contiguous pool [num_blocks, block_size, width] is required")
             ts, hs = out.stride(1), dim
-            if ts < heads * dim:
+            if out.dim() == 4:
+                if out.shape[2] < heads or out.shape[3] < dim:
+                    raise ValueError(f"out: a pool of {out.shape[2]} heads of {out.shape[3]}; "
+                                     f"{heads} of {dim} are needed")
+                hs = out.shape[3]
+            elif ts < heads * dim:
                 raise ValueError(f"out: pool rows of {ts} elements; {heads * dim} are needed")
         else:
             if tuple(out.shape) != (self.N, heads, dim) or out.stride(2) != 1 and dim > 1:
