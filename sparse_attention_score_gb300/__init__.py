@@ -212,6 +212,16 @@ def _rows(layout: "PagedLayout", width: int) -> int:
     return int(layout.num_blocks) * int(layout.block_size) * int(width)
 
 
+def _row_width(layout: "PagedLayout", pool, name: str) -> int:
+    """Elements between the rows of a K or V pool [num_blocks, block_size, width]
+    (or [.., 1, width]).  A pool of several heads is refused: its last dimension
+    is a head, not a row."""
+    if (pool.dim() == 4 and pool.shape[2] != 1 and pool.shape[1] == layout.block_size
+            and pool.shape[0] >= layout.num_blocks):
+        raise ValueError(f"{name}: {pool.shape[2]} heads per row; the call reads rows of one")
+    return pool.shape[-1]
+
+
 _F32, _I32, _BF16, _KEY, _WS = (4,), (4,), (2,), (1, 2), (1,)  # element sizes (bytes)
 
 
@@ -347,7 +357,7 @@ def sparse_attn_decode(layout: PagedLayout, q, k_pool, v_pool, idx, sm_scale, ou
                        stream=None):
     B, Hq, Dqk = q.shape
     Dv, K = out.shape[2], idx.shape[1]
-    ks, vs = k_pool.shape[-1], v_pool.shape[-1]
+    ks, vs = _row_width(layout, k_pool, "k_pool"), _row_width(layout, v_pool, "v_pool")
     a = _Args(layout).add(q, "q", _BF16).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
     a.add(v_pool, "v_pool", _BF16, _rows(layout, vs)).add(idx, "idx", _I32, B * K)
     a.add(out, "out", _BF16, B * Hq * Dv).add(lse, "lse", _F32, B * Hq)
@@ -362,7 +372,7 @@ def sparse_attn_prefill(layout: PagedLayout, q, k_pool, v_pool, idx, sm_scale, o
                         q_seq=None, q_pos=None, stream=None):
     Nq, Hq, Dqk = q.shape
     Dv, K = out.shape[2], idx.shape[1]
-    ks, vs = k_pool.shape[-1], v_pool.shape[-1]
+    ks, vs = _row_width(layout, k_pool, "k_pool"), _row_width(layout, v_pool, "v_pool")
     a = _Args(layout).add(q, "q", _BF16).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
     a.add(v_pool, "v_pool", _BF16, _rows(layout, vs)).add(idx, "idx", _I32, Nq * K)
     a.add(out, "out", _BF16, Nq * Hq * Dv).add(lse, "lse", _F32, Nq * Hq)
@@ -388,7 +398,7 @@ def cache_write(layout: PagedLayout, seq, pos, ws, kv_new=None, kv_pool=None, ki
     """
     N = int(seq.shape[0])
     row_elems = int(kv_new.shape[-1]) if kv_new is not None else 0
-    stride = int(kv_pool.shape[-1]) if kv_pool is not None else 0
+    stride = int(_row_width(layout, kv_pool, "kv_pool")) if kv_pool is not None else 0
     D_i = int(kidx_new.shape[-1]) if kidx_new is not None else 0
     kdt = _elt_dtype(kidx_new) if kidx_new is not None else DSA_BF16
     ke = (kidx_new.element_size(),) if kidx_new is not None else _KEY
@@ -474,7 +484,7 @@ def decode_step(layout: PagedLayout, k_new, k_pool, kidx_new, kidx_pool, q_idx, 
     H_i, D_i = q_idx.shape[1], q_idx.shape[2]
     Dv, K, ld = out.shape[2], int(K), scores.shape[1]
     vp = k_pool if v_pool is None else v_pool
-    ks, vs = k_pool.shape[-1], vp.shape[-1]
+    ks, vs = _row_width(layout, k_pool, "k_pool"), _row_width(layout, vp, "v_pool")
     ke = (q_idx.element_size(),)
     a.add(k_new, "k_new", _BF16, B * Dqk).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
     a.add(v_new, "v_new", _BF16, B * Dv).add(vp, "v_pool", _BF16, _rows(layout, vs))
@@ -501,7 +511,7 @@ def prefill_step(layout: PagedLayout, seq, q_pos, n_eligible, k_new, k_pool, kid
     H_i, D_i = q_idx.shape[1], q_idx.shape[2]
     Dv, K, ld = out.shape[2], int(K), scores.shape[1]
     vp = k_pool if v_pool is None else v_pool
-    ks, vs = k_pool.shape[-1], vp.shape[-1]
+    ks, vs = _row_width(layout, k_pool, "k_pool"), _row_width(layout, vp, "v_pool")
     ke = (q_idx.element_size(),)
     a.add(k_new, "k_new", _BF16, Nq * Dqk).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
     a.add(v_new, "v_new", _BF16, Nq * Dv).add(vp, "v_pool", _BF16, _rows(layout, vs))
@@ -533,7 +543,7 @@ def prefill_step_chunked(layout: PagedLayout, seq, q_pos, n_eligible, k_new, k_p
     H_i, D_i = q_idx.shape[1], q_idx.shape[2]
     Dv, K, ld = out.shape[2], int(K), int(ld)
     vp = k_pool if v_pool is None else v_pool
-    ks, vs = k_pool.shape[-1], vp.shape[-1]
+    ks, vs = _row_width(layout, k_pool, "k_pool"), _row_width(layout, vp, "v_pool")
     ke = (q_idx.element_size(),)
     a.add(k_new, "k_new", _BF16, Nq * Dqk).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
     a.add(v_new, "v_new", _BF16, Nq * Dv).add(vp, "v_pool", _BF16, _rows(layout, vs))
@@ -784,7 +794,7 @@ def prefix_attn_decode(layout: PagedLayout, q, k_pool, v_pool, prefix_len, sm_sc
     Dv = out.shape[2]
     if B != layout.batch:
         raise ValueError(f"q: {B} sequences; the layout has {layout.batch}")
-    ks, vs = k_pool.shape[-1], v_pool.shape[-1]
+    ks, vs = _row_width(layout, k_pool, "k_pool"), _row_width(layout, v_pool, "v_pool")
     rows = layout.num_blocks * layout.block_size
     dev = q.get_device()   # -1: the sizes are checked all the same, then q is refused
     pq = _vec(q, "q", 2, 0, dev)

@@ -33,3 +33,59 @@ def test_a_part_s_rows_and_heads_lie_where_the_pool_s_shape_says(heads, dim, sha
 def test_a_pool_whose_heads_do_not_hold_the_part_s_is_refused(shape):
     with pytest.raises(ValueError, match="pool"):
         dsa.HeadParts([dsa.HeadPart(_x(4, 64), torch.zeros(shape, dtype=BF))]).c(True)
+
+
+# ------------------------------------------------ pools of several heads, read --
+def _layout(nb=4, bs=64):
+    bt = torch.arange(nb, dtype=torch.int32).reshape(2, nb // 2)
+    return dsa.PagedLayout(bt, torch.full((2,), 100, dtype=torch.int32), bs, nb, 128)
+
+
+def _z(*shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def _attention_calls(k, v):
+    """Every call that reads K and V pools, on host tensors."""
+    lay, ws = _layout(), _z(4096, dtype=torch.uint8)
+    q, out, lse = _z(2, 4, 64), _z(2, 4, 64), _z(2, 4, dtype=torch.float32)
+    idx, one = _z(2, 8, dtype=torch.int32), _z(2, dtype=torch.int32)
+    qi, w, kidx = _z(2, 4, 64), _z(2, 4, dtype=torch.float32), _z(4, 64, 64)
+    new = _z(2, 64)
+    sc = _z(2, 128, dtype=torch.float32)
+    step = (new, k, new, kidx, qi, w, q, 8, 0.1)
+    return {
+        "prefix_attn_decode": lambda: dsa.prefix_attn_decode(lay, q, k, v, 0, 0.1, out, lse, ws),
+        "sparse_attn_decode": lambda: dsa.sparse_attn_decode(lay, q, k, v, idx, 0.1, out, lse, ws),
+        "sparse_attn_prefill": lambda: dsa.sparse_attn_prefill(lay, q, k, v, idx, 0.1, out, lse, ws,
+                                                               q_seq=one, q_pos=one),
+        "decode_step": lambda: dsa.decode_step(lay, *step, sc, idx, out, lse, ws, v_new=new, v_pool=v),
+        "prefill_step": lambda: dsa.prefill_step(lay, 0, one, one, *step, sc, idx, out, lse, ws,
+                                                 v_new=new, v_pool=v),
+        "prefill_step_chunked": lambda: dsa.prefill_step_chunked(lay, 0, one, one, *step, 128, idx, out,
+                                                                 lse, ws, v_new=new, v_pool=v),
+        "cache_write": lambda: dsa.cache_write(lay, one, one, ws, kv_new=new, kv_pool=k),
+    }
+
+
+CALLS = list(_attention_calls(None, None))
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_pool_of_several_heads_is_not_read_as_rows_of_one(call):
+    """The calls read one row of a position per pool; the last dimension of
+    [num_blocks, block_size, heads, dim] is a head, not a row."""
+    one, four = _z(4, 64, 64), _z(4, 64, 4, 64)
+    with pytest.raises(ValueError, match="heads"):
+        _attention_calls(four, one)[call]()
+    if call != "cache_write":
+        with pytest.raises(ValueError, match="heads"):
+            _attention_calls(one, four)[call]()
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_pools_of_one_head_are_taken_with_and_without_the_dimension(call):
+    """... up to the check that host tensors stop at."""
+    for k in (_z(4, 64, 64), _z(4, 64, 1, 64), _z(256, 64)):
+        with pytest.raises(ValueError, match="CUDA"):
+            _attention_calls(k, k)[call]()
