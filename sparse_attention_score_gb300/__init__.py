@@ -24,6 +24,7 @@ raises if ``libdsa.so`` has not been built, and every call raises
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -612,7 +613,7 @@ class HeadPart:
         if paged:
             if out.dim() not in (3, 4) or not out.is_contiguous():
                 raise ValueError("out: a contiguous pool [num_blocks, block_size, width] is required")
-            ts, hs = out.stride(1), dim
+            ts, hs = self.row(), dim
             if out.dim() == 4:
                 if out.shape[2] < heads or out.shape[3] < dim:
                     raise ValueError(f"out: a pool of {out.shape[2]} heads of {out.shape[3]}; "
@@ -634,6 +635,11 @@ class HeadPart:
                          _elt_dtype(out), heads, dim, norm, norm_dim, eps, opt(self.weight),
                          opt(self.bias), roff, rdim, inter, 0, opt(self.inv_freq))
 
+    def row(self) -> int:
+        """Elements of a row of `out` as a pool (from its shape: a page of one
+        row may carry any stride)."""
+        return math.prod(self.out.shape[2:])
+
     def tensors(self):
         return [(t, n) for t, n in ((self.x, "x"), (self.out, "out"), (self.weight, "weight"),
                                     (self.bias, "bias"), (self.inv_freq, "inv_freq"))
@@ -654,7 +660,7 @@ class HeadParts:
         self.rotates = any(p._spec[6] for p in self.parts)
         self.n = len(self.parts)
         # rows of the smallest pool, for parts that go to paged pools
-        self.pool_rows = min((p.out.numel() // max(1, p.out.stride(1)) if p.out.dim() >= 3 else 0)
+        self.pool_rows = min(p.out.numel() // max(1, p.row()) if p.out.dim() >= 3 else 0
                              for p in self.parts)
         self._arrays = {}
         self._device = None

@@ -89,3 +89,17 @@ def test_pools_of_one_head_are_taken_with_and_without_the_dimension(call):
     for k in (_z(4, 64, 64), _z(4, 64, 1, 64), _z(256, 64)):
         with pytest.raises(ValueError, match="CUDA"):
             _attention_calls(k, k)[call]()
+
+
+# ------------------------------------------------------------- pages of one row --
+@pytest.mark.parametrize("make", [
+    lambda: _z(1, 8, 256).transpose(0, 1),                       # strides (256, 2048, 1)
+    lambda: _z(8, 256).as_strided((8, 1, 256), (256, 8, 1)),     # (256, 8, 1)
+    lambda: _z(1, 8, 4, 64).transpose(0, 1),
+], ids=["transposed", "as-strided", "with-heads"])
+def test_pages_of_one_row_may_carry_any_stride(make):
+    pool = make()
+    assert pool.shape[:2] == (8, 1) and pool.is_contiguous()
+    parts = dsa.HeadParts([dsa.HeadPart(_x(4, 64), pool)])
+    c = parts.c(True)[0]
+    assert (c.out_token_stride, c.out_head_stride, parts.pool_rows) == (256, 64, 8)
