@@ -713,13 +713,13 @@ def _here(device: int, stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-def _vec(t, name: str, elt: int, numel: int, device: int):
-    """Address of a contiguous operand on `device`, checked as _Args does."""
+def _vec(t, name: str, dtype, numel: int, device: int):
+    """Address of a contiguous operand on `device`, checked as _Args does, and
+    its type (another type of the same size would be read as `dtype`)."""
     if t is None:
         return None
-    if t.element_size() != elt:
-        raise TypeError(f"{name}: {t.dtype} has {t.element_size()}-byte elements; "
-                        f"the call needs {elt}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}; {dtype} is required")
     if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements; the call needs at least {numel}")
     if t.get_device() != device:
@@ -740,9 +740,9 @@ def head_norm_rope(parts, pos=None, stream=None):
     dev = parts._device
     if dev is None:
         if pos is not None and not pos.is_cuda:   # sizes first, then residency, as everywhere
-            _vec(pos, "pos", 4, parts.N, -1)
+            _vec(pos, "pos", torch.int32, parts.N, -1)
         dev = parts.device()
-    rc = _lib.dsa_head_norm_rope(arr, parts.n, _vec(pos, "pos", 4, parts.N, dev), parts.N,
+    rc = _lib.dsa_head_norm_rope(arr, parts.n, _vec(pos, "pos", torch.int32, parts.N, dev), parts.N,
                                  _here(dev, stream))
     if rc:
         raise DsaError(rc, "dsa_head_norm_rope")
@@ -772,16 +772,17 @@ def cache_append(layout: PagedLayout, seq, pos, cache, ws, heads=None, stream=No
         harr, nh = heads.c(False), heads.n
     dev = cache._device
     if dev is None:
-        for t, name, elt, numel in ((seq, "seq", 4, N), (pos, "pos", 4, N), (ws, "ws", 1, 0)):
+        for t, name, dtype, numel in ((seq, "seq", torch.int32, N), (pos, "pos", torch.int32, N),
+                                      (ws, "ws", torch.uint8, 0)):
             if t is not None and not t.is_cuda:   # sizes first, then residency, as everywhere
-                _vec(t, name, elt, numel, -1)
+                _vec(t, name, dtype, numel, -1)
         dev = cache.device()
     if nh and heads.device() != dev:
         raise ValueError("heads: on another device than the cache parts")
     if layout.block_table.get_device() != dev or layout.seq_lens.get_device() != dev:
         raise ValueError(f"layout: block_table and seq_lens must be CUDA tensors on cuda:{dev}")
-    rc = _lib.dsa_cache_append(layout.c(), _vec(seq, "seq", 4, N, dev), _vec(pos, "pos", 4, N, dev),
-                               N, arr, cache.n, harr, nh, _vec(ws, "ws", 1, 0, dev), ws.numel(),
+    rc = _lib.dsa_cache_append(layout.c(), _vec(seq, "seq", torch.int32, N, dev), _vec(pos, "pos", torch.int32, N, dev),
+                               N, arr, cache.n, harr, nh, _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(),
                                _here(dev, stream))
     if rc:
         raise DsaError(rc, "dsa_cache_append")
@@ -803,12 +804,12 @@ def prefix_attn_decode(layout: PagedLayout, q, k_pool, v_pool, prefix_len, sm_sc
     ks, vs = _row_width(layout, k_pool, "k_pool"), _row_width(layout, v_pool, "v_pool")
     rows = layout.num_blocks * layout.block_size
     dev = q.get_device()   # -1: the sizes are checked all the same, then q is refused
-    pq = _vec(q, "q", 2, 0, dev)
-    pk = _vec(k_pool, "k_pool", 2, rows * ks, dev)
-    pv = pk if v_pool is k_pool else _vec(v_pool, "v_pool", 2, rows * vs, dev)
-    po = _vec(out, "out", 2, B * Hq * Dv, dev)
-    pl = _vec(lse, "lse", 4, B * Hq, dev)
-    pws = _vec(ws, "ws", 1, 0, dev)
+    pq = _vec(q, "q", torch.bfloat16, 0, dev)
+    pk = _vec(k_pool, "k_pool", torch.bfloat16, rows * ks, dev)
+    pv = pk if v_pool is k_pool else _vec(v_pool, "v_pool", torch.bfloat16, rows * vs, dev)
+    po = _vec(out, "out", torch.bfloat16, B * Hq * Dv, dev)
+    pl = _vec(lse, "lse", torch.float32, B * Hq, dev)
+    pws = _vec(ws, "ws", torch.uint8, 0, dev)
     if dev < 0:
         raise ValueError("q: a CUDA tensor is required")
     if layout.block_table.get_device() != dev or layout.seq_lens.get_device() != dev:

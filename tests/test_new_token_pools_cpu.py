@@ -103,3 +103,28 @@ def test_pages_of_one_row_may_carry_any_stride(make):
     parts = dsa.HeadParts([dsa.HeadPart(_x(4, 64), pool)])
     c = parts.c(True)[0]
     assert (c.out_token_stride, c.out_head_stride, parts.pool_rows) == (256, 64, 8)
+
+
+# ---------------------------------------------------------------- operand types --
+@pytest.mark.parametrize("name,dtype", [("q", torch.float16), ("q", torch.int16), ("k_pool", torch.float16),
+                                        ("v_pool", torch.float16), ("out", torch.float16),
+                                        ("lse", torch.int32), ("ws", torch.float32)])
+def test_the_attention_refuses_operands_of_another_type_of_the_same_size(name, dtype):
+    a = dict(q=_z(2, 4, 64), k_pool=_z(4, 64, 64), v_pool=_z(4, 64, 64), out=_z(2, 4, 64),
+             lse=_z(2, 4, dtype=torch.float32), ws=_z(4096, dtype=torch.uint8))
+    a[name] = a[name].to(dtype)
+    with pytest.raises(TypeError, match=name):
+        dsa.prefix_attn_decode(_layout(), a["q"], a["k_pool"], a["v_pool"], 0, 0.1, a["out"], a["lse"],
+                               a["ws"])
+
+
+@pytest.mark.parametrize("name", ["seq", "pos"])
+def test_the_appends_refuse_positions_that_are_not_int32(name):
+    a = dict(seq=_z(3, dtype=torch.int32), pos=_z(3, dtype=torch.int32))
+    a[name] = a[name].float()
+    with pytest.raises(TypeError, match=name):
+        dsa.cache_append(_layout(), a["seq"], a["pos"], [dsa.HeadPart(_x(1, 64), _z(4, 64, 64))],
+                         _z(4096, dtype=torch.uint8))
+    if name == "pos":
+        with pytest.raises(TypeError, match=name):
+            dsa.head_norm_rope([dsa.HeadPart(_x(1, 64), _x(1, 64))], a["pos"])
