@@ -546,6 +546,11 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
  *   DSA_STATUS_TIMEOUT is OR-ed into the status word of ws (>= 256 bytes);
  *   expire == 0: the barrier completes first and nothing is recorded.  For
  *   testing the give-up path without a hang; the context stays usable.
+ * dsa_selftest_warp_wait: the same for the whole-warp wait of
+ *   dsa_prefix_attn_decode.  mode 0: the barrier completes first; 1: nothing
+ *   arrives; 2: nothing arrives and another warp raises the kernel's abort flag
+ *   after 5 ms, which ends the wait before its limit.  Modes 1 and 2 set
+ *   DSA_STATUS_TIMEOUT.
  */
 int dsa_get_status(void* ws, dsa_stream_t stream, int32_t* status, int clear);
 const char* dsa_last_error_string(void);
@@ -553,6 +558,8 @@ uint64_t dsa_launch_count(void);
 int dsa_version(void);
 int dsa_selftest_bounded_wait(int expire, uint64_t limit_ns, void* ws, size_t ws_bytes,
                               dsa_stream_t stream);
+int dsa_selftest_warp_wait(int mode, uint64_t limit_ns, void* ws, size_t ws_bytes,
+                           dsa_stream_t stream);
 
 #ifdef __cplusplus
 }

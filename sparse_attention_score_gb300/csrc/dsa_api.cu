@@ -443,6 +443,18 @@ int dsa_selftest_bounded_wait(int expire, uint64_t limit_ns, void* ws, size_t ws
                                reinterpret_cast<int*>(ws), reinterpret_cast<cudaStream_t>(stream));
 }
 
+int dsa_selftest_warp_wait(int mode, uint64_t limit_ns, void* ws, size_t ws_bytes,
+                           dsa_stream_t stream) {
+  if (mode < 0 || mode > 2)
+    return set_error(DSA_ERR_INVALID, "selftest_warp_wait: mode must be 0, 1 or 2");
+  if (limit_ns < 1000 || limit_ns > 1000000000ull)
+    return set_error(DSA_ERR_INVALID, "selftest_warp_wait: limit_ns must be in [1 us, 1 s]");
+  int rc = check_ws(ws, ws_bytes, kWsHeader);
+  if (rc) return rc;
+  return warp_wait_selftest(mode, (unsigned long long)limit_ns, reinterpret_cast<int*>(ws),
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
 // ---------------------------------------------------------------- steps --
 // A step workspace: the step's status header, then one region per stage
 // (each region 256-byte aligned and laid out as that stage's own workspace).

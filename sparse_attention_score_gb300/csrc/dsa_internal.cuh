@@ -120,6 +120,7 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 
 // selftest.cu
 int bounded_wait_selftest(int expire, unsigned long long limit_ns, int* status, cudaStream_t s);
+int warp_wait_selftest(int mode, unsigned long long limit_ns, int* status, cudaStream_t s);
 
 // cache_write.cu
 int cache_write(const LayoutDev& lay, const int32_t* seq, const int32_t* pos, int N,

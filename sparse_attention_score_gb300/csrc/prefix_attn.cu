@@ -387,34 +387,6 @@ __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
                : "memory");
 }
 
-// mbar_wait of a whole warp on a barrier that the pair's other CTA may arrive
-// on.  (Default semantics: what crosses CTAs is ordered by the async proxy's
-// own completion, or was made visible to it by its writer's proxy fence.  With
-// .acquire.cluster and .release.cluster the softmax spent 1,100 cycles more
-// per tile.)
-__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          uint64_t limit_ns = 2000000000ull) {
-  auto done = [&] {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return __all_sync(0xffffffffu, ok != 0) != 0;
-  };
-  if (done()) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (done()) return true;
-    if ((it & 63u) == 0) {
-      if (__any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > limit_ns)) return false;
-    }
-  }
-}
-
 // The issuing roles run as whole warps on warp-uniform values and one elected
 // lane (always the same) issues: descriptors and coordinates then stay in
 // uniform registers.  Issued from a single-lane branch each MMA cost ~140

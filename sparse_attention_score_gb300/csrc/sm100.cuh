@@ -80,6 +80,34 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// mbar_wait of a whole warp (bar: the barrier's shared address), on a barrier
+// that the other CTA of a pair may arrive on.  (Default semantics: what crosses
+// CTAs is ordered by the async proxy's own completion, or was made visible to it
+// by its writer's proxy fence.  With .acquire.cluster and .release.cluster the
+// softmax of the prefix attention spent 1,100 cycles more per tile.)
+__device__ __forceinline__ bool pair_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns = 2000000000ull) {
+  auto done = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, ok != 0) != 0;
+  };
+  if (done()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (done()) return true;
+    if ((it & 63u) == 0) {
+      if (__any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > limit_ns)) return false;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ TMA --
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int x, int y) {
