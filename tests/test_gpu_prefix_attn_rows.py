@@ -9,6 +9,7 @@ from heads_reference import assert_attn_close, attend64
 from test_gpu_prefix_attn import LATENT, Problem
 
 pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
 
 
 def _again(dsa, p):
@@ -95,3 +96,95 @@ def test_short_sequences_of_other_shapes(shape):
     for _ in range(20):
         _again(dsa, p)
         assert torch.equal(p.out, first)
+
+
+# --------------------------------------------------------- positions that decide --
+class Planted(Problem):
+    """A problem in which chosen positions decide one head each: K there is that
+    head's query scaled to a score of 24, e^24 against at most 8191 others of
+    N(0, 1) (their sum ~ e^9.5), so that the head's output is the position's
+    row of V."""
+
+    def __init__(self, seed, lens, **kw):
+        super().__init__(seed, lens, **kw)
+        self.plants = []
+
+    def plant(self, b, h, pos, table=None):
+        t = b if table is None else table
+        page, r = int(self.bt[t, pos // self.bs]), pos % self.bs
+        q = self.q[b, h].float()
+        self.kp[page, r, :self.Dqk] = (q * (24.0 / (self.scale * float(q @ q)))).to(BF)
+        self.plants.append((b, h, page, r))
+
+    def check_plants(self, what):
+        """The weight of the row is 1 to 1e-4 (fp32), rounded to bf16 at most
+        once, and so is the output: 2^-7 of the value, and 1e-3 for the others
+        (1e-4 times values of up to 6).  A position counted twice would move
+        the lse, which check() holds, by log 2."""
+        self.check(what)
+        for b, h, page, r in self.plants:
+            v = self.vp[page, r, :self.Dv].double()
+            err = (self.out[b, h].double() - v).abs()
+            assert bool((err <= 2.0 ** -7 * v.abs() + 1e-3).all()), (what, b, h, page, r)
+
+
+def edges(p0, p1, step):
+    """First and last positions of the tiles and of the chunks of 64 of a line
+    over [p0, p1), the line's ends first."""
+    at = [p1 - 1, p0]
+    for a in range(p0 - p0 % step, p1, step):
+        at += [a, a + step - 1]
+    for a in range(p0 - p0 % 64, p1, 64):
+        at += [a, a + 63]
+    return list(dict.fromkeys(p for p in at if p0 <= p < p1))
+
+
+PLANTED = [dict(Hq=64, Dqk=576, Dv=512, latent=True), dict(Hq=128, Dqk=128, Dv=64, latent=False)]
+
+
+@pytest.mark.parametrize("shape", PLANTED, ids=["latent", "gqa"])
+@pytest.mark.parametrize("bs", [16, 64])
+def test_every_edge_of_a_long_line_counts_once(bs, shape):
+    need_gpu()
+    dsa = lib()
+    lens = [5000, 8191, 8191, 8191, 4096, 300, 512, 513, 1]
+    p = Planted(bs, lens, bs=bs, prefix=0, **shape)
+    done = {}
+    for b, n in enumerate(lens):
+        at = edges(0, n, 128 if n <= SHORT else 256)
+        first = done.get(n, 0)                           # equal lengths share the edges out
+        for h, pos in enumerate(at[first:first + p.Hq]):
+            p.plant(b, h, pos)
+        done[n] = first + p.Hq
+    p.run(dsa).check_plants(f"pages of {bs}")
+    assert dsa.get_status(p.ws) == 0
+
+
+@pytest.mark.parametrize("shape", PLANTED, ids=["latent", "gqa"])
+@pytest.mark.parametrize("bs,prefix", [(64, 4100), (16, 4096), (48, 5001), (64, 300)])
+def test_every_edge_of_a_prefix_and_behind_it_counts_once(bs, prefix, shape):
+    need_gpu()
+    dsa = lib()
+    lens = [prefix + k for k in (0, 1, 300, 2100)] + [prefix + 511, prefix + 512, prefix - 1, prefix + 64]
+    p = Planted(prefix + bs, lens, bs=bs, prefix=prefix, **shape)
+    shared = edges(0, prefix, 128 if prefix <= SHORT else 256)
+    box = next(r for r in (64, 32, 16, 8) if bs % r == 0)
+    start = prefix - prefix % box                        # where the sequences' own tiles begin
+    nth = 0
+    for b, n in enumerate(lens):
+        h = 0
+        if n >= prefix:                                  # half of its heads to its own positions
+            step = 128 if n <= SHORT else 256
+            own = [n - 1, prefix] + [a + d for a in range(start, n, step) for d in (0, step - 1)]
+            for pos in list(dict.fromkeys(x for x in own if prefix <= x < n))[:p.Hq // 2]:
+                p.plant(b, h, pos)
+                h += 1
+            for pos in shared[nth:nth + p.Hq - h]:       # the others to the prefix's edges
+                p.plant(b, h, pos, table=0)              # sequence 0 has all of it
+                h += 1
+                nth += 1
+        else:
+            for h, pos in enumerate(edges(0, n, 256)[:p.Hq]):
+                p.plant(b, h, pos)
+    p.run(dsa).check_plants(f"prefix {prefix}")
+    assert dsa.get_status(p.ws) == 0
