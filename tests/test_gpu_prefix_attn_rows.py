@@ -188,3 +188,19 @@ def test_every_edge_of_a_prefix_and_behind_it_counts_once(bs, prefix, shape):
                 p.plant(b, h, pos)
     p.run(dsa).check_plants(f"prefix {prefix}")
     assert dsa.get_status(p.ws) == 0
+
+
+@pytest.mark.parametrize("Hq", [65, 72, 127])
+def test_lines_with_few_rows_in_the_second_cta_stay_in_step(Hq):
+    """Heads beyond 64 lie in the pair's second CTA: one row, a handful, all but
+    one.  Many runs of one problem, all equal bit for bit."""
+    need_gpu()
+    dsa = lib()
+    g = np.random.default_rng(Hq)
+    p = Problem(Hq, [int(n) for n in g.integers(1, 2049, 40)], bs=64, prefix=0, Hq=Hq, Dqk=576, Dv=512,
+                latent=True).run(dsa)
+    p.check("first run")
+    first = p.out.clone()
+    for _ in range(100):
+        _again(dsa, p)
+        assert torch.equal(p.out, first)
