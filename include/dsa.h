@@ -433,6 +433,12 @@ int dsa_index_bounded_stats(void* ws, dsa_stream_t stream, uint64_t* tiles_skipp
  * aligned, an FP8 out 8-byte; weight and bias 16-byte aligned; rope_offset
  * and rope_dim even.  out may be in itself (bf16, same strides); apart from
  * that no part's out may overlap any part's in or out.
+ *
+ * All parts of a launch take one code path, the slowest that one of them needs:
+ * a norm_dim, or a rotated range or half of one, that is no multiple of 8; a dim
+ * beyond 768; dims beyond 256 beside such a rotation; a pair with only one
+ * element inside the norm.  Such a part costs the others up to six times their
+ * time, and is better given a call of its own where speed counts.
  */
 #define DSA_NORM_NONE 0
 #define DSA_NORM_RMS 1
@@ -519,6 +525,9 @@ int dsa_cache_append(const dsa_paged_layout* layout, const int32_t* seq, const i
  *  out         [B][Hq][Dv] bf16 (0 for an empty sequence)
  *  lse         [B][Hq] fp32, or NULL (-inf for an empty sequence)
  *  ws          dsa_prefix_attn_decode_workspace_size() bytes
+ * A call has one key head.  Rows of several (as dsa_cache_append stores them)
+ * take a call per key head: k_pool and v_pool at that head's first element of
+ * row 0, the strides those of the whole rows, q and out of its query heads.
  * Errors: DSA_ERR_INVALID / DSA_ERR_UNSUPPORTED as for
  * dsa_sparse_attn_decode, for prefix_len out of range, and for more than 2^30
  * tiles of 128 rows x 256 positions.  Device: a position behind a bad block id

@@ -797,7 +797,10 @@ def prefix_attn_decode(layout: PagedLayout, q, k_pool, v_pool, prefix_len, sm_sc
                        stream=None):
     """Exact attention of one query per sequence over all its cached positions;
     the first prefix_len, shared by the batch, are read once (include/dsa.h,
-    dsa_prefix_attn_decode).  prefix_len 0: dense decode attention."""
+    dsa_prefix_attn_decode).  prefix_len 0: dense decode attention.  q, out and
+    the pools bfloat16, lse float32 or None.  One key head per pool row (the
+    first Dqk and Dv elements of it): pools of several key heads take the C call
+    once per head, at the head's offset."""
     B, Hq, Dqk = q.shape
     Dv = out.shape[2]
     if B != layout.batch:
