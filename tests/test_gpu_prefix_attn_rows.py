@@ -204,3 +204,24 @@ def test_lines_with_few_rows_in_the_second_cta_stay_in_step(Hq):
     for _ in range(100):
         _again(dsa, p)
         assert torch.equal(p.out, first)
+
+
+def test_both_attention_calls_meet_the_same_bar_on_short_sequences():
+    """Every position selected: the sparse call and this one, each within the
+    common bar of the exact values."""
+    need_gpu()
+    dsa = lib()
+    lens = [2, 3, 1, 17, 200, 511, 512, 700] + [2, 3] * 8
+    p = Problem(80, lens, bs=64, prefix=0, **LATENT).run(dsa)
+    check_short(p, "prefix attention")
+    B, K = len(lens), 768
+    idx = torch.full((B, K), -1, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        idx[b, :n] = torch.arange(n, dtype=torch.int32)
+    out, lse = torch.empty_like(p.out), torch.empty_like(p.lse)
+    ws = dsa.workspace(dsa.sparse_attn_decode_workspace_size(B, 64, 576, 512, K))
+    dsa.sparse_attn_decode(p.lay, p.q, p.kp, p.vp, idx.cuda(), p.scale, out, lse, ws)
+    w, l, _ = attend64(p.q, p.kp, p.vp, p.bt, p.lens, p.bs, p.nb, 0, p.scale, p.Dv)
+    assert_out_close(out, lse, w.numpy(), l.numpy(), "sparse attention, all selected")
+    assert_out_close(p.out, p.lse, w.numpy(), l.numpy(), "prefix attention")
+    assert dsa.get_status(ws) == 0 and dsa.get_status(p.ws) == 0
