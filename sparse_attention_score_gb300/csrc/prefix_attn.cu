@@ -58,11 +58,11 @@
 // cycles of the tensor cores for 71 MFLOP.  Per CTA it also takes 278 KB from
 // L2 through 112 KB of rings: a stage comes round in ~1,450 cycles (copy 840,
 // MMAs 256, barriers and issue the rest), which allows ~77 bytes a cycle and
-// needs 64.  Measured on GB300: ~5,700 cycles per tile; 64 sequences of 64
-// heads behind a prefix of 65,536: 346 us, 1,690 TFLOP/s (88 % of the cuBLAS
-// rate); 32 sequences behind 16,384: 64 us, 1,210 TFLOP/s.  Short lines are
-// bound by the chain from the lengths to the output (one tile: 11.4 us, of it
-// 3 until the first copy of K is issued, 1 to write O and 3 for the join).
+// needs 64.  Measured on GB300 (in a graph, warm): ~5,800 cycles per tile; 64
+// sequences of 64 heads behind a prefix of 65,536: 350 us, 1,670 TFLOP/s (87 %
+// of the cuBLAS rate); 32 behind 16,384: 66 us, 1,170 TFLOP/s.  Short lines are
+// bound by the chain from the lengths to the output (a tile a pair: 10.5 us,
+// 3 of them until the first copy of K is issued, 1 to write O, 3 for the join).
 //
 // Boxes are R rows high, R the largest power of two (at most 64) that divides
 // the page size: such a group of positions never crosses a page.  A sequence's
@@ -73,7 +73,7 @@
 // included) never meets a weight of 0.  Pages below 64 rows take more boxes, and
 // what a box costs is its issue: rows come out of a lane's register by shuffle,
 // loops are short, and 16 or 32 rows of V take both 64-column blocks in one box.
-// 32 sequences behind 16,384 positions, own parts of up to 512: 56 us with
+// 32 sequences behind 16,384 positions, own parts of up to 512: 58 us with
 // pages of 64, 64 with 32, 72 with 16, 92 with 8 (rows read from shared memory
 // one by one: 56, 87, 126 and 203).
 // Every wait is bounded (DSA_STATUS_TIMEOUT, then the pair winds down).
