@@ -209,13 +209,16 @@ class _Args:
         return [_ptr(t) for t, _ in self._t]
 
 
-def _rows(layout: "PagedLayout", width: int) -> int:
-    """Elements of a paged pool of `width`-element rows."""
+def _rows(layout: "PagedLayout", width: int, kidx_pool=None) -> int:
+    """Elements of a paged pool of `width`-element rows (kidx_pool: the pool, to be
+    of one head)."""
+    if kidx_pool is not None:
+        _row_width(layout, kidx_pool, "kidx_pool")
     return int(layout.num_blocks) * int(layout.block_size) * int(width)
 
 
 def _row_width(layout: "PagedLayout", pool, name: str) -> int:
-    """Elements between the rows of a K or V pool [num_blocks, block_size, width]
+    """Elements between the rows of a pool [num_blocks, block_size, width]
     (or [.., 1, width]).  A pool of several heads is refused: its last dimension
     is a head, not a row."""
     if (pool.dim() == 4 and pool.shape[2] != 1 and pool.shape[1] == layout.block_size
@@ -303,7 +306,7 @@ def index_score(layout: PagedLayout, q_idx, w, kidx_pool, scores, ws, q_seq=None
     Nq, H_i, D_i = q_idx.shape
     ld = scores.shape[1]
     a = _Args(layout).add(q_idx, "q_idx", _KEY).add(w, "w", _F32, Nq * H_i)
-    a.add(kidx_pool, "kidx_pool", (q_idx.element_size(),), _rows(layout, D_i))
+    a.add(kidx_pool, "kidx_pool", (q_idx.element_size(),), _rows(layout, D_i, kidx_pool))
     a.add(q_seq, "q_seq", _I32, Nq).add(q_pos, "q_pos", _I32, Nq)
     a.add(scores, "scores", _F32, Nq * ld).add(ws, "ws", _WS)
     pq, pw, pk, pseq, ppos, ps, pws = a.ptrs()
@@ -318,7 +321,7 @@ def index_score_prefill(layout: PagedLayout, seq, q_idx, w, kidx_pool, scores, w
     Nq, H_i, D_i = q_idx.shape
     ld = scores.shape[1]
     a = _Args(layout).add(q_idx, "q_idx", _KEY).add(w, "w", _F32, Nq * H_i)
-    a.add(kidx_pool, "kidx_pool", (q_idx.element_size(),), _rows(layout, D_i))
+    a.add(kidx_pool, "kidx_pool", (q_idx.element_size(),), _rows(layout, D_i, kidx_pool))
     a.add(q_pos, "q_pos", _I32, Nq).add(scores, "scores", _F32, Nq * ld).add(ws, "ws", _WS)
     pq, pw, pk, ppos, ps, pws = a.ptrs()
     rc = _lib.dsa_index_score_prefill(layout.c(), int(seq), pq, pw, pk, _elt_dtype(kidx_pool), H_i,
@@ -408,7 +411,8 @@ def cache_write(layout: PagedLayout, seq, pos, ws, kv_new=None, kv_pool=None, ki
     a.add(kv_new, "kv_new", _BF16, N * row_elems)
     a.add(kv_pool, "kv_pool", _BF16, _rows(layout, stride) if kv_new is not None else None)
     a.add(kidx_new, "kidx_new", _KEY, N * D_i)
-    a.add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i) if kidx_new is not None else None)
+    a.add(kidx_pool, "kidx_pool", ke,
+          _rows(layout, D_i, kidx_pool) if kidx_new is not None else None)
     a.add(ws, "ws", _WS)
     pseq, ppos, pkv, pkp, pin, pip, pws = a.ptrs()
     rc = _lib.dsa_cache_write(layout.c(), pseq, ppos, N, pkv, row_elems, pkp, stride, pin, D_i, kdt,
@@ -429,7 +433,7 @@ def index_bounds_update(layout: PagedLayout, kidx_pool, kbound_pool, ws, seq=Non
     N = int(seq.shape[0]) if seq is not None else 0
     ke = (kidx_pool.element_size(),)
     a = _Args(layout).add(seq, "seq", _I32, N).add(pos, "pos", _I32, N)
-    a.add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i))
+    a.add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i, kidx_pool))
     a.add(kbound_pool, "kbound_pool", ke, layout.num_blocks * 2 * D_i).add(ws, "ws", _WS)
     pseq, ppos, pk, pb, pws = a.ptrs()
     rc = _lib.dsa_index_bounds_update(layout.c(), pseq, ppos, N, pk, D_i, _elt_dtype(kidx_pool),
@@ -450,7 +454,7 @@ def index_score_bounded(layout: PagedLayout, q_idx, w, kidx_pool, kbound_pool, K
     ld = scores.shape[1]
     ke = (kidx_pool.element_size(),)
     a = _Args(layout).add(q_idx, "q_idx", _KEY).add(w, "w", _F32, B * H_i)
-    a.add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i))
+    a.add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i, kidx_pool))
     a.add(kbound_pool, "kbound_pool", ke, layout.num_blocks * 2 * D_i)
     a.add(scores, "scores", _F32, B * ld).add(ws, "ws", _WS)
     pq, pw, pk, pb, ps, pws = a.ptrs()
@@ -490,7 +494,8 @@ def decode_step(layout: PagedLayout, k_new, k_pool, kidx_new, kidx_pool, q_idx, 
     ke = (q_idx.element_size(),)
     a.add(k_new, "k_new", _BF16, B * Dqk).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
     a.add(v_new, "v_new", _BF16, B * Dv).add(vp, "v_pool", _BF16, _rows(layout, vs))
-    a.add(kidx_new, "kidx_new", ke, B * D_i).add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i))
+    a.add(kidx_new, "kidx_new", ke, B * D_i)
+    a.add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i, kidx_pool))
     a.add(q_idx, "q_idx", _KEY).add(w, "w", _F32, B * H_i).add(q, "q", _BF16)
     a.add(scores, "scores", _F32, B * ld).add(idx, "idx", _I32, B * K)
     a.add(out, "out", _BF16, B * Hq * Dv).add(lse, "lse", _F32, B * Hq).add(ws, "ws", _WS)
@@ -517,7 +522,8 @@ def prefill_step(layout: PagedLayout, seq, q_pos, n_eligible, k_new, k_pool, kid
     ke = (q_idx.element_size(),)
     a.add(k_new, "k_new", _BF16, Nq * Dqk).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
     a.add(v_new, "v_new", _BF16, Nq * Dv).add(vp, "v_pool", _BF16, _rows(layout, vs))
-    a.add(kidx_new, "kidx_new", ke, Nq * D_i).add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i))
+    a.add(kidx_new, "kidx_new", ke, Nq * D_i)
+    a.add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i, kidx_pool))
     a.add(q_idx, "q_idx", _KEY).add(w, "w", _F32, Nq * H_i).add(q, "q", _BF16)
     a.add(scores, "scores", _F32, Nq * ld).add(idx, "idx", _I32, Nq * K)
     a.add(out, "out", _BF16, Nq * Hq * Dv).add(lse, "lse", _F32, Nq * Hq).add(ws, "ws", _WS)
@@ -549,7 +555,8 @@ def prefill_step_chunked(layout: PagedLayout, seq, q_pos, n_eligible, k_new, k_p
     ke = (q_idx.element_size(),)
     a.add(k_new, "k_new", _BF16, Nq * Dqk).add(k_pool, "k_pool", _BF16, _rows(layout, ks))
     a.add(v_new, "v_new", _BF16, Nq * Dv).add(vp, "v_pool", _BF16, _rows(layout, vs))
-    a.add(kidx_new, "kidx_new", ke, Nq * D_i).add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i))
+    a.add(kidx_new, "kidx_new", ke, Nq * D_i)
+    a.add(kidx_pool, "kidx_pool", ke, _rows(layout, D_i, kidx_pool))
     a.add(q_idx, "q_idx", _KEY).add(w, "w", _F32, Nq * H_i).add(q, "q", _BF16)
     a.add(idx, "idx", _I32, Nq * K).add(out, "out", _BF16, Nq * Hq * Dv)
     a.add(lse, "lse", _F32, Nq * Hq).add(ws, "ws", _WS)

@@ -128,3 +128,32 @@ def test_the_appends_refuse_positions_that_are_not_int32(name):
     if name == "pos":
         with pytest.raises(TypeError, match=name):
             dsa.head_norm_rope([dsa.HeadPart(_x(1, 64), _x(1, 64))], a["pos"])
+
+
+def _index_calls(kidx):
+    """Every call that reads or writes an indexer-key pool, on host tensors."""
+    lay, ws = _layout(), _z(4096, dtype=torch.uint8)
+    qi, w, one = _z(2, 4, 64), _z(2, 4, dtype=torch.float32), _z(2, dtype=torch.int32)
+    sc, idx, bound = _z(2, 128, dtype=torch.float32), _z(2, 8, dtype=torch.int32), _z(4, 2, 64)
+    q, out, lse, new, kv = _z(2, 4, 64), _z(2, 4, 64), _z(2, 4, dtype=torch.float32), _z(2, 64), _z(4, 64, 64)
+    step = (new, kv, new, kidx, qi, w, q, 8, 0.1)
+    return {
+        "index_score": lambda: dsa.index_score(lay, qi, w, kidx, sc, ws),
+        "index_score_prefill": lambda: dsa.index_score_prefill(lay, 0, qi, w, kidx, sc, ws),
+        "index_bounds_update": lambda: dsa.index_bounds_update(lay, kidx, bound, ws),
+        "index_score_bounded": lambda: dsa.index_score_bounded(lay, qi, w, kidx, bound, 8, sc, ws),
+        "decode_step": lambda: dsa.decode_step(lay, *step, sc, idx, out, lse, ws),
+        "prefill_step": lambda: dsa.prefill_step(lay, 0, one, one, *step, sc, idx, out, lse, ws),
+        "prefill_step_chunked": lambda: dsa.prefill_step_chunked(lay, 0, one, one, *step, 128, idx, out,
+                                                                 lse, ws),
+        "cache_write": lambda: dsa.cache_write(lay, one, one, ws, kidx_new=new, kidx_pool=kidx),
+    }
+
+
+@pytest.mark.parametrize("call", list(_index_calls(None)))
+def test_an_indexer_key_pool_of_several_heads_is_refused_too(call):
+    with pytest.raises(ValueError, match="heads"):
+        _index_calls(_z(4, 64, 2, 64))[call]()
+    for k in (_z(4, 64, 64), _z(4, 64, 1, 64), _z(256, 64)):
+        with pytest.raises(ValueError, match="CUDA"):
+            _index_calls(k)[call]()
