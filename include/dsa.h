@@ -542,6 +542,86 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
                            void* ws, size_t ws_bytes, dsa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * A K/V cache held in 4 bits, for grouped heads.  The pages are those of the
+ * layout; what a page holds is the calls' own:
+ *   pool  uint8 [num_blocks][Hk][block_size][row bytes], 16-byte aligned, row
+ *         bytes = dsa_cache4_row_bytes(Dk, Dv) (0 for unsupported dims).
+ * A row is one position of one key head: Dk / 2 bytes of K codes, Dv / 2 of V
+ * codes (two E2M1 codes a byte, the lower dim in the lower half), one E4M3
+ * scale per 16 dims of K, then of V, and zeros up to a multiple of 16 bytes.
+ * A code c stands for  head scale * group scale * c.  A group of 16 elements
+ * y = x / head scale is kept as
+ *     group scale s = E4M3(min(max |y| / 6, 448)),  c = E2M1 nearest to y / s
+ * (ties to the even code; codes are 0 where s is 0 or NaN).  An infinity is
+ * kept as +-2688 head scales, a NaN makes its whole group NaN.
+ *  Hk, Dk, Dv  Hk >= 1; Dk and Dv multiples of 16, 16..256
+ *  k_scale, v_scale  [Hk] fp32 head scales, finite and positive, or NULL (1)
+ */
+size_t dsa_cache4_row_bytes(int Dk, int Dv);
+
+/* dsa_cache4_write: K and V rows of N new tokens into the pool.
+ *  seq, pos    as for dsa_cache_append: [N] int32, or both NULL (token i is
+ *              position seq_lens[i] - 1 of sequence i, N <= batch)
+ *  k, v        bf16, token i head h at ptr + i * token stride + h * head
+ *              stride; 16-byte aligned, strides in elements, multiples of 8,
+ *              not negative
+ *  k_out, v_out  [N][Hk][Dk] and [N][Hk][Dv] bf16, 16-byte aligned, both or
+ *              neither: the values that the cache keeps, rounded to bf16 (exact
+ *              where the head scale is 1), for an attention of the prompt that
+ *              sees what later steps will see.  May not overlap k or v.
+ *  ws          dsa_cache4_write_workspace_size() bytes (the status word)
+ * A token whose sequence, position or page is out of range is not stored and
+ * sets DSA_STATUS_BAD_BLOCK; its k_out and v_out are written all the same.  The
+ * same position twice in one call: each group comes from one of the two.
+ * Rows that no token names keep every byte.
+ * Errors: DSA_ERR_INVALID for null pointers, N, strides or alignment;
+ * DSA_ERR_UNSUPPORTED for other dims and for N * Hk beyond 2^31 - 1.
+ */
+size_t dsa_cache4_write_workspace_size(void);
+int dsa_cache4_write(const dsa_paged_layout* layout, const int32_t* seq, const int32_t* pos, int N,
+                     const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                     int64_t v_token_stride, int64_t v_head_stride, int Hk, int Dk, int Dv,
+                     const float* k_scale, const float* v_scale, void* pool, void* k_out,
+                     void* v_out, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* dsa_cache4_read: the values of N positions of the pool as bf16 heads, such as
+ * a cached prefix for the dsa_prompt_attn of the chunk behind it.
+ *  seq, pos    [N] int32, both given
+ *  k_out, v_out  [N][Hk][Dk] and [N][Hk][Dv] bf16, 16-byte aligned
+ * A token out of range reads as zeros and sets DSA_STATUS_BAD_BLOCK.  Errors as
+ * for dsa_cache4_write.
+ */
+size_t dsa_cache4_read_workspace_size(void);
+int dsa_cache4_read(const dsa_paged_layout* layout, const int32_t* seq, const int32_t* pos, int N,
+                    int Hk, int Dk, int Dv, const float* k_scale, const float* v_scale,
+                    const void* pool, void* k_out, void* v_out, void* ws, size_t ws_bytes,
+                    dsa_stream_t stream);
+
+/* dsa_cache4_attn_decode: exact attention of one query per sequence over all of
+ * its positions in the 4-bit pool: for query head h over key head h / (Hq / Hk)
+ *     z_p = sm_scale * q[b][h] . K_p,  out[b][h] = sum_p softmax(z)_p V_p,
+ *     lse[b][h] = log sum_p exp(z_p),  p < seq_lens[b]
+ * on the values that the codes stand for.  Scores, maxima and sums are fp32; a
+ * weight enters the product with V as fp16, off by at most 2^-11 of itself, or by
+ * 2^-32 of the row's largest weight; out is rounded once.
+ *  q           [B][Hq][Dk] bf16, B = layout->batch, Hq a multiple of Hk
+ *  out         [B][Hq][Dv] bf16 (0 for an empty sequence)
+ *  lse         [B][Hq] fp32, or NULL (-inf for an empty sequence)
+ *  ws          dsa_cache4_attn_decode_workspace_size() bytes
+ * Errors: DSA_ERR_INVALID for null pointers, alignment (q, pool and out 16
+ * bytes) or sm_scale; DSA_ERR_UNSUPPORTED for other dims, Hq no multiple of Hk,
+ * and beyond 2^31 units of 256 positions.  Device: a position behind a bad block
+ * id is left out and sets DSA_STATUS_BAD_BLOCK; a length beyond max_seq_len is
+ * cut there and sets DSA_STATUS_BAD_LENGTH; a bounded wait that ran out sets
+ * DSA_STATUS_TIMEOUT (the outputs are then not valid).
+ */
+size_t dsa_cache4_attn_decode_workspace_size(int B, int Hq, int Hk, int Dk, int Dv);
+int dsa_cache4_attn_decode(const dsa_paged_layout* layout, const void* q, const void* pool, int Hq,
+                           int Hk, int Dk, int Dv, const float* k_scale, const float* v_scale,
+                           float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                           dsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Utilities (no counterpart on the pages).
  * dsa_get_status: copy the status word of a workspace to *status (host), after
  *   the work queued on `stream` so far has finished (this call synchronises the

@@ -135,6 +135,15 @@ _sig("dsa_cache_append", _i, [_LP, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _sz, _vp
 _sig("dsa_prefix_attn_decode_workspace_size", _sz, [_i, _i, _i, _i, _i])
 _sig("dsa_prefix_attn_decode", _i, [_LP, _vp, _vp, _i64, _vp, _i64, _i, _i, _i, _i, _f, _vp, _vp,
                                     _vp, _sz, _vp])
+_sig("dsa_cache4_row_bytes", _sz, [_i, _i])
+_sig("dsa_cache4_write_workspace_size", _sz, [])
+_sig("dsa_cache4_write", _i, [_LP, _vp, _vp, _i, _vp, _i64, _i64, _vp, _i64, _i64, _i, _i, _i, _vp, _vp,
+                              _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("dsa_cache4_read_workspace_size", _sz, [])
+_sig("dsa_cache4_read", _i, [_LP, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("dsa_cache4_attn_decode_workspace_size", _sz, [_i, _i, _i, _i, _i])
+_sig("dsa_cache4_attn_decode", _i, [_LP, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _f, _vp, _vp, _vp, _sz,
+                                    _vp])
 
 SYMBOLS = ("dsa_version", "dsa_launch_count", "dsa_last_error_string", "dsa_get_status",
            "dsa_selftest_bounded_wait", "dsa_selftest_warp_wait",
@@ -152,7 +161,10 @@ SYMBOLS = ("dsa_version", "dsa_launch_count", "dsa_last_error_string", "dsa_get_
            "dsa_index_score_bounded_workspace_size", "dsa_index_score_bounded",
            "dsa_index_bounded_stats",
            "dsa_head_norm_rope", "dsa_cache_append_workspace_size", "dsa_cache_append",
-           "dsa_prefix_attn_decode_workspace_size", "dsa_prefix_attn_decode")
+           "dsa_prefix_attn_decode_workspace_size", "dsa_prefix_attn_decode",
+           "dsa_cache4_row_bytes", "dsa_cache4_write_workspace_size", "dsa_cache4_write",
+           "dsa_cache4_read_workspace_size", "dsa_cache4_read",
+           "dsa_cache4_attn_decode_workspace_size", "dsa_cache4_attn_decode")
 
 
 def lib() -> ctypes.CDLL:
@@ -829,6 +841,135 @@ def prefix_attn_decode(layout: PagedLayout, q, k_pool, v_pool, prefix_len, sm_sc
                                      sm_scale, po, pl, pws, ws.numel(), _here(dev, stream))
     if rc:
         raise DsaError(rc, "dsa_prefix_attn_decode")
+
+
+# ------------------------------------------------------------ 4-bit cache --
+def cache4_row_bytes(Dk, Dv) -> int:
+    """Bytes of a row of the 4-bit pool (one position of one key head)."""
+    n = int(_lib.dsa_cache4_row_bytes(Dk, Dv))
+    if n == 0:
+        raise ValueError(f"head dims {Dk} / {Dv}: multiples of 16 up to 256 are taken")
+    return n
+
+
+def cache4_pool(num_blocks, heads, block_size, Dk, Dv, device=None) -> torch.Tensor:
+    """A zero-filled 4-bit pool [num_blocks, heads, block_size, row bytes]."""
+    return torch.zeros((num_blocks, heads, block_size, cache4_row_bytes(Dk, Dv)), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def _pool4(layout: PagedLayout, pool, Dk: int, Dv: int, dev: int):
+    """(address, heads) of a 4-bit pool, checked against the layout's pages."""
+    if pool.dim() != 4 or pool.shape[2] != layout.block_size or pool.shape[3] != cache4_row_bytes(Dk, Dv):
+        raise ValueError(f"pool: [num_blocks, heads, {layout.block_size}, {cache4_row_bytes(Dk, Dv)}] is "
+                         f"required, not {tuple(pool.shape)}")
+    if pool.shape[0] < layout.num_blocks:
+        raise ValueError(f"pool: {pool.shape[0]} pages; the layout has {layout.num_blocks}")
+    return _vec(pool, "pool", torch.uint8, 0, dev), pool.shape[1]
+
+
+def _strided(t, name: str, dev: int):
+    """(address, token stride, head stride) of bf16 heads [N, heads, dim]."""
+    if t.dim() != 3:
+        raise ValueError(f"{name}: [tokens, heads, dim] is required, not {tuple(t.shape)}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: {t.dtype}; torch.bfloat16 is required")
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: a CUDA tensor on cuda:{dev} is required")
+    # the stride of a dimension of one element is never used and may be anything
+    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _on_gpu(dev: int, name: str, layout: Optional[PagedLayout] = None):
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor is required")
+    if layout is not None and (layout.block_table.get_device() != dev
+                               or layout.seq_lens.get_device() != dev):
+        raise ValueError(f"layout: block_table and seq_lens must be CUDA tensors on cuda:{dev}")
+
+
+def cache4_write_workspace_size() -> int:
+    return int(_lib.dsa_cache4_write_workspace_size())
+
+
+def cache4_write(layout: PagedLayout, seq, pos, k, v, pool, ws, k_scale=None, v_scale=None, k_out=None,
+                 v_out=None, stream=None):
+    """Store new tokens' K [N, Hk, Dk] and V [N, Hk, Dv] (bf16, strided) in the
+    4-bit pool (include/dsa.h, dsa_cache4_write).  seq, pos [N] int32, or both
+    None: token i is position seq_lens[i] - 1 of sequence i.  k_scale, v_scale
+    [Hk] float32 or None; k_out, v_out: the values that the cache keeps, bf16."""
+    dev = k.get_device()
+    pk, kts, khs = _strided(k, "k", dev)
+    pv, vts, vhs = _strided(v, "v", dev)
+    (N, Hk, Dk), Dv = k.shape, v.shape[2]
+    if v.shape[:2] != k.shape[:2]:
+        raise ValueError(f"v: {tuple(v.shape[:2])} tokens and heads; k has {(N, Hk)}")
+    pp, heads = _pool4(layout, pool, Dk, Dv, dev)
+    if heads != Hk:
+        raise ValueError(f"pool: {heads} heads; k has {Hk}")
+    args = (_vec(k_scale, "k_scale", torch.float32, Hk, dev), _vec(v_scale, "v_scale", torch.float32, Hk, dev),
+            pp, _vec(k_out, "k_out", torch.bfloat16, N * Hk * Dk, dev),
+            _vec(v_out, "v_out", torch.bfloat16, N * Hk * Dv, dev), _vec(ws, "ws", torch.uint8, 0, dev))
+    ps, po = _vec(seq, "seq", torch.int32, N, dev), _vec(pos, "pos", torch.int32, N, dev)
+    _on_gpu(dev, "k", layout)
+    rc = _lib.dsa_cache4_write(layout.c(), ps, po, N, pk, kts, khs, pv, vts, vhs, Hk, Dk, Dv, *args,
+                               ws.numel(), _here(dev, stream))
+    if rc:
+        raise DsaError(rc, "dsa_cache4_write")
+
+
+def cache4_read_workspace_size() -> int:
+    return int(_lib.dsa_cache4_read_workspace_size())
+
+
+def cache4_read(layout: PagedLayout, seq, pos, pool, k_out, v_out, ws, k_scale=None, v_scale=None,
+                stream=None):
+    """The values of N positions of the 4-bit pool as bf16 heads k_out
+    [N, Hk, Dk] and v_out [N, Hk, Dv] (include/dsa.h, dsa_cache4_read)."""
+    dev = k_out.get_device()
+    if k_out.dim() != 3 or v_out.dim() != 3 or v_out.shape[:2] != k_out.shape[:2]:
+        raise ValueError("k_out, v_out: [tokens, heads, dim] of the same tokens and heads are required")
+    (N, Hk, Dk), Dv = k_out.shape, v_out.shape[2]
+    pp, heads = _pool4(layout, pool, Dk, Dv, dev)
+    if heads != Hk:
+        raise ValueError(f"pool: {heads} heads; k_out has {Hk}")
+    ps, po = _vec(seq, "seq", torch.int32, N, dev), _vec(pos, "pos", torch.int32, N, dev)
+    args = (_vec(k_scale, "k_scale", torch.float32, Hk, dev), _vec(v_scale, "v_scale", torch.float32, Hk, dev),
+            pp, _vec(k_out, "k_out", torch.bfloat16, 0, dev), _vec(v_out, "v_out", torch.bfloat16, 0, dev),
+            _vec(ws, "ws", torch.uint8, 0, dev))
+    _on_gpu(dev, "k_out", layout)
+    rc = _lib.dsa_cache4_read(layout.c(), ps, po, N, Hk, Dk, Dv, *args, ws.numel(), _here(dev, stream))
+    if rc:
+        raise DsaError(rc, "dsa_cache4_read")
+
+
+def cache4_attn_decode_workspace_size(B, Hq, Hk, Dk, Dv) -> int:
+    return int(_lib.dsa_cache4_attn_decode_workspace_size(B, Hq, Hk, Dk, Dv))
+
+
+def cache4_attn_decode(layout: PagedLayout, q, pool, sm_scale, out, lse, ws, k_scale=None, v_scale=None,
+                       stream=None):
+    """Exact attention of one query per sequence, q [B, Hq, Dk], over all its
+    positions in the 4-bit pool (include/dsa.h, dsa_cache4_attn_decode); Hq a
+    multiple of the pool's heads, out [B, Hq, Dv] bfloat16, lse float32 or
+    None."""
+    dev = q.get_device()
+    if q.dim() != 3 or out.dim() != 3 or out.shape[:2] != q.shape[:2]:
+        raise ValueError("q, out: [sequences, heads, dim] of the same sequences and heads are required")
+    (B, Hq, Dk), Dv = q.shape, out.shape[2]
+    if B != layout.batch:
+        raise ValueError(f"q: {B} sequences; the layout has {layout.batch}")
+    pp, Hk = _pool4(layout, pool, Dk, Dv, dev)
+    pq, po = _vec(q, "q", torch.bfloat16, 0, dev), _vec(out, "out", torch.bfloat16, 0, dev)
+    pl, pw = _vec(lse, "lse", torch.float32, B * Hq, dev), _vec(ws, "ws", torch.uint8, 0, dev)
+    ks, vs = _vec(k_scale, "k_scale", torch.float32, Hk, dev), _vec(v_scale, "v_scale", torch.float32, Hk, dev)
+    _on_gpu(dev, "q", layout)
+    rc = _lib.dsa_cache4_attn_decode(layout.c(), pq, pp, Hq, Hk, Dk, Dv, ks, vs, sm_scale, po, pl, pw,
+                                     ws.numel(), _here(dev, stream))
+    if rc:
+        raise DsaError(rc, "dsa_cache4_attn_decode")
 
 
 def get_status(ws, clear: bool = True, stream=None) -> int:

@@ -8,6 +8,7 @@
 #include <string>
 
 #include "dsa.h"
+#include "cache4.cuh"
 #include "dsa_internal.cuh"
 
 namespace dsa {
@@ -356,6 +357,135 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
   p.lse = lse;
   p.status = reinterpret_cast<int*>(ws);
   return launch_prefix_attn(p, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------ 4-bit cache --
+static bool cache4_dims(int Hk, int Dk, int Dv) {
+  return Hk >= 1 && Dk >= 16 && Dk <= 256 && Dk % 16 == 0 && Dv >= 16 && Dv <= 256 && Dv % 16 == 0;
+}
+
+static bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= (1LL << 40); }
+
+size_t dsa_cache4_row_bytes(int Dk, int Dv) {
+  return cache4_dims(1, Dk, Dv) ? (size_t)cache4_row_bytes(Dk, Dv) : 0;
+}
+
+size_t dsa_cache4_write_workspace_size(void) { return kWsHeader; }
+size_t dsa_cache4_read_workspace_size(void) { return kWsHeader; }
+
+// What both row calls check and fill in.
+static int cache4_rows(const char* what, const dsa_paged_layout* layout, const int32_t* seq,
+                       const int32_t* pos, int N, int Hk, int Dk, int Dv, const float* k_scale,
+                       const float* v_scale, const void* pool, void* k_out, void* v_out, void* ws,
+                       size_t ws_bytes, Cache4RowsParams* p) {
+  const std::string w(what);
+  int rc = check_layout(layout, &p->lay);
+  if (rc) return rc;
+  if (N < 0) return set_error(DSA_ERR_INVALID, w + ": N < 0");
+  if (!pool) return set_error(DSA_ERR_INVALID, w + ": NULL tensor pointer");
+  if (!cache4_dims(Hk, Dk, Dv))
+    return set_error(DSA_ERR_UNSUPPORTED, w + ": supported Hk >= 1, Dk and Dv 16..256 in multiples of 16");
+  if ((long long)N * Hk > 0x7fffffffLL)
+    return set_error(DSA_ERR_UNSUPPORTED, w + ": N * Hk beyond 2^31 - 1");
+  if (!aligned16(pool) || !aligned16(k_out) || !aligned16(v_out))
+    return set_error(DSA_ERR_INVALID, w + ": tensors must be 16-byte aligned");
+  rc = check_ws(ws, ws_bytes, kWsHeader);
+  if (rc) return rc;
+  p->seq = seq;
+  p->pos = pos;
+  p->N = N;
+  p->Hk = Hk;
+  p->Dk = Dk;
+  p->Dv = Dv;
+  p->row_bytes = cache4_row_bytes(Dk, Dv);
+  p->k_scale = k_scale;
+  p->v_scale = v_scale;
+  p->pool = reinterpret_cast<uint8_t*>(const_cast<void*>(pool));
+  p->k_out = reinterpret_cast<__nv_bfloat16*>(k_out);
+  p->v_out = reinterpret_cast<__nv_bfloat16*>(v_out);
+  p->status = reinterpret_cast<int*>(ws);
+  return DSA_OK;
+}
+
+int dsa_cache4_write(const dsa_paged_layout* layout, const int32_t* seq, const int32_t* pos, int N,
+                     const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                     int64_t v_token_stride, int64_t v_head_stride, int Hk, int Dk, int Dv,
+                     const float* k_scale, const float* v_scale, void* pool, void* k_out,
+                     void* v_out, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  Cache4RowsParams p{};
+  if (!k || !v) return set_error(DSA_ERR_INVALID, "cache4_write: NULL tensor pointer");
+  int rc = cache4_rows("cache4_write", layout, seq, pos, N, Hk, Dk, Dv, k_scale, v_scale, pool, k_out,
+                       v_out, ws, ws_bytes, &p);
+  if (rc) return rc;
+  if ((seq == nullptr) != (pos == nullptr))
+    return set_error(DSA_ERR_INVALID, "cache4_write: give both seq and pos, or neither (append)");
+  if (!seq && N > layout->batch)
+    return set_error(DSA_ERR_INVALID, "cache4_write: append form needs N <= batch");
+  if ((k_out == nullptr) != (v_out == nullptr))
+    return set_error(DSA_ERR_INVALID, "cache4_write: give both k_out and v_out, or neither");
+  if (!aligned16(k) || !aligned16(v))
+    return set_error(DSA_ERR_INVALID, "cache4_write: k / v must be 16-byte aligned");
+  if (!stride_ok(k_token_stride) || !stride_ok(k_head_stride) || !stride_ok(v_token_stride) ||
+      !stride_ok(v_head_stride))
+    return set_error(DSA_ERR_INVALID, "cache4_write: strides must be multiples of 8, 0..2^40");
+  p.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  p.k_ts = k_token_stride;
+  p.k_hs = k_head_stride;
+  p.v_ts = v_token_stride;
+  p.v_hs = v_head_stride;
+  return launch_cache4_rows(p, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dsa_cache4_read(const dsa_paged_layout* layout, const int32_t* seq, const int32_t* pos, int N,
+                    int Hk, int Dk, int Dv, const float* k_scale, const float* v_scale,
+                    const void* pool, void* k_out, void* v_out, void* ws, size_t ws_bytes,
+                    dsa_stream_t stream) {
+  Cache4RowsParams p{};
+  if (!k_out || !v_out || !seq || !pos)
+    return set_error(DSA_ERR_INVALID, "cache4_read: NULL tensor pointer");
+  int rc = cache4_rows("cache4_read", layout, seq, pos, N, Hk, Dk, Dv, k_scale, v_scale, pool, k_out,
+                       v_out, ws, ws_bytes, &p);
+  if (rc) return rc;
+  return launch_cache4_rows(p, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dsa_cache4_attn_decode_workspace_size(int B, int Hq, int Hk, int Dk, int Dv) {
+  if (B < 1 || Hq < 1 || !cache4_dims(Hk, Dk, Dv) || Hq % Hk) return kWsHeader;
+  return cache4_attn_ws(B, Hq, Hk, Dk, Dv);
+}
+
+int dsa_cache4_attn_decode(const dsa_paged_layout* layout, const void* q, const void* pool, int Hq,
+                           int Hk, int Dk, int Dv, const float* k_scale, const float* v_scale,
+                           float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                           dsa_stream_t stream) {
+  Cache4AttnParams p{};
+  int rc = check_layout(layout, &p.lay);
+  if (rc) return rc;
+  if (!q || !pool || !out) return set_error(DSA_ERR_INVALID, "cache4_attn_decode: NULL tensor pointer");
+  if (!cache4_dims(Hk, Dk, Dv) || Hq < 1 || Hq % Hk)
+    return set_error(DSA_ERR_UNSUPPORTED,
+                     "cache4_attn_decode: supported Hq a multiple of Hk, Dk and Dv 16..256 in multiples of 16");
+  if (!aligned16(q) || !aligned16(pool) || !aligned16(out))
+    return set_error(DSA_ERR_INVALID, "cache4_attn_decode: q / pool / out must be 16-byte aligned");
+  if (!(sm_scale > 0.0f) || sm_scale > 1e38f)
+    return set_error(DSA_ERR_INVALID, "cache4_attn_decode: sm_scale must be a positive number up to 1e38");
+  rc = check_ws(ws, ws_bytes, cache4_attn_ws(layout->batch, Hq, Hk, Dk, Dv));
+  if (rc) return rc;
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.pool = reinterpret_cast<const uint8_t*>(pool);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.Dk = Dk;
+  p.Dv = Dv;
+  p.row_bytes = cache4_row_bytes(Dk, Dv);
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = reinterpret_cast<int*>(ws);
+  return launch_cache4_attn(p, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 static int attn_common(const dsa_paged_layout* layout, const void* q, const void* k_pool,
