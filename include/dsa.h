@@ -542,6 +542,44 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
                            void* ws, size_t ws_bytes, dsa_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * dsa_prompt_attn: exact causal attention of whole prompts, or of chunks behind
+ * keys that are in hand, several sequences packed end to end, grouped heads.
+ * The first pages' prefill selects keys; this call is for layers, or prompts no
+ * longer than the selection, that attend every one of them.  Token i of the nq
+ * query tokens of a sequence with nk keys sees keys j <= i + nk - nq (the last
+ * token sees all):
+ *     z_j = sm_scale * q[i][h] . k[j][h'],  out[i][h] = sum_j softmax(z)_j v[j][h'],
+ *     lse[i][h] = log sum_j exp(z_j),  h' = h / (Hq / Hk)
+ * A token that sees no key (nk < nq) has out 0 and lse -inf.  Scores, maxima and
+ * sums are fp32.  A weight enters the product with V as bf16, off by at most 2^-9
+ * of itself, and as bf16 hi + lo (2^-17) for the tokens whose tile begins with
+ * one that sees no more than 512 keys; out is rounded once.  What a token does
+ * not see does not reach it, NaN and infinities included.
+ *  q, k, v     bf16: token i head h at ptr + i * token stride + h * head stride
+ *              (elements, multiples of 8, heads not overlapping); q has Nq tokens
+ *              and Hq heads, k and v Nk tokens and Hk heads; 16-byte aligned
+ *  cu_q, cu_k  device int32 [B + 1], not decreasing: sequence b has query tokens
+ *              cu_q[b] .. cu_q[b + 1] - 1 and keys cu_k[b] .. cu_k[b + 1] - 1;
+ *              NULL (with B = 1): all of them.  Tokens of no sequence are not
+ *              written.
+ *  Hq, Hk      Hq a multiple of Hk;  Dk, Dv multiples of 8, 8..256
+ *  out         bf16 [Nq][Hq][Dv] with strides like q's;  lse [Nq][Hq] fp32 or NULL
+ *  ws          dsa_prompt_attn_workspace_size() bytes
+ * Errors: DSA_ERR_INVALID for null pointers, strides, alignment or sm_scale;
+ * DSA_ERR_UNSUPPORTED for other heads and dims and beyond 2^31 items of 256 rows.
+ * Device: a sequence whose offsets are not inside the tokens is left out and sets
+ * DSA_STATUS_BAD_LENGTH; a bounded wait that ran out sets DSA_STATUS_TIMEOUT (the
+ * outputs are then not valid).
+ */
+size_t dsa_prompt_attn_workspace_size(int B, int Nq, int Hq, int Hk, int Dk, int Dv);
+int dsa_prompt_attn(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                    int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                    int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
+                    const int32_t* cu_k, int B, int Nq, int Nk, int Hq, int Hk, int Dk, int Dv,
+                    float sm_scale, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                    float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * A K/V cache held in 4 bits, for grouped heads.  The pages are those of the
  * layout; what a page holds is the calls' own:
  *   pool  uint8 [num_blocks][Hk][block_size][row bytes], 16-byte aligned, row

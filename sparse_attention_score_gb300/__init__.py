@@ -135,6 +135,9 @@ _sig("dsa_cache_append", _i, [_LP, _vp, _vp, _i, _vp, _i, _vp, _i, _vp, _sz, _vp
 _sig("dsa_prefix_attn_decode_workspace_size", _sz, [_i, _i, _i, _i, _i])
 _sig("dsa_prefix_attn_decode", _i, [_LP, _vp, _vp, _i64, _vp, _i64, _i, _i, _i, _i, _f, _vp, _vp,
                                     _vp, _sz, _vp])
+_sig("dsa_prompt_attn_workspace_size", _sz, [_i, _i, _i, _i, _i, _i])
+_sig("dsa_prompt_attn", _i, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i, _i, _i, _i,
+                             _i, _i, _i, _f, _vp, _i64, _i64, _vp, _vp, _sz, _vp])
 _sig("dsa_cache4_row_bytes", _sz, [_i, _i])
 _sig("dsa_cache4_write_workspace_size", _sz, [])
 _sig("dsa_cache4_write", _i, [_LP, _vp, _vp, _i, _vp, _i64, _i64, _vp, _i64, _i64, _i, _i, _i, _vp, _vp,
@@ -162,6 +165,7 @@ SYMBOLS = ("dsa_version", "dsa_launch_count", "dsa_last_error_string", "dsa_get_
            "dsa_index_bounded_stats",
            "dsa_head_norm_rope", "dsa_cache_append_workspace_size", "dsa_cache_append",
            "dsa_prefix_attn_decode_workspace_size", "dsa_prefix_attn_decode",
+           "dsa_prompt_attn_workspace_size", "dsa_prompt_attn",
            "dsa_cache4_row_bytes", "dsa_cache4_write_workspace_size", "dsa_cache4_write",
            "dsa_cache4_read_workspace_size", "dsa_cache4_read",
            "dsa_cache4_attn_decode_workspace_size", "dsa_cache4_attn_decode")
@@ -843,6 +847,68 @@ def prefix_attn_decode(layout: PagedLayout, q, k_pool, v_pool, prefix_len, sm_sc
         raise DsaError(rc, "dsa_prefix_attn_decode")
 
 
+# ------------------------------------------------------- prompt attention --
+def _strided(t, name: str, dev: int):
+    """(address, token stride, head stride) of bf16 heads [N, heads, dim]."""
+    if t.dim() != 3:
+        raise ValueError(f"{name}: [tokens, heads, dim] is required, not {tuple(t.shape)}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: {t.dtype}; torch.bfloat16 is required")
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: a CUDA tensor on cuda:{dev} is required")
+    # the stride of a dimension of one element is never used and may be anything
+    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _on_gpu(dev: int, name: str, layout: Optional[PagedLayout] = None):
+    if dev < 0:
+        raise ValueError(f"{name}: a CUDA tensor is required")
+    if layout is not None and (layout.block_table.get_device() != dev
+                               or layout.seq_lens.get_device() != dev):
+        raise ValueError(f"layout: block_table and seq_lens must be CUDA tensors on cuda:{dev}")
+
+
+def prompt_attn_workspace_size(B, Nq, Hq, Hk, Dk, Dv) -> int:
+    return int(_lib.dsa_prompt_attn_workspace_size(B, Nq, Hq, Hk, Dk, Dv))
+
+
+def prompt_attn(q, k, v, sm_scale, out, lse, ws, cu_q=None, cu_k=None, stream=None):
+    """Exact causal attention of packed prompts with grouped heads
+    (include/dsa.h, dsa_prompt_attn): q [Nq, Hq, Dk], k [Nk, Hk, Dk],
+    v [Nk, Hk, Dv] and out [Nq, Hq, Dv] bfloat16, strided; lse [Nq, Hq] float32
+    or None.  cu_q, cu_k [B + 1] int32: where each sequence's tokens begin; only
+    cu_q given: the keys are the same tokens; neither: one sequence."""
+    dev = q.get_device()
+    pq, pk, pv, po = (_strided(t, n, dev) for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")))
+    (Nq, Hq, Dk), (Nk, Hk, _), Dv = q.shape, k.shape, v.shape[2]
+    if k.shape[2] != Dk:
+        raise ValueError(f"k: heads of {k.shape[2]}; q has heads of {Dk}")
+    if v.shape[:2] != k.shape[:2]:
+        raise ValueError(f"v: {tuple(v.shape[:2])} tokens and heads; k has {(Nk, Hk)}")
+    if tuple(out.shape) != (Nq, Hq, Dv):
+        raise ValueError(f"out: {tuple(out.shape)}; the call writes {(Nq, Hq, Dv)}")
+    if cu_q is None and cu_k is not None:
+        raise ValueError("cu_q: required with cu_k")
+    B = 1
+    if cu_q is not None:
+        if cu_k is None:
+            if Nk != Nq:
+                raise ValueError(f"cu_k: required, q has {Nq} tokens and k {Nk}")
+            cu_k = cu_q
+        B = cu_q.numel() - 1
+        if B < 1:
+            raise ValueError("cu_q: the beginning of each sequence and the end of the last are required")
+    pc = (_vec(cu_q, "cu_q", torch.int32, B + 1, dev), _vec(cu_k, "cu_k", torch.int32, B + 1, dev))
+    pl, pw = _vec(lse, "lse", torch.float32, Nq * Hq, dev), _vec(ws, "ws", torch.uint8, 0, dev)
+    _on_gpu(dev, "q")
+    rc = _lib.dsa_prompt_attn(*pq, *pk, *pv, *pc, B, Nq, Nk, Hq, Hk, Dk, Dv, sm_scale, *po, pl, pw,
+                              ws.numel(), _here(dev, stream))
+    if rc:
+        raise DsaError(rc, "dsa_prompt_attn")
+
+
 # ------------------------------------------------------------ 4-bit cache --
 def cache4_row_bytes(Dk, Dv) -> int:
     """Bytes of a row of the 4-bit pool (one position of one key head)."""
@@ -866,28 +932,6 @@ def _pool4(layout: PagedLayout, pool, Dk: int, Dv: int, dev: int):
     if pool.shape[0] < layout.num_blocks:
         raise ValueError(f"pool: {pool.shape[0]} pages; the layout has {layout.num_blocks}")
     return _vec(pool, "pool", torch.uint8, 0, dev), pool.shape[1]
-
-
-def _strided(t, name: str, dev: int):
-    """(address, token stride, head stride) of bf16 heads [N, heads, dim]."""
-    if t.dim() != 3:
-        raise ValueError(f"{name}: [tokens, heads, dim] is required, not {tuple(t.shape)}")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: {t.dtype}; torch.bfloat16 is required")
-    if t.stride(2) != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: a CUDA tensor on cuda:{dev} is required")
-    # the stride of a dimension of one element is never used and may be anything
-    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
-
-
-def _on_gpu(dev: int, name: str, layout: Optional[PagedLayout] = None):
-    if dev < 0:
-        raise ValueError(f"{name}: a CUDA tensor is required")
-    if layout is not None and (layout.block_table.get_device() != dev
-                               or layout.seq_lens.get_device() != dev):
-        raise ValueError(f"layout: block_table and seq_lens must be CUDA tensors on cuda:{dev}")
 
 
 def cache4_write_workspace_size() -> int:

@@ -10,6 +10,7 @@
 #include "dsa.h"
 #include "cache4.cuh"
 #include "dsa_internal.cuh"
+#include "prompt_attn.cuh"
 
 namespace dsa {
 
@@ -359,12 +360,81 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
   return launch_prefix_attn(p, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
+static bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= (1LL << 38); }
+
+// -------------------------------------------------------- prompt attention --
+size_t dsa_prompt_attn_workspace_size(int B, int Nq, int Hq, int Hk, int Dk, int Dv) {
+  (void)B, (void)Nq, (void)Hq, (void)Hk, (void)Dk, (void)Dv;
+  return prompt_attn_ws();
+}
+
+// Strides of [tokens][heads][dim]: unused ones may be anything, the others have
+// to keep rows apart.
+static bool heads_ok(int tokens, int heads, int dim, int64_t ts, int64_t hs) {
+  if (tokens > 1 && (!stride_ok(ts) || ts < dim)) return false;
+  return heads <= 1 || (stride_ok(hs) && hs >= dim);
+}
+
+int dsa_prompt_attn(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                    int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                    int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
+                    const int32_t* cu_k, int B, int Nq, int Nk, int Hq, int Hk, int Dk, int Dv,
+                    float sm_scale, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                    float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  if (B < 1 || Nq < 0 || Nk < 0)
+    return set_error(DSA_ERR_INVALID, "prompt_attn: need B >= 1, Nq >= 0, Nk >= 0");
+  if (Hk < 1 || Hq < 1 || Hq % Hk || Dk < 8 || Dk > 256 || Dk % 8 || Dv < 8 || Dv > 256 || Dv % 8)
+    return set_error(DSA_ERR_UNSUPPORTED,
+                     "prompt_attn: supported Hq a multiple of Hk, Dk and Dv 8..256 in multiples of 8");
+  if (B > 1 && (!cu_q || !cu_k))
+    return set_error(DSA_ERR_INVALID, "prompt_attn: several sequences need cu_q and cu_k");
+  if (!(sm_scale > 0.0f) || sm_scale > 1e38f)
+    return set_error(DSA_ERR_INVALID, "prompt_attn: sm_scale must be a positive number up to 1e38");
+  if ((Nq > 0 && (!q || !out)) || (Nk > 0 && (!k || !v)))
+    return set_error(DSA_ERR_INVALID, "prompt_attn: NULL tensor pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+    return set_error(DSA_ERR_INVALID, "prompt_attn: q / k / v / out must be 16-byte aligned");
+  if (!heads_ok(Nq, Hq, Dk, q_token_stride, q_head_stride) ||
+      !heads_ok(Nk, Hk, Dk, k_token_stride, k_head_stride) ||
+      !heads_ok(Nk, Hk, Dv, v_token_stride, v_head_stride) ||
+      !heads_ok(Nq, Hq, Dv, out_token_stride, out_head_stride))
+    return set_error(DSA_ERR_INVALID,
+                     "prompt_attn: strides must be multiples of 8 up to 2^38 that keep heads apart");
+  int rc = check_ws(ws, ws_bytes, prompt_attn_ws());
+  if (rc) return rc;
+  if (Nq == 0) return DSA_OK;
+  PromptAttnParams p{};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.v = reinterpret_cast<const __nv_bfloat16*>(v);
+  p.q_ts = q_token_stride;
+  p.q_hs = q_head_stride;
+  p.k_ts = k_token_stride;
+  p.k_hs = k_head_stride;
+  p.v_ts = v_token_stride;
+  p.v_hs = v_head_stride;
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.B = B;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.Dk = Dk;
+  p.Dv = Dv;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.o_ts = out_token_stride;
+  p.o_hs = out_head_stride;
+  p.lse = lse;
+  p.status = reinterpret_cast<int*>(ws);
+  return launch_prompt_attn(p, ws, reinterpret_cast<cudaStream_t>(stream));
+}
+
 // ------------------------------------------------------------ 4-bit cache --
 static bool cache4_dims(int Hk, int Dk, int Dv) {
   return Hk >= 1 && Dk >= 16 && Dk <= 256 && Dk % 16 == 0 && Dv >= 16 && Dv <= 256 && Dv % 16 == 0;
 }
-
-static bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= (1LL << 40); }
 
 size_t dsa_cache4_row_bytes(int Dk, int Dv) {
   return cache4_dims(1, Dk, Dv) ? (size_t)cache4_row_bytes(Dk, Dv) : 0;
@@ -427,7 +497,7 @@ int dsa_cache4_write(const dsa_paged_layout* layout, const int32_t* seq, const i
     return set_error(DSA_ERR_INVALID, "cache4_write: k / v must be 16-byte aligned");
   if (!stride_ok(k_token_stride) || !stride_ok(k_head_stride) || !stride_ok(v_token_stride) ||
       !stride_ok(v_head_stride))
-    return set_error(DSA_ERR_INVALID, "cache4_write: strides must be multiples of 8, 0..2^40");
+    return set_error(DSA_ERR_INVALID, "cache4_write: strides must be multiples of 8, 0..2^38");
   p.k = reinterpret_cast<const __nv_bfloat16*>(k);
   p.v = reinterpret_cast<const __nv_bfloat16*>(v);
   p.k_ts = k_token_stride;

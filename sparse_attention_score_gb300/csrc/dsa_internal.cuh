@@ -166,6 +166,12 @@ int make_tmap_2d(CUtensorMap* map, const void* base, bool one_byte, uint64_t inn
 // block after block in shared memory (128-byte swizzle); cols a multiple of 64.
 int make_tmap_blocks(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                      uint64_t row_stride_bytes, uint32_t box_rows, uint32_t box_blocks);
+// bf16 heads [tokens][heads][dim] (strides in elements, any value where there is
+// one token or head) in boxes of box_dims x box_heads x box_tokens, a token's
+// heads one after the other; dims past the head and tokens past the last read as 0.
+int make_tmap_heads(CUtensorMap* map, const void* base, int dim, int heads, int tokens,
+                    long long head_stride, long long token_stride, uint32_t box_dims,
+                    uint32_t box_heads, uint32_t box_tokens);
 int sm_count();  // of the current device
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current
 // device (once per kernel and device, thread-safe); DSA_ERR_CUDA on failure.

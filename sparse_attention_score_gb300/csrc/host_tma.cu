@@ -61,6 +61,26 @@ int make_tmap_blocks(CUtensorMap* map, const void* base, uint64_t cols, uint64_t
   return DSA_OK;
 }
 
+int make_tmap_heads(CUtensorMap* map, const void* base, int dim, int heads, int tokens,
+                    long long head_stride, long long token_stride, uint32_t box_dims,
+                    uint32_t box_heads, uint32_t box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return set_error(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const long long row = ((long long)dim + 7) / 8 * 8;
+  if (heads <= 1) head_stride = row;
+  if (tokens <= 1) token_stride = row;
+  cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)(tokens > 0 ? tokens : 1)};
+  cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
+  cuuint32_t box[3] = {box_dims, box_heads, box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(DSA_ERR_CUDA, "cuTensorMapEncodeTiled failed with " + std::to_string((int)r));
+  return DSA_OK;
+}
+
 int sm_count() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;

@@ -1,0 +1,812 @@
+// prompt_attn.cu -- exact causal attention of whole prompts, several sequences
+// packed end to end, grouped heads, on the tensor cores.
+//
+// The exact softmax of the sparse attention ("Day-0 Adaptation of
+// Trillion-Parameter MoE Models on Domestic GPUs", section 3 (3): the
+// compute-bound prefill) with every causal position selected, on keys and
+// values that are still in hand as packed heads, so nothing is gathered.
+//
+// Rows and tiles.  A row is one (token, query head).  The heads that share a key
+// head and the tokens of a sequence are laid together in tiles of 128 rows:
+// gp heads (the largest power of two that divides the group) of 128 / gp
+// tokens, which a TMA box brings in as such.  An item is two such tiles, A and
+// B, one behind the other in the sequence, over all the keys that they see, in
+// tiles of 128 keys.  CTAs (one per SM, persistent) take items off a counter,
+// those of late tokens, which see most, first.
+//
+// One key tile (tcgen05, M = 128, one accumulator of 128 columns each):
+//   S_X [128 x 128] = Q_X K^T       X = A, B; operands in shared memory;
+//   softmax: a thread has a row of S_X in registers; the running maximum is
+//       raised only when a tile exceeds it by more than 2^8, O_X rescaled then;
+//   P_X bf16 over S_X in TMEM;  O_X [128 x Dv] += P_X V, P_X from TMEM.
+// The tensor cores alternate: while the softmax of A works on its scores, they
+// do O and the next S of B.  TMEM: S_A, S_B, O_A, O_B, 128 columns each.  V of
+// more than 128 columns is taken in two halves, each an item of its own that
+// computes S again.
+//
+// P is rounded to bf16 once (each weight by at most 2^-9 of itself, like the
+// output), except where rows see few keys and such roundings do not average out:
+// an item whose first row sees no more than 512 keys keeps P as bf16 hi + lo
+// (2^-17), both multiplied with the same V.  Statistics and sums are fp32.
+//
+// What no row may see.  Scores of hidden keys are set to -inf by the row's own
+// limit.  V has no such place: a hidden row's weight is 0, but 0 times what an
+// unrelated sequence, or a later token, has there may be NaN.  Two warps
+// therefore look through V of the key tiles that some row sees in part (one or
+// two per item), before the product: rows that no row of the item sees become
+// zeros, and so do infinities and NaN; an item with such values adds them to the
+// rows that do see them when it writes its output.
+//
+// Warp roles (384 threads): 0-3 softmax of A, 4-7 of B, 8 fills the ring of K
+// and V (chunks of 64 dims of 128 keys) and Q, 9 issues the products, 10 and 11
+// look through V.  Every wait is bounded (DSA_STATUS_TIMEOUT, then the CTA winds
+// down).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "device_common.cuh"
+#include "dsa_internal.cuh"
+#include "prompt_attn.cuh"
+#include "sm100.cuh"
+
+namespace dsa {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kTile = 128;              // rows of a tile, keys of a tile
+constexpr int kChunk = 64;              // dims of a chunk
+constexpr int kChunkBytes = kTile * kChunk * 2;
+constexpr int kThreads = 384;
+constexpr int kMaxRing = 12;            // chunks
+constexpr int kSlots = 4;               // item descriptors in flight
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 X
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kShort = 512;
+constexpr int kVWidth = 128;            // columns of V per item
+constexpr int kReaders = 11;            // warps that read an item's descriptor
+
+struct Item {
+  int end;        // no more items
+  int q0;         // tile A's first token in q
+  int tok;        // ... and in its sequence
+  int nq, nk, k0; // of the sequence
+  int hk, h0;     // key head, first query head
+  int v0, dv;     // columns of V
+  int n[2];       // key tiles of A and B
+  int lim;        // keys that the first row sees
+};
+
+struct Smem {
+  uint64_t full[kMaxRing], empty[kMaxRing];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2];
+  uint64_t vclean, ifull[kSlots], iempty[kSlots], done;
+  Item item[kSlots];
+  int odd[2][2 * kSlots];  // per reader of V: the item's V held infinities or NaN
+  int vissued;       // V tiles to look through whose copies were issued
+  int fills, qfills[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+struct Geo {
+  PromptAttnParams a;
+  int G, lgp, HB;     // query heads per key head, log2 of gp, G / gp
+  int VH;             // items per head over V's columns
+  int HH;             // items per pair of tiles
+  int nkc;            // chunks of Q and K
+  int ring;           // chunks
+  int* next;          // the next item
+  int* left;          // CTAs that are done
+};
+
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void expect_elected(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A from TMEM: a row per lane, two bf16 of a row per column
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Wait of a whole warp until *count (in shared memory, only growing) is at
+// least n; bounded like pair_wait.
+__device__ __forceinline__ bool count_wait(volatile int* count, int n, volatile int* abort) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, *count >= n)) return true;
+    if ((it & 63u) == 0 && __any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > 2000000000ull))
+      return false;
+  }
+}
+
+__device__ __forceinline__ void fail(Smem& sm, int* status) {
+  sm.abort = 1;
+  flag_status(status, DSA_STATUS_TIMEOUT);
+}
+
+// Tokens and keys of sequence b, empty if its offsets are not inside q and k.
+__device__ __forceinline__ bool sequence(const PromptAttnParams& a, int b, int* q0, int* nq, int* k0, int* nk) {
+  const int qa = a.cu_q ? __ldg(&a.cu_q[b]) : 0, qb = a.cu_q ? __ldg(&a.cu_q[b + 1]) : a.Nq;
+  const int ka = a.cu_k ? __ldg(&a.cu_k[b]) : 0, kb = a.cu_k ? __ldg(&a.cu_k[b + 1]) : a.Nk;
+  const bool good = qa >= 0 && qb >= qa && qb <= a.Nq && ka >= 0 && kb >= ka && kb <= a.Nk;
+  *q0 = good ? qa : 0;
+  *nq = good ? qb - qa : 0;
+  *k0 = good ? ka : 0;
+  *nk = good ? kb - ka : 0;
+  return good;
+}
+
+__device__ __forceinline__ int visible(int tok, int nq, int nk) {  // keys that a token sees
+  const long long v = (long long)tok + 1 + nk - nq;
+  return v < 0 ? 0 : (int)(v > nk ? nk : v);
+}
+
+__device__ __forceinline__ long long scan_add(long long v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// The sequence that item `at` belongs to, found from the last one on.
+struct Finder {
+  int b0 = 0;             // a group of 32 sequences
+  long long base = 0;     // items before it
+  long long mine = 0, end = 0;  // of this lane's sequence: items, where they end
+  int q0 = 0, nq = 0, k0 = 0, nk = 0;
+  __device__ __forceinline__ void load(const Geo& g, int lane) {
+    const int b = b0 + lane;
+    mine = 0;
+    if (b < g.a.B) {
+      if (!sequence(g.a, b, &q0, &nq, &k0, &nk)) flag_status(g.a.status, DSA_STATUS_BAD_LENGTH);
+      const int per = 2 * kTile >> g.lgp;
+      mine = (long long)((nq + (long long)per - 1) / per) * g.HH;
+    }
+    end = base + scan_add(mine, lane);
+  }
+  __device__ bool find(const Geo& g, long long at, int lane, Item* it) {
+    for (;;) {
+      const unsigned hit = __ballot_sync(0xffffffffu, end > at);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        const long long first = __shfl_sync(0xffffffffu, end - mine, l);
+        const int items = (int)(__shfl_sync(0xffffffffu, mine, l) / g.HH);
+        const int sq0 = __shfl_sync(0xffffffffu, q0, l), snq = __shfl_sync(0xffffffffu, nq, l);
+        const int sk0 = __shfl_sync(0xffffffffu, k0, l), snk = __shfl_sync(0xffffffffu, nk, l);
+        const long long r = at - first;
+        const int pair = (int)(r / g.HH);
+        int x = (int)(r - (long long)pair * g.HH);
+        const int vh = x % g.VH;
+        x /= g.VH;
+        const int hb = x % g.HB;
+        it->end = 0;
+        it->hk = x / g.HB;
+        it->h0 = it->hk * g.G + (hb << g.lgp);
+        const int per = kTile >> g.lgp;
+        it->tok = (items - 1 - pair) * 2 * per;  // late tokens first
+        it->q0 = sq0 + it->tok;
+        it->nq = snq;
+        it->nk = snk;
+        it->k0 = sk0;
+        it->v0 = vh * kVWidth;
+        it->dv = min(g.a.Dv - it->v0, kVWidth);
+        it->lim = visible(it->tok, snq, snk);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int first_tok = it->tok + t * per;
+          const int last = min(first_tok + per, snq) - 1;
+          it->n[t] = first_tok < snq ? (visible(last, snq, snk) + kTile - 1) / kTile : 0;
+        }
+        return true;
+      }
+      base = __shfl_sync(0xffffffffu, end, 31);
+      b0 += 32;
+      if (b0 >= g.a.B) return false;
+      load(g, lane);
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_prompt_attn(const __grid_constant__ Maps maps, const __grid_constant__ Geo g) {
+  extern __shared__ uint8_t smraw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  const PromptAttnParams& a = g.a;
+  const uint32_t qsm = smem_u32(base);                              // [2][nkc] chunks
+  const uint32_t rsm = qsm + 2 * g.nkc * kChunkBytes;               // [ring] chunks
+  uint8_t* rptr = base + 2 * g.nkc * kChunkBytes;
+  Smem& sm = *reinterpret_cast<Smem*>(rptr + g.ring * kChunkBytes);
+  const int lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5);
+  launch_dependents();
+  if (threadIdx.x == 0) {
+    sm.abort = sm.vissued = 0;
+    sm.fills = sm.qfills[0] = sm.qfills[1] = 0;
+    for (int i = 0; i < g.ring; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.qfull[i], 1);
+      mbar_init(&sm.qempty[i], 1);
+      mbar_init(&sm.sfull[i], 1);
+      mbar_init(&sm.pfull[i], 4);
+      mbar_init(&sm.ofull[i], 1);
+    }
+    mbar_init(&sm.vclean, 2);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sm.ifull[i], 1);
+      mbar_init(&sm.iempty[i], kReaders);
+    }
+    for (int i = 0; i < 4 * kSlots; ++i) sm.odd[i / (2 * kSlots)][i % (2 * kSlots)] = 0;
+    mbar_init(&sm.done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&sm.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
+  grid_dependency_wait();
+
+  const int per = kTile >> g.lgp;  // tokens of a tile
+  const int nkc = g.nkc;
+  // The next item's descriptor, for every warp but the producer's.
+  int islot = 0;
+  uint32_t iphase = 0;
+  auto next_item = [&](Item& it) -> bool {
+    if (!pair_wait(smem_u32(&sm.ifull[islot]), iphase, &sm.abort)) {
+      if (lane == 0) fail(sm, a.status);
+      return false;
+    }
+    it = sm.item[islot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.iempty[islot]);
+    if (++islot == kSlots) {
+      islot = 0;
+      iphase ^= 1;
+    }
+    return uniform(it.end) == 0;
+  };
+
+  if (warp >= 8) {
+    if (warp == 8) {
+      // --------------------------------------------------------- producer --
+      Finder f;
+      f.load(g, lane);
+      int rs = 0;
+      uint32_t rphase = 1;  // an empty ring's barriers have completed "phase 1"
+      int nfill = 0, nv = 0, nq[2] = {0, 0};
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(g.next, 1);
+        at = uniform(at);
+        Item it;
+        const bool have = f.find(g, at, lane, &it);
+        it.end = have ? 0 : 1;
+        const int s = k % kSlots;
+        if (!pair_wait(smem_u32(&sm.iempty[s]), ((k / kSlots) & 1) ^ 1, &sm.abort)) { ok = false; break; }
+        if (lane == 0) {
+          sm.item[s] = it;
+          mbar_arrive(&sm.ifull[s]);
+        }
+        __syncwarp();
+        if (!have) break;
+        const int N = max(it.n[0], it.n[1]);
+        const int nvc = (it.dv + kChunk - 1) / kChunk;
+        auto fill = [&](const CUtensorMap* map, int x, int y, int z) {
+          if (!pair_wait(smem_u32(&sm.empty[rs]), rphase, &sm.abort)) return false;
+          const uint32_t bar = smem_u32(&sm.full[rs]);
+          expect_elected(bar, kChunkBytes);
+          tma_3d(rsm + rs * kChunkBytes, map, bar, x, y, z);
+          ++nfill;
+          if (++rs == g.ring) {
+            rs = 0;
+            rphase ^= 1;
+          }
+          return true;
+        };
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (it.n[t] == 0) continue;
+          if (!pair_wait(smem_u32(&sm.qempty[t]), (nq[t] & 1) ^ 1, &sm.abort)) { ok = false; break; }
+          const uint32_t bar = smem_u32(&sm.qfull[t]);
+          expect_elected(bar, nkc * kChunkBytes);
+          for (int c = 0; c < nkc; ++c)
+            tma_3d(qsm + (t * nkc + c) * kChunkBytes, &maps.q, bar, kChunk * c, it.h0, it.q0 + t * per);
+          ++nq[t];
+        }
+        for (int j = 0; j < N && ok; ++j) {
+          for (int c = 0; c < nkc && ok; ++c) ok = fill(&maps.k, kChunk * c, it.hk, it.k0 + kTile * j);
+          for (int c = 0; c < nvc && ok; ++c) ok = fill(&maps.v, it.v0 + kChunk * c, it.hk, it.k0 + kTile * j);
+          if (j >= it.lim / kTile) {
+            ++nv;
+            __syncwarp();
+            if (lane == 0) *(volatile int*)&sm.vissued = nv;
+          }
+        }
+      }
+      if (lane == 0) {
+        sm.fills = nfill;
+        sm.qfills[0] = nq[0];
+        sm.qfills[1] = nq[1];
+        if (!ok) fail(sm, a.status);
+      }
+    } else if (warp == 9) {
+      // ----------------------------------------------------------- issuer --
+      const uint32_t id_s = instr_desc(128, 128, 1, 1, 0, 0);
+      const uint64_t dq = smem_desc(qsm, 16, 1024, kSwizzle128B);
+      const uint64_t dk = smem_desc(rsm, 16, 1024, kSwizzle128B);
+      const uint64_t dv = smem_desc(rsm, kChunkBytes, 1024, kSwizzle128B);  // blocks of 64 columns, chunk after chunk
+      constexpr int kStep = kChunkBytes / 16;  // a chunk, in descriptor units
+      int rs = 0;          // the ring's next chunk
+      uint32_t rphase = 0;
+      auto advance = [&](int n) {
+        rs += n;
+        if (rs >= g.ring) {
+          rs -= g.ring;
+          rphase ^= 1;
+        }
+      };
+      uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0}, vphase = 0;
+      bool ok = true;
+      Item it;
+      while (ok && next_item(it)) {
+        const int N = max(it.n[0], it.n[1]);
+        const int nvc = (it.dv + kChunk - 1) / kChunk;
+        const bool brief = it.lim <= kShort;
+        const int jm = it.lim / kTile;  // from this tile on V is looked through
+        int vs = 0;                     // first chunk of V of the tile before
+        uint32_t vturn = 0;             // ... and its phase
+        for (int j = 0; j <= N && ok; ++j) {
+          // chunks of this tile's K and V are rs .. rs + nkc + nvc - 1
+          bool kready = false, vready = j == 0;
+          const int ks = rs;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (j > 0 && j - 1 < it.n[t]) {  // O_X += P_X V of the tile before
+              if (!vready) {
+                for (int c = 0; c < nvc && ok; ++c) {
+                  const int s = vs + c;
+                  const bool wrap = s >= g.ring;
+                  ok = pair_wait(smem_u32(&sm.full[wrap ? s - g.ring : s]), wrap ? vturn ^ 1 : vturn, &sm.abort);
+                }
+                if (ok && j - 1 >= jm) {
+                  ok = pair_wait(smem_u32(&sm.vclean), vphase, &sm.abort);
+                  vphase ^= 1;
+                }
+                vready = true;
+                if (!ok) break;
+              }
+              if (!pair_wait(smem_u32(&sm.pfull[t]), pphase[t], &sm.abort)) { ok = false; break; }
+              pphase[t] ^= 1;
+              tc_fence_after();
+              const uint32_t d = tbase + kColO + 128 * t, p = tbase + kColS + 128 * t;
+              const bool split = vs + nvc > g.ring;  // the two chunks lie at the ring's ends
+              for (int part = 0; part < (split ? 2 : 1); ++part) {
+                const int s = part ? 0 : vs;
+                const int cols = split ? kChunk : kChunk * nvc;
+                const uint32_t id = instr_desc(128, cols, 1, 1, 0, 1);
+                const uint64_t vb = dv + (uint64_t)(kStep * s);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  mma_ts(d + kChunk * part, p + 8 * k, vb + 128 * k, id, (j > 1 || k > 0) ? 1 : 0);
+                if (brief) {
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) mma_ts(d + kChunk * part, p + 64 + 8 * k, vb + 128 * k, id, 1);
+                }
+              }
+              if (j == it.n[t]) commit_elected(smem_u32(&sm.ofull[t]));
+            }
+            if (j < it.n[t]) {  // S_X of this tile
+              if (j == 0) {
+                if (!pair_wait(smem_u32(&sm.qfull[t]), qphase[t], &sm.abort)) { ok = false; break; }
+                qphase[t] ^= 1;
+              }
+              uint64_t qa = dq + (uint64_t)(kStep * nkc * t);
+              for (int c = 0; c < nkc && ok; ++c, qa += kStep) {
+                int s = ks + c;
+                const bool wrap = s >= g.ring;
+                if (wrap) s -= g.ring;
+                if (!kready) {
+                  ok = pair_wait(smem_u32(&sm.full[s]), wrap ? rphase ^ 1 : rphase, &sm.abort);
+                  if (!ok) break;
+                }
+                tc_fence_after();
+                const uint64_t kb = dk + (uint64_t)(kStep * s);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_ss(tbase + kColS + 128 * t, qa + 2 * k, kb + 2 * k, id_s, (c > 0 || k > 0) ? 1 : 0);
+              }
+              if (!ok) break;
+              kready = true;
+              commit_elected(smem_u32(&sm.sfull[t]));
+              if (j + 1 == it.n[t]) commit_elected(smem_u32(&sm.qempty[t]));
+            }
+          }
+          if (!ok) break;
+          if (j > 0)  // V of the tile before is done with
+            for (int c = 0; c < nvc; ++c) {
+              const int s = vs + c;
+              commit_elected(smem_u32(&sm.empty[s >= g.ring ? s - g.ring : s]));
+            }
+          if (j < N) {
+            for (int c = 0; c < nkc; ++c) {
+              const int s = ks + c;
+              commit_elected(smem_u32(&sm.empty[s >= g.ring ? s - g.ring : s]));
+            }
+            advance(nkc);
+            vs = rs;
+            vturn = rphase;
+            advance(nvc);
+          }
+        }
+      }
+      if (!ok && lane == 0) fail(sm, a.status);
+      commit_elected(smem_u32(&sm.done));
+    } else {
+      // ------------------------------------------------ V of partial tiles --
+      int rs = 0, k = 0, nv = 0;
+      uint32_t rphase = 0;
+      bool ok = true;
+      Item it;
+      while (ok && next_item(it)) {
+        const int N = max(it.n[0], it.n[1]);
+        const int nvc = (it.dv + kChunk - 1) / kChunk;
+        const int jm = it.lim / kTile;
+        int* odds = sm.odd[warp - 10];
+        const int slot = k % (2 * kSlots);
+        ++k;
+        // Cleared two items ahead of its use.  It was item k - 6's: every warp
+        // has read descriptor k - 4, so every softmax warp is done with k - 5.
+        if (lane == 0) odds[(slot + 2) % (2 * kSlots)] = 0;
+        auto step = [&] {
+          if (++rs == g.ring) {
+            rs = 0;
+            rphase ^= 1;
+          }
+        };
+        const int seen = visible(min(it.tok + 2 * per, it.nq) - 1, it.nq, it.nk);
+        for (int j = 0; j < N && ok; ++j) {
+          for (int c = 0; c < nkc; ++c) step();
+          bool odd = false;
+          // the copies of this lap of the ring are under way: only then does a
+          // chunk's barrier tell this lap's completion from one before
+          if (j >= jm && !count_wait(&sm.vissued, ++nv, &sm.abort)) { ok = false; break; }
+          for (int c = 0; c < nvc && ok; ++c, step()) {
+            if (j < jm) continue;
+            if (!pair_wait(smem_u32(&sm.full[rs]), rphase, &sm.abort)) { ok = false; break; }
+            uint4* chunk = reinterpret_cast<uint4*>(rptr + rs * kChunkBytes);
+            const int rows = min(seen - kTile * j, kTile);  // of the tile that some row sees
+            // warp 10 takes even groups of four rows, warp 11 odd ones
+#pragma unroll 4
+            for (int i = warp - 10; i < kTile / 4; i += 2) {
+              uint4* x = chunk + 32 * i + lane;  // 8 lanes a row of 128 bytes
+              const int row = 4 * i + (lane >> 3);
+              if (row >= rows) {
+                *x = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              const uint4 v = *x;
+              auto bad = [](uint32_t w) {  // an exponent of all ones, in either half
+                const uint32_t e = w & 0x7f807f80u;
+                return ((e & 0x7f80u) == 0x7f80u) | ((e >> 16) == 0x7f80u);
+              };
+              if (bad(v.x) | bad(v.y) | bad(v.z) | bad(v.w)) {
+                odd = true;
+                auto scrub = [](uint32_t w) {
+                  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+                  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+                  return w;
+                };
+                *x = make_uint4(scrub(v.x), scrub(v.y), scrub(v.z), scrub(v.w));
+              }
+            }
+          }
+          if (!ok) break;
+          if (j >= jm) {
+            if (odd) odds[slot] = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.vclean);
+          }
+        }
+      }
+      if (!ok && lane == 0) fail(sm, a.status);
+    }
+  } else {
+    // ------------------------------------------------------------- softmax --
+    const int t = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tbase + lanes + kColS + 128 * t, to = tbase + lanes + kColO + 128 * t;
+    const float c = a.scale_log2;
+    uint32_t sphase = 0, ophase = 0;
+    bool ok = true;
+    int k = 0;
+    Item it;
+    while (ok && next_item(it)) {
+      const int slot = k % (2 * kSlots);
+      ++k;
+      const int tok = it.tok + t * per + (row >> g.lgp);
+      const int lim = tok < it.nq ? visible(tok, it.nq, it.nk) : 0;
+      const bool brief = it.lim <= kShort;
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < it.n[t]; ++j) {
+        if (!pair_wait(smem_u32(&sm.sfull[t]), sphase, &sm.abort)) { ok = false; break; }
+        sphase ^= 1;
+        tc_fence_after();
+        uint32_t z[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld_32cols(ts + 32 * q, z[q]);
+        tmem_wait_ld();
+        const int see = lim - kTile * j;  // columns that this row sees
+        if (__any_sync(0xffffffffu, see < kTile)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * q + i >= see) z[q][i] = 0xff800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(z[q][i]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        float f = 1.0f;
+        bool resc = false;
+        if (mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY)) {
+          if (m > -INFINITY) {
+            f = exp2f(m - mt);
+            resc = true;
+          }
+          m = mt;
+        }
+        const float mm = m == -INFINITY ? 0.0f : m;
+        if (__any_sync(0xffffffffu, resc)) {
+          // (S of this tile came after O of the one before)
+          l *= f;
+#pragma unroll 1
+          for (int q = 0; 32 * q < it.dv; ++q) {
+            uint32_t v[32];
+            tmem_ld_32cols(to + 32 * q, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+            tmem_st_32cols(to + 32 * q, v);
+          }
+        }
+        float ls[4] = {l, 0.0f, 0.0f, 0.0f};
+        if (!brief) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float e0 = ex2_approx(fmaf(__uint_as_float(z[q][2 * i]), c, -mm));
+              const float e1 = ex2_approx(fmaf(__uint_as_float(z[q][2 * i + 1]), c, -mm));
+              ls[(2 * i) & 3] += e0;
+              ls[(2 * i + 1) & 3] += e1;
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+              pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            tmem_st_16cols(ts + 16 * q, pk);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float e0 = ex2_approx(fmaf(__uint_as_float(z[q][2 * i]), c, -mm));
+              const float e1 = ex2_approx(fmaf(__uint_as_float(z[q][2 * i + 1]), c, -mm));
+              ls[(2 * i) & 3] += e0;
+              ls[(2 * i + 1) & 3] += e1;
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
+              const float2 h = __bfloat1622float2(h2);
+              const __nv_bfloat162 l2 = __floats2bfloat162_rn(e0 - h.x, e1 - h.y);
+              hi[i] = *reinterpret_cast<const uint32_t*>(&h2);
+              lo[i] = *reinterpret_cast<const uint32_t*>(&l2);
+            }
+            tmem_st_16cols(ts + 16 * q, hi);
+            tmem_st_16cols(ts + 64 + 16 * q, lo);
+          }
+        }
+        l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.pfull[t]);
+      }
+      if (!ok) break;
+      // ---- O out of TMEM
+      const bool any = it.n[t] > 0;
+      if (any) {
+        if (!pair_wait(smem_u32(&sm.ofull[t]), ophase, &sm.abort)) { ok = false; break; }
+        ophase ^= 1;
+        tc_fence_after();
+      }
+      const bool mine = tok < it.nq;
+      const int head = it.h0 + (row & ((1 << g.lgp) - 1));
+      const long long tr = (long long)it.q0 + t * per + (row >> g.lgp);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const bool odd = (sm.odd[0][slot] | sm.odd[1][slot]) != 0;
+      __nv_bfloat16* out = a.out + tr * a.o_ts + (long long)head * a.o_hs + it.v0;
+#pragma unroll 1
+      for (int q = 0; 32 * q < it.dv; ++q) {
+        uint32_t v[32];
+        if (any) {
+          tmem_ld_32cols(to + 32 * q, v);
+          tmem_wait_ld();
+        }
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = any ? __uint_as_float(v[i]) * inv : 0.0f;
+        if (odd && mine) {
+          // infinities and NaN that were kept out of the products
+          for (int p = it.lim / kTile * kTile; p < lim; ++p) {
+            const __nv_bfloat16* vr = a.v + (long long)(it.k0 + p) * a.v_ts + (long long)it.hk * a.v_hs + it.v0;
+            for (int i = 0; i < 32; ++i)
+              if (32 * q + i < it.dv) {
+                const float y = __bfloat162float(vr[32 * q + i]);
+                if (!isfinite(y)) x[i] += y;
+              }
+          }
+        }
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (32 * q + 8 * i >= it.dv) break;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[8 * i + 2 * e], x[8 * i + 2 * e + 1]);
+              w[e] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            *reinterpret_cast<uint4*>(out + 32 * q + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (mine && a.lse && it.v0 == 0)
+        a.lse[tr * a.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+    if (!ok && lane == 0) fail(sm, a.status);
+  }
+
+  __syncthreads();
+  if (warp == 0) {
+    int never = 0;
+    pair_wait(smem_u32(&sm.done), 0, &never, 100000000ull);  // the products are done
+    if (sm.abort) {  // and, after a failure, the copies in flight
+      for (int i = 0; i < g.ring; ++i) {
+        const int n = (sm.fills - i + g.ring - 1) / g.ring;
+        if (n > 0) pair_wait(smem_u32(&sm.full[i]), (n - 1) & 1, &never, 10000000ull);
+      }
+      for (int t = 0; t < 2; ++t)
+        if (sm.qfills[t] > 0) pair_wait(smem_u32(&sm.qfull[t]), (sm.qfills[t] - 1) & 1, &never, 10000000ull);
+    }
+    if (lane == 0) {  // the last CTA leaves both counters at zero for the next call
+      __threadfence();
+      if (atomicAdd(g.left, 1) == (int)gridDim.x - 1) {
+        *g.next = 0;
+        *g.left = 0;
+        __threadfence();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kTmemCols);
+  }
+}
+
+int ring_of(int nkc) {
+  const int room = 227 * 1024 - 1024 - (int)sizeof(Smem) - 2 * nkc * kChunkBytes;
+  return std::min(kMaxRing, room / kChunkBytes);
+}
+
+}  // namespace
+
+size_t prompt_attn_ws() { return kWsHeader; }
+
+int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
+  Geo g{};
+  g.a = p;
+  g.G = p.Hq / p.Hk;
+  while (g.lgp < 7 && g.G % (2 << g.lgp) == 0) ++g.lgp;
+  g.HB = g.G >> g.lgp;
+  g.VH = (p.Dv + kVWidth - 1) / kVWidth;
+  g.HH = p.Hk * g.HB * g.VH;
+  g.nkc = (p.Dk + kChunk - 1) / kChunk;
+  g.ring = ring_of(g.nkc);
+  g.next = reinterpret_cast<int*>(ws) + 16;
+  g.left = reinterpret_cast<int*>(ws) + 32;
+  const int per = 2 * kTile >> g.lgp;
+  const long long bound = ((long long)p.Nq / per + p.B) * g.HH;
+  if (bound > 0x7fff0000LL)
+    return set_error(DSA_ERR_UNSUPPORTED, "prompt_attn: rows beyond 2^31 pairs of tiles of 128");
+  Maps m{};
+  int rc = make_tmap_heads(&m.q, p.q, p.Dk, p.Hq, p.Nq, p.q_hs, p.q_ts, kChunk, 1u << g.lgp, kTile >> g.lgp);
+  // no keys at all: nothing is loaded, the maps only have to exist
+  const void *k = p.Nk > 0 ? p.k : p.q, *v = p.Nk > 0 ? p.v : p.q;
+  if (!rc) rc = make_tmap_heads(&m.k, k, p.Dk, p.Hk, p.Nk, p.k_hs, p.k_ts, kChunk, 1, kTile);
+  if (!rc) rc = make_tmap_heads(&m.v, v, p.Dv, p.Hk, p.Nk, p.v_hs, p.v_ts, kChunk, 1, kTile);
+  if (rc) return rc;
+  const int smem = 1024 + (2 * g.nkc + g.ring) * kChunkBytes + (int)sizeof(Smem);
+  rc = ensure_dynamic_smem((const void*)k_prompt_attn, smem, "prompt_attn");
+  if (rc) return rc;
+  const int ctas = (int)std::min<long long>(sm_count(), bound);
+  const cudaError_t e = launch_pdl(k_prompt_attn, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, s, m, g);
+  count_launch();
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
+  return check_launch("prompt_attn");
+}
+
+}  // namespace dsa

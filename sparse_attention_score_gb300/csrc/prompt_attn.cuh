@@ -1,0 +1,25 @@
+// prompt_attn.cuh -- parameter block of the packed prompt attention.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "dsa_internal.cuh"
+
+namespace dsa {
+
+struct PromptAttnParams {
+  const __nv_bfloat16 *q, *k, *v;  // [tokens][heads][dim] with strides in elements
+  long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;
+  const int32_t *cu_q, *cu_k;  // [B + 1] or NULL (one sequence)
+  int B, Nq, Nk, Hq, Hk, Dk, Dv;
+  float scale_log2;
+  __nv_bfloat16* out;
+  long long o_ts, o_hs;
+  float* lse;  // [Nq][Hq] or NULL
+  int* status;
+};
+size_t prompt_attn_ws();
+int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s);
+
+}  // namespace dsa
