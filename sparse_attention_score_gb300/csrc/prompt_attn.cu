@@ -84,10 +84,11 @@ struct Item {
 struct Smem {
   uint64_t full[kMaxRing], empty[kMaxRing];
   uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2];
-  uint64_t vclean, ifull[kSlots], iempty[kSlots], done;
+  uint64_t ifull[kSlots], iempty[kSlots], done;
   Item item[kSlots];
   int odd[2][2 * kSlots];  // per reader of V: the item's V held infinities or NaN
-  int vissued;       // V tiles to look through whose copies were issued
+  int vissued;       // V tiles to look through: whose copies were issued,
+  int vclean[2];     // ... which each of the two warps is done with
   int fills, qfills[2];
   uint32_t tmem_base;
   int abort;
@@ -162,15 +163,61 @@ __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t* r
       : "memory");
 }
 
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair2(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split2(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Scores of columns 32 q .. 32 q + 31 that lie at or behind `see` are hidden.
+__device__ __forceinline__ void hide(uint32_t (&z)[32], int q, int see) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (32 * q + i >= see) z[i] = 0xff800000u;
+}
+
 // Wait of a whole warp until *count (in shared memory, only growing) is at
 // least n; bounded like pair_wait.
-__device__ __forceinline__ bool count_wait(volatile int* count, int n, volatile int* abort) {
+__device__ __forceinline__ bool count_wait(const int* count, int n, volatile int* abort) {
+  const uint32_t addr = smem_u32(count);
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (__all_sync(0xffffffffu, *count >= n)) return true;
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    if (__all_sync(0xffffffffu, v >= n)) return true;
     if ((it & 63u) == 0 && __any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > 2000000000ull))
       return false;
   }
+}
+
+__device__ __forceinline__ void count_set(int* count, int n) {
+  asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(count)), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ void fail(Smem& sm, int* status) {
@@ -276,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5);
   launch_dependents();
   if (threadIdx.x == 0) {
-    sm.abort = sm.vissued = 0;
+    sm.abort = sm.vissued = sm.vclean[0] = sm.vclean[1] = 0;
     sm.fills = sm.qfills[0] = sm.qfills[1] = 0;
     for (int i = 0; i < g.ring; ++i) {
       mbar_init(&sm.full[i], 1);
@@ -289,7 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.pfull[i], 4);
       mbar_init(&sm.ofull[i], 1);
     }
-    mbar_init(&sm.vclean, 2);
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sm.ifull[i], 1);
       mbar_init(&sm.iempty[i], kReaders);
@@ -386,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j >= it.lim / kTile) {
             ++nv;
             __syncwarp();
-            if (lane == 0) *(volatile int*)&sm.vissued = nv;
+            if (lane == 0) count_set(&sm.vissued, nv);
           }
         }
       }
@@ -412,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           rphase ^= 1;
         }
       };
-      uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0}, vphase = 0;
+      uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0};
+      int nclean = 0;
       bool ok = true;
       Item it;
       while (ok && next_item(it)) {
@@ -435,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   ok = pair_wait(smem_u32(&sm.full[wrap ? s - g.ring : s]), wrap ? vturn ^ 1 : vturn, &sm.abort);
                 }
                 if (ok && j - 1 >= jm) {
-                  ok = pair_wait(smem_u32(&sm.vclean), vphase, &sm.abort);
-                  vphase ^= 1;
+                  ++nclean;
+                  ok = count_wait(&sm.vclean[0], nclean, &sm.abort) && count_wait(&sm.vclean[1], nclean, &sm.abort);
                 }
                 vready = true;
                 if (!ok) break;
@@ -571,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (odd) odds[slot] = 1;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.vclean);
+            if (lane == 0) count_set(&sm.vclean[warp - 10], nv);
           }
         }
       }
@@ -594,29 +641,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = it.tok + t * per + (row >> g.lgp);
       const int lim = tok < it.nq ? visible(tok, it.nq, it.nk) : 0;
       const bool brief = it.lim <= kShort;
+      const int n = t ? it.n[1] : it.n[0];
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < it.n[t]; ++j) {
+      for (int j = 0; j < n; ++j) {
         if (!pair_wait(smem_u32(&sm.sfull[t]), sphase, &sm.abort)) { ok = false; break; }
         sphase ^= 1;
         tc_fence_after();
-        uint32_t z[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld_32cols(ts + 32 * q, z[q]);
-        tmem_wait_ld();
         const int see = lim - kTile * j;  // columns that this row sees
-        if (__any_sync(0xffffffffu, see < kTile)) {
+        const bool part = __any_sync(0xffffffffu, see < kTile);
+        // Two passes over the scores in TMEM: all 128 of a row in registers at
+        // once would leave none for the rest.
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; q += 2) {
+          uint32_t z[2][32];
+          tmem_ld_32cols(ts + 32 * q, z[0]);
+          tmem_ld_32cols(ts + 32 * q + 32, z[1]);
+          tmem_wait_ld();
+          if (part) {
+            hide(z[0], q, see);
+            hide(z[1], q + 1, see);
+          }
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * q + i >= see) z[q][i] = 0xff800000u;
+          for (int i = 0; i < 32; i += 2)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              mx[e] = max3(mx[e], __uint_as_float(z[e][i]), __uint_as_float(z[e][i + 1]));
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(z[q][i]));
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const float mt = fmaxf(mx[0], mx[1]) * c;
         float f = 1.0f;
         bool resc = false;
         if (mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY)) {
@@ -640,43 +692,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_32cols(to + 32 * q, v);
           }
         }
-        float ls[4] = {l, 0.0f, 0.0f, 0.0f};
+        const uint64_t c2 = pair2(c, c), mm2 = pair2(-mm, -mm);
+        uint64_t sum[2] = {pair2(l, 0.0f), pair2(0.0f, 0.0f)};
         if (!brief) {
+          uint32_t z[2][32];
+          tmem_ld_32cols(ts, z[0]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
+            tmem_wait_ld();
+            if (q < 3) tmem_ld_32cols(ts + 32 * q + 32, z[(q + 1) & 1]);
+            uint32_t(&y)[32] = z[q & 1];
+            if (part) hide(y, q, see);
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float e0 = ex2_approx(fmaf(__uint_as_float(z[q][2 * i]), c, -mm));
-              const float e1 = ex2_approx(fmaf(__uint_as_float(z[q][2 * i + 1]), c, -mm));
-              ls[(2 * i) & 3] += e0;
-              ls[(2 * i + 1) & 3] += e1;
+              const float2 x = split2(fma2(pair2(y[2 * i], y[2 * i + 1]), c2, mm2));
+              const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
+              sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
               pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
             }
             tmem_st_16cols(ts + 16 * q, pk);
           }
         } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t hi[16], lo[16];
+          // hi in the first 64 columns, lo in the others: the second half's
+          // scores are read before the first half's lo is written over them
+          uint32_t hi[4][16], lo[4][16];
+          auto weigh = [&](int q) {
+            uint32_t y[32];
+            tmem_ld_32cols(ts + 32 * q, y);
+            tmem_wait_ld();
+            if (part) hide(y, q, see);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float e0 = ex2_approx(fmaf(__uint_as_float(z[q][2 * i]), c, -mm));
-              const float e1 = ex2_approx(fmaf(__uint_as_float(z[q][2 * i + 1]), c, -mm));
-              ls[(2 * i) & 3] += e0;
-              ls[(2 * i + 1) & 3] += e1;
+              const float2 x = split2(fma2(pair2(y[2 * i], y[2 * i + 1]), c2, mm2));
+              const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
+              sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
               const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
               const float2 h = __bfloat1622float2(h2);
               const __nv_bfloat162 l2 = __floats2bfloat162_rn(e0 - h.x, e1 - h.y);
-              hi[i] = *reinterpret_cast<const uint32_t*>(&h2);
-              lo[i] = *reinterpret_cast<const uint32_t*>(&l2);
+              hi[q][i] = *reinterpret_cast<const uint32_t*>(&h2);
+              lo[q][i] = *reinterpret_cast<const uint32_t*>(&l2);
             }
-            tmem_st_16cols(ts + 16 * q, hi);
-            tmem_st_16cols(ts + 64 + 16 * q, lo);
-          }
+          };
+          weigh(2);
+          weigh(3);
+          tmem_st_16cols(ts + 96, lo[2]);
+          tmem_st_16cols(ts + 112, lo[3]);
+          weigh(0);
+          tmem_st_16cols(ts, hi[0]);
+          tmem_st_16cols(ts + 64, lo[0]);
+          weigh(1);
+          tmem_st_16cols(ts + 16, hi[1]);
+          tmem_st_16cols(ts + 32, hi[2]);
+          tmem_st_16cols(ts + 48, hi[3]);
+          tmem_st_16cols(ts + 80, lo[1]);
         }
-        l = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        const float2 s0 = split2(add2(sum[0], sum[1]));
+        l = s0.x + s0.y;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -684,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- O out of TMEM
-      const bool any = it.n[t] > 0;
+      const bool any = n > 0;
       if (any) {
         if (!pair_wait(smem_u32(&sm.ofull[t]), ophase, &sm.abort)) { ok = false; break; }
         ophase ^= 1;
