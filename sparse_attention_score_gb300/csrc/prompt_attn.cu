@@ -376,6 +376,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       islot = 0;
       iphase ^= 1;
     }
+    // known to be the same in every lane: descriptors and coordinates made from
+    // these stay in uniform registers, and an MMA is one instruction (without it
+    // the 32 MMAs of a key tile took ~4,500 cycles to issue, now under 2,048)
+    it.dv = uniform(it.dv);
+    it.n[0] = uniform(it.n[0]);
+    it.n[1] = uniform(it.n[1]);
+    it.lim = uniform(it.lim);
     return uniform(it.end) == 0;
   };
 
@@ -417,7 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        for (int t = 0; t < 2 && ok; ++t) {
+        _Pragma("unroll")
+          for (int t = 0; t < 2; ++t) {
+            if (!ok) break;
           if (it.n[t] == 0) continue;
           if (!pair_wait(smem_u32(&sm.qempty[t]), (nq[t] & 1) ^ 1, &sm.abort)) { ok = false; break; }
           const uint32_t bar = smem_u32(&sm.qfull[t]);
@@ -473,7 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // chunks of this tile's K and V are rs .. rs + nkc + nvc - 1
           bool kready = false, vready = j == 0;
           const int ks = rs;
-          for (int t = 0; t < 2 && ok; ++t) {
+          _Pragma("unroll")
+          for (int t = 0; t < 2; ++t) {
+            if (!ok) break;
             if (j > 0 && j - 1 < it.n[t]) {  // O_X += P_X V of the tile before
               if (!vready) {
                 for (int c = 0; c < nvc && ok; ++c) {
@@ -498,12 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int cols = split ? kChunk : kChunk * nvc;
                 const uint32_t id = instr_desc(128, cols, 1, 1, 0, 1);
                 const uint64_t vb = dv + (uint64_t)(kStep * s);
+                // (bf16 weights: 8 columns of P per 16 keys; hi + lo: 32 columns of
+                // hi and 32 of lo per 64 keys)
+                if (!brief) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  mma_ts(d + kChunk * part, p + 8 * k, vb + 128 * k, id, (j > 1 || k > 0) ? 1 : 0);
-                if (brief) {
+                  for (int k = 0; k < 8; ++k)
+                    mma_ts(d + kChunk * part, p + 8 * k, vb + 128 * k, id, (j > 1 || k > 0) ? 1 : 0);
+                } else {
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) mma_ts(d + kChunk * part, p + 64 + 8 * k, vb + 128 * k, id, 1);
+                  for (int k = 0; k < 8; ++k) {
+                    mma_ts(d + kChunk * part, p + 8 * k + 32 * (k >> 2), vb + 128 * k, id, (j > 1 || k > 0) ? 1 : 0);
+                    mma_ts(d + kChunk * part, p + 8 * k + 32 * (k >> 2) + 32, vb + 128 * k, id, 1);
+                  }
                 }
               }
               if (j == it.n[t]) commit_elected(smem_u32(&sm.ofull[t]));
@@ -649,107 +666,133 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int see = lim - kTile * j;  // columns that this row sees
         const bool part = __any_sync(0xffffffffu, see < kTile);
-        // Two passes over the scores in TMEM: all 128 of a row in registers at
-        // once would leave none for the rest.
-        float mx[2] = {-INFINITY, -INFINITY};
+        const uint64_t c2 = pair2(c, c);
+        uint64_t sum[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
+        // 32 weights of scores z against the reference r2 = (-m, -m)
+        auto weigh = [&](const uint32_t (&z)[32], uint64_t r2, uint32_t* hi) {
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          uint32_t z[2][32];
-          tmem_ld_32cols(ts + 32 * q, z[0]);
-          tmem_ld_32cols(ts + 32 * q + 32, z[1]);
-          tmem_wait_ld();
-          if (part) {
-            hide(z[0], q, see);
-            hide(z[1], q + 1, see);
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = split2(fma2(pair2(z[2 * i], z[2 * i + 1]), c2, r2));
+            const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
+            sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
+            hi[i] = *reinterpret_cast<const uint32_t*>(&b2);
           }
+        };
+        auto top = [](const uint32_t (&z)[32], float x) {
+          float y = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              mx[e] = max3(mx[e], __uint_as_float(z[e][i]), __uint_as_float(z[e][i + 1]));
-        }
-        const float mt = fmaxf(mx[0], mx[1]) * c;
-        float f = 1.0f;
-        bool resc = false;
-        if (mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY)) {
-          if (m > -INFINITY) {
-            f = exp2f(m - mt);
-            resc = true;
+          for (int i = 0; i < 32; i += 4) {
+            x = max3(x, __uint_as_float(z[i]), __uint_as_float(z[i + 1]));
+            y = max3(y, __uint_as_float(z[i + 2]), __uint_as_float(z[i + 3]));
           }
-          m = mt;
-        }
-        const float mm = m == -INFINITY ? 0.0f : m;
-        if (__any_sync(0xffffffffu, resc)) {
-          // (S of this tile came after O of the one before)
-          l *= f;
-#pragma unroll 1
-          for (int q = 0; 32 * q < it.dv; ++q) {
-            uint32_t v[32];
-            tmem_ld_32cols(to + 32 * q, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tmem_st_32cols(to + 32 * q, v);
-          }
-        }
-        const uint64_t c2 = pair2(c, c), mm2 = pair2(-mm, -mm);
-        uint64_t sum[2] = {pair2(l, 0.0f), pair2(0.0f, 0.0f)};
-        if (!brief) {
-          uint32_t z[2][32];
+          return fmaxf(x, y);
+        };
+        bool done = false;
+        if (!brief && j > 0) {
+          // One pass: weights against the reference of the tiles before, kept in
+          // registers until the tile's maximum is known not to pass it by 2^8.
+          const float mm = m == -INFINITY ? 0.0f : m;
+          const uint64_t r2 = pair2(-mm, -mm);
+          float mt = -INFINITY;
+          uint32_t z[2][32], pk[4][16];
           tmem_ld_32cols(ts, z[0]);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             tmem_wait_ld();
             if (q < 3) tmem_ld_32cols(ts + 32 * q + 32, z[(q + 1) & 1]);
-            uint32_t(&y)[32] = z[q & 1];
-            if (part) hide(y, q, see);
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = split2(fma2(pair2(y[2 * i], y[2 * i + 1]), c2, mm2));
-              const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
-              sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
-              pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            tmem_st_16cols(ts + 16 * q, pk);
+            if (part) hide(z[q & 1], q, see);
+            mt = top(z[q & 1], mt);
+            weigh(z[q & 1], r2, pk[q]);
           }
-        } else {
-          // hi in the first 64 columns, lo in the others: the second half's
-          // scores are read before the first half's lo is written over them
-          uint32_t hi[4][16], lo[4][16];
-          auto weigh = [&](int q) {
-            uint32_t y[32];
-            tmem_ld_32cols(ts + 32 * q, y);
-            tmem_wait_ld();
-            if (part) hide(y, q, see);
+          mt *= c;
+          done = !__any_sync(0xffffffffu, mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY));
+          if (done) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = split2(fma2(pair2(y[2 * i], y[2 * i + 1]), c2, mm2));
-              const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
-              sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
-              const float2 h = __bfloat1622float2(h2);
-              const __nv_bfloat162 l2 = __floats2bfloat162_rn(e0 - h.x, e1 - h.y);
-              hi[q][i] = *reinterpret_cast<const uint32_t*>(&h2);
-              lo[q][i] = *reinterpret_cast<const uint32_t*>(&l2);
+            for (int q = 0; q < 4; ++q) tmem_st_16cols(ts + 16 * q, pk[q]);
+          } else {
+            sum[0] = sum[1] = pair2(0.0f, 0.0f);
+          }
+        }
+        if (!done) {
+          // Two passes: the maximum, then the weights.
+          float mt = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t z[32];
+            tmem_ld_32cols(ts + 32 * q, z);
+            tmem_wait_ld();
+            if (part) hide(z, q, see);
+            mt = top(z, mt);
+          }
+          mt *= c;
+          float f = 1.0f;
+          bool resc = false;
+          if (mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY)) {
+            if (m > -INFINITY) {
+              f = exp2f(m - mt);
+              resc = true;
             }
-          };
-          weigh(2);
-          weigh(3);
-          tmem_st_16cols(ts + 96, lo[2]);
-          tmem_st_16cols(ts + 112, lo[3]);
-          weigh(0);
-          tmem_st_16cols(ts, hi[0]);
-          tmem_st_16cols(ts + 64, lo[0]);
-          weigh(1);
-          tmem_st_16cols(ts + 16, hi[1]);
-          tmem_st_16cols(ts + 32, hi[2]);
-          tmem_st_16cols(ts + 48, hi[3]);
-          tmem_st_16cols(ts + 80, lo[1]);
+            m = mt;
+          }
+          const float mm = m == -INFINITY ? 0.0f : m;
+          const uint64_t r2 = pair2(-mm, -mm);
+          if (__any_sync(0xffffffffu, resc)) {
+            // (S of this tile came after O of the one before)
+            l *= f;
+#pragma unroll 1
+            for (int q = 0; 32 * q < it.dv; ++q) {
+              uint32_t v[32];
+              tmem_ld_32cols(to + 32 * q, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+              tmem_st_32cols(to + 32 * q, v);
+            }
+          }
+          if (!brief) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t z[32], pk[16];
+              tmem_ld_32cols(ts + 32 * q, z);
+              tmem_wait_ld();
+              if (part) hide(z, q, see);
+              weigh(z, r2, pk);
+              tmem_st_16cols(ts + 16 * q, pk);
+            }
+          } else {
+            // Halves of 64 scores: bf16 weights over the half's first 32 columns,
+            // what that leaves over the others.
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              uint32_t z[2][32], hi[2][16];
+              tmem_ld_32cols(ts + 64 * h, z[0]);
+              tmem_ld_32cols(ts + 64 * h + 32, z[1]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                if (part) hide(z[q], 2 * h + q, see);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float2 x = split2(fma2(pair2(z[q][2 * i], z[q][2 * i + 1]), c2, r2));
+                  const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
+                  sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
+                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
+                  const float2 hf = __bfloat1622float2(h2);
+                  const __nv_bfloat162 l2 = __floats2bfloat162_rn(e0 - hf.x, e1 - hf.y);
+                  hi[q][i] = *reinterpret_cast<const uint32_t*>(&h2);
+                  z[q][i] = *reinterpret_cast<const uint32_t*>(&l2);
+                }
+              }
+              tmem_st_16cols(ts + 64 * h, hi[0]);
+              tmem_st_16cols(ts + 64 * h + 16, hi[1]);
+              tmem_st_16cols(ts + 64 * h + 32, z[0]);
+              tmem_st_16cols(ts + 64 * h + 48, z[1]);
+            }
+          }
         }
         const float2 s0 = split2(add2(sum[0], sum[1]));
-        l = s0.x + s0.y;
+        l += s0.x + s0.y;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
