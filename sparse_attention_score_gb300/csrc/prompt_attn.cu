@@ -45,6 +45,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "dsa_internal.cuh"
@@ -83,7 +84,7 @@ struct Item {
 
 struct Smem {
   uint64_t full[kMaxRing], empty[kMaxRing];
-  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2][2], ofull[2];
   uint64_t ifull[kSlots], iempty[kSlots], done;
   Item item[kSlots];
   int odd[2][2 * kSlots];  // per reader of V: the item's V held infinities or NaN
@@ -163,6 +164,22 @@ __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t* r
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_8cols(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Two fp32 at a time.
 __device__ __forceinline__ uint64_t pair2(float x, float y) {
   uint64_t r;
@@ -200,6 +217,28 @@ __device__ __forceinline__ void hide(uint32_t (&z)[32], int q, int see) {
 #pragma unroll
   for (int i = 0; i < 32; ++i)
     if (32 * q + i >= see) z[i] = 0xff800000u;
+}
+
+// pair_wait with less code: the warps of a scheduler share an instruction cache
+// that holds little more than the loops below.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok != 0)) return true;
+    if ((it & 63u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xffffffffu, *abort != 0 || now - t0 > 2000000000ull)) return false;
+    }
+  }
 }
 
 // Wait of a whole warp until *count (in shared memory, only growing) is at
@@ -315,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smraw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
   const PromptAttnParams& a = g.a;
-  const uint32_t qsm = smem_u32(base);                              // [2][nkc] chunks
+  const uint32_t qsm = (uint32_t)uniform((int)smem_u32(base));                              // [2][nkc] chunks
   const uint32_t rsm = qsm + 2 * g.nkc * kChunkBytes;               // [ring] chunks
   uint8_t* rptr = base + 2 * g.nkc * kChunkBytes;
   Smem& sm = *reinterpret_cast<Smem*>(rptr + g.ring * kChunkBytes);
@@ -333,7 +372,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.qfull[i], 1);
       mbar_init(&sm.qempty[i], 1);
       mbar_init(&sm.sfull[i], 1);
-      mbar_init(&sm.pfull[i], 4);
+      mbar_init(&sm.pfull[i][0], 4);
+      mbar_init(&sm.pfull[i][1], 4);
       mbar_init(&sm.ofull[i], 1);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -361,29 +401,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int per = kTile >> g.lgp;  // tokens of a tile
   const int nkc = g.nkc;
-  // The next item's descriptor, for every warp but the producer's.
+  // The next item's descriptor, for every warp but the producer's: it may be
+  // read until item_done().
   int islot = 0;
   uint32_t iphase = 0;
-  auto next_item = [&](Item& it) -> bool {
-    if (!pair_wait(smem_u32(&sm.ifull[islot]), iphase, &sm.abort)) {
+  auto wait_item = [&]() -> bool {
+    if (!warp_wait(smem_u32(&sm.ifull[islot]), iphase, &sm.abort)) {
       if (lane == 0) fail(sm, a.status);
       return false;
     }
-    it = sm.item[islot];
+    return uniform(sm.item[islot].end) == 0;
+  };
+  auto item_done = [&] {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.iempty[islot]);
     if (++islot == kSlots) {
       islot = 0;
       iphase ^= 1;
     }
-    // known to be the same in every lane: descriptors and coordinates made from
-    // these stay in uniform registers, and an MMA is one instruction (without it
-    // the 32 MMAs of a key tile took ~4,500 cycles to issue, now under 2,048)
-    it.dv = uniform(it.dv);
-    it.n[0] = uniform(it.n[0]);
-    it.n[1] = uniform(it.n[1]);
-    it.lim = uniform(it.lim);
-    return uniform(it.end) == 0;
+  };
+  // A copy of what the issuer and the readers of V need, known to be the same in
+  // every lane: descriptors made from these stay in uniform registers, and an MMA
+  // is one instruction (without it the 32 MMAs of a key tile took ~4,500 cycles).
+  auto next_item = [&](Item& it) -> bool {
+    if (!wait_item()) return false;
+    const Item& x = sm.item[islot];
+    it.tok = uniform(x.tok);
+    it.nq = uniform(x.nq);
+    it.nk = uniform(x.nk);
+    it.dv = uniform(x.dv);
+    it.n[0] = uniform(x.n[0]);
+    it.n[1] = uniform(x.n[1]);
+    it.lim = uniform(x.lim);
+    item_done();
+    return true;
   };
 
   if (warp >= 8) {
@@ -403,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool have = f.find(g, at, lane, &it);
         it.end = have ? 0 : 1;
         const int s = k % kSlots;
-        if (!pair_wait(smem_u32(&sm.iempty[s]), ((k / kSlots) & 1) ^ 1, &sm.abort)) { ok = false; break; }
+        if (!warp_wait(smem_u32(&sm.iempty[s]), ((k / kSlots) & 1) ^ 1, &sm.abort)) { ok = false; break; }
         if (lane == 0) {
           sm.item[s] = it;
           mbar_arrive(&sm.ifull[s]);
@@ -413,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int N = max(it.n[0], it.n[1]);
         const int nvc = (it.dv + kChunk - 1) / kChunk;
         auto fill = [&](const CUtensorMap* map, int x, int y, int z) {
-          if (!pair_wait(smem_u32(&sm.empty[rs]), rphase, &sm.abort)) return false;
+          if (!warp_wait(smem_u32(&sm.empty[rs]), rphase, &sm.abort)) return false;
           const uint32_t bar = smem_u32(&sm.full[rs]);
           expect_elected(bar, kChunkBytes);
           tma_3d(rsm + rs * kChunkBytes, map, bar, x, y, z);
@@ -428,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < 2; ++t) {
             if (!ok) break;
           if (it.n[t] == 0) continue;
-          if (!pair_wait(smem_u32(&sm.qempty[t]), (nq[t] & 1) ^ 1, &sm.abort)) { ok = false; break; }
+          if (!warp_wait(smem_u32(&sm.qempty[t]), (nq[t] & 1) ^ 1, &sm.abort)) { ok = false; break; }
           const uint32_t bar = smem_u32(&sm.qfull[t]);
           expect_elected(bar, nkc * kChunkBytes);
           for (int c = 0; c < nkc; ++c)
@@ -467,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           rphase ^= 1;
         }
       };
-      uint32_t qphase[2] = {0, 0}, pphase[2] = {0, 0};
+      uint32_t qphase = 0, pphase = 0;  // bit X
       int nclean = 0;
       bool ok = true;
       Item it;
@@ -478,90 +529,93 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int jm = it.lim / kTile;  // from this tile on V is looked through
         int vs = 0;                     // first chunk of V of the tile before
         uint32_t vturn = 0;             // ... and its phase
+        // waits for chunks s .. s + n - 1 of the ring, s being in phase `turn`
+        auto landed = [&](int s, int n, uint32_t turn) {
+          bool all = true;
+#pragma unroll 1
+          for (int c = 0; c < n && all; ++c, ++s) {
+            if (s == g.ring) {
+              s = 0;
+              turn ^= 1;
+            }
+            all = warp_wait(smem_u32(&sm.full[s]), turn, &sm.abort);
+          }
+          return all;
+        };
+        auto release = [&](int s, int n) {
+#pragma unroll 1
+          for (int c = 0; c < n; ++c, ++s) {
+            if (s == g.ring) s = 0;
+            commit_elected(smem_u32(&sm.empty[s]));
+          }
+        };
+#pragma unroll 1
         for (int j = 0; j <= N && ok; ++j) {
-          // chunks of this tile's K and V are rs .. rs + nkc + nvc - 1
-          bool kready = false, vready = j == 0;
-          const int ks = rs;
-          _Pragma("unroll")
+          // this tile's K is chunks rs .. rs + nkc - 1, its V the nvc behind
+          if (j > 0) {
+            ok = landed(vs, nvc, vturn);
+            if (ok && j - 1 >= jm) {
+              ++nclean;
+              ok = count_wait(&sm.vclean[0], nclean, &sm.abort) && count_wait(&sm.vclean[1], nclean, &sm.abort);
+            }
+          }
+          if (!ok) break;
+          bool kready = false;
+#pragma unroll 1
           for (int t = 0; t < 2; ++t) {
-            if (!ok) break;
-            if (j > 0 && j - 1 < it.n[t]) {  // O_X += P_X V of the tile before
-              if (!vready) {
-                for (int c = 0; c < nvc && ok; ++c) {
-                  const int s = vs + c;
-                  const bool wrap = s >= g.ring;
-                  ok = pair_wait(smem_u32(&sm.full[wrap ? s - g.ring : s]), wrap ? vturn ^ 1 : vturn, &sm.abort);
-                }
-                if (ok && j - 1 >= jm) {
-                  ++nclean;
-                  ok = count_wait(&sm.vclean[0], nclean, &sm.abort) && count_wait(&sm.vclean[1], nclean, &sm.abort);
-                }
-                vready = true;
-                if (!ok) break;
-              }
-              if (!pair_wait(smem_u32(&sm.pfull[t]), pphase[t], &sm.abort)) { ok = false; break; }
-              pphase[t] ^= 1;
-              tc_fence_after();
-              const uint32_t d = tbase + kColO + 128 * t, p = tbase + kColS + 128 * t;
+            const int n = t ? it.n[1] : it.n[0];
+            const uint32_t ts = tbase + kColS + 128 * t;
+            if (j > 0 && j - 1 < n) {  // O_X += P_X V of the tile before
+              const uint32_t d = tbase + kColO + 128 * t;
               const bool split = vs + nvc > g.ring;  // the two chunks lie at the ring's ends
-              for (int part = 0; part < (split ? 2 : 1); ++part) {
-                const int s = part ? 0 : vs;
-                const int cols = split ? kChunk : kChunk * nvc;
-                const uint32_t id = instr_desc(128, cols, 1, 1, 0, 1);
-                const uint64_t vb = dv + (uint64_t)(kStep * s);
-                // (bf16 weights: 8 columns of P per 16 keys; hi + lo: 32 columns of
-                // hi and 32 of lo per 64 keys)
-                if (!brief) {
+              const uint32_t id = (uint32_t)uniform((int)instr_desc(128, split ? kChunk : kChunk * nvc, 1, 1, 0, 1));
+#pragma unroll 1
+              for (int h = 1; h >= 0; --h) {  // 64 keys at a time, as their weights are ready
+                if (!warp_wait(smem_u32(&sm.pfull[t][h]), pphase >> t & 1, &sm.abort)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll 1
+                for (int part = 0; part < (split ? 2 : 1); ++part) {
+                  const uint64_t vb = dv + (uint64_t)(uint32_t)uniform(kStep * (part ? 0 : vs) + 512 * h);
+                  const uint32_t p = ts + 64 * h;
 #pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    mma_ts(d + kChunk * part, p + 8 * k, vb + 128 * k, id, (j > 1 || k > 0) ? 1 : 0);
-                } else {
+                  for (int k = 0; k < 4; ++k)
+                    mma_ts(d + kChunk * part, p + 8 * k, vb + 128 * k, id, (j > 1 || h == 0 || k > 0) ? 1 : 0);
+                  if (brief) {
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    mma_ts(d + kChunk * part, p + 8 * k + 32 * (k >> 2), vb + 128 * k, id, (j > 1 || k > 0) ? 1 : 0);
-                    mma_ts(d + kChunk * part, p + 8 * k + 32 * (k >> 2) + 32, vb + 128 * k, id, 1);
+                    for (int k = 0; k < 4; ++k) mma_ts(d + kChunk * part, p + 32 + 8 * k, vb + 128 * k, id, 1);
                   }
                 }
               }
-              if (j == it.n[t]) commit_elected(smem_u32(&sm.ofull[t]));
+              if (!ok) break;
+              pphase ^= 1u << t;
+              if (j == n) commit_elected(smem_u32(&sm.ofull[t]));
+              if (t == 1 || j - 1 >= it.n[1]) release(vs, nvc);  // V of the tile before is done with
             }
-            if (j < it.n[t]) {  // S_X of this tile
+            if (j < n) {  // S_X of this tile
               if (j == 0) {
-                if (!pair_wait(smem_u32(&sm.qfull[t]), qphase[t], &sm.abort)) { ok = false; break; }
-                qphase[t] ^= 1;
+                if (!warp_wait(smem_u32(&sm.qfull[t]), qphase >> t & 1, &sm.abort)) { ok = false; break; }
+                qphase ^= 1u << t;
               }
-              uint64_t qa = dq + (uint64_t)(kStep * nkc * t);
-              for (int c = 0; c < nkc && ok; ++c, qa += kStep) {
-                int s = ks + c;
-                const bool wrap = s >= g.ring;
-                if (wrap) s -= g.ring;
-                if (!kready) {
-                  ok = pair_wait(smem_u32(&sm.full[s]), wrap ? rphase ^ 1 : rphase, &sm.abort);
-                  if (!ok) break;
-                }
+              int s = rs;
+#pragma unroll 1
+              for (int c = 0; c < nkc; ++c, ++s) {
+                if (s == g.ring) s = 0;
+                if (!kready && !warp_wait(smem_u32(&sm.full[s]), s < rs ? rphase ^ 1 : rphase, &sm.abort)) { ok = false; break; }
                 tc_fence_after();
-                const uint64_t kb = dk + (uint64_t)(kStep * s);
+                const uint64_t qa = dq + (uint64_t)(uint32_t)uniform(kStep * (nkc * t + c));
+                const uint64_t kb = dk + (uint64_t)(uint32_t)uniform(kStep * s);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_ss(tbase + kColS + 128 * t, qa + 2 * k, kb + 2 * k, id_s, (c > 0 || k > 0) ? 1 : 0);
+                for (int k = 0; k < 4; ++k) mma_ss(ts, qa + 2 * k, kb + 2 * k, id_s, (c > 0 || k > 0) ? 1 : 0);
+                if (t == 1 || j >= it.n[1]) commit_elected(smem_u32(&sm.empty[s]));  // the chunk's last use
               }
               if (!ok) break;
               kready = true;
               commit_elected(smem_u32(&sm.sfull[t]));
-              if (j + 1 == it.n[t]) commit_elected(smem_u32(&sm.qempty[t]));
+              if (j + 1 == n) commit_elected(smem_u32(&sm.qempty[t]));
             }
           }
           if (!ok) break;
-          if (j > 0)  // V of the tile before is done with
-            for (int c = 0; c < nvc; ++c) {
-              const int s = vs + c;
-              commit_elected(smem_u32(&sm.empty[s >= g.ring ? s - g.ring : s]));
-            }
           if (j < N) {
-            for (int c = 0; c < nkc; ++c) {
-              const int s = ks + c;
-              commit_elected(smem_u32(&sm.empty[s >= g.ring ? s - g.ring : s]));
-            }
             advance(nkc);
             vs = rs;
             vturn = rphase;
@@ -602,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j >= jm && !count_wait(&sm.vissued, ++nv, &sm.abort)) { ok = false; break; }
           for (int c = 0; c < nvc && ok; ++c, step()) {
             if (j < jm) continue;
-            if (!pair_wait(smem_u32(&sm.full[rs]), rphase, &sm.abort)) { ok = false; break; }
+            if (!warp_wait(smem_u32(&sm.full[rs]), rphase, &sm.abort)) { ok = false; break; }
             uint4* chunk = reinterpret_cast<uint4*>(rptr + rs * kChunkBytes);
             const int rows = min(seen - kTile * j, kTile);  // of the tile that some row sees
             // warp 10 takes even groups of four rows, warp 11 odd ones
@@ -651,158 +705,133 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sphase = 0, ophase = 0;
     bool ok = true;
     int k = 0;
-    Item it;
-    while (ok && next_item(it)) {
-      const int slot = k % (2 * kSlots);
-      ++k;
-      const int tok = it.tok + t * per + (row >> g.lgp);
-      const int lim = tok < it.nq ? visible(tok, it.nq, it.nk) : 0;
+    for (; ok && wait_item(); item_done()) {
+      const Item& it = sm.item[islot];
+      auto token = [&] { return it.tok + t * per + (row >> g.lgp); };
       const bool brief = it.lim <= kShort;
-      const int n = t ? it.n[1] : it.n[0];
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < n; ++j) {
-        if (!pair_wait(smem_u32(&sm.sfull[t]), sphase, &sm.abort)) { ok = false; break; }
+      // columns of the tile that this row sees
+      int see = token() < it.nq ? visible(token(), it.nq, it.nk) : 0;
+#pragma unroll 1
+      for (int left = it.n[t]; left > 0; --left, see -= kTile) {
+        if (!warp_wait(smem_u32(&sm.sfull[t]), sphase, &sm.abort)) { ok = false; break; }
         sphase ^= 1;
         tc_fence_after();
-        const int see = lim - kTile * j;  // columns that this row sees
+        // All four quarters of a row for its maximum; for the weights the first two
+        // are read again (128 scores and the rest do not fit in 168 registers).
+        uint32_t z[2][32];  // quarters 2 and 3
         const bool part = __any_sync(0xffffffffu, see < kTile);
-        const uint64_t c2 = pair2(c, c);
-        uint64_t sum[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
-        // 32 weights of scores z against the reference r2 = (-m, -m)
-        auto weigh = [&](const uint32_t (&z)[32], uint64_t r2, uint32_t* hi) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 x = split2(fma2(pair2(z[2 * i], z[2 * i + 1]), c2, r2));
-            const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
-            sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
-            hi[i] = *reinterpret_cast<const uint32_t*>(&b2);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        {
+          uint32_t y[2][32];
+          tmem_ld_32cols(ts, y[0]);
+          tmem_ld_32cols(ts + 32, y[1]);
+          tmem_ld_32cols(ts + 64, z[0]);
+          tmem_ld_32cols(ts + 96, z[1]);
+          tmem_wait_ld();
+          if (part) {
+            hide(y[0], 0, see);
+            hide(y[1], 1, see);
+            hide(z[0], 2, see);
+            hide(z[1], 3, see);
           }
-        };
-        auto top = [](const uint32_t (&z)[32], float x) {
-          float y = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            x = max3(x, __uint_as_float(z[i]), __uint_as_float(z[i + 1]));
-            y = max3(y, __uint_as_float(z[i + 2]), __uint_as_float(z[i + 3]));
-          }
-          return fmaxf(x, y);
-        };
-        bool done = false;
-        if (!brief && j > 0) {
-          // One pass: weights against the reference of the tiles before, kept in
-          // registers until the tile's maximum is known not to pass it by 2^8.
-          const float mm = m == -INFINITY ? 0.0f : m;
-          const uint64_t r2 = pair2(-mm, -mm);
-          float mt = -INFINITY;
-          uint32_t z[2][32], pk[4][16];
-          tmem_ld_32cols(ts, z[0]);
+          for (int i = 0; i < 32; i += 2)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_wait_ld();
-            if (q < 3) tmem_ld_32cols(ts + 32 * q + 32, z[(q + 1) & 1]);
-            if (part) hide(z[q & 1], q, see);
-            mt = top(z[q & 1], mt);
-            weigh(z[q & 1], r2, pk[q]);
-          }
-          mt *= c;
-          done = !__any_sync(0xffffffffu, mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY));
-          if (done) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_st_16cols(ts + 16 * q, pk[q]);
-          } else {
-            sum[0] = sum[1] = pair2(0.0f, 0.0f);
-          }
+            for (int q = 0; q < 2; ++q) {
+              mx[q] = max3(mx[q], __uint_as_float(y[q][i]), __uint_as_float(y[q][i + 1]));
+              mx[2 + q] = max3(mx[2 + q], __uint_as_float(z[q][i]), __uint_as_float(z[q][i + 1]));
+            }
         }
-        if (!done) {
-          // Two passes: the maximum, then the weights.
-          float mt = -INFINITY;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t z[32];
-            tmem_ld_32cols(ts + 32 * q, z);
-            tmem_wait_ld();
-            if (part) hide(z, q, see);
-            mt = top(z, mt);
+        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+        float f = 1.0f;
+        bool resc = false;
+        if (mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY)) {
+          if (m > -INFINITY) {
+            f = exp2f(m - mt);
+            resc = true;
           }
-          mt *= c;
-          float f = 1.0f;
-          bool resc = false;
-          if (mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY)) {
-            if (m > -INFINITY) {
-              f = exp2f(m - mt);
-              resc = true;
-            }
-            m = mt;
-          }
-          const float mm = m == -INFINITY ? 0.0f : m;
-          const uint64_t r2 = pair2(-mm, -mm);
-          if (__any_sync(0xffffffffu, resc)) {
-            // (S of this tile came after O of the one before)
-            l *= f;
-#pragma unroll 1
-            for (int q = 0; 32 * q < it.dv; ++q) {
-              uint32_t v[32];
-              tmem_ld_32cols(to + 32 * q, v);
-              tmem_wait_ld();
+          m = mt;
+        }
+        const float mm = m == -INFINITY ? 0.0f : m;
+        const bool rescale = __any_sync(0xffffffffu, resc);
+        const uint64_t c2 = pair2(c, c), r2 = pair2(-mm, -mm);
+        uint64_t sum[2] = {pair2(l * f, 0.0f), pair2(0.0f, 0.0f)};
+        // A quarter's weights over scores that were read: bf16 to columns `at`,
+        // what that leaves (short items) 32 behind.
+        auto weigh = [&](const uint32_t (&x)[32], uint32_t at, auto both) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              tmem_st_32cols(to + 32 * q, v);
-            }
-          }
-          if (!brief) {
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              uint32_t z[32], pk[16];
-              tmem_ld_32cols(ts + 32 * q, z);
-              tmem_wait_ld();
-              if (part) hide(z, q, see);
-              weigh(z, r2, pk);
-              tmem_st_16cols(ts + 16 * q, pk);
-            }
-          } else {
-            // Halves of 64 scores: bf16 weights over the half's first 32 columns,
-            // what that leaves over the others.
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              uint32_t z[2][32], hi[2][16];
-              tmem_ld_32cols(ts + 64 * h, z[0]);
-              tmem_ld_32cols(ts + 64 * h + 32, z[1]);
-              tmem_wait_ld();
+          for (int i0 = 0; i0 < 32; i0 += 16) {
+            uint32_t hi[8], lo[8];
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                if (part) hide(z[q], 2 * h + q, see);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float2 x = split2(fma2(pair2(z[q][2 * i], z[q][2 * i + 1]), c2, r2));
-                  const float e0 = ex2_approx(x.x), e1 = ex2_approx(x.y);
-                  sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
-                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
-                  const float2 hf = __bfloat1622float2(h2);
-                  const __nv_bfloat162 l2 = __floats2bfloat162_rn(e0 - hf.x, e1 - hf.y);
-                  hi[q][i] = *reinterpret_cast<const uint32_t*>(&h2);
-                  z[q][i] = *reinterpret_cast<const uint32_t*>(&l2);
-                }
+            for (int i = 0; i < 8; ++i) {
+              const float2 e = split2(fma2(pair2(x[i0 + 2 * i], x[i0 + 2 * i + 1]), c2, r2));
+              const float e0 = ex2_approx(e.x), e1 = ex2_approx(e.y);
+              sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
+              hi[i] = *reinterpret_cast<const uint32_t*>(&h2);
+              if (decltype(both)::value) {
+                const float2 h = __bfloat1622float2(h2);
+                const __nv_bfloat162 l2 = __floats2bfloat162_rn(e0 - h.x, e1 - h.y);
+                lo[i] = *reinterpret_cast<const uint32_t*>(&l2);
               }
-              tmem_st_16cols(ts + 64 * h, hi[0]);
-              tmem_st_16cols(ts + 64 * h + 16, hi[1]);
-              tmem_st_16cols(ts + 64 * h + 32, z[0]);
-              tmem_st_16cols(ts + 64 * h + 48, z[1]);
+            }
+            tmem_st_8cols(at + i0 / 2, hi);
+            if (decltype(both)::value) tmem_st_8cols(at + 32 + i0 / 2, lo);
+          }
+        };
+        auto hand_over = [&](int h) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.pfull[t][h]);
+        };
+        // The second half of the keys first: its weights' products run while the
+        // first half's are made.
+        auto halves = [&](auto both) {
+#pragma unroll 1
+          for (int h = 1;; h = 0) {
+            weigh(z[0], ts + 64 * h, both);
+            weigh(z[1], ts + 64 * h + 16, both);
+            if (h == 0) break;
+            if (rescale) {
+              // O of the tiles before (S of this tile came after it)
+#pragma unroll 1
+              for (int i = 0; 16 * i < it.dv; ++i) {
+                uint32_t v[16];
+                tmem_ld_16cols(to + 16 * i, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                tmem_st_16cols(to + 16 * i, v);
+              }
+            }
+            tmem_ld_32cols(ts, z[0]);
+            tmem_ld_32cols(ts + 32, z[1]);
+            hand_over(1);
+            tmem_wait_ld();
+            if (part) {
+              hide(z[0], 0, see);
+              hide(z[1], 1, see);
             }
           }
-        }
+          hand_over(0);
+        };
+        if (brief)
+          halves(std::true_type{});
+        else
+          halves(std::false_type{});
         const float2 s0 = split2(add2(sum[0], sum[1]));
-        l += s0.x + s0.y;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.pfull[t]);
+        l = s0.x + s0.y;
       }
       if (!ok) break;
       // ---- O out of TMEM
-      const bool any = n > 0;
+      const bool any = it.n[t] > 0;
+      const int slot = k % (2 * kSlots), tok = token();
+      const int lim = tok < it.nq ? visible(tok, it.nq, it.nk) : 0;
+      ++k;
       if (any) {
-        if (!pair_wait(smem_u32(&sm.ofull[t]), ophase, &sm.abort)) { ok = false; break; }
+        if (!warp_wait(smem_u32(&sm.ofull[t]), ophase, &sm.abort)) { ok = false; break; }
         ophase ^= 1;
         tc_fence_after();
       }
