@@ -592,7 +592,8 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
 #pragma unroll
       for (int r = kWarps / 2; r >= 1; r >>= 1) {
         if (warp >= r && warp < 2 * r) {
-          float4* dst = reinterpret_cast<float4*>(join + (warp - r) * Sh::kO) + lane;
+          // (from the second round on the buffer that this warp itself has read)
+          float4* dst = reinterpret_cast<float4*>(join + (r == kWarps / 2 ? warp - r : warp) * Sh::kO) + lane;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
         }
         __syncthreads();
         if (warp < r) {
-          const float4* src = reinterpret_cast<const float4*>(join + warp * Sh::kO) + lane;
+          const float4* src = reinterpret_cast<const float4*>(join + (r == kWarps / 2 ? warp : warp + r) * Sh::kO) + lane;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
