@@ -66,6 +66,7 @@ struct Geo {
   int gk, gv;        // groups of 16 dims
   int stages;
   int lgbs;          // log2 of the page size, or -1
+  int one;           // every warp's tile lies in one page
   int* off;          // [B + 1] first unit of each sequence, then the total
   float2* ml;        // [2 slots per CTA][rows]
   float* po;         // [2 slots per CTA][rows][Dv]
@@ -225,7 +226,9 @@ struct Shared {
   static constexpr int kRing = kJoin + 4 * kO * (kWarps / 2);
 };
 
-template <int NC, int NT>
+// kFull: Dk = Dv = 64 NC, where a row's layout is known at compile time (its
+// loads are one instruction each) and no group of 16 dims is missing.
+template <int NC, int NT, bool kFull>
 __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
     k_cache4_attn(const __grid_constant__ Geo g) {
   using Sh = Shared<NC, NT>;
@@ -269,7 +272,9 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
   const int lo = first_unit(T, G, blockIdx.x);
   const int mine = first_unit(T, G, blockIdx.x + 1) - lo;
 
-  const int RB = a.row_bytes;
+  const int RB = kFull ? (72 * NC + 15) / 16 * 16 : a.row_bytes;
+  const int Dk = kFull ? 64 * NC : a.Dk, Dv = kFull ? 64 * NC : a.Dv;
+  const int gk = kFull ? 4 * NC : g.gk, gv = kFull ? 4 * NC : g.gv;
   const uint32_t stage_bytes = kRowsW * RB;
   const uint32_t ring = smem_u32(sm + Sh::kRing) + warp * g.stages * stage_bytes;
   const int stages = g.stages;
@@ -287,8 +292,9 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
     if (pw.left <= 0) return;
     const int p0 = pw.unit * kUnit + warp * kRowsW;
     prow = min(pw.L - p0, kRowsW);
-    if (lane < prow) {
-      const unsigned p = (unsigned)(p0 + lane);
+    const int i = g.one ? 0 : lane;  // (one page holds the whole tile)
+    if (i < prow) {
+      const unsigned p = (unsigned)(p0 + i);
       const unsigned s = g.lgbs >= 0 ? p >> g.lgbs : p / (unsigned)a.lay.bs;
       poff = (int)(p - s * (unsigned)a.lay.bs);
       page = __ldg(&a.lay.bt[(long long)pw.b * a.lay.maxb + s]);
@@ -302,9 +308,13 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
       locate();
     }
     if (pw.left <= 0) return;
-    const bool have = lane < prow, good = have && page >= 0 && page < a.lay.nb;
+    const bool have = g.one || lane < prow, good = have && page >= 0 && page < a.lay.nb;
     if (have && !good) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
-    const unsigned valid = __ballot_sync(0xffffffffu, good);
+    unsigned valid;
+    if (g.one)
+      valid = good ? 0xffffffffu >> (kRowsW - prow) : 0u;
+    else
+      valid = __ballot_sync(0xffffffffu, good);
     const int s = rs;
     if (++rs == stages) rs = 0;
     if (lane == 0) {
@@ -312,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
       mbar_arrive_expect_tx(&bars[s], (uint32_t)__popc(valid) * RB);
     }
     __syncwarp();
-    if (good && (lane == 0 || poff == 0)) {
+    if (good && (lane == 0 || (!g.one && poff == 0))) {
       const int run = min(a.lay.bs - poff, prow - lane);
       const int hk = pw.hh / g.HB;
       const uint8_t* src = a.pool + (((long long)page * a.Hk + hk) * a.lay.bs + poff) * RB;
@@ -326,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
   for (int i = 0; i < stages; ++i) request();
 
   // ---- consumer
-  const int nck = (g.gk + 3) >> 2, ncv = (g.gv + 3) >> 2;
-  const int sk = (a.Dk + a.Dv) / 2, sv = sk + g.gk;  // scales of K and V within a row
+  const int nck = (gk + 3) >> 2, ncv = (gv + 3) >> 2;
+  const int sk = (Dk + Dv) / 2, sv = sk + gk;  // scales of K and V within a row
   uint32_t qf[NC][4][NT][2];
   float cs[NT][2];              // score factor of this lane's two columns
   float o[NT][NC * 4][4];
@@ -346,14 +356,14 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int h = 8 * nt + gq;
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)cw.b * a.Hq + h0 + h) * a.Dk);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)cw.b * a.Hq + h0 + h) * Dk);
         uint4 x[NC][2];
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           x[c][0] = x[c][1] = make_uint4(0, 0, 0, 0);
           const int j = 4 * c + t;
-          if (h < heads && j < g.gk) {
+          if (h < heads && j < gk) {
             x[c][0] = __ldg(&src[2 * j]);
             x[c][1] = __ldg(&src[2 * j + 1]);
           }
@@ -410,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
         }
       }
       const uint32_t valid = masks[s];
+      const bool whole = valid == 0xffffffffu;
       const uint32_t base = ring + s * stage_bytes;
       float z[2][NT][4];
 #pragma unroll
@@ -421,11 +432,11 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
         const uint32_t r0 = base + (16 * mt + gq) * RB, r1 = r0 + 8 * RB;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          if (NC > 1 && c >= nck) break;
+          if (!kFull && NC > 1 && c >= nck) break;
           const int j = 4 * c + t;
           uint2 w0 = make_uint2(0, 0), w1 = make_uint2(0, 0);
           uint32_t s0 = 0, s1 = 0;
-          if (j < g.gk) {
+          if (kFull || j < gk) {
             w0 = lds64(r0 + 8 * j);
             w1 = lds64(r1 + 8 * j);
             s0 = lds8(r0 + sk + j);
@@ -449,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
           }
         }
       }
-      if (valid != 0xffffffffu) {
+      if (!whole) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -458,36 +469,41 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) z[mt][nt][k] = -INFINITY;
       }
+      // the lane's own scores first: the maximum of a column is only needed
+      // where one passes the running one by 2^8
       bool up = false;
-      float f[NT][2];
+      float x[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           // cs > 0, so the maximum of the scores is that of the products
-          float x = fmaxf(fmaxf(z[0][nt][e], z[0][nt][e + 2]), fmaxf(z[1][nt][e], z[1][nt][e + 2]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x *= cs[nt][e];
-          f[nt][e] = 1.0f;
-          if (x > m[nt][e] + kRescaleLog2 || (m[nt][e] == -INFINITY && x > -INFINITY)) {
-            f[nt][e] = ex2_approx(m[nt][e] - x);
-            m[nt][e] = x;
-            up = true;
-          }
+          x[nt][e] = fmaxf(fmaxf(z[0][nt][e], z[0][nt][e + 2]), fmaxf(z[1][nt][e], z[1][nt][e + 2])) * cs[nt][e];
+          up |= x[nt][e] > m[nt][e] + kRescaleLog2;
         }
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          l[nt][0] *= f[nt][0];
-          l[nt][1] *= f[nt][1];
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y = x[nt][e];
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+            f[e] = 1.0f;
+            if (y > m[nt][e] + kRescaleLog2) {
+              f[e] = ex2_approx(m[nt][e] - y);
+              m[nt][e] = y;
+            }
+            l[nt][e] *= f[e];
+          }
 #pragma unroll
           for (int i = 0; i < NC * 4; ++i) {
-            o[nt][i][0] *= f[nt][0];
-            o[nt][i][1] *= f[nt][1];
-            o[nt][i][2] *= f[nt][0];
-            o[nt][i][3] *= f[nt][1];
+            o[nt][i][0] *= f[0];
+            o[nt][i][1] *= f[1];
+            o[nt][i][2] *= f[0];
+            o[nt][i][3] *= f[1];
           }
         }
       }
@@ -519,11 +535,11 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
         const uint32_t keep_cd = ((v4 & 0x100u) ? 0xffu : 0u) | ((v4 & 0x200u) ? 0xff00u : 0u);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          if (NC > 1 && c >= ncv) break;
+          if (!kFull && NC > 1 && c >= ncv) break;
           const int j = 4 * c + (gq >> 1);  // the lane's 8 dims are half of group j
           uint32_t wa = 0, wb = 0, wc = 0, wd = 0, sab = 0, scd = 0;
-          if (j < g.gv) {
-            const uint32_t at = ra + a.Dk / 2 + 32 * c + 4 * gq, st = ra + sv + j;
+          if (kFull || j < gv) {
+            const uint32_t at = ra + Dk / 2 + 32 * c + 4 * gq, st = ra + sv + j;
             wa = lds32(at);
             wb = lds32(at + RB);
             wc = lds32(at + 8 * RB);
@@ -531,8 +547,12 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
             sab = lds8(st) | (lds8(st + RB) << 8);
             scd = lds8(st + 8 * RB) | (lds8(st + 9 * RB) << 8);
           }
-          sab = widen_scales(sab & keep_ab);
-          scd = widen_scales(scd & keep_cd);
+          if (!whole) {
+            sab &= keep_ab;
+            scd &= keep_cd;
+          }
+          sab = widen_scales(sab);
+          scd = widen_scales(scd);
           // byte i: dim 2 i (2 i + 1) of both positions
           uint32_t e_ab[4], o_ab[4], e_cd[4], o_cd[4];
           widen((wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u), e_ab);
@@ -773,7 +793,7 @@ Layout ws_layout(int B, int Dk, int Dv, int G) {
   return w;
 }
 
-template <int NC, int NT>
+template <int NC, int NT, bool kFull>
 int launch(Geo& g, cudaStream_t s, long long bound, int* ctas_out) {
   using Sh = Shared<NC, NT>;
   constexpr int per = NC <= 2 && NT == 1 ? 2 : 1;
@@ -781,12 +801,12 @@ int launch(Geo& g, cudaStream_t s, long long bound, int* ctas_out) {
   const int room = 227 * 1024 / per - 1024 * (per - 1) - Sh::kRing;
   g.stages = std::min(kMaxStages, room / stage);
   const int smem = Sh::kRing + g.stages * stage;
-  const void* k = (const void*)k_cache4_attn<NC, NT>;
+  const void* k = (const void*)k_cache4_attn<NC, NT, kFull>;
   int rc = ensure_dynamic_smem(k, smem, "cache4_attn_decode");
   if (rc) return rc;
   const int ctas = (int)std::min<long long>(std::min(kMaxCtas, per * sm_count()), std::max(1LL, bound));
   *ctas_out = ctas;
-  const cudaError_t e = launch_pdl(k_cache4_attn<NC, NT>, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, s, g);
+  const cudaError_t e = launch_pdl(k_cache4_attn<NC, NT, kFull>, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, s, g);
   count_launch();
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
   return check_launch("cache4_attn_decode");
@@ -819,13 +839,19 @@ int launch_cache4_attn(const Cache4AttnParams& p, void* ws, cudaStream_t s) {
   const long long bound = items * (((long long)p.lay.max_len + kUnit - 1) / kUnit);
   if (bound > 0x7fffffffLL || items > 0x7fffffffLL)
     return set_error(DSA_ERR_UNSUPPORTED, "cache4_attn_decode: heads x positions beyond 2^31 units of 256");
+  g.one = p.lay.bs % kRowsW == 0;
+  const bool full = p.Dk == 64 * nc && p.Dv == 64 * nc;
   int ctas = 0, rc;
-  if (nc == 1)
-    rc = heads == 8 ? launch<1, 1>(g, s, bound, &ctas) : launch<1, 2>(g, s, bound, &ctas);
+  if (nc == 1 && heads == 8)
+    rc = full ? launch<1, 1, true>(g, s, bound, &ctas) : launch<1, 1, false>(g, s, bound, &ctas);
+  else if (nc == 1)
+    rc = full ? launch<1, 2, true>(g, s, bound, &ctas) : launch<1, 2, false>(g, s, bound, &ctas);
+  else if (nc == 2 && heads == 8)
+    rc = full ? launch<2, 1, true>(g, s, bound, &ctas) : launch<2, 1, false>(g, s, bound, &ctas);
   else if (nc == 2)
-    rc = heads == 8 ? launch<2, 1>(g, s, bound, &ctas) : launch<2, 2>(g, s, bound, &ctas);
+    rc = full ? launch<2, 2, true>(g, s, bound, &ctas) : launch<2, 2, false>(g, s, bound, &ctas);
   else
-    rc = launch<4, 1>(g, s, bound, &ctas);
+    rc = full ? launch<4, 1, true>(g, s, bound, &ctas) : launch<4, 1, false>(g, s, bound, &ctas);
   if (rc) return rc;
   const cudaError_t e = launch_pdl(k_cache4_merge, dim3((unsigned)items), dim3(256), 0, s, g, ctas, heads);
   count_launch();
