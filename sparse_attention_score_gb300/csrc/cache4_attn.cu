@@ -31,8 +31,7 @@
 // Work is counted in units of 256 positions of one (sequence, key head, block
 // of heads); all units, item after item, are split evenly over the CTAs.  A
 // warp takes 32 positions of a unit, with its own ring of bulk copies (one per
-// run of positions inside a page) and its own softmax; an item's warps are
-// joined through shared memory, its CTAs by k_cache4_merge in a fixed order.
+// run of positions inside a page) and its own softmax; an item's warps are joined through shared memory, its CTAs by k_cache4_merge in a fixed order.
 // Lengths are read on the device, so a captured call follows them.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -212,19 +211,48 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   return r;
 }
 
-// Shared memory: barriers, masks, the warps' (reference, sum), the join's
-// buffers (half of the warps' O), then the rings.
+// Shared memory: barriers, what a stage holds, the warps' (maximum, sum), the
+// join's buffers (half of the warps' O), then the warps' rings.
 template <int NC, int NT>
 struct Shared {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kO = kHeads * 64 * NC;  // floats of a warp's O
   static constexpr int kBars = 0;
-  static constexpr int kMasks = kBars + 8 * kWarps * kMaxStages;
-  static constexpr int kMl = kMasks + 4 * kWarps * kMaxStages;
+  static constexpr int kMeta = kBars + 8 * kWarps * kMaxStages;
+  static constexpr int kMl = kMeta + 16 * kWarps * kMaxStages;
   static constexpr int kAbort = kMl + 8 * kWarps * kHeads;
   static constexpr int kJoin = (kAbort + 4 + 127) / 128 * 128;
   static constexpr int kRing = kJoin + 4 * kO * (kWarps / 2);
 };
+
+// Flags of a unit, of its item's part in this CTA.
+constexpr uint32_t kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8;
+
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split2(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // kFull: Dk = Dv = 64 NC, where a row's layout is known at compile time (its
 // loads are one instruction each) and no group of 16 dims is missing.
@@ -239,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
   const int gq = lane >> 2, t = lane & 3;  // row and column groups of a fragment
   launch_dependents();
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::kBars) + warp * kMaxStages;
-  uint32_t* masks = reinterpret_cast<uint32_t*>(sm + Sh::kMasks) + warp * kMaxStages;
+  uint4* meta = reinterpret_cast<uint4*>(sm + Sh::kMeta) + warp * kMaxStages;
   float2* ml = reinterpret_cast<float2*>(sm + Sh::kMl);
   int* abort = reinterpret_cast<int*>(sm + Sh::kAbort);
   float* join = reinterpret_cast<float*>(sm + Sh::kJoin);
@@ -279,84 +307,107 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
   const uint32_t ring = smem_u32(sm + Sh::kRing) + warp * g.stages * stage_bytes;
   const int stages = g.stages;
 
-  // ---- producer state: the next tile to request, its pages one tile ahead
-  Walk pw = start_at(g, lo, mine, lane);
-  Walk cw = pw;
+  // ---- requests, a unit at a time: this warp's 32 positions of it (none at an
+  // item's end), and what the unit is.  The pages are looked up a unit ahead.
+  Walk w = start_at(g, lo, mine, lane);
   int rs = 0, us = 0;           // stage to fill, stage to read
   uint32_t uphase = 0;
   int pending = 0;              // stages filled and not yet waited for
-  int page = -1, poff = 0, prow = 0;
-  auto locate = [&] {  // page and row of this lane's position of tile pw
-    prow = 0;
-    page = -1;
-    if (pw.left <= 0) return;
-    const int p0 = pw.unit * kUnit + warp * kRowsW;
-    prow = min(pw.L - p0, kRowsW);
+  int page = -1, poff = 0, rows = 0;
+  uint32_t flags = kFirst | (w.unit == 0 ? kFromStart : 0);
+  bool ok = true;               // no wait of this CTA's ran out
+  auto locate = [&] {  // page and row of this lane's position of the unit
+    const int p0 = w.unit * kUnit + warp * kRowsW;
+    rows = min(w.L - p0, kRowsW);
     const int i = g.one ? 0 : lane;  // (one page holds the whole tile)
-    if (i < prow) {
+    if (i < rows) {
       const unsigned p = (unsigned)(p0 + i);
       const unsigned s = g.lgbs >= 0 ? p >> g.lgbs : p / (unsigned)a.lay.bs;
       poff = (int)(p - s * (unsigned)a.lay.bs);
-      page = __ldg(&a.lay.bt[(long long)pw.b * a.lay.maxb + s]);
+      page = __ldg(&a.lay.bt[(long long)w.b * a.lay.maxb + s]);
     }
   };
-  // request tile pw (if this warp has rows of it) and go to the next
   auto request = [&] {
-    // a tile without rows of this warp takes no stage
-    while (pw.left > 0 && prow <= 0) {
-      pw.next(g);
-      locate();
-    }
-    if (pw.left <= 0) return;
-    const bool have = g.one || lane < prow, good = have && page >= 0 && page < a.lay.nb;
-    if (have && !good) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
-    unsigned valid;
-    if (g.one)
-      valid = good ? 0xffffffffu >> (kRowsW - prow) : 0u;
-    else
-      valid = __ballot_sync(0xffffffffu, good);
-    const int s = rs;
-    if (++rs == stages) rs = 0;
+    if (w.left <= 0) return;
+    const int i = g.one ? 0 : lane;
+    const bool good = i < rows && page >= 0 && page < a.lay.nb;
+    if (i < rows && !good) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
+    unsigned valid = g.one ? (good ? 0xffffffffu >> (kRowsW - rows) : 0u) : __ballot_sync(0xffffffffu, good);
+    if (!ok) valid = 0;  // the units go by all the same: the warps meet at an item's end
+    if (w.unit + 1 == w.n) flags |= kLast | kToEnd;
+    if (w.left == 1) flags |= kLast;
     if (lane == 0) {
-      masks[s] = valid;
-      mbar_arrive_expect_tx(&bars[s], (uint32_t)__popc(valid) * RB);
+      meta[rs] = make_uint4(valid, flags, (uint32_t)w.b, (uint32_t)w.hh);
+      if (ok) mbar_arrive_expect_tx(&bars[rs], (uint32_t)__popc(valid) * RB);
     }
     __syncwarp();
-    if (good && (lane == 0 || (!g.one && poff == 0))) {
-      const int run = min(a.lay.bs - poff, prow - lane);
-      const int hk = pw.hh / g.HB;
+    if (ok && good && (lane == 0 || (!g.one && poff == 0))) {
+      const int run = min(a.lay.bs - poff, rows - lane);
+      const int hk = w.hh / g.HB;
       const uint8_t* src = a.pool + (((long long)page * a.Hk + hk) * a.lay.bs + poff) * RB;
-      bulk_copy(ring + s * stage_bytes + lane * RB, src, (uint32_t)(run * RB), smem_u32(&bars[s]));
+      bulk_copy(ring + rs * stage_bytes + lane * RB, src, (uint32_t)(run * RB), smem_u32(&bars[rs]));
     }
+    if (++rs == stages) rs = 0;
     ++pending;
-    pw.next(g);
-    locate();
+    flags = (flags & kLast) ? kFirst | kFromStart : flags & kFromStart;
+    w.next(g);
+    if (w.left > 0) locate();
   };
   locate();
   for (int i = 0; i < stages; ++i) request();
 
-  // ---- consumer
+  // ---- the products
   const int nck = (gk + 3) >> 2, ncv = (gv + 3) >> 2;
   const int sk = (Dk + Dv) / 2, sv = sk + gk;  // scales of K and V within a row
   uint32_t qf[NC][4][NT][2];
   float cs[NT][2];              // score factor of this lane's two columns
   float o[NT][NC * 4][4];
-  float m[NT][2], l[NT][2];     // running maximum (log2), sum
-  bool ok = true;
-  bool fresh = true;            // the item's first unit of this CTA
-  int unit0 = cw.unit;          // ... and which it is
-  while (cw.left > 0) {
-    const int hk = cw.hh / g.HB, hb = cw.hh - hk * g.HB;
-    const int h0 = hk * g.G + hb * kHeads;               // first query head of the block
-    const int heads = min(kHeads, g.G - hb * kHeads);
-    if (fresh) {
-      fresh = false;
-      unit0 = cw.unit;
+  float m[NT][2], l[NT][2];     // running maximum (log2), sum of the lane's weights
+  float zt[NT][2];              // the product that passes the maximum by 2^8
+  uint64_t r2[NT];              // kLift - m of both columns
+  while (pending > 0) {
+    if (ok && !pair_wait(smem_u32(&bars[us]), uphase, abort)) {
+      ok = false;
+      if (lane == 0) {
+        *abort = 1;
+        flag_status(a.status, DSA_STATUS_TIMEOUT);
+      }
+      // this warp's copies still on their way have a moment to land
+      int never = 0, s = us;
+      uint32_t ph = uphase;
+      for (int i = 0; i < pending; ++i) {
+        pair_wait(smem_u32(&bars[s]), ph, &never, 10000000ull);
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    const uint4 what = meta[us];
+    const uint32_t valid = ok ? what.x : 0u;
+    const uint32_t base = ring + us * stage_bytes;
+    if (++us == stages) {
+      us = 0;
+      uphase ^= 1;
+    }
+    --pending;
+    const int b = (int)what.z;
+    // key head, first query head of the block, heads of the block
+    auto heads_of_item = [&](int* hk, int* h0, int* heads) {
+      const int hh = (int)what.w;
+      *hk = hh / g.HB;
+      const int hb = hh - *hk * g.HB;
+      *h0 = *hk * g.G + hb * kHeads;
+      *heads = min(kHeads, g.G - hb * kHeads);
+    };
+    if (what.y & kFirst) {
+      int hk, h0, heads;
+      heads_of_item(&hk, &h0, &heads);
       const float ks = a.k_scale ? __ldg(&a.k_scale[hk]) : 1.0f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int h = 8 * nt + gq;
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)cw.b * a.Hq + h0 + h) * Dk);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)b * a.Hq + h0 + h) * Dk);
         uint4 x[NC][2];
         uint32_t top = 0;
 #pragma unroll
@@ -397,31 +448,16 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
         cs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
         m[nt][0] = m[nt][1] = -INFINITY;
         l[nt][0] = l[nt][1] = 0.0f;
+        zt[nt][0] = zt[nt][1] = -INFINITY;
+        r2[nt] = pair2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < NC * 4; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.0f;
       }
     }
-    const int p0 = cw.unit * kUnit + warp * kRowsW;
-    if (p0 < cw.L) {
-      const int s = us;
-      if (ok) {
-        ok = pair_wait(smem_u32(&bars[s]), uphase, abort);
-        if (ok) {
-          --pending;
-          if (++us == stages) {
-            us = 0;
-            uphase ^= 1;
-          }
-        } else if (lane == 0) {
-          *abort = 1;
-          flag_status(a.status, DSA_STATUS_TIMEOUT);
-        }
-      }
-      const uint32_t valid = masks[s];
+    if (valid != 0) {
       const bool whole = valid == 0xffffffffu;
-      const uint32_t base = ring + s * stage_bytes;
       float z[2][NT][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
@@ -469,35 +505,35 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) z[mt][nt][k] = -INFINITY;
       }
-      // the lane's own scores first: the maximum of a column is only needed
-      // where one passes the running one by 2^8
+      // The lane's own scores first: the maximum of a column is only needed where
+      // one passes the running one by 2^8 (in the products' own scale: zt).
       bool up = false;
-      float x[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // cs > 0, so the maximum of the scores is that of the products
-          x[nt][e] = fmaxf(fmaxf(z[0][nt][e], z[0][nt][e + 2]), fmaxf(z[1][nt][e], z[1][nt][e + 2])) * cs[nt][e];
-          up |= x[nt][e] > m[nt][e] + kRescaleLog2;
-        }
+        for (int e = 0; e < 2; ++e)
+          up |= fmaxf(max3(z[0][nt][e], z[0][nt][e + 2], z[1][nt][e]), z[1][nt][e + 2]) > zt[nt][e];
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float y = x[nt][e];
+            float y = fmaxf(max3(z[0][nt][e], z[0][nt][e + 2], z[1][nt][e]), z[1][nt][e + 2]);
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
             f[e] = 1.0f;
-            if (y > m[nt][e] + kRescaleLog2) {
-              f[e] = ex2_approx(m[nt][e] - y);
-              m[nt][e] = y;
+            if (y > zt[nt][e]) {
+              const float top = y * cs[nt][e];  // (cs > 0)
+              f[e] = ex2_approx(m[nt][e] - top);
+              m[nt][e] = top;
+              zt[nt][e] = y + kRescaleLog2 / cs[nt][e];
             }
-            l[nt][e] *= f[e];
           }
+          l[nt][0] *= f[0];
+          l[nt][1] *= f[1];
+          r2[nt] = pair2(kLift - m[nt][0], kLift - m[nt][1]);
 #pragma unroll
           for (int i = 0; i < NC * 4; ++i) {
             o[nt][i][0] *= f[0];
@@ -510,19 +546,20 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
       uint32_t pf[2][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float r0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0] - kLift;
-        const float r1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1] - kLift;
+        const uint64_t c2 = pair2(cs[nt][0], cs[nt][1]);
+        uint64_t sum = pair2(l[nt][0], l[nt][1]);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const float e0 = ex2_approx(fmaf(z[mt][nt][0], cs[nt][0], -r0));
-          const float e1 = ex2_approx(fmaf(z[mt][nt][1], cs[nt][1], -r1));
-          const float e2 = ex2_approx(fmaf(z[mt][nt][2], cs[nt][0], -r0));
-          const float e3 = ex2_approx(fmaf(z[mt][nt][3], cs[nt][1], -r1));
-          l[nt][0] += e0 + e2;
-          l[nt][1] += e1 + e3;
-          pf[mt][nt][0] = transpose8(pack_half2(e0, e1));
-          pf[mt][nt][1] = transpose8(pack_half2(e2, e3));
-        }
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 y = split2(fma2(pair2(z[mt][nt][2 * k], z[mt][nt][2 * k + 1]), c2, r2[nt]));
+            const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
+            sum = add2(sum, pair2(e0, e1));
+            pf[mt][nt][k] = transpose8(pack_half2(e0, e1));
+          }
+        const float2 l2 = split2(sum);
+        l[nt][0] = l2.x;
+        l[nt][1] = l2.y;
       }
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
@@ -569,11 +606,12 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
           }
         }
       }
-      __syncwarp();  // every lane has read the stage
-      if (ok) request();
     }
-    const bool last = cw.left == 1 || cw.unit + 1 == cw.n;
-    if (last) {
+    __syncwarp();  // every lane has read the stage and what it held
+    request();
+    if (what.y & kLast) {
+      int hk, h0, heads;
+      heads_of_item(&hk, &h0, &heads);
       // ---- join the warps: references and sums, then O in three rounds
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -637,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
       }
       if (warp == 0) {
         // the lane's eight dims 64 c + 8 gq of columns 2 t and 2 t + 1
-        const bool whole = unit0 == 0 && cw.unit + 1 == cw.n;
-        const int slot = 2 * blockIdx.x + (unit0 == 0 ? 1 : 0);
+        const bool whole = (what.y & kFromStart) && (what.y & kToEnd);
+        const int slot = 2 * blockIdx.x + ((what.y & kFromStart) ? 1 : 0);
         const float vs = a.v_scale ? __ldg(&a.v_scale[hk]) : 1.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -646,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
           for (int e = 0; e < 2; ++e) {
             const int h = 8 * nt + 2 * t + e;
             if (h >= heads) continue;
-            const size_t row = (size_t)cw.b * a.Hq + h0 + h;
+            const size_t row = (size_t)b * a.Hq + h0 + h;
             const float f = whole ? (sum[nt][e] == 0.0f ? 0.0f : vs / sum[nt][e]) : 1.0f;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -681,19 +719,6 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
                                  : (top[nt][e] - kLift + log2f(sum[nt][e])) * 0.6931471805599453f;
             }
           }
-      }
-      fresh = true;
-    }
-    cw.next(g);
-  }
-  // a wait ran out: the copies still on their way have a moment to land
-  if (!ok) {
-    int never = 0;
-    for (; pending > 0; --pending) {
-      pair_wait(smem_u32(&bars[us]), uphase, &never, 10000000ull);
-      if (++us == stages) {
-        us = 0;
-        uphase ^= 1;
       }
     }
   }
@@ -797,7 +822,7 @@ template <int NC, int NT, bool kFull>
 int launch(Geo& g, cudaStream_t s, long long bound, int* ctas_out) {
   using Sh = Shared<NC, NT>;
   constexpr int per = NC <= 2 && NT == 1 ? 2 : 1;
-  const int stage = kWarps * kRowsW * g.a.row_bytes;
+  const int stage = kUnit * g.a.row_bytes;  // of all warps
   const int room = 227 * 1024 / per - 1024 * (per - 1) - Sh::kRing;
   g.stages = std::min(kMaxStages, room / stage);
   const int smem = Sh::kRing + g.stages * stage;
