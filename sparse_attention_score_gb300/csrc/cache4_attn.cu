@@ -52,8 +52,6 @@ using namespace sm100;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRowsW = 32;                  // positions of a warp's tile
-constexpr int kUnit = kRowsW * kWarps;      // positions of a unit
 constexpr int kMaxCtas = 320;               // partial slots are laid out for these
 constexpr int kMaxStages = 8;
 constexpr float kLift = 7.0f;               // weights are 2^7 times their size
@@ -64,6 +62,7 @@ struct Geo {
   int G, HB, HH;     // query heads per key head, blocks of them, items per sequence
   int gk, gv;        // groups of 16 dims
   int stages;
+  int unit, lgunit;  // positions of a unit
   int lgbs;          // log2 of the page size, or -1
   int one;           // every warp's tile lies in one page
   int* off;          // [B + 1] first unit of each sequence, then the total
@@ -77,7 +76,7 @@ __device__ __forceinline__ int seq_len(const Cache4AttnParams& a, int b) {
   const int L = __ldg(&a.lay.seq_lens[b]);
   return L < 0 ? 0 : min(L, a.lay.max_len);  // the bound that the host counted with
 }
-__device__ __forceinline__ int units_of(int L) { return (L + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int units_of(const Geo& g, int L) { return (L + g.unit - 1) >> g.lgunit; }
 
 __device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll
@@ -95,7 +94,7 @@ struct Walk {
   int left;         // units of this CTA from here on, this one included
   __device__ __forceinline__ void load(const Geo& g) {
     L = uniform(seq_len(g.a, b));
-    n = units_of(L);
+    n = units_of(g, L);
   }
   // to the next unit; sequences without positions have none
   __device__ __forceinline__ void next(const Geo& g) {
@@ -121,7 +120,7 @@ __device__ __forceinline__ int owner(int T, int G, int x) {
 
 __device__ __forceinline__ int total_units(const Geo& g, int lane) {
   int sum = 0;
-  for (int b = lane; b < g.a.lay.batch; b += 32) sum += units_of(seq_len(g.a, b));
+  for (int b = lane; b < g.a.lay.batch; b += 32) sum += units_of(g, seq_len(g.a, b));
   return uniform(__reduce_add_sync(0xffffffffu, sum)) * g.HH;
 }
 
@@ -132,7 +131,7 @@ __device__ __forceinline__ Walk start_at(const Geo& g, int lo, int n, int lane) 
   int at = 0;
   for (int b0 = 0; b0 < g.a.lay.batch; b0 += 32) {
     const int b = b0 + lane;
-    const int u = b < g.a.lay.batch ? units_of(seq_len(g.a, b)) * g.HH : 0;
+    const int u = b < g.a.lay.batch ? units_of(g, seq_len(g.a, b)) * g.HH : 0;
     const int end = at + warp_scan(u, lane);
     const unsigned hit = __ballot_sync(0xffffffffu, end > lo);
     if (hit) {
@@ -228,6 +227,17 @@ struct Shared {
 // Flags of a unit, of its item's part in this CTA.
 constexpr uint32_t kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8;
 
+// A load that stays where it is written, a unit ahead of its use.
+__device__ __forceinline__ int ld_early(const int32_t* p) {
+  int r;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
+}
+
+__device__ __forceinline__ float power_of_two(int e) {  // -126 <= e <= 127
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
 __device__ __forceinline__ uint64_t pair2(float x, float y) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
@@ -254,13 +264,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// kFull: Dk = Dv = 64 NC, where a row's layout is known at compile time (its
+constexpr int per_sm(int NC, int NT, int RW) { return NC * NT * (RW / 32) <= 2 ? 2 : 1; }
+
+// RW: positions of a warp's tile.  kFull: Dk = Dv = 64 NC, where a row's layout is known at compile time (its
 // loads are one instruction each) and no group of 16 dims is missing.
-template <int NC, int NT, bool kFull>
-__global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
+template <int NC, int NT, int RW, bool kFull>
+__global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
     k_cache4_attn(const __grid_constant__ Geo g) {
   using Sh = Shared<NC, NT>;
   constexpr int kHeads = Sh::kHeads;
+  constexpr int kRowsW = RW, kUnit = RW * kWarps, kHalves = RW / 32, kMt = RW / 16;
   extern __shared__ __align__(128) uint8_t sm[];
   const Cache4AttnParams& a = g.a;
   const int lane = threadIdx.x & 31, warp = uniform(threadIdx.x >> 5);
@@ -286,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
       int u = 0;
       if (b < a.lay.batch) {
         const int L = seq_len(a, b);
-        u = units_of(L) * g.HH;
+        u = units_of(g, L) * g.HH;
         if (__ldg(&a.lay.seq_lens[b]) > L) flag_status(a.status, DSA_STATUS_BAD_LENGTH);
       }
       const int end = at + warp_scan(u, lane);
@@ -313,39 +326,61 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
   int rs = 0, us = 0;           // stage to fill, stage to read
   uint32_t uphase = 0;
   int pending = 0;              // stages filled and not yet waited for
-  int page = -1, poff = 0, rows = 0;
+  int page[kHalves], poff[kHalves], rows = 0;
   uint32_t flags = kFirst | (w.unit == 0 ? kFromStart : 0);
   bool ok = true;               // no wait of this CTA's ran out
-  auto locate = [&] {  // page and row of this lane's position of the unit
+  auto locate = [&] {  // page and row of this lane's positions of the unit
     const int p0 = w.unit * kUnit + warp * kRowsW;
     rows = min(w.L - p0, kRowsW);
-    const int i = g.one ? 0 : lane;  // (one page holds the whole tile)
-    if (i < rows) {
-      const unsigned p = (unsigned)(p0 + i);
-      const unsigned s = g.lgbs >= 0 ? p >> g.lgbs : p / (unsigned)a.lay.bs;
-      poff = (int)(p - s * (unsigned)a.lay.bs);
-      page = __ldg(&a.lay.bt[(long long)w.b * a.lay.maxb + s]);
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const int i = g.one ? 0 : 32 * h + lane;  // (one page holds the whole tile)
+      if (i < rows && (h == 0 || !g.one)) {
+        const unsigned p = (unsigned)(p0 + i);
+        const unsigned s = g.lgbs >= 0 ? p >> g.lgbs : p / (unsigned)a.lay.bs;
+        poff[h] = (int)(p - s * (unsigned)a.lay.bs);
+        page[h] = ld_early(&a.lay.bt[(long long)w.b * a.lay.maxb + s]);
+      }
     }
   };
   auto request = [&] {
     if (w.left <= 0) return;
-    const int i = g.one ? 0 : lane;
-    const bool good = i < rows && page >= 0 && page < a.lay.nb;
-    if (i < rows && !good) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
-    unsigned valid = g.one ? (good ? 0xffffffffu >> (kRowsW - rows) : 0u) : __ballot_sync(0xffffffffu, good);
-    if (!ok) valid = 0;  // the units go by all the same: the warps meet at an item's end
+    uint32_t valid[2] = {0, 0};
+    bool good[kHalves];
+    if (g.one) {
+      good[0] = rows > 0 && page[0] >= 0 && page[0] < a.lay.nb;
+      if (rows > 0 && !good[0]) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
+      if (good[0]) {
+        valid[0] = rows >= 32 ? 0xffffffffu : (1u << rows) - 1u;
+        if (kHalves > 1) valid[1] = rows >= 64 ? 0xffffffffu : rows > 32 ? (1u << (rows - 32)) - 1u : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        const bool have = 32 * h + lane < rows;
+        good[h] = have && page[h] >= 0 && page[h] < a.lay.nb;
+        if (have && !good[h]) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
+        valid[h] = __ballot_sync(0xffffffffu, good[h]);
+      }
+    }
+    if (!ok) valid[0] = valid[1] = 0;  // the units go by all the same: the warps meet at an item's end
     if (w.unit + 1 == w.n) flags |= kLast | kToEnd;
     if (w.left == 1) flags |= kLast;
     if (lane == 0) {
-      meta[rs] = make_uint4(valid, flags, (uint32_t)w.b, (uint32_t)w.hh);
-      if (ok) mbar_arrive_expect_tx(&bars[rs], (uint32_t)__popc(valid) * RB);
+      meta[rs] = make_uint4(valid[0], valid[1], (uint32_t)w.b, (uint32_t)w.hh << 4 | flags);
+      if (ok) mbar_arrive_expect_tx(&bars[rs], (uint32_t)(__popc(valid[0]) + __popc(valid[1])) * RB);
     }
     __syncwarp();
-    if (ok && good && (lane == 0 || (!g.one && poff == 0))) {
-      const int run = min(a.lay.bs - poff, rows - lane);
-      const int hk = w.hh / g.HB;
-      const uint8_t* src = a.pool + (((long long)page * a.Hk + hk) * a.lay.bs + poff) * RB;
-      bulk_copy(ring + rs * stage_bytes + lane * RB, src, (uint32_t)(run * RB), smem_u32(&bars[rs]));
+    const uint8_t* head = a.pool + (long long)(w.hh / g.HB) * a.lay.bs * RB;
+    const long long step = (long long)a.Hk * a.lay.bs * RB;  // to the next page
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      const int i = g.one ? 0 : 32 * h + lane;
+      if (ok && (h == 0 || !g.one) && good[h] && (g.one ? lane == 0 : lane == 0 || poff[h] == 0)) {
+        const int run = g.one ? rows : min(a.lay.bs - poff[h], min(rows - i, 32 - lane));
+        bulk_copy(ring + rs * stage_bytes + i * RB, head + page[h] * step + (long long)poff[h] * RB,
+                  (uint32_t)(run * RB), smem_u32(&bars[rs]));
+      }
     }
     if (++rs == stages) rs = 0;
     ++pending;
@@ -384,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
       }
     }
     const uint4 what = meta[us];
-    const uint32_t valid = ok ? what.x : 0u;
+    const uint32_t valid[2] = {ok ? what.x : 0u, ok ? what.y : 0u};
+    const uint32_t part = what.w & 15u;
     const uint32_t base = ring + us * stage_bytes;
     if (++us == stages) {
       us = 0;
@@ -394,13 +430,13 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
     const int b = (int)what.z;
     // key head, first query head of the block, heads of the block
     auto heads_of_item = [&](int* hk, int* h0, int* heads) {
-      const int hh = (int)what.w;
+      const int hh = (int)(what.w >> 4);
       *hk = hh / g.HB;
       const int hb = hh - *hk * g.HB;
       *h0 = *hk * g.G + hb * kHeads;
       *heads = min(kHeads, g.G - hb * kHeads);
     };
-    if (what.y & kFirst) {
+    if (part & kFirst) {
       int hk, h0, heads;
       heads_of_item(&hk, &h0, &heads);
       const float ks = a.k_scale ? __ldg(&a.k_scale[hk]) : 1.0f;
@@ -427,9 +463,11 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the head's largest element to [1, 2); nothing to do for 0, infinity, NaN
-        int e = 0;
-        if (top != 0 && top < 0x7f800000u) e = ilogbf(__uint_as_float(top));
+        // The head's largest element to [1, 2) or, of a subnormal one, below; in
+        // two factors, as 2^-e itself may pass fp32's range.  0, infinity and NaN
+        // stay what they are.
+        const int e = top < 0x7f800000u ? max((int)(top >> 23), 1) - 127 : 0;
+        const float down = power_of_two(-(e >> 1)), down2 = power_of_two((e >> 1) - e);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -437,13 +475,13 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
             // step k of the chunk: dims 4 k .. 4 k + 3 of the lane's group
             const uint4 v = x[c][k >> 1];
             const uint32_t w0 = (k & 1) ? v.z : v.x, w1 = (k & 1) ? v.w : v.y;
-            qf[c][k][nt][0] = pack_half2(scalbnf(__uint_as_float(w0 << 16), -e),
-                                         scalbnf(__uint_as_float(w0 & 0xffff0000u), -e));
-            qf[c][k][nt][1] = pack_half2(scalbnf(__uint_as_float(w1 << 16), -e),
-                                         scalbnf(__uint_as_float(w1 & 0xffff0000u), -e));
+            qf[c][k][nt][0] = pack_half2(__uint_as_float(w0 << 16) * down * down2,
+                                         __uint_as_float(w0 & 0xffff0000u) * down * down2);
+            qf[c][k][nt][1] = pack_half2(__uint_as_float(w1 << 16) * down * down2,
+                                         __uint_as_float(w1 & 0xffff0000u) * down * down2);
           }
         // columns 2 t and 2 t + 1 are heads of lanes 8 t and 8 t + 4
-        const float f = scalbnf(a.scale_log2 * ks, e);
+        const float f = a.scale_log2 * ks * power_of_two(e >> 1) * power_of_two(e - (e >> 1));
         cs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
         cs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
         m[nt][0] = m[nt][1] = -INFINITY;
@@ -456,11 +494,11 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
           for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.0f;
       }
     }
-    if (valid != 0) {
-      const bool whole = valid == 0xffffffffu;
-      float z[2][NT][4];
+    if ((valid[0] | valid[1]) != 0) {
+      const bool whole = (valid[0] & (kHalves > 1 ? valid[1] : 0xffffffffu)) == 0xffffffffu;
+      float z[kMt][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < kMt; ++mt) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -498,28 +536,34 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
       }
       if (!whole) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (!((valid >> (16 * mt + gq + 8 * (k >> 1))) & 1u))
+            if (!((valid[mt >> 1] >> (16 * (mt & 1) + gq + 8 * (k >> 1))) & 1u))
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) z[mt][nt][k] = -INFINITY;
       }
       // The lane's own scores first: the maximum of a column is only needed where
       // one passes the running one by 2^8 (in the products' own scale: zt).
+      auto top_of = [&](int nt, int e) {
+        float y = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
+#pragma unroll
+        for (int mt = 1; mt < kMt; ++mt) y = max3(y, z[mt][nt][e], z[mt][nt][e + 2]);
+        return y;
+      };
       bool up = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          up |= fmaxf(max3(z[0][nt][e], z[0][nt][e + 2], z[1][nt][e]), z[1][nt][e + 2]) > zt[nt][e];
+          up |= top_of(nt, e) > zt[nt][e];
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float y = fmaxf(max3(z[0][nt][e], z[0][nt][e + 2], z[1][nt][e]), z[1][nt][e + 2]);
+            float y = top_of(nt, e);
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
@@ -543,13 +587,13 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
           }
         }
       }
-      uint32_t pf[2][NT][2];
+      uint32_t pf[kMt][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint64_t c2 = pair2(cs[nt][0], cs[nt][1]);
         uint64_t sum = pair2(l[nt][0], l[nt][1]);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float2 y = split2(fma2(pair2(z[mt][nt][2 * k], z[mt][nt][2 * k + 1]), c2, r2[nt]));
@@ -562,12 +606,10 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
         l[nt][1] = l2.y;
       }
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < kMt; ++mt) {
         // positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the 16
         const uint32_t ra = base + (16 * mt + 2 * t) * RB;
-        // scales of unusable positions become 0: their weight is 0, but what
-        // the row holds there may be NaN
-        const uint32_t v4 = valid >> (16 * mt + 2 * t);
+        const uint32_t v4 = valid[mt >> 1] >> (16 * (mt & 1) + 2 * t);
         const uint32_t keep_ab = ((v4 & 1u) ? 0xffu : 0u) | ((v4 & 2u) ? 0xff00u : 0u);
         const uint32_t keep_cd = ((v4 & 0x100u) ? 0xffu : 0u) | ((v4 & 0x200u) ? 0xff00u : 0u);
 #pragma unroll
@@ -609,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
     }
     __syncwarp();  // every lane has read the stage and what it held
     request();
-    if (what.y & kLast) {
+    if (part & kLast) {
       int hk, h0, heads;
       heads_of_item(&hk, &h0, &heads);
       // ---- join the warps: references and sums, then O in three rounds
@@ -675,8 +717,8 @@ __global__ void __launch_bounds__(kThreads, NC <= 2 && NT == 1 ? 2 : 1)
       }
       if (warp == 0) {
         // the lane's eight dims 64 c + 8 gq of columns 2 t and 2 t + 1
-        const bool whole = (what.y & kFromStart) && (what.y & kToEnd);
-        const int slot = 2 * blockIdx.x + ((what.y & kFromStart) ? 1 : 0);
+        const bool whole = (part & kFromStart) && (part & kToEnd);
+        const int slot = 2 * blockIdx.x + ((part & kFromStart) ? 1 : 0);
         const float vs = a.v_scale ? __ldg(&a.v_scale[hk]) : 1.0f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -801,6 +843,9 @@ int chunks_of(int Dk, int Dv) {
   const int n = (std::max(Dk, Dv) + 63) / 64;
   return n > 2 ? 4 : n;
 }
+// Positions of a warp's tile: what a tile costs beside its rows weighs most where
+// the rows are short.
+constexpr int rows_of(int nc, int heads) { return nc == 1 ? 64 : 32; }
 int heads_of(int Dk, int Dv, int G) { return G > 8 && chunks_of(Dk, Dv) <= 2 ? 16 : 8; }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -818,20 +863,20 @@ Layout ws_layout(int B, int Dk, int Dv, int G) {
   return w;
 }
 
-template <int NC, int NT, bool kFull>
+template <int NC, int NT, int RW, bool kFull>
 int launch(Geo& g, cudaStream_t s, long long bound, int* ctas_out) {
   using Sh = Shared<NC, NT>;
-  constexpr int per = NC <= 2 && NT == 1 ? 2 : 1;
-  const int stage = kUnit * g.a.row_bytes;  // of all warps
+  constexpr int per = per_sm(NC, NT, RW);
+  const int stage = RW * kWarps * g.a.row_bytes;  // of all warps
   const int room = 227 * 1024 / per - 1024 * (per - 1) - Sh::kRing;
   g.stages = std::min(kMaxStages, room / stage);
   const int smem = Sh::kRing + g.stages * stage;
-  const void* k = (const void*)k_cache4_attn<NC, NT, kFull>;
+  const void* k = (const void*)k_cache4_attn<NC, NT, RW, kFull>;
   int rc = ensure_dynamic_smem(k, smem, "cache4_attn_decode");
   if (rc) return rc;
   const int ctas = (int)std::min<long long>(std::min(kMaxCtas, per * sm_count()), std::max(1LL, bound));
   *ctas_out = ctas;
-  const cudaError_t e = launch_pdl(k_cache4_attn<NC, NT, kFull>, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, s, g);
+  const cudaError_t e = launch_pdl(k_cache4_attn<NC, NT, RW, kFull>, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, s, g);
   count_launch();
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
   return check_launch("cache4_attn_decode");
@@ -861,22 +906,26 @@ int launch_cache4_attn(const Cache4AttnParams& p, void* ws, cudaStream_t s) {
   g.ml = reinterpret_cast<float2*>(base + w.ml);
   g.po = reinterpret_cast<float*>(base + w.po);
   const long long items = (long long)p.lay.batch * g.HH;
-  const long long bound = items * (((long long)p.lay.max_len + kUnit - 1) / kUnit);
+  const int rw = rows_of(nc, heads);
+  g.unit = rw * kWarps;
+  g.lgunit = rw == 64 ? 9 : 8;
+  const long long bound = items * (((long long)p.lay.max_len + g.unit - 1) / g.unit);
   if (bound > 0x7fffffffLL || items > 0x7fffffffLL)
     return set_error(DSA_ERR_UNSUPPORTED, "cache4_attn_decode: heads x positions beyond 2^31 units of 256");
-  g.one = p.lay.bs % kRowsW == 0;
+  if (g.HH >= 1 << 27) return set_error(DSA_ERR_UNSUPPORTED, "cache4_attn_decode: 2^27 blocks of heads or more");
+  g.one = p.lay.bs % rw == 0;
   const bool full = p.Dk == 64 * nc && p.Dv == 64 * nc;
   int ctas = 0, rc;
-  if (nc == 1 && heads == 8)
-    rc = full ? launch<1, 1, true>(g, s, bound, &ctas) : launch<1, 1, false>(g, s, bound, &ctas);
-  else if (nc == 1)
-    rc = full ? launch<1, 2, true>(g, s, bound, &ctas) : launch<1, 2, false>(g, s, bound, &ctas);
-  else if (nc == 2 && heads == 8)
-    rc = full ? launch<2, 1, true>(g, s, bound, &ctas) : launch<2, 1, false>(g, s, bound, &ctas);
+#define DSA_LAUNCH(NC, NT) \
+  (full ? launch<NC, NT, rows_of(NC, 8 * NT), true>(g, s, bound, &ctas) \
+        : launch<NC, NT, rows_of(NC, 8 * NT), false>(g, s, bound, &ctas))
+  if (nc == 1)
+    rc = heads == 8 ? DSA_LAUNCH(1, 1) : DSA_LAUNCH(1, 2);
   else if (nc == 2)
-    rc = full ? launch<2, 2, true>(g, s, bound, &ctas) : launch<2, 2, false>(g, s, bound, &ctas);
+    rc = heads == 8 ? DSA_LAUNCH(2, 1) : DSA_LAUNCH(2, 2);
   else
-    rc = full ? launch<4, 1, true>(g, s, bound, &ctas) : launch<4, 1, false>(g, s, bound, &ctas);
+    rc = DSA_LAUNCH(4, 1);
+#undef DSA_LAUNCH
   if (rc) return rc;
   const cudaError_t e = launch_pdl(k_cache4_merge, dim3((unsigned)items), dim3(256), 0, s, g, ctas, heads);
   count_launch();
