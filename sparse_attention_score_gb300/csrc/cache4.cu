@@ -12,13 +12,18 @@
 // a product of at most 7 significant bits that fp32 holds exactly, so no
 // division rounds an element over a midpoint; ties go to the even code.
 //
-// Both kernels take a group per thread: 32 bytes of bf16, 8 bytes of codes and
-// one scale.  They are bound by those bytes; see the launchers for figures.
+// Both kernels take half a group per thread, so that a warp's accesses of 16 bytes
+// of bf16 and of 4 bytes of codes lie side by side (with a group per thread the
+// two accesses of 16 bytes, or one of 32, took 1.3 times as long).  A thread keeps its place in a token's row (key head, group) and goes
+// from token to token, so that no division is left in the loop, the
+// tokens' places in the pool having been looked up once per block.  They are bound by those bytes; see
+// the launcher for figures.
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <string>
 
 #include "cache4.cuh"
@@ -30,162 +35,210 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kChunk = 64;
 
 struct Geo {
   Cache4RowsParams a;
-  int gk, groups;  // groups of 16 elements: of K, of K and V
-  long long units;  // N * Hk * groups
+  int gk, groups;  // groups of 16 elements of a row: of K, of K and V
+  int units;       // half groups of a token: 2 * Hk * groups
+  int tokens;      // tokens of a block at a time (0: one, its units in turn)
+  int chunk;       // tokens of a block, at most kChunk
 };
 
-// Row of the pool that token n's head h belongs to, -1 without one.
-__device__ __forceinline__ long long token_row(const Cache4RowsParams& a, long long n, int h) {
-  const int b = a.seq ? __ldg(&a.seq[n]) : (int)n;
-  if (b < 0 || b >= a.lay.batch) return -1;
-  const long long pos = a.pos ? __ldg(&a.pos[n]) : (long long)__ldg(&a.lay.seq_lens[b]) - 1;
-  if (pos < 0) return -1;
-  const long long slot = pos / a.lay.bs;
-  if (slot >= a.lay.maxb) return -1;
-  const int page = __ldg(&a.lay.bt[(long long)b * a.lay.maxb + slot]);
-  if (page < 0 || page >= a.lay.nb) return -1;
-  return ((long long)page * a.Hk + h) * a.lay.bs + (pos - slot * a.lay.bs);
-}
-
-struct Unit {
-  long long n;
-  int h, group, j;  // j: group of K or of V
+// A thread's place in a token: key head, group of the row, half of the group.
+struct Place {
+  int h, group, j, half;  // j: group of K or of V
   bool is_v;
+  __device__ __forceinline__ Place(const Geo& g, int unit) {
+    half = unit & 1;
+    h = (unit >> 1) / g.groups;
+    group = (unit >> 1) - h * g.groups;
+    is_v = group >= g.gk;
+    j = is_v ? group - g.gk : group;
+  }
 };
 
-__device__ __forceinline__ Unit unit_of(const Geo& g, long long u) {
-  Unit x;
-  long long row;
-  if (u >> 32) {
-    row = u / g.groups;
-    x.n = row / g.a.Hk;
-  } else {
-    row = (uint32_t)u / (uint32_t)g.groups;
-    x.n = (uint32_t)row / (uint32_t)g.a.Hk;
-  }
-  x.group = (int)(u - row * g.groups);
-  x.h = (int)(row - x.n * g.a.Hk);
-  x.is_v = x.group >= g.gk;
-  x.j = x.is_v ? x.group - g.gk : x.group;
-  return x;
+// Page of token n and its offset in it, -1 without one.
+__device__ __forceinline__ int token_page(const Cache4RowsParams& a, int n, int* off) {
+  const int b = a.seq ? __ldg(&a.seq[n]) : n;
+  if (b < 0 || b >= a.lay.batch) return -1;
+  const int pos = a.pos ? __ldg(&a.pos[n]) : __ldg(&a.lay.seq_lens[b]) - 1;
+  if (pos < 0) return -1;
+  const int slot = pos / a.lay.bs;
+  if (slot >= a.lay.maxb) return -1;
+  *off = pos - slot * a.lay.bs;
+  const int page = __ldg(&a.lay.bt[(long long)b * a.lay.maxb + slot]);
+  return page >= 0 && page < a.lay.nb ? page : -1;
 }
 
-// Byte offsets of a group's codes and scale within a row.
-__device__ __forceinline__ int codes_at(const Geo& g, int group) { return 8 * group; }
-__device__ __forceinline__ int scale_at(const Geo& g, int group) { return 8 * g.groups + group; }
-
-// The 16 values of a group: code * group scale (exact in fp16 and so in fp32)
-// * head scale, rounded once to bf16.
-__device__ __forceinline__ void kept_values(uint2 codes, uint32_t s8, float hs, uint4 (&o)[2]) {
+// The eight values of half a group: code * group scale (exact in fp16 and so in
+// fp32) * head scale, rounded once to bf16.
+__device__ __forceinline__ uint4 kept_values(uint32_t codes, uint32_t s8, float hs) {
   const __half_raw sr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3);
-  const float f = __half2float(__half(sr));
-  uint32_t w[8];
+  const __half2 f = __half2half2(__half(sr));
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t c = (i < 4 ? codes.x : codes.y) >> (8 * (i & 3));
-    const __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(c & 0xffu), __NV_E2M1);
-    const float2 v = __half22float2(__half2(hr));
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x * f * hs, v.y * f * hs);
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(codes >> (8 * i) & 0xffu), __NV_E2M1);
+    const float2 v = __half22float2(__hmul2(__half2(hr), f));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x * hs, v.y * hs);
     w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) k_cache4_write(const __grid_constant__ Geo g) {
+__device__ __forceinline__ float scale_value(uint32_t s8) {
+  const __half_raw sr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3);
+  return __half2float(__half(sr));
+}
+
+// x / d by a reciprocal r of d, correctly rounded for quotients well inside
+// fp32's range: the rounded product, its exact remainder, and one correction
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, d, x), r, q);
+}
+
+// Two codes of y / s; w: the elements' own bits, for the sign (also a zero's).  The
+// nearest E2M1 value of the quotient rounded to fp32 is that of the quotient itself
+// unless the rounding arrives at a midpoint between two codes: the remainder then
+// says on which side of it the quotient lies, and moves it there.  (Elements that
+// were not divided have 8 significant bits and s has 4: their quotient is a
+// midpoint or 2^-12 away from it.)
+__device__ __forceinline__ uint32_t two_codes(float y0, float y1, uint32_t w, float s, float r, bool divided) {
+  float q[2];
+  const float y[2] = {y0, y1};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float t = quotient(y[i], s, r);
+    int b = __float_as_int(t);
+    if (divided) {
+      const float rest = fmaf(-t, s, y[i]) * t;  // > 0: further from zero
+      b += rest > 0.0f;
+      b -= rest < 0.0f;
+    }
+    q[i] = __int_as_float((b & 0x7fffffff) | ((i ? w : w << 16) & 0x80000000u));
+  }
+  return __nv_cvt_float2_to_fp4x2(make_float2(q[0], q[1]), __NV_E2M1, cudaRoundNearest);
+}
+
+// Half a group of bf16 elements (the other half is the neighbour lane's): the
+// group's scale and the codes.
+template <bool scaled>
+__device__ __forceinline__ uint32_t quantise(uint4 in, float hs, uint32_t* codes) {
+  const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+  // the largest magnitude by its bits, so that a NaN is the largest of all
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
+  top = max(top, __shfl_xor_sync(3u << (threadIdx.x & 30), top, 1));
+  float most = __uint_as_float(top);
+  if (scaled) most = __fdiv_rn(most, hs);
+  const uint32_t s8 = __nv_cvt_float_to_fp8(__fdiv_rn(most, 6.0f), __NV_SATFINITE, __NV_E4M3);
+  const float s = scale_value(s8);
+  *codes = 0;
+  if (!(s > 0.0f)) return s8;  // codes 0 where the scale is 0 or NaN
+  const float r = __frcp_rn(s);
+  // The short division holds for quotients inside fp32's range: what lies below
+  // it has code 0 either way.
+  const bool plain = most < 1e30f && hs > 1e-20f && hs < 1e20f;
+  const float rh = scaled && plain ? __frcp_rn(hs) : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float y0 = __uint_as_float(w[i] << 16), y1 = __uint_as_float(w[i] & 0xffff0000u);
+    if (!plain) {
+      if (scaled) {
+        y0 = __fdiv_rn(y0, hs);
+        y1 = __fdiv_rn(y1, hs);
+      }
+      y0 = fminf(fmaxf(y0, -1e30f), 1e30f);  // far beyond 6 s <= 2688
+      y1 = fminf(fmaxf(y1, -1e30f), 1e30f);
+    } else if (scaled) {
+      y0 = quotient(y0, hs, rh);
+      y1 = quotient(y1, hs, rh);
+    }
+    *codes |= two_codes(y0, y1, w[i], s, r, scaled) << (8 * i);
+  }
+  return s8;
+}
+
+// A thread's half group of the block's tokens t, t + step, ...; rows: where each
+// token's row of head 0 begins in the pool, or -1.
+template <bool kWrite, bool kScaled>
+__device__ __forceinline__ void rows_of_unit(const Geo& g, int unit, const long long* rows, long long n0, int t,
+                                             int step, int n) {
+  constexpr int kBatch = kWrite ? 2 : 4;  // tokens in flight (a writer's registers are worth more warps)
   const Cache4RowsParams& a = g.a;
-  grid_dependency_wait();
-  launch_dependents();
-  const long long step = (long long)gridDim.x * kThreads;
-  for (long long u = (long long)blockIdx.x * kThreads + threadIdx.x; u < g.units; u += step) {
-    const Unit x = unit_of(g, u);
-    const __nv_bfloat16* src = x.is_v ? a.v + x.n * a.v_ts + x.h * a.v_hs : a.k + x.n * a.k_ts + x.h * a.k_hs;
-    const uint4* p = reinterpret_cast<const uint4*>(src + 16 * x.j);
-    const uint4 in[2] = {__ldg(p), __ldg(p + 1)};
-    const float* hp = x.is_v ? a.v_scale : a.k_scale;
-    const float hs = hp ? __ldg(&hp[x.h]) : 1.0f;
-    const long long row = token_row(a, x.n, x.h);
-    float y[16];
-    const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
+  const Place x(g, unit);
+  const float* hp = x.is_v ? a.v_scale : a.k_scale;
+  const float hs = hp ? __ldg(&hp[x.h]) : 1.0f;
+  const int D = x.is_v ? a.Dv : a.Dk, d = 16 * x.j + 8 * x.half;
+  const long long ts = x.is_v ? a.v_ts : a.k_ts;
+  const __nv_bfloat16* src =
+      kWrite ? (x.is_v ? a.v + x.h * a.v_hs : a.k + x.h * a.k_hs) + n0 * ts + d : nullptr;
+  const long long out_step = (long long)a.Hk * D;
+  __nv_bfloat16* out = x.is_v ? a.v_out : a.k_out;
+  if (out) out += n0 * out_step + (long long)x.h * D + d;
+  uint8_t* pool = a.pool + (long long)x.h * a.lay.bs * a.row_bytes;
+  const int at = 8 * x.group + 4 * x.half, scale_at = 8 * g.groups + x.group;  // in a row
+  for (int m0 = t; m0 < n; m0 += kBatch * step) {
+    uint4 in[kBatch];
+    uint32_t codes[kBatch], s8[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[2 * i] = __uint_as_float(w[i] << 16);
-      y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-    if (hp) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], hs);
-    }
-    // the largest magnitude by its bits, so that a NaN is the largest of all
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
-    const uint32_t s8 = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.0f), __NV_SATFINITE,
-                                              __NV_E4M3);
-    const __half_raw sr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3);
-    const float t = __half2float(__half(sr));
-    uint2 codes = make_uint2(0, 0);
-    if (t > 0.0f) {  // none where the scale is 0 or NaN
-      const float t0 = 0.25f * t, t1 = 0.75f * t, t2 = 1.25f * t, t3 = 1.75f * t, t4 = 2.5f * t,
-                  t5 = 3.5f * t, t6 = 5.0f * t;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float m = fabsf(y[i]);
-        uint32_t c = (m > t0) + (m >= t1) + (m > t2) + (m >= t3) + (m > t4) + (m >= t5) + (m > t6);
-        c |= (__float_as_uint(y[i]) >> 28) & 8u;
-        if (i < 8)
-          codes.x |= c << (4 * i);
-        else
-          codes.y |= c << (4 * (i - 8));
+    for (int i = 0; i < kBatch; ++i) {
+      const int m = m0 + i * step;
+      if (m >= n) break;
+      if (kWrite) {
+        in[i] = __ldg(reinterpret_cast<const uint4*>(src + m * ts));
+      } else {
+        codes[i] = s8[i] = 0;
+        if (rows[m] >= 0) {
+          codes[i] = __ldg(reinterpret_cast<const uint32_t*>(pool + rows[m] + at));
+          s8[i] = __ldg(pool + rows[m] + scale_at);
+        }
       }
     }
-    if (row >= 0) {
-      uint8_t* dst = a.pool + row * a.row_bytes;
-      *reinterpret_cast<uint2*>(dst + codes_at(g, x.group)) = codes;
-      dst[scale_at(g, x.group)] = (uint8_t)s8;
-      if (x.group == g.groups - 1)
-        for (int i = 9 * g.groups; i < a.row_bytes; ++i) dst[i] = 0;
-    } else if (x.group == 0) {
-      flag_status(a.status, DSA_STATUS_BAD_BLOCK);
-    }
-    __nv_bfloat16* out = x.is_v ? a.v_out : a.k_out;
-    if (out) {
-      uint4 o[2];
-      kept_values(codes, s8, hs, o);
-      const int D = x.is_v ? a.Dv : a.Dk;
-      uint4* q = reinterpret_cast<uint4*>(out + (x.n * a.Hk + x.h) * D + 16 * x.j);
-      q[0] = o[0];
-      q[1] = o[1];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int m = m0 + i * step;
+      if (m >= n) break;
+      if (kWrite) {
+        s8[i] = quantise<kScaled>(in[i], hs, &codes[i]);
+        if (rows[m] >= 0) {
+          uint8_t* p = pool + rows[m];
+          *reinterpret_cast<uint32_t*>(p + at) = codes[i];
+          if (x.half == 0) p[scale_at] = (uint8_t)s8[i];
+          if (x.group == g.groups - 1 && x.half)
+            for (int e = 9 * g.groups; e < a.row_bytes; ++e) p[e] = 0;
+        }
+      }
+      if (out) *reinterpret_cast<uint4*>(out + m * out_step) = kept_values(codes[i], s8[i], hs);
     }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) k_cache4_read(const __grid_constant__ Geo g) {
+template <bool kWrite, bool kScaled>
+__global__ void __launch_bounds__(kThreads, kWrite ? 5 : 1) k_cache4_rows(const __grid_constant__ Geo g) {
+  __shared__ long long rows[kChunk];
   const Cache4RowsParams& a = g.a;
   grid_dependency_wait();
   launch_dependents();
-  const long long step = (long long)gridDim.x * kThreads;
-  for (long long u = (long long)blockIdx.x * kThreads + threadIdx.x; u < g.units; u += step) {
-    const Unit x = unit_of(g, u);
-    const float* hp = x.is_v ? a.v_scale : a.k_scale;
-    const float hs = hp ? __ldg(&hp[x.h]) : 1.0f;
-    const long long row = token_row(a, x.n, x.h);
-    uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (row >= 0) {
-      const uint8_t* src = a.pool + row * a.row_bytes;
-      kept_values(__ldg(reinterpret_cast<const uint2*>(src + codes_at(g, x.group))),
-                  __ldg(src + scale_at(g, x.group)), hs, o);
-    } else if (x.group == 0) {
-      flag_status(a.status, DSA_STATUS_BAD_BLOCK);
-    }
-    __nv_bfloat16* out = x.is_v ? a.v_out : a.k_out;
-    const int D = x.is_v ? a.Dv : a.Dk;
-    uint4* q = reinterpret_cast<uint4*>(out + (x.n * a.Hk + x.h) * D + 16 * x.j);
-    q[0] = o[0];
-    q[1] = o[1];
+  const long long n0 = (long long)blockIdx.x * g.chunk;
+  const int n = (int)min((long long)g.chunk, a.N - n0);
+  if ((int)threadIdx.x < n) {
+    int off = 0;
+    const int page = token_page(a, (int)n0 + threadIdx.x, &off);
+    if (page < 0) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
+    rows[threadIdx.x] = page < 0 ? -1 : ((long long)page * a.Hk * a.lay.bs + off) * a.row_bytes;
+  }
+  __syncthreads();
+  if (g.tokens > 0) {
+    const int t = threadIdx.x / g.units, unit = threadIdx.x - t * g.units;
+    if (t < g.tokens) rows_of_unit<kWrite, kScaled>(g, unit, rows, n0, t, g.tokens, n);
+  } else {
+    for (int unit = threadIdx.x; unit < g.units; unit += kThreads) rows_of_unit<kWrite, kScaled>(g, unit, rows, n0, 0, 1, n);
   }
 }
 
@@ -196,12 +249,17 @@ int launch_cache4_rows(const Cache4RowsParams& p, bool write, cudaStream_t s) {
   g.a = p;
   g.gk = p.Dk / 16;
   g.groups = (p.Dk + p.Dv) / 16;
-  g.units = (long long)p.N * p.Hk * g.groups;
-  if (g.units == 0) return DSA_OK;
-  const long long blocks = (g.units + kThreads - 1) / kThreads;
-  const long long most = 16LL * sm_count();
-  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-  const cudaError_t e = launch_pdl(write ? k_cache4_write : k_cache4_read, dim3(grid), dim3(kThreads), 0, s, g);
+  if (p.N == 0) return DSA_OK;
+  g.units = 2 * p.Hk * g.groups;
+  g.tokens = kThreads / g.units;
+  // as few tokens a block as fill the GPU, in whole passes of the block
+  const int pass = std::max(g.tokens, 1), want = (int)((p.N + 8LL * sm_count() - 1) / (8LL * sm_count()));
+  g.chunk = std::min(kChunk, (want + pass - 1) / pass * pass);
+  const unsigned grid = (unsigned)((p.N + (long long)g.chunk - 1) / g.chunk);
+  const cudaError_t e = launch_pdl(!write                      ? k_cache4_rows<false, false>
+                             : p.k_scale || p.v_scale ? k_cache4_rows<true, true>
+                                                      : k_cache4_rows<true, false>,
+                             dim3(grid), dim3(kThreads), 0, s, g);
   count_launch();
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
   return check_launch(write ? "cache4_write" : "cache4_read");
