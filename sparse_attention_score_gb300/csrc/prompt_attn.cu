@@ -78,8 +78,10 @@ struct Item {
   int nq, nk, k0; // of the sequence
   int hk, h0;     // key head, first query head
   int v0, dv;     // columns of V
-  int n[2];       // key tiles of A and B
+  int j0;         // the first key tile of the item
+  int n[2];       // key tiles of A and B from there on
   int lim;        // keys that the first row sees
+  int slot;       // of the partial result, -1: the item sees all its keys' tiles
 };
 
 struct Smem {
@@ -99,9 +101,17 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
+constexpr int kMinPiece = 6;            // key tiles that a piece of a cut item has at least
+constexpr int kSlotRows = 2 * kTile;
+
 struct Geo {
   PromptAttnParams a;
+  int slots;          // partial results that the workspace holds, 0: no item is cut
+  int ctas;
+  float2* ml;         // [slot][256] (maximum, sum)
+  float* po;          // [slot][columns / 4][256][4]
   int G, lgp, HB;     // query heads per key head, log2 of gp, G / gp
+  int lgpair;         // log2 of a pair's tokens
   int VH;             // items per head over V's columns
   int HH;             // items per pair of tiles
   int nkc;            // chunks of Q and K
@@ -276,75 +286,187 @@ __device__ __forceinline__ bool sequence(const PromptAttnParams& a, int b, int* 
   return good;
 }
 
-__device__ __forceinline__ int visible(int tok, int nq, int nk) {  // keys that a token sees
+__host__ __device__ __forceinline__ int visible(int tok, int nq, int nk) {  // keys that a token sees
   const long long v = (long long)tok + 1 + nk - nq;
   return v < 0 ? 0 : (int)(v > nk ? nk : v);
 }
 
-__device__ __forceinline__ long long scan_add(long long v, int lane) {
+__device__ __forceinline__ int scan_add(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
 }
 
-// The sequence that item `at` belongs to, found from the last one on.
-struct Finder {
-  int b0 = 0;             // a group of 32 sequences
-  long long base = 0;     // items before it
-  long long mine = 0, end = 0;  // of this lane's sequence: items, where they end
-  int q0 = 0, nq = 0, k0 = 0, nk = 0;
-  __device__ __forceinline__ void load(const Geo& g, int lane) {
-    const int b = b0 + lane;
-    mine = 0;
-    if (b < g.a.B) {
-      if (!sequence(g.a, b, &q0, &nq, &k0, &nk)) flag_status(g.a.status, DSA_STATUS_BAD_LENGTH);
-      const int per = 2 * kTile >> g.lgp;
-      mine = (long long)((nq + (long long)per - 1) / per) * g.HH;
-    }
-    end = base + scan_add(mine, lane);
+// One sequence's items.  Pairs of tiles are counted from the last token's on, so
+// that the number of keys that they see falls.  (Counts fit 32 bits: the host
+// refuses more items.)
+struct Seq {
+  int q0, nq, k0, nk;
+  int pairs;       // pairs of tiles, of 2^lg tokens
+  int most;        // key tiles of the first pair
+  int cut, pieces; // the first `cut` pairs are cut in up to `pieces` pieces
+  __host__ __device__ __forceinline__ int tiles_of(int lg, int pair) const {
+    const long long end = (long long)(pairs - pair) << lg;
+    return (visible((int)(end < nq ? end : nq) - 1, nq, nk) + kTile - 1) / kTile;
   }
-  __device__ bool find(const Geo& g, long long at, int lane, Item* it) {
+  __host__ __device__ __forceinline__ void shape(int lg) {
+    pairs = (int)(((long long)nq + (1 << lg) - 1) >> lg);
+    most = pairs > 0 ? tiles_of(lg, 0) : 0;
+    cut = 0;
+    pieces = 1;
+  }
+  // about the key tiles of all pairs: they fall evenly to the last pair that sees any
+  __host__ __device__ __forceinline__ float work(int lg) const {
+    if (pairs == 0) return 0.0f;
+    const int least = tiles_of(lg, pairs - 1);
+    const int some = least > 0 ? pairs : (nk >> lg) + 1;
+    return 0.5f * (float)(some < pairs ? some : pairs) * (float)(most + least + 1);
+  }
+  // Pairs of N >= 2 c key tiles are cut in N / c pieces (c tiles and less than c
+  // more, so that an even share stays one): those whose last token sees more than
+  // (2 c - 1) * 128 keys.
+  __device__ __forceinline__ void cut_at(int lg, int c) {
+    if (c <= 0 || most < 2 * c) return;
+    pieces = most / c;
+    const long long first = (long long)(2 * c - 1) * kTile + nq - nk;  // the first such token
+    const long long below = first <= 0 ? 0 : first >> lg;              // pairs that end before it
+    cut = below < pairs ? pairs - (int)below : 0;
+  }
+};
+
+// Key tiles of a piece: an even share of the work, but no less than pays for a
+// partial result and the join; 0 where nothing is cut.
+__host__ __device__ __forceinline__ int piece_of(float work, int HH, int ctas) {
+  const float c = ceilf(work * (float)HH / (float)ctas);
+  return c < (float)kMinPiece ? kMinPiece : c < 1e6f ? (int)c : 1000000;
+}
+
+// Read by every CTA and by the join from the same lengths.
+__device__ __forceinline__ int piece_tiles(const Geo& g, int lane) {
+  if (g.slots == 0) return 0;
+  float sum = 0.0f;
+  for (int b0 = 0; b0 < g.a.B; b0 += 32) {
+    Seq s;
+    s.nq = s.nk = 0;
+    if (b0 + lane < g.a.B) sequence(g.a, b0 + lane, &s.q0, &s.nq, &s.k0, &s.nk);
+    s.shape(g.lgpair);
+    sum += s.work(g.lgpair);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return piece_of(sum, g.HH, g.ctas);
+}
+
+// Sequences in groups of 32, a lane each: items and slots of the partial results,
+// counted up from group to group.
+struct Group {
+  int b0 = -32;
+  int base = 0, end = 0, mine = 0;     // items: before the group, up to this lane's sequence, its own
+  int sbase = 0, send = 0, smine = 0;  // slots
+  Seq s;
+  __device__ __forceinline__ bool next(const Geo& g, int c, int lane, bool flag) {
+    b0 += 32;
+    if (b0 >= g.a.B) return false;
+    if (b0 > 0) {
+      base = __shfl_sync(0xffffffffu, end, 31);
+      sbase = __shfl_sync(0xffffffffu, send, 31);
+    }
+    s.q0 = s.nq = s.k0 = s.nk = 0;
+    if (b0 + lane < g.a.B && !sequence(g.a, b0 + lane, &s.q0, &s.nq, &s.k0, &s.nk) && flag)
+      flag_status(g.a.status, DSA_STATUS_BAD_LENGTH);
+    s.shape(g.lgpair);
+    s.cut_at(g.lgpair, c);
+    // (an even share needs about two slots per SM; where that does not hold, what
+    // has no slots is not cut)
+    smine = min((long long)s.cut * s.pieces * g.HH, (long long)g.slots + 1);
+    send = sbase + scan_add(smine, lane);
+    if (send > g.slots) {
+      s.cut = 0;
+      s.pieces = 1;
+      send = g.slots;  // (and nothing behind it is)
+    }
+    mine = (s.pairs + s.cut * (s.pieces - 1)) * g.HH;
+    end = base + scan_add(mine, lane);
+    return true;
+  }
+};
+
+// The item `at`, found from the last one on.
+struct Finder {
+  Group grp;
+  int c = 0;
+  __device__ __forceinline__ void init(const Geo& g, int lane) {
+    c = piece_tiles(g, lane);
+    grp.next(g, c, lane, true);
+  }
+  // 1: an item, 0: none are left, 2: an empty piece
+  __device__ int find(const Geo& g, int at, int lane, Item* it) {
     for (;;) {
-      const unsigned hit = __ballot_sync(0xffffffffu, end > at);
+      const unsigned hit = __ballot_sync(0xffffffffu, grp.end > at);
       if (hit) {
         const int l = __ffs(hit) - 1;
-        const long long first = __shfl_sync(0xffffffffu, end - mine, l);
-        const int items = (int)(__shfl_sync(0xffffffffu, mine, l) / g.HH);
-        const int sq0 = __shfl_sync(0xffffffffu, q0, l), snq = __shfl_sync(0xffffffffu, nq, l);
-        const int sk0 = __shfl_sync(0xffffffffu, k0, l), snk = __shfl_sync(0xffffffffu, nk, l);
-        const long long r = at - first;
-        const int pair = (int)(r / g.HH);
-        int x = (int)(r - (long long)pair * g.HH);
-        const int vh = x % g.VH;
-        x /= g.VH;
+        auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
+        Seq s;
+        s.q0 = of(grp.s.q0);
+        s.nq = of(grp.s.nq);
+        s.k0 = of(grp.s.k0);
+        s.nk = of(grp.s.nk);
+        s.pairs = of(grp.s.pairs);
+        s.cut = of(grp.s.cut);
+        s.pieces = of(grp.s.pieces);
+        int r = at - of(grp.end - grp.mine);
+        const int slot0 = of(grp.send - grp.smine), in_cut = s.cut * s.pieces * g.HH;
+        int pair, piece = 0, x;
+        it->slot = -1;
+        if (r < in_cut) {
+          const int each = s.pieces * g.HH;
+          pair = r / each;
+          const int y = r - pair * each;
+          piece = y / g.HH;
+          x = y - piece * g.HH;
+          it->slot = slot0 + (pair * g.HH + x) * s.pieces + piece;
+        } else {
+          r -= in_cut;
+          pair = r / g.HH;
+          x = r - pair * g.HH;
+          pair += s.cut;
+        }
+        const int vh = g.VH == 2 ? x & 1 : 0;
+        x >>= g.VH - 1;
         const int hb = x % g.HB;
         it->end = 0;
         it->hk = x / g.HB;
         it->h0 = it->hk * g.G + (hb << g.lgp);
         const int per = kTile >> g.lgp;
-        it->tok = (items - 1 - pair) * 2 * per;  // late tokens first
-        it->q0 = sq0 + it->tok;
-        it->nq = snq;
-        it->nk = snk;
-        it->k0 = sk0;
+        it->tok = (s.pairs - 1 - pair) * 2 * per;
+        it->q0 = s.q0 + it->tok;
+        it->nq = s.nq;
+        it->nk = s.nk;
+        it->k0 = s.k0;
         it->v0 = vh * kVWidth;
         it->dv = min(g.a.Dv - it->v0, kVWidth);
-        it->lim = visible(it->tok, snq, snk);
+        it->lim = visible(it->tok, s.nq, s.nk);
+        int j1 = 1 << 30;
+        it->j0 = 0;
+        if (it->slot >= 0) {
+          const int N = s.tiles_of(g.lgpair, pair), used = N / c, width = (N + used - 1) / used;
+          if (piece >= used) return 2;
+          it->j0 = piece * width;
+          j1 = it->j0 + width;
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int first_tok = it->tok + t * per;
-          const int last = min(first_tok + per, snq) - 1;
-          it->n[t] = first_tok < snq ? (visible(last, snq, snk) + kTile - 1) / kTile : 0;
+          const int last = min(first_tok + per, s.nq) - 1;
+          const int n = first_tok < s.nq ? (visible(last, s.nq, s.nk) + kTile - 1) / kTile : 0;
+          it->n[t] = max(min(n, j1) - it->j0, 0);
         }
-        return true;
+        return 1;
       }
-      base = __shfl_sync(0xffffffffu, end, 31);
-      b0 += 32;
-      if (b0 >= g.a.B) return false;
-      load(g, lane);
+      if (!grp.next(g, c, lane, true)) return 0;
     }
   }
 };
@@ -433,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     it.n[0] = uniform(x.n[0]);
     it.n[1] = uniform(x.n[1]);
     it.lim = uniform(x.lim);
+    it.j0 = uniform(x.j0);
     item_done();
     return true;
   };
@@ -441,17 +564,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
       // --------------------------------------------------------- producer --
       Finder f;
-      f.load(g, lane);
+      f.init(g, lane);
       int rs = 0;
       uint32_t rphase = 1;  // an empty ring's barriers have completed "phase 1"
       int nfill = 0, nv = 0, nq[2] = {0, 0};
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        int at = 0;
-        if (lane == 0) at = atomicAdd(g.next, 1);
-        at = uniform(at);
         Item it;
-        const bool have = f.find(g, at, lane, &it);
+        int found;
+        do {
+          int at = 0;
+          if (lane == 0) at = atomicAdd(g.next, 1);
+          found = f.find(g, uniform(at), lane, &it);
+        } while (found == 2);
+        const bool have = found == 1;
         it.end = have ? 0 : 1;
         const int s = k % kSlots;
         if (!warp_wait(smem_u32(&sm.iempty[s]), ((k / kSlots) & 1) ^ 1, &sm.abort)) { ok = false; break; }
@@ -487,9 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nq[t];
         }
         for (int j = 0; j < N && ok; ++j) {
-          for (int c = 0; c < nkc && ok; ++c) ok = fill(&maps.k, kChunk * c, it.hk, it.k0 + kTile * j);
-          for (int c = 0; c < nvc && ok; ++c) ok = fill(&maps.v, it.v0 + kChunk * c, it.hk, it.k0 + kTile * j);
-          if (j >= it.lim / kTile) {
+          for (int c = 0; c < nkc && ok; ++c) ok = fill(&maps.k, kChunk * c, it.hk, it.k0 + kTile * (it.j0 + j));
+          for (int c = 0; c < nvc && ok; ++c) ok = fill(&maps.v, it.v0 + kChunk * c, it.hk, it.k0 + kTile * (it.j0 + j));
+          if (it.j0 + j >= it.lim / kTile) {
             ++nv;
             __syncwarp();
             if (lane == 0) count_set(&sm.vissued, nv);
@@ -526,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int N = max(it.n[0], it.n[1]);
         const int nvc = (it.dv + kChunk - 1) / kChunk;
         const bool brief = it.lim <= kShort;
-        const int jm = it.lim / kTile;  // from this tile on V is looked through
+        const int jm = max(it.lim / kTile - it.j0, 0);  // from this tile on V is looked through
         int vs = 0;                     // first chunk of V of the tile before
         uint32_t vturn = 0;             // ... and its phase
         // waits for chunks s .. s + n - 1 of the ring, s being in phase `turn`
@@ -634,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && next_item(it)) {
         const int N = max(it.n[0], it.n[1]);
         const int nvc = (it.dv + kChunk - 1) / kChunk;
-        const int jm = it.lim / kTile;
+        const int jm = max(it.lim / kTile - it.j0, 0);
         int* odds = sm.odd[warp - 10];
         const int slot = k % (2 * kSlots);
         ++k;
@@ -658,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j < jm) continue;
             if (!warp_wait(smem_u32(&sm.full[rs]), rphase, &sm.abort)) { ok = false; break; }
             uint4* chunk = reinterpret_cast<uint4*>(rptr + rs * kChunkBytes);
-            const int rows = min(seen - kTile * j, kTile);  // of the tile that some row sees
+            const int rows = min(seen - kTile * (it.j0 + j), kTile);  // of the tile that some row sees
             // warp 10 takes even groups of four rows, warp 11 odd ones
 #pragma unroll 4
             for (int i = warp - 10; i < kTile / 4; i += 2) {
@@ -711,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool brief = it.lim <= kShort;
       float m = -INFINITY, l = 0.0f;
       // columns of the tile that this row sees
-      int see = token() < it.nq ? visible(token(), it.nq, it.nk) : 0;
+      int see = token() < it.nq ? visible(token(), it.nq, it.nk) - kTile * it.j0 : 0;
 #pragma unroll 1
       for (int left = it.n[t]; left > 0; --left, see -= kTile) {
         if (!warp_wait(smem_u32(&sm.sfull[t]), sphase, &sm.abort)) { ok = false; break; }
@@ -838,7 +964,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = tok < it.nq;
       const int head = it.h0 + (row & ((1 << g.lgp) - 1));
       const long long tr = (long long)it.q0 + t * per + (row >> g.lgp);
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int slot_out = it.slot;  // of a partial result
+      const float inv = l == 0.0f ? 0.0f : slot_out >= 0 ? 1.0f : 1.0f / l;
       const bool odd = (sm.odd[0][slot] | sm.odd[1][slot]) != 0;
       __nv_bfloat16* out = a.out + tr * a.o_ts + (long long)head * a.o_hs + it.v0;
 #pragma unroll 1
@@ -853,7 +980,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 32; ++i) x[i] = any ? __uint_as_float(v[i]) * inv : 0.0f;
         if (odd && mine) {
           // infinities and NaN that were kept out of the products
-          for (int p = it.lim / kTile * kTile; p < lim; ++p) {
+          const int p1 = min(lim, kTile * (it.j0 + it.n[t]));
+          for (int p = max(it.lim / kTile, it.j0) * kTile; p < p1; ++p) {
             const __nv_bfloat16* vr = a.v + (long long)(it.k0 + p) * a.v_ts + (long long)it.hk * a.v_hs + it.v0;
             for (int i = 0; i < 32; ++i)
               if (32 * q + i < it.dv) {
@@ -862,7 +990,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
           }
         }
-        if (mine) {
+        if (mine && slot_out >= 0) {
+          float4* po = reinterpret_cast<float4*>(g.po) + ((size_t)slot_out * (kVWidth / 4) + 8 * q) * kSlotRows + kTile * t + row;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (32 * q + 4 * i < it.dv)
+              po[(size_t)i * kSlotRows] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        } else if (mine) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (32 * q + 8 * i >= it.dv) break;
@@ -877,7 +1011,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      if (mine && a.lse && it.v0 == 0)
+      if (mine && slot_out >= 0) g.ml[(size_t)slot_out * kSlotRows + kTile * t + row] = make_float2(m, l);
+      if (mine && slot_out < 0 && a.lse && it.v0 == 0)
         a.lse[tr * a.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
     if (!ok && lane == 0) fail(sm, a.status);
@@ -912,6 +1047,127 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// The join of the pieces of cut items: a block takes 32 rows of an item at a time
+// (a lane each), a warp every eighth group of four columns.
+__global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ Geo g) {
+  constexpr int kBatch = 2;
+  const PromptAttnParams& a = g.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();
+  launch_dependents();
+  const int c = piece_tiles(g, lane);
+  Group grp;
+  int first = 0;  // cut items before the group
+  while (grp.next(g, c, lane, false)) {
+    const int own = grp.s.cut * g.HH, upto = scan_add(own, lane);
+    const int all = __shfl_sync(0xffffffffu, upto, 31);
+    // unit u: item u / 8 of the group, 32 rows of it
+    int u = ((int)blockIdx.x - 8 * first) % (int)gridDim.x;
+    if (u < 0) u += gridDim.x;
+    for (; u < 8 * all; u += gridDim.x) {
+      const int item = u >> 3;
+      const int l = __ffs(__ballot_sync(0xffffffffu, upto > item)) - 1;
+      auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
+      Seq s;
+      s.q0 = of(grp.s.q0);
+      s.nq = of(grp.s.nq);
+      s.nk = of(grp.s.nk);
+      s.pairs = of(grp.s.pairs);
+      s.pieces = of(grp.s.pieces);
+      const int r = item - of(upto - own), slot0 = of(grp.send - grp.smine);
+      const int pair = r / g.HH;
+      int x = r - pair * g.HH;
+      const int N = s.tiles_of(g.lgpair, pair), used = N / c;
+      const int slot = slot0 + r * s.pieces;
+      const int vh = g.VH == 2 ? x & 1 : 0;
+      x >>= g.VH - 1;
+      const int hk = x / g.HB, hb = x - hk * g.HB, per = kTile >> g.lgp;
+      const int row = 32 * (u & 7) + lane;
+      const int tok = (s.pairs - 1 - pair) * 2 * per + (row / kTile) * per + ((row % kTile) >> g.lgp);
+      const int head = hk * g.G + (hb << g.lgp) + (row & ((1 << g.lgp) - 1));
+      if (tok >= s.nq) continue;  // (a whole warp's or some lanes': no lane is waited for below)
+      const long long tr = (long long)s.q0 + tok;
+      const int v0 = vh * kVWidth, dv = min(a.Dv - v0, kVWidth);
+      const float2* ml = g.ml + (size_t)slot * kSlotRows + row;
+      float M = -INFINITY, l_sum = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < used; ++i) M = fmaxf(M, __ldcg(&ml[(size_t)i * kSlotRows]).x);
+      const float ref = M == -INFINITY ? 0.0f : M;
+#pragma unroll 4
+      for (int i = 0; i < used; ++i) {
+        const float2 st = __ldcg(&ml[(size_t)i * kSlotRows]);
+        if (st.y != 0.0f) l_sum = fmaf(st.y, exp2f(st.x - ref), l_sum);
+      }
+      const float inv = l_sum == 0.0f ? 0.0f : 1.0f / l_sum;
+      // the warp's four groups of columns at once, two partials in flight
+      constexpr int kGroups = kVWidth / 4 / 8;
+      const float4* po = reinterpret_cast<const float4*>(g.po) + ((size_t)slot * (kVWidth / 4) + warp) * kSlotRows + row;
+      float4 acc[kGroups];
+#pragma unroll
+      for (int d = 0; d < kGroups; ++d) acc[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < used; i0 += kBatch) {
+        float2 st[kBatch];
+        float4 v[kBatch][kGroups];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          st[e] = make_float2(-INFINITY, 0.0f);
+          if (i0 + e < used) st[e] = __ldcg(&ml[(size_t)(i0 + e) * kSlotRows]);
+#pragma unroll
+          for (int d = 0; d < kGroups; ++d) {
+            v[e][d] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + e < used && 4 * (warp + 8 * d) < dv)
+              v[e][d] = __ldcg(po + ((size_t)(i0 + e) * (kVWidth / 4) + 8 * d) * kSlotRows);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          if (st[e].y == 0.0f) continue;  // the row sees no key of the piece
+          const float w = exp2f(st[e].x - ref);
+#pragma unroll
+          for (int d = 0; d < kGroups; ++d) {
+            acc[d].x = fmaf(v[e][d].x, w, acc[d].x);
+            acc[d].y = fmaf(v[e][d].y, w, acc[d].y);
+            acc[d].z = fmaf(v[e][d].z, w, acc[d].z);
+            acc[d].w = fmaf(v[e][d].w, w, acc[d].w);
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < kGroups; ++d) {
+        const int x0 = 4 * (warp + 8 * d);
+        if (x0 >= dv) break;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[d].x * inv, acc[d].y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[d].z * inv, acc[d].w * inv);
+        *reinterpret_cast<uint2*>(a.out + tr * a.o_ts + (long long)head * a.o_hs + v0 + x0) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
+      if (warp == 0 && a.lse && v0 == 0)
+        a.lse[tr * a.Hq + head] = l_sum == 0.0f ? -INFINITY : (M + log2f(l_sum)) * 0.6931471805599453f;
+    }
+    first += all;
+  }
+}
+
+// Partial results that a call may need: none where there are items for every SM
+// several times over, else at most about two pieces per SM and one remainder each.
+constexpr int kMaxSlots = 384;
+struct Shape {
+  int G, lgp, HB, VH, HH;
+  long long items;  // at most
+};
+Shape shape_of(int B, int Nq, int Hq, int Hk, int Dv) {
+  Shape s{};
+  s.G = Hq / Hk;
+  while (s.lgp < 7 && s.G % (2 << s.lgp) == 0) ++s.lgp;
+  s.HB = s.G >> s.lgp;
+  s.VH = (Dv + kVWidth - 1) / kVWidth;
+  s.HH = Hk * s.HB * s.VH;
+  s.items = ((long long)Nq / (2 * kTile >> s.lgp) + B) * s.HH;
+  return s;
+}
+bool may_cut(const Shape& s) { return s.items < 4LL * sm_count(); }
+size_t ml_bytes() { return sizeof(float2) * kMaxSlots * kSlotRows; }
+
 int ring_of(int nkc) {
   const int room = 227 * 1024 - 1024 - (int)sizeof(Smem) - 2 * nkc * kChunkBytes;
   return std::min(kMaxRing, room / kChunkBytes);
@@ -919,23 +1175,43 @@ int ring_of(int nkc) {
 
 }  // namespace
 
-size_t prompt_attn_ws() { return kWsHeader; }
+size_t prompt_attn_ws(int B, int Nq, int Hq, int Hk, int Dv) {
+  if (!may_cut(shape_of(B, Nq, Hq, Hk, Dv))) return kWsHeader;
+  return kWsHeader + ml_bytes() + sizeof(float) * kMaxSlots * kSlotRows * kVWidth;
+}
 
 int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   Geo g{};
   g.a = p;
-  g.G = p.Hq / p.Hk;
-  while (g.lgp < 7 && g.G % (2 << g.lgp) == 0) ++g.lgp;
-  g.HB = g.G >> g.lgp;
-  g.VH = (p.Dv + kVWidth - 1) / kVWidth;
-  g.HH = p.Hk * g.HB * g.VH;
+  const Shape sh = shape_of(p.B, p.Nq, p.Hq, p.Hk, p.Dv);
+  g.G = sh.G;
+  g.lgp = sh.lgp;
+  g.HB = sh.HB;
+  g.lgpair = 8 - sh.lgp;
+  g.VH = sh.VH;
+  g.HH = sh.HH;
+  g.ctas = (int)std::min<long long>(sm_count(), sh.items);
+  // Whether anything may be cut: for one sequence its lengths say so, several may
+  // have any (but none more keys than there are).
+  bool cut = may_cut(sh) && ((long long)p.Nk + kTile - 1) / kTile >= 2 * kMinPiece;
+  if (cut && p.B == 1) {
+    Seq one{};
+    one.nq = p.Nq;
+    one.nk = p.Nk;
+    one.shape(g.lgpair);
+    cut = one.most >= 2 * piece_of(one.work(g.lgpair), g.HH, sm_count());
+  }
+  if (cut) {
+    g.slots = kMaxSlots;
+    g.ctas = sm_count();
+    g.ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + kWsHeader);
+    g.po = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + kWsHeader + ml_bytes());
+  }
   g.nkc = (p.Dk + kChunk - 1) / kChunk;
   g.ring = ring_of(g.nkc);
   g.next = reinterpret_cast<int*>(ws) + 16;
   g.left = reinterpret_cast<int*>(ws) + 32;
-  const int per = 2 * kTile >> g.lgp;
-  const long long bound = ((long long)p.Nq / per + p.B) * g.HH;
-  if (bound > 0x7fff0000LL)
+  if (sh.items > 0x7fff0000LL)
     return set_error(DSA_ERR_UNSUPPORTED, "prompt_attn: rows beyond 2^31 pairs of tiles of 128");
   Maps m{};
   int rc = make_tmap_heads(&m.q, p.q, p.Dk, p.Hq, p.Nq, p.q_hs, p.q_ts, kChunk, 1u << g.lgp, kTile >> g.lgp);
@@ -947,11 +1223,15 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   const int smem = 1024 + (2 * g.nkc + g.ring) * kChunkBytes + (int)sizeof(Smem);
   rc = ensure_dynamic_smem((const void*)k_prompt_attn, smem, "prompt_attn");
   if (rc) return rc;
-  const int ctas = (int)std::min<long long>(sm_count(), bound);
-  const cudaError_t e = launch_pdl(k_prompt_attn, dim3((unsigned)ctas), dim3(kThreads), (size_t)smem, s, m, g);
+  cudaError_t e = launch_pdl(k_prompt_attn, dim3((unsigned)g.ctas), dim3(kThreads), (size_t)smem, s, m, g);
   count_launch();
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
-  return check_launch("prompt_attn");
+  rc = check_launch("prompt_attn");
+  if (rc || g.slots == 0) return rc;
+  e = launch_pdl(k_prompt_merge, dim3((unsigned)(4 * sm_count())), dim3(256), 0, s, g);
+  count_launch();
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
+  return check_launch("prompt_attn merge");
 }
 
 }  // namespace dsa

@@ -19,7 +19,7 @@ struct PromptAttnParams {
   float* lse;  // [Nq][Hq] or NULL
   int* status;
 };
-size_t prompt_attn_ws();
+size_t prompt_attn_ws(int B, int Nq, int Hq, int Hk, int Dv);
 int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s);
 
 }  // namespace dsa
