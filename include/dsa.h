@@ -551,8 +551,8 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
  *     z_j = sm_scale * q[i][h] . k[j][h'],  out[i][h] = sum_j softmax(z)_j v[j][h'],
  *     lse[i][h] = log sum_j exp(z_j),  h' = h / (Hq / Hk)
  * A token that sees no key (nk < nq) has out 0 and lse -inf.  Scores, maxima and
- * sums are fp32.  A weight enters the product with V as bf16, off by at most 2^-9
- * of itself, and as bf16 hi + lo (2^-17) for the tokens whose tile begins with
+ * sums are fp32.  A weight enters the product with V as bf16, off by at most 2^-8
+ * of itself, and as bf16 hi + lo (2^-16) for the tokens whose tile begins with
  * one that sees no more than 512 keys; out is rounded once.  What a token does
  * not see does not reach it, NaN and infinities included.
  *  q, k, v     bf16: token i head h at ptr + i * token stride + h * head stride

@@ -116,8 +116,7 @@ __device__ __forceinline__ uint32_t two_codes(float y0, float y1, uint32_t w, fl
     int b = __float_as_int(t);
     if (divided) {
       const float rest = fmaf(-t, s, y[i]) * t;  // > 0: further from zero
-      b += rest > 0.0f;
-      b -= rest < 0.0f;
+      if ((b & 0xfffff) == 0) b += (rest > 0.0f) - (rest < 0.0f);  // (midpoints have 3 significant bits)
     }
     q[i] = __int_as_float((b & 0x7fffffff) | ((i ? w : w << 16) & 0x80000000u));
   }

@@ -484,6 +484,7 @@ int dsa_cache4_write(const dsa_paged_layout* layout, const int32_t* seq, const i
                      const float* k_scale, const float* v_scale, void* pool, void* k_out,
                      void* v_out, void* ws, size_t ws_bytes, dsa_stream_t stream) {
   Cache4RowsParams p{};
+  if (N == 0) return DSA_OK;
   if (!k || !v) return set_error(DSA_ERR_INVALID, "cache4_write: NULL tensor pointer");
   int rc = cache4_rows("cache4_write", layout, seq, pos, N, Hk, Dk, Dv, k_scale, v_scale, pool, k_out,
                        v_out, ws, ws_bytes, &p);
@@ -513,6 +514,7 @@ int dsa_cache4_read(const dsa_paged_layout* layout, const int32_t* seq, const in
                     const void* pool, void* k_out, void* v_out, void* ws, size_t ws_bytes,
                     dsa_stream_t stream) {
   Cache4RowsParams p{};
+  if (N == 0) return DSA_OK;
   if (!k_out || !v_out || !seq || !pos)
     return set_error(DSA_ERR_INVALID, "cache4_read: NULL tensor pointer");
   int rc = cache4_rows("cache4_read", layout, seq, pos, N, Hk, Dk, Dv, k_scale, v_scale, pool, k_out,

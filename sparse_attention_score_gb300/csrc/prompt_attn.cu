@@ -24,10 +24,10 @@
 // more than 128 columns is taken in two halves, each an item of its own that
 // computes S again.
 //
-// P is rounded to bf16 once (each weight by at most 2^-9 of itself, like the
+// P is rounded to bf16 once (each weight by at most 2^-8 of itself, like the
 // output), except where rows see few keys and such roundings do not average out:
 // an item whose first row sees no more than 512 keys keeps P as bf16 hi + lo
-// (2^-17), both multiplied with the same V.  Statistics and sums are fp32.
+// (2^-16), both multiplied with the same V.  Statistics and sums are fp32.
 //
 // What no row may see.  Scores of hidden keys are set to -inf by the row's own
 // limit.  V has no such place: a hidden row's weight is 0, but 0 times what an
@@ -81,6 +81,7 @@ struct Item {
   int j0;         // the first key tile of the item
   int n[2];       // key tiles of A and B from there on
   int lim;        // keys that the first row sees
+  int jm;         // the first key tile whose V is looked through
   int slot;       // of the partial result, -1: the item sees all its keys' tiles
 };
 
@@ -449,6 +450,8 @@ struct Finder {
         it->v0 = vh * kVWidth;
         it->dv = min(g.a.Dv - it->v0, kVWidth);
         it->lim = visible(it->tok, s.nq, s.nk);
+        // (lo of hi + lo may be 0 or negative: no infinity may meet it either)
+        it->jm = it->lim <= kShort ? 0 : it->lim / kTile;
         int j1 = 1 << 30;
         it->j0 = 0;
         if (it->slot >= 0) {
@@ -555,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     it.n[0] = uniform(x.n[0]);
     it.n[1] = uniform(x.n[1]);
     it.lim = uniform(x.lim);
+    it.jm = uniform(x.jm);
     it.j0 = uniform(x.j0);
     item_done();
     return true;
@@ -615,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < N && ok; ++j) {
           for (int c = 0; c < nkc && ok; ++c) ok = fill(&maps.k, kChunk * c, it.hk, it.k0 + kTile * (it.j0 + j));
           for (int c = 0; c < nvc && ok; ++c) ok = fill(&maps.v, it.v0 + kChunk * c, it.hk, it.k0 + kTile * (it.j0 + j));
-          if (it.j0 + j >= it.lim / kTile) {
+          if (it.j0 + j >= it.jm) {
             ++nv;
             __syncwarp();
             if (lane == 0) count_set(&sm.vissued, nv);
@@ -652,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int N = max(it.n[0], it.n[1]);
         const int nvc = (it.dv + kChunk - 1) / kChunk;
         const bool brief = it.lim <= kShort;
-        const int jm = max(it.lim / kTile - it.j0, 0);  // from this tile on V is looked through
+        const int jm = max(it.jm - it.j0, 0);  // from this tile on V is looked through
         int vs = 0;                     // first chunk of V of the tile before
         uint32_t vturn = 0;             // ... and its phase
         // waits for chunks s .. s + n - 1 of the ring, s being in phase `turn`
@@ -760,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && next_item(it)) {
         const int N = max(it.n[0], it.n[1]);
         const int nvc = (it.dv + kChunk - 1) / kChunk;
-        const int jm = max(it.lim / kTile - it.j0, 0);
+        const int jm = max(it.jm - it.j0, 0);
         int* odds = sm.odd[warp - 10];
         const int slot = k % (2 * kSlots);
         ++k;
@@ -981,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (odd && mine) {
           // infinities and NaN that were kept out of the products
           const int p1 = min(lim, kTile * (it.j0 + it.n[t]));
-          for (int p = max(it.lim / kTile, it.j0) * kTile; p < p1; ++p) {
+          for (int p = max(it.jm, it.j0) * kTile; p < p1; ++p) {
             const __nv_bfloat16* vr = a.v + (long long)(it.k0 + p) * a.v_ts + (long long)it.hk * a.v_hs + it.v0;
             for (int i = 0; i < 32; ++i)
               if (32 * q + i < it.dv) {
