@@ -226,6 +226,7 @@ struct Shared {
 
 // Flags of a unit, of its item's part in this CTA.
 constexpr uint32_t kFirst = 1, kLast = 2, kFromStart = 4, kToEnd = 8;
+constexpr uint32_t kEnd = 1u << 31;  // beside the sequence: the CTA's last unit
 
 // A load that stays where it is written, a unit ahead of its use.
 __device__ __forceinline__ int ld_early(const int32_t* p) {
@@ -325,13 +326,12 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
   Walk w = start_at(g, lo, mine, lane);
   int rs = 0, us = 0;           // stage to fill, stage to read
   uint32_t uphase = 0;
-  int pending = 0;              // stages filled and not yet waited for
-  int page[kHalves], poff[kHalves], rows = 0;
+  int page[kHalves], poff[kHalves];
   uint32_t flags = kFirst | (w.unit == 0 ? kFromStart : 0);
   bool ok = true;               // no wait of this CTA's ran out
   auto locate = [&] {  // page and row of this lane's positions of the unit
     const int p0 = w.unit * kUnit + warp * kRowsW;
-    rows = min(w.L - p0, kRowsW);
+    const int rows = min(w.L - p0, kRowsW);
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const int i = g.one ? 0 : 32 * h + lane;  // (one page holds the whole tile)
@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
   };
   auto request = [&] {
     if (w.left <= 0) return;
+    const int rows = min(w.L - (w.unit * kUnit + warp * kRowsW), kRowsW);
     uint32_t valid[2] = {0, 0};
     bool good[kHalves];
     if (g.one) {
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
     if (w.unit + 1 == w.n) flags |= kLast | kToEnd;
     if (w.left == 1) flags |= kLast;
     if (lane == 0) {
-      meta[rs] = make_uint4(valid[0], valid[1], (uint32_t)w.b, (uint32_t)w.hh << 4 | flags);
+      meta[rs] = make_uint4(valid[0], valid[1], (uint32_t)w.b | (w.left == 1 ? kEnd : 0u), (uint32_t)w.hh << 4 | flags);
       if (ok) mbar_arrive_expect_tx(&bars[rs], (uint32_t)(__popc(valid[0]) + __popc(valid[1])) * RB);
     }
     __syncwarp();
@@ -383,7 +384,6 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
       }
     }
     if (++rs == stages) rs = 0;
-    ++pending;
     flags = (flags & kLast) ? kFirst | kFromStart : flags & kFromStart;
     w.next(g);
     if (w.left > 0) locate();
@@ -397,37 +397,15 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
   uint32_t qf[NC][4][NT][2];
   float cs[NT][2];              // score factor of this lane's two columns
   float o[NT][NC * 4][4];
-  float m[NT][2], l[NT][2];     // running maximum (log2), sum of the lane's weights
-  float zt[NT][2];              // the product that passes the maximum by 2^8
-  uint64_t r2[NT];              // kLift - m of both columns
-  while (pending > 0) {
-    if (ok && !pair_wait(smem_u32(&bars[us]), uphase, abort)) {
-      ok = false;
-      if (lane == 0) {
-        *abort = 1;
-        flag_status(a.status, DSA_STATUS_TIMEOUT);
-      }
-      // this warp's copies still on their way have a moment to land
-      int never = 0, s = us;
-      uint32_t ph = uphase;
-      for (int i = 0; i < pending; ++i) {
-        pair_wait(smem_u32(&bars[s]), ph, &never, 10000000ull);
-        if (++s == stages) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-    }
+  float l[NT][2];               // sum of the lane's weights
+  float zt[NT][2];              // the product that passes the running maximum by 2^8; -inf: none yet
+  float r[NT][2];               // kLift - the running maximum (log2)
+  for (bool more = mine > 0; more;) {
     const uint4 what = meta[us];
-    const uint32_t valid[2] = {ok ? what.x : 0u, ok ? what.y : 0u};
     const uint32_t part = what.w & 15u;
     const uint32_t base = ring + us * stage_bytes;
-    if (++us == stages) {
-      us = 0;
-      uphase ^= 1;
-    }
-    --pending;
-    const int b = (int)what.z;
+    const int b = (int)(what.z & ~kEnd);
+    more = (what.z & kEnd) == 0;
     // key head, first query head of the block, heads of the block
     auto heads_of_item = [&](int* hk, int* h0, int* heads) {
       const int hh = (int)(what.w >> 4);
@@ -484,16 +462,39 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
         const float f = a.scale_log2 * ks * power_of_two(e >> 1) * power_of_two(e - (e >> 1));
         cs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
         cs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-        m[nt][0] = m[nt][1] = -INFINITY;
         l[nt][0] = l[nt][1] = 0.0f;
         zt[nt][0] = zt[nt][1] = -INFINITY;
-        r2[nt] = pair2(0.0f, 0.0f);
+        r[nt][0] = r[nt][1] = 0.0f;
 #pragma unroll
         for (int i = 0; i < NC * 4; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.0f;
       }
     }
+    // (the queries came in while the item's first rows were on their way)
+    if (ok && !pair_wait(smem_u32(&bars[us]), uphase, abort)) {
+      ok = false;
+      if (lane == 0) {
+        *abort = 1;
+        flag_status(a.status, DSA_STATUS_TIMEOUT);
+      }
+      // this warp's copies still on their way have a moment to land (a stage that
+      // holds none is waited for in vain)
+      int never = 0, s = us;
+      uint32_t ph = uphase;
+      for (int i = 0; i < stages; ++i) {
+        pair_wait(smem_u32(&bars[s]), ph, &never, 10000000ull);
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (++us == stages) {
+      us = 0;
+      uphase ^= 1;
+    }
+    const uint32_t valid[2] = {ok ? what.x : 0u, ok ? what.y : 0u};
     if ((valid[0] | valid[1]) != 0) {
       const bool whole = (valid[0] & (kHalves > 1 ? valid[1] : 0xffffffffu)) == 0xffffffffu;
       float z[kMt][NT][4];
@@ -570,14 +571,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
             f[e] = 1.0f;
             if (y > zt[nt][e]) {
               const float top = y * cs[nt][e];  // (cs > 0)
-              f[e] = ex2_approx(m[nt][e] - top);
-              m[nt][e] = top;
+              f[e] = zt[nt][e] == -INFINITY ? 0.0f : ex2_approx(kLift - r[nt][e] - top);
+              r[nt][e] = kLift - top;
               zt[nt][e] = y + kRescaleLog2 / cs[nt][e];
             }
           }
           l[nt][0] *= f[0];
           l[nt][1] *= f[1];
-          r2[nt] = pair2(kLift - m[nt][0], kLift - m[nt][1]);
 #pragma unroll
           for (int i = 0; i < NC * 4; ++i) {
             o[nt][i][0] *= f[0];
@@ -590,13 +590,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
       uint32_t pf[kMt][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint64_t c2 = pair2(cs[nt][0], cs[nt][1]);
+        const uint64_t c2 = pair2(cs[nt][0], cs[nt][1]), r2 = pair2(r[nt][0], r[nt][1]);
         uint64_t sum = pair2(l[nt][0], l[nt][1]);
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float2 y = split2(fma2(pair2(z[mt][nt][2 * k], z[mt][nt][2 * k + 1]), c2, r2[nt]));
+            const float2 y = split2(fma2(pair2(z[mt][nt][2 * k], z[mt][nt][2 * k + 1]), c2, r2));
             const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
             sum = add2(sum, pair2(e0, e1));
             pf[mt][nt][k] = transpose8(pack_half2(e0, e1));
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
           x += __shfl_xor_sync(0xffffffffu, x, 4);
           x += __shfl_xor_sync(0xffffffffu, x, 8);
           x += __shfl_xor_sync(0xffffffffu, x, 16);
-          if (gq == 0) ml[warp * kHeads + 8 * nt + 2 * t + e] = make_float2(m[nt][e], x);
+          if (gq == 0) ml[warp * kHeads + 8 * nt + 2 * t + e] = make_float2(zt[nt][e] == -INFINITY ? -INFINITY : kLift - r[nt][e], x);
         }
       __syncthreads();
       float sum[NT][2], top[NT][2];
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
           }
           top[nt][e] = M;
           sum[nt][e] = S;
-          const float f = ex2_approx(m[nt][e] - ref);
+          const float f = zt[nt][e] == -INFINITY ? 0.0f : ex2_approx(kLift - r[nt][e] - ref);
 #pragma unroll
           for (int i = 0; i < NC * 4; ++i) {
             o[nt][i][e] *= f;

@@ -379,6 +379,23 @@ struct Group {
     if (b0 + lane < g.a.B && !sequence(g.a, b0 + lane, &s.q0, &s.nq, &s.k0, &s.nk) && flag)
       flag_status(g.a.status, DSA_STATUS_BAD_LENGTH);
     s.shape(g.lgpair);
+    if (g.a.B > 1) {
+      // those that see most first: the last items to be taken are then small ones
+      int rank = 0, from = lane;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const int m = __shfl_sync(0xffffffffu, s.most, i);
+        rank += m > s.most || (m == s.most && i < lane);
+      }
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i)
+        if (__shfl_sync(0xffffffffu, rank, i) == lane) from = i;
+      s.q0 = __shfl_sync(0xffffffffu, s.q0, from);
+      s.nq = __shfl_sync(0xffffffffu, s.nq, from);
+      s.k0 = __shfl_sync(0xffffffffu, s.k0, from);
+      s.nk = __shfl_sync(0xffffffffu, s.nk, from);
+      s.shape(g.lgpair);
+    }
     s.cut_at(g.lgpair, c);
     // (an even share needs about two slots per SM; where that does not hold, what
     // has no slots is not cut)
