@@ -235,6 +235,10 @@ __device__ __forceinline__ int ld_early(const int32_t* p) {
   return r;
 }
 
+__device__ __forceinline__ void sts8(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ float power_of_two(int e) {  // -126 <= e <= 127
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
@@ -536,6 +540,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
         }
       }
       if (!whole) {
+        // The scales of V of unusable positions become 0: their weight is 0, but
+        // what the row holds there may be NaN.
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          if (!((valid[h] >> lane) & 1u))
+#pragma unroll 1
+            for (int j = 0; j < gv; ++j) sts8(base + (32 * h + lane) * RB + sv + j, 0);
+        __syncwarp();
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
@@ -609,9 +621,6 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
       for (int mt = 0; mt < kMt; ++mt) {
         // positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the 16
         const uint32_t ra = base + (16 * mt + 2 * t) * RB;
-        const uint32_t v4 = valid[mt >> 1] >> (16 * (mt & 1) + 2 * t);
-        const uint32_t keep_ab = ((v4 & 1u) ? 0xffu : 0u) | ((v4 & 2u) ? 0xff00u : 0u);
-        const uint32_t keep_cd = ((v4 & 0x100u) ? 0xffu : 0u) | ((v4 & 0x200u) ? 0xff00u : 0u);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           if (!kFull && NC > 1 && c >= ncv) break;
@@ -625,10 +634,6 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
             wd = lds32(at + 9 * RB);
             sab = lds8(st) | (lds8(st + RB) << 8);
             scd = lds8(st + 8 * RB) | (lds8(st + 9 * RB) << 8);
-          }
-          if (!whole) {
-            sab &= keep_ab;
-            scd &= keep_cd;
           }
           sab = widen_scales(sab);
           scd = widen_scales(scd);
