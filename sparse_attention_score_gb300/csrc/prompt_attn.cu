@@ -109,6 +109,7 @@ struct Geo {
   PromptAttnParams a;
   int slots;          // partial results that the workspace holds, 0: no item is cut
   int ctas;
+  int many;           // there may be more items than CTAs
   float2* ml;         // [slot][256] (maximum, sum)
   float* po;          // [slot][columns / 4][256][4]
   int G, lgp, HB;     // query heads per key head, log2 of gp, G / gp
@@ -309,6 +310,7 @@ struct Seq {
   int pairs;       // pairs of tiles, of 2^lg tokens
   int most;        // key tiles of the first pair
   int cut, pieces; // the first `cut` pairs are cut in up to `pieces` pieces
+  int tail, tpieces;  // the last `tail` pairs in up to `tpieces`
   __host__ __device__ __forceinline__ int tiles_of(int lg, int pair) const {
     const long long end = (long long)(pairs - pair) << lg;
     return (visible((int)(end < nq ? end : nq) - 1, nq, nk) + kTile - 1) / kTile;
@@ -316,8 +318,8 @@ struct Seq {
   __host__ __device__ __forceinline__ void shape(int lg) {
     pairs = (int)(((long long)nq + (1 << lg) - 1) >> lg);
     most = pairs > 0 ? tiles_of(lg, 0) : 0;
-    cut = 0;
-    pieces = 1;
+    cut = tail = 0;
+    pieces = tpieces = 1;
   }
   // about the key tiles of all pairs: they fall evenly to the last pair that sees any
   __host__ __device__ __forceinline__ float work(int lg) const {
@@ -325,6 +327,10 @@ struct Seq {
     const int least = tiles_of(lg, pairs - 1);
     const int some = least > 0 ? pairs : (nk >> lg) + 1;
     return 0.5f * (float)(some < pairs ? some : pairs) * (float)(most + least + 1);
+  }
+  // pieces of a cut pair of N key tiles
+  __device__ __forceinline__ int used(int N, int pair, int c) const {
+    return pair < cut ? N / c : max(min(tpieces, N / kMinPiece), 1);
   }
   // Pairs of N >= 2 c key tiles are cut in N / c pieces (c tiles and less than c
   // more, so that an even share stays one): those whose last token sees more than
@@ -345,20 +351,34 @@ __host__ __device__ __forceinline__ int piece_of(float work, int HH, int ctas) {
   return c < (float)kMinPiece ? kMinPiece : c < 1e6f ? (int)c : 1000000;
 }
 
+// Where items of about one size leave the last wave of CTAs mostly idle, those of
+// that wave are cut too: `rest` of `items` are over, of N key tiles each.
+__host__ __device__ __forceinline__ bool cut_tail(long long items, int ctas, int rest, int N) {
+  return items >= ctas && items < 12LL * ctas && rest > 0 && N >= 2 * kMinPiece &&
+         (long long)(ctas - rest) * N >= 8LL * ctas;
+}
+
 // Read by every CTA and by the join from the same lengths.
-__device__ __forceinline__ int piece_tiles(const Geo& g, int lane) {
-  if (g.slots == 0) return 0;
+struct Cuts {
+  int c;          // key tiles of a piece, 0: nothing is cut
+  int items;      // uncut
+};
+__device__ __forceinline__ Cuts find_cuts(const Geo& g, int lane) {
+  if (g.slots == 0) return Cuts{0, 0};
   float sum = 0.0f;
+  int pairs = 0;
   for (int b0 = 0; b0 < g.a.B; b0 += 32) {
     Seq s;
     s.nq = s.nk = 0;
     if (b0 + lane < g.a.B) sequence(g.a, b0 + lane, &s.q0, &s.nq, &s.k0, &s.nk);
     s.shape(g.lgpair);
     sum += s.work(g.lgpair);
+    pairs += s.pairs;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return piece_of(sum, g.HH, g.ctas);
+  if (g.many) pairs = __reduce_add_sync(0xffffffffu, pairs);
+  return Cuts{piece_of(sum, g.HH, g.ctas), pairs * g.HH};
 }
 
 // Sequences in groups of 32, a lane each: items and slots of the partial results,
@@ -368,7 +388,7 @@ struct Group {
   int base = 0, end = 0, mine = 0;     // items: before the group, up to this lane's sequence, its own
   int sbase = 0, send = 0, smine = 0;  // slots
   Seq s;
-  __device__ __forceinline__ bool next(const Geo& g, int c, int lane, bool flag) {
+  __device__ __forceinline__ bool next(const Geo& g, const Cuts& cuts, int lane, bool flag) {
     b0 += 32;
     if (b0 >= g.a.B) return false;
     if (b0 > 0) {
@@ -379,24 +399,7 @@ struct Group {
     if (b0 + lane < g.a.B && !sequence(g.a, b0 + lane, &s.q0, &s.nq, &s.k0, &s.nk) && flag)
       flag_status(g.a.status, DSA_STATUS_BAD_LENGTH);
     s.shape(g.lgpair);
-    if (g.a.B > 1) {
-      // those that see most first: the last items to be taken are then small ones
-      int rank = 0, from = lane;
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i) {
-        const int m = __shfl_sync(0xffffffffu, s.most, i);
-        rank += m > s.most || (m == s.most && i < lane);
-      }
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i)
-        if (__shfl_sync(0xffffffffu, rank, i) == lane) from = i;
-      s.q0 = __shfl_sync(0xffffffffu, s.q0, from);
-      s.nq = __shfl_sync(0xffffffffu, s.nq, from);
-      s.k0 = __shfl_sync(0xffffffffu, s.k0, from);
-      s.nk = __shfl_sync(0xffffffffu, s.nk, from);
-      s.shape(g.lgpair);
-    }
-    s.cut_at(g.lgpair, c);
+    s.cut_at(g.lgpair, cuts.c);
     // (an even share needs about two slots per SM; where that does not hold, what
     // has no slots is not cut)
     smine = min((long long)s.cut * s.pieces * g.HH, (long long)g.slots + 1);
@@ -406,7 +409,24 @@ struct Group {
       s.pieces = 1;
       send = g.slots;  // (and nothing behind it is)
     }
-    mine = (s.pairs + s.cut * (s.pieces - 1)) * g.HH;
+    if (g.many && b0 + 32 >= g.a.B && cuts.c > 0) {
+      // the last sequence's last pairs
+      const unsigned some = __ballot_sync(0xffffffffu, s.pairs > 0);
+      if (some && lane == 31 - __clz(some)) {
+        const int rest = cuts.items % g.ctas, tail = min((rest + g.HH - 1) / g.HH, s.pairs - s.cut);
+        if (tail > 0) {
+          const int N = s.tiles_of(g.lgpair, s.pairs - tail);
+          const int n = min(N / kMinPiece, (g.slots - send) / (tail * g.HH));
+          if (n >= 2 && cut_tail(cuts.items, g.ctas, rest, N)) {
+            s.tail = tail;
+            s.tpieces = n;
+            smine += tail * n * g.HH;
+            send += tail * n * g.HH;
+          }
+        }
+      }
+    }
+    mine = (s.pairs + s.cut * (s.pieces - 1) + s.tail * (s.tpieces - 1)) * g.HH;
     end = base + scan_add(mine, lane);
     return true;
   }
@@ -415,10 +435,10 @@ struct Group {
 // The item `at`, found from the last one on.
 struct Finder {
   Group grp;
-  int c = 0;
+  Cuts cuts{};
   __device__ __forceinline__ void init(const Geo& g, int lane) {
-    c = piece_tiles(g, lane);
-    grp.next(g, c, lane, true);
+    cuts = find_cuts(g, lane);
+    grp.next(g, cuts, lane, true);
   }
   // 1: an item, 0: none are left, 2: an empty piece
   __device__ int find(const Geo& g, int at, int lane, Item* it) {
@@ -435,23 +455,35 @@ struct Finder {
         s.pairs = of(grp.s.pairs);
         s.cut = of(grp.s.cut);
         s.pieces = of(grp.s.pieces);
+        s.tail = of(grp.s.tail);
+        s.tpieces = of(grp.s.tpieces);
         int r = at - of(grp.end - grp.mine);
-        const int slot0 = of(grp.send - grp.smine), in_cut = s.cut * s.pieces * g.HH;
+        int slot0 = of(grp.send - grp.smine), pair0 = 0, pieces = s.pieces;
+        const int in_cut = s.cut * s.pieces * g.HH, whole = (s.pairs - s.cut - s.tail) * g.HH;
         int pair, piece = 0, x;
         it->slot = -1;
-        if (r < in_cut) {
-          const int each = s.pieces * g.HH;
+        if (r >= in_cut + whole) {  // of the tail
+          r -= in_cut + whole;
+          slot0 += in_cut;
+          pair0 = s.pairs - s.tail;
+          pieces = s.tpieces;
+        } else if (r >= in_cut) {
+          r -= in_cut;
+          pair0 = s.cut;
+          pieces = 0;
+        }
+        if (pieces > 0) {
+          const int each = pieces * g.HH;
           pair = r / each;
           const int y = r - pair * each;
           piece = y / g.HH;
           x = y - piece * g.HH;
-          it->slot = slot0 + (pair * g.HH + x) * s.pieces + piece;
+          it->slot = slot0 + (pair * g.HH + x) * pieces + piece;
         } else {
-          r -= in_cut;
           pair = r / g.HH;
           x = r - pair * g.HH;
-          pair += s.cut;
         }
+        pair += pair0;
         const int vh = g.VH == 2 ? x & 1 : 0;
         x >>= g.VH - 1;
         const int hb = x % g.HB;
@@ -472,7 +504,7 @@ struct Finder {
         int j1 = 1 << 30;
         it->j0 = 0;
         if (it->slot >= 0) {
-          const int N = s.tiles_of(g.lgpair, pair), used = N / c, width = (N + used - 1) / used;
+          const int N = s.tiles_of(g.lgpair, pair), used = s.used(N, pair, cuts.c), width = (N + used - 1) / used;
           if (piece >= used) return 2;
           it->j0 = piece * width;
           j1 = it->j0 + width;
@@ -486,7 +518,7 @@ struct Finder {
         }
         return 1;
       }
-      if (!grp.next(g, c, lane, true)) return 0;
+      if (!grp.next(g, cuts, lane, true)) return 0;
     }
   }
 };
@@ -1076,11 +1108,11 @@ __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ Ge
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   launch_dependents();
-  const int c = piece_tiles(g, lane);
+  const Cuts cuts = find_cuts(g, lane);
   Group grp;
   int first = 0;  // cut items before the group
-  while (grp.next(g, c, lane, false)) {
-    const int own = grp.s.cut * g.HH, upto = scan_add(own, lane);
+  while (grp.next(g, cuts, lane, false)) {
+    const int own = (grp.s.cut + grp.s.tail) * g.HH, upto = scan_add(own, lane);
     const int all = __shfl_sync(0xffffffffu, upto, 31);
     // unit u: item u / 8 of the group, 32 rows of it
     int u = ((int)blockIdx.x - 8 * first) % (int)gridDim.x;
@@ -1095,11 +1127,14 @@ __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ Ge
       s.nk = of(grp.s.nk);
       s.pairs = of(grp.s.pairs);
       s.pieces = of(grp.s.pieces);
-      const int r = item - of(upto - own), slot0 = of(grp.send - grp.smine);
-      const int pair = r / g.HH;
-      int x = r - pair * g.HH;
-      const int N = s.tiles_of(g.lgpair, pair), used = N / c;
-      const int slot = slot0 + r * s.pieces;
+      s.cut = of(grp.s.cut);
+      s.tail = of(grp.s.tail);
+      s.tpieces = of(grp.s.tpieces);
+      const int r = item - of(upto - own), slot0 = of(grp.send - grp.smine), in_cut = s.cut * g.HH;
+      int pair = r / g.HH, x = r - pair * g.HH;
+      const int slot = r < in_cut ? slot0 + r * s.pieces : slot0 + in_cut * s.pieces + (r - in_cut) * s.tpieces;
+      if (r >= in_cut) pair += s.pairs - s.tail - s.cut;
+      const int used = s.used(s.tiles_of(g.lgpair, pair), pair, cuts.c);
       const int vh = g.VH == 2 ? x & 1 : 0;
       x >>= g.VH - 1;
       const int hk = x / g.HB, hb = x - hk * g.HB, per = kTile >> g.lgp;
@@ -1186,7 +1221,7 @@ Shape shape_of(int B, int Nq, int Hq, int Hk, int Dv) {
   s.items = ((long long)Nq / (2 * kTile >> s.lgp) + B) * s.HH;
   return s;
 }
-bool may_cut(const Shape& s) { return s.items < 4LL * sm_count(); }
+bool may_cut(const Shape& s) { return s.items < 12LL * sm_count(); }
 size_t ml_bytes() { return sizeof(float2) * kMaxSlots * kSlotRows; }
 
 int ring_of(int nkc) {
@@ -1212,15 +1247,22 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   g.VH = sh.VH;
   g.HH = sh.HH;
   g.ctas = (int)std::min<long long>(sm_count(), sh.items);
+  g.many = sh.items > sm_count();
   // Whether anything may be cut: for one sequence its lengths say so, several may
-  // have any (but none more keys than there are).
-  bool cut = may_cut(sh) && ((long long)p.Nk + kTile - 1) / kTile >= 2 * kMinPiece;
+  // have any (but none more keys than there are).  Whole prompts of one and a half
+  // items for every SM and more even out by themselves, the small ones coming last;
+  // the join's launch would cost them ~5 us.
+  bool cut = may_cut(sh) && ((long long)p.Nk + kTile - 1) / kTile >= 2 * kMinPiece &&
+             (2 * sh.items < 3LL * sm_count() || p.Nk >= 2LL * p.Nq);
   if (cut && p.B == 1) {
     Seq one{};
     one.nq = p.Nq;
     one.nk = p.Nk;
     one.shape(g.lgpair);
-    cut = one.most >= 2 * piece_of(one.work(g.lgpair), g.HH, sm_count());
+    const long long items = (long long)one.pairs * g.HH;
+    const int rest = (int)(items % sm_count()), tail = std::min((rest + g.HH - 1) / g.HH, one.pairs);
+    cut = one.most >= 2 * piece_of(one.work(g.lgpair), g.HH, sm_count()) ||
+          (tail > 0 && cut_tail(items, sm_count(), rest, one.tiles_of(g.lgpair, one.pairs - tail)));
   }
   if (cut) {
     g.slots = kMaxSlots;
