@@ -836,30 +836,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < nvc && ok; ++c, step()) {
             if (j < jm) continue;
             if (!warp_wait(smem_u32(&sm.full[rs]), rphase, &sm.abort)) { ok = false; break; }
-            uint4* chunk = reinterpret_cast<uint4*>(rptr + rs * kChunkBytes);
+            uint4* chunk = reinterpret_cast<uint4*>(rptr + rs * kChunkBytes) + lane;  // 8 lanes a row of 128 bytes
             const int rows = min(seen - kTile * (it.j0 + j), kTile);  // of the tile that some row sees
-            // warp 10 takes even groups of four rows, warp 11 odd ones
-#pragma unroll 4
-            for (int i = warp - 10; i < kTile / 4; i += 2) {
-              uint4* x = chunk + 32 * i + lane;  // 8 lanes a row of 128 bytes
-              const int row = 4 * i + (lane >> 3);
-              if (row >= rows) {
-                *x = make_uint4(0, 0, 0, 0);
-                continue;
+            // One warp takes even groups of four rows, the other odd ones, eight at a
+            // time: a sum of products with 0 is NaN if any element was none of the
+            // finite ones (with every element looked at by itself, items of four tiles
+            // took 43 us, 39 so).
+#pragma unroll 1
+            for (int i0 = warp - 10; i0 < kTile / 4; i0 += 16) {
+              uint4 x[8];
+              __nv_bfloat162 sum[4];
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                x[u] = 4 * (i0 + 2 * u) + (lane >> 3) < rows ? chunk[32 * (i0 + 2 * u)] : make_uint4(0, 0, 0, 0);
+              const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum[e] = zero;
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), zero, sum[e]);
               }
-              const uint4 v = *x;
-              auto bad = [](uint32_t w) {  // an exponent of all ones, in either half
-                const uint32_t e = w & 0x7f807f80u;
-                return ((e & 0x7f80u) == 0x7f80u) | ((e >> 16) == 0x7f80u);
-              };
-              if (bad(v.x) | bad(v.y) | bad(v.z) | bad(v.w)) {
-                odd = true;
-                auto scrub = [](uint32_t w) {
-                  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-                  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-                  return w;
-                };
-                *x = make_uint4(scrub(v.x), scrub(v.y), scrub(v.z), scrub(v.w));
+              const __nv_bfloat162 all = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+              const bool bad = __hisnan(all.x) || __hisnan(all.y);
+              if (__any_sync(0xffffffffu, bad) || rows < kTile) {
+                odd |= bad;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                  auto scrub = [](uint32_t w) {
+                    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+                    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+                    return w;
+                  };
+                  chunk[32 * (i0 + 2 * u)] = make_uint4(scrub(x[u].x), scrub(x[u].y), scrub(x[u].z), scrub(x[u].w));
+                }
               }
             }
           }
