@@ -92,35 +92,35 @@ __device__ __forceinline__ float scale_value(uint32_t s8) {
   return __half2float(__half(sr));
 }
 
-// x / d by a reciprocal r of d, correctly rounded for quotients well inside
-// fp32's range: the rounded product, its exact remainder, and one correction
-// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990).
-__device__ __forceinline__ float quotient(float x, float d, float r) {
-  const float q = x * r;
-  return fmaf(fmaf(-q, d, x), r, q);
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split2(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
-// Two codes of y / s; w: the elements' own bits, for the sign (also a zero's).  The
-// nearest E2M1 value of the quotient rounded to fp32 is that of the quotient itself
-// unless the rounding arrives at a midpoint between two codes: the remainder then
-// says on which side of it the quotient lies, and moves it there.  (Elements that
-// were not divided have 8 significant bits and s has 4: their quotient is a
-// midpoint or 2^-12 away from it.)
-__device__ __forceinline__ uint32_t two_codes(float y0, float y1, uint32_t w, float s, float r, bool divided) {
-  float q[2];
-  const float y[2] = {y0, y1};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float t = quotient(y[i], s, r);
-    int b = __float_as_int(t);
-    if (divided) {
-      const float rest = fmaf(-t, s, y[i]) * t;  // > 0: further from zero
-      if ((b & 0xfffff) == 0) b += (rest > 0.0f) - (rest < 0.0f);  // (midpoints have 3 significant bits)
-    }
-    q[i] = __int_as_float((b & 0x7fffffff) | ((i ? w : w << 16) & 0x80000000u));
-  }
-  return __nv_cvt_float2_to_fp4x2(make_float2(q[0], q[1]), __NV_E2M1, cudaRoundNearest);
+// x / d by a reciprocal r of d (neg: -d), correctly rounded for quotients well
+// inside fp32's range: the rounded product, its exact remainder, and one correction
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).
+__device__ __forceinline__ uint64_t quotients(uint64_t x, uint64_t neg, uint64_t r) {
+  const uint64_t q = mul2(x, r);
+  return fma2(fma2(q, neg, x), r, q);
 }
 
 // Half a group of bf16 elements (the other half is the neighbour lane's): the
@@ -139,26 +139,60 @@ __device__ __forceinline__ uint32_t quantise(uint4 in, float hs, uint32_t* codes
   const float s = scale_value(s8);
   *codes = 0;
   if (!(s > 0.0f)) return s8;  // codes 0 where the scale is 0 or NaN
-  const float r = __frcp_rn(s);
+  uint64_t y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = pair2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   // The short division holds for quotients inside fp32's range: what lies below
   // it has code 0 either way.
-  const bool plain = most < 1e30f && hs > 1e-20f && hs < 1e20f;
-  const float rh = scaled && plain ? __frcp_rn(hs) : 1.0f;
+  if (most < 1e30f && hs > 1e-20f && hs < 1e20f) {
+    if (scaled) {
+      const float rh = __frcp_rn(hs);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = quotients(y[i], pair2(-hs, -hs), pair2(rh, rh));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 v = split2(y[i]);
+      if (scaled) v = make_float2(__fdiv_rn(v.x, hs), __fdiv_rn(v.y, hs));
+      // (1e30: far beyond 6 s <= 2688)
+      y[i] = pair2(fminf(fmaxf(v.x, -1e30f), 1e30f), fminf(fmaxf(v.y, -1e30f), 1e30f));
+    }
+  }
+  // The nearest E2M1 value of y / s rounded to fp32 is that of y / s itself, unless
+  // the rounding arrives at a midpoint between two codes.  (Elements that were not
+  // divided have 8 significant bits and s has 4: their quotient is a midpoint or
+  // 2^-12 away from it.)
+  const float r = __frcp_rn(s);
+  const uint64_t neg = pair2(-s, -s), rr = pair2(r, r);
+  uint32_t q[8], low = 0xffffffffu;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float y0 = __uint_as_float(w[i] << 16), y1 = __uint_as_float(w[i] & 0xffff0000u);
-    if (!plain) {
-      if (scaled) {
-        y0 = __fdiv_rn(y0, hs);
-        y1 = __fdiv_rn(y1, hs);
+    const float2 t = split2(quotients(y[i], neg, rr));
+    q[2 * i] = __float_as_uint(t.x);
+    q[2 * i + 1] = __float_as_uint(t.y);
+    if (scaled) low = min(low, min(q[2 * i] & 0xfffff, q[2 * i + 1] & 0xfffff));
+  }
+  if (scaled && low == 0) {
+    // A midpoint (they have 3 significant bits) among them: the remainder says on
+    // which side of it the quotient lies, and moves it there.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = split2(y[i]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float t = __uint_as_float(q[2 * i + e]), x = e ? v.y : v.x;
+        const float rest = fmaf(-t, s, x) * t;  // > 0: further from zero
+        if ((q[2 * i + e] & 0xfffff) == 0) q[2 * i + e] += (rest > 0.0f) - (rest < 0.0f);
       }
-      y0 = fminf(fmaxf(y0, -1e30f), 1e30f);  // far beyond 6 s <= 2688
-      y1 = fminf(fmaxf(y1, -1e30f), 1e30f);
-    } else if (scaled) {
-      y0 = quotient(y0, hs, rh);
-      y1 = quotient(y1, hs, rh);
     }
-    *codes |= two_codes(y0, y1, w[i], s, r, scaled) << (8 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // (the sign is the element's own, also a zero's)
+    const float2 v = make_float2(__uint_as_float((q[2 * i] & 0x7fffffffu) | (w[i] << 16 & 0x80000000u)),
+                                 __uint_as_float((q[2 * i + 1] & 0x7fffffffu) | (w[i] & 0x80000000u)));
+    *codes |= (uint32_t)__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest) << (8 * i);
   }
   return s8;
 }
