@@ -849,17 +849,19 @@ def prefix_attn_decode(layout: PagedLayout, q, k_pool, v_pool, prefix_len, sm_sc
 
 # ------------------------------------------------------- prompt attention --
 def _strided(t, name: str, dev: int):
-    """(address, token stride, head stride) of bf16 heads [N, heads, dim]."""
-    if t.dim() != 3:
-        raise ValueError(f"{name}: [tokens, heads, dim] is required, not {tuple(t.shape)}")
+    """(address, token stride, head stride) and shape of bf16 heads [N, heads, dim]."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name}: {t.dtype}; torch.bfloat16 is required")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    shape, st = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name}: [tokens, heads, dim] is required, not {tuple(shape)}")
+    n, heads, dim = shape
+    if st[2] != 1 and dim > 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name}: a CUDA tensor on cuda:{dev} is required")
     # the stride of a dimension of one element is never used and may be anything
-    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    return (t.data_ptr(), st[0] if n > 1 else 0, st[1] if heads > 1 else 0), n, heads, dim
 
 
 def _on_gpu(dev: int, name: str, layout: Optional[PagedLayout] = None):
@@ -881,14 +883,16 @@ def prompt_attn(q, k, v, sm_scale, out, lse, ws, cu_q=None, cu_k=None, stream=No
     or None.  cu_q, cu_k [B + 1] int32: where each sequence's tokens begin; only
     cu_q given: the keys are the same tokens; neither: one sequence."""
     dev = q.get_device()
-    pq, pk, pv, po = (_strided(t, n, dev) for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")))
-    (Nq, Hq, Dk), (Nk, Hk, _), Dv = q.shape, k.shape, v.shape[2]
-    if k.shape[2] != Dk:
-        raise ValueError(f"k: heads of {k.shape[2]}; q has heads of {Dk}")
-    if v.shape[:2] != k.shape[:2]:
-        raise ValueError(f"v: {tuple(v.shape[:2])} tokens and heads; k has {(Nk, Hk)}")
-    if tuple(out.shape) != (Nq, Hq, Dv):
-        raise ValueError(f"out: {tuple(out.shape)}; the call writes {(Nq, Hq, Dv)}")
+    pq, Nq, Hq, Dk = _strided(q, "q", dev)
+    pk, Nk, Hk, dk = _strided(k, "k", dev)
+    pv, nv, hv, Dv = _strided(v, "v", dev)
+    po, no, ho, do = _strided(out, "out", dev)
+    if dk != Dk:
+        raise ValueError(f"k: heads of {dk}; q has heads of {Dk}")
+    if nv != Nk or hv != Hk:
+        raise ValueError(f"v: {(nv, hv)} tokens and heads; k has {(Nk, Hk)}")
+    if no != Nq or ho != Hq or do != Dv:
+        raise ValueError(f"out: {(no, ho, do)}; the call writes {(Nq, Hq, Dv)}")
     if cu_q is None and cu_k is not None:
         raise ValueError("cu_q: required with cu_k")
     B = 1
@@ -912,10 +916,16 @@ def prompt_attn(q, k, v, sm_scale, out, lse, ws, cu_q=None, cu_k=None, stream=No
 # ------------------------------------------------------------ 4-bit cache --
 def cache4_row_bytes(Dk, Dv) -> int:
     """Bytes of a row of the 4-bit pool (one position of one key head)."""
-    n = int(_lib.dsa_cache4_row_bytes(Dk, Dv))
-    if n == 0:
-        raise ValueError(f"head dims {Dk} / {Dv}: multiples of 16 up to 256 are taken")
+    n = _row_bytes.get((Dk, Dv))
+    if n is None:
+        n = int(_lib.dsa_cache4_row_bytes(Dk, Dv))
+        if n == 0:
+            raise ValueError(f"head dims {Dk} / {Dv}: multiples of 16 up to 256 are taken")
+        _row_bytes[(Dk, Dv)] = n
     return n
+
+
+_row_bytes = {}  # of the dims met so far
 
 
 def cache4_pool(num_blocks, heads, block_size, Dk, Dv, device=None) -> torch.Tensor:
@@ -926,12 +936,12 @@ def cache4_pool(num_blocks, heads, block_size, Dk, Dv, device=None) -> torch.Ten
 
 def _pool4(layout: PagedLayout, pool, Dk: int, Dv: int, dev: int):
     """(address, heads) of a 4-bit pool, checked against the layout's pages."""
-    if pool.dim() != 4 or pool.shape[2] != layout.block_size or pool.shape[3] != cache4_row_bytes(Dk, Dv):
-        raise ValueError(f"pool: [num_blocks, heads, {layout.block_size}, {cache4_row_bytes(Dk, Dv)}] is "
-                         f"required, not {tuple(pool.shape)}")
-    if pool.shape[0] < layout.num_blocks:
-        raise ValueError(f"pool: {pool.shape[0]} pages; the layout has {layout.num_blocks}")
-    return _vec(pool, "pool", torch.uint8, 0, dev), pool.shape[1]
+    shape, row = pool.shape, cache4_row_bytes(Dk, Dv)
+    if len(shape) != 4 or shape[2] != layout.block_size or shape[3] != row:
+        raise ValueError(f"pool: [num_blocks, heads, {layout.block_size}, {row}] is required, not {tuple(shape)}")
+    if shape[0] < layout.num_blocks:
+        raise ValueError(f"pool: {shape[0]} pages; the layout has {layout.num_blocks}")
+    return _vec(pool, "pool", torch.uint8, 0, dev), shape[1]
 
 
 def cache4_write_workspace_size() -> int:
@@ -945,11 +955,10 @@ def cache4_write(layout: PagedLayout, seq, pos, k, v, pool, ws, k_scale=None, v_
     None: token i is position seq_lens[i] - 1 of sequence i.  k_scale, v_scale
     [Hk] float32 or None; k_out, v_out: the values that the cache keeps, bf16."""
     dev = k.get_device()
-    pk, kts, khs = _strided(k, "k", dev)
-    pv, vts, vhs = _strided(v, "v", dev)
-    (N, Hk, Dk), Dv = k.shape, v.shape[2]
-    if v.shape[:2] != k.shape[:2]:
-        raise ValueError(f"v: {tuple(v.shape[:2])} tokens and heads; k has {(N, Hk)}")
+    pk, N, Hk, Dk = _strided(k, "k", dev)
+    pv, nv, hv, Dv = _strided(v, "v", dev)
+    if nv != N or hv != Hk:
+        raise ValueError(f"v: {(nv, hv)} tokens and heads; k has {(N, Hk)}")
     pp, heads = _pool4(layout, pool, Dk, Dv, dev)
     if heads != Hk:
         raise ValueError(f"pool: {heads} heads; k has {Hk}")
@@ -958,7 +967,7 @@ def cache4_write(layout: PagedLayout, seq, pos, k, v, pool, ws, k_scale=None, v_
             _vec(v_out, "v_out", torch.bfloat16, N * Hk * Dv, dev), _vec(ws, "ws", torch.uint8, 0, dev))
     ps, po = _vec(seq, "seq", torch.int32, N, dev), _vec(pos, "pos", torch.int32, N, dev)
     _on_gpu(dev, "k", layout)
-    rc = _lib.dsa_cache4_write(layout.c(), ps, po, N, pk, kts, khs, pv, vts, vhs, Hk, Dk, Dv, *args,
+    rc = _lib.dsa_cache4_write(layout.c(), ps, po, N, *pk, *pv, Hk, Dk, Dv, *args,
                                ws.numel(), _here(dev, stream))
     if rc:
         raise DsaError(rc, "dsa_cache4_write")
@@ -973,9 +982,10 @@ def cache4_read(layout: PagedLayout, seq, pos, pool, k_out, v_out, ws, k_scale=N
     """The values of N positions of the 4-bit pool as bf16 heads k_out
     [N, Hk, Dk] and v_out [N, Hk, Dv] (include/dsa.h, dsa_cache4_read)."""
     dev = k_out.get_device()
-    if k_out.dim() != 3 or v_out.dim() != 3 or v_out.shape[:2] != k_out.shape[:2]:
+    sk, sv = k_out.shape, v_out.shape
+    if len(sk) != 3 or len(sv) != 3 or sk[0] != sv[0] or sk[1] != sv[1]:
         raise ValueError("k_out, v_out: [tokens, heads, dim] of the same tokens and heads are required")
-    (N, Hk, Dk), Dv = k_out.shape, v_out.shape[2]
+    (N, Hk, Dk), Dv = sk, sv[2]
     pp, heads = _pool4(layout, pool, Dk, Dv, dev)
     if heads != Hk:
         raise ValueError(f"pool: {heads} heads; k_out has {Hk}")
@@ -1000,9 +1010,10 @@ def cache4_attn_decode(layout: PagedLayout, q, pool, sm_scale, out, lse, ws, k_s
     multiple of the pool's heads, out [B, Hq, Dv] bfloat16, lse float32 or
     None."""
     dev = q.get_device()
-    if q.dim() != 3 or out.dim() != 3 or out.shape[:2] != q.shape[:2]:
+    sq, so = q.shape, out.shape
+    if len(sq) != 3 or len(so) != 3 or sq[0] != so[0] or sq[1] != so[1]:
         raise ValueError("q, out: [sequences, heads, dim] of the same sequences and heads are required")
-    (B, Hq, Dk), Dv = q.shape, out.shape[2]
+    (B, Hq, Dk), Dv = sq, so[2]
     if B != layout.batch:
         raise ValueError(f"q: {B} sequences; the layout has {layout.batch}")
     pp, Hk = _pool4(layout, pool, Dk, Dv, dev)
