@@ -563,7 +563,9 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
  *              NULL (with B = 1): all of them.  Tokens of no sequence are not
  *              written.
  *  Hq, Hk      Hq a multiple of Hk;  Dk, Dv multiples of 8, 8..256
- *  out         bf16 [Nq][Hq][Dv] with strides like q's;  lse [Nq][Hq] fp32 or NULL
+ *  out         bf16 [Nq][Hq][Dv] with strides like q's;  lse [Nq][Hq] fp32 or NULL.
+ *              May not overlap q, k or v: an item writes its tokens while others
+ *              still read them.
  *  ws          dsa_prompt_attn_workspace_size() bytes
  * Errors: DSA_ERR_INVALID for null pointers, strides, alignment or sm_scale;
  * DSA_ERR_UNSUPPORTED for other heads and dims and beyond 2^31 items of 256 rows.
@@ -610,7 +612,9 @@ size_t dsa_cache4_row_bytes(int Dk, int Dv);
  *  ws          dsa_cache4_write_workspace_size() bytes (the status word)
  * A token whose sequence, position or page is out of range is not stored and
  * sets DSA_STATUS_BAD_BLOCK; its k_out and v_out are written all the same.  The
- * same position twice in one call: each group comes from one of the two.
+ * same position twice in one call (a caller error the call does not detect): each
+ * byte of its rows comes from one of the two, which one unspecified, so that a
+ * group may get the codes of one and the scale of the other.
  * Rows that no token names keep every byte.
  * Errors: DSA_ERR_INVALID for null pointers, N, strides or alignment;
  * DSA_ERR_UNSUPPORTED for other dims and for N * Hk beyond 2^31 - 1.

@@ -14,10 +14,15 @@
 //
 // Both kernels take half a group per thread, so that a warp's accesses of 16 bytes
 // of bf16 and of 4 bytes of codes lie side by side (with a group per thread the
-// two accesses of 16 bytes, or one of 32, took 1.3 times as long).  A thread keeps its place in a token's row (key head, group) and goes
-// from token to token, so that no division is left in the loop, the
-// tokens' places in the pool having been looked up once per block.  They are bound by those bytes; see
-// the launcher for figures.
+// two accesses of 16 bytes, or one of 32, took 1.3 times as long).  A thread keeps
+// its place in a token's row (key head, group) and goes from token to token, so that
+// no division is left in the loop, the tokens' places in the pool having been looked
+// up once per block.
+//
+// Measured: 32,768 tokens of 8 heads of 128 / 128 read in 35 us (172 MB, 72 % of the
+// copy rate); 16,384 written, with head scales and the values back, in 48 us (153 MB,
+// 47 %), bound by issue (2.7 instructions a cycle, half of them on the ALU at half
+// rate): an element costs ~9 instructions, most for dividing it exactly.
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>

@@ -28,11 +28,26 @@
 // most 2^-11 of itself), 2^7 above their own size so that small weights of long
 // sequences stay clear of its underflow; sums and statistics are fp32.
 //
-// Work is counted in units of 256 positions of one (sequence, key head, block
-// of heads); all units, item after item, are split evenly over the CTAs.  A
-// warp takes 32 positions of a unit, with its own ring of bulk copies (one per
-// run of positions inside a page) and its own softmax; an item's warps are joined through shared memory, its CTAs by k_cache4_merge in a fixed order.
+// Work is counted in units of 256 (dims up to 64: 512) positions of one (sequence,
+// key head, block of heads); all units, item after item, are split evenly over the
+// CTAs.  A warp takes 32 (64) positions of a unit, with its own ring of bulk copies
+// (one per run of positions inside a page) and its own softmax; an item's warps are
+// joined through shared memory, its CTAs by k_cache4_merge in a fixed order.
 // Lengths are read on the device, so a captured call follows them.
+//
+// Measured: 32 sequences of 8 to 32 thousand positions, 64 heads over 8 of 128: 158
+// us for 746 MB (4.7 TB/s, 70 % of the copy rate); 4 of 65 to 262 thousand, 32 heads
+// over 4 of 64: 59 us (3.7 TB/s; rows of 72 bytes are kept in 80).  It is bound by
+// issue: 2.9 lane-instructions an element of the three that the copy rate leaves, 49 %
+// of the ALU's cycles (conversions and logic run at half rate).  On the way, for the
+// first of these: 228 us with the dims read from the arguments, 187 with a row's
+// layout known at compile time, 170 with what a unit is told by its stage instead of
+// found again, 158 without spills and with the scales of unusable positions zeroed in
+// place (for 8,192 positions a sequence a single spilled value made 77 us 120: shared
+// memory leaves the L1 no room).  A warp of its own to fill one ring for all would
+// leave 96 registers, which spill.  Tiles of 64 positions gain only where rows are
+// short.  One sequence of 4,096: 12.8 us, the chain from the lengths over one tile a
+// warp to the join.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -271,8 +286,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 constexpr int per_sm(int NC, int NT, int RW) { return NC * NT * (RW / 32) <= 2 ? 2 : 1; }
 
-// RW: positions of a warp's tile.  kFull: Dk = Dv = 64 NC, where a row's layout is known at compile time (its
-// loads are one instruction each) and no group of 16 dims is missing.
+// RW: positions of a warp's tile.  kFull: Dk = Dv = 64 NC, where a row's layout is
+// known at compile time (its loads are one instruction each) and no group of 16 dims
+// is missing: 32 x 8,192, 64 heads over 8 of 128 in 72 us, without it 85; 131,072 x
+// 4, 32 over 4 of 64: 44 and 49; 8,192 x 16, 32 over 4 of 256: 45 and 58.
 template <int NC, int NT, int RW, bool kFull>
 __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
     k_cache4_attn(const __grid_constant__ Geo g) {
@@ -849,8 +866,13 @@ int chunks_of(int Dk, int Dv) {
   return n > 2 ? 4 : n;
 }
 // Positions of a warp's tile: what a tile costs beside its rows weighs most where
-// the rows are short.
+// the rows are short (64 dims, 131,072 x 4 positions, at the time: 48 us with 64, 55 with 32;
+// 128 dims, 8,192 x 32: 81 with 64, 80 with 32).
 constexpr int rows_of(int nc, int heads) { return nc == 1 ? 64 : 32; }
+// Heads of a block, the columns of both products: 16 read the rows of a larger group
+// once (32 x 8,192, 128 heads over 8 of 128: 111 us, blocks of 8 133; 128 over 4 of
+// 64: 63 and 74); in groups of up to 8 they would only carry zeros, and with more
+// than 128 dims their accumulators do not fit the registers.
 int heads_of(int Dk, int Dv, int G) { return G > 8 && chunks_of(Dk, Dv) <= 2 ? 16 : 8; }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }

@@ -16,7 +16,7 @@
 //
 // One key tile (tcgen05, M = 128, one accumulator of 128 columns each):
 //   S_X [128 x 128] = Q_X K^T       X = A, B; operands in shared memory;
-//   softmax: a thread has a row of S_X in registers; the running maximum is
+//   softmax: a thread has a row of S_X; the running maximum is
 //       raised only when a tile exceeds it by more than 2^8, O_X rescaled then;
 //   P_X bf16 over S_X in TMEM;  O_X [128 x Dv] += P_X V, P_X from TMEM.
 // The tensor cores alternate: while the softmax of A works on its scores, they
@@ -33,14 +33,39 @@
 // limit.  V has no such place: a hidden row's weight is 0, but 0 times what an
 // unrelated sequence, or a later token, has there may be NaN.  Two warps
 // therefore look through V of the key tiles that some row sees in part (one or
-// two per item), before the product: rows that no row of the item sees become
-// zeros, and so do infinities and NaN; an item with such values adds them to the
-// rows that do see them when it writes its output.
+// two per item; of every tile where weights are hi + lo, whose lo may be 0 or
+// negative), before the product: rows that no row of the item sees become zeros,
+// and so do infinities and NaN; an item with such values adds them to the rows
+// that do see them when it writes its output.
+//
+// Few rows over many keys.  Items are cut along the keys where one would take more
+// than twice an even share of the work, and where items of one size leave the last
+// wave of CTAs mostly idle: a piece leaves its unnormalised (O, m, l) in the
+// workspace and k_prompt_merge joins a row's pieces in a fixed order.  8 tokens of
+// 24 heads over 6 behind 6,177 keys: 32 us, uncut 104; ~3,000 tokens of 64 heads
+// of 192 / 128 behind 6,000 keys (5.05 items per SM) 608 us, uncut 656.
 //
 // Warp roles (384 threads): 0-3 softmax of A, 4-7 of B, 8 fills the ring of K
 // and V (chunks of 64 dims of 128 keys) and Q, 9 issues the products, 10 and 11
 // look through V.  Every wait is bounded (DSA_STATUS_TIMEOUT, then the CTA winds
 // down).
+//
+// What bounds it.  A key tile of an item is 2,048 cycles of MMAs (128 dims) and
+// 256 KB through shared memory (scores read both operands there), as many cycles
+// at 128 bytes each; the exponentials take 1,024 of the special-function units.
+// 16384 tokens of 64 heads over 8 key heads of 128: 2,900 us, 1,515 TFLOP/s (80 % of
+// the cuBLAS rate, 89 % of its rate under the power cap), the matrix unit 60 % busy;
+// 8192 of 64 heads of 192 / 128: 1,440 TFLOP/s; 12 ragged prompts of up to 1,500
+// tokens, 24 heads over 4 of 80: 94 us, bound by the chain of a tile (scores,
+// softmax, weights: ~1.9 us) where items have a handful of them.
+// Measured on the way, for the first of these: MMAs whose operands the compiler
+// cannot prove warp-uniform 4,317 us (each is then a loop over lanes; shuffles make
+// them uniform now: 3,244 with the weights in one pass where the maximum holds); all
+// 128 scores of a row in registers at once, spilled: 4,320; 16 softmax warps with half
+// a row each: 3,226 where 8 took 3,030; less code per role, weights handed over in
+// halves and chunks released by their own last product: 2,890.  A split of the
+// registers between the roles (setmaxnreg 72 / 216) did not end; the cause is not
+// known and it is left out.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -195,6 +195,24 @@ def test_append_form_and_tokens_without_a_place():
     assert dsa.get_status(ws) == 0 and torch.equal(c.pool.cpu(), full)
 
 
+def test_a_position_named_twice_holds_bytes_of_either():
+    """... and no other position is touched."""
+    need_gpu()
+    dsa = lib()
+    c = Cache(5, [300], 3, 64, bs=64, fill=False)
+    N = 200
+    k, v = (torch.randn((N, 3, 64), generator=c.g).to(BF).cuda() for _ in range(2))
+    pos = (torch.arange(N, device="cuda", dtype=torch.int32) % 100)          # each of 100 twice
+    ws = dsa.workspace(dsa.cache4_write_workspace_size())
+    dsa.cache4_write(c.layout(dsa), torch.zeros_like(pos), pos, k, v, c.pool, ws)
+    assert dsa.get_status(ws) == 0
+    want = pack_rows(quantise64(k), quantise64(v), c.row).cpu()              # [N][Hk][row]
+    pool = c.pool.cpu()
+    got = torch.stack([pool[int(c.bt[0, p // 64]), :, p % 64] for p in range(300)])
+    assert bool(((got[:100] == want[:100]) | (got[:100] == want[100:])).all())
+    assert bool((got[100:] == 0xff).all())
+
+
 # ------------------------------------------------------------------------------- attention
 CASES = {
     "one-position": dict(lens=[1], Hq=1, Hk=1, Dk=64),

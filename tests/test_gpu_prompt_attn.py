@@ -93,6 +93,10 @@ CASES = {
     "cut-chunk": dict(seqs=[(40, 3500), (3, 2600), (200, 1700), (1, 100)], Hq=4, Hk=2, Dk=64),
     "cut-wide-v": dict(seqs=[(9, 2600), (16, 40)], Hq=6, Hk=2, Dk=136, Dv=200),
     "cut-prompt": dict(seqs=[(2300, 2300)], Hq=2, Hk=1, Dk=64),
+    # more items than CTAs, the last of them in pieces
+    "cut-last-wave": dict(seqs=[(600, 2000)], Hq=64, Hk=64, Dk=64),
+    "cut-last-wave-of-two": dict(seqs=[(5, 40), (900, 3100), (0, 3)], Hq=40, Hk=8, Dk=64),
+    "cut-last-wave-wide-v": dict(seqs=[(300, 1900)], Hq=40, Hk=40, Dk=40, Dv=136),
 }
 
 
