@@ -42,7 +42,7 @@
 // than twice an even share of the work, and where items of one size leave the last
 // wave of CTAs mostly idle: a piece leaves its unnormalised (O, m, l) in the
 // workspace and k_prompt_merge joins a row's pieces in a fixed order.  8 tokens of
-// 24 heads over 6 behind 6,177 keys: 32 us, uncut 104; ~3,000 tokens of 64 heads
+// 24 heads over 6 behind 6,177 keys: 27 us, uncut 104; ~3,000 tokens of 64 heads
 // of 192 / 128 behind 6,000 keys (5.05 items per SM) 608 us, uncut 656.
 //
 // Warp roles (384 threads): 0-3 softmax of A, 4-7 of B, 8 fills the ring of K
@@ -127,7 +127,11 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
-constexpr int kMinPiece = 6;            // key tiles that a piece of a cut item has at least
+// Key tiles that a piece of a cut item has at least: it costs its setup, a partial
+// result and its part of the join.  A token of 32 heads over 8 behind 4,096 keys takes
+// 24.2 us with 3, 22.8 with 4, 26.3 with 6, 27.6 with 8 and 40.6 with 12; 8 tokens of
+// 24 over 6 behind 6,177 keys 26.8, 26.5, 28.3, 31.1 and 36.4.
+constexpr int kMinPiece = 4;
 constexpr int kSlotRows = 2 * kTile;
 
 struct Geo {
@@ -379,7 +383,7 @@ __host__ __device__ __forceinline__ int piece_of(float work, int HH, int ctas) {
 // Where items of about one size leave the last wave of CTAs mostly idle, those of
 // that wave are cut too: `rest` of `items` are over, of N key tiles each.
 __host__ __device__ __forceinline__ bool cut_tail(long long items, int ctas, int rest, int N) {
-  return items >= ctas && items < 12LL * ctas && rest > 0 && N >= 2 * kMinPiece &&
+  return items >= ctas && items < 12LL * ctas && rest > 0 && N >= 3 * kMinPiece &&
          (long long)(ctas - rest) * N >= 8LL * ctas;
 }
 
@@ -1288,7 +1292,7 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   // have any (but none more keys than there are).  Whole prompts of one and a half
   // items for every SM and more even out by themselves, the small ones coming last;
   // the join's launch would cost them ~5 us.
-  bool cut = may_cut(sh) && ((long long)p.Nk + kTile - 1) / kTile >= 2 * kMinPiece &&
+  bool cut = may_cut(sh) && ((long long)p.Nk + kTile - 1) / kTile >= 3 * kMinPiece &&
              (2 * sh.items < 3LL * sm_count() || p.Nk >= 2LL * p.Nq);
   if (cut && p.B == 1) {
     Seq one{};
@@ -1297,7 +1301,8 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
     one.shape(g.lgpair);
     const long long items = (long long)one.pairs * g.HH;
     const int rest = (int)(items % sm_count()), tail = std::min((rest + g.HH - 1) / g.HH, one.pairs);
-    cut = one.most >= 2 * piece_of(one.work(g.lgpair), g.HH, sm_count()) ||
+    // (three tiles less on the longest item pay for the join)
+    cut = one.most >= 2 * piece_of(one.work(g.lgpair), g.HH, sm_count()) + 3 ||
           (tail > 0 && cut_tail(items, sm_count(), rest, one.tiles_of(g.lgpair, one.pairs - tail)));
   }
   if (cut) {
