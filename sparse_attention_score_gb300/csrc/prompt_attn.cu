@@ -41,7 +41,8 @@
 // Few rows over many keys.  Items are cut along the keys where one would take more
 // than twice an even share of the work, and where items of one size leave the last
 // wave of CTAs mostly idle: a piece leaves its unnormalised (O, m, l) in the
-// workspace and k_prompt_merge joins a row's pieces in a fixed order.  8 tokens of
+// workspace, an item's first piece names the item there, and k_prompt_merge joins a
+// row's pieces in a fixed order.  8 tokens of
 // 24 heads over 6 behind 6,177 keys: 27 us, uncut 104; ~3,000 tokens of 64 heads
 // of 192 / 128 behind 6,000 keys (5.05 items per SM) 608 us, uncut 656.
 //
@@ -121,6 +122,8 @@ struct Smem {
   int fills, qfills[2];
   uint32_t tmem_base;
   int abort;
+  float work[kThreads / 32];  // what each warp found of the sequences' work and pairs
+  int pairs[kThreads / 32];
 };
 
 struct Maps {
@@ -134,6 +137,14 @@ struct Maps {
 constexpr int kMinPiece = 4;
 constexpr int kSlotRows = 2 * kTile;
 
+// A cut item, for the join.
+struct __align__(16) Join {
+  int slot, used;  // its first partial result and how many there are
+  int q0, left;    // tile A's first token in q; the sequence's tokens from there on
+  int h0, v0;      // first query head, first column of V
+  int pad[2];
+};
+
 struct Geo {
   PromptAttnParams a;
   int slots;          // partial results that the workspace holds, 0: no item is cut
@@ -141,6 +152,9 @@ struct Geo {
   int many;           // there may be more items than CTAs
   float2* ml;         // [slot][256] (maximum, sum)
   float* po;          // [slot][columns / 4][256][4]
+  Join* join;         // [joins], at most one per slot
+  int* joins;
+  int* jleft;         // blocks of the join that are done
   int G, lgp, HB;     // query heads per key head, log2 of gp, G / gp
   int lgpair;         // log2 of a pair's tokens
   int VH;             // items per head over V's columns
@@ -387,16 +401,18 @@ __host__ __device__ __forceinline__ bool cut_tail(long long items, int ctas, int
          (long long)(ctas - rest) * N >= 8LL * ctas;
 }
 
-// Read by every CTA and by the join from the same lengths.
+// Read by every CTA from the same lengths, in the same order.
 struct Cuts {
   int c;          // key tiles of a piece, 0: nothing is cut
   int items;      // uncut
 };
-__device__ __forceinline__ Cuts find_cuts(const Geo& g, int lane) {
-  if (g.slots == 0) return Cuts{0, 0};
+// A warp's part: every twelfth group of 32 sequences (~1 us for each group; with one
+// warp of every CTA, and again in the join, 608 sequences of 256 tokens behind as many
+// took 129 us, 83 so).
+__device__ __forceinline__ void add_up(const Geo& g, Smem& sm, int warp, int lane) {
   float sum = 0.0f;
   int pairs = 0;
-  for (int b0 = 0; b0 < g.a.B; b0 += 32) {
+  for (int b0 = 32 * warp; b0 < g.a.B; b0 += kThreads) {
     Seq s;
     s.nq = s.nk = 0;
     if (b0 + lane < g.a.B) sequence(g.a, b0 + lane, &s.q0, &s.nq, &s.k0, &s.nk);
@@ -406,7 +422,21 @@ __device__ __forceinline__ Cuts find_cuts(const Geo& g, int lane) {
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (g.many) pairs = __reduce_add_sync(0xffffffffu, pairs);
+  pairs = __reduce_add_sync(0xffffffffu, pairs);
+  if (lane == 0) {
+    sm.work[warp] = sum;
+    sm.pairs[warp] = pairs;
+  }
+}
+__device__ __forceinline__ Cuts find_cuts(const Geo& g, const Smem& sm) {
+  if (g.slots == 0) return Cuts{0, 0};
+  float sum = 0.0f;
+  int pairs = 0;
+#pragma unroll 1
+  for (int i = 0; i < kThreads / 32; ++i) {
+    sum += sm.work[i];
+    pairs += sm.pairs[i];
+  }
   return Cuts{piece_of(sum, g.HH, g.ctas), pairs * g.HH};
 }
 
@@ -417,7 +447,7 @@ struct Group {
   int base = 0, end = 0, mine = 0;     // items: before the group, up to this lane's sequence, its own
   int sbase = 0, send = 0, smine = 0;  // slots
   Seq s;
-  __device__ __forceinline__ bool next(const Geo& g, const Cuts& cuts, int lane, bool flag) {
+  __device__ __forceinline__ bool next(const Geo& g, const Cuts& cuts, int lane) {
     b0 += 32;
     if (b0 >= g.a.B) return false;
     if (b0 > 0) {
@@ -425,7 +455,7 @@ struct Group {
       sbase = __shfl_sync(0xffffffffu, send, 31);
     }
     s.q0 = s.nq = s.k0 = s.nk = 0;
-    if (b0 + lane < g.a.B && !sequence(g.a, b0 + lane, &s.q0, &s.nq, &s.k0, &s.nk) && flag)
+    if (b0 + lane < g.a.B && !sequence(g.a, b0 + lane, &s.q0, &s.nq, &s.k0, &s.nk))
       flag_status(g.a.status, DSA_STATUS_BAD_LENGTH);
     s.shape(g.lgpair);
     s.cut_at(g.lgpair, cuts.c);
@@ -465,9 +495,10 @@ struct Group {
 struct Finder {
   Group grp;
   Cuts cuts{};
-  __device__ __forceinline__ void init(const Geo& g, int lane) {
-    cuts = find_cuts(g, lane);
-    grp.next(g, cuts, lane, true);
+  int joined = 0;  // of an item's first piece: how many there are
+  __device__ __forceinline__ void init(const Geo& g, const Smem& sm, int lane) {
+    cuts = find_cuts(g, sm);
+    grp.next(g, cuts, lane);
   }
   // 1: an item, 0: none are left, 2: an empty piece
   __device__ int find(const Geo& g, int at, int lane, Item* it) {
@@ -534,6 +565,7 @@ struct Finder {
         it->j0 = 0;
         if (it->slot >= 0) {
           const int N = s.tiles_of(g.lgpair, pair), used = s.used(N, pair, cuts.c), width = (N + used - 1) / used;
+          joined = piece == 0 ? used : 0;
           if (piece >= used) return 2;
           it->j0 = piece * width;
           j1 = it->j0 + width;
@@ -547,7 +579,7 @@ struct Finder {
         }
         return 1;
       }
-      if (!grp.next(g, cuts, lane, true)) return 0;
+      if (!grp.next(g, cuts, lane)) return 0;
     }
   }
 };
@@ -601,6 +633,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
   grid_dependency_wait();
+  if (g.slots > 0) {
+    add_up(g, sm, warp, lane);
+    __syncthreads();
+  }
 
   const int per = kTile >> g.lgp;  // tokens of a tile
   const int nkc = g.nkc;
@@ -646,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
       // --------------------------------------------------------- producer --
       Finder f;
-      f.init(g, lane);
+      f.init(g, sm, lane);
       int rs = 0;
       uint32_t rphase = 1;  // an empty ring's barriers have completed "phase 1"
       int nfill = 0, nv = 0, nq[2] = {0, 0};
@@ -666,6 +702,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           sm.item[s] = it;
           mbar_arrive(&sm.ifull[s]);
+          if (have && it.slot >= 0 && f.joined > 0) {
+            const int i = atomicAdd(g.joins, 1);
+            if (i < g.slots) g.join[i] = Join{it.slot, f.joined, it.q0, it.nq - it.tok, it.h0, it.v0, {0, 0}};
+          }
         }
         __syncwarp();
         if (!have) break;
@@ -1148,99 +1188,79 @@ __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ Ge
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   launch_dependents();
-  const Cuts cuts = find_cuts(g, lane);
-  Group grp;
-  int first = 0;  // cut items before the group
-  while (grp.next(g, cuts, lane, false)) {
-    const int own = (grp.s.cut + grp.s.tail) * g.HH, upto = scan_add(own, lane);
-    const int all = __shfl_sync(0xffffffffu, upto, 31);
-    // unit u: item u / 8 of the group, 32 rows of it
-    int u = ((int)blockIdx.x - 8 * first) % (int)gridDim.x;
-    if (u < 0) u += gridDim.x;
-    for (; u < 8 * all; u += gridDim.x) {
-      const int item = u >> 3;
-      const int l = __ffs(__ballot_sync(0xffffffffu, upto > item)) - 1;
-      auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
-      Seq s;
-      s.q0 = of(grp.s.q0);
-      s.nq = of(grp.s.nq);
-      s.nk = of(grp.s.nk);
-      s.pairs = of(grp.s.pairs);
-      s.pieces = of(grp.s.pieces);
-      s.cut = of(grp.s.cut);
-      s.tail = of(grp.s.tail);
-      s.tpieces = of(grp.s.tpieces);
-      const int r = item - of(upto - own), slot0 = of(grp.send - grp.smine), in_cut = s.cut * g.HH;
-      int pair = r / g.HH, x = r - pair * g.HH;
-      const int slot = r < in_cut ? slot0 + r * s.pieces : slot0 + in_cut * s.pieces + (r - in_cut) * s.tpieces;
-      if (r >= in_cut) pair += s.pairs - s.tail - s.cut;
-      const int used = s.used(s.tiles_of(g.lgpair, pair), pair, cuts.c);
-      const int vh = g.VH == 2 ? x & 1 : 0;
-      x >>= g.VH - 1;
-      const int hk = x / g.HB, hb = x - hk * g.HB, per = kTile >> g.lgp;
-      const int row = 32 * (u & 7) + lane;
-      const int tok = (s.pairs - 1 - pair) * 2 * per + (row / kTile) * per + ((row % kTile) >> g.lgp);
-      const int head = hk * g.G + (hb << g.lgp) + (row & ((1 << g.lgp) - 1));
-      if (tok >= s.nq) continue;  // (a whole warp's or some lanes': no lane is waited for below)
-      const long long tr = (long long)s.q0 + tok;
-      const int v0 = vh * kVWidth, dv = min(a.Dv - v0, kVWidth);
-      const float2* ml = g.ml + (size_t)slot * kSlotRows + row;
-      float M = -INFINITY, l_sum = 0.0f;
+  const int joins = min(__ldcg(g.joins), g.slots);
+  // unit u: item u / 8, 32 rows of it
+  for (int u = blockIdx.x; u < 8 * joins; u += gridDim.x) {
+    const int4* jp = reinterpret_cast<const int4*>(g.join + (u >> 3));
+    const int4 j0 = __ldcg(jp), j1 = __ldcg(jp + 1);
+    const int slot = j0.x, used = j0.y, per = kTile >> g.lgp;
+    const int row = 32 * (u & 7) + lane;
+    const int tok = (row / kTile) * per + ((row % kTile) >> g.lgp);
+    const int head = j1.x + (row & ((1 << g.lgp) - 1));
+    if (tok >= j0.w) continue;  // (a whole warp's or some lanes': no lane is waited for below)
+    const long long tr = (long long)j0.z + tok;
+    const int v0 = j1.y, dv = min(a.Dv - v0, kVWidth);
+    const float2* ml = g.ml + (size_t)slot * kSlotRows + row;
+    float M = -INFINITY, l_sum = 0.0f;
 #pragma unroll 4
-      for (int i = 0; i < used; ++i) M = fmaxf(M, __ldcg(&ml[(size_t)i * kSlotRows]).x);
-      const float ref = M == -INFINITY ? 0.0f : M;
+    for (int i = 0; i < used; ++i) M = fmaxf(M, __ldcg(&ml[(size_t)i * kSlotRows]).x);
+    const float ref = M == -INFINITY ? 0.0f : M;
 #pragma unroll 4
-      for (int i = 0; i < used; ++i) {
-        const float2 st = __ldcg(&ml[(size_t)i * kSlotRows]);
-        if (st.y != 0.0f) l_sum = fmaf(st.y, exp2f(st.x - ref), l_sum);
-      }
-      const float inv = l_sum == 0.0f ? 0.0f : 1.0f / l_sum;
-      // the warp's four groups of columns at once, two partials in flight
-      constexpr int kGroups = kVWidth / 4 / 8;
-      const float4* po = reinterpret_cast<const float4*>(g.po) + ((size_t)slot * (kVWidth / 4) + warp) * kSlotRows + row;
-      float4 acc[kGroups];
-#pragma unroll
-      for (int d = 0; d < kGroups; ++d) acc[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i0 = 0; i0 < used; i0 += kBatch) {
-        float2 st[kBatch];
-        float4 v[kBatch][kGroups];
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          st[e] = make_float2(-INFINITY, 0.0f);
-          if (i0 + e < used) st[e] = __ldcg(&ml[(size_t)(i0 + e) * kSlotRows]);
-#pragma unroll
-          for (int d = 0; d < kGroups; ++d) {
-            v[e][d] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i0 + e < used && 4 * (warp + 8 * d) < dv)
-              v[e][d] = __ldcg(po + ((size_t)(i0 + e) * (kVWidth / 4) + 8 * d) * kSlotRows);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          if (st[e].y == 0.0f) continue;  // the row sees no key of the piece
-          const float w = exp2f(st[e].x - ref);
-#pragma unroll
-          for (int d = 0; d < kGroups; ++d) {
-            acc[d].x = fmaf(v[e][d].x, w, acc[d].x);
-            acc[d].y = fmaf(v[e][d].y, w, acc[d].y);
-            acc[d].z = fmaf(v[e][d].z, w, acc[d].z);
-            acc[d].w = fmaf(v[e][d].w, w, acc[d].w);
-          }
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < kGroups; ++d) {
-        const int x0 = 4 * (warp + 8 * d);
-        if (x0 >= dv) break;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[d].x * inv, acc[d].y * inv);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[d].z * inv, acc[d].w * inv);
-        *reinterpret_cast<uint2*>(a.out + tr * a.o_ts + (long long)head * a.o_hs + v0 + x0) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-      }
-      if (warp == 0 && a.lse && v0 == 0)
-        a.lse[tr * a.Hq + head] = l_sum == 0.0f ? -INFINITY : (M + log2f(l_sum)) * 0.6931471805599453f;
+    for (int i = 0; i < used; ++i) {
+      const float2 st = __ldcg(&ml[(size_t)i * kSlotRows]);
+      if (st.y != 0.0f) l_sum = fmaf(st.y, exp2f(st.x - ref), l_sum);
     }
-    first += all;
+    const float inv = l_sum == 0.0f ? 0.0f : 1.0f / l_sum;
+    // the warp's four groups of columns at once, two partials in flight
+    constexpr int kGroups = kVWidth / 4 / 8;
+    const float4* po = reinterpret_cast<const float4*>(g.po) + ((size_t)slot * (kVWidth / 4) + warp) * kSlotRows + row;
+    float4 acc[kGroups];
+#pragma unroll
+    for (int d = 0; d < kGroups; ++d) acc[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < used; i0 += kBatch) {
+      float2 st[kBatch];
+      float4 v[kBatch][kGroups];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        st[e] = make_float2(-INFINITY, 0.0f);
+        if (i0 + e < used) st[e] = __ldcg(&ml[(size_t)(i0 + e) * kSlotRows]);
+#pragma unroll
+        for (int d = 0; d < kGroups; ++d) {
+          v[e][d] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i0 + e < used && 4 * (warp + 8 * d) < dv)
+            v[e][d] = __ldcg(po + ((size_t)(i0 + e) * (kVWidth / 4) + 8 * d) * kSlotRows);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        if (st[e].y == 0.0f) continue;  // the row sees no key of the piece
+        const float w = exp2f(st[e].x - ref);
+#pragma unroll
+        for (int d = 0; d < kGroups; ++d) {
+          acc[d].x = fmaf(v[e][d].x, w, acc[d].x);
+          acc[d].y = fmaf(v[e][d].y, w, acc[d].y);
+          acc[d].z = fmaf(v[e][d].z, w, acc[d].z);
+          acc[d].w = fmaf(v[e][d].w, w, acc[d].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < kGroups; ++d) {
+      const int x0 = 4 * (warp + 8 * d);
+      if (x0 >= dv) break;
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[d].x * inv, acc[d].y * inv);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[d].z * inv, acc[d].w * inv);
+      *reinterpret_cast<uint2*>(a.out + tr * a.o_ts + (long long)head * a.o_hs + v0 + x0) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+    if (warp == 0 && a.lse && v0 == 0)
+      a.lse[tr * a.Hq + head] = l_sum == 0.0f ? -INFINITY : (M + log2f(l_sum)) * 0.6931471805599453f;
+  }
+  // the last block leaves both counters at zero for the next call
+  __syncthreads();
+  if (threadIdx.x == 0 && atomicAdd(g.jleft, 1) == (int)gridDim.x - 1) {
+    *g.joins = 0;
+    *g.jleft = 0;
   }
 }
 
@@ -1273,7 +1293,7 @@ int ring_of(int nkc) {
 
 size_t prompt_attn_ws(int B, int Nq, int Hq, int Hk, int Dv) {
   if (!may_cut(shape_of(B, Nq, Hq, Hk, Dv))) return kWsHeader;
-  return kWsHeader + ml_bytes() + sizeof(float) * kMaxSlots * kSlotRows * kVWidth;
+  return kWsHeader + ml_bytes() + sizeof(Join) * kMaxSlots + sizeof(float) * kMaxSlots * kSlotRows * kVWidth;
 }
 
 int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
@@ -1309,12 +1329,15 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
     g.slots = kMaxSlots;
     g.ctas = sm_count();
     g.ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + kWsHeader);
-    g.po = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + kWsHeader + ml_bytes());
+    g.join = reinterpret_cast<Join*>(reinterpret_cast<char*>(ws) + kWsHeader + ml_bytes());
+    g.po = reinterpret_cast<float*>(g.join + kMaxSlots);
   }
   g.nkc = (p.Dk + kChunk - 1) / kChunk;
   g.ring = ring_of(g.nkc);
   g.next = reinterpret_cast<int*>(ws) + 16;
   g.left = reinterpret_cast<int*>(ws) + 32;
+  g.joins = reinterpret_cast<int*>(ws) + 48;
+  g.jleft = reinterpret_cast<int*>(ws) + 49;
   if (sh.items > 0x7fff0000LL)
     return set_error(DSA_ERR_UNSUPPORTED, "prompt_attn: rows beyond 2^31 pairs of tiles of 128");
   Maps m{};
