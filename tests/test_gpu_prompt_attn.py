@@ -93,6 +93,10 @@ CASES = {
     "cut-chunk": dict(seqs=[(40, 3500), (3, 2600), (200, 1700), (1, 100)], Hq=4, Hk=2, Dk=64),
     "cut-wide-v": dict(seqs=[(9, 2600), (16, 40)], Hq=6, Hk=2, Dk=136, Dv=200),
     "cut-prompt": dict(seqs=[(2300, 2300)], Hq=2, Hk=1, Dk=64),
+    "cut-rows-of-many": dict(seqs=[(1, 4000)] * 40 + [(0, 0), (3, 2)], Hq=4, Hk=2, Dk=64),
+    "cut-some-of-200": dict(seqs=[((7 * i) % 30, (7 * i) % 30 + (2900 if i % 60 == 0 else i % 90)) for i in range(200)],
+                            Hq=4, Hk=2, Dk=64),
+    "more-rows-than-pieces": dict(seqs=[(1, 2500)] * 70, Hq=8, Hk=8, Dk=32),
     # more items than CTAs, the last of them in pieces
     "cut-last-wave": dict(seqs=[(600, 2000)], Hq=64, Hk=64, Dk=64),
     "cut-last-wave-of-two": dict(seqs=[(5, 40), (900, 3100), (0, 3)], Hq=40, Hk=8, Dk=64),
@@ -292,6 +296,23 @@ def test_captured_call_follows_the_offsets():
         o, l, m = attend_prompt64(p.q, p.k, p.v, cu(nq), cu(nk), p.scale)
         assert_rows_close(p.out[:n], p.lse[:n], o[:n], l[:n], m[:n], ONE, f"{nq} over {nk}")
         assert bool((p.out[n:] == 9).all())
+
+
+def test_two_graphs_of_one_workspace():
+    need_gpu()
+    dsa = lib()
+    p = Problem(32, [(5, 4000), (100, 900)], Hq=4, Hk=2, Dk=64).run(dsa)
+    want, other, graphs = p.out.clone(), torch.empty_like(p.out), []
+    for out in (p.out, other):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            dsa.prompt_attn(p.q, p.k, p.v, p.scale, out, p.lse, p.ws, cu_q=p.cu_q, cu_k=p.cu_k)
+        out.zero_()
+    for _ in range(20):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(p.out, want) and torch.equal(other, want)
 
 
 def test_one_workspace_serves_problems_of_any_shape():
