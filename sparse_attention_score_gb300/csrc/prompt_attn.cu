@@ -33,8 +33,8 @@
 // limit.  V has no such place: a hidden row's weight is 0, but 0 times what an
 // unrelated sequence, or a later token, has there may be NaN.  Two warps
 // therefore look through V of the key tiles that some row sees in part (one or
-// two per item; of every tile where weights are hi + lo, whose lo may be 0 or
-// negative), before the product: rows that no row of the item sees become zeros,
+// two per item; of every tile where weights are hi + lo, whose lo may be 0), before
+// the product: rows that no row of the item sees become zeros,
 // and so do infinities and NaN; an item with such values adds them to the rows
 // that do see them when it writes its output.
 //
@@ -57,7 +57,7 @@
 // 16384 tokens of 64 heads over 8 key heads of 128: 2,900 us, 1,515 TFLOP/s (80 % of
 // the cuBLAS rate, 89 % of its rate under the power cap), the matrix unit 60 % busy;
 // 8192 of 64 heads of 192 / 128: 1,440 TFLOP/s; 12 ragged prompts of up to 1,500
-// tokens, 24 heads over 4 of 80: 94 us, bound by the chain of a tile (scores,
+// tokens, 24 heads over 4 of 80: 92 us, bound by the chain of a tile (scores,
 // softmax, weights: ~1.9 us) where items have a handful of them.
 // Measured on the way, for the first of these: MMAs whose operands the compiler
 // cannot prove warp-uniform 4,317 us (each is then a loop over lanes; shuffles make
@@ -559,7 +559,7 @@ struct Finder {
         it->v0 = vh * kVWidth;
         it->dv = min(g.a.Dv - it->v0, kVWidth);
         it->lim = visible(it->tok, s.nq, s.nk);
-        // (lo of hi + lo may be 0 or negative: no infinity may meet it either)
+        // (lo of hi + lo may be 0: no infinity may meet it either)
         it->jm = it->lim <= kShort ? 0 : it->lim / kTile;
         int j1 = 1 << 30;
         it->j0 = 0;
@@ -1027,12 +1027,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 e = split2(fma2(pair2(x[i0 + 2 * i], x[i0 + 2 * i + 1]), c2, r2));
               const float e0 = ex2_approx(e.x), e1 = ex2_approx(e.y);
               sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
-              hi[i] = *reinterpret_cast<const uint32_t*>(&h2);
               if (decltype(both)::value) {
-                const float2 h = __bfloat1622float2(h2);
-                const __nv_bfloat162 l2 = __floats2bfloat162_rn(e0 - h.x, e1 - h.y);
+                // hi cut off, so that lo is below 2^-7 and off by half a step of it, 2^-16
+                const uint32_t u0 = __float_as_uint(e0), u1 = __float_as_uint(e1);
+                hi[i] = __byte_perm(u0, u1, 0x7632);
+                const float2 d = split2(fma2(pair2(__uint_as_float(u0 & 0xffff0000u), __uint_as_float(u1 & 0xffff0000u)),
+                                             pair2(-1.0f, -1.0f), pair2(e0, e1)));
+                const __nv_bfloat162 l2 = __floats2bfloat162_rn(d.x, d.y);
                 lo[i] = *reinterpret_cast<const uint32_t*>(&l2);
+              } else {
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(e0, e1);
+                hi[i] = *reinterpret_cast<const uint32_t*>(&h2);
               }
             }
             tmem_st_8cols(at + i0 / 2, hi);
