@@ -34,17 +34,17 @@
 // unrelated sequence, or a later token, has there may be NaN.  Two warps
 // therefore look through V of the key tiles that some row sees in part (one or
 // two per item; of every tile where weights are hi + lo, whose lo may be 0), before
-// the product: rows that no row of the item sees become zeros,
-// and so do infinities and NaN; an item with such values adds them to the rows
-// that do see them when it writes its output.
+// the product: rows that no row of the item sees become zeros, and so do
+// infinities and NaN; an item with such values adds them to the rows that do see
+// them when it writes its output.
 //
 // Few rows over many keys.  Items are cut along the keys where one would take more
 // than twice an even share of the work, and where items of one size leave the last
 // wave of CTAs mostly idle: a piece leaves its unnormalised (O, m, l) in the
 // workspace, an item's first piece names the item there, and k_prompt_merge joins a
-// row's pieces in a fixed order.  8 tokens of
-// 24 heads over 6 behind 6,177 keys: 27 us, uncut 104; ~3,000 tokens of 64 heads
-// of 192 / 128 behind 6,000 keys (5.05 items per SM) 608 us, uncut 656.
+// row's pieces in a fixed order.  8 tokens of 24 heads over 6 behind 6,177 keys: 27
+// us, uncut 104; ~3,000 tokens of 64 heads of 192 / 128 behind 6,000 keys (5.05 items
+// per SM) 608 us when uncut ones took 656.
 //
 // Warp roles (384 threads): 0-3 softmax of A, 4-7 of B, 8 fills the ring of K
 // and V (chunks of 64 dims of 128 keys) and Q, 9 issues the products, 10 and 11
@@ -54,10 +54,10 @@
 // What bounds it.  A key tile of an item is 2,048 cycles of MMAs (128 dims) and
 // 256 KB through shared memory (scores read both operands there), as many cycles
 // at 128 bytes each; the exponentials take 1,024 of the special-function units.
-// 16384 tokens of 64 heads over 8 key heads of 128: 2,900 us, 1,515 TFLOP/s (80 % of
-// the cuBLAS rate, 89 % of its rate under the power cap), the matrix unit 60 % busy;
-// 8192 of 64 heads of 192 / 128: 1,440 TFLOP/s; 12 ragged prompts of up to 1,500
-// tokens, 24 heads over 4 of 80: 92 us, bound by the chain of a tile (scores,
+// 16384 tokens of 64 heads over 8 key heads of 128: 2,845 us, 1,545 TFLOP/s (81 % of
+// the cuBLAS rate, 91 % of its rate under the power cap), the matrix unit 60 % busy;
+// chunks of 64 heads of 192 / 128: 1,440 TFLOP/s; 12 ragged prompts of up to 1,500
+// tokens, 24 heads over 4 of 80: 86 us, bound by the chain of a tile (scores,
 // softmax, weights: ~1.9 us) where items have a handful of them.
 // Measured on the way, for the first of these: MMAs whose operands the compiler
 // cannot prove warp-uniform 4,317 us (each is then a loop over lanes; shuffles make
@@ -1112,10 +1112,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (any) {
           tmem_ld_32cols(to + 32 * q, v);
           tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0;
         }
+        // (as few instructions as may be, for they run once an item and come from
+        // memory: a multiplication and a selection for each element took 608 items of
+        // 256 rows 51 us, this 45; 64 or all 128 columns at once 46 and 51)
         float x[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = any ? __uint_as_float(v[i]) * inv : 0.0f;
+        for (int i = 0; i < 32; i += 2) {
+          const float2 y = split2(fma2(pair2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pair2(inv, inv),
+                                       pair2(-0.0f, -0.0f)));
+          x[i] = y.x;
+          x[i + 1] = y.y;
+        }
         if (odd && mine) {
           // infinities and NaN that were kept out of the products
           const int p1 = min(lim, kTile * (it.j0 + it.n[t]));
