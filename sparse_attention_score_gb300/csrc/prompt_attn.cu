@@ -55,7 +55,7 @@
 // 256 KB through shared memory (scores read both operands there), as many cycles
 // at 128 bytes each; the exponentials take 1,024 of the special-function units.
 // 16384 tokens of 64 heads over 8 key heads of 128: 2,845 us, 1,545 TFLOP/s (81 % of
-// the cuBLAS rate, 91 % of its rate under the power cap), the matrix unit 60 % busy;
+// the cuBLAS rate, 91 % of its rate under the power cap), the matrix unit 62 % busy;
 // chunks of 64 heads of 192 / 128: 1,440 TFLOP/s; 12 ragged prompts of up to 1,500
 // tokens, 24 heads over 4 of 80: 86 us, bound by the chain of a tile (scores,
 // softmax, weights: ~1.9 us) where items have a handful of them.
