@@ -558,12 +558,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
       }
       if (!whole) {
         // The scales of V of unusable positions become 0: their weight is 0, but
-        // what the row holds there may be NaN.
+        // what the row holds there may be NaN.  (The fence orders these stores before
+        // the bulk copy that refills the stage: only it orders the two proxies.)
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
           if (!((valid[h] >> lane) & 1u))
 #pragma unroll 1
             for (int j = 0; j < gv; ++j) sts8(base + (32 * h + lane) * RB + sv + j, 0);
+        fence_proxy_async_smem();
         __syncwarp();
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
