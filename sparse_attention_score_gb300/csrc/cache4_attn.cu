@@ -480,7 +480,10 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
                                          __uint_as_float(w1 & 0xffff0000u) * down * down2);
           }
         // columns 2 t and 2 t + 1 are heads of lanes 8 t and 8 t + 4
-        const float f = a.scale_log2 * ks * power_of_two(e >> 1) * power_of_two(e - (e >> 1));
+        // (a factor of 0 would make NaN of the -inf of hidden positions; products of at
+        // most 2^21 times the smallest normal number are scores of 0 all the same)
+        const float f0 = a.scale_log2 * ks * power_of_two(e >> 1) * power_of_two(e - (e >> 1));
+        const float f = f0 < power_of_two(-126) ? power_of_two(-126) : f0;
         cs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
         cs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
         l[nt][0] = l[nt][1] = 0.0f;

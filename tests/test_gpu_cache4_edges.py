@@ -25,3 +25,19 @@ def test_whole_tiles_in_the_place_of_partial_ones(D, bs):
         p.out.fill_(3.0)
         p.call(dsa)
         assert torch.equal(p.out, first) and torch.equal(p.lse, lse)
+
+
+@pytest.mark.parametrize("ks", [1e-7, 1e-8, 1e-30, 1e-45])
+@pytest.mark.parametrize("bs", [64, 48])
+def test_a_vanishing_score_factor_leaves_the_mean(ks, bs):
+    """Queries of zeros or next to it behind head scales next to it: every weight is 1 / n, also in
+    tiles that the sequence's end or a bad page leaves partly unused."""
+    need_gpu()
+    dsa = lib()
+    for q_amp in (0.0, 1e-30):
+        p = Attn(41, [70, 300, 1, 513, 0], Hq=12, Hk=2, Dk=64, bs=bs, scaled=True, q_amp=q_amp)
+        p.ks = torch.full((2,), ks, device="cuda")
+        p.bt[1, 1] = -1
+        p.run(dsa)
+        assert dsa.get_status(p.ws) == dsa.STATUS_BAD_BLOCK
+        p.check(f"{q_amp} x {ks}")
