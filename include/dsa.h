@@ -37,8 +37,9 @@
  *    caller-owned device buffer of at least that size, 256-byte aligned and
  *    ZERO-FILLED before its first use.  The library leaves it in a reusable
  *    state after every call (counters return to zero; the status word is sticky
- *    until read with clear=1).  Calls that share a workspace must not overlap
- *    on the GPU (issue them on one stream, or order the streams).
+ *    until read with clear=1).  A workspace may serve different calls in turn;
+ *    calls that share one must not overlap on the GPU (issue them on one
+ *    stream, or order the streams).
  */
 #ifndef DSA_H_
 #define DSA_H_

@@ -15,8 +15,11 @@
 namespace dsa {
 
 // Bytes reserved at the head of every workspace: the status word and small
-// self-resetting counters.
+// counters.  A workspace may serve any call after any other, so each kind of
+// counter has a place of its own there.
 constexpr size_t kWsHeader = 256;
+constexpr size_t kBoundedCounters = 64;   // two uint64, kept until the next bounded call
+constexpr size_t kPromptCounters = 128;   // four int32 32 bytes apart, zero between calls
 
 struct LayoutDev {
   int bs, nb, maxb, batch, max_len;
@@ -197,7 +200,6 @@ int launch_topk(const TopkParams& p, void* ws, size_t ws_bytes, cudaStream_t s);
 // index_bounds.cu: per-page bounds of the indexer keys, and the decode
 // indexer that leaves out tiles which cannot reach the top-K.  The bounded
 // call counts skipped and bounded tiles in two uint64 of its workspace header.
-constexpr size_t kBoundedCounters = 64;
 int index_bounds_update(const LayoutDev& lay, const int32_t* seq, const int32_t* pos, int N,
                         const void* kidx, int D, int dtype, void* kbound, int* status,
                         cudaStream_t s);

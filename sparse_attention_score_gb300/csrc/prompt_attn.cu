@@ -1350,10 +1350,11 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   }
   g.nkc = (p.Dk + kChunk - 1) / kChunk;
   g.ring = ring_of(g.nkc);
-  g.next = reinterpret_cast<int*>(ws) + 16;
-  g.left = reinterpret_cast<int*>(ws) + 32;
-  g.joins = reinterpret_cast<int*>(ws) + 48;
-  g.jleft = reinterpret_cast<int*>(ws) + 49;
+  int* counters = reinterpret_cast<int*>(reinterpret_cast<char*>(ws) + kPromptCounters);
+  g.next = counters;
+  g.left = counters + 8;
+  g.joins = counters + 16;
+  g.jleft = counters + 24;
   if (sh.items > 0x7fff0000LL)
     return set_error(DSA_ERR_UNSUPPORTED, "prompt_attn: rows beyond 2^31 pairs of tiles of 128");
   Maps m{};
