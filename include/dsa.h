@@ -567,7 +567,9 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
  *  out         bf16 [Nq][Hq][Dv] with strides like q's;  lse [Nq][Hq] fp32 or NULL.
  *              May not overlap q, k or v: an item writes its tokens while others
  *              still read them.
- *  ws          dsa_prompt_attn_workspace_size() bytes
+ *  ws          dsa_prompt_attn_workspace_size() bytes: 51 MB of partial results,
+ *              the same for every call, so that a workspace asked for once
+ *              serves longer and shorter ones
  * Errors: DSA_ERR_INVALID for null pointers, strides, alignment or sm_scale;
  * DSA_ERR_UNSUPPORTED for other heads and dims and beyond 2^31 items of 256 rows.
  * Device: a sequence whose offsets are not inside the tokens is left out and sets

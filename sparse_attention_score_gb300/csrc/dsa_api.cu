@@ -366,7 +366,7 @@ static bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= (1LL << 3
 size_t dsa_prompt_attn_workspace_size(int B, int Nq, int Hq, int Hk, int Dk, int Dv) {
   (void)Dk;
   if (B < 1 || Nq < 0 || Hk < 1 || Hq < 1 || Hq % Hk || Dv < 1) return kWsHeader;
-  return prompt_attn_ws(B, Nq, Hq, Hk, Dv);
+  return prompt_attn_ws();
 }
 
 // Strides of [tokens][heads][dim]: unused ones may be anything, the others have
@@ -401,7 +401,7 @@ int dsa_prompt_attn(const void* q, int64_t q_token_stride, int64_t q_head_stride
       !heads_ok(Nq, Hq, Dv, out_token_stride, out_head_stride))
     return set_error(DSA_ERR_INVALID,
                      "prompt_attn: strides must be multiples of 8 up to 2^38 that keep heads apart");
-  int rc = check_ws(ws, ws_bytes, prompt_attn_ws(B, Nq, Hq, Hk, Dv));
+  int rc = check_ws(ws, ws_bytes, prompt_attn_uses(B, Nq, Hq, Hk, Dv));
   if (rc) return rc;
   if (Nq == 0) return DSA_OK;
   PromptAttnParams p{};

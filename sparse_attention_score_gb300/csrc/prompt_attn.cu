@@ -1307,9 +1307,12 @@ int ring_of(int nkc) {
 
 }  // namespace
 
-size_t prompt_attn_ws(int B, int Nq, int Hq, int Hk, int Dv) {
-  if (!may_cut(shape_of(B, Nq, Hq, Hk, Dv))) return kWsHeader;
+size_t prompt_attn_ws() {
   return kWsHeader + ml_bytes() + sizeof(Join) * kMaxSlots + sizeof(float) * kMaxSlots * kSlotRows * kVWidth;
+}
+
+size_t prompt_attn_uses(int B, int Nq, int Hq, int Hk, int Dv) {
+  return may_cut(shape_of(B, Nq, Hq, Hk, Dv)) ? prompt_attn_ws() : kWsHeader;
 }
 
 int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {

@@ -19,7 +19,10 @@ struct PromptAttnParams {
   float* lse;  // [Nq][Hq] or NULL
   int* status;
 };
-size_t prompt_attn_ws(int B, int Nq, int Hq, int Hk, int Dv);
+// Bytes of a workspace that serves calls of any size, and those of it that this one uses
+// (no partial results where there are items for every SM many times over).
+size_t prompt_attn_ws();
+size_t prompt_attn_uses(int B, int Nq, int Hq, int Hk, int Dv);
 int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s);
 
 }  // namespace dsa

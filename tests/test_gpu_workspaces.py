@@ -36,3 +36,13 @@ def test_bounded_scores_and_prompts_in_turn():
         p.run(dsa, ws=ws).check("a prompt on the scores' workspace")
         assert dsa.index_bounded_stats(ws) == counts
     assert dsa.get_status(ws) == 0
+
+
+def test_a_workspace_for_the_largest_prompt_serves_the_shortest():
+    need_gpu()
+    dsa = lib()
+    ws = dsa.workspace(dsa.prompt_attn_workspace_size(8, 16384, 64, 64, 16, 16))
+    for seqs in ([(1, 4000)], [(100, 100)], [(40, 3500), (3, 2600), (200, 1700), (1, 100)]):
+        p = Problem(62, seqs, Hq=64, Hk=64, Dk=16).run(dsa, ws=ws)
+        p.check(f"{seqs}")
+    assert dsa.get_status(ws) == 0
