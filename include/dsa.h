@@ -620,7 +620,8 @@ size_t dsa_cache4_row_bytes(int Dk, int Dv);
  * group may get the codes of one and the scale of the other.
  * Rows that no token names keep every byte.
  * Errors: DSA_ERR_INVALID for null pointers, N, strides or alignment;
- * DSA_ERR_UNSUPPORTED for other dims and for N * Hk beyond 2^31 - 1.
+ * DSA_ERR_UNSUPPORTED for other dims, for N * Hk beyond 2^31 - 1 and for
+ * Hk * (Dk + Dv) beyond 2^33.
  */
 size_t dsa_cache4_write_workspace_size(void);
 int dsa_cache4_write(const dsa_paged_layout* layout, const int32_t* seq, const int32_t* pos, int N,

@@ -458,6 +458,8 @@ static int cache4_rows(const char* what, const dsa_paged_layout* layout, const i
     return set_error(DSA_ERR_UNSUPPORTED, w + ": supported Hk >= 1, Dk and Dv 16..256 in multiples of 16");
   if ((long long)N * Hk > 0x7fffffffLL)
     return set_error(DSA_ERR_UNSUPPORTED, w + ": N * Hk beyond 2^31 - 1");
+  if ((long long)Hk * (Dk + Dv) > 1LL << 33)  // a block counts a token's half groups in 31 bits
+    return set_error(DSA_ERR_UNSUPPORTED, w + ": Hk * (Dk + Dv) beyond 2^33");
   if (!aligned16(pool) || !aligned16(k_out) || !aligned16(v_out))
     return set_error(DSA_ERR_INVALID, w + ": tensors must be 16-byte aligned");
   rc = check_ws(ws, ws_bytes, kWsHeader);
