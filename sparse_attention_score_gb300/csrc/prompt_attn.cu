@@ -1284,7 +1284,8 @@ __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ Ge
 // several times over, else at most about two pieces per SM and one remainder each.
 constexpr int kMaxSlots = 384;
 struct Shape {
-  int G, lgp, HB, VH, HH;
+  int G, lgp, HB, VH;
+  long long HH;     // items per pair of tiles
   long long items;  // at most
 };
 Shape shape_of(int B, int Nq, int Hq, int Hk, int Dv) {
@@ -1293,8 +1294,9 @@ Shape shape_of(int B, int Nq, int Hq, int Hk, int Dv) {
   while (s.lgp < 7 && s.G % (2 << s.lgp) == 0) ++s.lgp;
   s.HB = s.G >> s.lgp;
   s.VH = (Dv + kVWidth - 1) / kVWidth;
-  s.HH = Hk * s.HB * s.VH;
-  s.items = ((long long)Nq / (2 * kTile >> s.lgp) + B) * s.HH;
+  s.HH = (long long)Hk * s.HB * s.VH;
+  const long long pairs = (long long)Nq / (2 * kTile >> s.lgp) + B;
+  s.items = pairs > (1LL << 62) / s.HH ? 1LL << 62 : pairs * s.HH;
   return s;
 }
 bool may_cut(const Shape& s) { return s.items < 12LL * sm_count(); }
@@ -1319,12 +1321,14 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   Geo g{};
   g.a = p;
   const Shape sh = shape_of(p.B, p.Nq, p.Hq, p.Hk, p.Dv);
+  if (sh.items > 0x7fff0000LL)
+    return set_error(DSA_ERR_UNSUPPORTED, "prompt_attn: rows beyond 2^31 pairs of tiles of 128");
   g.G = sh.G;
   g.lgp = sh.lgp;
   g.HB = sh.HB;
   g.lgpair = 8 - sh.lgp;
   g.VH = sh.VH;
-  g.HH = sh.HH;
+  g.HH = (int)sh.HH;
   g.ctas = (int)std::min<long long>(sm_count(), sh.items);
   g.many = sh.items > sm_count();
   // Whether anything may be cut: for one sequence its lengths say so, several may
@@ -1358,8 +1362,6 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   g.left = counters + 8;
   g.joins = counters + 16;
   g.jleft = counters + 24;
-  if (sh.items > 0x7fff0000LL)
-    return set_error(DSA_ERR_UNSUPPORTED, "prompt_attn: rows beyond 2^31 pairs of tiles of 128");
   Maps m{};
   int rc = make_tmap_heads(&m.q, p.q, p.Dk, p.Hq, p.Nq, p.q_hs, p.q_ts, kChunk, 1u << g.lgp, kTile >> g.lgp);
   // no keys at all: nothing is loaded, the maps only have to exist

@@ -34,3 +34,14 @@ def test_rows_of_more_heads_than_a_block_counts_are_refused(Hk, D):
     assert L.dsa_cache4_read(_lay(), FAKE, FAKE, 1, Hk, D, D, None, None, FAKE, FAKE, FAKE, FAKE, 256, None) == -2
     assert L.dsa_cache4_write(_lay(), FAKE, FAKE, 1, FAKE, D, D, FAKE, D, D, Hk, D, D, None, None, FAKE, None, None,
                               FAKE, 256, None) == -2
+
+
+@pytest.mark.parametrize("Hq,Hk,B,Nq", [(1 << 30, 1 << 30, 1, 1), ((1 << 31) - 1, (1 << 31) - 1, 1, 1),
+                                        (1 << 30, 1 << 29, (1 << 31) - 1, 1), ((1 << 31) - 1, 1, (1 << 31) - 1, 1000),
+                                        ((1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1)])
+def test_prompts_of_more_items_than_32_bits_count_are_refused(Hq, Hk, B, Nq):
+    """(Heads of 256 take two items each: 2^30 of them were a negative count.)"""
+    ws = dsa.prompt_attn_workspace_size(B, Nq, Hq, Hk, 256, 256)
+    ts = 256 << 28
+    assert dsa.lib().dsa_prompt_attn(FAKE, ts, 256, FAKE, ts, 256, FAKE, ts, 256, FAKE, FAKE, B, Nq, 1, Hq, Hk, 256, 256,
+                                     0.1, FAKE, ts, 256, None, FAKE, ws, None) == -2
