@@ -91,7 +91,9 @@ __device__ __forceinline__ int seq_len(const Cache4AttnParams& a, int b) {
   const int L = __ldg(&a.lay.seq_lens[b]);
   return L < 0 ? 0 : min(L, a.lay.max_len);  // the bound that the host counted with
 }
-__device__ __forceinline__ int units_of(const Geo& g, int L) { return (L + g.unit - 1) >> g.lgunit; }
+__device__ __forceinline__ int units_of(const Geo& g, int L) {  // (L may be 2^31 - 1)
+  return (int)(((unsigned)L + (unsigned)g.unit - 1u) >> g.lgunit);
+}
 
 __device__ __forceinline__ int warp_scan(int v, int lane) {
 #pragma unroll

@@ -1,12 +1,21 @@
 """GPU tests of the 4-bit cache's decode attention at the edges of its ranges."""
+import math
+
 import pytest
 import torch
 
 from gpu_common import lib, need_gpu
+from prompt_reference import values64
 from test_gpu_cache4 import Attn
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
+
+# Sums over 2^31 positions: a warp has 2^31 / 2432 of them, its lane 110,000 fp32 additions (each off
+# by half a step, 2^-25, of a sum that is half of the last on average: together 2^-24 * 55,000) and its
+# products 55,000 accumulations (each cut off, 2^-23, likewise: 2^-23 * 27,500); beside these 2^-11 for
+# a weight as fp16 and 2^-11 for its score.
+LONG = 55000 * 2.0 ** -24 + 27500 * 2.0 ** -23 + 2.0 ** -10
 
 
 @pytest.mark.parametrize("D,bs", [(64, 64), (64, 48), (128, 32), (256, 16)])
@@ -41,3 +50,42 @@ def test_a_vanishing_score_factor_leaves_the_mean(ks, bs):
         p.run(dsa)
         assert dsa.get_status(p.ws) == dsa.STATUS_BAD_BLOCK
         p.check(f"{q_amp} x {ks}")
+
+
+@pytest.mark.parametrize("short", [0, 1, 510, 511, 700])
+def test_lengths_next_to_the_largest(short):
+    """2^31 - 1 positions and somewhat fewer, over the same three pages again and again but for the
+    table's last; queries along the last position's key, which decides heads 0 and 2 where it is long."""
+    need_gpu()
+    dsa = lib()
+    L, bs, D = (1 << 31) - 1 - short, 1024, 16
+    p = Attn(42, [4 * bs], Hq=4, Hk=2, Dk=D, bs=bs)
+    p.lay = p.layout(dsa)
+    pages = p.bt[0].long()
+    slots = torch.arange((L + bs - 1) // bs) % 3
+    slots[-1] = 3
+    p.lay = dsa.PagedLayout(pages[slots].to(torch.int32)[None].cuda(), torch.tensor([L], dtype=torch.int32).cuda(), bs,
+                            p.nb, L)
+    rows = p.pool.cpu()[pages].permute(1, 0, 2, 3)                       # [Hk][4 pages][bs][row]
+    k, v = values64(rows.flatten(0, 2), D, D)                            # [2 * 4 * bs][D]
+    k, v = k.view(2, 4, bs, D), v.view(2, 4, bs, D)
+    last = (L - 1) % bs
+    p.q[0, 0], p.q[0, 2] = (k[0, 3, last] * 256).to(BF), (k[1, 3, last] * 256).to(BF)
+    p.ws = dsa.workspace(dsa.cache4_attn_decode_workspace_size(1, 4, 2, D, D))
+    p.call(dsa)
+    assert dsa.get_status(p.ws) == 0
+    count = torch.bincount(slots, minlength=4).double()[:, None].expand(4, bs).clone()
+    count[3] = (torch.arange(bs) <= last).double()
+    for h in range(4):
+        z = (k[h // 2] @ p.q[0, h].double().cpu()) * p.scale
+        z = torch.where(count > 0, z + count.log(), -math.inf)
+        l = torch.logsumexp(z.flatten(), 0)
+        w = torch.exp(z - l)
+        # a single position's weight that is small beside the largest is lost below fp16's range: off by
+        # itself at most, and by 2^-32 of the largest (which stands at 2^7, and half a step is 2^-25)
+        one = torch.where(count > 0, w / count.clamp(min=1), 0.0)
+        lost = count * torch.minimum(one, 2.0 ** -32 * one.max())
+        want, mag = (w[..., None] * v[h // 2]).sum((0, 1)), (w[..., None] * v[h // 2].abs()).sum((0, 1))
+        tol = 2.0 ** -8 * want.abs() + LONG * mag + (lost[..., None] * v[h // 2].abs()).sum((0, 1))
+        assert abs(float(p.lse[0, h]) - float(l)) <= LONG, h
+        assert bool(((p.out[0, h].double().cpu() - want).abs() <= tol).all()), h
