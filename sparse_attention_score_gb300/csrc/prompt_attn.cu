@@ -336,6 +336,9 @@ __host__ __device__ __forceinline__ int visible(int tok, int nq, int nk) {  // k
   return v < 0 ? 0 : (int)(v > nk ? nk : v);
 }
 
+// Key tiles over n keys (which may be 2^31 - 1).
+__host__ __device__ __forceinline__ int tiles_over(int n) { return (int)(((unsigned)n + kTile - 1u) / kTile); }
+
 __device__ __forceinline__ int scan_add(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -356,7 +359,7 @@ struct Seq {
   int tail, tpieces;  // the last `tail` pairs in up to `tpieces`
   __host__ __device__ __forceinline__ int tiles_of(int lg, int pair) const {
     const long long end = (long long)(pairs - pair) << lg;
-    return (visible((int)(end < nq ? end : nq) - 1, nq, nk) + kTile - 1) / kTile;
+    return tiles_over(visible((int)(end < nq ? end : nq) - 1, nq, nk));
   }
   __host__ __device__ __forceinline__ void shape(int lg) {
     pairs = (int)(((long long)nq + (1 << lg) - 1) >> lg);
@@ -573,8 +576,8 @@ struct Finder {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int first_tok = it->tok + t * per;
-          const int last = min(first_tok + per, s.nq) - 1;
-          const int n = first_tok < s.nq ? (visible(last, s.nq, s.nk) + kTile - 1) / kTile : 0;
+          const int last = first_tok + min(per, s.nq - first_tok) - 1;
+          const int n = first_tok < s.nq ? tiles_over(visible(last, s.nq, s.nk)) : 0;
           it->n[t] = max(min(n, j1) - it->j0, 0);
         }
         return 1;
@@ -895,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             rphase ^= 1;
           }
         };
-        const int seen = visible(min(it.tok + 2 * per, it.nq) - 1, it.nq, it.nk);
+        const int seen = visible(it.tok + min(2 * per, it.nq - it.tok) - 1, it.nq, it.nk);
         for (int j = 0; j < N && ok; ++j) {
           for (int c = 0; c < nkc; ++c) step();
           bool odd = false;
@@ -1129,7 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (odd && mine) {
           // infinities and NaN that were kept out of the products
-          const int p1 = min(lim, kTile * (it.j0 + it.n[t]));
+          const int p1 = (int)min((unsigned)lim, (unsigned)kTile * (unsigned)(it.j0 + it.n[t]));
           for (int p = max(it.jm, it.j0) * kTile; p < p1; ++p) {
             const __nv_bfloat16* vr = a.v + (long long)(it.k0 + p) * a.v_ts + (long long)it.hk * a.v_hs + it.v0;
             for (int i = 0; i < 32; ++i)
