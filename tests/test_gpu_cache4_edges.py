@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_common import lib, need_gpu
-from prompt_reference import values64
+from prompt_reference import pack_rows, quantise64, values64
 from test_gpu_cache4 import Attn
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +89,45 @@ def test_lengths_next_to_the_largest(short):
         tol = 2.0 ** -8 * want.abs() + LONG * mag + (lost[..., None] * v[h // 2].abs()).sum((0, 1))
         assert abs(float(p.lse[0, h]) - float(l)) <= LONG, h
         assert bool(((p.out[0, h].double().cpu() - want).abs() <= tol).all()), h
+
+
+@pytest.mark.parametrize("Hk,G,D,bs,L", [(1, 16, 64, 64, 6000), (2, 8, 64, 48, 2500), (1, 16, 128, 128, 4000),
+                                         (1, 4, 256, 32, 1500), (1, 24, 80, 1, 700)])
+def test_every_position_counts_once(Hk, G, D, bs, L):
+    """Keys of +-1 behind 16 sequences of about the same positions: every row asks for a position by its
+    key's signs, next to the borders of tiles, units and CTAs and all others in turn."""
+    need_gpu()
+    dsa = lib()
+    B = 16
+    one = Attn(43, [L], Hq=Hk * G, Hk=Hk, Dk=D, bs=bs, fill=False)
+    k = torch.where(torch.randn((L, Hk, D), generator=one.g) > 0, 1.0, -1.0).to(BF)
+    v = torch.randn((L, Hk, D), generator=one.g).to(BF)
+    rows = pack_rows(quantise64(k), quantise64(v), one.row)
+    i = torch.arange(L)
+    pool = one.pool.cpu()
+    pool[one.bt[0].long()[i // bs], :, i % bs] = rows
+    k, v = (x.cuda() for x in values64(rows, D, D))                     # [L][Hk][D]
+    lens = torch.tensor([L - b for b in range(B)], dtype=torch.int32).cuda()
+    lay = dsa.PagedLayout(one.bt.expand(B, -1).contiguous().cuda(), lens, bs, one.nb, L)
+    pool, out = pool.cuda(), torch.empty((B, Hk * G, D), dtype=BF, device="cuda")
+    lse = torch.empty((B, Hk * G), device="cuda")
+    ws = dsa.workspace(dsa.cache4_attn_decode_workspace_size(B, Hk * G, Hk, D, D))
+    heads = torch.arange(Hk * G, device="cuda") // G
+    hidden = torch.arange(L, device="cuda") >= lens[:, None, None]
+    for r in range(-(-L // (B * G))):
+        target = (torch.arange(B * G, device="cuda").view(B, 1, G) + r * B * G).expand(B, Hk, G).reshape(B, -1)
+        target = torch.minimum(target, lens[:, None] - 1).long()
+        q = torch.sign(k[target, heads.expand_as(target)]).to(BF)
+        out.fill_(5.0)
+        dsa.cache4_attn_decode(lay, q, pool, 1.0, out, lse, ws)
+        z = torch.einsum("bhd,lhd->bhl", q.double(), k[:, heads]).masked_fill_(hidden, -math.inf)
+        l = torch.logsumexp(z, -1)
+        w = torch.exp(z - l[..., None])
+        o, m = torch.einsum("bhl,lhd->bhd", w, v[:, heads]), torch.einsum("bhl,lhd->bhd", w, v[:, heads].abs())
+        # (keys are of one size, so scores have few bits; a weight is off by 2^-11, or by 2^-32 of the largest)
+        tol = 2.0 ** -8 * o.abs() + 2.0 ** -10 * m + 2.0 ** -32 * v[:, heads].abs().sum(0)
+        d = (out.double() - o).abs()
+        assert bool((d <= tol).all()), (d > tol).any(-1).nonzero()[0].tolist()
+        # (a score below 264 is 2^8.6 in log2 units, and rounded at most four times)
+        assert float((lse.double() - l).abs().max()) <= 2.0 ** -13
+    assert dsa.get_status(ws) == 0

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from gpu_common import lib, need_gpu
+from test_gpu_prompt_attn import Problem, same
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -62,3 +63,113 @@ def test_tokens_next_to_the_largest_count(short, room):
     for i in range(0, N - 3, 1 << 28):
         j = min(N - 3, i + (1 << 28))
         assert int(out[i:j].count_nonzero()) == 0 and bool((lse[i:j] == -math.inf).all())
+
+
+def _deciding(seqs, Hq, Hk, rounds):
+    """A problem of keys of +-1 (a code of 64 dims for each), every row asking for one key by that key's
+    code: the ones next to the borders of tiles, the sequence's first and last, in turn."""
+    p = Problem(71, seqs, Hq=Hq, Hk=Hk, Dk=64, scale=1.0)
+    p.k = torch.where(p.k.float() > 0, 1.0, -1.0).to(BF)
+    G, queries = Hq // Hk, []
+    for r in range(rounds):
+        target, at, ak = [], 0, 0
+        for s, (nq, nk) in enumerate(seqs):
+            near = [x for x in range(nk) if x % 64 in (0, 1, 62, 63)] + [nk - 1, nk - 2]
+            near = torch.tensor([x for x in near if x >= 0] or [0], device="cuda")
+            i = torch.arange(nq * Hq, device="cuda").view(nq, Hq)
+            t = near[(i + 7 * s + r * nq * Hq) % len(near)]
+            last = torch.arange(nq, device="cuda")[:, None] + nk - nq
+            target.append(ak + torch.where(t <= last, t, last.clamp(min=0)))
+            at, ak = at + nq, ak + nk
+        target = torch.cat(target)
+        heads = torch.arange(Hq, device="cuda") // G
+        queries.append(p.k[target, heads.expand_as(target)])
+    return p, queries
+
+
+def _check_exact(p, what, lse_tol=2.0 ** -15):
+    """Against 64 bits on the GPU.  lse: products of +-1 are whole, so a score is off by the rounding of
+    log2(e), of its product with a score up to 64 (2^6.6 in log2 units) and of the sum with the logarithm,
+    2^-24 each of 2^6.6; beside it the sum of weights, 2^-20."""
+    G, aq, ak = p.Hq // p.Hk, 0, 0
+    for nq, nk in zip(p.nq, p.nk):
+        last = torch.arange(nq, device="cuda") + nk - nq
+        hidden = torch.arange(nk, device="cuda")[None, :] > last[:, None]
+        for h in range(p.Hq):
+            q, k, v = p.q[aq:aq + nq, h].double(), p.k[ak:ak + nk, h // G].double(), p.v[ak:ak + nk, h // G].double()
+            z = (q @ k.t() * p.scale).masked_fill_(hidden, -math.inf)
+            l = torch.logsumexp(z, -1)
+            w = torch.exp(z - torch.where(l > -math.inf, l, 0.0)[:, None])
+            o, m = w @ v, w @ v.abs()
+            tol = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -11) * m
+            d = (p.out[aq:aq + nq, h].double() - o).abs()
+            assert bool((d <= tol).all()), f"{what}: head {h}, row {(d > tol).any(-1).nonzero()[0].item()} of {nq} x {nk}"
+            some = l > -math.inf
+            assert bool(((p.lse[aq:aq + nq, h].double() - l)[some].abs() <= lse_tol).all()), f"{what}: lse, head {h}"
+        aq, ak = aq + nq, ak + nk
+
+
+DECIDING = {
+    "one-row": dict(seqs=[(1, 5000)], Hq=128, Hk=1, rounds=3),
+    "one-row-of-each-head": dict(seqs=[(1, 2500)] * 70, Hq=8, Hk=8, rounds=3),
+    "chunks-in-pieces": dict(seqs=[(40, 3500), (3, 2600), (200, 1700), (1, 100)], Hq=4, Hk=2, rounds=3),
+    "a-prompt-in-pieces": dict(seqs=[(2300, 2300)], Hq=2, Hk=1, rounds=2),
+    "last-wave-in-pieces": dict(seqs=[(5, 40), (900, 3100), (0, 3)], Hq=40, Hk=8, rounds=1),
+    "ragged": dict(seqs=[((37 * i) % 300, (37 * i) % 300 + (i % 3) * 150) for i in range(60)], Hq=6, Hk=2, rounds=2),
+    "uncut": dict(seqs=[(700, 700), (1300, 1300)], Hq=3, Hk=3, rounds=2),
+}
+
+
+@pytest.mark.parametrize("name", DECIDING)
+def test_every_key_at_a_border_counts_once(name):
+    need_gpu()
+    dsa = lib()
+    p, queries = _deciding(**DECIDING[name])
+    p.ws = p.workspace(dsa)
+    for q in queries:
+        p.q = q
+        p.out.fill_(5.0)
+        p.run(dsa, ws=p.ws)
+        _check_exact(p, name)
+    assert dsa.get_status(p.ws) == 0
+
+
+def test_a_long_prompt_of_many_items_per_sm():
+    """From twelve items per SM on nothing is cut: 4,000 tokens of 120 heads, and ragged ones."""
+    need_gpu()
+    dsa = lib()
+    p, (q,) = _deciding([(4000, 4000)], 120, 120, 1)
+    p.q = q
+    p.run(dsa)
+    _check_exact(p, "long")
+    p = Problem(72, same(1700, 3, 900, 128, 2100), Hq=128, Hk=32, Dk=128).run(dsa)
+    # (N(0, 1): a score is a sum of 128 products of size 1, off by 2^-24 of each partial sum below 64 at
+    # worst, 128 * 2^-18 / 11)
+    _check_exact(p, "ragged", lse_tol=2.0 ** -14)
+    assert dsa.get_status(p.ws) == 0
+
+
+def test_many_items_with_and_without_odd_values():
+    """Sixteen items and more for every CTA, one in eight of them with infinities or NaN in V."""
+    need_gpu()
+    dsa = lib()
+    seqs = [(1 + (37 * i) % 100, 1 + (37 * i) % 100 + (600 if i % 3 == 0 else i % 50)) for i in range(640)]
+    p = Problem(73, seqs, Hq=4, Hk=4, Dk=32)
+    g = torch.Generator().manual_seed(74)
+    begin = p.cu_k.tolist()
+    v = p.v.cpu()
+    for i in range(0, 640, 8):
+        nk = seqs[i][1]
+        for value in (math.inf, -math.inf, math.nan):
+            at = torch.randint(0, nk, (1,), generator=g).item()
+            h, d = torch.randint(0, 4, (1,), generator=g).item(), torch.randint(0, 32, (1,), generator=g).item()
+            v[begin[i] + at, h, d] = value
+    p.v = v.cuda()
+    p.run(dsa)
+    assert dsa.get_status(p.ws) == 0
+    p.check("odd values")
+    first, lse = p.out.clone(), p.lse.clone()
+    for _ in range(20):
+        p.out.fill_(3.0)
+        p.run(dsa, ws=p.ws)
+        assert torch.equal(p.out.view(torch.int16), first.view(torch.int16)) and torch.equal(p.lse, lse)
