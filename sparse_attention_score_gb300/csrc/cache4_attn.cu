@@ -53,6 +53,7 @@
 
 #include <algorithm>
 #include <string>
+#include <type_traits>
 
 #include "cache4.cuh"
 #include "device_common.cuh"
@@ -71,6 +72,12 @@ constexpr int kMaxCtas = 320;               // partial slots are laid out for th
 constexpr int kMaxStages = 8;
 constexpr float kLift = 7.0f;               // weights are 2^7 times their size
 constexpr float kRescaleLog2 = 8.0f;        // the maximum may lag by 2^8: weights stay below 2^15
+// A weight is 2^(z cs + r) in one fma, exact but for the rounding of r and of zt, which
+// grow with the maximum: an eighth of a power of two each at 2^20, whole ones that pass
+// fp16's range beyond.  From there on z cs is rounded before r is added to it, and
+// the maximum does not lag.  (Such a column's zt is NaN, so that every tile looks for
+// its maximum.)
+constexpr float kFar = 1048576.0f;
 
 struct Geo {
   Cache4AttnParams a;
@@ -593,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          up |= top_of(nt, e) > zt[nt][e];
+          up |= !(top_of(nt, e) <= zt[nt][e]);
+      bool far = false;
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -605,12 +613,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
             f[e] = 1.0f;
-            if (y > zt[nt][e]) {
-              const float top = y * cs[nt][e];  // (cs > 0)
-              f[e] = zt[nt][e] == -INFINITY ? 0.0f : ex2_approx(kLift - r[nt][e] - top);
+            const float top = __fmul_rn(y, cs[nt][e]), old = kLift - r[nt][e];  // (cs > 0; rounded before it meets others)
+            if (y > zt[nt][e] || (isnan(zt[nt][e]) && top > old)) {
+              f[e] = zt[nt][e] == -INFINITY ? 0.0f : ex2_approx(old - top);
               r[nt][e] = kLift - top;
-              zt[nt][e] = y + kRescaleLog2 / cs[nt][e];
+              zt[nt][e] = fabsf(top) > kFar ? NAN : y + kRescaleLog2 / cs[nt][e];
             }
+            far |= isnan(zt[nt][e]);
           }
           l[nt][0] *= f[0];
           l[nt][1] *= f[1];
@@ -622,25 +631,37 @@ __global__ void __launch_bounds__(kThreads, per_sm(NC, NT, RW))
             o[nt][i][3] *= f[1];
           }
         }
+        far = __any_sync(0xffffffffu, far);
       }
       uint32_t pf[kMt][NT][2];
+      auto weigh = [&](auto apart) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint64_t c2 = pair2(cs[nt][0], cs[nt][1]), r2 = pair2(r[nt][0], r[nt][1]);
-        uint64_t sum = pair2(l[nt][0], l[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint64_t c2 = pair2(cs[nt][0], cs[nt][1]), r2 = pair2(r[nt][0], r[nt][1]);
+          uint64_t sum = pair2(l[nt][0], l[nt][1]);
 #pragma unroll
-        for (int mt = 0; mt < kMt; ++mt)
+          for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float2 y = split2(fma2(pair2(z[mt][nt][2 * k], z[mt][nt][2 * k + 1]), c2, r2));
-            const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
-            sum = add2(sum, pair2(e0, e1));
-            pf[mt][nt][k] = transpose8(pack_half2(e0, e1));
-          }
-        const float2 l2 = split2(sum);
-        l[nt][0] = l2.x;
-        l[nt][1] = l2.y;
-      }
+            for (int k = 0; k < 2; ++k) {
+              const float z0 = z[mt][nt][2 * k], z1 = z[mt][nt][2 * k + 1];
+              float2 y;
+              if (decltype(apart)::value)
+                y = make_float2(__fadd_rn(__fmul_rn(z0, cs[nt][0]), r[nt][0]), __fadd_rn(__fmul_rn(z1, cs[nt][1]), r[nt][1]));
+              else
+                y = split2(fma2(pair2(z0, z1), c2, r2));
+              const float e0 = ex2_approx(y.x), e1 = ex2_approx(y.y);
+              sum = add2(sum, pair2(e0, e1));
+              pf[mt][nt][k] = transpose8(pack_half2(e0, e1));
+            }
+          const float2 l2 = split2(sum);
+          l[nt][0] = l2.x;
+          l[nt][1] = l2.y;
+        }
+      };
+      if (far)
+        weigh(std::true_type{});
+      else
+        weigh(std::false_type{});
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
         // positions 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the 16

@@ -93,6 +93,11 @@ constexpr int kSlots = 4;               // item descriptors in flight
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 X
 constexpr float kRescaleLog2 = 8.0f;
+// A weight is 2^(z c - m) in one fma, exact but for the rounding of the maximum m, which
+// all weights of a row have in common and their sum takes out again.  From |m| = 2^24
+// on that rounding is a power of two and more, and past 2^31 or so of infinity: there
+// z c is rounded like m before m leaves it, and the largest weight is 1 again.
+constexpr float kFar = 16777216.0f;
 constexpr int kShort = 512;
 constexpr int kVWidth = 128;            // columns of V per item
 constexpr int kReaders = 11;            // warps that read an item's descriptor
@@ -971,7 +976,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item& it = sm.item[islot];
       auto token = [&] { return it.tok + t * per + (row >> g.lgp); };
       const bool brief = it.lim <= kShort;
-      float m = -INFINITY, l = 0.0f;
+      // (pass: what the maximum is raised for; -inf: for anything)
+      float m = -INFINITY, pass = -INFINITY, l = 0.0f;
       // columns of the tile that this row sees
       int see = token() < it.nq ? visible(token(), it.nq, it.nk) - kTile * it.j0 : 0;
 #pragma unroll 1
@@ -1005,29 +1011,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx[2 + q] = max3(mx[2 + q], __uint_as_float(z[q][i]), __uint_as_float(z[q][i + 1]));
             }
         }
-        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+        const float mt = __fmul_rn(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), c);  // (rounded before it meets m)
         float f = 1.0f;
-        bool resc = false;
-        if (mt > m + kRescaleLog2 || (m == -INFINITY && mt > -INFINITY)) {
-          if (m > -INFINITY) {
-            f = exp2f(m - mt);
-            resc = true;
+        bool rescale = false, far = false;
+        if (__any_sync(0xffffffffu, mt > pass)) {
+          bool resc = false;
+          if (mt > pass && mt > m) {
+            resc = m > -INFINITY;
+            if (resc) f = exp2f(m - mt);
+            m = mt;
+            pass = fabsf(m) > kFar ? -INFINITY : m + kRescaleLog2;
           }
-          m = mt;
+          rescale = __any_sync(0xffffffffu, resc);
+          far = __any_sync(0xffffffffu, m > -INFINITY && fabsf(m) > kFar);
         }
         const float mm = m == -INFINITY ? 0.0f : m;
-        const bool rescale = __any_sync(0xffffffffu, resc);
         const uint64_t c2 = pair2(c, c), r2 = pair2(-mm, -mm);
         uint64_t sum[2] = {pair2(l * f, 0.0f), pair2(0.0f, 0.0f)};
         // A quarter's weights over scores that were read: bf16 to columns `at`,
         // what that leaves (short items) 32 behind.
-        auto weigh = [&](const uint32_t (&x)[32], uint32_t at, auto both) {
+        auto weigh = [&](const uint32_t (&x)[32], uint32_t at, auto both, auto apart) {
 #pragma unroll
           for (int i0 = 0; i0 < 32; i0 += 16) {
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float2 e = split2(fma2(pair2(x[i0 + 2 * i], x[i0 + 2 * i + 1]), c2, r2));
+              float2 e;
+              if (decltype(apart)::value)
+                e = make_float2(__fsub_rn(__fmul_rn(__uint_as_float(x[i0 + 2 * i]), c), mm),
+                                __fsub_rn(__fmul_rn(__uint_as_float(x[i0 + 2 * i + 1]), c), mm));
+              else
+                e = split2(fma2(pair2(x[i0 + 2 * i], x[i0 + 2 * i + 1]), c2, r2));
               const float e0 = ex2_approx(e.x), e1 = ex2_approx(e.y);
               sum[i & 1] = add2(sum[i & 1], pair2(e0, e1));
               if (decltype(both)::value) {
@@ -1055,11 +1069,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // The second half of the keys first: its weights' products run while the
         // first half's are made.
-        auto halves = [&](auto both) {
+        auto halves = [&](auto both, auto apart) {
 #pragma unroll 1
           for (int h = 1;; h = 0) {
-            weigh(z[0], ts + 64 * h, both);
-            weigh(z[1], ts + 64 * h + 16, both);
+            weigh(z[0], ts + 64 * h, both, apart);
+            weigh(z[1], ts + 64 * h + 16, both, apart);
             if (h == 0) break;
             if (rescale) {
               // O of the tiles before (S of this tile came after it)
@@ -1084,10 +1098,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           hand_over(0);
         };
-        if (brief)
-          halves(std::true_type{});
-        else
-          halves(std::false_type{});
+        // (in this order: with the rare case first long prompts take 2 % more)
+        if (__builtin_expect(!far && !brief, 1)) {
+          halves(std::false_type{}, std::false_type{});
+        } else if (__builtin_expect(!far, 1)) {
+          halves(std::true_type{}, std::false_type{});
+        } else {
+          brief ? halves(std::true_type{}, std::true_type{}) : halves(std::false_type{}, std::true_type{});
+        }
         const float2 s0 = split2(add2(sum[0], sum[1]));
         l = s0.x + s0.y;
       }

@@ -5,8 +5,8 @@ import pytest
 import torch
 
 from gpu_common import lib, need_gpu
-from prompt_reference import pack_rows, quantise64, values64
-from test_gpu_cache4 import Attn
+from prompt_reference import assert_rows_close, attend_cache64, pack_rows, quantise64, values64
+from test_gpu_cache4 import FP16, Attn
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -131,3 +131,55 @@ def test_every_position_counts_once(Hk, G, D, bs, L):
         # (a score below 264 is 2^8.6 in log2 units, and rounded at most four times)
         assert float((lse.double() - l).abs().max()) <= 2.0 ** -13
     assert dsa.get_status(ws) == 0
+
+
+@pytest.mark.parametrize("power", [0, 5, 10, 12, 14, 16, 18, 20, 25, 30, 60, 115])
+def test_scores_of_any_size(power):
+    """Scores of up to 64 * 2^power, up to where fp32 ends, every position of a tile's pattern 40 times over:
+    the places of the key that a head asks for share the row evenly."""
+    need_gpu()
+    dsa = lib()
+    D, n, times, Hq = 64, 100, 40, 16
+    p = Attn(44, [n * times, n * times - 33], Hq=Hq, Hk=1, Dk=D, fill=False)
+    k = torch.where(torch.randn((n, 1, D), generator=p.g) > 0, 1.0, -1.0).to(BF)
+    v = torch.randn((n * times, 1, D), generator=p.g).to(BF)
+    rows = pack_rows(quantise64(k.repeat(times, 1, 1)), quantise64(v), p.row)
+    pool = p.pool.cpu()
+    for b in range(2):
+        i = torch.arange(p.lens[b])
+        pool[p.bt[b].long()[i // 64], :, i % 64] = rows[:p.lens[b]]
+    p.pool, p.scale = pool.cuda(), 1.0
+    p.q = (k[torch.arange(2 * Hq) * 3, 0].view(2, Hq, D).double() * 2.0 ** power).to(BF).cuda()
+    p.run(dsa)
+    assert dsa.get_status(p.ws) == 0
+    o, l, m, total = attend_cache64(p.q, p.pool, p.bt, p.lens, 64, p.nb, D, D, 1.0)
+    assert_rows_close(p.out, None, o, l, m, FP16, f"2^{power}", floor=2.0 ** -32 * total)
+    # a score of 68 * 2^power is 2^(6.7 + power) in log2 units, and rounded at most four times
+    assert bool(((p.lse.double().cpu() - l).abs() <= 2.0 ** (power - 15)).all())
+
+
+def test_large_scores_that_rise_by_less_than_the_lag():
+    """Maxima of 2^12 to 2^21 that rise by up to 8 (log2) from tile to tile: no weight passes fp16's range."""
+    need_gpu()
+    dsa = lib()
+    n = 4096
+    for top in (4e3, 1e5, 5e5, 7e5, 1.4e6):
+        p = Attn(45, [n], Hq=2, Hk=1, Dk=32, fill=False)
+        k = torch.zeros((n, 1, 32), dtype=BF)
+        k[:, :, :16] = 6.0                                               # codes of 6 behind a scale of 1
+        k[:, 0, 16] = 6.0
+        k[:, 0, 17] = (torch.arange(n) // 64 % 5).to(BF)                 # 0 to 4
+        rows = pack_rows(quantise64(k), quantise64(torch.randn((n, 1, 32), generator=p.g).to(BF)), p.row)
+        i = torch.arange(n)
+        pool = p.pool.cpu()
+        pool[p.bt[0].long()[i // 64], :, i % 64] = rows
+        p.pool, p.scale = pool.cuda(), 1.0
+        p.q.zero_()
+        p.q[0, :, 0] = float(torch.tensor(top / 6).to(BF))
+        p.q[0, :, 17] = 1.25
+        p.run(dsa)
+        o, l, m, total = attend_cache64(p.q, p.pool, p.bt, p.lens, 64, p.nb, 32, 32, 1.0)
+        # a score is exact; its product with log2(e), where rounded, is off by half a step, 2^-24 of it, and a
+        # weight by that power of two
+        weight = 2.0 ** (2 * top * 1.4427 * 2.0 ** -24) - 1
+        assert_rows_close(p.out, None, o, l, m, FP16 + weight, f"{top}", floor=2.0 ** -32 * total)

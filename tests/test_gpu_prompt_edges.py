@@ -99,7 +99,7 @@ def _check_exact(p, what, lse_tol=2.0 ** -15):
             q, k, v = p.q[aq:aq + nq, h].double(), p.k[ak:ak + nk, h // G].double(), p.v[ak:ak + nk, h // G].double()
             z = (q @ k.t() * p.scale).masked_fill_(hidden, -math.inf)
             l = torch.logsumexp(z, -1)
-            w = torch.exp(z - torch.where(l > -math.inf, l, 0.0)[:, None])
+            w = torch.where((l > -math.inf)[:, None], torch.softmax(z, -1), 0.0)
             o, m = w @ v, w @ v.abs()
             tol = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -11) * m
             d = (p.out[aq:aq + nq, h].double() - o).abs()
@@ -173,3 +173,24 @@ def test_many_items_with_and_without_odd_values():
         p.out.fill_(3.0)
         p.run(dsa, ws=p.ws)
         assert torch.equal(p.out.view(torch.int16), first.view(torch.int16)) and torch.equal(p.lse, lse)
+
+
+@pytest.mark.parametrize("power", [0, 5, 10, 14, 16, 18, 20, 22, 25, 30, 60, 115])
+@pytest.mark.parametrize("seqs,Hq,Hk", [([(3, 3000), (70, 70)], 16, 2), ([(2, 5000)], 128, 1), ([(300, 700)], 3, 3)])
+def test_scores_of_any_size(seqs, Hq, Hk, power):
+    """Scores of up to 64 * 2^power, whole and exact in fp32, up to where fp32 ends: the key that a row asks
+    for is there twice (tiles or pieces apart), so that its two places share the row in halves."""
+    need_gpu()
+    dsa = lib()
+    p, (q,) = _deciding(seqs, Hq, Hk, 1)
+    ak = 0
+    for nq, nk in seqs:                                   # the second half of the keys repeats the first
+        p.k[ak + nk // 2:ak + nk // 2 * 2] = p.k[ak:ak + nk // 2]
+        ak += nk
+    target = torch.tensor([min(7, nk // 2 - 1) for nq, nk in seqs for _ in range(nq)], device="cuda")
+    base = torch.tensor([b for (nq, _), b in zip(seqs, p.cu_k.tolist()) for _ in range(nq)], device="cuda")
+    p.q = p.k[base + target].repeat_interleave(Hq // Hk, 1) * 2.0 ** power
+    p.run(dsa)
+    assert dsa.get_status(p.ws) == 0
+    # lse: as _check_exact's, of scores 2^power times as large
+    _check_exact(p, f"2^{power}", lse_tol=2.0 ** (power - 15))
