@@ -16,6 +16,12 @@ Stages (names as in the C ABI):
   attention over the selected rows gathered through the block table (first
   page, section 3 (2)-(3)).
 
+Around them: :func:`head_norm_rope` and :func:`cache_append` (heads of new
+tokens), :func:`prefix_attn_decode` (every position, a shared prefix read once)
+and, for layers with grouped heads, :func:`prompt_attn` (exact causal attention
+of packed prompts) and a cache of 4 bits per element (:func:`cache4_pool`,
+:func:`cache4_write`, :func:`cache4_read`, :func:`cache4_attn_decode`).
+
 :func:`decode` and :func:`prefill` chain the three stages with workspaces
 allocated through torch.  There is no CPU fallback: importing this package
 raises if ``libdsa.so`` has not been built, and every call raises

@@ -8,9 +8,10 @@
 //
 // Quantisation of a group of 16 elements y = x / head scale:
 //   s = E4M3(min(max |y| / 6, 448)),  code = the E2M1 value nearest to y / s.
-// The nearest code is decided on |y| against (midpoint between two codes) * s,
-// a product of at most 7 significant bits that fp32 holds exactly, so no
-// division rounds an element over a midpoint; ties go to the even code.
+// y is x / head scale rounded to fp32, and the nearest code is that of y / s itself,
+// ties to the even one: y / s is divided in fp32, correctly rounded, and a quotient
+// that arrives at a midpoint between two codes goes to the side that its exact
+// remainder says.
 //
 // Both kernels take half a group per thread, so that a warp's accesses of 16 bytes
 // of bf16 and of 4 bytes of codes lie side by side (with a group per thread the
@@ -21,8 +22,10 @@
 //
 // Measured: 32,768 tokens of 8 heads of 128 / 128 read in 35 us (172 MB, 72 % of the
 // copy rate); 16,384 written, with head scales and the values back, in 48 us (153 MB,
-// 47 %), bound by issue (2.7 instructions a cycle, half of them on the ALU at half
-// rate): an element costs ~9 instructions, most for dividing it exactly.
+// 47 %): an element costs ~9 instructions, most for dividing it exactly twice, which
+// keep 68 % of the issue slots and 54 % of the ALU (the fullest pipe) busy; most
+// stalls are waits for a turn, for a fixed latency and for the pipe.  The bound of five
+// blocks an SM spills 32 bytes a thread in both writing kernels.
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
@@ -77,7 +80,7 @@ __device__ __forceinline__ int token_page(const Cache4RowsParams& a, int n, int*
 }
 
 // The eight values of half a group: code * group scale (exact in fp16 and so in
-// fp32) * head scale, rounded once to bf16.
+// fp32), which is rounded to bf16 once; times a head scale to fp32 first.
 __device__ __forceinline__ uint4 kept_values(uint32_t codes, uint32_t s8, float hs) {
   const __half_raw sr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)s8, __NV_E4M3);
   const __half2 f = __half2half2(__half(sr));

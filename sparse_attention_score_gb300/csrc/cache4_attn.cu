@@ -35,11 +35,13 @@
 // joined through shared memory, its CTAs by k_cache4_merge in a fixed order.
 // Lengths are read on the device, so a captured call follows them.
 //
-// Measured: 32 sequences of 8 to 32 thousand positions, 64 heads over 8 of 128: 158
+// Measured: 32 sequences of 8 to 32 thousand positions, 64 heads over 8 of 128: 159
 // us for 746 MB (4.7 TB/s, 70 % of the copy rate); 4 of 65 to 262 thousand, 32 heads
-// over 4 of 64: 59 us (3.7 TB/s; rows of 72 bytes are kept in 80).  It is bound by
-// issue: 2.9 lane-instructions an element of the three that the copy rate leaves, 49 %
-// of the ALU's cycles (conversions and logic run at half rate).  On the way, for the
+// over 4 of 64: 59 us (3.7 TB/s; rows of 72 bytes are kept in 80).  An element takes
+// 2.9 lane-instructions of the three that the copy rate leaves; at 61 % of the issue
+// slots and 49 % of the ALU (conversions and logic run at half rate) no unit is full:
+// 16 warps an SM wait for their own chains (fixed latencies first, then a turn and the
+// math pipes; little for memory).  On the way, for the
 // first of these: 228 us with the dims read from the arguments, 187 with a row's
 // layout known at compile time, 170 with what a unit is told by its stage instead of
 // found again, 158 without spills and with the scales of unusable positions zeroed in

@@ -16,18 +16,24 @@
 //
 // One key tile (tcgen05, M = 128, one accumulator of 128 columns each):
 //   S_X [128 x 128] = Q_X K^T       X = A, B; operands in shared memory;
-//   softmax: a thread has a row of S_X; the running maximum is
-//       raised only when a tile exceeds it by more than 2^8, O_X rescaled then;
+//   softmax: a thread has a row of S_X; the running maximum is raised only when a
+//       tile exceeds it by more than 2^8, and O_X rescaled then (an economy known
+//       from published attention kernels);
 //   P_X bf16 over S_X in TMEM;  O_X [128 x Dv] += P_X V, P_X from TMEM.
 // The tensor cores alternate: while the softmax of A works on its scores, they
 // do O and the next S of B.  TMEM: S_A, S_B, O_A, O_B, 128 columns each.  V of
 // more than 128 columns is taken in two halves, each an item of its own that
 // computes S again.
 //
-// P is rounded to bf16 once (each weight by at most 2^-8 of itself, like the
-// output), except where rows see few keys and such roundings do not average out:
-// an item whose first row sees no more than 512 keys keeps P as bf16 hi + lo
-// (2^-16), both multiplied with the same V.  Statistics and sums are fp32.
+// P is rounded to bf16 once, each weight by at most 2^-8 of itself, which gives up
+// exactness for speed: over values of mixed sign the output shrinks by the same root
+// of the number of keys as the summed roundings, so they add about as much as the
+// bf16 output's own rounding, however many keys there are (0.0023 of the output's
+// norm instead of 0.0017 behind 6,000 keys).  hi + lo weights (2^-16, both multiplied
+// with the same V) take that away for half as many products again: 16384 tokens of 64
+// heads over 8 4,369 us, now 3,042, chunks behind 6,000 keys 875 and 670.  They are
+// taken where that costs little: by an item whose first row sees no more than 512
+// keys.  Statistics and sums are fp32.
 //
 // What no row may see.  Scores of hidden keys are set to -inf by the row's own
 // limit.  V has no such place: a hidden row's weight is 0, but 0 times what an
@@ -44,21 +50,23 @@
 // workspace, an item's first piece names the item there, and k_prompt_merge joins a
 // row's pieces in a fixed order.  8 tokens of 24 heads over 6 behind 6,177 keys: 27
 // us, uncut 104; ~3,000 tokens of 64 heads of 192 / 128 behind 6,000 keys (5.05 items
-// per SM) 608 us when uncut ones took 656.
+// per SM) 608 us when uncut ones took 656 (595 since).
 //
 // Warp roles (384 threads): 0-3 softmax of A, 4-7 of B, 8 fills the ring of K
 // and V (chunks of 64 dims of 128 keys) and Q, 9 issues the products, 10 and 11
 // look through V.  Every wait is bounded (DSA_STATUS_TIMEOUT, then the CTA winds
 // down).
 //
-// What bounds it.  A key tile of an item is 2,048 cycles of MMAs (128 dims) and
-// 256 KB through shared memory (scores read both operands there), as many cycles
-// at 128 bytes each; the exponentials take 1,024 of the special-function units.
-// 16384 tokens of 64 heads over 8 key heads of 128: 2,845 us, 1,545 TFLOP/s (81 % of
+// What bounds it.  A key tile of an item is 2,048 cycles of MMAs (128 dims) and, by
+// count, 256 KB through shared memory (scores read both operands there), as many
+// cycles at 128 bytes each; the exponentials take 1,024 of the special-function units.
+// 16384 tokens of 64 heads over 8 key heads of 128: 2,855 us, 1,540 TFLOP/s (81 % of
 // the cuBLAS rate, 91 % of its rate under the power cap), the matrix unit 62 % busy;
-// chunks of 64 heads of 192 / 128: 1,440 TFLOP/s; 12 ragged prompts of up to 1,500
-// tokens, 24 heads over 4 of 80: 86 us, bound by the chain of a tile (scores,
-// softmax, weights: ~1.9 us) where items have a handful of them.
+// chunks of 64 heads of 192 / 128: 1,440 TFLOP/s, with keys and values of all heads
+// read from memory 2.7 times (items go pair by pair, over all heads); 12 ragged prompts
+// of up to 1,500 tokens, 24 heads over 4 of 80: 86 us, bound by the chain of a tile
+// (scores, softmax, weights: ~1.9 us) and an item's setup and output (~4.6 us) where
+// items have a handful of tiles.
 // Measured on the way, for the first of these: MMAs whose operands the compiler
 // cannot prove warp-uniform 4,317 us (each is then a loop over lanes; shuffles make
 // them uniform now: 3,244 with the weights in one pass where the maximum holds); all
@@ -986,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sphase ^= 1;
         tc_fence_after();
         // All four quarters of a row for its maximum; for the weights the first two
-        // are read again (128 scores and the rest do not fit in 168 registers).
+        // are read again (128 scores and the rest do not fit in a thread's 168 registers).
         uint32_t z[2][32];  // quarters 2 and 3
         const bool part = __any_sync(0xffffffffu, see < kTile);
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
