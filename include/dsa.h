@@ -577,9 +577,7 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
  * DSA_ERR_UNSUPPORTED for other heads and dims and beyond 2^31 items of 256 rows.
  * Device: a sequence whose offsets are not inside the tokens is left out and sets
  * DSA_STATUS_BAD_LENGTH; a bounded wait that ran out sets DSA_STATUS_TIMEOUT (the
- * outputs are then not valid).  Waits are bounded by 2 s, the time that 256 rows take
- * for about 10^8 keys: longer sequences want a call of fewer than 12 items of 256
- * rows per SM, whose items are cut.
+ * outputs are then not valid).
  */
 size_t dsa_prompt_attn_workspace_size(int B, int Nq, int Hq, int Hk, int Dk, int Dv);
 int dsa_prompt_attn(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,

@@ -287,9 +287,14 @@ __device__ __forceinline__ void hide(uint32_t (&z)[32], int q, int see) {
     if (32 * q + i >= see) z[i] = 0xff800000u;
 }
 
+// A warp that has nothing to do in an item waits as long as the others work on it (256
+// rows take 12 ns a key: 26 s over 2^31 of them); whoever gives up sets *abort, which
+// ends this wait too.  Every other wait is for one step of a neighbour.
+constexpr uint64_t kStepNs = 2000000000ull, kItemNs = 60000000000ull;
+
 // pair_wait with less code: the warps of a scheduler share an instruction cache
 // that holds little more than the loops below.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit = kStepNs) {
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     uint32_t ok;
@@ -304,22 +309,21 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     if ((it & 63u) == 0) {
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
-      if (__any_sync(0xffffffffu, *abort != 0 || now - t0 > 2000000000ull)) return false;
+      if (__any_sync(0xffffffffu, *abort != 0 || now - t0 > limit)) return false;
     }
   }
 }
 
 // Wait of a whole warp until *count (in shared memory, only growing) is at
 // least n; bounded like pair_wait.
-__device__ __forceinline__ bool count_wait(const int* count, int n, volatile int* abort) {
+__device__ __forceinline__ bool count_wait(const int* count, int n, volatile int* abort, uint64_t limit = kStepNs) {
   const uint32_t addr = smem_u32(count);
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     int v;
     asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     if (__all_sync(0xffffffffu, v >= n)) return true;
-    if ((it & 63u) == 0 && __any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > 2000000000ull))
-      return false;
+    if ((it & 63u) == 0 && __any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > limit)) return false;
   }
 }
 
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int islot = 0;
   uint32_t iphase = 0;
   auto wait_item = [&]() -> bool {
-    if (!warp_wait(smem_u32(&sm.ifull[islot]), iphase, &sm.abort)) {
+    if (!warp_wait(smem_u32(&sm.ifull[islot]), iphase, &sm.abort, kItemNs)) {
       if (lane == 0) fail(sm, a.status);
       return false;
     }
@@ -917,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool odd = false;
           // the copies of this lap of the ring are under way: only then does a
           // chunk's barrier tell this lap's completion from one before
-          if (j >= jm && !count_wait(&sm.vissued, ++nv, &sm.abort)) { ok = false; break; }
+          if (j >= jm && !count_wait(&sm.vissued, ++nv, &sm.abort, kItemNs)) { ok = false; break; }
           for (int c = 0; c < nvc && ok; ++c, step()) {
             if (j < jm) continue;
             if (!warp_wait(smem_u32(&sm.full[rs]), rphase, &sm.abort)) { ok = false; break; }

@@ -194,3 +194,22 @@ def test_scores_of_any_size(seqs, Hq, Hk, power):
     assert dsa.get_status(p.ws) == 0
     # lse: as _check_exact's, of scores 2^power times as large
     _check_exact(p, f"2^{power}", lse_tol=2.0 ** (power - 15))
+
+
+def test_items_that_take_longer_than_a_wait_of_their_parts(room):
+    """One token of 193 heads over 200 million keys: more items than SMs and too few partial results to cut
+    them, so the warps that an item has no work for wait seconds for the next."""
+    dsa = lib()
+    N, Hq = 200_000_000, 193
+    k, v = torch.zeros((N, 1, 8), dtype=BF, device="cuda"), torch.full((N, 1, 8), 0.5, dtype=BF, device="cuda")
+    q = torch.ones((1, Hq, 8), dtype=BF, device="cuda")
+    q[0, 1::2] = -1.0
+    k[-1], v[-1] = 8.0, 3.0
+    out, lse = torch.full((1, Hq, 8), 5.0, dtype=BF, device="cuda"), torch.full((1, Hq), 5.0, device="cuda")
+    ws = dsa.workspace(dsa.prompt_attn_workspace_size(1, 1, Hq, 1, 8, 8))
+    dsa.prompt_attn(q, k, v, 1.0, out, lse, ws)
+    assert dsa.get_status(ws) == 0
+    # even heads see the last key alone (the others weigh exp(-64) N < 2^-60), odd ones all but it: the sums
+    # of ones end at 2^24 in fp32, as the sums of halves do, so what is left is the order of size
+    assert bool((out[0, ::2] == 3.0).all()) and bool(((lse[0, ::2] - 64.0).abs() <= 2.0 ** -15).all())
+    assert bool(((out[0, 1::2] > 0.2) & (out[0, 1::2] < 1.1)).all())
