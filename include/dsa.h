@@ -551,14 +551,14 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
  * token sees all):
  *     z_j = sm_scale * q[i][h] . k[j][h'],  out[i][h] = sum_j softmax(z)_j v[j][h'],
  *     lse[i][h] = log sum_j exp(z_j),  h' = h / (Hq / Hk)
- * A token that sees no key (nk < nq) has out 0 and lse -inf.  Scores, maxima and
- * sums are fp32.  A weight enters the product with V as bf16, off by at most 2^-8
- * of itself, and as bf16 hi + lo (2^-16) for the tokens whose tile begins with
- * one that sees no more than 512 keys; out is rounded once.  The single rounding
- * of the weights adds about as much to the error of out as its own rounding does
- * (0.0023 of its norm instead of 0.0017 behind 6,000 keys), in exchange for a third
- * of the matrix work.  What a token does not see does not reach it, NaN and
- * infinities included.
+ * A token that sees no key (nk < nq) has out 0 and lse -inf. Scores, maxima and
+ * sums are fp32 (the matrix unit's own run over 65,536 keys at most). A weight
+ * enters the product with V as bf16, off by at most 2^-8 of itself, and as bf16
+ * hi + lo (2^-16) for the tokens whose tile begins with one that sees no more
+ * than 512 keys; out is rounded once. The single rounding of the weights adds
+ * about as much to the error of out as its own rounding does (0.0023 of its norm
+ * instead of 0.0017 behind 6,000 keys), in exchange for a third of the matrix
+ * work. What a token does not see does not reach it, NaN and infinities included.
  *  q, k, v     bf16: token i head h at ptr + i * token stride + h * head stride
  *              (elements, multiples of 8, heads not overlapping); q has Nq tokens
  *              and Hq heads, k and v Nk tokens and Hk heads; 16-byte aligned
@@ -570,9 +570,9 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
  *  out         bf16 [Nq][Hq][Dv] with strides like q's;  lse [Nq][Hq] fp32 or NULL.
  *              May not overlap q, k or v: an item writes its tokens while others
  *              still read them.
- *  ws          dsa_prompt_attn_workspace_size() bytes: 51 MB of partial results,
- *              the same for every call, so that a workspace asked for once
- *              serves longer and shorter ones
+ *  ws          dsa_prompt_attn_workspace_size() bytes: 72 MB of partial results
+ *              and sums, the same for every call, so that a workspace asked for
+ *              once serves longer and shorter ones
  * Errors: DSA_ERR_INVALID for null pointers, strides, alignment or sm_scale;
  * DSA_ERR_UNSUPPORTED for other heads and dims and beyond 2^31 items of 256 rows.
  * Device: a sequence whose offsets are not inside the tokens is left out and sets

@@ -401,7 +401,7 @@ int dsa_prompt_attn(const void* q, int64_t q_token_stride, int64_t q_head_stride
       !heads_ok(Nq, Hq, Dv, out_token_stride, out_head_stride))
     return set_error(DSA_ERR_INVALID,
                      "prompt_attn: strides must be multiples of 8 up to 2^38 that keep heads apart");
-  int rc = check_ws(ws, ws_bytes, prompt_attn_uses(B, Nq, Hq, Hk, Dv));
+  int rc = check_ws(ws, ws_bytes, prompt_attn_uses(B, Nq, Nk, Hq, Hk, Dv));
   if (rc) return rc;
   if (Nq == 0) return DSA_OK;
   PromptAttnParams p{};

@@ -107,6 +107,11 @@ constexpr float kRescaleLog2 = 8.0f;
 // z c is rounded like m before m leaves it, and the largest weight is 1 again.
 constexpr float kFar = 16777216.0f;
 constexpr int kShort = 512;
+// Key tiles after which O leaves TMEM for a sum of its own in the workspace.  The matrix
+// unit cuts its sums off where an fp32 addition rounds, so that O shrinks by about 2^-27
+// for every key: 0.7 % over 10^6, an eighth of bf16's half step over the 65,536 of this.
+constexpr int kFlush = 512;
+constexpr int kMaxCtas = 160;
 constexpr int kVWidth = 128;            // columns of V per item
 constexpr int kReaders = 11;            // warps that read an item's descriptor
 
@@ -165,6 +170,7 @@ struct Geo {
   int many;           // there may be more items than CTAs
   float2* ml;         // [slot][256] (maximum, sum)
   float* po;          // [slot][columns / 4][256][4]
+  float* acc;         // [CTA][columns / 4][256][4]: O of an item's tiles but the last ones
   Join* join;         // [joins], at most one per slot
   int* joins;
   int* jleft;         // blocks of the join that are done
@@ -604,6 +610,9 @@ struct Finder {
   }
 };
 
+// kLong: sequences may have more keys than kFlush tiles.  (Asked for at run time it
+// costs every call: 16384 tokens of 64 heads over 8 2,920 us, without 2,846.)
+template <bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     k_prompt_attn(const __grid_constant__ Maps maps, const __grid_constant__ Geo g) {
   extern __shared__ uint8_t smraw[];
@@ -990,6 +999,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool brief = it.lim <= kShort;
       // (pass: what the maximum is raised for; -inf: for anything)
       float m = -INFINITY, pass = -INFINITY, l = 0.0f;
+      float fa = 1.0f;    // factor of what the workspace holds of O
+      bool kept = false;  // ... if it holds any
+      auto sum_at = [&](int col) {  // of this row, four columns at a time
+        return reinterpret_cast<float4*>(g.acc) + ((size_t)blockIdx.x * (kVWidth / 4) + col / 4) * kSlotRows + kTile * t + row;
+      };
       // columns of the tile that this row sees
       int see = token() < it.nq ? visible(token(), it.nq, it.nk) - kTile * it.j0 : 0;
 #pragma unroll 1
@@ -1039,7 +1053,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float mm = m == -INFINITY ? 0.0f : m;
         const uint64_t c2 = pair2(c, c), r2 = pair2(-mm, -mm);
-        uint64_t sum[2] = {pair2(l * f, 0.0f), pair2(0.0f, 0.0f)};
+        uint64_t sum[2] = {pair2(kLong ? 0.0f : l * f, 0.0f), pair2(0.0f, 0.0f)};  // (small next to a long l)
+        if (kLong && left != it.n[t] && ((it.n[t] - left) & (kFlush - 1)) == 0) {
+          // (S of this tile came after O of the tiles before)
+#pragma unroll 1
+          for (int i = 0; 16 * i < it.dv; ++i) {
+            uint32_t v[16];
+            tmem_ld_16cols(to + 16 * i, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              float4* p = sum_at(16 * i + e);
+              const float4 a = kept ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+              *p = make_float4(fmaf(a.x, fa, __uint_as_float(v[e])), fmaf(a.y, fa, __uint_as_float(v[e + 1])),
+                               fmaf(a.z, fa, __uint_as_float(v[e + 2])), fmaf(a.w, fa, __uint_as_float(v[e + 3])));
+              v[e] = v[e + 1] = v[e + 2] = v[e + 3] = 0;
+            }
+            tmem_st_16cols(to + 16 * i, v);
+          }
+          tmem_wait_st();
+          kept = true;
+          fa = 1.0f;
+        }
+        if (kLong) fa *= f;
         // A quarter's weights over scores that were read: bf16 to columns `at`,
         // what that leaves (short items) 32 behind.
         auto weigh = [&](const uint32_t (&x)[32], uint32_t at, auto both, auto apart) {
@@ -1119,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           brief ? halves(std::true_type{}, std::true_type{}) : halves(std::false_type{}, std::true_type{});
         }
         const float2 s0 = split2(add2(sum[0], sum[1]));
-        l = s0.x + s0.y;
+        l = kLong ? fmaf(l, f, s0.x + s0.y) : s0.x + s0.y;
       }
       if (!ok) break;
       // ---- O out of TMEM
@@ -1148,6 +1184,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0;
+        }
+        if (kLong && kept) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            if (32 * q + i >= it.dv) break;
+            const float4 a = *sum_at(32 * q + i);
+            v[i] = __float_as_uint(fmaf(a.x, fa, __uint_as_float(v[i])));
+            v[i + 1] = __float_as_uint(fmaf(a.y, fa, __uint_as_float(v[i + 1])));
+            v[i + 2] = __float_as_uint(fmaf(a.z, fa, __uint_as_float(v[i + 2])));
+            v[i + 3] = __float_as_uint(fmaf(a.w, fa, __uint_as_float(v[i + 3])));
+          }
         }
         // (as few instructions as may be, for they run once an item and come from
         // memory: a multiplication and a selection for each element took 608 items of
@@ -1343,11 +1390,11 @@ int ring_of(int nkc) {
 }  // namespace
 
 size_t prompt_attn_ws() {
-  return kWsHeader + ml_bytes() + sizeof(Join) * kMaxSlots + sizeof(float) * kMaxSlots * kSlotRows * kVWidth;
+  return kWsHeader + ml_bytes() + sizeof(Join) * kMaxSlots + sizeof(float) * (kMaxSlots + kMaxCtas) * kSlotRows * kVWidth;
 }
 
-size_t prompt_attn_uses(int B, int Nq, int Hq, int Hk, int Dv) {
-  return may_cut(shape_of(B, Nq, Hq, Hk, Dv)) ? prompt_attn_ws() : kWsHeader;
+size_t prompt_attn_uses(int B, int Nq, int Nk, int Hq, int Hk, int Dv) {
+  return may_cut(shape_of(B, Nq, Hq, Hk, Dv)) || Nk > kFlush * kTile ? prompt_attn_ws() : kWsHeader;
 }
 
 int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
@@ -1362,31 +1409,33 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   g.lgpair = 8 - sh.lgp;
   g.VH = sh.VH;
   g.HH = (int)sh.HH;
-  g.ctas = (int)std::min<long long>(sm_count(), sh.items);
-  g.many = sh.items > sm_count();
+  const int sms = std::min(sm_count(), kMaxCtas);
+  g.ctas = (int)std::min<long long>(sms, sh.items);
+  g.many = sh.items > sms;
   // Whether anything may be cut: for one sequence its lengths say so, several may
   // have any (but none more keys than there are).  Whole prompts of one and a half
   // items for every SM and more even out by themselves, the small ones coming last;
   // the join's launch would cost them ~5 us.
   bool cut = may_cut(sh) && ((long long)p.Nk + kTile - 1) / kTile >= 3 * kMinPiece &&
-             (2 * sh.items < 3LL * sm_count() || p.Nk >= 2LL * p.Nq);
+             (2 * sh.items < 3LL * sms || p.Nk >= 2LL * p.Nq);
   if (cut && p.B == 1) {
     Seq one{};
     one.nq = p.Nq;
     one.nk = p.Nk;
     one.shape(g.lgpair);
     const long long items = (long long)one.pairs * g.HH;
-    const int rest = (int)(items % sm_count()), tail = std::min((rest + g.HH - 1) / g.HH, one.pairs);
+    const int rest = (int)(items % sms), tail = std::min((rest + g.HH - 1) / g.HH, one.pairs);
     // (three tiles less on the longest item pay for the join)
-    cut = one.most >= 2 * piece_of(one.work(g.lgpair), g.HH, sm_count()) + 3 ||
-          (tail > 0 && cut_tail(items, sm_count(), rest, one.tiles_of(g.lgpair, one.pairs - tail)));
+    cut = one.most >= 2 * piece_of(one.work(g.lgpair), g.HH, sms) + 3 ||
+          (tail > 0 && cut_tail(items, sms, rest, one.tiles_of(g.lgpair, one.pairs - tail)));
   }
+  g.ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + kWsHeader);
+  g.join = reinterpret_cast<Join*>(reinterpret_cast<char*>(ws) + kWsHeader + ml_bytes());
+  g.po = reinterpret_cast<float*>(g.join + kMaxSlots);
+  g.acc = g.po + (size_t)kMaxSlots * kSlotRows * kVWidth;
   if (cut) {
     g.slots = kMaxSlots;
-    g.ctas = sm_count();
-    g.ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + kWsHeader);
-    g.join = reinterpret_cast<Join*>(reinterpret_cast<char*>(ws) + kWsHeader + ml_bytes());
-    g.po = reinterpret_cast<float*>(g.join + kMaxSlots);
+    g.ctas = sms;
   }
   g.nkc = (p.Dk + kChunk - 1) / kChunk;
   g.ring = ring_of(g.nkc);
@@ -1403,9 +1452,10 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   if (!rc) rc = make_tmap_heads(&m.v, v, p.Dv, p.Hk, p.Nk, p.v_hs, p.v_ts, kChunk, 1, kTile);
   if (rc) return rc;
   const int smem = 1024 + (2 * g.nkc + g.ring) * kChunkBytes + (int)sizeof(Smem);
-  rc = ensure_dynamic_smem((const void*)k_prompt_attn, smem, "prompt_attn");
+  const auto kernel = p.Nk > kFlush * kTile ? k_prompt_attn<true> : k_prompt_attn<false>;
+  rc = ensure_dynamic_smem((const void*)kernel, smem, "prompt_attn");
   if (rc) return rc;
-  cudaError_t e = launch_pdl(k_prompt_attn, dim3((unsigned)g.ctas), dim3(kThreads), (size_t)smem, s, m, g);
+  cudaError_t e = launch_pdl(kernel, dim3((unsigned)g.ctas), dim3(kThreads), (size_t)smem, s, m, g);
   count_launch();
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, cudaGetErrorString(e));
   rc = check_launch("prompt_attn");

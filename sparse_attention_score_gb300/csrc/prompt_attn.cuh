@@ -20,9 +20,10 @@ struct PromptAttnParams {
   int* status;
 };
 // Bytes of a workspace that serves calls of any size, and those of it that this one uses
-// (no partial results where there are items for every SM many times over).
+// (no partial results where there are items for every SM many times over, no sums of
+// their own where there are few keys).
 size_t prompt_attn_ws();
-size_t prompt_attn_uses(int B, int Nq, int Hq, int Hk, int Dv);
+size_t prompt_attn_uses(int B, int Nq, int Nk, int Hq, int Hk, int Dv);
 int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s);
 
 }  // namespace dsa

@@ -213,3 +213,44 @@ def test_items_that_take_longer_than_a_wait_of_their_parts(room):
     # of ones end at 2^24 in fp32, as the sums of halves do, so what is left is the order of size
     assert bool((out[0, ::2] == 3.0).all()) and bool(((lse[0, ::2] - 64.0).abs() <= 2.0 ** -15).all())
     assert bool(((out[0, 1::2] > 0.2) & (out[0, 1::2] < 1.1)).all())
+
+
+def test_long_sums_are_not_cut_off():
+    """193 heads of one token over a million keys and positive values, in as many uncut items.  A weight's
+    rounding averages out over so many; the matrix unit's sums lose 2^-27 for each of 65,536 keys, an item's
+    sum of them and the sum of weights next to nothing; the output is rounded once."""
+    need_gpu()
+    dsa = lib()
+    N, Hq = 1_000_000, 193
+    g = torch.Generator().manual_seed(75)
+    k, q = torch.randn((N, 1, 8), generator=g).to(BF).cuda(), (torch.randn((1, Hq, 8), generator=g) * 0.5).to(BF).cuda()
+    v = (torch.rand((N, 1, 8), generator=g) + 0.5).to(BF).cuda()
+    out, lse = torch.full((1, Hq, 8), 5.0, dtype=BF, device="cuda"), torch.full((1, Hq), 5.0, device="cuda")
+    ws = dsa.workspace(dsa.prompt_attn_workspace_size(1, 1, Hq, 1, 8, 8))
+    dsa.prompt_attn(q, k, v, 1.0, out, lse, ws)
+    assert dsa.get_status(ws) == 0
+    z = q[0].double() @ k[:, 0].double().t()
+    want, l = torch.softmax(z, -1) @ v[:, 0].double(), torch.logsumexp(z, -1)
+    d = (out[0].double() - want) / want
+    assert float(d.abs().max()) <= 2.0 ** -8 + 2.0 ** -10, float(d.abs().max())
+    assert abs(float(d.mean())) <= 2.0 ** -10, float(d.mean())
+    # (7,813 tiles' sums added one by one, half a step of a sum that is half of the last on average)
+    assert float((lse[0].double() - l).abs().max()) <= 7813 * 2.0 ** -25
+
+
+@pytest.mark.parametrize("Hq,nq,nk", [(193, 1, 300_000), (16, 2, 200_000), (256, 130, 70_000)])
+def test_maxima_that_rise_across_long_sums(Hq, nq, nk):
+    """Every row asks for one key of many: O that has left for the workspace is scaled with what follows."""
+    need_gpu()
+    dsa = lib()
+    p = Problem(76, [(nq, nk)], Hq=Hq, Hk=1, Dk=64, Dv=40, scale=1.0)
+    p.k = torch.where(p.k.float() > 0, 1.0, -1.0).to(BF)
+    g = torch.Generator().manual_seed(77)
+    target = torch.randint(0, nk - nq, (nq, Hq), generator=g)
+    target[0, :3] = torch.tensor([0, 65535, 65536])
+    for scale in (1.0, 0.3, 2.0 ** 40):                    # one key; a few; scores that are rounded
+        p.q, p.scale = p.k[target.cuda(), 0], scale
+        p.out.fill_(5.0)
+        p.run(dsa)
+        assert dsa.get_status(p.ws) == 0
+        _check_exact(p, f"scale {scale}", lse_tol=2.0 ** -15 * max(1.0, scale))
