@@ -552,7 +552,7 @@ int dsa_prefix_attn_decode(const dsa_paged_layout* layout, const void* q, const 
  *     z_j = sm_scale * q[i][h] . k[j][h'],  out[i][h] = sum_j softmax(z)_j v[j][h'],
  *     lse[i][h] = log sum_j exp(z_j),  h' = h / (Hq / Hk)
  * A token that sees no key (nk < nq) has out 0 and lse -inf. Scores, maxima and
- * sums are fp32 (the matrix unit's own run over 65,536 keys at most). A weight
+ * sums are fp32 (the matrix unit's own run over 2^18 keys at most). A weight
  * enters the product with V as bf16, off by at most 2^-8 of itself, and as bf16
  * hi + lo (2^-16) for the tokens whose tile begins with one that sees no more
  * than 512 keys; out is rounded once. The single rounding of the weights adds

@@ -110,7 +110,11 @@ constexpr int kShort = 512;
 // Key tiles after which O leaves TMEM for a sum of its own in the workspace.  The matrix
 // unit cuts its sums off where an fp32 addition rounds, so that O shrinks by about 2^-27
 // for every key: 0.7 % over 10^6, an eighth of bf16's half step over the 65,536 of this.
+// Asking for it costs 2 % (16384 tokens of 64 heads over 8 2,900 us, without 2,853; 12
+// ragged prompts 88 and 86), so it is an instantiation of its own for calls with more
+// keys than 2^18, over which a sequence would lose half of bf16's half step.
 constexpr int kFlush = 512;
+constexpr int kLongKeys = 1 << 18;
 constexpr int kMaxCtas = 160;
 constexpr int kVWidth = 128;            // columns of V per item
 constexpr int kReaders = 11;            // warps that read an item's descriptor
@@ -610,8 +614,7 @@ struct Finder {
   }
 };
 
-// kLong: sequences may have more keys than kFlush tiles.  (Asked for at run time it
-// costs every call: 16384 tokens of 64 heads over 8 2,920 us, without 2,846.)
+// kLong: a sequence may have more than kLongKeys keys.
 template <bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     k_prompt_attn(const __grid_constant__ Maps maps, const __grid_constant__ Geo g) {
@@ -1007,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // columns of the tile that this row sees
       int see = token() < it.nq ? visible(token(), it.nq, it.nk) - kTile * it.j0 : 0;
 #pragma unroll 1
-      for (int left = it.n[t]; left > 0; --left, see -= kTile) {
+      for (int left = it.n[t], flush = kFlush; left > 0; --left, --flush, see -= kTile) {
         if (!warp_wait(smem_u32(&sm.sfull[t]), sphase, &sm.abort)) { ok = false; break; }
         sphase ^= 1;
         tc_fence_after();
@@ -1054,7 +1057,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mm = m == -INFINITY ? 0.0f : m;
         const uint64_t c2 = pair2(c, c), r2 = pair2(-mm, -mm);
         uint64_t sum[2] = {pair2(kLong ? 0.0f : l * f, 0.0f), pair2(0.0f, 0.0f)};  // (small next to a long l)
-        if (kLong && left != it.n[t] && ((it.n[t] - left) & (kFlush - 1)) == 0) {
+        if (kLong && __builtin_expect(flush == 0, 0)) {
+          flush = kFlush;
           // (S of this tile came after O of the tiles before)
 #pragma unroll 1
           for (int i = 0; 16 * i < it.dv; ++i) {
@@ -1185,7 +1189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0;
         }
-        if (kLong && kept) {
+        if (kLong && __builtin_expect(kept, 0)) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             if (32 * q + i >= it.dv) break;
@@ -1394,7 +1398,7 @@ size_t prompt_attn_ws() {
 }
 
 size_t prompt_attn_uses(int B, int Nq, int Nk, int Hq, int Hk, int Dv) {
-  return may_cut(shape_of(B, Nq, Hq, Hk, Dv)) || Nk > kFlush * kTile ? prompt_attn_ws() : kWsHeader;
+  return may_cut(shape_of(B, Nq, Hq, Hk, Dv)) || Nk > kLongKeys ? prompt_attn_ws() : kWsHeader;
 }
 
 int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
@@ -1452,7 +1456,7 @@ int launch_prompt_attn(const PromptAttnParams& p, void* ws, cudaStream_t s) {
   if (!rc) rc = make_tmap_heads(&m.v, v, p.Dv, p.Hk, p.Nk, p.v_hs, p.v_ts, kChunk, 1, kTile);
   if (rc) return rc;
   const int smem = 1024 + (2 * g.nkc + g.ring) * kChunkBytes + (int)sizeof(Smem);
-  const auto kernel = p.Nk > kFlush * kTile ? k_prompt_attn<true> : k_prompt_attn<false>;
+  const auto kernel = p.Nk > kLongKeys ? k_prompt_attn<true> : k_prompt_attn<false>;
   rc = ensure_dynamic_smem((const void*)kernel, smem, "prompt_attn");
   if (rc) return rc;
   cudaError_t e = launch_pdl(kernel, dim3((unsigned)g.ctas), dim3(kThreads), (size_t)smem, s, m, g);
